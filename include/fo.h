@@ -340,6 +340,154 @@ FO_API fo_status fo_attn_layer(fo_ctx* ctx, const fo_mat* X_shards, const fo_mat
 FO_API fo_status fo_gemm_rs_noalloc(const fo_mat* X, const fo_mat* W_row, int P, const fo_mat* Y,
                                     uint32_t timeout_us, uint32_t* status, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Training: the operators around the projections of a transformer block.
+ * ------------------------------------------------------------------------- */
+
+/* Which (query, key) pairs of fo_attn_forward / fo_attn_backward attend, and the scale.
+ * One sequence per rank by default: query i of Lq and key j of Lk; causal != 0: j attends i
+ * iff j <= i + (Lk - Lq) (the last query sees every key), so with Lk < Lq the first Lq - Lk
+ * queries see no key.
+ * num_seqs > 0: packed sequences.  q_offsets (device, num_seqs + 1 int32): sequence s holds
+ * the query rows q_offsets[s] .. q_offsets[s+1]; k_offsets likewise for the key rows (null:
+ * q_offsets, K then has as many rows as Q).  Sequences may be empty.  Rows in front of the
+ * first and behind the last sequence are neither read nor written, whatever they hold.  The
+ * offsets are read on the device: values that decrease or lie outside [0, rows] end the call
+ * with FO_ERR_RANGE from fo_ctx_poll and nothing is computed. */
+typedef struct {
+  int32_t causal;
+  int32_t num_seqs;           /* 0: one sequence of all rows */
+  const int32_t* q_offsets;
+  const int32_t* k_offsets;
+  float scale;                /* of the scores; 0: 1/sqrt(head_dim) */
+  int32_t reserved;
+} fo_attn_mask;
+
+/* Attention with the row statistics that its backward pass needs (the attention between the
+ * QKV and the output projection, as inside fo_attn_layer: each of the P ranks holds all
+ * tokens of its own heads, no ring).
+ *   Q[r] [Mq, heads*head_dim], K[r], V[r] [Mk, kv_heads*head_dim], O[r] as Q: bf16 (views of
+ *   one QKV matrix will do); LSE[r] [heads, Mq] fp32.  heads is a multiple of kv_heads: query
+ *   head h reads key/value head h / (heads / kv_heads).  head_dim 64 or 128.
+ *   S = scale Q K^T over the mask's pairs, LSE_i = log sum_j exp S_ij,
+ *   O = exp(S - LSE) V.  A query without keys: O = 0, LSE = -infinity.
+ * Any number of rows.  Softmax statistics and sums are fp32; the weights enter the product
+ * with V as bf16.  Values of the sequences' rows have to be finite.
+ * opts: timeout_us applies (null: defaults). */
+FO_API fo_status fo_attn_forward(fo_ctx* ctx, const fo_mat* Q, const fo_mat* K, const fo_mat* V, int P,
+                                 int heads, int kv_heads, int head_dim, const fo_attn_mask* mask,
+                                 const fo_mat* O, const fo_mat* LSE, const fo_opts* opts, void* stream);
+
+/* Backward of fo_attn_forward from its inputs, its outputs O and LSE and the gradient dO.
+ * The probabilities are recomputed, never stored:
+ *   P = exp(S - LSE), delta_i = sum_d dO_id O_id, dS = P (dO V^T - delta),
+ *   dQ = scale dS K, dK = scale dS^T Q, dV = P^T dO; dK and dV sum over the query heads that
+ *   share a key/value head.
+ * dQ as Q, dK and dV as K (bf16, rounded once; P and dS enter their products as bf16).  The
+ * outputs must not overlap the inputs.  No atomics: the same inputs give the same bits.
+ * Workspace: 8 bytes per query row and head, and, where a rank has few key blocks, fp32
+ * partial dK / dV (at most 256 MiB); it is kept for later calls. */
+FO_API fo_status fo_attn_backward(fo_ctx* ctx, const fo_mat* Q, const fo_mat* K, const fo_mat* V,
+                                  const fo_mat* O, const fo_mat* LSE, const fo_mat* dO, int P, int heads,
+                                  int kv_heads, int head_dim, const fo_attn_mask* mask, const fo_mat* dQ,
+                                  const fo_mat* dK, const fo_mat* dV, const fo_opts* opts, void* stream);
+
+/* Parameters of the norms around a block: vectors are [1, H] matrices (bf16 or fp32 each),
+ * null where the call has none. */
+typedef struct {
+  const fo_mat* w_post;       /* weight of the norm of the block's output (null: no such norm) */
+  const fo_mat* w_pre;        /* weight of the norm in front of the next block (null: none)    */
+  const fo_mat* gate;         /* null: 1; one [1, H] matrix, or P matrices [m, H]              */
+  int32_t gate_per_token;     /* 1: gate is P matrices [m, H]                                  */
+  float residual_scale;
+  float eps;
+  int32_t reserved;
+} fo_norm_params;
+
+/* Where the backward writes the parameters' gradients: null exactly where fo_norm_params has
+ * null.  Vectors: [1, H] in either type, summed over the tokens of all ranks; a per-token
+ * gate's: P matrices [m, H] of the gate's type. */
+typedef struct {
+  const fo_mat* w_post;
+  const fo_mat* w_pre;
+  const fo_mat* gate;
+} fo_norm_grads;
+
+/* The norms after a block and before the next one, fused with the block's gate and the
+ * residual addition, on every rank's token slice:
+ *   z = Y w_post / rms(Y)  (Y without w_post);  R_out = residual_scale R + gate z;
+ *   X = R_out w_pre / rms(R_out),   rms(v) = sqrt(mean over the H columns of v^2 + eps).
+ *   R[r], R_out[r] [m, H] bf16 or fp32; Y[r], X[r] [m, H] bf16 or fp32.  H <= 16384, any.
+ * X null (with w_pre null): no norm behind.  Y and R_out null: X = R w_pre / rms(R), the norm
+ * in front of the first block (then residual_scale must be 1 and w_post, gate null).
+ * fp32 arithmetic, each output rounded once (X from the unrounded R_out).  R_out may be R, X
+ * may be Y; no other overlap. */
+FO_API fo_status fo_norm_residual(fo_ctx* ctx, const fo_mat* R, const fo_mat* Y, int P,
+                                  const fo_norm_params* params, const fo_mat* R_out, const fo_mat* X,
+                                  void* stream);
+
+/* Backward of fo_norm_residual.  R_out: the residual stream after the block (without a block
+ * output: R); dX: gradient of X (null iff there is no w_pre); dR_out: gradient that reaches R_out from elsewhere
+ * (null: none; not both null).  dR: gradient of R; dY: of Y (null iff Y is).  The rms values
+ * are computed again from R_out and Y.  dR may be dR_out, dY may be dX; no other overlap.  No
+ * atomics: the same inputs give the same bits. */
+FO_API fo_status fo_norm_residual_backward(fo_ctx* ctx, const fo_mat* R_out, const fo_mat* Y, const fo_mat* dX,
+                                           const fo_mat* dR_out, int P, const fo_norm_params* params,
+                                           const fo_mat* dR, const fo_mat* dY, const fo_norm_grads* grads,
+                                           void* stream);
+
+#define FO_ROPE_MAX_PAIRS 256
+
+/* Frequencies of rotary positions: pair i of a head turns by turns[i] / 2^64 of a full turn
+ * per position; the result is scaled by `amplitude`. */
+typedef struct {
+  int32_t rot_dim;                       /* dimensions that turn: 2 per pair */
+  float amplitude;
+  uint64_t turns[FO_ROPE_MAX_PAIRS];
+} fo_rope_table;
+
+typedef enum {
+  FO_ROPE_UNSCALED = 0,  /* f_i = base^(-2i/rot_dim)                                              */
+  FO_ROPE_LINEAR = 1,    /* f_i / factor                                                          */
+  FO_ROPE_BANDED = 2,    /* pairs that turn less than `low` times over original_length positions:
+                            f_i / factor; more than `high` times: f_i; between: mixed linearly in
+                            the number of turns                                                    */
+  FO_ROPE_RAMPED = 3     /* f_i up to the pair (rounded down) that turns `high` times, f_i / factor
+                            from the pair (rounded up) that turns `low` times, mixed linearly in i
+                            between; amplitude 0.1 ln(factor) + 1 (factor > 1)                     */
+} fo_rope_kind;
+
+typedef struct {
+  int32_t kind;              /* fo_rope_kind */
+  int32_t reserved;
+  double factor, low, high;  /* low, high: FO_ROPE_BANDED and FO_ROPE_RAMPED */
+  int64_t original_length;
+} fo_rope_scaling;
+
+typedef enum {
+  FO_ROPE_HALF = 0,        /* pair i = dimensions i and i + rot_dim/2 of the head */
+  FO_ROPE_INTERLEAVED = 1  /* pair i = dimensions 2i and 2i + 1                    */
+} fo_rope_layout;
+
+/* Fills *table (host only, no GPU).  scaling null: unscaled.  rot_dim even, 2 .. 512. */
+FO_API fo_status fo_rope_table_init(fo_rope_table* table, int rot_dim, double base,
+                                    const fo_rope_scaling* scaling);
+
+/* Rotary positions on every rank's matrix: X[r] [m, n*head_dim] (n heads side by side, for
+ * instance the query and key columns of a QKV matrix), bf16 or fp32, Y[r] alike.  Of each
+ * head the first table->rot_dim dimensions turn, the others are copied.  Row i of rank r is at
+ * position positions[r][i] (device int32), or, with positions null, at
+ * start + r*rank_stride + i.  fp32 arithmetic, angles exact to 2^-33 of a turn at any
+ * position, one rounding.  Y may be X (in place; the same view); no other overlap. */
+FO_API fo_status fo_rope(fo_ctx* ctx, const fo_mat* X, int P, const fo_rope_table* table, int head_dim,
+                         int layout, const int32_t* const* positions, int64_t start, int64_t rank_stride,
+                         const fo_mat* Y, void* stream);
+
+/* Backward of fo_rope: the gradient dY of its output turned back into dX. */
+FO_API fo_status fo_rope_backward(fo_ctx* ctx, const fo_mat* dY, int P, const fo_rope_table* table, int head_dim,
+                                  int layout, const int32_t* const* positions, int64_t start,
+                                  int64_t rank_stride, const fo_mat* dX, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

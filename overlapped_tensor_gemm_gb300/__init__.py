@@ -28,13 +28,17 @@ ORDERS = {"flash": 0, "naive": 1, "slicing": 2, "serial": 3}
 LINKS = {"default": 0, "ce": 1, "push": 2}
 FAULTS = {"none": 0, "skip_hop": 1}
 EPILOGUES = {"plain": 0, "silu": 1}
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {None: 0, "linear": 1, "banded": 2, "ramped": 3}
+ROPE_MAX_PAIRS = 256
 
 # Every entry point declared in include/fo.h.
 ABI_SYMBOLS = ("fo_version", "fo_last_error_string", "fo_ctx_create", "fo_ctx_destroy", "fo_ctx_poll",
                "fo_ctx_phase_ms", "fo_gemm", "fo_ag_gemm", "fo_gemm_rs", "fo_silu_mul", "fo_mlp_layer",
                "fo_mlp_layer_host", "fo_qsplit_attn", "fo_attn_layer", "fo_gemm_a2a", "fo_a2a_gemm", "fo_col_linear_backward",
                "fo_row_linear_backward", "fo_step_order",
-               "fo_gemm_rs_noalloc")
+               "fo_gemm_rs_noalloc", "fo_attn_forward", "fo_attn_backward", "fo_norm_residual",
+               "fo_norm_residual_backward", "fo_rope_table_init", "fo_rope", "fo_rope_backward")
 
 
 class FoMat(ctypes.Structure):
@@ -47,6 +51,32 @@ class FoOpts(ctypes.Structure):
                 ("timeout_us", ctypes.c_uint32), ("causal_prune", ctypes.c_int32), ("num_sms", ctypes.c_int32),
                 ("fault", ctypes.c_int32), ("epilogue", ctypes.c_int32), ("sm_pairs", ctypes.c_int32),
                 ("compute_only", ctypes.c_int32), ("split_layer", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class FoAttnMask(ctypes.Structure):
+    _fields_ = [("causal", ctypes.c_int32), ("num_seqs", ctypes.c_int32), ("q_offsets", ctypes.c_void_p),
+                ("k_offsets", ctypes.c_void_p), ("scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class FoNormParams(ctypes.Structure):
+    _fields_ = [("w_post", ctypes.POINTER(FoMat)), ("w_pre", ctypes.POINTER(FoMat)),
+                ("gate", ctypes.POINTER(FoMat)), ("gate_per_token", ctypes.c_int32),
+                ("residual_scale", ctypes.c_float), ("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class FoNormGrads(ctypes.Structure):
+    _fields_ = [("w_post", ctypes.POINTER(FoMat)), ("w_pre", ctypes.POINTER(FoMat)),
+                ("gate", ctypes.POINTER(FoMat))]
+
+
+class FoRopeTable(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("amplitude", ctypes.c_float),
+                ("turns", ctypes.c_uint64 * ROPE_MAX_PAIRS)]
+
+
+class FoRopeScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("reserved", ctypes.c_int32), ("factor", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double), ("original_length", ctypes.c_int64)]
 
 
 class FoError(RuntimeError):
@@ -91,6 +121,17 @@ def load() -> ctypes.CDLL:
                                            P(FoOpts), vp]
         lib.fo_step_order.argtypes = [ctypes.c_int, ctypes.c_int, ctypes.c_int, P(ctypes.c_int32),
                                       P(ctypes.c_int32), ctypes.c_int]
+        ci, i64 = ctypes.c_int, ctypes.c_int64
+        lib.fo_attn_forward.argtypes = [vp, P(FoMat), P(FoMat), P(FoMat), ci, ci, ci, ci, P(FoAttnMask), P(FoMat),
+                                        P(FoMat), P(FoOpts), vp]
+        lib.fo_attn_backward.argtypes = [vp, P(FoMat), P(FoMat), P(FoMat), P(FoMat), P(FoMat), P(FoMat), ci, ci, ci,
+                                         ci, P(FoAttnMask), P(FoMat), P(FoMat), P(FoMat), P(FoOpts), vp]
+        lib.fo_norm_residual.argtypes = [vp, P(FoMat), P(FoMat), ci, P(FoNormParams), P(FoMat), P(FoMat), vp]
+        lib.fo_norm_residual_backward.argtypes = [vp, P(FoMat), P(FoMat), P(FoMat), P(FoMat), ci, P(FoNormParams),
+                                                  P(FoMat), P(FoMat), P(FoNormGrads), vp]
+        lib.fo_rope_table_init.argtypes = [P(FoRopeTable), ci, ctypes.c_double, P(FoRopeScaling)]
+        for name in ("fo_rope", "fo_rope_backward"):
+            getattr(lib, name).argtypes = [vp, P(FoMat), ci, P(FoRopeTable), ci, ci, P(vp), i64, i64, P(FoMat), vp]
         lib.fo_gemm_rs_noalloc.argtypes = [P(FoMat), P(FoMat), ctypes.c_int, P(FoMat), ctypes.c_uint32,
                                            vp, vp]
         for name in ABI_SYMBOLS:
@@ -125,6 +166,12 @@ def mat(t) -> FoMat:
     return FoMat(t.data_ptr(), dt, 0, t.shape[0], t.shape[1], max(ld, t.shape[1]))
 
 
+def _pad_ld(a: FoMat) -> FoMat:
+    """A one-row matrix of any width: its (unused) row pitch as a whole number of 16 bytes."""
+    a.ld = -(-a.ld // 8) * 8
+    return a
+
+
 def _mats(ts: Sequence) -> ctypes.Array:
     arr = (FoMat * len(ts))()
     for i, t in enumerate(ts):
@@ -146,6 +193,25 @@ def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+
+
+class RopeTable:
+    """Frequencies of rotary positions: pair i turns by base^(-2i/rot_dim) radians per position, scaled for a
+    longer context by ``scaling`` ("linear": all by 1/factor; "banded": pairs that turn fewer than low_factor
+    times over original_length positions by 1/factor, more than high_factor times not; "ramped": by pair index
+    between those that turn beta_fast and beta_slow times, with an amplitude).  Host only."""
+
+    def __init__(self, rot_dim: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+                 low_factor: float = 1.0, high_factor: float = 4.0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                 original_length: int = 0):
+        low, high = (beta_slow, beta_fast) if scaling == "ramped" else (low_factor, high_factor)
+        how = FoRopeScaling(ROPE_SCALINGS[scaling], 0, factor, low, high, original_length)
+        self.c = FoRopeTable()
+        _check(load().fo_rope_table_init(ctypes.byref(self.c), rot_dim, base, ctypes.byref(how)))
+
+    @property
+    def rot_dim(self) -> int:
+        return self.c.rot_dim
 
 
 class Context:
@@ -257,6 +323,145 @@ class Context:
         o = opts(**kw)
         _check(self._lib.fo_attn_layer(self._h, _mats(X_shards), _mats(W_qkv), _mats(W_o), P, heads, head_dim,
                                        int(causal), _mats(Z), ctypes.byref(o), _stream(stream)))
+
+
+    # -- training operators ------------------------------------------------------------------
+
+    def _list(self, ts, P: int, what: str, keep=None):
+        """P matrices on the context's device (None stays None)."""
+        if ts is None:
+            return None
+        if len(ts) != P:
+            raise ValueError(f"{what}: {len(ts)} matrices for {P} ranks")
+        for t in ts:
+            self._here(t, what)
+        arr = _mats(ts)
+        if arr[0].rows == 1:
+            for a in arr:
+                _pad_ld(a)
+        return arr
+
+    def _here(self, t, what: str) -> None:
+        if t.device.type != "cuda" or t.device.index != self.device:
+            raise ValueError(f"{what} is on {t.device}, the context on cuda:{self.device}")
+
+    def _vector(self, t, what: str):
+        """[1, H] matrix of a vector (None stays None)."""
+        if t is None:
+            return None
+        if t.dim() != 1:
+            raise ValueError(f"{what} must be a vector")
+        self._here(t, what)
+        return ctypes.pointer(_pad_ld(mat(t.unsqueeze(0))))
+
+    def _own_stream(self, stream):
+        import torch
+        return _stream(torch.cuda.current_stream(self.device) if stream is None else stream)
+
+    def _mask(self, causal, scale, q_offsets, k_offsets):
+        import torch
+        if q_offsets is None and k_offsets is not None:
+            raise ValueError("k_offsets without q_offsets")
+        for t, what in ((q_offsets, "q_offsets"), (k_offsets, "k_offsets")):
+            if t is None:
+                continue
+            self._here(t, what)
+            if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or t.numel() < 2:
+                raise ValueError(f"{what} must be a contiguous int32 vector of num_seqs + 1 entries")
+            if t.numel() != q_offsets.numel():
+                raise ValueError("q_offsets and k_offsets must have one length")
+        if scale is not None and not scale > 0:
+            raise ValueError("scale must be positive")
+        return FoAttnMask(int(causal), 0 if q_offsets is None else q_offsets.numel() - 1,
+                          None if q_offsets is None else q_offsets.data_ptr(),
+                          None if k_offsets is None else k_offsets.data_ptr(), 0.0 if scale is None else scale, 0)
+
+    def attn_forward(self, Q, K, V, O, LSE, heads: int, kv_heads: int | None = None, head_dim: int = 128,
+                     causal: bool = True, scale: float | None = None, q_offsets=None, k_offsets=None, stream=None,
+                     **kw) -> None:
+        """O = softmax(scale Q K^T) V per rank and head, LSE [heads, tokens] its row statistics.  kv_heads < heads:
+        shared key/value heads.  q_offsets / k_offsets: int32 tensors, boundaries of packed sequences."""
+        P = len(Q)
+        m = self._mask(causal, scale, q_offsets, k_offsets)
+        o = opts(**kw)
+        _check(self._lib.fo_attn_forward(
+            self._h, self._list(Q, P, "Q"), self._list(K, P, "K"), self._list(V, P, "V"), P, heads,
+            heads if kv_heads is None else kv_heads, head_dim, ctypes.byref(m), self._list(O, P, "O"),
+            self._list(LSE, P, "LSE"), ctypes.byref(o), self._own_stream(stream)))
+
+    def attn_backward(self, Q, K, V, O, LSE, dO, dQ, dK, dV, heads: int, kv_heads: int | None = None,
+                      head_dim: int = 128, causal: bool = True, scale: float | None = None, q_offsets=None,
+                      k_offsets=None, stream=None, **kw) -> None:
+        """Gradients dQ, dK, dV of attn_forward from its inputs, its O and LSE, and dO."""
+        P = len(Q)
+        m = self._mask(causal, scale, q_offsets, k_offsets)
+        o = opts(**kw)
+        _check(self._lib.fo_attn_backward(
+            self._h, self._list(Q, P, "Q"), self._list(K, P, "K"), self._list(V, P, "V"), self._list(O, P, "O"),
+            self._list(LSE, P, "LSE"), self._list(dO, P, "dO"), P, heads, heads if kv_heads is None else kv_heads,
+            head_dim, ctypes.byref(m), self._list(dQ, P, "dQ"), self._list(dK, P, "dK"), self._list(dV, P, "dV"),
+            ctypes.byref(o), self._own_stream(stream)))
+
+    def _norm_params(self, P, w_post, gate, w_pre, residual_scale, eps, what="gate"):
+        token = gate is not None and isinstance(gate, (list, tuple))
+        g = self._list(gate, P, what) if token else self._vector(gate, what)
+        g = None if g is None else ctypes.cast(g, ctypes.POINTER(FoMat))
+        return FoNormParams(self._vector(w_post, "w_post"), self._vector(w_pre, "w_pre"), g, int(token),
+                            residual_scale, eps, 0)
+
+    def norm_residual(self, R, Y, R_out, X, w_post=None, gate=None, w_pre=None, residual_scale: float = 1.0,
+                      eps: float = 1e-6, stream=None) -> None:
+        """R_out = residual_scale R + gate (w_post Y / rms(Y)); X = w_pre R_out / rms(R_out), per rank's token slice.
+        gate: None, a vector, or a list of P matrices (per token).  Y and R_out None: X from R alone.  X None: no
+        norm behind (w_pre None)."""
+        P = len(R)
+        prm = self._norm_params(P, w_post, gate, w_pre, residual_scale, eps)
+        _check(self._lib.fo_norm_residual(self._h, self._list(R, P, "R"), self._list(Y, P, "Y"), P, ctypes.byref(prm),
+                                          self._list(R_out, P, "R_out"), self._list(X, P, "X"),
+                                          self._own_stream(stream)))
+
+    def norm_residual_backward(self, R_out, Y, dX, dR_out, dR, dY, w_post=None, gate=None, w_pre=None, dw_post=None,
+                               dgate=None, dw_pre=None, residual_scale: float = 1.0, eps: float = 1e-6,
+                               stream=None) -> None:
+        """Backward of norm_residual: dR, dY and the parameters' gradients (vectors summed over all ranks' tokens;
+        a per-token gate's as a list of P matrices)."""
+        P = len(R_out)
+        prm = self._norm_params(P, w_post, gate, w_pre, residual_scale, eps)
+        got = self._norm_params(P, dw_post, dgate, dw_pre, residual_scale, eps, "dgate")
+        if (dgate is not None) != (gate is not None) or got.gate_per_token != prm.gate_per_token:
+            raise ValueError("dgate must have gate's form")
+        grads = FoNormGrads(got.w_post, got.w_pre, got.gate)
+        _check(self._lib.fo_norm_residual_backward(
+            self._h, self._list(R_out, P, "R_out"), self._list(Y, P, "Y"), self._list(dX, P, "dX"),
+            self._list(dR_out, P, "dR_out"), P, ctypes.byref(prm), self._list(dR, P, "dR"), self._list(dY, P, "dY"),
+            ctypes.byref(grads), self._own_stream(stream)))
+
+    def _rope(self, call, X, Y, table, head_dim, layout, positions, start, rank_stride, stream) -> None:
+        import torch
+        P = len(X)
+        pos = None
+        if positions is not None:
+            if len(positions) != P:
+                raise ValueError(f"positions: {len(positions)} vectors for {P} ranks")
+            for t, x in zip(positions, X):
+                self._here(t, "positions")
+                if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or t.numel() != x.shape[0]:
+                    raise ValueError("positions must be contiguous int32 vectors, one entry per row")
+            pos = (ctypes.c_void_p * P)(*(t.data_ptr() for t in positions))
+        _check(call(self._h, self._list(X, P, "X"), P, ctypes.byref(table.c),
+                    table.rot_dim if head_dim is None else head_dim, ROPE_LAYOUTS[layout], pos, start, rank_stride,
+                    self._list(Y, P, "Y"), self._own_stream(stream)))
+
+    def rope(self, X, Y, table: RopeTable, head_dim: int | None = None, layout: str = "half", positions=None,
+             start: int = 0, rank_stride: int = 0, stream=None) -> None:
+        """Turns the heads of X into Y (Y may be X).  Row i of rank r is at positions[r][i], or at
+        start + r * rank_stride + i."""
+        self._rope(self._lib.fo_rope, X, Y, table, head_dim, layout, positions, start, rank_stride, stream)
+
+    def rope_backward(self, dY, dX, table: RopeTable, head_dim: int | None = None, layout: str = "half",
+                      positions=None, start: int = 0, rank_stride: int = 0, stream=None) -> None:
+        """dX from the gradient dY of rope's output (dX may be dY)."""
+        self._rope(self._lib.fo_rope_backward, dY, dX, table, head_dim, layout, positions, start, rank_stride, stream)
 
 
 def step_order(op: str, P: int, order: str = "flash") -> list[list[tuple[int, int]]]:

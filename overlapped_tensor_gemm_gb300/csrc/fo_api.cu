@@ -18,6 +18,7 @@
 #include <string>
 #include <vector>
 
+#include "fo_host.h"
 #include "fo_internal.h"
 
 namespace fo {
@@ -154,6 +155,7 @@ struct fo_ctx {
   int pair_clusters = 0;  // resident SM pairs for the 256x256-tile kernel (0: unavailable)
   uint32_t done_total[kMaxP] = {};  // running targets of the per-rank completion counters
   std::map<int, Buffer> bufs;
+  std::vector<void*> retired;  // outgrown workspaces that a captured launch may still use
 };
 
 namespace {
@@ -1683,6 +1685,7 @@ fo_status fo_ctx_destroy(fo_ctx* ctx) {
   cudaDeviceSynchronize();
   for (auto& kv : ctx->bufs)
     if (kv.second.ptr) cudaFree(kv.second.ptr);
+  for (void* p : ctx->retired) cudaFree(p);
   if (ctx->ctrl) cudaFree(ctx->ctrl);
   for (int r = 0; r < kMaxP; ++r) {
     if (ctx->link[r]) cudaStreamDestroy(ctx->link[r]);
@@ -1707,6 +1710,9 @@ fo_status fo_ctx_poll(fo_ctx* ctx) {
   FO_CUDA(cudaMemcpy(w, ctx->ctrl, sizeof(w), cudaMemcpyDeviceToHost));
   if (w[kCtrlError] == 0) return FO_OK;
   FO_CUDA(cudaMemset(ctx->ctrl, 0, sizeof(w)));
+  if (w[kCtrlError] == FO_ERR_RANGE && w[kCtrlWhere] == kSiteOffsets)
+    return fail(FO_ERR_RANGE, "sequence offsets out of range (entry %u): they have to start at 0 or above, not "
+                "decrease and end at or below the row count; nothing was computed", w[kCtrlDetail]);
   if (w[kCtrlError] == FO_ERR_RANGE)
     return fail(FO_ERR_RANGE, "input value out of the kernels' range (site %u, row %u): |V| above 65504, "
                 "the largest finite fp16 value", w[kCtrlWhere], w[kCtrlDetail]);
@@ -2008,6 +2014,60 @@ fo_status host_check_mat(const fo_mat& a, int32_t dtype, const char* what, int r
   return check_mat(a, dtype, what, r);
 }
 fo_status host_fail(fo_status st, const char* msg) { return fail(st, "%s", msg); }
+fo_status host_failf(fo_status st, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  return fail(st, "%s", buf);
+}
+fo_status host_check_ctx(const fo_ctx* ctx, int P) {
+  if (!ctx) return fail(FO_ERR_INVALID_ARG, "null context");
+  if (P < 1 || P > kMaxP) return fail(FO_ERR_INVALID_ARG, "P=%d outside [1, %d]", P, kMaxP);
+  return FO_OK;
+}
+int host_device(const fo_ctx* ctx) { return ctx->device; }
+fo_status host_buffer_kept(fo_ctx* ctx, int slot, size_t bytes, cudaStream_t s, void** out) {
+  Buffer& b = ctx->bufs[kBufAttnRecv + slot];
+  if (b.bytes < bytes) {
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    FO_CUDA(cudaStreamIsCapturing(s, &cap));
+    if (cap != cudaStreamCaptureStatusNone)
+      return fail(FO_ERR_UNSUPPORTED, "the workspace has to grow, which a stream capture cannot hold: make the call "
+                  "once before capturing it");
+    const size_t want = bytes > 2 * b.bytes ? bytes : 2 * b.bytes;  // outgrown buffers sum to less than the last
+    const size_t rounded = (want + (2u << 20) - 1) & ~static_cast<size_t>((2u << 20) - 1);
+    void* p = nullptr;
+    if (cudaMalloc(&p, rounded) != cudaSuccess) {
+      cudaGetLastError();
+      return fail(FO_ERR_OOM, "workspace growth to %zu bytes failed", rounded);
+    }
+    if (b.ptr) ctx->retired.push_back(b.ptr);
+    b.ptr = p;
+    b.bytes = rounded;
+  }
+  *out = b.ptr;
+  return FO_OK;
+}
+bool host_same_view(const fo_mat& a, const fo_mat& b) {
+  return a.ptr == b.ptr && a.dtype == b.dtype && a.rows == b.rows && a.cols == b.cols && (a.ld == b.ld || a.rows <= 1);
+}
+bool host_mats_overlap(const fo_mat& a, const fo_mat& b) {
+  if (!a.ptr || !b.ptr || a.rows <= 0 || b.rows <= 0 || a.cols <= 0 || b.cols <= 0) return false;
+  const int64_t ea = static_cast<int64_t>(elem_size(a.dtype)), eb = static_cast<int64_t>(elem_size(b.dtype));
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.ptr), b0 = reinterpret_cast<uintptr_t>(b.ptr);
+  const uintptr_t a1 = a0 + ((a.rows - 1) * a.ld + a.cols) * ea, b1 = b0 + ((b.rows - 1) * b.ld + b.cols) * eb;
+  if (a1 <= b0 || b1 <= a0) return false;
+  const int64_t pitch = a.ld * ea;
+  if (a.rows > 1 && b.rows > 1 && pitch == b.ld * eb) {
+    // columns of one wider matrix: b's start within a row, counted from a's
+    const int64_t gap = b0 >= a0 ? static_cast<int64_t>((b0 - a0) % static_cast<uintptr_t>(pitch))
+                                 : (pitch - static_cast<int64_t>((a0 - b0) % static_cast<uintptr_t>(pitch))) % pitch;
+    return gap < a.cols * ea || gap + b.cols * eb > pitch;
+  }
+  return true;
+}
 bool host_copies_first() { return copies_first(); }
 uint64_t host_timeout_ns(const fo_opts& o) { return timeout_ns(o); }
 int host_grid(fo_ctx* ctx, const fo_opts& o, int work) { return grid_size(ctx, o, work); }

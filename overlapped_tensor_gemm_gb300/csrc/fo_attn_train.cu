@@ -1,0 +1,517 @@
+// Attention with row statistics and its backward pass, for training: P independent ranks (each
+// holds all tokens of its own heads), shared key/value heads, packed sequences of any length,
+// query and key lengths that differ.
+//
+//   S = scale Q K^T (over the mask's pairs), LSE_i = log sum_j exp S_ij, O = exp(S - LSE) V
+//   P = exp(S - LSE), delta_i = sum_d dO_id O_id, dS = P (dO V^T - delta)
+//   dQ = scale dS K, dK = scale dS^T Q, dV = P^T dO
+//
+// Work is cut into blocks of a sequence's query rows (forward, dQ) or key rows (dK / dV).  One
+// sequence: the block of an index follows from the lengths.  Packed sequences: a small kernel
+// reads the offsets on the device, checks them and writes a table of blocks, longest first.
+#include <cuda_bf16.h>
+
+#include <cmath>
+#include <cstring>
+
+#include "fo_host.h"
+#include "fo_internal.h"
+#include "fo_ptx.cuh"
+
+namespace fo {
+namespace {
+
+constexpr int kBlockInts = 8;        // a table entry: q0, q_len, k0, k_len, block, 3 unused
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanBuckets = 1024;
+
+// One block of a sequence: its query rows q0 .. q0 + q_len and key rows k0 .. k0 + k_len, and
+// the index of this block of `unit` rows inside it.
+struct Block {
+  int q0, q_len, k0, k_len, blk;
+};
+
+struct Blocks {           // how a kernel finds its blocks
+  const int32_t* table;   // null: one sequence of mq queries and mk keys
+  int32_t mq, mk, causal;
+  int32_t count;          // entries without a table; upper bound with one
+  int32_t unit, by_keys;  // rows per block; 1: blocks of key rows
+};
+
+// The e-th block; false past the last one.  Blocks with the most work come first: a causal
+// sequence's last queries see the most keys, its first keys are seen by the most queries.
+__device__ __forceinline__ bool block_at(const Blocks& b, int e, Block* out) {
+  if (b.table) {
+    if (e >= b.table[0]) return false;
+    const int32_t* t = b.table + kBlockInts * (1 + e);
+    *out = Block{t[0], t[1], t[2], t[3], t[4]};
+    return true;
+  }
+  if (e >= b.count) return false;
+  *out = Block{0, b.mq, 0, b.mk, b.by_keys ? e : b.count - 1 - e};
+  return true;
+}
+
+// Keys that queries [q, q + n) of a sequence see: [0, key_end)
+__host__ __device__ __forceinline__ int key_end(int causal, int q_end, int q_len, int k_len) {
+  if (!causal) return k_len;
+  const int e = q_end + (k_len - q_len);
+  return e < 0 ? 0 : e > k_len ? k_len : e;
+}
+// Queries that see a key of [k, ...): [query_begin, q_len)
+__host__ __device__ __forceinline__ int query_begin(int causal, int k, int q_len, int k_len) {
+  if (!causal) return 0;
+  const int q = k - (k_len - q_len);
+  return q < 0 ? 0 : q > q_len ? q_len : q;
+}
+
+struct PlanArgs {
+  const int32_t *q_off, *k_off;
+  int32_t n, mq, mk, causal;
+  int32_t unit[2], by_keys[2], cap[2];
+  int32_t* table[2];
+  uint32_t* ctrl;
+};
+
+// Blocks of packed sequences in order of decreasing work (a counting sort over 1024 classes;
+// the order inside a class does not matter to any result).  One CTA per table, one warp per
+// sequence.  Bad offsets: FO_ERR_RANGE is recorded and the table stays empty.
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PlanArgs a) {
+  __shared__ int start[kPlanBuckets];
+  __shared__ int bad;
+  const int tb = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int32_t* table = a.table[tb];
+  for (int i = threadIdx.x; i < kPlanBuckets; i += kPlanThreads) start[i] = 0;
+  if (threadIdx.x == 0) bad = -1;
+  __syncthreads();
+  for (int s = threadIdx.x; s <= a.n; s += kPlanThreads) {
+    const int q = a.q_off[s], k = a.k_off[s];
+    const int qp = s ? a.q_off[s - 1] : 0, kp = s ? a.k_off[s - 1] : 0;
+    if (q < qp || k < kp || q < 0 || k < 0 || q > a.mq || k > a.mk) bad = s;
+  }
+  __syncthreads();
+  if (bad >= 0) {
+    if (threadIdx.x == 0) {
+      table[0] = 0;
+      note_error(a.ctrl, FO_ERR_RANGE, kSiteOffsets, static_cast<uint32_t>(bad));
+    }
+    return;
+  }
+  const int unit = a.unit[tb], by_keys = a.by_keys[tb];
+  auto each = [&](auto&& f) {
+    for (int s = warp; s < a.n; s += kPlanThreads / 32) {
+      const int q0 = a.q_off[s], ql = a.q_off[s + 1] - q0, k0 = a.k_off[s], kl = a.k_off[s + 1] - k0;
+      const int rows = by_keys ? kl : ql, nb = (rows + unit - 1) / unit;
+      for (int b = lane; b < nb; b += 32) {
+        const int end = (b + 1) * unit < rows ? (b + 1) * unit : rows;
+        const int work = by_keys ? ql - query_begin(a.causal, b * unit, ql, kl) : key_end(a.causal, end, ql, kl);
+        const int w = (work + 127) / 128;
+        f(w < kPlanBuckets ? w : kPlanBuckets - 1, Block{q0, ql, k0, kl, b});
+      }
+    }
+  };
+  each([&](int w, const Block&) { atomicAdd(&start[w], 1); });
+  __syncthreads();
+  // start[w] = entries of a class above w: an inclusive scan from the top, less the class itself
+  const int w = kPlanBuckets - 1 - threadIdx.x;
+  const int own = start[w];
+  int sum = own;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += up;
+  }
+  __shared__ int warp_sum[32];
+  if (lane == 31) warp_sum[warp] = sum;
+  __syncthreads();
+  int before = 0;
+  for (int i = 0; i < warp; ++i) before += warp_sum[i];
+  start[w] = before + sum - own;
+  if (threadIdx.x == kPlanThreads - 1) table[0] = before + sum < a.cap[tb] ? before + sum : a.cap[tb];
+  __syncthreads();
+  each([&](int c, const Block& b) {
+    const int at = atomicAdd(&start[c], 1);
+    if (at >= a.cap[tb]) return;
+    int32_t* t = table + kBlockInts * (1 + at);
+    t[0] = b.q0;
+    t[1] = b.q_len;
+    t[2] = b.k0;
+    t[3] = b.k_len;
+    t[4] = b.blk;
+  });
+}
+
+struct TrainArgs {
+  const uint16_t *q[kMaxP], *k[kMaxP], *v[kMaxP], *o[kMaxP], *d_o[kMaxP];
+  uint16_t *out_o[kMaxP], *dq[kMaxP], *dk[kMaxP], *dv[kMaxP];
+  float* lse[kMaxP];
+  int64_t ld_q[kMaxP], ld_k[kMaxP], ld_v[kMaxP], ld_o[kMaxP], ld_do[kMaxP], ld_lse[kMaxP], ld_dq[kMaxP],
+      ld_dk[kMaxP], ld_dv[kMaxP];
+  Blocks blocks;
+  int32_t P, heads, kv_heads;
+  float scale;
+};
+
+// ---------------------------------------------------------------------------
+// Plain kernels: one warp per query row (forward, dQ) or key row (dK / dV), a lane holds
+// head_dim / 32 dimensions.
+// ---------------------------------------------------------------------------
+constexpr int kPlainUnit = 32;
+
+__device__ __forceinline__ float bf(const uint16_t* p) { return __uint_as_float(static_cast<uint32_t>(*p) << 16); }
+__device__ __forceinline__ uint16_t to_bf(float f) { return static_cast<uint16_t>(pack_bf16x2(f, 0.f) & 0xFFFFu); }
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+template <int D>
+__global__ void plain_fwd_kernel(const __grid_constant__ TrainArgs a) {
+  constexpr int N = D / 32;
+  const int lane = threadIdx.x & 31, hp = a.heads * a.P;
+  const int ph = blockIdx.x % hp, rk = ph / a.heads, h = ph % a.heads, kvh = h / (a.heads / a.kv_heads);
+  Block b;
+  if (!block_at(a.blocks, blockIdx.x / hp, &b)) return;
+  for (int i = b.blk * kPlainUnit + (threadIdx.x >> 5); i < (b.blk + 1) * kPlainUnit && i < b.q_len;
+       i += blockDim.x >> 5) {
+    const int64_t row = b.q0 + i;
+    float q[N], acc[N], m = -INFINITY, l = 0.f;
+    for (int d = 0; d < N; ++d) {
+      q[d] = bf(a.q[rk] + row * a.ld_q[rk] + h * D + d * 32 + lane);
+      acc[d] = 0.f;
+    }
+    const int nk = key_end(a.blocks.causal, i + 1, b.q_len, b.k_len);
+    for (int j = 0; j < nk; ++j) {
+      const int64_t kr = b.k0 + j;
+      float s = 0.f;
+      for (int d = 0; d < N; ++d) s += q[d] * bf(a.k[rk] + kr * a.ld_k[rk] + kvh * D + d * 32 + lane);
+      s = warp_sum(s) * a.scale;
+      const float mn = fmaxf(m, s), c = expf(m - mn), p = expf(s - mn);
+      l = l * c + p;
+      m = mn;
+      for (int d = 0; d < N; ++d)
+        acc[d] = acc[d] * c + p * bf(a.v[rk] + kr * a.ld_v[rk] + kvh * D + d * 32 + lane);
+    }
+    for (int d = 0; d < N; ++d)
+      a.out_o[rk][row * a.ld_o[rk] + h * D + d * 32 + lane] = to_bf(nk > 0 ? acc[d] / l : 0.f);
+    if (lane == 0) a.lse[rk][h * a.ld_lse[rk] + row] = nk > 0 ? m + logf(l) : -INFINITY;
+  }
+}
+
+template <int D>
+__device__ __forceinline__ float row_delta(const TrainArgs& a, int rk, int h, int64_t row, int lane) {
+  float s = 0.f;
+  for (int d = 0; d < D / 32; ++d)
+    s += bf(a.o[rk] + row * a.ld_o[rk] + h * D + d * 32 + lane) *
+         bf(a.d_o[rk] + row * a.ld_do[rk] + h * D + d * 32 + lane);
+  return warp_sum(s);
+}
+
+template <int D>
+__global__ void plain_dq_kernel(const __grid_constant__ TrainArgs a) {
+  constexpr int N = D / 32;
+  const int lane = threadIdx.x & 31, hp = a.heads * a.P;
+  const int ph = blockIdx.x % hp, rk = ph / a.heads, h = ph % a.heads, kvh = h / (a.heads / a.kv_heads);
+  Block b;
+  if (!block_at(a.blocks, blockIdx.x / hp, &b)) return;
+  for (int i = b.blk * kPlainUnit + (threadIdx.x >> 5); i < (b.blk + 1) * kPlainUnit && i < b.q_len;
+       i += blockDim.x >> 5) {
+    const int64_t row = b.q0 + i;
+    float q[N], g[N], acc[N];
+    for (int d = 0; d < N; ++d) {
+      q[d] = bf(a.q[rk] + row * a.ld_q[rk] + h * D + d * 32 + lane);
+      g[d] = bf(a.d_o[rk] + row * a.ld_do[rk] + h * D + d * 32 + lane);
+      acc[d] = 0.f;
+    }
+    const float delta = row_delta<D>(a, rk, h, row, lane), lse = a.lse[rk][h * a.ld_lse[rk] + row];
+    const int nk = key_end(a.blocks.causal, i + 1, b.q_len, b.k_len);
+    for (int j = 0; j < nk; ++j) {
+      const int64_t kr = b.k0 + j;
+      float s = 0.f, dp = 0.f, k[N];
+      for (int d = 0; d < N; ++d) {
+        k[d] = bf(a.k[rk] + kr * a.ld_k[rk] + kvh * D + d * 32 + lane);
+        s += q[d] * k[d];
+        dp += g[d] * bf(a.v[rk] + kr * a.ld_v[rk] + kvh * D + d * 32 + lane);
+      }
+      const float ds = expf(warp_sum(s) * a.scale - lse) * (warp_sum(dp) - delta);
+      for (int d = 0; d < N; ++d) acc[d] += ds * k[d];
+    }
+    for (int d = 0; d < N; ++d) a.dq[rk][row * a.ld_dq[rk] + h * D + d * 32 + lane] = to_bf(acc[d] * a.scale);
+  }
+}
+
+template <int D>
+__global__ void plain_dkv_kernel(const __grid_constant__ TrainArgs a) {
+  constexpr int N = D / 32;
+  const int lane = threadIdx.x & 31, hp = a.kv_heads * a.P, group = a.heads / a.kv_heads;
+  const int ph = blockIdx.x % hp, rk = ph / a.kv_heads, kvh = ph % a.kv_heads;
+  Block b;
+  if (!block_at(a.blocks, blockIdx.x / hp, &b)) return;
+  for (int j = b.blk * kPlainUnit + (threadIdx.x >> 5); j < (b.blk + 1) * kPlainUnit && j < b.k_len;
+       j += blockDim.x >> 5) {
+    const int64_t kr = b.k0 + j;
+    float k[N], v[N], dk[N], dv[N];
+    for (int d = 0; d < N; ++d) {
+      k[d] = bf(a.k[rk] + kr * a.ld_k[rk] + kvh * D + d * 32 + lane);
+      v[d] = bf(a.v[rk] + kr * a.ld_v[rk] + kvh * D + d * 32 + lane);
+      dk[d] = dv[d] = 0.f;
+    }
+    for (int h = kvh * group; h < (kvh + 1) * group; ++h)
+      for (int i = query_begin(a.blocks.causal, j, b.q_len, b.k_len); i < b.q_len; ++i) {
+        const int64_t row = b.q0 + i;
+        float s = 0.f, dp = 0.f, q[N], g[N];
+        for (int d = 0; d < N; ++d) {
+          q[d] = bf(a.q[rk] + row * a.ld_q[rk] + h * D + d * 32 + lane);
+          g[d] = bf(a.d_o[rk] + row * a.ld_do[rk] + h * D + d * 32 + lane);
+          s += q[d] * k[d];
+          dp += g[d] * v[d];
+        }
+        const float p = expf(warp_sum(s) * a.scale - a.lse[rk][h * a.ld_lse[rk] + row]);
+        const float ds = p * (warp_sum(dp) - row_delta<D>(a, rk, h, row, lane));
+        for (int d = 0; d < N; ++d) {
+          dv[d] += p * g[d];
+          dk[d] += ds * q[d];
+        }
+      }
+    for (int d = 0; d < N; ++d) {
+      a.dk[rk][kr * a.ld_dk[rk] + kvh * D + d * 32 + lane] = to_bf(dk[d] * a.scale);
+      a.dv[rk][kr * a.ld_dv[rk] + kvh * D + d * 32 + lane] = to_bf(dv[d]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+struct Call {
+  int P, heads, kv_heads, dim;
+  int64_t mq, mk;
+  const int32_t *q_off, *k_off;
+  int n;  // packed sequences, 0: one sequence
+  int causal;
+  float scale;
+};
+
+fo_status check_shape(const fo_mat* list, const char* what, int P, int64_t rows, int64_t cols, int32_t dtype) {
+  if (!list) return host_failf(FO_ERR_INVALID_ARG, "%s: null matrix array", what);
+  for (int r = 0; r < P; ++r) {
+    FO_TRY_HOST(host_check_mat(list[r], dtype, what, r));
+    if (list[r].rows != rows || list[r].cols != cols)
+      return host_failf(FO_ERR_SHAPE, "%s[%d] must be [%lld, %lld]", what, r, (long long)rows, (long long)cols);
+  }
+  return FO_OK;
+}
+
+fo_status check_call(const fo_mat* Q, const fo_mat* K, const fo_mat* V, int P, int heads, int kv_heads, int head_dim,
+                     const fo_attn_mask* mask, const fo_opts* opts, Call* c) {
+  if (P < 1 || P > kMaxP) return host_failf(FO_ERR_INVALID_ARG, "P=%d outside [1, %d]", P, kMaxP);
+  if (!Q || !K || !V || !mask) return host_fail(FO_ERR_INVALID_ARG, "null matrix array or mask");
+  if (heads < 1 || kv_heads < 1 || heads % kv_heads != 0)
+    return host_failf(FO_ERR_INVALID_ARG, "heads=%d must be a positive multiple of kv_heads=%d", heads, kv_heads);
+  if (head_dim != 64 && head_dim != 128) return host_fail(FO_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+  if (mask->causal != 0 && mask->causal != 1) return host_fail(FO_ERR_INVALID_ARG, "causal must be 0 or 1");
+  if (!(mask->scale >= 0.f) || !std::isfinite(mask->scale))
+    return host_fail(FO_ERR_INVALID_ARG, "scale must be positive, or 0 for 1/sqrt(head_dim)");
+  if (mask->num_seqs < 0) return host_fail(FO_ERR_INVALID_ARG, "num_seqs < 0");
+  if ((mask->num_seqs > 0) != (mask->q_offsets != nullptr) || (mask->k_offsets && !mask->q_offsets))
+    return host_fail(FO_ERR_INVALID_ARG, "num_seqs > 0 goes with q_offsets");
+  if (reinterpret_cast<uintptr_t>(mask->q_offsets) % 4 != 0 || reinterpret_cast<uintptr_t>(mask->k_offsets) % 4 != 0)
+    return host_fail(FO_ERR_UNSUPPORTED, "offsets not 4-byte aligned");
+  if (opts && opts->num_sms < 0) return host_fail(FO_ERR_INVALID_ARG, "num_sms < 0");
+  c->P = P;
+  c->heads = heads;
+  c->kv_heads = kv_heads;
+  c->dim = head_dim;
+  c->mq = Q[0].rows;
+  c->mk = K[0].rows;
+  c->n = mask->num_seqs;
+  c->q_off = mask->q_offsets;
+  c->k_off = mask->k_offsets ? mask->k_offsets : mask->q_offsets;
+  c->causal = mask->causal;
+  c->scale = mask->scale > 0.f ? mask->scale : static_cast<float>(1.0 / std::sqrt(static_cast<double>(head_dim)));
+  FO_TRY_HOST(check_shape(Q, "Q", P, c->mq, static_cast<int64_t>(heads) * head_dim, FO_BF16));
+  FO_TRY_HOST(check_shape(K, "K", P, c->mk, static_cast<int64_t>(kv_heads) * head_dim, FO_BF16));
+  FO_TRY_HOST(check_shape(V, "V", P, c->mk, static_cast<int64_t>(kv_heads) * head_dim, FO_BF16));
+  if (c->n > 0 && !mask->k_offsets && c->mk != c->mq)
+    return host_fail(FO_ERR_SHAPE, "without k_offsets K must have as many rows as Q");
+  if (c->n > (1 << 24)) return host_fail(FO_ERR_UNSUPPORTED, "more than 2^24 sequences");
+  return FO_OK;
+}
+
+struct View {
+  const fo_mat* m;
+  bool written;
+  const char* name;
+};
+fo_status check_apart(const View* v, int n, int P) {
+  for (int i = 0; i < n; ++i)
+    for (int j = 0; j < n && v[i].written; ++j)
+      for (int p = 0; p < P; ++p)
+        for (int q = 0; q < P; ++q)
+          if (!(i == j && p == q) && host_mats_overlap(v[i].m[p], v[j].m[q]))
+            return host_failf(FO_ERR_INVALID_ARG, "%s[%d] overlaps %s[%d]", v[i].name, p, v[j].name, q);
+  return FO_OK;
+}
+
+// Upper bound of the blocks of `unit` rows: exact for one sequence, one more per packed sequence
+int64_t block_bound(const Call& c, int64_t rows, int unit) {
+  return c.n > 0 ? rows / unit + c.n : (rows + unit - 1) / unit;
+}
+
+struct Cut {
+  int unit;
+  bool by_keys;
+};
+
+// Blocks for up to two cuts of the call's rows; packed sequences: launches the table kernel
+fo_status make_blocks(fo_ctx* ctx, const Call& c, const Cut* cuts, int n, cudaStream_t s, Blocks* out) {
+  PlanArgs p;
+  std::memset(&p, 0, sizeof(p));
+  int64_t at = 0;
+  for (int i = 0; i < n; ++i) {
+    const int64_t bound = block_bound(c, cuts[i].by_keys ? c.mk : c.mq, cuts[i].unit);
+    if (bound * c.heads * c.P > 0x7fffffffll) return host_fail(FO_ERR_UNSUPPORTED, "too many blocks");
+    out[i] = Blocks{nullptr, static_cast<int32_t>(c.mq), static_cast<int32_t>(c.mk), c.causal,
+                    static_cast<int32_t>(bound), cuts[i].unit, cuts[i].by_keys ? 1 : 0};
+    p.unit[i] = cuts[i].unit;
+    p.by_keys[i] = out[i].by_keys;
+    p.cap[i] = out[i].count;
+    at += (bound + 1) * kBlockInts;
+  }
+  if (c.n == 0) return FO_OK;
+  void* buf = nullptr;
+  FO_TRY_HOST(host_buffer_kept(ctx, kSlotAttnTable, static_cast<size_t>(at) * 4, s, &buf));
+  int32_t* t = static_cast<int32_t*>(buf);
+  for (int i = 0; i < n; ++i) {
+    p.table[i] = t;
+    out[i].table = t;
+    t += (static_cast<int64_t>(out[i].count) + 1) * kBlockInts;
+  }
+  p.q_off = c.q_off;
+  p.k_off = c.k_off;
+  p.n = c.n;
+  p.mq = static_cast<int32_t>(c.mq);
+  p.mk = static_cast<int32_t>(c.mk);
+  p.causal = c.causal;
+  p.ctrl = host_ctrl(ctx);
+  plan_kernel<<<n, kPlanThreads, 0, s>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? FO_OK : host_fail(FO_ERR_CUDA, cudaGetErrorString(e));
+}
+
+template <typename T>
+void fill(const fo_mat* list, int P, T** ptr, int64_t* ld) {
+  for (int r = 0; r < P; ++r) {
+    ptr[r] = static_cast<T*>(list[r].ptr);
+    ld[r] = list[r].ld;
+  }
+}
+
+void fill_args(const Call& c, const fo_mat* Q, const fo_mat* K, const fo_mat* V, TrainArgs* a) {
+  std::memset(a, 0, sizeof(*a));
+  fill(Q, c.P, a->q, a->ld_q);
+  fill(K, c.P, a->k, a->ld_k);
+  fill(V, c.P, a->v, a->ld_v);
+  a->P = c.P;
+  a->heads = c.heads;
+  a->kv_heads = c.kv_heads;
+  a->scale = c.scale;
+}
+
+}  // namespace
+}  // namespace fo
+
+using namespace fo;
+
+extern "C" {
+
+fo_status fo_attn_forward(fo_ctx* ctx, const fo_mat* Q, const fo_mat* K, const fo_mat* V, int P, int heads,
+                          int kv_heads, int head_dim, const fo_attn_mask* mask, const fo_mat* O, const fo_mat* LSE,
+                          const fo_opts* opts, void* stream) {
+  Call c;
+  FO_TRY_HOST(check_call(Q, K, V, P, heads, kv_heads, head_dim, mask, opts, &c));
+  FO_TRY_HOST(check_shape(O, "O", P, c.mq, static_cast<int64_t>(heads) * head_dim, FO_BF16));
+  FO_TRY_HOST(check_shape(LSE, "LSE", P, heads, c.mq, FO_F32));
+  const View views[] = {{Q, false, "Q"}, {K, false, "K"}, {V, false, "V"}, {O, true, "O"}, {LSE, true, "LSE"}};
+  FO_TRY_HOST(check_apart(views, 5, P));
+  FO_TRY_HOST(host_check_ctx(ctx, P));
+  if (c.mq == 0) return FO_OK;
+  DeviceGuard dev(host_device(ctx));
+  if (!dev.ok) return host_fail(FO_ERR_CUDA, "cudaSetDevice failed");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  TrainArgs a;
+  fill_args(c, Q, K, V, &a);
+  fill(O, P, a.out_o, a.ld_o);
+  fill(LSE, P, a.lse, a.ld_lse);
+  const Cut cut = {kPlainUnit, false};
+  FO_TRY_HOST(make_blocks(ctx, c, &cut, 1, s, &a.blocks));
+  const unsigned grid = static_cast<unsigned>(a.blocks.count) * heads * P;
+  if (head_dim == 64) {
+    plain_fwd_kernel<64><<<grid, 256, 0, s>>>(a);
+  } else {
+    plain_fwd_kernel<128><<<grid, 256, 0, s>>>(a);
+  }
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? FO_OK : host_fail(FO_ERR_CUDA, cudaGetErrorString(e));
+}
+
+fo_status fo_attn_backward(fo_ctx* ctx, const fo_mat* Q, const fo_mat* K, const fo_mat* V, const fo_mat* O,
+                           const fo_mat* LSE, const fo_mat* dO, int P, int heads, int kv_heads, int head_dim,
+                           const fo_attn_mask* mask, const fo_mat* dQ, const fo_mat* dK, const fo_mat* dV,
+                           const fo_opts* opts, void* stream) {
+  Call c;
+  FO_TRY_HOST(check_call(Q, K, V, P, heads, kv_heads, head_dim, mask, opts, &c));
+  const int64_t qc = static_cast<int64_t>(heads) * head_dim, kc = static_cast<int64_t>(kv_heads) * head_dim;
+  FO_TRY_HOST(check_shape(O, "O", P, c.mq, qc, FO_BF16));
+  FO_TRY_HOST(check_shape(LSE, "LSE", P, heads, c.mq, FO_F32));
+  FO_TRY_HOST(check_shape(dO, "dO", P, c.mq, qc, FO_BF16));
+  FO_TRY_HOST(check_shape(dQ, "dQ", P, c.mq, qc, FO_BF16));
+  FO_TRY_HOST(check_shape(dK, "dK", P, c.mk, kc, FO_BF16));
+  FO_TRY_HOST(check_shape(dV, "dV", P, c.mk, kc, FO_BF16));
+  const View views[] = {{Q, false, "Q"},     {K, false, "K"},  {V, false, "V"},  {O, false, "O"}, {LSE, false, "LSE"},
+                        {dO, false, "dO"}, {dQ, true, "dQ"}, {dK, true, "dK"}, {dV, true, "dV"}};
+  FO_TRY_HOST(check_apart(views, 9, P));
+  FO_TRY_HOST(host_check_ctx(ctx, P));
+  if (c.mq == 0 && c.mk == 0) return FO_OK;
+  DeviceGuard dev(host_device(ctx));
+  if (!dev.ok) return host_fail(FO_ERR_CUDA, "cudaSetDevice failed");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  TrainArgs a;
+  fill_args(c, Q, K, V, &a);
+  for (int r = 0; r < P; ++r) {
+    a.o[r] = static_cast<const uint16_t*>(O[r].ptr);
+    a.ld_o[r] = O[r].ld;
+    a.d_o[r] = static_cast<const uint16_t*>(dO[r].ptr);
+    a.ld_do[r] = dO[r].ld;
+  }
+  fill(LSE, P, a.lse, a.ld_lse);
+  fill(dQ, P, a.dq, a.ld_dq);
+  fill(dK, P, a.dk, a.ld_dk);
+  fill(dV, P, a.dv, a.ld_dv);
+  const Cut cuts[2] = {{kPlainUnit, true}, {kPlainUnit, false}};
+  Blocks b[2];
+  FO_TRY_HOST(make_blocks(ctx, c, cuts, 2, s, b));
+  a.blocks = b[0];
+  unsigned grid = static_cast<unsigned>(b[0].count) * kv_heads * P;
+  if (grid > 0) {
+    if (head_dim == 64) {
+      plain_dkv_kernel<64><<<grid, 256, 0, s>>>(a);
+    } else {
+      plain_dkv_kernel<128><<<grid, 256, 0, s>>>(a);
+    }
+  }
+  a.blocks = b[1];
+  grid = static_cast<unsigned>(b[1].count) * heads * P;
+  if (grid > 0) {
+    if (head_dim == 64) {
+      plain_dq_kernel<64><<<grid, 256, 0, s>>>(a);
+    } else {
+      plain_dq_kernel<128><<<grid, 256, 0, s>>>(a);
+    }
+  }
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? FO_OK : host_fail(FO_ERR_CUDA, cudaGetErrorString(e));
+}
+
+}  // extern "C"

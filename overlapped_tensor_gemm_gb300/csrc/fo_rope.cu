@@ -1,0 +1,307 @@
+// Rotary positions: each pair (x1, x2) of a head's first rot_dim dimensions turns by the angle
+// position * frequency,
+//   y1 = A (x1 cos - x2 sin),  y2 = A (x2 cos + x1 sin),
+// and the backward pass turns by the opposite angle (the rotation's transpose).
+//
+// Bound by HBM: the matrix is read and written once.  A CTA takes a few token rows, computes
+// their cos / sin once into shared memory (they serve every head), then walks the heads with
+// 16-byte accesses.  Angles: a frequency is a fraction of a turn per position, held as a 64-bit
+// fixed-point number; position * fraction wraps modulo one turn by integer overflow, so the
+// angle is as exact at position 2^31 as at 0 (a product in fp32 would be off by 0.1 rad at
+// position 2^20).
+#include <cuda_bf16.h>
+
+#include <cmath>
+#include <cstring>
+
+#include "fo_host.h"
+#include "fo_internal.h"
+#include "fo_ptx.cuh"
+
+namespace fo {
+namespace {
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeMaxPairs = FO_ROPE_MAX_PAIRS;
+constexpr int kRopeMaxRows = 8;  // token rows per CTA
+
+struct RopeArgs {
+  const void* x[kMaxP];
+  void* y[kMaxP];
+  int64_t ld_x[kMaxP], ld_y[kMaxP];
+  const int32_t* positions[kMaxP];  // null: start + r * rank_stride + row
+  int64_t start, rank_stride, m, total_rows;
+  int32_t heads, dim, pairs, rows_per_cta;
+  int32_t copy_rest;  // 1: dimensions behind rot_dim are copied (0: in place)
+  float amp, sign;
+  uint64_t turns[kRopeMaxPairs];
+};
+
+template <typename T>
+struct Vec;
+template <>
+struct Vec<uint16_t> {
+  static constexpr int n = 8;
+  __device__ static void load(const uint16_t* p, float (&v)[8]) {
+    const uint4 w = *reinterpret_cast<const uint4*>(p);
+    const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[2 * k] = __uint_as_float(q[k] << 16);
+      v[2 * k + 1] = __uint_as_float(q[k] & 0xFFFF0000u);
+    }
+  }
+  __device__ static void store(uint16_t* p, const float (&v)[8]) {
+    st_v4_u32(p, pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+  }
+  __device__ static float get(const uint16_t* p) { return __uint_as_float(static_cast<uint32_t>(*p) << 16); }
+  __device__ static void put(uint16_t* p, float v) { *p = static_cast<uint16_t>(pack_bf16x2(v, 0.f) & 0xFFFFu); }
+};
+template <>
+struct Vec<float> {
+  static constexpr int n = 4;
+  __device__ static void load(const float* p, float (&v)[4]) {
+    const float4 a = *reinterpret_cast<const float4*>(p);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  }
+  __device__ static void store(float* p, const float (&v)[4]) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  }
+  __device__ static float get(const float* p) { return *p; }
+  __device__ static void put(float* p, float v) { *p = v; }
+};
+
+// kVec: whole 16-byte vectors (half layout: rot_dim / 2 and head_dim multiples of the vector;
+// interleaved: rot_dim and head_dim); otherwise pair by pair.
+template <typename T, bool kInterleaved, bool kVec>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+  extern __shared__ float2 cs[];  // [rows_per_cta][pairs]: A cos, A sin
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * a.rows_per_cta;
+  const int rows = static_cast<int>(a.total_rows - row0 < a.rows_per_cta ? a.total_rows - row0 : a.rows_per_cta);
+  for (int i = threadIdx.x; i < rows * a.pairs; i += kRopeThreads) {
+    const int q = i / a.pairs, f = i - q * a.pairs;
+    const int rk = static_cast<int>((row0 + q) / a.m);
+    const int64_t row = row0 + q - rk * a.m;
+    const int64_t pos = a.positions[rk] ? static_cast<int64_t>(a.positions[rk][row]) : a.start + rk * a.rank_stride + row;
+    const int64_t turn = static_cast<int64_t>(static_cast<uint64_t>(pos) * a.turns[f]);  // in [-1/2, 1/2) of a turn
+    float s, c;
+    sincospif(__ll2float_rn(turn) * 0x1p-63f, &s, &c);
+    cs[i] = make_float2(a.amp * c, a.amp * a.sign * s);
+  }
+  __syncthreads();
+  constexpr int V = kVec ? Vec<T>::n : 1;
+  // items of a head: turning vectors (half layout: one item turns a vector of each half), then
+  // vectors behind rot_dim
+  const int turning = kInterleaved ? (kVec ? 2 * a.pairs / V : a.pairs) : a.pairs / V;
+  const int rest = a.copy_rest ? (a.dim - 2 * a.pairs) / V : 0;
+  const int per_head = turning + rest, per_row = per_head * a.heads;
+  for (int i = threadIdx.x; i < rows * per_row; i += kRopeThreads) {
+    const int q = i / per_row, j = i - q * per_row, h = j / per_head, u = j - h * per_head;
+    const int rk = static_cast<int>((row0 + q) / a.m);
+    const int64_t row = row0 + q - rk * a.m;
+    const T* x = static_cast<const T*>(a.x[rk]) + row * a.ld_x[rk] + static_cast<int64_t>(h) * a.dim;
+    T* y = static_cast<T*>(a.y[rk]) + row * a.ld_y[rk] + static_cast<int64_t>(h) * a.dim;
+    const float2* t = cs + q * a.pairs;
+    if (u >= turning) {
+      const int c = 2 * a.pairs + (u - turning) * V;
+      if constexpr (kVec) {
+        *reinterpret_cast<uint4*>(y + c) = *reinterpret_cast<const uint4*>(x + c);
+      } else {
+        y[c] = x[c];
+      }
+    } else if constexpr (!kVec) {
+      const int c1 = kInterleaved ? 2 * u : u, c2 = kInterleaved ? 2 * u + 1 : u + a.pairs;
+      const float x1 = Vec<T>::get(x + c1), x2 = Vec<T>::get(x + c2);
+      Vec<T>::put(y + c1, x1 * t[u].x - x2 * t[u].y);
+      Vec<T>::put(y + c2, x2 * t[u].x + x1 * t[u].y);
+    } else if constexpr (kInterleaved) {
+      float v[V], o[V];
+      Vec<T>::load(x + u * V, v);
+#pragma unroll
+      for (int k = 0; k < V / 2; ++k) {
+        const float2 w = t[u * (V / 2) + k];
+        o[2 * k] = v[2 * k] * w.x - v[2 * k + 1] * w.y;
+        o[2 * k + 1] = v[2 * k + 1] * w.x + v[2 * k] * w.y;
+      }
+      Vec<T>::store(y + u * V, o);
+    } else {
+      float v1[V], v2[V];
+      Vec<T>::load(x + u * V, v1);
+      Vec<T>::load(x + a.pairs + u * V, v2);
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const float2 w = t[u * V + k];
+        const float o1 = v1[k] * w.x - v2[k] * w.y;
+        v2[k] = v2[k] * w.x + v1[k] * w.y;
+        v1[k] = o1;
+      }
+      Vec<T>::store(y + u * V, v1);
+      Vec<T>::store(y + a.pairs + u * V, v2);
+    }
+  }
+}
+
+template <typename T>
+void launch(const RopeArgs& a, bool interleaved, bool vec, unsigned grid, int smem, cudaStream_t s) {
+  if (interleaved) {
+    vec ? rope_kernel<T, true, true><<<grid, kRopeThreads, smem, s>>>(a)
+        : rope_kernel<T, true, false><<<grid, kRopeThreads, smem, s>>>(a);
+  } else {
+    vec ? rope_kernel<T, false, true><<<grid, kRopeThreads, smem, s>>>(a)
+        : rope_kernel<T, false, false><<<grid, kRopeThreads, smem, s>>>(a);
+  }
+}
+
+fo_status rope_run(fo_ctx* ctx, const fo_mat* X, int P, const fo_rope_table* table, int head_dim, int layout,
+                   const int32_t* const* positions, int64_t start, int64_t rank_stride, const fo_mat* Y, float sign,
+                   void* stream) {
+  if (!X || !Y || !table) return host_fail(FO_ERR_INVALID_ARG, "null matrix array or table");
+  if (P < 1 || P > kMaxP) return host_failf(FO_ERR_INVALID_ARG, "P=%d outside [1, %d]", P, kMaxP);
+  if (layout != FO_ROPE_HALF && layout != FO_ROPE_INTERLEAVED)
+    return host_failf(FO_ERR_INVALID_ARG, "unknown layout %d", layout);
+  if (table->rot_dim < 2 || table->rot_dim % 2 != 0 || table->rot_dim > 2 * kRopeMaxPairs)
+    return host_fail(FO_ERR_INVALID_ARG, "table not initialised (fo_rope_table_init)");
+  if (head_dim < table->rot_dim)
+    return host_failf(FO_ERR_SHAPE, "head_dim %d below the table's rot_dim %d", head_dim, table->rot_dim);
+  const int64_t m = X[0].rows, cols = X[0].cols;
+  const int32_t dtype = X[0].dtype;
+  if (dtype != FO_BF16 && dtype != FO_F32) return host_fail(FO_ERR_INVALID_ARG, "X: unknown dtype");
+  if (cols < 1 || cols % head_dim != 0)
+    return host_failf(FO_ERR_SHAPE, "%lld columns are no whole number of heads of %d", (long long)cols, head_dim);
+  bool in_place = true;
+  for (int r = 0; r < P; ++r) {
+    FO_TRY_HOST(host_check_mat(X[r], dtype, "X", r));
+    FO_TRY_HOST(host_check_mat(Y[r], dtype, "Y", r));
+    if (X[r].rows != m || X[r].cols != cols || Y[r].rows != m || Y[r].cols != cols)
+      return host_fail(FO_ERR_SHAPE, "X and Y must all have one shape");
+    if (positions && !positions[r] && m > 0) return host_failf(FO_ERR_INVALID_ARG, "positions[%d]: null pointer", r);
+    if (positions && reinterpret_cast<uintptr_t>(positions[r]) % 4 != 0)
+      return host_failf(FO_ERR_UNSUPPORTED, "positions[%d]: not 4-byte aligned", r);
+    in_place = in_place && host_same_view(X[r], Y[r]);
+  }
+  for (int r = 0; r < P; ++r)
+    for (int q = 0; q < P; ++q) {
+      if (host_mats_overlap(Y[r], X[q]) && !(r == q && host_same_view(X[r], Y[r])))
+        return host_failf(FO_ERR_INVALID_ARG, "Y[%d] overlaps X[%d]", r, q);
+      if (r != q && host_mats_overlap(Y[r], Y[q])) return host_failf(FO_ERR_INVALID_ARG, "Y[%d] overlaps Y[%d]", r, q);
+    }
+  FO_TRY_HOST(host_check_ctx(ctx, P));
+  if (m == 0) return FO_OK;
+  DeviceGuard dev(host_device(ctx));
+  if (!dev.ok) return host_fail(FO_ERR_CUDA, "cudaSetDevice failed");
+  RopeArgs a;
+  std::memset(&a, 0, sizeof(a));
+  for (int r = 0; r < P; ++r) {
+    a.x[r] = X[r].ptr;
+    a.y[r] = Y[r].ptr;
+    a.ld_x[r] = X[r].ld;
+    a.ld_y[r] = Y[r].ld;
+    a.positions[r] = positions ? positions[r] : nullptr;
+  }
+  a.start = start;
+  a.rank_stride = rank_stride;
+  a.m = m;
+  a.total_rows = m * P;
+  a.heads = static_cast<int32_t>(cols / head_dim);
+  a.dim = head_dim;
+  a.pairs = table->rot_dim / 2;
+  a.copy_rest = in_place ? 0 : 1;
+  a.amp = table->amplitude;
+  a.sign = sign;
+  std::memcpy(a.turns, table->turns, sizeof(a.turns[0]) * a.pairs);
+  // a CTA's rows: enough pairs for its threads to compute, one row each while rows are few
+  int rows = kRopeThreads / a.pairs;
+  rows = rows < 1 ? 1 : rows > kRopeMaxRows ? kRopeMaxRows : rows;
+  while (rows > 1 && (a.total_rows + rows - 1) / rows < 4 * host_num_sms(ctx)) rows /= 2;
+  a.rows_per_cta = rows;
+  const int64_t grid = (a.total_rows + rows - 1) / rows;
+  if (grid > 0x7fffffffll) return host_fail(FO_ERR_UNSUPPORTED, "too many rows");
+  const int v = dtype == FO_F32 ? 4 : 8;
+  const bool vec = head_dim % v == 0 && (layout == FO_ROPE_INTERLEAVED ? 2 * a.pairs : a.pairs) % v == 0;
+  const int smem = rows * a.pairs * static_cast<int>(sizeof(float2));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (dtype == FO_F32) {
+    launch<float>(a, layout == FO_ROPE_INTERLEAVED, vec, static_cast<unsigned>(grid), smem, s);
+  } else {
+    launch<uint16_t>(a, layout == FO_ROPE_INTERLEAVED, vec, static_cast<unsigned>(grid), smem, s);
+  }
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? FO_OK : host_fail(FO_ERR_CUDA, cudaGetErrorString(e));
+}
+
+constexpr double kTwoPi = 6.283185307179586476925286766559;
+
+}  // namespace
+}  // namespace fo
+
+using namespace fo;
+
+extern "C" {
+
+fo_status fo_rope_table_init(fo_rope_table* table, int rot_dim, double base, const fo_rope_scaling* scaling) {
+  if (!table) return host_fail(FO_ERR_INVALID_ARG, "null table");
+  std::memset(table, 0, sizeof(*table));
+  if (rot_dim < 2 || rot_dim % 2 != 0 || rot_dim > 2 * kRopeMaxPairs)
+    return host_failf(FO_ERR_UNSUPPORTED, "rot_dim %d: an even number from 2 to %d", rot_dim, 2 * kRopeMaxPairs);
+  if (!(base > 1.0) || !std::isfinite(base)) return host_fail(FO_ERR_INVALID_ARG, "base must be above 1");
+  const int kind = scaling ? scaling->kind : FO_ROPE_UNSCALED;
+  if (kind < FO_ROPE_UNSCALED || kind > FO_ROPE_RAMPED) return host_failf(FO_ERR_INVALID_ARG, "unknown scaling %d", kind);
+  double factor = 1.0, length = 0.0, lo = 0.0, hi = 0.0;
+  if (kind != FO_ROPE_UNSCALED) {
+    factor = scaling->factor;
+    if (!(factor > 0.0) || !std::isfinite(factor)) return host_fail(FO_ERR_INVALID_ARG, "factor must be positive");
+  }
+  double amplitude = 1.0;
+  if (kind == FO_ROPE_BANDED || kind == FO_ROPE_RAMPED) {
+    length = static_cast<double>(scaling->original_length);
+    lo = scaling->low;
+    hi = scaling->high;
+    if (!(length > 0.0) || !(lo > 0.0) || !(hi > lo) || !std::isfinite(hi))
+      return host_fail(FO_ERR_INVALID_ARG, "original_length must be positive and 0 < low < high");
+  }
+  double ramp0 = 0.0, ramp1 = 0.0;
+  if (kind == FO_ROPE_RAMPED) {
+    amplitude = factor > 1.0 ? 0.1 * std::log(factor) + 1.0 : 1.0;
+    // index of the pair that makes `turns` turns over original_length positions
+    auto pair_of = [&](double turns) { return rot_dim * std::log(length / (kTwoPi * turns)) / (2.0 * std::log(base)); };
+    ramp0 = std::floor(pair_of(hi));
+    ramp1 = std::ceil(pair_of(lo));
+    if (ramp0 < 0.0) ramp0 = 0.0;
+    if (ramp1 > rot_dim - 1.0) ramp1 = rot_dim - 1.0;
+  }
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    double f = std::pow(base, -2.0 * i / rot_dim);
+    double keep = 0.0;  // share of the unscaled frequency
+    if (kind == FO_ROPE_UNSCALED) {
+      keep = 1.0;
+    } else if (kind == FO_ROPE_BANDED) {
+      keep = (length * f / kTwoPi - lo) / (hi - lo);
+    } else if (kind == FO_ROPE_RAMPED) {
+      const double width = ramp1 - ramp0;
+      keep = 1.0 - (i - ramp0) / (width > 0.001 ? width : 0.001);
+    }
+    keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
+    f = (1.0 - keep) * f / factor + keep * f;
+    double turn = f / kTwoPi;
+    turn -= std::floor(turn);
+    const double fixed = std::ldexp(turn, 64);
+    table->turns[i] = fixed >= 18446744073709549568.0 ? 0ull : static_cast<uint64_t>(fixed);
+  }
+  table->rot_dim = rot_dim;
+  table->amplitude = static_cast<float>(amplitude);
+  return FO_OK;
+}
+
+fo_status fo_rope(fo_ctx* ctx, const fo_mat* X, int P, const fo_rope_table* table, int head_dim, int layout,
+                  const int32_t* const* positions, int64_t start, int64_t rank_stride, const fo_mat* Y,
+                  void* stream) {
+  return rope_run(ctx, X, P, table, head_dim, layout, positions, start, rank_stride, Y, 1.f, stream);
+}
+
+fo_status fo_rope_backward(fo_ctx* ctx, const fo_mat* dY, int P, const fo_rope_table* table, int head_dim,
+                           int layout, const int32_t* const* positions, int64_t start, int64_t rank_stride,
+                           const fo_mat* dX, void* stream) {
+  return rope_run(ctx, dY, P, table, head_dim, layout, positions, start, rank_stride, dX, -1.f, stream);
+}
+
+}  // extern "C"
