@@ -43,6 +43,7 @@
 #include <cmath>
 #include <cstring>
 
+#include "fo_attn_common.cuh"
 #include "fo_host.h"
 #include "fo_internal.h"
 #include "fo_ptx.cuh"
@@ -344,19 +345,6 @@ __device__ void attn_producer(const AttnParams& p, uint8_t* smem, AttnCtl* ctl, 
   }
 }
 
-// D (TMEM) += A (TMEM) * B (shared memory descriptor), A = [128 rows in lanes, 16
-// 16-bit elements per 8 columns]: the form whose A operand never passes through
-// shared memory.
-__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                        uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 // S = Q K^T for one 128-key block: Q and K from the two 64-dim swizzle halves of their
 // shared-memory blocks (16 head dims per MMA).
 __device__ __forceinline__ void issue_s(uint32_t tmem_s, uint32_t q_addr, uint32_t k_addr) {
@@ -473,37 +461,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
   // the phase is usually complete already: test it inline before the bounded wait loop
   if (lane == 0) ok = mbar_wait_fast(bar, parity, p.ctrl, p.timeout_ns, site, detail) ? 1u : 0u;
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
-}
-
-// Packed fp32 pairs (sm_100-family f32x2 instructions): two scores per instruction.
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t x, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
-}
-__device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ float fmax3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
-__device__ __forceinline__ float fast_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 
 // Softmax warps 2-9.  Warp w serves TMEM lane quadrant q = w % 4 (query rows

@@ -1,0 +1,702 @@
+// Backward of attention on the tensor cores (tcgen05, accumulators in TMEM), the probabilities
+// recomputed from the row statistics:
+//
+//   P = exp(S - LSE), S = scale Q K^T;  delta_i = sum_d dO_id O_id;  dS = P (dO V^T - delta)
+//   dV = P^T dO,  dK = scale dS^T Q,  dQ = scale dS K
+//
+// Two passes over the (query, key) pairs: one holds a block of 128 keys and walks the queries
+// (dK, dV: four products), one holds a block of 128 queries and walks the keys (dQ: three).
+// Seven products instead of the five of a single pass, but each gradient is summed in TMEM by
+// the one CTA that owns it: no atomics, no fp32 gradient in memory, the same bits every time.
+// A single pass would add dQ's 128 x 128 fp32 block to memory once per pair of blocks: 64 KiB
+// through shared memory twice, about as long as the two products it saves.
+//
+// The pass over the queries computes S and dP transposed (keys on the TMEM lanes), so that P^T
+// and dS^T, written as bf16 over the scores they came from, are the A operands of the products
+// that follow straight from TMEM; the pass over the keys computes them upright for the same
+// reason.  Q and dO (K in the other pass) are read from one shared-memory tile in both
+// orientations: K-major for the scores, MN-major for the gradients.
+//
+// CTA layout (384 threads, one CTA per SM): warp 0 loads (TMA), warp 1 issues the MMAs, warp 2
+// loads the row statistics (dK / dV), warps 4-11 compute P and dS: two warps per 32 TMEM lanes,
+// one per 64 columns.
+//
+// Rows behind a sequence belong to another one or to nobody and may hold anything.  As rows of
+// a product's A operand, or as its columns, they only reach results that are not stored or that
+// a select sets to zero; as terms of a sum (Q and dO in dK / dV, K in dQ) they would turn the
+// sum into NaN even with weight 0, so the loader clears them in shared memory.
+#include <cuda_bf16.h>
+
+#include "fo_attn_common.cuh"
+#include "fo_internal.h"
+#include "fo_ptx.cuh"
+
+namespace fo {
+namespace {
+
+constexpr int kBlk = 128;                     // queries or keys per block
+constexpr uint32_t kHalf = kBlk * 128;        // 64 columns of a block: 128 rows of one 128-byte swizzle atom
+constexpr int kThreads = 384;
+constexpr int kWorkWarps = 8;                 // warps 4-11
+constexpr uint32_t kTmem = 512;
+constexpr uint64_t kDrainNs = 200ull * 1000 * 1000;
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const TrainArgs& p, uint32_t site, int lane) {
+  uint32_t ok = 0;
+  if (lane == 0) ok = mbar_wait_fast(bar, parity, p.ctrl, p.timeout_ns, site, blockIdx.x) ? 1u : 0u;
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
+// One block of a [rows, heads * D] matrix: D / 64 boxes of 64 columns, one after the other
+template <int D>
+__device__ __forceinline__ void load_block(const CUtensorMap* map, uint8_t* dst, uint64_t* bar, int col, int row) {
+#pragma unroll
+  for (int c = 0; c < D / 64; ++c) tma_load_2d(map, dst + c * kHalf, bar, col + c * 64, row);
+}
+
+// Loads a block whose rows are terms of a sum; called by a whole warp.  The block's `full`
+// barrier completes once it is in place; with rows behind the sequence (valid < 128) the load
+// completes on `fix` first and the rows are cleared.  False when that wait gave up.
+template <int D>
+__device__ bool load_summed(const TrainArgs& p, const CUtensorMap* map, uint8_t* dst, uint64_t* full, uint64_t* fix,
+                            uint32_t& fix_uses, int col, int row, int valid, int lane) {
+  uint64_t* bar = valid < kBlk ? fix : full;
+  if (lane == 0) {
+    mbar_arrive_expect_tx(bar, D / 64 * kHalf);
+    load_block<D>(map, dst, bar, col, row);
+  }
+  if (valid >= kBlk) return true;
+  const uint32_t parity = fix_uses & 1u;
+  ++fix_uses;
+  if (!warp_wait(fix, parity, p, kSiteFull, lane)) {
+    if (lane == 0) mbar_wait_drain(fix, parity, kDrainNs);
+    return false;
+  }
+  for (int c = 0; c < D / 64; ++c)
+    for (int i = valid * 8 + lane; i < kBlk * 8; i += 32)
+      *reinterpret_cast<uint4*>(dst + c * kHalf + i * 16) = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_shared();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(full);
+  return true;
+}
+
+// D[128 x 128] = A B^T over the D head dimensions, both operands K-major tiles
+template <int D>
+__device__ __forceinline__ void issue_scores(uint32_t d_tmem, uint32_t a, uint32_t b) {
+  constexpr uint32_t idesc = umma_idesc_bf16(128, 128);
+#pragma unroll
+  for (int k = 0; k < D / 16; ++k) {
+    const uint32_t off = (k >> 2) * kHalf + (k & 3) * 32;
+    umma_bf16_ss(d_tmem, umma_sdesc_sw128(a + off), umma_sdesc_sw128(b + off), idesc, k > 0 ? 1u : 0u);
+  }
+}
+// D[128 x D] += A B over 128 summed rows: A bf16 in TMEM (rows 64h + 2c, 64h + 2c + 1 of the sum
+// in column 64h + c), B the tile's rows as they lie (MN-major)
+template <int D>
+__device__ __forceinline__ void issue_grad(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, bool first) {
+  constexpr uint32_t idesc = umma_idesc_bf16_bmn(128, D);
+#pragma unroll
+  for (int k = 0; k < kBlk / 16; ++k)
+    umma_ts(d_tmem, a_tmem + (k >> 2) * 64 + (k & 3) * 8, umma_sdesc_sw128_mn(b + k * 2048, kHalf), idesc,
+            first && k == 0 ? 0u : 1u);
+}
+
+// 64 columns of this warp's lanes
+__device__ __forceinline__ void load64(uint32_t taddr, float (&v)[64]) {
+  uint32_t w[2][32];
+  tmem_ld32(taddr, w[0]);
+  tmem_ld32(taddr + 32, w[1]);
+  tmem_wait_ld();
+#pragma unroll
+  for (int k = 0; k < 64; ++k) v[k] = __uint_as_float(w[k >> 5][k & 31]);
+}
+// their bf16 values, two per column, over the first 32 of them
+__device__ __forceinline__ void store64_bf16(uint32_t taddr, const float (&v)[64]) {
+  uint32_t w[32];
+#pragma unroll
+  for (int k = 0; k < 32; ++k) w[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
+  tmem_st32(taddr, w);
+  tmem_wait_st();
+}
+__device__ __forceinline__ void publish(uint64_t* bar, int lane) {
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
+// A warp's 32 accumulator rows, columns [col0, col0 + n), times `scale`, as bf16 to `row` (null:
+// not stored); zero: nothing was accumulated
+__device__ __forceinline__ void store_rows(uint32_t taddr, int col0, int n, float scale, uint16_t* row, bool zero) {
+  for (int c = col0; c < col0 + n; c += 32) {
+    uint32_t v[32];
+    if (zero) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) v[k] = 0u;
+    } else {
+      tmem_ld32(taddr + c, v);
+      tmem_wait_ld();
+    }
+    if (!row) continue;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      st_v4_u32(row + c + 8 * k,
+                pack_bf16x2(__uint_as_float(v[8 * k + 0]) * scale, __uint_as_float(v[8 * k + 1]) * scale),
+                pack_bf16x2(__uint_as_float(v[8 * k + 2]) * scale, __uint_as_float(v[8 * k + 3]) * scale),
+                pack_bf16x2(__uint_as_float(v[8 * k + 4]) * scale, __uint_as_float(v[8 * k + 5]) * scale),
+                pack_bf16x2(__uint_as_float(v[8 * k + 6]) * scale, __uint_as_float(v[8 * k + 7]) * scale));
+  }
+}
+
+// ---------------------------------------------------------------------------
+// dK / dV: a block of 128 keys of one key/value head; walks the query heads of its group and
+// their blocks of 128 queries.
+//
+// TMEM: S^T (then P^T) [0, 128), dP^T (then dS^T) [128, 256), dV [256, 256 + D), dK [384, ...).
+// One buffer each: the tensor pipe runs dV_i and S_{i+1} while the working warps turn dP_i into
+// dS_i, and dK_i and dP_{i+1} while they turn S_{i+1} into P_{i+1}.  The MMAs of a CTA execute in
+// the order in which its one issuing thread issues them: S_{i+1} overwrites P_i after dV_i has
+// read it, dP_{i+1} overwrites dS_i after dK_i has.
+// ---------------------------------------------------------------------------
+constexpr uint32_t kColS = 0, kColP = 128, kColV = 256, kColK = 384;
+
+template <int D>
+struct DkvSmem {
+  static constexpr uint32_t tile = D / 64 * kHalf;
+  static constexpr uint32_t k = 0, v = tile, q = 2 * tile, d_o = 4 * tile, stats = 6 * tile;  // q, d_o: 2 stages
+  static constexpr uint32_t ctl = stats + 2 * 2 * kBlk * 4;
+};
+struct alignas(8) DkvCtl {
+  uint64_t kv_full, q_full[2], q_empty[2], do_full[2], do_empty[2], st_full[2], st_empty[2];
+  uint64_t s_full, p_full, dp_full, ds_full, acc_full, fix, drain;
+  uint32_t tmem_base, pad;
+};
+template <int D>
+constexpr int dkv_smem() {
+  return static_cast<int>(DkvSmem<D>::ctl + sizeof(DkvCtl) + 1024);
+}
+
+// Where the walk stands: query head and block of the i-th iteration
+struct QueryWalk {
+  int h0, first, per_head, n;  // first query head, first block, blocks per head, iterations
+  __device__ void head_block(int i, int* h, int* qb) const {
+    *h = h0 + i / per_head;
+    *qb = first + i % per_head;
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_constant__ TrainArgs p) {
+  using L = DkvSmem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  DkvCtl* ctl = reinterpret_cast<DkvCtl*>(smem + L::ctl);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hp = p.kv_heads * p.P, ph = blockIdx.x % hp, rk = ph / p.kv_heads, kvh = ph % p.kv_heads;
+  Block b;
+  if (!block_at(p.blocks, blockIdx.x / hp, &b)) return;
+  const int group = p.heads / p.kv_heads, key0 = b.blk * kBlk;
+  QueryWalk w;
+  w.h0 = kvh * group;
+  w.first = query_begin(p.blocks.causal, key0, b.q_len, b.k_len) / kBlk;
+  w.per_head = (b.q_len + kBlk - 1) / kBlk - w.first;
+  if (w.per_head < 0) w.per_head = 0;
+  w.n = group * w.per_head;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&ctl->kv_full, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&ctl->q_full[s], 1);
+      mbar_init(&ctl->q_empty[s], 1);
+      mbar_init(&ctl->do_full[s], 1);
+      mbar_init(&ctl->do_empty[s], 1);
+      mbar_init(&ctl->st_full[s], 1);
+      mbar_init(&ctl->st_empty[s], kWorkWarps);
+    }
+    mbar_init(&ctl->s_full, 1);
+    mbar_init(&ctl->p_full, kWorkWarps);
+    mbar_init(&ctl->dp_full, 1);
+    mbar_init(&ctl->ds_full, kWorkWarps);
+    mbar_init(&ctl->acc_full, 1);
+    mbar_init(&ctl->fix, 1);
+    mbar_init(&ctl->drain, 1);
+    fence_barrier_init();
+    fence_proxy_async_shared();
+  }
+  if (warp == 1) {
+    tmem_alloc(&ctl->tmem_base, kTmem);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+  const uint32_t sbase = smem_u32(smem);
+  float* stats = reinterpret_cast<float*>(smem + L::stats);  // [stage][lse, delta][128]
+
+  if (warp < 4) {
+    if (warp == 0) {  // ---- loads
+      uint32_t fix_uses = 0;
+      int armed = 0;  // iterations whose loads have been issued
+      bool ok = true, q_armed = false;
+      if (w.n > 0 && lane == 0) {
+        mbar_arrive_expect_tx(&ctl->kv_full, 2 * L::tile);
+        load_block<D>(&p.maps[p.P + rk], smem + L::k, &ctl->kv_full, kvh * D, b.k0 + key0);
+        load_block<D>(&p.maps[2 * p.P + rk], smem + L::v, &ctl->kv_full, kvh * D, b.k0 + key0);
+      }
+      for (int i = 0; ok && i < w.n; ++i) {
+        const int st = i & 1;
+        const uint32_t free_parity = ((i >> 1) & 1) ^ 1;
+        int h, qb;
+        w.head_block(i, &h, &qb);
+        const int valid = b.q_len - qb * kBlk;
+        q_armed = false;
+        ok = warp_wait(&ctl->q_empty[st], free_parity, p, kSiteEmpty, lane);
+        if (!ok) break;
+        ok = load_summed<D>(p, &p.maps[rk], smem + L::q + st * L::tile, &ctl->q_full[st], &ctl->fix, fix_uses, h * D,
+                            b.q0 + qb * kBlk, valid, lane);
+        if (!ok) break;
+        q_armed = true;
+        ok = warp_wait(&ctl->do_empty[st], free_parity, p, kSiteEmpty, lane) &&
+             load_summed<D>(p, &p.maps[3 * p.P + rk], smem + L::d_o + st * L::tile, &ctl->do_full[st], &ctl->fix,
+                            fix_uses, h * D, b.q0 + qb * kBlk, valid, lane);
+        if (ok) armed = i + 1;
+      }
+      if (!ok && lane == 0) {  // wait for the copies in flight
+        mbar_wait_drain(&ctl->kv_full, 0, kDrainNs);
+        for (int i = armed - 2 < 0 ? 0 : armed - 2; i < armed + (q_armed ? 1 : 0); ++i) {
+          mbar_wait_drain(&ctl->q_full[i & 1], (i >> 1) & 1, kDrainNs);
+          if (i < armed) mbar_wait_drain(&ctl->do_full[i & 1], (i >> 1) & 1, kDrainNs);
+        }
+      }
+    } else if (warp == 1 && lane == 0 && w.n > 0) {  // ---- MMAs
+      const uint32_t ka = sbase + L::k, va = sbase + L::v;
+      bool ok = mbar_wait_fast(&ctl->kv_full, 0, p.ctrl, p.timeout_ns, kSiteFull, blockIdx.x) &&
+                mbar_wait_fast(&ctl->q_full[0], 0, p.ctrl, p.timeout_ns, kSiteFull, blockIdx.x);
+      bool issued = false;
+      if (ok) {
+        tc_fence_after();
+        issue_scores<D>(tmem + kColS, ka, sbase + L::q);
+        umma_commit(&ctl->s_full);
+        issued = true;
+        ok = mbar_wait_fast(&ctl->do_full[0], 0, p.ctrl, p.timeout_ns, kSiteFull, blockIdx.x);
+        if (ok) {
+          issue_scores<D>(tmem + kColP, va, sbase + L::d_o);
+          umma_commit(&ctl->dp_full);
+        }
+      }
+      for (int i = 0; ok && i < w.n; ++i) {
+        const int st = i & 1, nx = st ^ 1;
+        const uint32_t ph = i & 1, nph = ((i + 1) >> 1) & 1;
+        ok = mbar_wait_fast(&ctl->p_full, ph, p.ctrl, p.timeout_ns, kSiteTmemFull, blockIdx.x);
+        if (!ok) break;
+        tc_fence_after();
+        issue_grad<D>(tmem + kColV, tmem + kColS, sbase + L::d_o + st * L::tile, i == 0);
+        umma_commit(&ctl->do_empty[st]);
+        if (i + 1 < w.n) {
+          ok = mbar_wait_fast(&ctl->q_full[nx], nph, p.ctrl, p.timeout_ns, kSiteFull, blockIdx.x);
+          if (!ok) break;
+          issue_scores<D>(tmem + kColS, ka, sbase + L::q + nx * L::tile);
+          umma_commit(&ctl->s_full);
+        }
+        ok = mbar_wait_fast(&ctl->ds_full, ph, p.ctrl, p.timeout_ns, kSiteTmemFull, blockIdx.x);
+        if (!ok) break;
+        tc_fence_after();
+        issue_grad<D>(tmem + kColK, tmem + kColP, sbase + L::q + st * L::tile, i == 0);
+        umma_commit(&ctl->q_empty[st]);
+        if (i + 1 < w.n) {
+          ok = mbar_wait_fast(&ctl->do_full[nx], nph, p.ctrl, p.timeout_ns, kSiteFull, blockIdx.x);
+          if (!ok) break;
+          issue_scores<D>(tmem + kColP, va, sbase + L::d_o + nx * L::tile);
+          umma_commit(&ctl->dp_full);
+        }
+      }
+      if (ok) {
+        umma_commit(&ctl->acc_full);
+      } else if (issued) {
+        umma_commit(&ctl->drain);
+        mbar_wait_drain(&ctl->drain, 0, kDrainNs);
+      }
+    } else if (warp == 2) {  // ---- row statistics of the queries
+      for (int i = 0; i < w.n; ++i) {
+        const int st = i & 1;
+        int h, qb;
+        w.head_block(i, &h, &qb);
+        if (!warp_wait(&ctl->st_empty[st], ((i >> 1) & 1) ^ 1, p, kSiteEmpty, lane)) break;
+        const float* lse = p.lse[rk] + h * p.ld_lse[rk] + b.q0;
+        const float* del = p.delta + (static_cast<int64_t>(rk) * p.heads + h) * p.mq + b.q0;
+        float* out = stats + st * 2 * kBlk;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int c = k * 32 + lane, q = qb * kBlk + c;
+          const float l = q < b.q_len ? lse[q] : -INFINITY;
+          // a query without keys, or behind the sequence: weight exp(s - infinity) = 0
+          out[c] = l == -INFINITY ? INFINITY : l * kLog2e;
+          out[kBlk + c] = q < b.q_len ? del[q] : 0.f;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->st_full[st]);
+      }
+    }
+  } else {  // ---- P and dS
+    const int quad = warp & 3, hf = (warp - 4) >> 2;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const int key = key0 + quad * 32 + lane;  // this thread's row of S^T
+    const int off = b.k_len - b.q_len;
+    const uint64_t c2 = pack2(p.scale_log2, p.scale_log2);
+    bool ok = true;
+    for (int i = 0; i < w.n; ++i) {
+      const int st = i & 1;
+      const uint32_t ph = i & 1;
+      int h, qb;
+      w.head_block(i, &h, &qb);
+      const float* lse = stats + st * 2 * kBlk + hf * 64;
+      const float* del = lse + kBlk;
+      ok = warp_wait(&ctl->st_full[st], (i >> 1) & 1, p, kSiteFull, lane) &&
+           warp_wait(&ctl->s_full, ph, p, kSiteTmemFull, lane);
+      if (!ok) break;
+      tc_fence_after();
+      float s[64];
+      load64(lanes + kColS + hf * 64, s);
+#pragma unroll
+      for (int k = 0; k < 64; k += 4) {
+        const float4 l = *reinterpret_cast<const float4*>(lse + k);
+        float x0, x1, x2, x3;
+        unpack2(ffma2(pack2(s[k], s[k + 1]), c2, pack2(-l.x, -l.y)), x0, x1);
+        unpack2(ffma2(pack2(s[k + 2], s[k + 3]), c2, pack2(-l.z, -l.w)), x2, x3);
+        s[k] = fast_exp2(x0);
+        s[k + 1] = fast_exp2(x1);
+        s[k + 2] = fast_exp2(x2);
+        s[k + 3] = fast_exp2(x3);
+      }
+      // a query sees this key from query key - off on
+      if (p.blocks.causal && key0 + kBlk - 1 > qb * kBlk + off) {
+        const int from = key - off - qb * kBlk - hf * 64;
+#pragma unroll
+        for (int k = 0; k < 64; ++k)
+          if (k < from) s[k] = 0.f;
+      }
+      store64_bf16(lanes + kColS + hf * 64, s);
+      publish(&ctl->p_full, lane);
+      ok = warp_wait(&ctl->dp_full, ph, p, kSiteTmemFull, lane);
+      if (!ok) break;
+      tc_fence_after();
+      float dp[64];
+      load64(lanes + kColP + hf * 64, dp);
+#pragma unroll
+      for (int k = 0; k < 64; k += 4) {
+        const float4 d = *reinterpret_cast<const float4*>(del + k);
+        dp[k] = s[k] * (dp[k] - d.x);
+        dp[k + 1] = s[k + 1] * (dp[k + 1] - d.y);
+        dp[k + 2] = s[k + 2] * (dp[k + 2] - d.z);
+        dp[k + 3] = s[k + 3] * (dp[k + 3] - d.w);
+      }
+      store64_bf16(lanes + kColP + hf * 64, dp);
+      publish(&ctl->ds_full, lane);
+      if (lane == 0) mbar_arrive(&ctl->st_empty[st]);
+    }
+    if (ok && w.n > 0) ok = warp_wait(&ctl->acc_full, 0, p, kSiteDrain, lane);
+    if (ok) {
+      tc_fence_after();
+      const bool live = key < b.k_len;
+      const int64_t row = b.k0 + key;
+      store_rows(lanes + kColV, hf * (D / 2), D / 2, 1.f, live ? p.dv[rk] + row * p.ld_dv[rk] + kvh * D : nullptr,
+                 w.n == 0);
+      store_rows(lanes + kColK, hf * (D / 2), D / 2, p.scale, live ? p.dk[rk] + row * p.ld_dk[rk] + kvh * D : nullptr,
+                 w.n == 0);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmem);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// dQ: a block of 128 queries of one query head; walks the blocks of 128 keys it sees.
+//
+// TMEM: S (then dS) [0, 128) and [128, 256) in turn, dP [256, 384), dQ [384, 384 + D).  While the
+// working warps turn S_i and dP_i into dS_i the tensor pipe runs S_{i+1}; dP_{i+1} follows as
+// soon as they have read dP_i, dQ_i once dS_i is written.
+// ---------------------------------------------------------------------------
+constexpr uint32_t kColDp = 256, kColDq = 384;
+constexpr int kKStages = 3, kVStages = 2;
+
+template <int D>
+struct DqSmem {
+  static constexpr uint32_t tile = D / 64 * kHalf;
+  static constexpr uint32_t q = 0, d_o = tile, k = 2 * tile, v = k + kKStages * tile, ctl = v + kVStages * tile;
+};
+struct alignas(8) DqCtl {
+  uint64_t q_full, k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
+  uint64_t s_full[2], dp_full, dp_free, ds_full, acc_full, fix, drain;
+  uint32_t tmem_base, pad;
+};
+template <int D>
+constexpr int dq_smem() {
+  return static_cast<int>(DqSmem<D>::ctl + sizeof(DqCtl) + 1024);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_constant__ TrainArgs p) {
+  using L = DqSmem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  DqCtl* ctl = reinterpret_cast<DqCtl*>(smem + L::ctl);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hp = p.heads * p.P, ph = blockIdx.x % hp, rk = ph / p.heads, h = ph % p.heads;
+  Block b;
+  if (!block_at(p.blocks, blockIdx.x / hp, &b)) return;
+  const int kvh = h / (p.heads / p.kv_heads), query0 = b.blk * kBlk;
+  const int q_end = query0 + kBlk < b.q_len ? query0 + kBlk : b.q_len;
+  const int n = (key_end(p.blocks.causal, q_end, b.q_len, b.k_len) + kBlk - 1) / kBlk;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&ctl->q_full, 1);
+    for (int s = 0; s < kKStages; ++s) {
+      mbar_init(&ctl->k_full[s], 1);
+      mbar_init(&ctl->k_empty[s], 1);
+    }
+    for (int s = 0; s < kVStages; ++s) {
+      mbar_init(&ctl->v_full[s], 1);
+      mbar_init(&ctl->v_empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) mbar_init(&ctl->s_full[s], 1);
+    mbar_init(&ctl->dp_full, 1);
+    mbar_init(&ctl->dp_free, kWorkWarps);
+    mbar_init(&ctl->ds_full, kWorkWarps);
+    mbar_init(&ctl->acc_full, 1);
+    mbar_init(&ctl->fix, 1);
+    mbar_init(&ctl->drain, 1);
+    fence_barrier_init();
+    fence_proxy_async_shared();
+  }
+  if (warp == 1) {
+    tmem_alloc(&ctl->tmem_base, kTmem);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+  const uint32_t sbase = smem_u32(smem);
+
+  if (warp < 4) {
+    if (warp == 0) {  // ---- loads
+      uint32_t fix_uses = 0;
+      int k_armed = 0, v_armed = 0;
+      bool ok = true;
+      if (n > 0 && lane == 0) {
+        mbar_arrive_expect_tx(&ctl->q_full, 2 * L::tile);
+        load_block<D>(&p.maps[rk], smem + L::q, &ctl->q_full, h * D, b.q0 + query0);
+        load_block<D>(&p.maps[3 * p.P + rk], smem + L::d_o, &ctl->q_full, h * D, b.q0 + query0);
+      }
+      for (int i = 0; ok && i < n; ++i) {
+        const int ks = i % kKStages, vs = i % kVStages;
+        ok = warp_wait(&ctl->k_empty[ks], ((i / kKStages) & 1) ^ 1, p, kSiteEmpty, lane) &&
+             load_summed<D>(p, &p.maps[p.P + rk], smem + L::k + ks * L::tile, &ctl->k_full[ks], &ctl->fix, fix_uses,
+                            kvh * D, b.k0 + i * kBlk, b.k_len - i * kBlk, lane);
+        if (!ok) break;
+        k_armed = i + 1;
+        ok = warp_wait(&ctl->v_empty[vs], ((i / kVStages) & 1) ^ 1, p, kSiteEmpty, lane);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&ctl->v_full[vs], L::tile);
+          load_block<D>(&p.maps[2 * p.P + rk], smem + L::v + vs * L::tile, &ctl->v_full[vs], kvh * D, b.k0 + i * kBlk);
+        }
+        v_armed = i + 1;
+      }
+      if (!ok && lane == 0) {  // wait for the copies in flight
+        mbar_wait_drain(&ctl->q_full, 0, kDrainNs);
+        for (int i = k_armed - kKStages < 0 ? 0 : k_armed - kKStages; i < k_armed; ++i)
+          mbar_wait_drain(&ctl->k_full[i % kKStages], (i / kKStages) & 1, kDrainNs);
+        for (int i = v_armed - kVStages < 0 ? 0 : v_armed - kVStages; i < v_armed; ++i)
+          mbar_wait_drain(&ctl->v_full[i % kVStages], (i / kVStages) & 1, kDrainNs);
+      }
+    } else if (warp == 1 && lane == 0 && n > 0) {  // ---- MMAs
+      const uint32_t qa = sbase + L::q, da = sbase + L::d_o;
+      bool issued = false;
+      auto scores = [&](int i) -> bool {
+        if (!mbar_wait_fast(&ctl->k_full[i % kKStages], (i / kKStages) & 1, p.ctrl, p.timeout_ns, kSiteFull, blockIdx.x))
+          return false;
+        tc_fence_after();
+        issue_scores<D>(tmem + (i & 1) * 128, qa, sbase + L::k + (i % kKStages) * L::tile);
+        umma_commit(&ctl->s_full[i & 1]);
+        issued = true;
+        return true;
+      };
+      auto dprob = [&](int i) -> bool {
+        if (!mbar_wait_fast(&ctl->v_full[i % kVStages], (i / kVStages) & 1, p.ctrl, p.timeout_ns, kSiteFull, blockIdx.x))
+          return false;
+        tc_fence_after();
+        issue_scores<D>(tmem + kColDp, da, sbase + L::v + (i % kVStages) * L::tile);
+        umma_commit(&ctl->dp_full);
+        umma_commit(&ctl->v_empty[i % kVStages]);
+        return true;
+      };
+      bool ok = mbar_wait_fast(&ctl->q_full, 0, p.ctrl, p.timeout_ns, kSiteFull, blockIdx.x) && scores(0) && dprob(0);
+      for (int i = 0; ok && i < n; ++i) {
+        if (i + 1 < n) {
+          ok = scores(i + 1) &&
+               mbar_wait_fast(&ctl->dp_free, i & 1, p.ctrl, p.timeout_ns, kSiteTmemEmpty, blockIdx.x) && dprob(i + 1);
+          if (!ok) break;
+        }
+        ok = mbar_wait_fast(&ctl->ds_full, i & 1, p.ctrl, p.timeout_ns, kSiteTmemFull, blockIdx.x);
+        if (!ok) break;
+        tc_fence_after();
+        issue_grad<D>(tmem + kColDq, tmem + (i & 1) * 128, sbase + L::k + (i % kKStages) * L::tile, i == 0);
+        umma_commit(&ctl->k_empty[i % kKStages]);
+      }
+      if (ok) {
+        umma_commit(&ctl->acc_full);
+      } else if (issued) {
+        umma_commit(&ctl->drain);
+        mbar_wait_drain(&ctl->drain, 0, kDrainNs);
+      }
+    }
+  } else {  // ---- P and dS
+    const int quad = warp & 3, hf = (warp - 4) >> 2;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const int query = query0 + quad * 32 + lane;  // this thread's row of S
+    const bool live = query < b.q_len;
+    float lse2 = INFINITY, delta = 0.f;
+    if (live) {
+      const float l = p.lse[rk][h * p.ld_lse[rk] + b.q0 + query];
+      lse2 = l == -INFINITY ? INFINITY : l * kLog2e;
+      delta = p.delta[(static_cast<int64_t>(rk) * p.heads + h) * p.mq + b.q0 + query];
+    }
+    const int see = key_end(p.blocks.causal, query + 1, b.q_len, b.k_len);          // keys of this row
+    const int all = key_end(p.blocks.causal, query0 + 1, b.q_len, b.k_len);         // keys of the block's first row
+    const uint64_t c2 = pack2(p.scale_log2, p.scale_log2), l2 = pack2(-lse2, -lse2);
+    bool ok = true;
+    for (int i = 0; i < n; ++i) {
+      const uint32_t buf = lanes + (i & 1) * 128 + hf * 64;
+      ok = warp_wait(&ctl->s_full[i & 1], (i >> 1) & 1, p, kSiteTmemFull, lane);
+      if (!ok) break;
+      tc_fence_after();
+      float s[64];
+      load64(buf, s);
+#pragma unroll
+      for (int k = 0; k < 64; k += 2) {
+        float x0, x1;
+        unpack2(ffma2(pack2(s[k], s[k + 1]), c2, l2), x0, x1);
+        s[k] = fast_exp2(x0);
+        s[k + 1] = fast_exp2(x1);
+      }
+      ok = warp_wait(&ctl->dp_full, i & 1, p, kSiteTmemFull, lane);
+      if (!ok) break;
+      tc_fence_after();
+      float dp[64];
+      load64(lanes + kColDp + hf * 64, dp);
+      publish(&ctl->dp_free, lane);
+#pragma unroll
+      for (int k = 0; k < 64; ++k) s[k] = s[k] * (dp[k] - delta);
+      if ((i + 1) * kBlk > all) {  // keys that this row does not see: whatever they hold
+        const int upto = see - i * kBlk - hf * 64;
+#pragma unroll
+        for (int k = 0; k < 64; ++k)
+          if (k >= upto) s[k] = 0.f;
+      }
+      store64_bf16(buf, s);
+      publish(&ctl->ds_full, lane);
+    }
+    if (ok && n > 0) ok = warp_wait(&ctl->acc_full, 0, p, kSiteDrain, lane);
+    if (ok) {
+      tc_fence_after();
+      const int64_t row = b.q0 + query;
+      store_rows(lanes + kColDq, hf * (D / 2), D / 2, p.scale, live ? p.dq[rk] + row * p.ld_dq[rk] + h * D : nullptr,
+                 n == 0);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmem);
+  }
+}
+
+// delta[rank][head][row] = sum_d dO O, D / 8 lanes per (row, head) with 16-byte loads
+template <int D>
+__global__ void __launch_bounds__(256) delta_kernel(const __grid_constant__ TrainArgs p) {
+  constexpr int kLanes = D / 8;
+  const int64_t total = static_cast<int64_t>(p.P) * p.mq * p.heads;
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / kLanes;
+  const int sub = threadIdx.x % kLanes;
+  float s = 0.f;
+  int rk = 0, h = 0;
+  int64_t row = 0;
+  if (i < total) {
+    h = static_cast<int>(i % p.heads);
+    const int64_t r = i / p.heads;
+    rk = static_cast<int>(r / p.mq);
+    row = r - static_cast<int64_t>(rk) * p.mq;
+    const uint4 x = *reinterpret_cast<const uint4*>(p.o[rk] + row * p.ld_o[rk] + h * D + sub * 8);
+    const uint4 y = *reinterpret_cast<const uint4*>(p.d_o[rk] + row * p.ld_do[rk] + h * D + sub * 8);
+    const uint32_t a[4] = {x.x, x.y, x.z, x.w}, c[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      s = fmaf(__uint_as_float(a[k] << 16), __uint_as_float(c[k] << 16), s);
+      s = fmaf(__uint_as_float(a[k] & 0xFFFF0000u), __uint_as_float(c[k] & 0xFFFF0000u), s);
+    }
+  }
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (i < total && sub == 0) p.delta[(static_cast<int64_t>(rk) * p.heads + h) * p.mq + row] = s;
+}
+
+}  // namespace
+
+template <typename K>
+static cudaError_t configure(K* kernel, int smem) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+}
+
+cudaError_t attn_bwd_configure() {
+  cudaError_t e = configure(attn_dkv_kernel<64>, dkv_smem<64>());
+  if (e == cudaSuccess) e = configure(attn_dkv_kernel<128>, dkv_smem<128>());
+  if (e == cudaSuccess) e = configure(attn_dq_kernel<64>, dq_smem<64>());
+  if (e == cudaSuccess) e = configure(attn_dq_kernel<128>, dq_smem<128>());
+  return e;
+}
+static_assert(dkv_smem<128>() <= 232448 && dq_smem<128>() <= 232448, "shared memory of one CTA");
+
+cudaError_t attn_delta_launch(const TrainArgs& a, int dim, cudaStream_t s) {
+  const int64_t threads = static_cast<int64_t>(a.P) * a.mq * a.heads * (dim / 8);
+  if (threads == 0) return cudaSuccess;
+  const unsigned grid = static_cast<unsigned>((threads + 255) / 256);
+  if (dim == 64) {
+    delta_kernel<64><<<grid, 256, 0, s>>>(a);
+  } else {
+    delta_kernel<128><<<grid, 256, 0, s>>>(a);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t attn_dkv_launch(const TrainArgs& a, int dim, cudaStream_t s) {
+  const unsigned grid = static_cast<unsigned>(a.blocks.count) * a.kv_heads * a.P;
+  if (grid == 0) return cudaSuccess;
+  if (dim == 64) {
+    attn_dkv_kernel<64><<<grid, kThreads, dkv_smem<64>(), s>>>(a);
+  } else {
+    attn_dkv_kernel<128><<<grid, kThreads, dkv_smem<128>(), s>>>(a);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t attn_dq_launch(const TrainArgs& a, int dim, cudaStream_t s) {
+  const unsigned grid = static_cast<unsigned>(a.blocks.count) * a.heads * a.P;
+  if (grid == 0) return cudaSuccess;
+  if (dim == 64) {
+    attn_dq_kernel<64><<<grid, kThreads, dq_smem<64>(), s>>>(a);
+  } else {
+    attn_dq_kernel<128><<<grid, kThreads, dq_smem<128>(), s>>>(a);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace fo

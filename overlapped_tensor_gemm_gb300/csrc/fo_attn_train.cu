@@ -14,6 +14,7 @@
 #include <cmath>
 #include <cstring>
 
+#include "fo_attn_common.cuh"
 #include "fo_host.h"
 #include "fo_internal.h"
 #include "fo_ptx.cuh"
@@ -21,49 +22,8 @@
 namespace fo {
 namespace {
 
-constexpr int kBlockInts = 8;        // a table entry: q0, q_len, k0, k_len, block, 3 unused
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanBuckets = 1024;
-
-// One block of a sequence: its query rows q0 .. q0 + q_len and key rows k0 .. k0 + k_len, and
-// the index of this block of `unit` rows inside it.
-struct Block {
-  int q0, q_len, k0, k_len, blk;
-};
-
-struct Blocks {           // how a kernel finds its blocks
-  const int32_t* table;   // null: one sequence of mq queries and mk keys
-  int32_t mq, mk, causal;
-  int32_t count;          // entries without a table; upper bound with one
-  int32_t unit, by_keys;  // rows per block; 1: blocks of key rows
-};
-
-// The e-th block; false past the last one.  Blocks with the most work come first: a causal
-// sequence's last queries see the most keys, its first keys are seen by the most queries.
-__device__ __forceinline__ bool block_at(const Blocks& b, int e, Block* out) {
-  if (b.table) {
-    if (e >= b.table[0]) return false;
-    const int32_t* t = b.table + kBlockInts * (1 + e);
-    *out = Block{t[0], t[1], t[2], t[3], t[4]};
-    return true;
-  }
-  if (e >= b.count) return false;
-  *out = Block{0, b.mq, 0, b.mk, b.by_keys ? e : b.count - 1 - e};
-  return true;
-}
-
-// Keys that queries [q, q + n) of a sequence see: [0, key_end)
-__host__ __device__ __forceinline__ int key_end(int causal, int q_end, int q_len, int k_len) {
-  if (!causal) return k_len;
-  const int e = q_end + (k_len - q_len);
-  return e < 0 ? 0 : e > k_len ? k_len : e;
-}
-// Queries that see a key of [k, ...): [query_begin, q_len)
-__host__ __device__ __forceinline__ int query_begin(int causal, int k, int q_len, int k_len) {
-  if (!causal) return 0;
-  const int q = k - (k_len - q_len);
-  return q < 0 ? 0 : q > q_len ? q_len : q;
-}
 
 struct PlanArgs {
   const int32_t *q_off, *k_off;
@@ -140,17 +100,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   });
 }
 
-struct TrainArgs {
-  const uint16_t *q[kMaxP], *k[kMaxP], *v[kMaxP], *o[kMaxP], *d_o[kMaxP];
-  uint16_t *out_o[kMaxP], *dq[kMaxP], *dk[kMaxP], *dv[kMaxP];
-  float* lse[kMaxP];
-  int64_t ld_q[kMaxP], ld_k[kMaxP], ld_v[kMaxP], ld_o[kMaxP], ld_do[kMaxP], ld_lse[kMaxP], ld_dq[kMaxP],
-      ld_dk[kMaxP], ld_dv[kMaxP];
-  Blocks blocks;
-  int32_t P, heads, kv_heads;
-  float scale;
-};
-
 // ---------------------------------------------------------------------------
 // Plain kernels: one warp per query row (forward, dQ) or key row (dK / dV), a lane holds
 // head_dim / 32 dimensions.
@@ -195,88 +144,6 @@ __global__ void plain_fwd_kernel(const __grid_constant__ TrainArgs a) {
     for (int d = 0; d < N; ++d)
       a.out_o[rk][row * a.ld_o[rk] + h * D + d * 32 + lane] = to_bf(nk > 0 ? acc[d] / l : 0.f);
     if (lane == 0) a.lse[rk][h * a.ld_lse[rk] + row] = nk > 0 ? m + logf(l) : -INFINITY;
-  }
-}
-
-template <int D>
-__device__ __forceinline__ float row_delta(const TrainArgs& a, int rk, int h, int64_t row, int lane) {
-  float s = 0.f;
-  for (int d = 0; d < D / 32; ++d)
-    s += bf(a.o[rk] + row * a.ld_o[rk] + h * D + d * 32 + lane) *
-         bf(a.d_o[rk] + row * a.ld_do[rk] + h * D + d * 32 + lane);
-  return warp_sum(s);
-}
-
-template <int D>
-__global__ void plain_dq_kernel(const __grid_constant__ TrainArgs a) {
-  constexpr int N = D / 32;
-  const int lane = threadIdx.x & 31, hp = a.heads * a.P;
-  const int ph = blockIdx.x % hp, rk = ph / a.heads, h = ph % a.heads, kvh = h / (a.heads / a.kv_heads);
-  Block b;
-  if (!block_at(a.blocks, blockIdx.x / hp, &b)) return;
-  for (int i = b.blk * kPlainUnit + (threadIdx.x >> 5); i < (b.blk + 1) * kPlainUnit && i < b.q_len;
-       i += blockDim.x >> 5) {
-    const int64_t row = b.q0 + i;
-    float q[N], g[N], acc[N];
-    for (int d = 0; d < N; ++d) {
-      q[d] = bf(a.q[rk] + row * a.ld_q[rk] + h * D + d * 32 + lane);
-      g[d] = bf(a.d_o[rk] + row * a.ld_do[rk] + h * D + d * 32 + lane);
-      acc[d] = 0.f;
-    }
-    const float delta = row_delta<D>(a, rk, h, row, lane), lse = a.lse[rk][h * a.ld_lse[rk] + row];
-    const int nk = key_end(a.blocks.causal, i + 1, b.q_len, b.k_len);
-    for (int j = 0; j < nk; ++j) {
-      const int64_t kr = b.k0 + j;
-      float s = 0.f, dp = 0.f, k[N];
-      for (int d = 0; d < N; ++d) {
-        k[d] = bf(a.k[rk] + kr * a.ld_k[rk] + kvh * D + d * 32 + lane);
-        s += q[d] * k[d];
-        dp += g[d] * bf(a.v[rk] + kr * a.ld_v[rk] + kvh * D + d * 32 + lane);
-      }
-      const float ds = expf(warp_sum(s) * a.scale - lse) * (warp_sum(dp) - delta);
-      for (int d = 0; d < N; ++d) acc[d] += ds * k[d];
-    }
-    for (int d = 0; d < N; ++d) a.dq[rk][row * a.ld_dq[rk] + h * D + d * 32 + lane] = to_bf(acc[d] * a.scale);
-  }
-}
-
-template <int D>
-__global__ void plain_dkv_kernel(const __grid_constant__ TrainArgs a) {
-  constexpr int N = D / 32;
-  const int lane = threadIdx.x & 31, hp = a.kv_heads * a.P, group = a.heads / a.kv_heads;
-  const int ph = blockIdx.x % hp, rk = ph / a.kv_heads, kvh = ph % a.kv_heads;
-  Block b;
-  if (!block_at(a.blocks, blockIdx.x / hp, &b)) return;
-  for (int j = b.blk * kPlainUnit + (threadIdx.x >> 5); j < (b.blk + 1) * kPlainUnit && j < b.k_len;
-       j += blockDim.x >> 5) {
-    const int64_t kr = b.k0 + j;
-    float k[N], v[N], dk[N], dv[N];
-    for (int d = 0; d < N; ++d) {
-      k[d] = bf(a.k[rk] + kr * a.ld_k[rk] + kvh * D + d * 32 + lane);
-      v[d] = bf(a.v[rk] + kr * a.ld_v[rk] + kvh * D + d * 32 + lane);
-      dk[d] = dv[d] = 0.f;
-    }
-    for (int h = kvh * group; h < (kvh + 1) * group; ++h)
-      for (int i = query_begin(a.blocks.causal, j, b.q_len, b.k_len); i < b.q_len; ++i) {
-        const int64_t row = b.q0 + i;
-        float s = 0.f, dp = 0.f, q[N], g[N];
-        for (int d = 0; d < N; ++d) {
-          q[d] = bf(a.q[rk] + row * a.ld_q[rk] + h * D + d * 32 + lane);
-          g[d] = bf(a.d_o[rk] + row * a.ld_do[rk] + h * D + d * 32 + lane);
-          s += q[d] * k[d];
-          dp += g[d] * v[d];
-        }
-        const float p = expf(warp_sum(s) * a.scale - a.lse[rk][h * a.ld_lse[rk] + row]);
-        const float ds = p * (warp_sum(dp) - row_delta<D>(a, rk, h, row, lane));
-        for (int d = 0; d < N; ++d) {
-          dv[d] += p * g[d];
-          dk[d] += ds * q[d];
-        }
-      }
-    for (int d = 0; d < N; ++d) {
-      a.dk[rk][kr * a.ld_dk[rk] + kvh * D + d * 32 + lane] = to_bf(dk[d] * a.scale);
-      a.dv[rk][kr * a.ld_dv[rk] + kvh * D + d * 32 + lane] = to_bf(dv[d]);
-    }
   }
 }
 
@@ -408,15 +275,44 @@ void fill(const fo_mat* list, int P, T** ptr, int64_t* ld) {
   }
 }
 
-void fill_args(const Call& c, const fo_mat* Q, const fo_mat* K, const fo_mat* V, TrainArgs* a) {
+constexpr int kBlk = 128;  // rows of a tensor map's box
+
+// Operand map of a [rows, cols] matrix, read in blocks of 128 rows; an empty matrix has none
+// (its call has no block that reads it)
+fo_status add_maps(CUtensorMap* maps, const fo_mat* list, int P) {
+  for (int r = 0; r < P; ++r)
+    if (list[r].rows > 0)
+      FO_TRY_HOST(host_encode_map(&maps[r], list[r].ptr, list[r].rows, list[r].cols, list[r].ld, kBlk));
+  return FO_OK;
+}
+
+fo_status fill_args(fo_ctx* ctx, const Call& c, const fo_mat* Q, const fo_mat* K, const fo_mat* V,
+                    const fo_opts* opts, TrainArgs* a) {
   std::memset(a, 0, sizeof(*a));
   fill(Q, c.P, a->q, a->ld_q);
   fill(K, c.P, a->k, a->ld_k);
   fill(V, c.P, a->v, a->ld_v);
+  FO_TRY_HOST(add_maps(a->maps, Q, c.P));
+  FO_TRY_HOST(add_maps(a->maps + c.P, K, c.P));
+  FO_TRY_HOST(add_maps(a->maps + 2 * c.P, V, c.P));
   a->P = c.P;
   a->heads = c.heads;
   a->kv_heads = c.kv_heads;
+  a->mq = static_cast<int32_t>(c.mq);
   a->scale = c.scale;
+  a->scale_log2 = static_cast<float>(static_cast<double>(c.scale) * 1.4426950408889634);
+  fo_opts o;
+  std::memset(&o, 0, sizeof(o));
+  if (opts) o = *opts;
+  a->timeout_ns = host_timeout_ns(o);
+  a->ctrl = host_ctrl(ctx);
+  static bool configured = false;
+  if (!configured) {
+    const cudaError_t e = attn_bwd_configure();
+    if (e != cudaSuccess) return host_fail(FO_ERR_CUDA, "attention kernel configuration failed");
+    configured = true;
+  }
+  return FO_OK;
 }
 
 }  // namespace
@@ -441,7 +337,7 @@ fo_status fo_attn_forward(fo_ctx* ctx, const fo_mat* Q, const fo_mat* K, const f
   if (!dev.ok) return host_fail(FO_ERR_CUDA, "cudaSetDevice failed");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   TrainArgs a;
-  fill_args(c, Q, K, V, &a);
+  FO_TRY_HOST(fill_args(ctx, c, Q, K, V, opts, &a));
   fill(O, P, a.out_o, a.ld_o);
   fill(LSE, P, a.lse, a.ld_lse);
   const Cut cut = {kPlainUnit, false};
@@ -478,7 +374,8 @@ fo_status fo_attn_backward(fo_ctx* ctx, const fo_mat* Q, const fo_mat* K, const 
   if (!dev.ok) return host_fail(FO_ERR_CUDA, "cudaSetDevice failed");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   TrainArgs a;
-  fill_args(c, Q, K, V, &a);
+  FO_TRY_HOST(fill_args(ctx, c, Q, K, V, opts, &a));
+  FO_TRY_HOST(add_maps(a.maps + 3 * P, dO, P));
   for (int r = 0; r < P; ++r) {
     a.o[r] = static_cast<const uint16_t*>(O[r].ptr);
     a.ld_o[r] = O[r].ld;
@@ -489,28 +386,17 @@ fo_status fo_attn_backward(fo_ctx* ctx, const fo_mat* Q, const fo_mat* K, const 
   fill(dQ, P, a.dq, a.ld_dq);
   fill(dK, P, a.dk, a.ld_dk);
   fill(dV, P, a.dv, a.ld_dv);
-  const Cut cuts[2] = {{kPlainUnit, true}, {kPlainUnit, false}};
+  void* delta = nullptr;
+  FO_TRY_HOST(host_buffer_kept(ctx, kSlotAttnStats, static_cast<size_t>(P) * heads * c.mq * 4, s, &delta));
+  a.delta = static_cast<float*>(delta);
+  const Cut cuts[2] = {{kBlk, true}, {kBlk, false}};
   Blocks b[2];
   FO_TRY_HOST(make_blocks(ctx, c, cuts, 2, s, b));
+  cudaError_t e = attn_delta_launch(a, head_dim, s);
   a.blocks = b[0];
-  unsigned grid = static_cast<unsigned>(b[0].count) * kv_heads * P;
-  if (grid > 0) {
-    if (head_dim == 64) {
-      plain_dkv_kernel<64><<<grid, 256, 0, s>>>(a);
-    } else {
-      plain_dkv_kernel<128><<<grid, 256, 0, s>>>(a);
-    }
-  }
+  if (e == cudaSuccess) e = attn_dkv_launch(a, head_dim, s);
   a.blocks = b[1];
-  grid = static_cast<unsigned>(b[1].count) * heads * P;
-  if (grid > 0) {
-    if (head_dim == 64) {
-      plain_dq_kernel<64><<<grid, 256, 0, s>>>(a);
-    } else {
-      plain_dq_kernel<128><<<grid, 256, 0, s>>>(a);
-    }
-  }
-  const cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) e = attn_dq_launch(a, head_dim, s);
   return e == cudaSuccess ? FO_OK : host_fail(FO_ERR_CUDA, cudaGetErrorString(e));
 }
 
