@@ -34,73 +34,9 @@
 namespace fo {
 namespace {
 
-constexpr int kBlk = 128;                     // queries or keys per block
-constexpr uint32_t kHalf = kBlk * 128;        // 64 columns of a block: 128 rows of one 128-byte swizzle atom
 constexpr int kThreads = 384;
 constexpr int kWorkWarps = 8;                 // warps 4-11
 constexpr uint32_t kTmem = 512;
-constexpr uint64_t kDrainNs = 200ull * 1000 * 1000;
-constexpr float kLog2e = 1.4426950408889634f;
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const TrainArgs& p, uint32_t site, int lane) {
-  uint32_t ok = 0;
-  if (lane == 0) ok = mbar_wait_fast(bar, parity, p.ctrl, p.timeout_ns, site, blockIdx.x) ? 1u : 0u;
-  return __shfl_sync(0xffffffffu, ok, 0) != 0;
-}
-
-// One block of a [rows, heads * D] matrix: D / 64 boxes of 64 columns, one after the other
-template <int D>
-__device__ __forceinline__ void load_block(const CUtensorMap* map, uint8_t* dst, uint64_t* bar, int col, int row) {
-#pragma unroll
-  for (int c = 0; c < D / 64; ++c) tma_load_2d(map, dst + c * kHalf, bar, col + c * 64, row);
-}
-
-// Loads a block whose rows are terms of a sum; called by a whole warp.  The block's `full`
-// barrier completes once it is in place; with rows behind the sequence (valid < 128) the load
-// completes on `fix` first and the rows are cleared.  False when that wait gave up.
-template <int D>
-__device__ bool load_summed(const TrainArgs& p, const CUtensorMap* map, uint8_t* dst, uint64_t* full, uint64_t* fix,
-                            uint32_t& fix_uses, int col, int row, int valid, int lane) {
-  uint64_t* bar = valid < kBlk ? fix : full;
-  if (lane == 0) {
-    mbar_arrive_expect_tx(bar, D / 64 * kHalf);
-    load_block<D>(map, dst, bar, col, row);
-  }
-  if (valid >= kBlk) return true;
-  const uint32_t parity = fix_uses & 1u;
-  ++fix_uses;
-  if (!warp_wait(fix, parity, p, kSiteFull, lane)) {
-    if (lane == 0) mbar_wait_drain(fix, parity, kDrainNs);
-    return false;
-  }
-  for (int c = 0; c < D / 64; ++c)
-    for (int i = valid * 8 + lane; i < kBlk * 8; i += 32)
-      *reinterpret_cast<uint4*>(dst + c * kHalf + i * 16) = make_uint4(0, 0, 0, 0);
-  fence_proxy_async_shared();
-  __syncwarp();
-  if (lane == 0) mbar_arrive(full);
-  return true;
-}
-
-// D[128 x 128] = A B^T over the D head dimensions, both operands K-major tiles
-template <int D>
-__device__ __forceinline__ void issue_scores(uint32_t d_tmem, uint32_t a, uint32_t b) {
-  constexpr uint32_t idesc = umma_idesc_bf16(128, 128);
-#pragma unroll
-  for (int k = 0; k < D / 16; ++k) {
-    const uint32_t off = (k >> 2) * kHalf + (k & 3) * 32;
-    umma_bf16_ss(d_tmem, umma_sdesc_sw128(a + off), umma_sdesc_sw128(b + off), idesc, k > 0 ? 1u : 0u);
-  }
-}
-// D[128 x D] += A B over 128 summed rows: A bf16 in TMEM (rows 64h + 2c, 64h + 2c + 1 of the sum
-// in column 64h + c), B the tile's rows as they lie (MN-major)
-template <int D>
-__device__ __forceinline__ void issue_grad(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, bool first) {
-  constexpr uint32_t idesc = umma_idesc_bf16_bmn(128, D);
-#pragma unroll
-  for (int k = 0; k < kBlk / 16; ++k)
-    umma_ts(d_tmem, a_tmem + (k >> 2) * 64 + (k & 3) * 8, umma_sdesc_sw128_mn(b + k * 2048, kHalf), idesc,
-            first && k == 0 ? 0u : 1u);
-}
 
 // 64 columns of this warp's lanes
 __device__ __forceinline__ void load64(uint32_t taddr, float (&v)[64]) {
@@ -119,35 +55,6 @@ __device__ __forceinline__ void store64_bf16(uint32_t taddr, const float (&v)[64
   tmem_st32(taddr, w);
   tmem_wait_st();
 }
-__device__ __forceinline__ void publish(uint64_t* bar, int lane) {
-  tc_fence_before();
-  __syncwarp();
-  if (lane == 0) mbar_arrive(bar);
-}
-
-// A warp's 32 accumulator rows, columns [col0, col0 + n), times `scale`, as bf16 to `row` (null:
-// not stored); zero: nothing was accumulated
-__device__ __forceinline__ void store_rows(uint32_t taddr, int col0, int n, float scale, uint16_t* row, bool zero) {
-  for (int c = col0; c < col0 + n; c += 32) {
-    uint32_t v[32];
-    if (zero) {
-#pragma unroll
-      for (int k = 0; k < 32; ++k) v[k] = 0u;
-    } else {
-      tmem_ld32(taddr + c, v);
-      tmem_wait_ld();
-    }
-    if (!row) continue;
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      st_v4_u32(row + c + 8 * k,
-                pack_bf16x2(__uint_as_float(v[8 * k + 0]) * scale, __uint_as_float(v[8 * k + 1]) * scale),
-                pack_bf16x2(__uint_as_float(v[8 * k + 2]) * scale, __uint_as_float(v[8 * k + 3]) * scale),
-                pack_bf16x2(__uint_as_float(v[8 * k + 4]) * scale, __uint_as_float(v[8 * k + 5]) * scale),
-                pack_bf16x2(__uint_as_float(v[8 * k + 6]) * scale, __uint_as_float(v[8 * k + 7]) * scale));
-  }
-}
-
 // ---------------------------------------------------------------------------
 // dK / dV: a block of 128 keys of one key/value head; walks the query heads of its group and
 // their blocks of 128 queries.
@@ -251,22 +158,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
         w.head_block(i, &h, &qb);
         const int valid = b.q_len - qb * kBlk;
         q_armed = false;
-        ok = warp_wait(&ctl->q_empty[st], free_parity, p, kSiteEmpty, lane);
+        ok = attn_wait(&ctl->q_empty[st], free_parity, p, kSiteEmpty, lane);
         if (!ok) break;
         ok = load_summed<D>(p, &p.maps[rk], smem + L::q + st * L::tile, &ctl->q_full[st], &ctl->fix, fix_uses, h * D,
                             b.q0 + qb * kBlk, valid, lane);
         if (!ok) break;
         q_armed = true;
-        ok = warp_wait(&ctl->do_empty[st], free_parity, p, kSiteEmpty, lane) &&
+        ok = attn_wait(&ctl->do_empty[st], free_parity, p, kSiteEmpty, lane) &&
              load_summed<D>(p, &p.maps[3 * p.P + rk], smem + L::d_o + st * L::tile, &ctl->do_full[st], &ctl->fix,
                             fix_uses, h * D, b.q0 + qb * kBlk, valid, lane);
         if (ok) armed = i + 1;
       }
       if (!ok && lane == 0) {  // wait for the copies in flight
-        mbar_wait_drain(&ctl->kv_full, 0, kDrainNs);
+        mbar_wait_drain(&ctl->kv_full, 0, kAttnDrainNs);
         for (int i = armed - 2 < 0 ? 0 : armed - 2; i < armed + (q_armed ? 1 : 0); ++i) {
-          mbar_wait_drain(&ctl->q_full[i & 1], (i >> 1) & 1, kDrainNs);
-          if (i < armed) mbar_wait_drain(&ctl->do_full[i & 1], (i >> 1) & 1, kDrainNs);
+          mbar_wait_drain(&ctl->q_full[i & 1], (i >> 1) & 1, kAttnDrainNs);
+          if (i < armed) mbar_wait_drain(&ctl->do_full[i & 1], (i >> 1) & 1, kAttnDrainNs);
         }
       }
     } else if (warp == 1 && lane == 0 && w.n > 0) {  // ---- MMAs
@@ -315,14 +222,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
         umma_commit(&ctl->acc_full);
       } else if (issued) {
         umma_commit(&ctl->drain);
-        mbar_wait_drain(&ctl->drain, 0, kDrainNs);
+        mbar_wait_drain(&ctl->drain, 0, kAttnDrainNs);
       }
     } else if (warp == 2) {  // ---- row statistics of the queries
       for (int i = 0; i < w.n; ++i) {
         const int st = i & 1;
         int h, qb;
         w.head_block(i, &h, &qb);
-        if (!warp_wait(&ctl->st_empty[st], ((i >> 1) & 1) ^ 1, p, kSiteEmpty, lane)) break;
+        if (!attn_wait(&ctl->st_empty[st], ((i >> 1) & 1) ^ 1, p, kSiteEmpty, lane)) break;
         const float* lse = p.lse[rk] + h * p.ld_lse[rk] + b.q0;
         const float* del = p.delta + (static_cast<int64_t>(rk) * p.heads + h) * p.mq + b.q0;
         float* out = stats + st * 2 * kBlk;
@@ -352,8 +259,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
       w.head_block(i, &h, &qb);
       const float* lse = stats + st * 2 * kBlk + hf * 64;
       const float* del = lse + kBlk;
-      ok = warp_wait(&ctl->st_full[st], (i >> 1) & 1, p, kSiteFull, lane) &&
-           warp_wait(&ctl->s_full, ph, p, kSiteTmemFull, lane);
+      ok = attn_wait(&ctl->st_full[st], (i >> 1) & 1, p, kSiteFull, lane) &&
+           attn_wait(&ctl->s_full, ph, p, kSiteTmemFull, lane);
       if (!ok) break;
       tc_fence_after();
       float s[64];
@@ -377,8 +284,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
           if (k < from) s[k] = 0.f;
       }
       store64_bf16(lanes + kColS + hf * 64, s);
-      publish(&ctl->p_full, lane);
-      ok = warp_wait(&ctl->dp_full, ph, p, kSiteTmemFull, lane);
+      attn_publish(&ctl->p_full, lane);
+      ok = attn_wait(&ctl->dp_full, ph, p, kSiteTmemFull, lane);
       if (!ok) break;
       tc_fence_after();
       float dp[64];
@@ -392,17 +299,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
         dp[k + 3] = s[k + 3] * (dp[k + 3] - d.w);
       }
       store64_bf16(lanes + kColP + hf * 64, dp);
-      publish(&ctl->ds_full, lane);
+      attn_publish(&ctl->ds_full, lane);
       if (lane == 0) mbar_arrive(&ctl->st_empty[st]);
     }
-    if (ok && w.n > 0) ok = warp_wait(&ctl->acc_full, 0, p, kSiteDrain, lane);
+    if (ok && w.n > 0) ok = attn_wait(&ctl->acc_full, 0, p, kSiteDrain, lane);
     if (ok) {
       tc_fence_after();
       const bool live = key < b.k_len;
       const int64_t row = b.k0 + key;
-      store_rows(lanes + kColV, hf * (D / 2), D / 2, 1.f, live ? p.dv[rk] + row * p.ld_dv[rk] + kvh * D : nullptr,
+      attn_store_rows(lanes + kColV, hf * (D / 2), D / 2, 1.f, live ? p.dv[rk] + row * p.ld_dv[rk] + kvh * D : nullptr,
                  w.n == 0);
-      store_rows(lanes + kColK, hf * (D / 2), D / 2, p.scale, live ? p.dk[rk] + row * p.ld_dk[rk] + kvh * D : nullptr,
+      attn_store_rows(lanes + kColK, hf * (D / 2), D / 2, p.scale, live ? p.dk[rk] + row * p.ld_dk[rk] + kvh * D : nullptr,
                  w.n == 0);
     }
   }
@@ -496,12 +403,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
       }
       for (int i = 0; ok && i < n; ++i) {
         const int ks = i % kKStages, vs = i % kVStages;
-        ok = warp_wait(&ctl->k_empty[ks], ((i / kKStages) & 1) ^ 1, p, kSiteEmpty, lane) &&
+        ok = attn_wait(&ctl->k_empty[ks], ((i / kKStages) & 1) ^ 1, p, kSiteEmpty, lane) &&
              load_summed<D>(p, &p.maps[p.P + rk], smem + L::k + ks * L::tile, &ctl->k_full[ks], &ctl->fix, fix_uses,
                             kvh * D, b.k0 + i * kBlk, b.k_len - i * kBlk, lane);
         if (!ok) break;
         k_armed = i + 1;
-        ok = warp_wait(&ctl->v_empty[vs], ((i / kVStages) & 1) ^ 1, p, kSiteEmpty, lane);
+        ok = attn_wait(&ctl->v_empty[vs], ((i / kVStages) & 1) ^ 1, p, kSiteEmpty, lane);
         if (!ok) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(&ctl->v_full[vs], L::tile);
@@ -510,11 +417,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
         v_armed = i + 1;
       }
       if (!ok && lane == 0) {  // wait for the copies in flight
-        mbar_wait_drain(&ctl->q_full, 0, kDrainNs);
+        mbar_wait_drain(&ctl->q_full, 0, kAttnDrainNs);
         for (int i = k_armed - kKStages < 0 ? 0 : k_armed - kKStages; i < k_armed; ++i)
-          mbar_wait_drain(&ctl->k_full[i % kKStages], (i / kKStages) & 1, kDrainNs);
+          mbar_wait_drain(&ctl->k_full[i % kKStages], (i / kKStages) & 1, kAttnDrainNs);
         for (int i = v_armed - kVStages < 0 ? 0 : v_armed - kVStages; i < v_armed; ++i)
-          mbar_wait_drain(&ctl->v_full[i % kVStages], (i / kVStages) & 1, kDrainNs);
+          mbar_wait_drain(&ctl->v_full[i % kVStages], (i / kVStages) & 1, kAttnDrainNs);
       }
     } else if (warp == 1 && lane == 0 && n > 0) {  // ---- MMAs
       const uint32_t qa = sbase + L::q, da = sbase + L::d_o;
@@ -554,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
         umma_commit(&ctl->acc_full);
       } else if (issued) {
         umma_commit(&ctl->drain);
-        mbar_wait_drain(&ctl->drain, 0, kDrainNs);
+        mbar_wait_drain(&ctl->drain, 0, kAttnDrainNs);
       }
     }
   } else {  // ---- P and dS
@@ -574,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
     bool ok = true;
     for (int i = 0; i < n; ++i) {
       const uint32_t buf = lanes + (i & 1) * 128 + hf * 64;
-      ok = warp_wait(&ctl->s_full[i & 1], (i >> 1) & 1, p, kSiteTmemFull, lane);
+      ok = attn_wait(&ctl->s_full[i & 1], (i >> 1) & 1, p, kSiteTmemFull, lane);
       if (!ok) break;
       tc_fence_after();
       float s[64];
@@ -586,12 +493,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
         s[k] = fast_exp2(x0);
         s[k + 1] = fast_exp2(x1);
       }
-      ok = warp_wait(&ctl->dp_full, i & 1, p, kSiteTmemFull, lane);
+      ok = attn_wait(&ctl->dp_full, i & 1, p, kSiteTmemFull, lane);
       if (!ok) break;
       tc_fence_after();
       float dp[64];
       load64(lanes + kColDp + hf * 64, dp);
-      publish(&ctl->dp_free, lane);
+      attn_publish(&ctl->dp_free, lane);
 #pragma unroll
       for (int k = 0; k < 64; ++k) s[k] = s[k] * (dp[k] - delta);
       if ((i + 1) * kBlk > all) {  // keys that this row does not see: whatever they hold
@@ -601,13 +508,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
           if (k >= upto) s[k] = 0.f;
       }
       store64_bf16(buf, s);
-      publish(&ctl->ds_full, lane);
+      attn_publish(&ctl->ds_full, lane);
     }
-    if (ok && n > 0) ok = warp_wait(&ctl->acc_full, 0, p, kSiteDrain, lane);
+    if (ok && n > 0) ok = attn_wait(&ctl->acc_full, 0, p, kSiteDrain, lane);
     if (ok) {
       tc_fence_after();
       const int64_t row = b.q0 + query;
-      store_rows(lanes + kColDq, hf * (D / 2), D / 2, p.scale, live ? p.dq[rk] + row * p.ld_dq[rk] + h * D : nullptr,
+      attn_store_rows(lanes + kColDq, hf * (D / 2), D / 2, p.scale, live ? p.dq[rk] + row * p.ld_dq[rk] + h * D : nullptr,
                  n == 0);
     }
   }

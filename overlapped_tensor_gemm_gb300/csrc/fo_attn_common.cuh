@@ -100,8 +100,6 @@ __host__ __device__ __forceinline__ int query_begin(int causal, int k, int q_len
 struct TrainArgs {
   // per rank r: Q = r, K = P + r, V = 2P + r, dO = 3P + r (boxes of 64 columns x 128 rows)
   CUtensorMap maps[4 * kMaxP];
-  const uint16_t *q[kMaxP], *k[kMaxP], *v[kMaxP];
-  int64_t ld_q[kMaxP], ld_k[kMaxP], ld_v[kMaxP];
   const uint16_t *o[kMaxP], *d_o[kMaxP];
   uint16_t *out_o[kMaxP], *dq[kMaxP], *dk[kMaxP], *dv[kMaxP];
   float* lse[kMaxP];
@@ -115,6 +113,104 @@ struct TrainArgs {
   uint32_t* ctrl;
 };
 
+constexpr uint64_t kAttnDrainNs = 200ull * 1000 * 1000;
+constexpr float kLog2e = 1.4426950408889634f;
+
+constexpr int kBlk = 128;                     // queries or keys per block
+constexpr uint32_t kHalf = kBlk * 128;        // 64 columns of a block: 128 rows of one 128-byte swizzle atom
+__device__ __forceinline__ bool attn_wait(uint64_t* bar, uint32_t parity, const TrainArgs& p, uint32_t site, int lane) {
+  uint32_t ok = 0;
+  if (lane == 0) ok = mbar_wait_fast(bar, parity, p.ctrl, p.timeout_ns, site, blockIdx.x) ? 1u : 0u;
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
+// One block of a [rows, heads * D] matrix: D / 64 boxes of 64 columns, one after the other
+template <int D>
+__device__ __forceinline__ void load_block(const CUtensorMap* map, uint8_t* dst, uint64_t* bar, int col, int row) {
+#pragma unroll
+  for (int c = 0; c < D / 64; ++c) tma_load_2d(map, dst + c * kHalf, bar, col + c * 64, row);
+}
+
+// Loads a block whose rows are terms of a sum; called by a whole warp.  The block's `full`
+// barrier completes once it is in place; with rows behind the sequence (valid < 128) the load
+// completes on `fix` first and the rows are cleared.  False when that wait gave up.
+template <int D>
+__device__ bool load_summed(const TrainArgs& p, const CUtensorMap* map, uint8_t* dst, uint64_t* full, uint64_t* fix,
+                            uint32_t& fix_uses, int col, int row, int valid, int lane) {
+  uint64_t* bar = valid < kBlk ? fix : full;
+  if (lane == 0) {
+    mbar_arrive_expect_tx(bar, D / 64 * kHalf);
+    load_block<D>(map, dst, bar, col, row);
+  }
+  if (valid >= kBlk) return true;
+  const uint32_t parity = fix_uses & 1u;
+  ++fix_uses;
+  if (!attn_wait(fix, parity, p, kSiteFull, lane)) {
+    if (lane == 0) mbar_wait_drain(fix, parity, kAttnDrainNs);
+    return false;
+  }
+  for (int c = 0; c < D / 64; ++c)
+    for (int i = valid * 8 + lane; i < kBlk * 8; i += 32)
+      *reinterpret_cast<uint4*>(dst + c * kHalf + i * 16) = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_shared();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(full);
+  return true;
+}
+
+// D[128 x 128] = A B^T over the D head dimensions, both operands K-major tiles
+template <int D>
+__device__ __forceinline__ void issue_scores(uint32_t d_tmem, uint32_t a, uint32_t b) {
+  constexpr uint32_t idesc = umma_idesc_bf16(128, 128);
+#pragma unroll
+  for (int k = 0; k < D / 16; ++k) {
+    const uint32_t off = (k >> 2) * kHalf + (k & 3) * 32;
+    umma_bf16_ss(d_tmem, umma_sdesc_sw128(a + off), umma_sdesc_sw128(b + off), idesc, k > 0 ? 1u : 0u);
+  }
+}
+// D[128 x D] += A B over 128 summed rows: A bf16 in TMEM (rows 64h + 2c, 64h + 2c + 1 of the sum
+// in column kGap h + c), B the tile's rows as they lie (MN-major)
+template <int D, int kGap = 64>
+__device__ __forceinline__ void issue_grad(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, bool first) {
+  constexpr uint32_t idesc = umma_idesc_bf16_bmn(128, D);
+#pragma unroll
+  for (int k = 0; k < kBlk / 16; ++k)
+    umma_ts(d_tmem, a_tmem + (k >> 2) * kGap + (k & 3) * 8, umma_sdesc_sw128_mn(b + k * 2048, kHalf), idesc,
+            first && k == 0 ? 0u : 1u);
+}
+
+__device__ __forceinline__ void attn_publish(uint64_t* bar, int lane) {
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
+// A warp's 32 accumulator rows, columns [col0, col0 + n), times `scale`, as bf16 to `row` (null:
+// not stored); zero: nothing was accumulated
+__device__ __forceinline__ void attn_store_rows(uint32_t taddr, int col0, int n, float scale, uint16_t* row, bool zero) {
+  for (int c = col0; c < col0 + n; c += 32) {
+    uint32_t v[32];
+    if (zero) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) v[k] = 0u;
+    } else {
+      tmem_ld32(taddr + c, v);
+      tmem_wait_ld();
+    }
+    if (!row) continue;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      st_v4_u32(row + c + 8 * k,
+                pack_bf16x2(__uint_as_float(v[8 * k + 0]) * scale, __uint_as_float(v[8 * k + 1]) * scale),
+                pack_bf16x2(__uint_as_float(v[8 * k + 2]) * scale, __uint_as_float(v[8 * k + 3]) * scale),
+                pack_bf16x2(__uint_as_float(v[8 * k + 4]) * scale, __uint_as_float(v[8 * k + 5]) * scale),
+                pack_bf16x2(__uint_as_float(v[8 * k + 6]) * scale, __uint_as_float(v[8 * k + 7]) * scale));
+  }
+}
+
+// fo_attn_fwd.cu
+cudaError_t attn_fwd_configure();
+cudaError_t attn_fwd_launch(const TrainArgs& a, int dim, cudaStream_t s);
 // fo_attn_bwd.cu
 cudaError_t attn_bwd_configure();
 cudaError_t attn_delta_launch(const TrainArgs& a, int dim, cudaStream_t s);

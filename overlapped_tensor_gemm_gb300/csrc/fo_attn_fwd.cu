@@ -1,0 +1,286 @@
+// Attention forward with row statistics on the tensor cores (tcgen05, accumulators in TMEM):
+// one pass over the keys with the running maximum and sum of the softmax.
+//
+// A CTA takes 256 queries of one head as two tiles of 128 that share every K and V block, so a
+// block is loaded once per 256 queries and one tile's softmax runs while the tensor pipe works
+// for the other.  384 threads, one CTA per SM: warp 0 loads (TMA), warp 1 issues the MMAs, warps
+// 4-7 and 8-11 are the softmax of tile 0 and tile 1 (a thread holds a whole query row: no
+// exchange between threads).
+//
+// TMEM: tile t's scores [128 t, 128 t + 128), overwritten in its first half by their bf16
+// weights, which the product with V reads as its A operand; tile t's output [256 + 128 t, + D).
+// Per tile and block the one issuing thread issues P V of block j, then the scores of block
+// j + 1 over the same columns: a CTA's MMAs execute in issue order.
+//
+// The output is rescaled only where a row's maximum grew by more than 2^8 since the last time
+// (the sum and the final division use the same reference, so this is exact); the weights, at
+// most 2^8, enter the product with V as bf16: half a step, 2^-9 of a weight's binade, as for any
+// bf16 operand, averaged over the keys.
+#include <cuda_bf16.h>
+
+#include "fo_attn_common.cuh"
+#include "fo_internal.h"
+#include "fo_ptx.cuh"
+
+namespace fo {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kTileWarps = 4;
+constexpr uint32_t kTmem = 512;
+constexpr uint32_t kColO = 256;
+constexpr int kKStages = 3, kVStages = 2;
+constexpr float kRescale = 8.0f;  // log2 units
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <int D>
+struct Smem {
+  static constexpr uint32_t tile = D / 64 * kHalf;
+  static constexpr uint32_t q = 0, k = 2 * tile, v = k + kKStages * tile, ctl = v + kVStages * tile;
+};
+struct alignas(8) Ctl {
+  uint64_t q_full[2], k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
+  uint64_t s_full[2], p_full[2], o_done[2], fix, drain;
+  uint32_t tmem_base, pad;
+};
+template <int D>
+constexpr int smem_bytes() {
+  return static_cast<int>(Smem<D>::ctl + sizeof(Ctl) + 1024);
+}
+static_assert(smem_bytes<128>() <= 232448, "shared memory of one CTA");
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_constant__ TrainArgs p) {
+  using L = Smem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + L::ctl);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hp = p.heads * p.P, ph = blockIdx.x % hp, rk = ph / p.heads, h = ph % p.heads;
+  Block b;
+  if (!block_at(p.blocks, blockIdx.x / hp, &b)) return;
+  const int kvh = h / (p.heads / p.kv_heads);
+  // first query of each tile and the key blocks it walks
+  int q0[2], n[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    q0[t] = b.blk * 2 * kBlk + t * kBlk;
+    const int end = q0[t] + kBlk < b.q_len ? q0[t] + kBlk : b.q_len;
+    n[t] = q0[t] < b.q_len ? (key_end(p.blocks.causal, end, b.q_len, b.k_len) + kBlk - 1) / kBlk : 0;
+  }
+  const int nmax = n[0] > n[1] ? n[0] : n[1];
+
+  if (threadIdx.x == 0) {
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&ctl->q_full[t], 1);
+      mbar_init(&ctl->s_full[t], 1);
+      mbar_init(&ctl->p_full[t], kTileWarps);
+      mbar_init(&ctl->o_done[t], 1);
+    }
+    for (int s = 0; s < kKStages; ++s) {
+      mbar_init(&ctl->k_full[s], 1);
+      mbar_init(&ctl->k_empty[s], 1);
+    }
+    for (int s = 0; s < kVStages; ++s) {
+      mbar_init(&ctl->v_full[s], 1);
+      mbar_init(&ctl->v_empty[s], 1);
+    }
+    mbar_init(&ctl->fix, 1);
+    mbar_init(&ctl->drain, 1);
+    fence_barrier_init();
+    fence_proxy_async_shared();
+  }
+  if (warp == 1) {
+    tmem_alloc(&ctl->tmem_base, kTmem);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+  const uint32_t sbase = smem_u32(smem);
+
+  if (warp == 0) {  // ---- loads
+    uint32_t fix_uses = 0;
+    int k_armed = 0, v_armed = 0;
+    bool ok = true;
+    if (lane == 0)
+      for (int t = 0; t < 2; ++t)
+        if (n[t] > 0) {
+          mbar_arrive_expect_tx(&ctl->q_full[t], L::tile);
+          load_block<D>(&p.maps[rk], smem + L::q + t * L::tile, &ctl->q_full[t], h * D, b.q0 + q0[t]);
+        }
+    for (int j = 0; ok && j < nmax; ++j) {
+      const int ks = j % kKStages, vs = j % kVStages;
+      ok = attn_wait(&ctl->k_empty[ks], ((j / kKStages) & 1) ^ 1, p, kSiteEmpty, lane);
+      if (!ok) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&ctl->k_full[ks], L::tile);
+        load_block<D>(&p.maps[p.P + rk], smem + L::k + ks * L::tile, &ctl->k_full[ks], kvh * D, b.k0 + j * kBlk);
+      }
+      k_armed = j + 1;
+      ok = attn_wait(&ctl->v_empty[vs], ((j / kVStages) & 1) ^ 1, p, kSiteEmpty, lane) &&
+           load_summed<D>(p, &p.maps[2 * p.P + rk], smem + L::v + vs * L::tile, &ctl->v_full[vs], &ctl->fix, fix_uses,
+                          kvh * D, b.k0 + j * kBlk, b.k_len - j * kBlk, lane);
+      if (ok) v_armed = j + 1;
+    }
+    if (!ok && lane == 0) {  // wait for the copies in flight
+      for (int t = 0; t < 2; ++t)
+        if (n[t] > 0) mbar_wait_drain(&ctl->q_full[t], 0, kAttnDrainNs);
+      for (int j = k_armed - kKStages < 0 ? 0 : k_armed - kKStages; j < k_armed; ++j)
+        mbar_wait_drain(&ctl->k_full[j % kKStages], (j / kKStages) & 1, kAttnDrainNs);
+      for (int j = v_armed - kVStages < 0 ? 0 : v_armed - kVStages; j < v_armed; ++j)
+        mbar_wait_drain(&ctl->v_full[j % kVStages], (j / kVStages) & 1, kAttnDrainNs);
+    }
+  } else if (warp == 1 && lane == 0 && nmax > 0) {  // ---- MMAs
+    bool ok = true, issued = false;
+    auto scores = [&](int t, int j) -> bool {
+      if (!mbar_wait_fast(&ctl->k_full[j % kKStages], (j / kKStages) & 1, p.ctrl, p.timeout_ns, kSiteFull, blockIdx.x))
+        return false;
+      tc_fence_after();
+      issue_scores<D>(tmem + t * 128, sbase + L::q + t * L::tile, sbase + L::k + (j % kKStages) * L::tile);
+      umma_commit(&ctl->s_full[t]);
+      issued = true;
+      return true;
+    };
+    for (int t = 0; ok && t < 2; ++t)
+      if (n[t] > 0)
+        ok = mbar_wait_fast(&ctl->q_full[t], 0, p.ctrl, p.timeout_ns, kSiteFull, blockIdx.x) && scores(t, 0);
+    if (ok) umma_commit(&ctl->k_empty[0]);
+    for (int j = 0; ok && j < nmax; ++j) {
+      const int vs = j % kVStages;
+      ok = mbar_wait_fast(&ctl->v_full[vs], (j / kVStages) & 1, p.ctrl, p.timeout_ns, kSiteFull, blockIdx.x);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (!ok || j >= n[t]) continue;
+        ok = mbar_wait_fast(&ctl->p_full[t], j & 1, p.ctrl, p.timeout_ns, kSiteTmemFull, blockIdx.x);
+        if (!ok) continue;
+        tc_fence_after();
+        issue_grad<D, 32>(tmem + kColO + t * 128, tmem + t * 128, sbase + L::v + vs * L::tile, j == 0);
+        umma_commit(&ctl->o_done[t]);
+        if (j + 1 < n[t]) ok = scores(t, j + 1);
+      }
+      if (!ok) break;
+      umma_commit(&ctl->v_empty[vs]);
+      if (j + 1 < nmax) umma_commit(&ctl->k_empty[(j + 1) % kKStages]);
+    }
+    if (!ok && issued) {
+      umma_commit(&ctl->drain);
+      mbar_wait_drain(&ctl->drain, 0, kAttnDrainNs);
+    }
+  } else if (warp >= 4) {  // ---- softmax
+    const int t = (warp - 4) >> 2, quad = warp & 3;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const uint32_t sc = lanes + t * 128, oc = lanes + kColO + t * 128;
+    const int query = q0[t] + quad * 32 + lane;
+    const int see = query < b.q_len ? key_end(p.blocks.causal, query + 1, b.q_len, b.k_len) : 0;  // keys of this row
+    const int all = key_end(p.blocks.causal, q0[t] + 1, b.q_len, b.k_len);                        // of the tile's first row
+    const uint64_t c2 = pack2(p.scale_log2, p.scale_log2);
+    float m_ref = -INFINITY;
+    uint64_t sum = pack2(0.f, 0.f);
+    bool ok = true;
+    for (int j = 0; j < n[t]; ++j) {
+      ok = attn_wait(&ctl->s_full[t], j & 1, p, kSiteTmemFull, lane);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t w[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(sc + c * 32, w[c]);
+      tmem_wait_ld();
+      float s[128];
+#pragma unroll
+      for (int k = 0; k < 128; ++k) s[k] = __uint_as_float(w[k >> 5][k & 31]);
+      if ((j + 1) * kBlk > all) {  // keys that this row does not see: whatever they hold
+        const int upto = see - j * kBlk;
+#pragma unroll
+        for (int k = 0; k < 128; ++k)
+          if (k >= upto) s[k] = -INFINITY;
+      }
+      float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int k = 0; k < 64; ++k) mq[k & 3] = fmax3(mq[k & 3], s[2 * k], s[2 * k + 1]);
+      const float mx = fmax3(fmaxf(mq[0], mq[1]), mq[2], mq[3]) * p.scale_log2;
+      float alpha = 1.f;
+      if (j == 0) {
+        m_ref = mx;
+      } else if (mx > m_ref + kRescale) {
+        alpha = fast_exp2(m_ref - mx);
+        m_ref = mx;
+      }
+      if (__any_sync(0xffffffffu, alpha != 1.f)) {
+        sum = ffma2(sum, pack2(alpha, alpha), pack2(0.f, 0.f));
+        // the output must hold every earlier block before it is rescaled
+        ok = attn_wait(&ctl->o_done[t], (j - 1) & 1, p, kSiteDrain, lane);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t v[32];
+          tmem_ld32(oc + c, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
+          tmem_st32(oc + c, v);
+        }
+      }
+      const float m = m_ref == -INFINITY ? 0.f : m_ref;  // a row without keys: every weight 0
+      const uint64_t nm = pack2(-m, -m);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t packed[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          float x0, x1;
+          unpack2(ffma2(pack2(s[c * 64 + 2 * k], s[c * 64 + 2 * k + 1]), c2, nm), x0, x1);
+          const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
+          packed[k] = pack_bf16x2(e0, e1);
+          sum = fadd2(sum, pack2(e0, e1));
+        }
+        tmem_st32(sc + c * 32, packed);
+      }
+      tmem_wait_st();
+      attn_publish(&ctl->p_full[t], lane);
+    }
+    if (ok && n[t] > 0) ok = attn_wait(&ctl->o_done[t], (n[t] - 1) & 1, p, kSiteDrain, lane);
+    if (ok && q0[t] < b.q_len) {
+      tc_fence_after();
+      float lo, hi;
+      unpack2(sum, lo, hi);
+      const float l = lo + hi;
+      const bool live = query < b.q_len;
+      const int64_t row = b.q0 + query;
+      if (live) p.lse[rk][h * p.ld_lse[rk] + row] = l > 0.f ? fmaf(m_ref, kLn2, logf(l)) : -INFINITY;
+      attn_store_rows(oc, 0, D, l > 0.f ? 1.f / l : 0.f, live ? p.out_o[rk] + row * p.ld_o[rk] + h * D : nullptr,
+                      n[t] == 0);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmem);
+  }
+}
+
+}  // namespace
+
+cudaError_t attn_fwd_configure() {
+  cudaError_t e = cudaFuncSetAttribute(attn_fwd_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<64>());
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(attn_fwd_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<128>());
+  return e;
+}
+
+cudaError_t attn_fwd_launch(const TrainArgs& a, int dim, cudaStream_t s) {
+  const unsigned grid = static_cast<unsigned>(a.blocks.count) * a.heads * a.P;
+  if (grid == 0) return cudaSuccess;
+  if (dim == 64) {
+    attn_fwd_kernel<64><<<grid, kThreads, smem_bytes<64>(), s>>>(a);
+  } else {
+    attn_fwd_kernel<128><<<grid, kThreads, smem_bytes<128>(), s>>>(a);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace fo

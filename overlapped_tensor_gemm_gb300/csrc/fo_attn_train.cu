@@ -101,53 +101,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
 }
 
 // ---------------------------------------------------------------------------
-// Plain kernels: one warp per query row (forward, dQ) or key row (dK / dV), a lane holds
-// head_dim / 32 dimensions.
-// ---------------------------------------------------------------------------
-constexpr int kPlainUnit = 32;
-
-__device__ __forceinline__ float bf(const uint16_t* p) { return __uint_as_float(static_cast<uint32_t>(*p) << 16); }
-__device__ __forceinline__ uint16_t to_bf(float f) { return static_cast<uint16_t>(pack_bf16x2(f, 0.f) & 0xFFFFu); }
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
-template <int D>
-__global__ void plain_fwd_kernel(const __grid_constant__ TrainArgs a) {
-  constexpr int N = D / 32;
-  const int lane = threadIdx.x & 31, hp = a.heads * a.P;
-  const int ph = blockIdx.x % hp, rk = ph / a.heads, h = ph % a.heads, kvh = h / (a.heads / a.kv_heads);
-  Block b;
-  if (!block_at(a.blocks, blockIdx.x / hp, &b)) return;
-  for (int i = b.blk * kPlainUnit + (threadIdx.x >> 5); i < (b.blk + 1) * kPlainUnit && i < b.q_len;
-       i += blockDim.x >> 5) {
-    const int64_t row = b.q0 + i;
-    float q[N], acc[N], m = -INFINITY, l = 0.f;
-    for (int d = 0; d < N; ++d) {
-      q[d] = bf(a.q[rk] + row * a.ld_q[rk] + h * D + d * 32 + lane);
-      acc[d] = 0.f;
-    }
-    const int nk = key_end(a.blocks.causal, i + 1, b.q_len, b.k_len);
-    for (int j = 0; j < nk; ++j) {
-      const int64_t kr = b.k0 + j;
-      float s = 0.f;
-      for (int d = 0; d < N; ++d) s += q[d] * bf(a.k[rk] + kr * a.ld_k[rk] + kvh * D + d * 32 + lane);
-      s = warp_sum(s) * a.scale;
-      const float mn = fmaxf(m, s), c = expf(m - mn), p = expf(s - mn);
-      l = l * c + p;
-      m = mn;
-      for (int d = 0; d < N; ++d)
-        acc[d] = acc[d] * c + p * bf(a.v[rk] + kr * a.ld_v[rk] + kvh * D + d * 32 + lane);
-    }
-    for (int d = 0; d < N; ++d)
-      a.out_o[rk][row * a.ld_o[rk] + h * D + d * 32 + lane] = to_bf(nk > 0 ? acc[d] / l : 0.f);
-    if (lane == 0) a.lse[rk][h * a.ld_lse[rk] + row] = nk > 0 ? m + logf(l) : -INFINITY;
-  }
-}
-
-// ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
 
@@ -267,6 +220,7 @@ fo_status make_blocks(fo_ctx* ctx, const Call& c, const Cut* cuts, int n, cudaSt
   return e == cudaSuccess ? FO_OK : host_fail(FO_ERR_CUDA, cudaGetErrorString(e));
 }
 
+// pointers and row pitches of P matrices
 template <typename T>
 void fill(const fo_mat* list, int P, T** ptr, int64_t* ld) {
   for (int r = 0; r < P; ++r) {
@@ -275,7 +229,7 @@ void fill(const fo_mat* list, int P, T** ptr, int64_t* ld) {
   }
 }
 
-constexpr int kBlk = 128;  // rows of a tensor map's box
+constexpr int kFwdUnit = 256;  // query rows of a forward block: two tiles
 
 // Operand map of a [rows, cols] matrix, read in blocks of 128 rows; an empty matrix has none
 // (its call has no block that reads it)
@@ -289,9 +243,6 @@ fo_status add_maps(CUtensorMap* maps, const fo_mat* list, int P) {
 fo_status fill_args(fo_ctx* ctx, const Call& c, const fo_mat* Q, const fo_mat* K, const fo_mat* V,
                     const fo_opts* opts, TrainArgs* a) {
   std::memset(a, 0, sizeof(*a));
-  fill(Q, c.P, a->q, a->ld_q);
-  fill(K, c.P, a->k, a->ld_k);
-  fill(V, c.P, a->v, a->ld_v);
   FO_TRY_HOST(add_maps(a->maps, Q, c.P));
   FO_TRY_HOST(add_maps(a->maps + c.P, K, c.P));
   FO_TRY_HOST(add_maps(a->maps + 2 * c.P, V, c.P));
@@ -308,7 +259,8 @@ fo_status fill_args(fo_ctx* ctx, const Call& c, const fo_mat* Q, const fo_mat* K
   a->ctrl = host_ctrl(ctx);
   static bool configured = false;
   if (!configured) {
-    const cudaError_t e = attn_bwd_configure();
+    cudaError_t e = attn_fwd_configure();
+    if (e == cudaSuccess) e = attn_bwd_configure();
     if (e != cudaSuccess) return host_fail(FO_ERR_CUDA, "attention kernel configuration failed");
     configured = true;
   }
@@ -340,15 +292,9 @@ fo_status fo_attn_forward(fo_ctx* ctx, const fo_mat* Q, const fo_mat* K, const f
   FO_TRY_HOST(fill_args(ctx, c, Q, K, V, opts, &a));
   fill(O, P, a.out_o, a.ld_o);
   fill(LSE, P, a.lse, a.ld_lse);
-  const Cut cut = {kPlainUnit, false};
+  const Cut cut = {kFwdUnit, false};
   FO_TRY_HOST(make_blocks(ctx, c, &cut, 1, s, &a.blocks));
-  const unsigned grid = static_cast<unsigned>(a.blocks.count) * heads * P;
-  if (head_dim == 64) {
-    plain_fwd_kernel<64><<<grid, 256, 0, s>>>(a);
-  } else {
-    plain_fwd_kernel<128><<<grid, 256, 0, s>>>(a);
-  }
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = attn_fwd_launch(a, head_dim, s);
   return e == cudaSuccess ? FO_OK : host_fail(FO_ERR_CUDA, cudaGetErrorString(e));
 }
 
