@@ -392,8 +392,8 @@ FO_API fo_status fo_attn_backward(fo_ctx* ctx, const fo_mat* Q, const fo_mat* K,
                                   int kv_heads, int head_dim, const fo_attn_mask* mask, const fo_mat* dQ,
                                   const fo_mat* dK, const fo_mat* dV, const fo_opts* opts, void* stream);
 
-/* Parameters of the norms around a block: vectors are [1, H] matrices (bf16 or fp32 each),
- * null where the call has none. */
+/* Parameters of the norms around a block: vectors are [1, H] matrices, null where the call has
+ * none; all of one type, bf16 or fp32. */
 typedef struct {
   const fo_mat* w_post;       /* weight of the norm of the block's output (null: no such norm) */
   const fo_mat* w_pre;        /* weight of the norm in front of the next block (null: none)    */

@@ -166,6 +166,17 @@ def mat(t) -> FoMat:
     return FoMat(t.data_ptr(), dt, 0, t.shape[0], t.shape[1], max(ld, t.shape[1]))
 
 
+_MAT_ARRAYS = [FoMat * n for n in range(65)]  # array types by length
+_DTYPE_CODES: dict = {}
+
+
+def _dtype_codes() -> dict:
+    if not _DTYPE_CODES:
+        import torch
+        _DTYPE_CODES.update({torch.bfloat16: FO_BF16, torch.float32: FO_F32})
+    return _DTYPE_CODES
+
+
 def _pad_ld(a: FoMat) -> FoMat:
     """A one-row matrix of any width: its (unused) row pitch as a whole number of 16 bytes."""
     a.ld = -(-a.ld // 8) * 8
@@ -327,17 +338,26 @@ class Context:
 
     # -- training operators ------------------------------------------------------------------
 
-    def _list(self, ts, P: int, what: str, keep=None):
+    def _list(self, ts, P: int, what: str):
         """P matrices on the context's device (None stays None)."""
         if ts is None:
             return None
-        if len(ts) != P:
+        if len(ts) != P or P >= len(_MAT_ARRAYS):
             raise ValueError(f"{what}: {len(ts)} matrices for {P} ranks")
-        for t in ts:
-            self._here(t, what)
-        arr = _mats(ts)
-        if arr[0].rows == 1:
-            for a in arr:
+        arr = _MAT_ARRAYS[P]()
+        for a, t in zip(arr, ts):
+            if t.get_device() != self.device:
+                self._here(t, what)
+            dt = _dtype_codes().get(t.dtype)
+            if dt is None or t.dim() != 2:
+                m = mat(t)
+                a.ptr, a.dtype, a.rows, a.cols, a.ld = m.ptr, m.dtype, m.rows, m.cols, m.ld
+            else:
+                (rows, cols), (ld, unit) = t.shape, t.stride()
+                if unit != 1 and cols > 1:
+                    raise ValueError("need a row-major 2-D view (unit column stride)")
+                a.ptr, a.dtype, a.rows, a.cols, a.ld = t.data_ptr(), dt, rows, cols, max(ld, cols) if rows > 1 else cols
+            if a.rows == 1:
                 _pad_ld(a)
         return arr
 

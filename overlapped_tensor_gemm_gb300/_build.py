@@ -18,7 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfo.so")
 SOURCES = ["fo_api.cu", "fo_gemm.cu", "fo_gemm2.cu", "fo_attn.cu", "fo_elem.cu", "fo_static.cu",
-           "fo_norm.cu", "fo_rope.cu", "fo_attn_train.cu", "fo_attn_fwd.cu", "fo_attn_bwd.cu"]
+           "fo_norm.cu", "fo_norm_fwd.cu", "fo_norm_bwd.cu", "fo_rope.cu", "fo_attn_train.cu", "fo_attn_fwd.cu", "fo_attn_bwd.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden", "--expt-relaxed-constexpr"]
 

@@ -1,374 +1,13 @@
-// Norms before and after a block, fused with its gate and residual scale, and their backward.
-//
-//   z  = Y w_post / rms(Y)            (z = Y without a post norm),  rms(v) = sqrt(mean(v^2) + eps)
-//   R' = a R + g z                    (the residual stream after the block)
-//   X  = R' w_pre / rms(R')           (the next block's input)
-//
-// backward, from X's gradient dX and the gradient dR' that reaches R' by its other uses, with
-// n = R' / rms(R'), u = Y / rms(Y):
-//   t  = dR' + (dX w_pre - n mean(dX w_pre n)) / rms(R'),   dw_pre = sum_tokens dX n
-//   dR = a t,   dg = t z (summed over tokens where g is one row),   dz = g t
-//   dw_post = sum_tokens dz u,   dY = (dz w_post - u mean(dz w_post u)) / rms(Y)
-//
-// Both directions are bound by HBM: every matrix is read once and written once, a row stays in
-// its threads' registers between the reductions and the stores.  `tpr` threads share a row,
-// each with C groups of 8 columns (8-column group i*tpr + t); all arithmetic is fp32, each
-// output is rounded once to its type (X from the unrounded R').
-#include <cuda_bf16.h>
-
+// Norms before and after a block with gate and residual: argument checks, launch plans and the
+// sums over tokens (formulas in fo_norm.cuh).
 #include <cmath>
 #include <cstring>
 
 #include "fo_host.h"
-#include "fo_internal.h"
-#include "fo_ptx.cuh"
+#include "fo_norm.cuh"
 
 namespace fo {
 namespace {
-
-constexpr int kNormMaxCols = 16384;
-constexpr int kNormThreads = 256;  // threads of a CTA where a row needs fewer
-
-enum GateMode : int32_t { kGateNone = 0, kGateRow = 1, kGateToken = 2 };
-
-struct NormArgs {
-  const void* r[kMaxP];       // residual stream in (backward: R', after the block)
-  const void* y[kMaxP];       // block output
-  const void* gate[kMaxP];    // kGateToken: [m, H]; kGateRow: gate[0], one row
-  void* r_out[kMaxP];         // forward: R'; backward: dR
-  void* x[kMaxP];             // forward: X; backward: dY
-  const void* dx[kMaxP];
-  const void* dr_out[kMaxP];
-  void* dgate[kMaxP];         // kGateToken
-  int64_t ld_r[kMaxP], ld_y[kMaxP], ld_gate[kMaxP], ld_r_out[kMaxP], ld_x[kMaxP], ld_dx[kMaxP], ld_dr_out[kMaxP],
-      ld_dgate[kMaxP];
-  const void* w_post;
-  const void* w_pre;
-  int64_t m, total_rows;      // rows per rank, rows of all ranks
-  int32_t cols, tpr, gate_mode;
-  int32_t gate_f32, post_f32, pre_f32;  // types of the parameters (1: fp32, 0: bf16)
-  float alpha, eps;
-  float* part;                // backward: [grid][3][cols] column sums (pre, gate, post)
-};
-
-// 8 columns of a row from column c on, the first n of them inside the row (n >= 1)
-__device__ __forceinline__ void load8(const uint16_t* p, int n, float (&v)[8]) {
-  if (n >= 8) {
-    const uint4 w = *reinterpret_cast<const uint4*>(p);
-    const uint32_t q[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[2 * k] = __uint_as_float(q[k] << 16);
-      v[2 * k + 1] = __uint_as_float(q[k] & 0xFFFF0000u);
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = k < n ? __uint_as_float(static_cast<uint32_t>(p[k]) << 16) : 0.f;
-  }
-}
-__device__ __forceinline__ void load8(const float* p, int n, float (&v)[8]) {
-  if (n >= 8) {
-    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = k < n ? p[k] : 0.f;
-  }
-}
-__device__ __forceinline__ void store8(uint16_t* p, int n, const float (&v)[8]) {
-  if (n >= 8) {
-    st_v4_u32(p, pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (k < n) p[k] = static_cast<uint16_t>(pack_bf16x2(v[k], 0.f) & 0xFFFFu);
-  }
-}
-__device__ __forceinline__ void store8(float* p, int n, const float (&v)[8]) {
-  if (n >= 8) {
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (k < n) p[k] = v[k];
-  }
-}
-template <typename T>
-__device__ __forceinline__ void load8_of(const void* base, int64_t off, int n, float (&v)[8]) {
-  load8(static_cast<const T*>(base) + off, n, v);
-}
-// a parameter of either type (uniform branch; parameters other than per-token gates come from L1/L2)
-__device__ __forceinline__ void load8_par(const void* base, int64_t off, int f32, int n, float (&v)[8]) {
-  if (f32) {
-    load8(static_cast<const float*>(base) + off, n, v);
-  } else {
-    load8(static_cast<const uint16_t*>(base) + off, n, v);
-  }
-}
-__device__ __forceinline__ void store8_par(void* base, int64_t off, int f32, int n, const float (&v)[8]) {
-  if (f32) {
-    store8(static_cast<float*>(base) + off, n, v);
-  } else {
-    store8(static_cast<uint16_t*>(base) + off, n, v);
-  }
-}
-
-constexpr int kSumBuf = 32 * 3;  // one half of row_sum's buffer: 32 warps, at most 3 values
-
-// Sums of N values over the tpr threads of a row; every thread of the CTA takes part.  tpr is
-// 32 or a multiple of it; with more than one warp per row the warps' sums meet in `buf`, of
-// which successive calls use alternate halves (so one barrier per call is enough).
-template <int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], int tpr, float* buf, int& turn) {
-#pragma unroll
-  for (int k = 0; k < N; ++k)
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-  if (tpr == 32) return;
-  float* b = buf + turn * kSumBuf;
-  turn ^= 1;
-  const int warp = threadIdx.x >> 5, wpr = tpr >> 5;
-  if ((threadIdx.x & 31) == 0)
-#pragma unroll
-    for (int k = 0; k < N; ++k) b[warp * N + k] = v[k];
-  __syncthreads();
-  const int w0 = warp / wpr * wpr;
-#pragma unroll
-  for (int k = 0; k < N; ++k) v[k] = 0.f;
-  for (int w = 0; w < wpr; ++w)
-#pragma unroll
-    for (int k = 0; k < N; ++k) v[k] += b[(w0 + w) * N + k];
-}
-
-template <typename TR, typename TA, int C>
-__global__ void __launch_bounds__(1024) norm_fwd_kernel(const __grid_constant__ NormArgs a) {
-  __shared__ float buf[2 * kSumBuf];
-  int turn = 0;
-  const int rpc = blockDim.x / a.tpr, t = threadIdx.x % a.tpr, sub = threadIdx.x / a.tpr;
-  const bool has_y = a.y[0] != nullptr, post = a.w_post != nullptr, pre = a.x[0] != nullptr;
-  const float inv_cols = 1.f / static_cast<float>(a.cols);
-  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * rpc; row0 < a.total_rows;
-       row0 += static_cast<int64_t>(gridDim.x) * rpc) {
-    const int64_t grow = row0 + sub;
-    const bool live = grow < a.total_rows;
-    const int rk = live ? static_cast<int>(grow / a.m) : 0;
-    const int64_t row = live ? grow - rk * a.m : 0;
-    float r[C][8], y[C][8];
-    float ss[1] = {0.f};
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-      const int c = (i * a.tpr + t) * 8, n = live ? a.cols - c : 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) r[i][k] = y[i][k] = 0.f;
-      if (n > 0) {
-        load8_of<TR>(a.r[rk], row * a.ld_r[rk] + c, n, r[i]);
-        if (has_y) load8_of<TA>(a.y[rk], row * a.ld_y[rk] + c, n, y[i]);
-      }
-    }
-    if (has_y) {
-      float inv = 1.f;
-      if (post) {
-#pragma unroll
-        for (int i = 0; i < C; ++i)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) ss[0] = fmaf(y[i][k], y[i][k], ss[0]);
-        row_sum<1>(ss, a.tpr, buf, turn);
-        inv = 1.f / sqrtf(ss[0] * inv_cols + a.eps);
-      }
-#pragma unroll
-      for (int i = 0; i < C; ++i) {
-        const int c = (i * a.tpr + t) * 8, n = live ? a.cols - c : 0;
-        if (n <= 0) continue;
-        if (post) {
-          float w[8];
-          load8_par(a.w_post, c, a.post_f32, n, w);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) y[i][k] = y[i][k] * inv * w[k];
-        }
-        if (a.gate_mode != kGateNone) {
-          float g[8];
-          load8_par(a.gate[a.gate_mode == kGateToken ? rk : 0],
-                    (a.gate_mode == kGateToken ? row * a.ld_gate[rk] : 0) + c, a.gate_f32, n, g);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) y[i][k] *= g[k];
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) r[i][k] = fmaf(a.alpha, r[i][k], y[i][k]);
-        store8(static_cast<TR*>(a.r_out[rk]) + row * a.ld_r_out[rk] + c, n, r[i]);
-      }
-    }
-    if (pre) {
-      ss[0] = 0.f;
-#pragma unroll
-      for (int i = 0; i < C; ++i)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) ss[0] = fmaf(r[i][k], r[i][k], ss[0]);
-      row_sum<1>(ss, a.tpr, buf, turn);
-      const float inv = 1.f / sqrtf(ss[0] * inv_cols + a.eps);
-#pragma unroll
-      for (int i = 0; i < C; ++i) {
-        const int c = (i * a.tpr + t) * 8, n = live ? a.cols - c : 0;
-        if (n <= 0) continue;
-        float w[8];
-        load8_par(a.w_pre, c, a.pre_f32, n, w);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) w[k] = r[i][k] * inv * w[k];
-        store8(static_cast<TA*>(a.x[rk]) + row * a.ld_x[rk] + c, n, w);
-      }
-    }
-  }
-}
-
-template <typename TR, typename TA, int C>
-__global__ void __launch_bounds__(1024) norm_bwd_kernel(const __grid_constant__ NormArgs a) {
-  __shared__ float buf[2 * kSumBuf];
-  extern __shared__ float sums[];  // [rows per CTA][cols]: column sums of the CTA's row groups
-  int turn = 0;
-  const int rpc = blockDim.x / a.tpr, t = threadIdx.x % a.tpr, sub = threadIdx.x / a.tpr;
-  const bool has_y = a.y[0] != nullptr, post = a.w_post != nullptr, pre = a.dx[0] != nullptr;
-  const bool has_dr = a.dr_out[0] != nullptr;
-  const float inv_cols = 1.f / static_cast<float>(a.cols);
-  float acc_pre[C][8], acc_gate[C][8], acc_post[C][8];
-#pragma unroll
-  for (int i = 0; i < C; ++i)
-#pragma unroll
-    for (int k = 0; k < 8; ++k) acc_pre[i][k] = acc_gate[i][k] = acc_post[i][k] = 0.f;
-  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * rpc; row0 < a.total_rows;
-       row0 += static_cast<int64_t>(gridDim.x) * rpc) {
-    const int64_t grow = row0 + sub;
-    const bool live = grow < a.total_rows;
-    const int rk = live ? static_cast<int>(grow / a.m) : 0;
-    const int64_t row = live ? grow - rk * a.m : 0;
-    float r[C][8], y[C][8], dx[C][8], dr[C][8];
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-      const int c = (i * a.tpr + t) * 8, n = live ? a.cols - c : 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) r[i][k] = y[i][k] = dx[i][k] = dr[i][k] = 0.f;
-      if (n > 0) {
-        if (pre) {
-          load8_of<TR>(a.r[rk], row * a.ld_r[rk] + c, n, r[i]);
-          load8_of<TA>(a.dx[rk], row * a.ld_dx[rk] + c, n, dx[i]);
-        }
-        if (has_y) load8_of<TA>(a.y[rk], row * a.ld_y[rk] + c, n, y[i]);
-        if (has_dr) load8_of<TR>(a.dr_out[rk], row * a.ld_dr_out[rk] + c, n, dr[i]);
-      }
-    }
-    // sums of R'^2, dX w_pre R' and Y^2: everything the two norms need before t is known
-    float s3[3] = {0.f, 0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-      const int c = (i * a.tpr + t) * 8, n = live ? a.cols - c : 0;
-      if (n <= 0) continue;
-      if (pre) {
-        float w[8];
-        load8_par(a.w_pre, c, a.pre_f32, n, w);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          s3[0] = fmaf(r[i][k], r[i][k], s3[0]);
-          s3[1] = fmaf(dx[i][k] * w[k], r[i][k], s3[1]);
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) s3[2] = fmaf(y[i][k], y[i][k], s3[2]);
-    }
-    row_sum<3>(s3, a.tpr, buf, turn);
-    const float inv_r = pre ? 1.f / sqrtf(s3[0] * inv_cols + a.eps) : 0.f;
-    const float mean_r = s3[1] * inv_r * inv_cols;  // mean(dX w_pre n)
-    const float inv_y = post ? 1.f / sqrtf(s3[2] * inv_cols + a.eps) : 1.f;
-    float s1[1] = {0.f};
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-      const int c = (i * a.tpr + t) * 8, n = live ? a.cols - c : 0;
-      if (n <= 0) continue;
-      if (pre) {
-        float w[8];
-        load8_par(a.w_pre, c, a.pre_f32, n, w);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float nk = r[i][k] * inv_r;
-          acc_pre[i][k] = fmaf(dx[i][k], nk, acc_pre[i][k]);
-          dr[i][k] = fmaf(inv_r, dx[i][k] * w[k] - nk * mean_r, dr[i][k]);
-        }
-      }
-      float o[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) o[k] = a.alpha * dr[i][k];
-      store8(static_cast<TR*>(a.r_out[rk]) + row * a.ld_r_out[rk] + c, n, o);
-      if (!has_y) continue;
-      // dr = t; y becomes u, dr becomes dz w_post
-      float w[8], g[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) w[k] = g[k] = 1.f;
-      if (post) load8_par(a.w_post, c, a.post_f32, n, w);
-      if (a.gate_mode != kGateNone)
-        load8_par(a.gate[a.gate_mode == kGateToken ? rk : 0],
-                  (a.gate_mode == kGateToken ? row * a.ld_gate[rk] : 0) + c, a.gate_f32, n, g);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        y[i][k] *= inv_y;
-        o[k] = dr[i][k] * (y[i][k] * w[k]);  // t z
-        acc_gate[i][k] += o[k];
-        const float dz = dr[i][k] * g[k];
-        acc_post[i][k] = fmaf(dz, y[i][k], acc_post[i][k]);
-        dr[i][k] = dz * w[k];
-        s1[0] = fmaf(dr[i][k], y[i][k], s1[0]);
-      }
-      if (a.gate_mode == kGateToken)
-        store8_par(a.dgate[rk], row * a.ld_dgate[rk] + c, a.gate_f32, n, o);
-    }
-    if (has_y) {
-      float mean_y = 0.f;
-      if (post) {
-        row_sum<1>(s1, a.tpr, buf, turn);
-        mean_y = s1[0] * inv_cols;
-      }
-#pragma unroll
-      for (int i = 0; i < C; ++i) {
-        const int c = (i * a.tpr + t) * 8, n = live ? a.cols - c : 0;
-        if (n <= 0) continue;
-        float o[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) o[k] = post ? inv_y * (dr[i][k] - y[i][k] * mean_y) : dr[i][k];
-        store8(static_cast<TA*>(a.x[rk]) + row * a.ld_x[rk] + c, n, o);
-      }
-    }
-  }
-  // column sums: the CTA's row groups in order, then one partial row per CTA and vector (a
-  // fixed order: the same inputs give the same bits)
-  float* part = a.part + static_cast<int64_t>(blockIdx.x) * 3 * a.cols;
-#pragma unroll
-  for (int v = 0; v < 3; ++v) {
-    float(&acc)[C][8] = v == 0 ? acc_pre : v == 1 ? acc_gate : acc_post;
-    if (v == 0 ? !pre : v == 1 ? !(has_y && a.gate_mode == kGateRow) : !post) continue;
-    if (rpc > 1) {
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < C; ++i)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int c = (i * a.tpr + t) * 8 + k;
-          if (c < a.cols) sums[sub * a.cols + c] = acc[i][k];
-        }
-      __syncthreads();
-      for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
-        float s = 0.f;
-        for (int q = 0; q < rpc; ++q) s += sums[q * a.cols + c];
-        part[v * a.cols + c] = s;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < C; ++i)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int c = (i * a.tpr + t) * 8 + k;
-          if (c < a.cols) part[v * a.cols + c] = acc[i][k];
-        }
-    }
-  }
-}
 
 // out_v[c] = sum over the partial rows, 32 columns per block (32 x 32 threads: coalesced reads,
 // then a fixed-order sum through shared memory)
@@ -403,24 +42,49 @@ __global__ void col_sum_kernel(const __grid_constant__ ColSumArgs a) {
 // host side
 // ---------------------------------------------------------------------------
 
-// threads per row: a multiple of 32 that covers the row with 8 C columns each
-int threads_per_row(int64_t cols, int c) {
-  int t = 32;
-  while (static_cast<int64_t>(t) * 8 * c < cols) t *= 2;
-  return t;
-}
+// How a call runs: a row's threads (16 columns each), the stages of its matrices, the CTAs
+struct Launch {
+  NormKernel kernel;
+  int threads, grid, smem;
+};
 
-typedef void (*NormKernel)(const NormArgs);
-
-template <int C>
-NormKernel fwd_kernel(bool r32, bool a32) {
-  return r32 ? (a32 ? norm_fwd_kernel<float, float, C> : norm_fwd_kernel<float, uint16_t, C>)
-             : (a32 ? norm_fwd_kernel<uint16_t, float, C> : norm_fwd_kernel<uint16_t, uint16_t, C>);
-}
-template <int C>
-NormKernel bwd_kernel(bool r32, bool a32) {
-  return r32 ? (a32 ? norm_bwd_kernel<float, float, C> : norm_bwd_kernel<float, uint16_t, C>)
-             : (a32 ? norm_bwd_kernel<uint16_t, float, C> : norm_bwd_kernel<uint16_t, uint16_t, C>);
+fo_status plan_launch(fo_ctx* ctx, NormArgs* a, bool backward, bool r32, bool a32, bool p32, Launch* l) {
+  a->tpr = 32;
+  while (a->tpr * 8 * 2 < a->cols) a->tpr *= 2;
+  l->threads = a->tpr > kNormThreads ? a->tpr : kNormThreads;
+  const int rpc = l->threads / a->tpr;
+  // matrices that fit two stages are staged, the others are read directly
+  uint32_t stage = 0;
+  bool vec = a->cols % 8 == 0;
+  for (int i = 0; i < kIns; ++i) {
+    NormIn& in = a->in[i];
+    if (!in.ptr[0]) continue;
+    const uint32_t bytes = static_cast<uint32_t>(a->cols) * in.esz / 16 * 16;
+    const uint32_t size = (bytes * rpc + 127) / 128 * 128;
+    if (bytes == 0 || 2 * (stage + size) > kNormSmem) {
+      vec = false;
+      continue;
+    }
+    in.off = stage;
+    in.pitch = in.bytes = bytes;
+    stage += size;
+  }
+  l->kernel = backward ? norm_bwd_kernel_of(r32, a32, p32, vec, l->threads)
+                       : norm_fwd_kernel_of(r32, a32, p32, vec, l->threads);
+  a->stage_bytes = stage;
+  const int per_sm = backward ? (l->threads < 512 ? 512 / l->threads : 1) : 1024 / l->threads;
+  a->stages = kNormMaxStages;
+  while (a->stages > 2 && static_cast<int64_t>(a->stages) * stage * per_sm > kNormSmem) --a->stages;
+  int ctas = stage ? static_cast<int>(kNormSmem / (a->stages * stage)) : per_sm;
+  if (ctas > per_sm) ctas = per_sm;
+  l->smem = static_cast<int>(a->stages * stage);
+  if (backward && rpc > 1 && l->smem < rpc * a->cols * 4) l->smem = rpc * a->cols * 4;
+  const int64_t groups = (a->total_rows + rpc - 1) / rpc, cap = static_cast<int64_t>(host_num_sms(ctx)) * ctas;
+  l->grid = static_cast<int>(groups < cap ? groups : cap);
+  if (l->smem > 44 * 1024 &&
+      cudaFuncSetAttribute(l->kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormSmem) != cudaSuccess)
+    return host_fail(FO_ERR_CUDA, "norm kernel configuration failed");
+  return FO_OK;
 }
 
 // `list` (null: absent) as P matrices of one shape and type
@@ -475,7 +139,7 @@ fo_status check_apart(const View* v, int n, const int (*in_place)[2], int n_in_p
 
 struct NormCall {
   int64_t m = 0, cols = 0;
-  int32_t tr = FO_BF16, ta = FO_BF16;
+  int32_t tr = FO_BF16, ta = FO_BF16, tp = -1;  // residual stream, activations, parameters
   int32_t gate_mode = kGateNone;
 };
 
@@ -515,41 +179,45 @@ fo_status check_norm(const fo_mat* R, const fo_mat* Y, const fo_mat* act2, int P
       FO_TRY_HOST(check_vector(prm->gate, "gate", c->cols));
     }
   }
+  const fo_mat* all[3] = {prm->w_post, prm->w_pre, prm->gate};
+  for (const fo_mat* v : all) {
+    if (!v) continue;
+    if (c->tp >= 0 && v->dtype != c->tp)
+      return host_fail(FO_ERR_UNSUPPORTED, "w_post, w_pre and gate must have one type");
+    c->tp = v->dtype;
+  }
   return FO_OK;
 }
 
-void fill(const fo_mat* list, int P, const void** ptr, int64_t* ld) {
-  for (int r = 0; r < P && list; ++r) {
-    ptr[r] = list[r].ptr;
-    ld[r] = list[r].ld;
-  }
-}
 void fill(const fo_mat* list, int P, void** ptr, int64_t* ld) {
   for (int r = 0; r < P && list; ++r) {
     ptr[r] = list[r].ptr;
     ld[r] = list[r].ld;
   }
 }
-void fill_common(NormArgs* a, const NormCall& c, int P, const fo_norm_params* prm) {
+void fill_in(const fo_mat* list, int P, NormIn* in) {
+  for (int r = 0; r < P && list; ++r) {
+    in->ptr[r] = list[r].ptr;
+    in->ld[r] = list[r].ld;
+    in->esz = list[r].dtype == FO_F32 ? 4 : 2;
+  }
+}
+void fill_common(NormArgs* a, fo_ctx* ctx, const NormCall& c, int P, const fo_norm_params* prm) {
   std::memset(a, 0, sizeof(*a));
   a->m = c.m;
   a->total_rows = c.m * P;
   a->cols = static_cast<int32_t>(c.cols);
   a->gate_mode = c.gate_mode;
-  if (prm->gate) {
-    fill(prm->gate, prm->gate_per_token ? P : 1, a->gate, a->ld_gate);
-    a->gate_f32 = prm->gate[0].dtype == FO_F32;
-  }
-  if (prm->w_post) {
-    a->w_post = prm->w_post->ptr;
-    a->post_f32 = prm->w_post->dtype == FO_F32;
-  }
-  if (prm->w_pre) {
-    a->w_pre = prm->w_pre->ptr;
-    a->pre_f32 = prm->w_pre->dtype == FO_F32;
-  }
+  if (c.gate_mode == kGateToken) fill_in(prm->gate, P, &a->in[kInGate]);
+  if (c.gate_mode == kGateRow) a->gate = prm->gate[0].ptr;
+  a->w_post = prm->w_post ? prm->w_post->ptr : nullptr;
+  a->w_pre = prm->w_pre ? prm->w_pre->ptr : nullptr;
   a->alpha = prm->residual_scale;
   a->eps = prm->eps;
+  fo_opts o;
+  std::memset(&o, 0, sizeof(o));
+  a->timeout_ns = host_timeout_ns(o);
+  a->ctrl = host_ctrl(ctx);
 }
 
 }  // namespace
@@ -580,18 +248,16 @@ fo_status fo_norm_residual(fo_ctx* ctx, const fo_mat* R, const fo_mat* Y, int P,
   DeviceGuard dev(host_device(ctx));
   if (!dev.ok) return host_fail(FO_ERR_CUDA, "cudaSetDevice failed");
   NormArgs a;
-  fill_common(&a, c, P, prm);
-  fill(R, P, a.r, a.ld_r);
-  fill(Y, P, a.y, a.ld_y);
+  fill_common(&a, ctx, c, P, prm);
+  fill_in(R, P, &a.in[kInR]);
+  fill_in(Y, P, &a.in[kInY]);
   fill(R_out, P, a.r_out, a.ld_r_out);
   fill(X, P, a.x, a.ld_x);
-  const bool r32 = c.tr == FO_F32, a32 = c.ta == FO_F32;
-  const int cc = c.cols <= 256 ? 1 : 2;
-  a.tpr = threads_per_row(c.cols, cc);
-  const int threads = a.tpr > kNormThreads ? a.tpr : kNormThreads, rpc = threads / a.tpr;
-  const int64_t blocks = (a.total_rows + rpc - 1) / rpc, cap = static_cast<int64_t>(host_num_sms(ctx)) * 16;
-  const NormKernel k = cc == 1 ? fwd_kernel<1>(r32, a32) : fwd_kernel<2>(r32, a32);
-  k<<<static_cast<unsigned>(blocks < cap ? blocks : cap), threads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  a.has_y = Y != nullptr;
+  a.pre = X != nullptr;
+  Launch l;
+  FO_TRY_HOST(plan_launch(ctx, &a, false, c.tr == FO_F32, c.ta == FO_F32, c.tp == FO_F32, &l));
+  l.kernel<<<l.grid, l.threads, l.smem, static_cast<cudaStream_t>(stream)>>>(a);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? FO_OK : host_fail(FO_ERR_CUDA, cudaGetErrorString(e));
 }
@@ -634,29 +300,25 @@ fo_status fo_norm_residual_backward(fo_ctx* ctx, const fo_mat* R_out, const fo_m
   if (!dev.ok) return host_fail(FO_ERR_CUDA, "cudaSetDevice failed");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   NormArgs a;
-  fill_common(&a, c, P, prm);
-  fill(R_out, P, a.r, a.ld_r);
-  fill(Y, P, a.y, a.ld_y);
-  fill(dX, P, a.dx, a.ld_dx);
-  fill(dR_out, P, a.dr_out, a.ld_dr_out);
+  fill_common(&a, ctx, c, P, prm);
+  if (dX) fill_in(R_out, P, &a.in[kInR]);  // without a norm behind, R_out itself is not read
+  fill_in(Y, P, &a.in[kInY]);
+  fill_in(dX, P, &a.in[kInDx]);
+  fill_in(dR_out, P, &a.in[kInDr]);
   fill(dR, P, a.r_out, a.ld_r_out);
   fill(dY, P, a.x, a.ld_x);
   if (token) fill(grads->gate, P, a.dgate, a.ld_dgate);
-  const bool r32 = c.tr == FO_F32, a32 = c.ta == FO_F32;
-  const int cc = c.cols <= 256 ? 1 : 2;
-  a.tpr = threads_per_row(c.cols, cc);
-  const int threads = a.tpr > kNormThreads ? a.tpr : kNormThreads, rpc = threads / a.tpr;
-  const int64_t blocks = (a.total_rows + rpc - 1) / rpc;
-  const int64_t per_sm = threads >= 1024 ? 1 : threads >= 512 ? 1 : 2;
-  const int64_t cap = static_cast<int64_t>(host_num_sms(ctx)) * per_sm;
-  const int grid = static_cast<int>(blocks < cap ? blocks : cap);
+  a.has_y = Y != nullptr;
+  a.pre = dX != nullptr;
+  a.has_dr = dR_out != nullptr;
+  Launch l;
+  FO_TRY_HOST(plan_launch(ctx, &a, true, c.tr == FO_F32, c.ta == FO_F32, c.tp == FO_F32, &l));
+  const int grid = l.grid;
   void* part = nullptr;
-  FO_TRY_HOST(host_buffer_kept(ctx, kSlotNormPart, static_cast<size_t>(cap) * 3 * c.cols * 4, s, &part));
+  FO_TRY_HOST(host_buffer_kept(ctx, kSlotNormPart, static_cast<size_t>(host_num_sms(ctx)) * 2 * 3 * c.cols * 4, s, &part));
   a.part = static_cast<float*>(part);
   if (grid > 0) {
-    const NormKernel k = cc == 1 ? bwd_kernel<1>(r32, a32) : bwd_kernel<2>(r32, a32);
-    const int smem = rpc > 1 ? static_cast<int>(rpc * c.cols * 4) : 0;
-    k<<<grid, threads, smem, s>>>(a);
+    l.kernel<<<grid, l.threads, l.smem, s>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return host_fail(FO_ERR_CUDA, cudaGetErrorString(e));
   }

@@ -1,0 +1,197 @@
+// Norms before and after a block with gate and residual: backward (formulas in fo_norm.cuh).
+#include "fo_norm.cuh"
+
+namespace fo {
+namespace {
+
+// T: most threads of a CTA; up to 512 threads share an SM (128 registers each: 48 of them hold
+// the sums over tokens)
+template <typename TR, typename TA, typename TP, bool kVec, int T>
+__global__ void __launch_bounds__(T, T <= 512 ? 512 / T : 1) norm_bwd_kernel(const __grid_constant__ NormArgs a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float buf[2 * kSumBuf];
+  __shared__ uint64_t bars[kNormMaxStages];
+  int turn = 0;
+  const int rpc = blockDim.x / a.tpr, t = threadIdx.x % a.tpr, sub = threadIdx.x / a.tpr;
+  const bool has_y = a.has_y, post = a.w_post != nullptr, pre = a.pre;
+  const float inv_cols = 1.f / static_cast<float>(a.cols);
+  Pair acc[3][kC][4];  // sums over this thread's tokens: dw_pre, dgate, dw_post
+#pragma unroll
+  for (int v = 0; v < 3; ++v)
+#pragma unroll
+    for (int i = 0; i < kC; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[v][i][k] = 0;
+  Walk walk;
+  walk.start(a, smem, bars, rpc);
+  RowAt at{0, static_cast<int64_t>(blockIdx.x) * rpc + sub};
+  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * rpc; row0 < a.total_rows; row0 += walk.step) {
+    const uint8_t* st = walk.next(a, row0);
+    if (!st) return;
+    const bool live = row0 + sub < a.total_rows;
+    if (live) at.wrap(a.m);
+    // sums of R'^2, dX w_pre R' and Y^2: everything the two norms need before t is known
+    Pair q3[3] = {0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < kC; ++i) {
+      const int c = (i * a.tpr + t) * 8, n = live ? a.cols - c : 0;
+      if (n <= 0) continue;
+      if (pre) {
+        Pair r[4], dx[4], w[4];
+        par8<TP, kVec>(a.w_pre, c, n, w);
+        get8<TR, kVec, kInR>(a, st, at, sub, c, n, r);
+        get8<TA, kVec, kInDx>(a, st, at, sub, c, n, dx);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          q3[0] = ffma2(r[k], r[k], q3[0]);
+          q3[1] = ffma2(mul2(dx[k], w[k]), r[k], q3[1]);
+        }
+      }
+      if (post) {
+        Pair y[4];
+        get8<TA, kVec, kInY>(a, st, at, sub, c, n, y);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) q3[2] = ffma2(y[k], y[k], q3[2]);
+      }
+    }
+    float s3[3] = {sum2(q3[0]), sum2(q3[1]), sum2(q3[2])};
+    if (pre || post) row_sum<3>(s3, a.tpr, buf, turn);
+    const float inv_r = pre ? rsqrtf(s3[0] * inv_cols + a.eps) : 0.f;
+    const float mean_r = s3[1] * inv_r * inv_cols;  // mean(dX w_pre n)
+    const float inv_y = post ? rsqrtf(s3[2] * inv_cols + a.eps) : 1.f;
+    const Pair inv_r2 = both(inv_r), mean_r2 = both(-mean_r), inv_y2 = both(inv_y), alpha2 = both(a.alpha);
+    Pair q1 = 0;
+    Pair dr[kC][4];
+#pragma unroll
+    for (int i = 0; i < kC; ++i) {
+      const int c = (i * a.tpr + t) * 8, n = live ? a.cols - c : 0;
+      if (n <= 0) continue;
+      if (a.has_dr) {
+        get8<TR, kVec, kInDr>(a, st, at, sub, c, n, dr[i]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) dr[i][k] = 0;
+      }
+      if (pre) {
+        Pair r[4], dx[4], w[4];
+        par8<TP, kVec>(a.w_pre, c, n, w);
+        get8<TR, kVec, kInR>(a, st, at, sub, c, n, r);
+        get8<TA, kVec, kInDx>(a, st, at, sub, c, n, dx);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const Pair nk = mul2(r[k], inv_r2);
+          acc[0][i][k] = ffma2(dx[k], nk, acc[0][i][k]);
+          dr[i][k] = ffma2(inv_r2, ffma2(nk, mean_r2, mul2(dx[k], w[k])), dr[i][k]);
+        }
+      }
+      Pair o[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[k] = mul2(alpha2, dr[i][k]);
+      put8<TR, kVec>(a.r_out, a.ld_r_out, at, c, n, o);
+      if (!has_y) continue;
+      // dr = t becomes dz w_post
+      Pair y[4], w[4];
+      get8<TA, kVec, kInY>(a, st, at, sub, c, n, y);
+      if (post) {
+        par8<TP, kVec>(a.w_post, c, n, w);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[k] = mul2(y[k], inv_y2);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = mul2(dr[i][k], mul2(y[k], w[k]));  // t z
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = mul2(dr[i][k], y[k]);
+      }
+      if (a.gate_mode != kGateNone) {
+        Pair g[4];
+        if (a.gate_mode == kGateToken) {
+          put8<TP, kVec>(a.dgate, a.ld_dgate, at, c, n, o);
+          get8<TP, kVec, kInGate>(a, st, at, sub, c, n, g);
+        } else {
+          par8<TP, kVec>(a.gate, c, n, g);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[1][i][k] = fadd2(acc[1][i][k], o[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) dr[i][k] = mul2(dr[i][k], g[k]);
+      }
+      if (post) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          acc[2][i][k] = ffma2(dr[i][k], y[k], acc[2][i][k]);
+          dr[i][k] = mul2(dr[i][k], w[k]);
+          q1 = ffma2(dr[i][k], y[k], q1);
+        }
+      }
+    }
+    if (has_y) {
+      Pair mean_y2 = 0;
+      if (post) {
+        float s1[1] = {sum2(q1)};
+        row_sum<1>(s1, a.tpr, buf, turn);
+        mean_y2 = both(-s1[0] * inv_cols * inv_y);
+      }
+#pragma unroll
+      for (int i = 0; i < kC; ++i) {
+        const int c = (i * a.tpr + t) * 8, n = live ? a.cols - c : 0;
+        if (n <= 0) continue;
+        if (post) {
+          Pair y[4];
+          get8<TA, kVec, kInY>(a, st, at, sub, c, n, y);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) dr[i][k] = mul2(inv_y2, ffma2(y[k], mean_y2, dr[i][k]));
+        }
+        put8<TA, kVec>(a.x, a.ld_x, at, c, n, dr[i]);
+      }
+    }
+    at.row += walk.step;
+  }
+  // column sums: the CTA's row groups in order, then one partial row per CTA and vector (a
+  // fixed order: the same inputs give the same bits)
+  float* part = a.part + static_cast<int64_t>(blockIdx.x) * 3 * a.cols;
+  float* sums = reinterpret_cast<float*>(smem);  // [row groups][cols]: the stages are done with
+#pragma unroll
+  for (int v = 0; v < 3; ++v) {
+    if (v == 0 ? !pre : v == 1 ? !(has_y && a.gate_mode == kGateRow) : !post) continue;
+    float* out = rpc > 1 ? sums + sub * a.cols : part + v * a.cols;
+    if (rpc > 1) __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kC; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int c = (i * a.tpr + t) * 8 + 2 * k;
+        float x, y;
+        unpack2(acc[v][i][k], x, y);
+        if (c < a.cols) out[c] = x;
+        if (c + 1 < a.cols) out[c + 1] = y;
+      }
+    if (rpc > 1) {
+      __syncthreads();
+      for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
+        float s = 0.f;
+        for (int q = 0; q < rpc; ++q) s += sums[q * a.cols + c];
+        part[v * a.cols + c] = s;
+      }
+    }
+  }
+}
+
+template <bool kVec, int T>
+NormKernel of(bool r32, bool a32, bool p32) {
+  const int i = (r32 ? 4 : 0) + (a32 ? 2 : 0) + (p32 ? 1 : 0);
+  const NormKernel k[8] = {norm_bwd_kernel<uint16_t, uint16_t, uint16_t, kVec, T>, norm_bwd_kernel<uint16_t, uint16_t, float, kVec, T>,
+                           norm_bwd_kernel<uint16_t, float, uint16_t, kVec, T>,    norm_bwd_kernel<uint16_t, float, float, kVec, T>,
+                           norm_bwd_kernel<float, uint16_t, uint16_t, kVec, T>,    norm_bwd_kernel<float, uint16_t, float, kVec, T>,
+                           norm_bwd_kernel<float, float, uint16_t, kVec, T>,       norm_bwd_kernel<float, float, float, kVec, T>};
+  return k[i];
+}
+
+}  // namespace
+
+NormKernel norm_bwd_kernel_of(bool r32, bool a32, bool p32, bool vec, int threads) {
+  if (!vec) return threads <= 512 ? of<false, 512>(r32, a32, p32) : of<false, 1024>(r32, a32, p32);
+  if (threads <= 256) return of<true, 256>(r32, a32, p32);
+  return threads <= 512 ? of<true, 512>(r32, a32, p32) : of<true, 1024>(r32, a32, p32);
+}
+
+}  // namespace fo

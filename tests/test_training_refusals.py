@@ -95,6 +95,7 @@ def test_norm_valid_calls_reach_the_context(lib):
     (lambda c: setattr(c, "w_post", _arr(_mat(16, 1, 23))), fo.FO_ERR_SHAPE, "w_post"),
     (lambda c: setattr(c, "w_post", _arr(_mat(16, 1, 24, 7))), fo.FO_ERR_INVALID_ARG, "w_post"),
     (lambda c: setattr(c, "gate", _arr(_mat(18, 4, 24))), fo.FO_ERR_SHAPE, "gate"),
+    (lambda c: setattr(c, "gate", _arr(_mat(18, 1, 24, fo.FO_F32))), fo.FO_ERR_UNSUPPORTED, "one type"),
     (lambda c: c.Y.__setitem__(1, _mat(3, 5, 24)), fo.FO_ERR_SHAPE, "Y[1]"),
     (lambda c: c.Y.__setitem__(1, _mat(3, 4, 24, fo.FO_F32)), fo.FO_ERR_INVALID_ARG, "Y[1]"),
     (lambda c: c.R.__setitem__(0, _mat(0, 4, 16400, fo.FO_F32)), fo.FO_ERR_UNSUPPORTED, "at most 16384"),
