@@ -118,9 +118,12 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 constexpr int kBlk = 128;                     // queries or keys per block
 constexpr uint32_t kHalf = kBlk * 128;        // 64 columns of a block: 128 rows of one 128-byte swizzle atom
+// A whole warp waits: every lane tests the phase (one broadcast access, no exchange between
+// lanes), only a phase that is not complete yet takes lane 0 into the bounded loop.
 __device__ __forceinline__ bool attn_wait(uint64_t* bar, uint32_t parity, const TrainArgs& p, uint32_t site, int lane) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   uint32_t ok = 0;
-  if (lane == 0) ok = mbar_wait_fast(bar, parity, p.ctrl, p.timeout_ns, site, blockIdx.x) ? 1u : 0u;
+  if (lane == 0) ok = mbar_wait(bar, parity, p.ctrl, p.timeout_ns, site, blockIdx.x) ? 1u : 0u;
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 

@@ -183,60 +183,100 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
       ok = attn_wait(&ctl->s_full[t], j & 1, p, kSiteTmemFull, lane);
       if (!ok) break;
       tc_fence_after();
-      uint32_t w[4][32];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(sc + c * 32, w[c]);
-      tmem_wait_ld();
-      float s[128];
-#pragma unroll
-      for (int k = 0; k < 128; ++k) s[k] = __uint_as_float(w[k >> 5][k & 31]);
-      if ((j + 1) * kBlk > all) {  // keys that this row does not see: whatever they hold
-        const int upto = see - j * kBlk;
-#pragma unroll
-        for (int k = 0; k < 128; ++k)
-          if (k >= upto) s[k] = -INFINITY;
-      }
+      const bool edge = (j + 1) * kBlk > all;  // a block with keys that some row does not see
+      const int upto = see - j * kBlk;
+      // the row's maximum in this block, four independent chains
       float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      auto maxima = [&](uint32_t (&w)[32], int c) {
+        if (edge) {
 #pragma unroll
-      for (int k = 0; k < 64; ++k) mq[k & 3] = fmax3(mq[k & 3], s[2 * k], s[2 * k + 1]);
-      const float mx = fmax3(fmaxf(mq[0], mq[1]), mq[2], mq[3]) * p.scale_log2;
+          for (int k = 0; k < 32; ++k)
+            if (c * 32 + k >= upto) w[k] = 0xff800000u;  // -infinity, whatever the key holds
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          mq[k & 3] = fmax3(mq[k & 3], __uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
+      };
+      uint64_t bsum[2];
+      uint32_t packed[64];
+      auto weights = [&](const uint32_t (&w)[32], int c, uint64_t nm) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          float x0, x1;
+          unpack2(ffma2(pack2(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1])), c2, nm), x0, x1);
+          const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
+          packed[c * 16 + k] = pack_bf16x2(e0, e1);
+          bsum[k & 1] = fadd2(bsum[k & 1], pack2(e0, e1));
+        }
+      };
+      // every chunk of 32 scores: `f`, while the next chunk is on its way from TMEM
+      auto chunks = [&](auto&& f) {
+        uint32_t wa[32], wb[32];
+        tmem_ld32(sc, wa);
+        tmem_wait_ld();
+        tmem_ld32(sc + 32, wb);
+        f(wa, 0);
+        tmem_wait_ld();
+        tmem_ld32(sc + 64, wa);
+        f(wb, 1);
+        tmem_wait_ld();
+        tmem_ld32(sc + 96, wb);
+        f(wa, 2);
+        tmem_wait_ld();
+        f(wb, 3);
+      };
+      auto block_max = [&]() { return fmax3(fmaxf(mq[0], mq[1]), mq[2], mq[3]) * p.scale_log2; };
+      // The weights against the reference so far, so that they do not wait for this block's
+      // maximum; a block that exceeds the reference by more than 2^8 (rare) computes them again.
       float alpha = 1.f;
+      bool again = j == 0;
       if (j == 0) {
-        m_ref = mx;
-      } else if (mx > m_ref + kRescale) {
-        alpha = fast_exp2(m_ref - mx);
-        m_ref = mx;
-      }
-      if (__any_sync(0xffffffffu, alpha != 1.f)) {
-        sum = ffma2(sum, pack2(alpha, alpha), pack2(0.f, 0.f));
-        // the output must hold every earlier block before it is rescaled
-        ok = attn_wait(&ctl->o_done[t], (j - 1) & 1, p, kSiteDrain, lane);
-        if (!ok) break;
-        tc_fence_after();
-#pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t v[32];
-          tmem_ld32(oc + c, v);
-          tmem_wait_ld();
-#pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
-          tmem_st32(oc + c, v);
+        chunks([&](uint32_t (&w)[32], int c) { maxima(w, c); });
+        m_ref = block_max();
+      } else {
+        const uint64_t nm = m_ref == -INFINITY ? 0 : pack2(-m_ref, -m_ref);
+        bsum[0] = bsum[1] = 0;
+        chunks([&](uint32_t (&w)[32], int c) {
+          maxima(w, c);
+          weights(w, c, nm);
+        });
+        const float mx = block_max();
+        if (mx > m_ref + kRescale) {
+          alpha = fast_exp2(m_ref - mx);
+          m_ref = mx;
+          again = true;
         }
       }
-      const float m = m_ref == -INFINITY ? 0.f : m_ref;  // a row without keys: every weight 0
-      const uint64_t nm = pack2(-m, -m);
+      if (__any_sync(0xffffffffu, again)) {
+        const uint64_t nm = m_ref == -INFINITY ? 0 : pack2(-m_ref, -m_ref);  // no key: every weight 0
+        bsum[0] = bsum[1] = 0;
+        chunks([&](uint32_t (&w)[32], int c) {
+          maxima(w, c);
+          weights(w, c, nm);
+        });
+        if (j > 0) {
+          // the output must hold every earlier block before it is rescaled
+          ok = attn_wait(&ctl->o_done[t], (j - 1) & 1, p, kSiteDrain, lane);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t v[32];
+            tmem_ld32(oc + c, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
+            tmem_st32(oc + c, v);
+          }
+        }
+      }
+      sum = ffma2(sum, pack2(alpha, alpha), fadd2(bsum[0], bsum[1]));
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        uint32_t packed[32];
+        uint32_t w[32];
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          float x0, x1;
-          unpack2(ffma2(pack2(s[c * 64 + 2 * k], s[c * 64 + 2 * k + 1]), c2, nm), x0, x1);
-          const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
-          packed[k] = pack_bf16x2(e0, e1);
-          sum = fadd2(sum, pack2(e0, e1));
-        }
-        tmem_st32(sc + c * 32, packed);
+        for (int k = 0; k < 32; ++k) w[k] = packed[c * 32 + k];
+        tmem_st32(sc + c * 32, w);
       }
       tmem_wait_st();
       attn_publish(&ctl->p_full[t], lane);
