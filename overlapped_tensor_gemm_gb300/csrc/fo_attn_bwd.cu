@@ -74,7 +74,7 @@ struct DkvSmem {
   static constexpr uint32_t ctl = stats + 2 * 2 * kBlk * 4;
 };
 struct alignas(8) DkvCtl {
-  uint64_t kv_full, q_full[2], q_empty[2], do_full[2], do_empty[2], st_full[2], st_empty[2];
+  uint64_t kv_full, q_full[2], do_full[2], empty[2], st_full[2], st_empty[2];
   uint64_t s_full, p_full, dp_full, ds_full, acc_full, fix, drain;
   uint32_t tmem_base, pad;
 };
@@ -114,9 +114,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
     mbar_init(&ctl->kv_full, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&ctl->q_full[s], 1);
-      mbar_init(&ctl->q_empty[s], 1);
       mbar_init(&ctl->do_full[s], 1);
-      mbar_init(&ctl->do_empty[s], 1);
+      mbar_init(&ctl->empty[s], 1);
       mbar_init(&ctl->st_full[s], 1);
       mbar_init(&ctl->st_empty[s], kWorkWarps);
     }
@@ -158,14 +157,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
         w.head_block(i, &h, &qb);
         const int valid = b.q_len - qb * kBlk;
         q_armed = false;
-        ok = attn_wait(&ctl->q_empty[st], free_parity, p, kSiteEmpty, lane);
+        ok = attn_wait(&ctl->empty[st], free_parity, p, kSiteEmpty, lane);
         if (!ok) break;
         ok = load_summed<D>(p, &p.maps[rk], smem + L::q + st * L::tile, &ctl->q_full[st], &ctl->fix, fix_uses, h * D,
                             b.q0 + qb * kBlk, valid, lane);
         if (!ok) break;
         q_armed = true;
-        ok = attn_wait(&ctl->do_empty[st], free_parity, p, kSiteEmpty, lane) &&
-             load_summed<D>(p, &p.maps[3 * p.P + rk], smem + L::d_o + st * L::tile, &ctl->do_full[st], &ctl->fix,
+        ok = load_summed<D>(p, &p.maps[3 * p.P + rk], smem + L::d_o + st * L::tile, &ctl->do_full[st], &ctl->fix,
                             fix_uses, h * D, b.q0 + qb * kBlk, valid, lane);
         if (ok) armed = i + 1;
       }
@@ -176,53 +174,53 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
           if (i < armed) mbar_wait_drain(&ctl->do_full[i & 1], (i >> 1) & 1, kAttnDrainNs);
         }
       }
-    } else if (warp == 1 && lane == 0 && w.n > 0) {  // ---- MMAs
+    } else if (warp == 1 && w.n > 0) {  // ---- MMAs
+      const uint32_t on = lane == 0 ? 1u : 0u;
       const uint32_t ka = sbase + L::k, va = sbase + L::v;
-      bool ok = mbar_wait_fast(&ctl->kv_full, 0, p.ctrl, p.timeout_ns, kSiteFull, blockIdx.x) &&
-                mbar_wait_fast(&ctl->q_full[0], 0, p.ctrl, p.timeout_ns, kSiteFull, blockIdx.x);
+      bool ok = attn_wait(&ctl->kv_full, 0, p, kSiteFull, lane) &&
+                attn_wait(&ctl->q_full[0], 0, p, kSiteFull, lane);
       bool issued = false;
       if (ok) {
         tc_fence_after();
-        issue_scores<D>(tmem + kColS, ka, sbase + L::q);
-        umma_commit(&ctl->s_full);
+        issue_scores<D>(on, tmem + kColS, ka, sbase + L::q);
+        mma_commit(on, &ctl->s_full);
         issued = true;
-        ok = mbar_wait_fast(&ctl->do_full[0], 0, p.ctrl, p.timeout_ns, kSiteFull, blockIdx.x);
+        ok = attn_wait(&ctl->do_full[0], 0, p, kSiteFull, lane);
         if (ok) {
-          issue_scores<D>(tmem + kColP, va, sbase + L::d_o);
-          umma_commit(&ctl->dp_full);
+          issue_scores<D>(on, tmem + kColP, va, sbase + L::d_o);
+          mma_commit(on, &ctl->dp_full);
         }
       }
       for (int i = 0; ok && i < w.n; ++i) {
         const int st = i & 1, nx = st ^ 1;
         const uint32_t ph = i & 1, nph = ((i + 1) >> 1) & 1;
-        ok = mbar_wait_fast(&ctl->p_full, ph, p.ctrl, p.timeout_ns, kSiteTmemFull, blockIdx.x);
+        const bool more = i + 1 < w.n;
+        // the next block's operands first: once P_i is there, sixteen products follow without a pause
+        ok = (!more || attn_wait(&ctl->q_full[nx], nph, p, kSiteFull, lane)) &&
+             attn_wait(&ctl->p_full, ph, p, kSiteTmemFull, lane);
         if (!ok) break;
         tc_fence_after();
-        issue_grad<D>(tmem + kColV, tmem + kColS, sbase + L::d_o + st * L::tile, i == 0);
-        umma_commit(&ctl->do_empty[st]);
-        if (i + 1 < w.n) {
-          ok = mbar_wait_fast(&ctl->q_full[nx], nph, p.ctrl, p.timeout_ns, kSiteFull, blockIdx.x);
-          if (!ok) break;
-          issue_scores<D>(tmem + kColS, ka, sbase + L::q + nx * L::tile);
-          umma_commit(&ctl->s_full);
+        issue_grad<D, 64>(on, tmem + kColV, tmem + kColS, sbase + L::d_o + st * L::tile, i == 0);
+        if (more) {
+          issue_scores<D>(on, tmem + kColS, ka, sbase + L::q + nx * L::tile);
+          mma_commit(on, &ctl->s_full);
         }
-        ok = mbar_wait_fast(&ctl->ds_full, ph, p.ctrl, p.timeout_ns, kSiteTmemFull, blockIdx.x);
+        ok = (!more || attn_wait(&ctl->do_full[nx], nph, p, kSiteFull, lane)) &&
+             attn_wait(&ctl->ds_full, ph, p, kSiteTmemFull, lane);
         if (!ok) break;
         tc_fence_after();
-        issue_grad<D>(tmem + kColK, tmem + kColP, sbase + L::q + st * L::tile, i == 0);
-        umma_commit(&ctl->q_empty[st]);
-        if (i + 1 < w.n) {
-          ok = mbar_wait_fast(&ctl->do_full[nx], nph, p.ctrl, p.timeout_ns, kSiteFull, blockIdx.x);
-          if (!ok) break;
-          issue_scores<D>(tmem + kColP, va, sbase + L::d_o + nx * L::tile);
-          umma_commit(&ctl->dp_full);
+        issue_grad<D, 64>(on, tmem + kColK, tmem + kColP, sbase + L::q + st * L::tile, i == 0);
+        mma_commit(on, &ctl->empty[st]);  // dV_i and dK_i have read the stage
+        if (more) {
+          issue_scores<D>(on, tmem + kColP, va, sbase + L::d_o + nx * L::tile);
+          mma_commit(on, &ctl->dp_full);
         }
       }
       if (ok) {
-        umma_commit(&ctl->acc_full);
+        mma_commit(on, &ctl->acc_full);
       } else if (issued) {
-        umma_commit(&ctl->drain);
-        mbar_wait_drain(&ctl->drain, 0, kAttnDrainNs);
+        mma_commit(on, &ctl->drain);
+        if (lane == 0) mbar_wait_drain(&ctl->drain, 0, kAttnDrainNs);
       }
     } else if (warp == 2) {  // ---- row statistics of the queries
       for (int i = 0; i < w.n; ++i) {
@@ -327,7 +325,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
 //
 // TMEM: S (then dS) [0, 128) and [128, 256) in turn, dP [256, 384), dQ [384, 384 + D).  While the
 // working warps turn S_i and dP_i into dS_i the tensor pipe runs S_{i+1}; dP_{i+1} follows as
-// soon as they have read dP_i, dQ_i once dS_i is written.
+// soon as they have read dP_i, dQ_i once dS_i is written.  Two warps issue, one the scores and one
+// the gradient: what an issuing warp spends on barriers passes while the pipe runs the other's.
 // ---------------------------------------------------------------------------
 constexpr uint32_t kColDp = 256, kColDq = 384;
 constexpr int kKStages = 3, kVStages = 2;
@@ -339,7 +338,7 @@ struct DqSmem {
 };
 struct alignas(8) DqCtl {
   uint64_t q_full, k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
-  uint64_t s_full[2], dp_full, dp_free, ds_full, acc_full, fix, drain;
+  uint64_t s_full[2], s_free[2], dp_full, dp_free, ds_full, acc_full, fix, drain[2];
   uint32_t tmem_base, pad;
 };
 template <int D>
@@ -371,13 +370,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
       mbar_init(&ctl->v_full[s], 1);
       mbar_init(&ctl->v_empty[s], 1);
     }
-    for (int s = 0; s < 2; ++s) mbar_init(&ctl->s_full[s], 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&ctl->s_full[s], 1);
+      mbar_init(&ctl->s_free[s], 1);
+      mbar_init(&ctl->drain[s], 1);
+    }
     mbar_init(&ctl->dp_full, 1);
     mbar_init(&ctl->dp_free, kWorkWarps);
     mbar_init(&ctl->ds_full, kWorkWarps);
     mbar_init(&ctl->acc_full, 1);
     mbar_init(&ctl->fix, 1);
-    mbar_init(&ctl->drain, 1);
     fence_barrier_init();
     fence_proxy_async_shared();
   }
@@ -423,45 +425,60 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
         for (int i = v_armed - kVStages < 0 ? 0 : v_armed - kVStages; i < v_armed; ++i)
           mbar_wait_drain(&ctl->v_full[i % kVStages], (i / kVStages) & 1, kAttnDrainNs);
       }
-    } else if (warp == 1 && lane == 0 && n > 0) {  // ---- MMAs
+    } else if (warp == 1 && n > 0) {  // ---- MMAs of S and dP
+      const uint32_t on = lane == 0 ? 1u : 0u;
       const uint32_t qa = sbase + L::q, da = sbase + L::d_o;
-      bool issued = false;
-      auto scores = [&](int i) -> bool {
-        if (!mbar_wait_fast(&ctl->k_full[i % kKStages], (i / kKStages) & 1, p.ctrl, p.timeout_ns, kSiteFull, blockIdx.x))
-          return false;
-        tc_fence_after();
-        issue_scores<D>(tmem + (i & 1) * 128, qa, sbase + L::k + (i % kKStages) * L::tile);
-        umma_commit(&ctl->s_full[i & 1]);
-        issued = true;
-        return true;
-      };
-      auto dprob = [&](int i) -> bool {
-        if (!mbar_wait_fast(&ctl->v_full[i % kVStages], (i / kVStages) & 1, p.ctrl, p.timeout_ns, kSiteFull, blockIdx.x))
-          return false;
-        tc_fence_after();
-        issue_scores<D>(tmem + kColDp, da, sbase + L::v + (i % kVStages) * L::tile);
-        umma_commit(&ctl->dp_full);
-        umma_commit(&ctl->v_empty[i % kVStages]);
-        return true;
-      };
-      bool ok = mbar_wait_fast(&ctl->q_full, 0, p.ctrl, p.timeout_ns, kSiteFull, blockIdx.x) && scores(0) && dprob(0);
+      bool ok = attn_wait(&ctl->q_full, 0, p, kSiteFull, lane), issued = false;
+      int ks = 0, vs = 0;
+      uint32_t kph = 0, vph = 0;
       for (int i = 0; ok && i < n; ++i) {
-        if (i + 1 < n) {
-          ok = scores(i + 1) &&
-               mbar_wait_fast(&ctl->dp_free, i & 1, p.ctrl, p.timeout_ns, kSiteTmemEmpty, blockIdx.x) && dprob(i + 1);
-          if (!ok) break;
-        }
-        ok = mbar_wait_fast(&ctl->ds_full, i & 1, p.ctrl, p.timeout_ns, kSiteTmemFull, blockIdx.x);
+        // S_i overwrites dS_{i-2}, which dQ_{i-2} has read; dP_i overwrites dP_{i-1}, which has been read
+        ok = attn_wait(&ctl->k_full[ks], kph, p, kSiteFull, lane) &&
+             (i < 2 || attn_wait(&ctl->s_free[i & 1], ((i >> 1) & 1) ^ 1, p, kSiteTmemEmpty, lane));
         if (!ok) break;
         tc_fence_after();
-        issue_grad<D>(tmem + kColDq, tmem + (i & 1) * 128, sbase + L::k + (i % kKStages) * L::tile, i == 0);
-        umma_commit(&ctl->k_empty[i % kKStages]);
+        issue_scores<D>(on, tmem + (i & 1) * 128, qa, sbase + L::k + ks * L::tile);
+        mma_commit(on, &ctl->s_full[i & 1]);
+        issued = true;
+        ok = attn_wait(&ctl->v_full[vs], vph, p, kSiteFull, lane) &&
+             (i < 1 || attn_wait(&ctl->dp_free, (i - 1) & 1, p, kSiteTmemEmpty, lane));
+        if (!ok) break;
+        tc_fence_after();
+        issue_scores<D>(on, tmem + kColDp, da, sbase + L::v + vs * L::tile);
+        mma_commit(on, &ctl->dp_full);
+        mma_commit(on, &ctl->v_empty[vs]);
+        if (++ks == kKStages) {
+          ks = 0;
+          kph ^= 1;
+        }
+        if (++vs == kVStages) {
+          vs = 0;
+          vph ^= 1;
+        }
+      }
+      if (!ok && issued) {
+        mma_commit(on, &ctl->drain[0]);
+        if (lane == 0) mbar_wait_drain(&ctl->drain[0], 0, kAttnDrainNs);
+      }
+    } else if (warp == 2 && n > 0) {  // ---- MMAs of dQ
+      const uint32_t on = lane == 0 ? 1u : 0u;
+      bool ok = true, issued = false;
+      int ks = 0;
+      for (int i = 0; ok && i < n; ++i) {
+        ok = attn_wait(&ctl->ds_full, i & 1, p, kSiteTmemFull, lane);
+        if (!ok) break;
+        tc_fence_after();
+        issue_grad<D, 64>(on, tmem + kColDq, tmem + (i & 1) * 128, sbase + L::k + ks * L::tile, i == 0);
+        mma_commit(on, &ctl->s_free[i & 1]);
+        mma_commit(on, &ctl->k_empty[ks]);
+        issued = true;
+        if (++ks == kKStages) ks = 0;
       }
       if (ok) {
-        umma_commit(&ctl->acc_full);
+        mma_commit(on, &ctl->acc_full);
       } else if (issued) {
-        umma_commit(&ctl->drain);
-        mbar_wait_drain(&ctl->drain, 0, kAttnDrainNs);
+        mma_commit(on, &ctl->drain[1]);
+        if (lane == 0) mbar_wait_drain(&ctl->drain[1], 0, kAttnDrainNs);
       }
     }
   } else {  // ---- P and dS

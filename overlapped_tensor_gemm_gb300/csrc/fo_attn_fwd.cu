@@ -10,7 +10,8 @@
 // TMEM: tile t's scores [128 t, 128 t + 128), overwritten in its first half by their bf16
 // weights, which the product with V reads as its A operand; tile t's output [256 + 128 t, + D).
 // Per tile and block the one issuing thread issues P V of block j, then the scores of block
-// j + 1 over the same columns: a CTA's MMAs execute in issue order.
+// j + 1 over the same columns: a thread's MMAs execute in issue order.  (One issuing warp per tile
+// measured 20% slower: the two tiles' products interleave and both finish late.)
 //
 // The output is rescaled only where a row's maximum grew by more than 2^8 since the last time
 // (the sum and the final division use the same reference, so this is exact); the weights, at
@@ -132,41 +133,56 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
       for (int j = v_armed - kVStages < 0 ? 0 : v_armed - kVStages; j < v_armed; ++j)
         mbar_wait_drain(&ctl->v_full[j % kVStages], (j / kVStages) & 1, kAttnDrainNs);
     }
-  } else if (warp == 1 && lane == 0 && nmax > 0) {  // ---- MMAs
-    bool ok = true, issued = false;
-    auto scores = [&](int t, int j) -> bool {
-      if (!mbar_wait_fast(&ctl->k_full[j % kKStages], (j / kKStages) & 1, p.ctrl, p.timeout_ns, kSiteFull, blockIdx.x))
-        return false;
+  } else if (warp == 1 && nmax > 0) {  // ---- MMAs
+    const uint32_t on = lane == 0 ? 1u : 0u;
+    bool ok = attn_wait(&ctl->k_full[0], 0, p, kSiteFull, lane), issued = false;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      if (!ok || n[t] == 0) continue;
+      ok = attn_wait(&ctl->q_full[t], 0, p, kSiteFull, lane);
+      if (!ok) continue;
       tc_fence_after();
-      issue_scores<D>(tmem + t * 128, sbase + L::q + t * L::tile, sbase + L::k + (j % kKStages) * L::tile);
-      umma_commit(&ctl->s_full[t]);
+      issue_scores<D>(on, tmem + t * 128, sbase + L::q + t * L::tile, sbase + L::k);
+      mma_commit(on, &ctl->s_full[t]);
       issued = true;
-      return true;
-    };
-    for (int t = 0; ok && t < 2; ++t)
-      if (n[t] > 0)
-        ok = mbar_wait_fast(&ctl->q_full[t], 0, p.ctrl, p.timeout_ns, kSiteFull, blockIdx.x) && scores(t, 0);
-    if (ok) umma_commit(&ctl->k_empty[0]);
+    }
+    if (ok) mma_commit(on, &ctl->k_empty[0]);
+    int ks = 1, vs = 0;  // stages of block j + 1's keys and of block j's values
+    uint32_t kph = 0, vph = 0;
     for (int j = 0; ok && j < nmax; ++j) {
-      const int vs = j % kVStages;
-      ok = mbar_wait_fast(&ctl->v_full[vs], (j / kVStages) & 1, p.ctrl, p.timeout_ns, kSiteFull, blockIdx.x);
+      // the operands first: once a tile's weights are there, its sixteen products follow
+      // without a pause
+      const bool more = j + 1 < nmax;
+      ok = attn_wait(&ctl->v_full[vs], vph, p, kSiteFull, lane) &&
+           (!more || attn_wait(&ctl->k_full[ks], kph, p, kSiteFull, lane));
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         if (!ok || j >= n[t]) continue;
-        ok = mbar_wait_fast(&ctl->p_full[t], j & 1, p.ctrl, p.timeout_ns, kSiteTmemFull, blockIdx.x);
+        ok = attn_wait(&ctl->p_full[t], j & 1, p, kSiteTmemFull, lane);
         if (!ok) continue;
         tc_fence_after();
-        issue_grad<D, 32>(tmem + kColO + t * 128, tmem + t * 128, sbase + L::v + vs * L::tile, j == 0);
-        umma_commit(&ctl->o_done[t]);
-        if (j + 1 < n[t]) ok = scores(t, j + 1);
+        issue_grad<D, 128>(on, tmem + kColO + t * 128, tmem + t * 128, sbase + L::v + vs * L::tile, j == 0);
+        mma_commit(on, &ctl->o_done[t]);
+        if (j + 1 < n[t]) {
+          issue_scores<D>(on, tmem + t * 128, sbase + L::q + t * L::tile, sbase + L::k + ks * L::tile);
+          mma_commit(on, &ctl->s_full[t]);
+        }
       }
       if (!ok) break;
-      umma_commit(&ctl->v_empty[vs]);
-      if (j + 1 < nmax) umma_commit(&ctl->k_empty[(j + 1) % kKStages]);
+      mma_commit(on, &ctl->v_empty[vs]);
+      if (more) mma_commit(on, &ctl->k_empty[ks]);
+      if (++ks == kKStages) {
+        ks = 0;
+        kph ^= 1;
+      }
+      if (++vs == kVStages) {
+        vs = 0;
+        vph ^= 1;
+      }
     }
     if (!ok && issued) {
-      umma_commit(&ctl->drain);
-      mbar_wait_drain(&ctl->drain, 0, kAttnDrainNs);
+      mma_commit(on, &ctl->drain);
+      if (lane == 0) mbar_wait_drain(&ctl->drain, 0, kAttnDrainNs);
     }
   } else if (warp >= 4) {  // ---- softmax
     const int t = (warp - 4) >> 2, quad = warp & 3;
