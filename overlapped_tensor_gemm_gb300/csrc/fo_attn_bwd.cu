@@ -175,21 +175,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
         }
       }
     } else if (warp == 1 && w.n > 0) {  // ---- MMAs
-      const uint32_t on = lane == 0 ? 1u : 0u;
       const uint32_t ka = sbase + L::k, va = sbase + L::v;
       bool ok = attn_wait(&ctl->kv_full, 0, p, kSiteFull, lane) &&
                 attn_wait(&ctl->q_full[0], 0, p, kSiteFull, lane);
       bool issued = false;
       if (ok) {
         tc_fence_after();
-        issue_scores<D>(on, tmem + kColS, ka, sbase + L::q);
-        mma_commit(on, &ctl->s_full);
+        if (elect_lane()) {
+          issue_scores<D>(tmem + kColS, ka, sbase + L::q);
+          umma_commit(&ctl->s_full);
+        }
+        __syncwarp();
         issued = true;
         ok = attn_wait(&ctl->do_full[0], 0, p, kSiteFull, lane);
-        if (ok) {
-          issue_scores<D>(on, tmem + kColP, va, sbase + L::d_o);
-          mma_commit(on, &ctl->dp_full);
+        if (ok && elect_lane()) {
+          issue_scores<D>(tmem + kColP, va, sbase + L::d_o);
+          umma_commit(&ctl->dp_full);
         }
+        __syncwarp();
       }
       for (int i = 0; ok && i < w.n; ++i) {
         const int st = i & 1, nx = st ^ 1;
@@ -200,27 +203,32 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
              attn_wait(&ctl->p_full, ph, p, kSiteTmemFull, lane);
         if (!ok) break;
         tc_fence_after();
-        issue_grad<D, 64>(on, tmem + kColV, tmem + kColS, sbase + L::d_o + st * L::tile, i == 0);
-        if (more) {
-          issue_scores<D>(on, tmem + kColS, ka, sbase + L::q + nx * L::tile);
-          mma_commit(on, &ctl->s_full);
+        if (elect_lane()) {
+          issue_grad<D, 64>(tmem + kColV, tmem + kColS, sbase + L::d_o + st * L::tile, i == 0);
+          if (more) {
+            issue_scores<D>(tmem + kColS, ka, sbase + L::q + nx * L::tile);
+            umma_commit(&ctl->s_full);
+          }
         }
+        __syncwarp();
         ok = (!more || attn_wait(&ctl->do_full[nx], nph, p, kSiteFull, lane)) &&
              attn_wait(&ctl->ds_full, ph, p, kSiteTmemFull, lane);
         if (!ok) break;
         tc_fence_after();
-        issue_grad<D, 64>(on, tmem + kColK, tmem + kColP, sbase + L::q + st * L::tile, i == 0);
-        mma_commit(on, &ctl->empty[st]);  // dV_i and dK_i have read the stage
-        if (more) {
-          issue_scores<D>(on, tmem + kColP, va, sbase + L::d_o + nx * L::tile);
-          mma_commit(on, &ctl->dp_full);
+        if (elect_lane()) {
+          issue_grad<D, 64>(tmem + kColK, tmem + kColP, sbase + L::q + st * L::tile, i == 0);
+          umma_commit(&ctl->empty[st]);  // dV_i and dK_i have read the stage
+          if (more) {
+            issue_scores<D>(tmem + kColP, va, sbase + L::d_o + nx * L::tile);
+            umma_commit(&ctl->dp_full);
+          }
         }
+        __syncwarp();
       }
-      if (ok) {
-        mma_commit(on, &ctl->acc_full);
-      } else if (issued) {
-        mma_commit(on, &ctl->drain);
-        if (lane == 0) mbar_wait_drain(&ctl->drain, 0, kAttnDrainNs);
+      if (ok && elect_lane()) umma_commit(&ctl->acc_full);
+      if (!ok && issued && elect_lane()) {
+        umma_commit(&ctl->drain);
+        mbar_wait_drain(&ctl->drain, 0, kAttnDrainNs);
       }
     } else if (warp == 2) {  // ---- row statistics of the queries
       for (int i = 0; i < w.n; ++i) {
@@ -426,7 +434,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
           mbar_wait_drain(&ctl->v_full[i % kVStages], (i / kVStages) & 1, kAttnDrainNs);
       }
     } else if (warp == 1 && n > 0) {  // ---- MMAs of S and dP
-      const uint32_t on = lane == 0 ? 1u : 0u;
       const uint32_t qa = sbase + L::q, da = sbase + L::d_o;
       bool ok = attn_wait(&ctl->q_full, 0, p, kSiteFull, lane), issued = false;
       int ks = 0, vs = 0;
@@ -437,16 +444,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
              (i < 2 || attn_wait(&ctl->s_free[i & 1], ((i >> 1) & 1) ^ 1, p, kSiteTmemEmpty, lane));
         if (!ok) break;
         tc_fence_after();
-        issue_scores<D>(on, tmem + (i & 1) * 128, qa, sbase + L::k + ks * L::tile);
-        mma_commit(on, &ctl->s_full[i & 1]);
+        if (elect_lane()) {
+          issue_scores<D>(tmem + (i & 1) * 128, qa, sbase + L::k + ks * L::tile);
+          umma_commit(&ctl->s_full[i & 1]);
+        }
+        __syncwarp();
         issued = true;
         ok = attn_wait(&ctl->v_full[vs], vph, p, kSiteFull, lane) &&
              (i < 1 || attn_wait(&ctl->dp_free, (i - 1) & 1, p, kSiteTmemEmpty, lane));
         if (!ok) break;
         tc_fence_after();
-        issue_scores<D>(on, tmem + kColDp, da, sbase + L::v + vs * L::tile);
-        mma_commit(on, &ctl->dp_full);
-        mma_commit(on, &ctl->v_empty[vs]);
+        if (elect_lane()) {
+          issue_scores<D>(tmem + kColDp, da, sbase + L::v + vs * L::tile);
+          umma_commit(&ctl->dp_full);
+          umma_commit(&ctl->v_empty[vs]);
+        }
+        __syncwarp();
         if (++ks == kKStages) {
           ks = 0;
           kph ^= 1;
@@ -456,29 +469,30 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
           vph ^= 1;
         }
       }
-      if (!ok && issued) {
-        mma_commit(on, &ctl->drain[0]);
-        if (lane == 0) mbar_wait_drain(&ctl->drain[0], 0, kAttnDrainNs);
+      if (!ok && issued && elect_lane()) {
+        umma_commit(&ctl->drain[0]);
+        mbar_wait_drain(&ctl->drain[0], 0, kAttnDrainNs);
       }
     } else if (warp == 2 && n > 0) {  // ---- MMAs of dQ
-      const uint32_t on = lane == 0 ? 1u : 0u;
       bool ok = true, issued = false;
       int ks = 0;
       for (int i = 0; ok && i < n; ++i) {
         ok = attn_wait(&ctl->ds_full, i & 1, p, kSiteTmemFull, lane);
         if (!ok) break;
         tc_fence_after();
-        issue_grad<D, 64>(on, tmem + kColDq, tmem + (i & 1) * 128, sbase + L::k + ks * L::tile, i == 0);
-        mma_commit(on, &ctl->s_free[i & 1]);
-        mma_commit(on, &ctl->k_empty[ks]);
+        if (elect_lane()) {
+          issue_grad<D, 64>(tmem + kColDq, tmem + (i & 1) * 128, sbase + L::k + ks * L::tile, i == 0);
+          umma_commit(&ctl->s_free[i & 1]);
+          umma_commit(&ctl->k_empty[ks]);
+        }
+        __syncwarp();
         issued = true;
         if (++ks == kKStages) ks = 0;
       }
-      if (ok) {
-        mma_commit(on, &ctl->acc_full);
-      } else if (issued) {
-        mma_commit(on, &ctl->drain[1]);
-        if (lane == 0) mbar_wait_drain(&ctl->drain[1], 0, kAttnDrainNs);
+      if (ok && elect_lane()) umma_commit(&ctl->acc_full);
+      if (!ok && issued && elect_lane()) {
+        umma_commit(&ctl->drain[1]);
+        mbar_wait_drain(&ctl->drain[1], 0, kAttnDrainNs);
       }
     }
   } else {  // ---- P and dS

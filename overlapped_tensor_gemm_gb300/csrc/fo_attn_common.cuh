@@ -161,62 +161,54 @@ __device__ bool load_summed(const TrainArgs& p, const CUtensorMap* map, uint8_t*
   return true;
 }
 
-// MMAs and commits as the whole issuing warp executes them, with one lane taking effect (`on`):
-// the warp's control flow stays uniform, so that descriptors live in uniform registers.  Issued
-// from a branch that one lane takes, every MMA first moves its operands there, which for
-// 128 x 128 x 16 products (64 cycles each) was as long as the product.
-__device__ __forceinline__ void mma_ss(uint32_t on, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                       uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(on)
-      : "memory");
+// True for one lane of a converged warp, the same one every time.  The compiler knows that code
+// under it runs in one thread and keeps descriptors in uniform registers: an MMA then takes two
+// instructions fewer to issue than under `lane == 0`, on a warp that competes with the softmax
+// warps for issue slots.
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(r));
+  return r != 0;
 }
-__device__ __forceinline__ void mma_ts(uint32_t on, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                       uint32_t accumulate) {
+
+// One MMA with the accumulation known at compile time.
+template <bool kAdd>
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
+      "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(on)
-      : "memory");
-}
-__device__ __forceinline__ void mma_commit(uint32_t on, uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "setp.ne.b32 q, %1, 0;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(smem_u32(bar)),
-      "r"(on)
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "n"(kAdd ? 1 : 0)
       : "memory");
 }
 
 // D[128 x 128] = A B^T over the D head dimensions, both operands K-major tiles (shared memory
 // offsets enter a descriptor in units of 16 bytes)
 template <int D>
-__device__ __forceinline__ void issue_scores(uint32_t on, uint32_t d_tmem, uint32_t a, uint32_t b) {
+__device__ __forceinline__ void issue_scores(uint32_t d_tmem, uint32_t a, uint32_t b) {
   constexpr uint32_t idesc = umma_idesc_bf16(128, 128);
   const uint64_t ad = umma_sdesc_sw128(a), bd = umma_sdesc_sw128(b);
 #pragma unroll
   for (int k = 0; k < D / 16; ++k) {
     const uint32_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
-    mma_ss(on, d_tmem, ad + off, bd + off, idesc, k > 0 ? 1u : 0u);
+    if (k == 0) {
+      mma_ss<false>(d_tmem, ad, bd, idesc);
+    } else {
+      mma_ss<true>(d_tmem, ad + off, bd + off, idesc);
+    }
   }
 }
 // D[128 x D] += A B over 128 summed rows: A bf16 in TMEM (rows kPart h + 2c, kPart h + 2c + 1 of the
 // sum in column kPart h + c: each group of kPart score columns, overwritten in its first half), B the
 // tile's rows as they lie (MN-major)
 template <int D, int kPart>
-__device__ __forceinline__ void issue_grad(uint32_t on, uint32_t d_tmem, uint32_t a_tmem, uint32_t b, bool first) {
+__device__ __forceinline__ void issue_grad(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, bool first) {
   constexpr uint32_t idesc = umma_idesc_bf16_bmn(128, D);
   const uint64_t bd = umma_sdesc_sw128_mn(b, kHalf);
 #pragma unroll
   for (int k = 0; k < kBlk / 16; ++k)
-    mma_ts(on, d_tmem, a_tmem + k * 16 / kPart * kPart + k * 16 % kPart / 2, bd + k * (2048 >> 4), idesc,
-           first && k == 0 ? 0u : 1u);
+    umma_ts(d_tmem, a_tmem + k * 16 / kPart * kPart + k * 16 % kPart / 2, bd + k * (2048 >> 4), idesc,
+            first && k == 0 ? 0u : 1u);
 }
 __device__ __forceinline__ void attn_publish(uint64_t* bar, int lane) {
   tc_fence_before();
