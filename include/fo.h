@@ -385,8 +385,8 @@ FO_API fo_status fo_attn_forward(fo_ctx* ctx, const fo_mat* Q, const fo_mat* K, 
  *   share a key/value head.
  * dQ as Q, dK and dV as K (bf16, rounded once; P and dS enter their products as bf16).  The
  * outputs must not overlap the inputs.  No atomics: the same inputs give the same bits.
- * Workspace: 8 bytes per query row and head, and, where a rank has few key blocks, fp32
- * partial dK / dV (at most 256 MiB); it is kept for later calls. */
+ * Workspace: 4 bytes per query row and head and, where few blocks of rows would leave SMs idle,
+ * fp32 partial sums (at most 256 MiB); it is kept for later calls. */
 FO_API fo_status fo_attn_backward(fo_ctx* ctx, const fo_mat* Q, const fo_mat* K, const fo_mat* V,
                                   const fo_mat* O, const fo_mat* LSE, const fo_mat* dO, int P, int heads,
                                   int kv_heads, int head_dim, const fo_attn_mask* mask, const fo_mat* dQ,

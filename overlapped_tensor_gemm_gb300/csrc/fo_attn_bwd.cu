@@ -85,10 +85,10 @@ constexpr int dkv_smem() {
 
 // Where the walk stands: query head and block of the i-th iteration
 struct QueryWalk {
-  int h0, first, per_head, n;  // first query head, first block, blocks per head, iterations
+  int h0, first, per_head, i0, n;  // first query head, first block, blocks per head, iterations [i0, i0 + n)
   __device__ void head_block(int i, int* h, int* qb) const {
-    *h = h0 + i / per_head;
-    *qb = first + i % per_head;
+    *h = h0 + (i0 + i) / per_head;
+    *qb = first + (i0 + i) % per_head;
   }
 };
 
@@ -99,16 +99,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   DkvCtl* ctl = reinterpret_cast<DkvCtl*>(smem + L::ctl);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int hp = p.kv_heads * p.P, ph = blockIdx.x % hp, rk = ph / p.kv_heads, kvh = ph % p.kv_heads;
+  const int split = blockIdx.x % p.splits, item = blockIdx.x / p.splits;
+  const int hp = p.kv_heads * p.P, ph = item % hp, rk = ph / p.kv_heads, kvh = ph % p.kv_heads;
   Block b;
-  if (!block_at(p.blocks, blockIdx.x / hp, &b)) return;
+  if (!block_at(p.blocks, item / hp, &b)) return;
   const int group = p.heads / p.kv_heads, key0 = b.blk * kBlk;
   QueryWalk w;
   w.h0 = kvh * group;
   w.first = query_begin(p.blocks.causal, key0, b.q_len, b.k_len) / kBlk;
   w.per_head = (b.q_len + kBlk - 1) / kBlk - w.first;
   if (w.per_head < 0) w.per_head = 0;
-  w.n = group * w.per_head;
+  const int walk = group * w.per_head;
+  w.i0 = static_cast<int>(static_cast<int64_t>(walk) * split / p.splits);
+  w.n = static_cast<int>(static_cast<int64_t>(walk) * (split + 1) / p.splits) - w.i0;
 
   if (threadIdx.x == 0) {
     mbar_init(&ctl->kv_full, 1);
@@ -313,10 +316,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
       tc_fence_after();
       const bool live = key < b.k_len;
       const int64_t row = b.k0 + key;
-      attn_store_rows(lanes + kColV, hf * (D / 2), D / 2, 1.f, live ? p.dv[rk] + row * p.ld_dv[rk] + kvh * D : nullptr,
-                 w.n == 0);
-      attn_store_rows(lanes + kColK, hf * (D / 2), D / 2, p.scale, live ? p.dk[rk] + row * p.ld_dk[rk] + kvh * D : nullptr,
-                 w.n == 0);
+      if (p.splits > 1) {
+        const int64_t at = ((static_cast<int64_t>(split) * p.P + rk) * p.blocks.mk + row) * p.kv_heads * D + kvh * D;
+        attn_store_rows(lanes + kColV, hf * (D / 2), D / 2, 1.f, live ? p.part_v + at : nullptr, w.n == 0);
+        attn_store_rows(lanes + kColK, hf * (D / 2), D / 2, p.scale, live ? p.part + at : nullptr, w.n == 0);
+      } else {
+        attn_store_rows(lanes + kColV, hf * (D / 2), D / 2, 1.f,
+                        live ? p.dv[rk] + row * p.ld_dv[rk] + kvh * D : nullptr, w.n == 0);
+        attn_store_rows(lanes + kColK, hf * (D / 2), D / 2, p.scale,
+                        live ? p.dk[rk] + row * p.ld_dk[rk] + kvh * D : nullptr, w.n == 0);
+      }
     }
   }
   __syncwarp();
@@ -361,12 +370,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   DqCtl* ctl = reinterpret_cast<DqCtl*>(smem + L::ctl);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int hp = p.heads * p.P, ph = blockIdx.x % hp, rk = ph / p.heads, h = ph % p.heads;
+  const int split = blockIdx.x % p.splits, item = blockIdx.x / p.splits;
+  const int hp = p.heads * p.P, ph = item % hp, rk = ph / p.heads, h = ph % p.heads;
   Block b;
-  if (!block_at(p.blocks, blockIdx.x / hp, &b)) return;
+  if (!block_at(p.blocks, item / hp, &b)) return;
   const int kvh = h / (p.heads / p.kv_heads), query0 = b.blk * kBlk;
   const int q_end = query0 + kBlk < b.q_len ? query0 + kBlk : b.q_len;
-  const int n = (key_end(p.blocks.causal, q_end, b.q_len, b.k_len) + kBlk - 1) / kBlk;
+  // key blocks [i0, i0 + n) of the walk
+  const int walk = (key_end(p.blocks.causal, q_end, b.q_len, b.k_len) + kBlk - 1) / kBlk;
+  const int i0 = static_cast<int>(static_cast<int64_t>(walk) * split / p.splits);
+  const int n = static_cast<int>(static_cast<int64_t>(walk) * (split + 1) / p.splits) - i0;
 
   if (threadIdx.x == 0) {
     mbar_init(&ctl->q_full, 1);
@@ -415,14 +428,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
         const int ks = i % kKStages, vs = i % kVStages;
         ok = attn_wait(&ctl->k_empty[ks], ((i / kKStages) & 1) ^ 1, p, kSiteEmpty, lane) &&
              load_summed<D>(p, &p.maps[p.P + rk], smem + L::k + ks * L::tile, &ctl->k_full[ks], &ctl->fix, fix_uses,
-                            kvh * D, b.k0 + i * kBlk, b.k_len - i * kBlk, lane);
+                            kvh * D, b.k0 + (i0 + i) * kBlk, b.k_len - (i0 + i) * kBlk, lane);
         if (!ok) break;
         k_armed = i + 1;
         ok = attn_wait(&ctl->v_empty[vs], ((i / kVStages) & 1) ^ 1, p, kSiteEmpty, lane);
         if (!ok) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(&ctl->v_full[vs], L::tile);
-          load_block<D>(&p.maps[2 * p.P + rk], smem + L::v + vs * L::tile, &ctl->v_full[vs], kvh * D, b.k0 + i * kBlk);
+          load_block<D>(&p.maps[2 * p.P + rk], smem + L::v + vs * L::tile, &ctl->v_full[vs], kvh * D,
+                        b.k0 + (i0 + i) * kBlk);
         }
         v_armed = i + 1;
       }
@@ -532,8 +546,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
       attn_publish(&ctl->dp_free, lane);
 #pragma unroll
       for (int k = 0; k < 64; ++k) s[k] = s[k] * (dp[k] - delta);
-      if ((i + 1) * kBlk > all) {  // keys that this row does not see: whatever they hold
-        const int upto = see - i * kBlk - hf * 64;
+      if ((i0 + i + 1) * kBlk > all) {  // keys that this row does not see: whatever they hold
+        const int upto = see - (i0 + i) * kBlk - hf * 64;
 #pragma unroll
         for (int k = 0; k < 64; ++k)
           if (k >= upto) s[k] = 0.f;
@@ -545,8 +559,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
     if (ok) {
       tc_fence_after();
       const int64_t row = b.q0 + query;
-      attn_store_rows(lanes + kColDq, hf * (D / 2), D / 2, p.scale, live ? p.dq[rk] + row * p.ld_dq[rk] + h * D : nullptr,
-                 n == 0);
+      if (p.splits > 1) {
+        const int64_t at = ((static_cast<int64_t>(split) * p.P + rk) * p.mq + row) * p.heads * D + h * D;
+        attn_store_rows(lanes + kColDq, hf * (D / 2), D / 2, p.scale, live ? p.part + at : nullptr, n == 0);
+      } else {
+        attn_store_rows(lanes + kColDq, hf * (D / 2), D / 2, p.scale,
+                        live ? p.dq[rk] + row * p.ld_dq[rk] + h * D : nullptr, n == 0);
+      }
     }
   }
   __syncwarp();
@@ -587,6 +606,29 @@ __global__ void __launch_bounds__(256) delta_kernel(const __grid_constant__ Trai
   if (i < total && sub == 0) p.delta[(static_cast<int64_t>(rk) * p.heads + h) * p.mq + row] = s;
 }
 
+// Sums of the parts in order (the same inputs give the same bits), 4 columns per thread
+__global__ void __launch_bounds__(256) part_sum_kernel(const __grid_constant__ PartSumArgs a) {
+  if (a.table && a.table[0] == 0) return;
+  const int v = blockIdx.y, per_row = a.cols / 4;
+  const int64_t total = a.P * a.rows * per_row, i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= total) return;
+  const int64_t grow = i / per_row, row = grow % a.rows;
+  const int c = static_cast<int>(i - grow * per_row) * 4, rk = static_cast<int>(grow / a.rows);
+  if (a.off && (row < a.off[0] || row >= a.off[a.n])) return;
+  const float* part = a.part[v] + grow * a.cols + c;
+  const int64_t stride = a.P * a.rows * a.cols;
+  float4 s = *reinterpret_cast<const float4*>(part);
+  for (int k = 1; k < a.splits; ++k) {
+    const float4 x = *reinterpret_cast<const float4*>(part + k * stride);
+    s.x += x.x;
+    s.y += x.y;
+    s.z += x.z;
+    s.w += x.w;
+  }
+  *reinterpret_cast<uint2*>(a.out[v][rk] + row * a.ld_out[v][rk] + c) =
+      make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+}
+
 }  // namespace
 
 template <typename K>
@@ -615,8 +657,15 @@ cudaError_t attn_delta_launch(const TrainArgs& a, int dim, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+cudaError_t attn_part_sum_launch(const PartSumArgs& a, cudaStream_t s) {
+  const int64_t work = a.P * a.rows * (a.cols / 4);
+  if (work == 0) return cudaSuccess;
+  part_sum_kernel<<<dim3(static_cast<unsigned>((work + 255) / 256), a.outputs), 256, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
 cudaError_t attn_dkv_launch(const TrainArgs& a, int dim, cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>(a.blocks.count) * a.kv_heads * a.P;
+  const unsigned grid = static_cast<unsigned>(a.blocks.count) * a.kv_heads * a.P * a.splits;
   if (grid == 0) return cudaSuccess;
   if (dim == 64) {
     attn_dkv_kernel<64><<<grid, kThreads, dkv_smem<64>(), s>>>(a);
@@ -627,7 +676,7 @@ cudaError_t attn_dkv_launch(const TrainArgs& a, int dim, cudaStream_t s) {
 }
 
 cudaError_t attn_dq_launch(const TrainArgs& a, int dim, cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>(a.blocks.count) * a.heads * a.P;
+  const unsigned grid = static_cast<unsigned>(a.blocks.count) * a.heads * a.P * a.splits;
   if (grid == 0) return cudaSuccess;
   if (dim == 64) {
     attn_dq_kernel<64><<<grid, kThreads, dq_smem<64>(), s>>>(a);

@@ -105,6 +105,10 @@ struct TrainArgs {
   float* lse[kMaxP];
   int64_t ld_o[kMaxP], ld_do[kMaxP], ld_lse[kMaxP], ld_dq[kMaxP], ld_dk[kMaxP], ld_dv[kMaxP];
   float* delta;                 // backward: [P][heads][mq]
+  // Backward, a block's walk cut into `splits` parts (0, 1: not cut): part s of rank r writes its
+  // fp32 sums to part[((s * P + r) * rows + row) * cols + col] (dV: part_v), which are added after
+  int32_t splits;
+  float *part, *part_v;
   Blocks blocks;
   int32_t P, heads, kv_heads;
   int32_t mq;
@@ -226,8 +230,27 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
       : "memory");
 }
 
-// A warp's 32 accumulator rows, columns [col0, col0 + n), times `scale`, as bf16 to `row` (null:
+// A warp's 32 accumulator rows, columns [col0, col0 + n), times `scale`, as fp32 to `row` (null:
 // not stored); zero: nothing was accumulated
+__device__ __forceinline__ void attn_store_rows(uint32_t taddr, int col0, int n, float scale, float* row, bool zero) {
+  for (int c = col0; c < col0 + n; c += 32) {
+    uint32_t v[32];
+    if (zero) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) v[k] = 0u;
+    } else {
+      tmem_ld32(taddr + c, v);
+      tmem_wait_ld();
+    }
+    if (!row) continue;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      *reinterpret_cast<float4*>(row + c + 4 * k) =
+          make_float4(__uint_as_float(v[4 * k]) * scale, __uint_as_float(v[4 * k + 1]) * scale,
+                      __uint_as_float(v[4 * k + 2]) * scale, __uint_as_float(v[4 * k + 3]) * scale);
+  }
+}
+// The same as bf16
 __device__ __forceinline__ void attn_store_rows(uint32_t taddr, int col0, int n, float scale, uint16_t* row, bool zero) {
   for (int c = col0; c < col0 + n; c += 32) {
     uint32_t v[32];
@@ -257,5 +280,17 @@ cudaError_t attn_bwd_configure();
 cudaError_t attn_delta_launch(const TrainArgs& a, int dim, cudaStream_t s);
 cudaError_t attn_dkv_launch(const TrainArgs& a, int dim, cudaStream_t s);
 cudaError_t attn_dq_launch(const TrainArgs& a, int dim, cudaStream_t s);
+// out[r][row, col] = sum over the parts, rounded to bf16, for the rows of the sequences
+struct PartSumArgs {
+  const float* part[2];
+  uint16_t* out[2][kMaxP];
+  int64_t ld_out[2][kMaxP];
+  int64_t rows;
+  int32_t cols, splits, P, outputs;
+  const int32_t* off;           // packed sequences: their first and last boundary
+  const int32_t* table;         // and their block table (empty: nothing was computed)
+  int32_t n;
+};
+cudaError_t attn_part_sum_launch(const PartSumArgs& a, cudaStream_t s);
 
 }  // namespace fo

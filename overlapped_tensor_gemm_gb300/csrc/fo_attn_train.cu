@@ -220,6 +220,19 @@ fo_status make_blocks(fo_ctx* ctx, const Call& c, const Cut* cuts, int n, cudaSt
   return e == cudaSuccess ? FO_OK : host_fail(FO_ERR_CUDA, cudaGetErrorString(e));
 }
 
+constexpr int64_t kPartBytes = 256ll << 20;  // most workspace for partial sums
+constexpr int kPartWalk = 8;                 // fewest blocks of a part
+
+// Parts that a pass's walks are cut into: two CTAs per SM are wanted (the last, longest-first
+// wave then fills), each part of at least kPartWalk blocks of the longest possible walk, their
+// partial sums (`bytes` each) within kPartBytes.
+int split_of(int sms, int64_t items, int64_t walk, size_t bytes) {
+  int64_t s = (2 * sms + items - 1) / items;
+  if (s > walk / kPartWalk) s = walk / kPartWalk;
+  if (bytes > 0 && s > kPartBytes / static_cast<int64_t>(bytes)) s = kPartBytes / static_cast<int64_t>(bytes);
+  return s < 1 ? 1 : static_cast<int>(s);
+}
+
 // pointers and row pitches of P matrices
 template <typename T>
 void fill(const fo_mat* list, int P, T** ptr, int64_t* ld) {
@@ -339,10 +352,46 @@ fo_status fo_attn_backward(fo_ctx* ctx, const fo_mat* Q, const fo_mat* K, const 
   Blocks b[2];
   FO_TRY_HOST(make_blocks(ctx, c, cuts, 2, s, b));
   cudaError_t e = attn_delta_launch(a, head_dim, s);
-  a.blocks = b[0];
-  if (e == cudaSuccess) e = attn_dkv_launch(a, head_dim, s);
-  a.blocks = b[1];
-  if (e == cudaSuccess) e = attn_dq_launch(a, head_dim, s);
+  // dK / dV, then dQ: a walk that would leave SMs idle is cut into parts
+  const int group = heads / kv_heads;
+  for (int pass = 0; pass < 2 && e == cudaSuccess; ++pass) {
+    const bool keys = pass == 0;
+    const int64_t rows = keys ? c.mk : c.mq, cols = keys ? kc : qc;
+    a.blocks = b[pass];
+    if (a.blocks.count == 0) continue;
+    const int64_t walk = keys ? (c.mq + kBlk - 1) / kBlk * group : (c.mk + kBlk - 1) / kBlk;
+    a.splits = split_of(host_num_sms(ctx), static_cast<int64_t>(a.blocks.count) * (keys ? kv_heads : heads) * P, walk,
+                        static_cast<size_t>(P) * rows * cols * 4 * (keys ? 2 : 1));
+    if (a.splits > 1) {
+      void* part = nullptr;
+      const int64_t floats = static_cast<int64_t>(a.splits) * P * rows * cols;
+      FO_TRY_HOST(host_buffer_kept(ctx, kSlotAttnPart, static_cast<size_t>(floats) * 4 * (keys ? 2 : 1), s, &part));
+      a.part = static_cast<float*>(part);
+      a.part_v = a.part + floats;
+    }
+    e = keys ? attn_dkv_launch(a, head_dim, s) : attn_dq_launch(a, head_dim, s);
+    if (a.splits > 1 && e == cudaSuccess) {
+      PartSumArgs ps;
+      std::memset(&ps, 0, sizeof(ps));
+      ps.part[0] = a.part;
+      ps.part[1] = a.part_v;
+      for (int r = 0; r < P; ++r) {
+        ps.out[0][r] = keys ? a.dk[r] : a.dq[r];
+        ps.ld_out[0][r] = keys ? a.ld_dk[r] : a.ld_dq[r];
+        ps.out[1][r] = a.dv[r];
+        ps.ld_out[1][r] = a.ld_dv[r];
+      }
+      ps.rows = rows;
+      ps.cols = static_cast<int32_t>(cols);
+      ps.splits = a.splits;
+      ps.P = P;
+      ps.outputs = keys ? 2 : 1;
+      ps.table = a.blocks.table;
+      ps.off = c.n > 0 ? (keys ? c.k_off : c.q_off) : nullptr;
+      ps.n = c.n;
+      e = attn_part_sum_launch(ps, s);
+    }
+  }
   return e == cudaSuccess ? FO_OK : host_fail(FO_ERR_CUDA, cudaGetErrorString(e));
 }
 

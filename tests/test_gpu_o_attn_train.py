@@ -188,6 +188,16 @@ def test_packed_sequences_with_their_own_key_lengths(ctx, d):
     _check(ctx, Problem(1, 2, 1, d, seqs, False, 78 + d))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_walks_cut_into_parts(ctx, d):
+    """Few key blocks under many query heads (dK, dV summed from parts), few queries under many keys (dQ likewise),
+    packed and with rows outside the sequences."""
+    _check(ctx, Problem(1, 16, 1, d, [(390, 390)], True, 51 + d))
+    _check(ctx, Problem(1, 1, 1, d, [(70, 2200)], True, 52 + d))
+    _check(ctx, Problem(1, 8, 1, d, [(260, 260), (0, 0), (300, 300)], True, 53 + d, front=2, behind=30))
+    _check(ctx, Problem(1, 2, 2, d, [(1500, 130)], False, 54 + d))
+
+
 def test_more_sequences_than_one_pass_of_the_table_kernel(ctx):
     rng = np.random.default_rng(4)
     _check(ctx, Problem(1, 1, 1, 64, [(int(n), int(n)) for n in rng.integers(0, 4, 1500)], True, 9))
