@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Sequence
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -167,6 +168,9 @@ def mat(t) -> FoMat:
 
 
 _MAT_ARRAYS = [FoMat * n for n in range(65)]  # array types by length
+_MAT_BYTES = ctypes.sizeof(FoMat)
+_PACK_MAT = struct.Struct("@Piiqqq").pack_into  # FoMat's fields
+assert struct.calcsize("@Piiqqq") == _MAT_BYTES
 _DTYPE_CODES: dict = {}
 
 
@@ -175,12 +179,6 @@ def _dtype_codes() -> dict:
         import torch
         _DTYPE_CODES.update({torch.bfloat16: FO_BF16, torch.float32: FO_F32})
     return _DTYPE_CODES
-
-
-def _pad_ld(a: FoMat) -> FoMat:
-    """A one-row matrix of any width: its (unused) row pitch as a whole number of 16 bytes."""
-    a.ld = -(-a.ld // 8) * 8
-    return a
 
 
 def _mats(ts: Sequence) -> ctypes.Array:
@@ -345,20 +343,21 @@ class Context:
         if len(ts) != P or P >= len(_MAT_ARRAYS):
             raise ValueError(f"{what}: {len(ts)} matrices for {P} ranks")
         arr = _MAT_ARRAYS[P]()
-        for a, t in zip(arr, ts):
+        at = 0
+        codes = _DTYPE_CODES or _dtype_codes()
+        for t in ts:
             if t.get_device() != self.device:
                 self._here(t, what)
-            dt = _dtype_codes().get(t.dtype)
-            if dt is None or t.dim() != 2:
+            dt, shape, stride = codes.get(t.dtype), t.shape, t.stride()
+            if dt is None or len(shape) != 2 or (stride[1] != 1 and shape[1] > 1):
                 m = mat(t)
-                a.ptr, a.dtype, a.rows, a.cols, a.ld = m.ptr, m.dtype, m.rows, m.cols, m.ld
+                ptr, dt, rows, cols, ld = m.ptr, m.dtype, m.rows, m.cols, m.ld
             else:
-                (rows, cols), (ld, unit) = t.shape, t.stride()
-                if unit != 1 and cols > 1:
-                    raise ValueError("need a row-major 2-D view (unit column stride)")
-                a.ptr, a.dtype, a.rows, a.cols, a.ld = t.data_ptr(), dt, rows, cols, max(ld, cols) if rows > 1 else cols
-            if a.rows == 1:
-                _pad_ld(a)
+                ptr, (rows, cols), ld = t.data_ptr(), shape, stride[0]
+            if rows <= 1:  # the row pitch of one row is not used: any whole number of 16 bytes
+                ld = cols + 7 & -8
+            _PACK_MAT(arr, at, ptr or 0, dt, 0, rows, cols, ld if ld > cols else cols)
+            at += _MAT_BYTES
         return arr
 
     def _here(self, t, what: str) -> None:
@@ -369,14 +368,20 @@ class Context:
         """[1, H] matrix of a vector (None stays None)."""
         if t is None:
             return None
-        if t.dim() != 1:
-            raise ValueError(f"{what} must be a vector")
-        self._here(t, what)
-        return ctypes.pointer(_pad_ld(mat(t.unsqueeze(0))))
+        dt = (_DTYPE_CODES or _dtype_codes()).get(t.dtype)
+        if dt is None or t.dim() != 1 or (t.stride(0) != 1 and t.shape[0] > 1):
+            raise ValueError(f"{what} must be a contiguous bf16 or fp32 vector")
+        if t.get_device() != self.device:
+            self._here(t, what)
+        arr, n = _MAT_ARRAYS[1](), t.shape[0]
+        _PACK_MAT(arr, 0, t.data_ptr(), dt, 0, 1, n, n + 7 & -8)
+        return arr
 
     def _own_stream(self, stream):
-        import torch
-        return _stream(torch.cuda.current_stream(self.device) if stream is None else stream)
+        if stream is None:
+            import torch
+            stream = torch.cuda.current_stream(self.device)
+        return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
     def _mask(self, causal, scale, q_offsets, k_offsets):
         import torch
@@ -425,7 +430,6 @@ class Context:
     def _norm_params(self, P, w_post, gate, w_pre, residual_scale, eps, what="gate"):
         token = gate is not None and isinstance(gate, (list, tuple))
         g = self._list(gate, P, what) if token else self._vector(gate, what)
-        g = None if g is None else ctypes.cast(g, ctypes.POINTER(FoMat))
         return FoNormParams(self._vector(w_post, "w_post"), self._vector(w_pre, "w_pre"), g, int(token),
                             residual_scale, eps, 0)
 
