@@ -50,7 +50,7 @@ struct Launch {
 
 fo_status plan_launch(fo_ctx* ctx, NormArgs* a, bool backward, bool r32, bool a32, bool p32, Launch* l) {
   a->tpr = 32;
-  while (a->tpr * 8 * 2 < a->cols) a->tpr *= 2;
+  while (a->tpr * 8 * kC < a->cols) a->tpr *= 2;
   l->threads = a->tpr > kNormThreads ? a->tpr : kNormThreads;
   const int rpc = l->threads / a->tpr;
   // matrices that fit two stages are staged, the others are read directly
@@ -61,7 +61,7 @@ fo_status plan_launch(fo_ctx* ctx, NormArgs* a, bool backward, bool r32, bool a3
     if (!in.ptr[0]) continue;
     const uint32_t bytes = static_cast<uint32_t>(a->cols) * in.esz / 16 * 16;
     const uint32_t size = (bytes * rpc + 127) / 128 * 128;
-    if (bytes == 0 || 2 * (stage + size) > kNormSmem) {
+    if (bytes == 0 || 2 * (stage + size) > kNormSmem - kNormStatic) {
       vec = false;
       continue;
     }
@@ -72,15 +72,21 @@ fo_status plan_launch(fo_ctx* ctx, NormArgs* a, bool backward, bool r32, bool a3
   l->kernel = backward ? norm_bwd_kernel_of(r32, a32, p32, vec, l->threads)
                        : norm_fwd_kernel_of(r32, a32, p32, vec, l->threads);
   a->stage_bytes = stage;
-  const int per_sm = backward ? (l->threads < 512 ? 512 / l->threads : 1) : 1024 / l->threads;
-  a->stages = kNormMaxStages;
-  while (a->stages > 2 && static_cast<int64_t>(a->stages) * stage * per_sm > kNormSmem) --a->stages;
-  int ctas = stage ? static_cast<int>(kNormSmem / (a->stages * stage)) : per_sm;
-  if (ctas > per_sm) ctas = per_sm;
-  l->smem = static_cast<int>(a->stages * stage);
+  // CTAs per SM by registers; two stages and, where they fit as well, the parameters
+  int ctas = backward ? (l->threads < 512 ? 512 / l->threads : 1) : 1024 / l->threads;
+  while (ctas > 1 && 2 * static_cast<int>(stage) > kNormSmem / ctas - kNormStatic) --ctas;
+  const int room = kNormSmem / ctas - kNormStatic;
+  uint32_t pitch = (static_cast<uint32_t>(a->cols) * (p32 ? 4 : 2) + 127) / 128 * 128;
+  if (!backward || !vec || !(a->w_post || a->w_pre || a->gate) || 2 * static_cast<int>(stage) + 3 * static_cast<int>(pitch) > room)
+    pitch = 0;
+  a->par_pitch = pitch;
+  a->stages = stage ? (room - 3 * static_cast<int>(pitch)) / static_cast<int>(stage) : 2;
+  if (a->stages > kNormMaxStages) a->stages = kNormMaxStages;
+  a->par_off = a->stages * stage;
+  l->smem = static_cast<int>(a->par_off + 3 * pitch);
   if (backward && rpc > 1 && l->smem < rpc * a->cols * 4) l->smem = rpc * a->cols * 4;
-  const int64_t groups = (a->total_rows + rpc - 1) / rpc, cap = static_cast<int64_t>(host_num_sms(ctx)) * ctas;
-  l->grid = static_cast<int>(groups < cap ? groups : cap);
+  const int64_t row_groups = (a->total_rows + rpc - 1) / rpc, cap = static_cast<int64_t>(host_num_sms(ctx)) * ctas;
+  l->grid = static_cast<int>(row_groups < cap ? row_groups : cap);
   if (l->smem > 44 * 1024 &&
       cudaFuncSetAttribute(l->kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormSmem) != cudaSuccess)
     return host_fail(FO_ERR_CUDA, "norm kernel configuration failed");

@@ -30,7 +30,8 @@ namespace fo {
 
 constexpr int kNormMaxCols = 16384;
 constexpr int kNormThreads = 256;             // threads of a CTA where a row needs fewer
-constexpr int kNormSmem = 220 * 1024;         // shared memory of an SM that the stages may take
+constexpr int kNormSmem = 224 * 1024;         // shared memory of an SM that its CTAs may take
+constexpr int kNormStatic = 2 * 1024;         // of it, per CTA: static and the system's
 constexpr int kNormMaxStages = 4;
 
 enum GateMode : int32_t { kGateNone = 0, kGateRow = 1, kGateToken = 2 };
@@ -58,6 +59,7 @@ struct NormArgs {
   int64_t m, total_rows;      // rows per rank, rows of all ranks
   int32_t cols, tpr, gate_mode, stages;
   uint32_t stage_bytes;
+  uint32_t par_off, par_pitch;  // copies of w_post, w_pre and gate in shared memory (pitch 0: none)
   int32_t has_y, pre, has_dr;
   float alpha, eps;
   float* part;                // backward: [grid][3][cols] column sums (pre, gate, post)
@@ -197,6 +199,20 @@ __device__ __forceinline__ void get8(const NormArgs& a, const uint8_t* stage, co
 template <typename T, bool kVec>
 __device__ __forceinline__ void par8(const void* base, int c, int n, Pair (&v)[4]) {
   load8(static_cast<const T*>(base) + c, kVec ? 8 : n, v);
+}
+// A parameter vector as the backward reads it: its copy in shared memory (slot k) where there is
+// room, else where it lies.  Read from L2 anew for every row, the vectors of a wide row are as
+// many bytes as the row itself.  (The forward, two CTAs of 64 registers per SM, has no registers
+// for it: 233 -> 262 us at 16384 rows of 8192.)  Called by every thread; Walk::start has the barrier behind it.
+template <typename T>
+__device__ __forceinline__ const T* place_par(const NormArgs& a, uint8_t* smem, int k, const void* base) {
+  const T* p = static_cast<const T*>(base);
+  if (!p || a.par_pitch == 0) return p;
+  uint8_t* to = smem + a.par_off + k * a.par_pitch;
+  const int n = a.cols * static_cast<int>(sizeof(T)) / 16;  // whole 16-byte vectors: kVec rows
+  for (int i = threadIdx.x; i < n; i += blockDim.x)
+    reinterpret_cast<uint4*>(to)[i] = reinterpret_cast<const uint4*>(p)[i];
+  return reinterpret_cast<const T*>(to);
 }
 template <typename T, bool kVec>
 __device__ __forceinline__ void put8(void* const* base, const int64_t* ld, const RowAt& r, int c, int n,

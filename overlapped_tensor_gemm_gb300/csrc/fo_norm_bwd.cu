@@ -22,6 +22,9 @@ __global__ void __launch_bounds__(T, T <= 512 ? 512 / T : 1) norm_bwd_kernel(con
     for (int i = 0; i < kC; ++i)
 #pragma unroll
       for (int k = 0; k < 4; ++k) acc[v][i][k] = 0;
+  const TP* w_post = place_par<TP>(a, smem, 0, a.w_post);
+  const TP* w_pre = place_par<TP>(a, smem, 1, a.w_pre);
+  const TP* w_gate = place_par<TP>(a, smem, 2, a.gate);
   Walk walk;
   walk.start(a, smem, bars, rpc);
   RowAt at{0, static_cast<int64_t>(blockIdx.x) * rpc + sub};
@@ -38,7 +41,7 @@ __global__ void __launch_bounds__(T, T <= 512 ? 512 / T : 1) norm_bwd_kernel(con
       if (n <= 0) continue;
       if (pre) {
         Pair r[4], dx[4], w[4];
-        par8<TP, kVec>(a.w_pre, c, n, w);
+        par8<TP, kVec>(w_pre, c, n, w);
         get8<TR, kVec, kInR>(a, st, at, sub, c, n, r);
         get8<TA, kVec, kInDx>(a, st, at, sub, c, n, dx);
 #pragma unroll
@@ -74,7 +77,7 @@ __global__ void __launch_bounds__(T, T <= 512 ? 512 / T : 1) norm_bwd_kernel(con
       }
       if (pre) {
         Pair r[4], dx[4], w[4];
-        par8<TP, kVec>(a.w_pre, c, n, w);
+        par8<TP, kVec>(w_pre, c, n, w);
         get8<TR, kVec, kInR>(a, st, at, sub, c, n, r);
         get8<TA, kVec, kInDx>(a, st, at, sub, c, n, dx);
 #pragma unroll
@@ -93,7 +96,7 @@ __global__ void __launch_bounds__(T, T <= 512 ? 512 / T : 1) norm_bwd_kernel(con
       Pair y[4], w[4];
       get8<TA, kVec, kInY>(a, st, at, sub, c, n, y);
       if (post) {
-        par8<TP, kVec>(a.w_post, c, n, w);
+        par8<TP, kVec>(w_post, c, n, w);
 #pragma unroll
         for (int k = 0; k < 4; ++k) y[k] = mul2(y[k], inv_y2);
 #pragma unroll
@@ -108,7 +111,7 @@ __global__ void __launch_bounds__(T, T <= 512 ? 512 / T : 1) norm_bwd_kernel(con
           put8<TP, kVec>(a.dgate, a.ld_dgate, at, c, n, o);
           get8<TP, kVec, kInGate>(a, st, at, sub, c, n, g);
         } else {
-          par8<TP, kVec>(a.gate, c, n, g);
+          par8<TP, kVec>(w_gate, c, n, g);
 #pragma unroll
           for (int k = 0; k < 4; ++k) acc[1][i][k] = fadd2(acc[1][i][k], o[k]);
         }
