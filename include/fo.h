@@ -380,7 +380,8 @@ FO_API fo_status fo_attn_forward(fo_ctx* ctx, const fo_mat* Q, const fo_mat* K, 
 
 /* Backward of fo_attn_forward from its inputs, its outputs O and LSE and the gradient dO.
  * The probabilities are recomputed, never stored:
- *   P = exp(S - LSE), delta_i = sum_d dO_id O_id, dS = P (dO V^T - delta),
+ *   P = exp(S - LSE), delta_i = sum_j P_ij (dO V^T)_ij (= sum_d dO_id O_id; taken from the
+ *   given O, whose rounding is then corrected), dS = P (dO V^T - delta),
  *   dQ = scale dS K, dK = scale dS^T Q, dV = P^T dO; dK and dV sum over the query heads that
  *   share a key/value head.
  * dQ as Q, dK and dV as K (bf16, rounded once; P and dS enter their products as bf16).  The

@@ -342,7 +342,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
 //
 // TMEM: S (then dS) [0, 128) and [128, 256) in turn, dP [256, 384), dQ [384, 384 + D).  While the
 // working warps turn S_i and dP_i into dS_i the tensor pipe runs S_{i+1}; dP_{i+1} follows as
-// soon as they have read dP_i, dQ_i once dS_i is written.  Two warps issue, one the scores and one
+// soon as they have read dP_i, dQ_i once dS_i is written.
+//
+// delta.  dS = P (dP - delta) with delta = sum_j P_j dP_j = sum_d dO_d O_d; the kernel is given O
+// rounded to bf16, and where a row attends to few keys the two terms cancel and that rounding is
+// most of dS's error (rows of 1-8 keys: dQ's and dK's error 2.3 times the output's rounding).
+// But sum_j dS_j of a row is exactly what delta is off by, and costs one sum.  So this pass runs
+// before dK / dV, which then have the corrected delta; and a block whose dS is off by more than
+// 2^-11 (2-norm over its rows of the error's sum against that of |dS|) walks its keys a second
+// time.  For spread attention these are the first one or two blocks of a sequence.
+//
+// Two warps issue, one the scores and one
 // the gradient: what an issuing warp spends on barriers passes while the pipe runs the other's.
 // ---------------------------------------------------------------------------
 constexpr uint32_t kColDp = 256, kColDq = 384;
@@ -414,31 +424,50 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
   const uint32_t tmem = ctl->tmem_base;
   const uint32_t sbase = smem_u32(smem);
 
+  // what each role carries from one round over the keys to the next
+  bool ok = true, issued = false;
+  uint32_t fix_uses = 0, kph = 0, vph = 0;
+  int ks = 0, vs = 0;
+  const int quad = warp & 3, hf = (warp - 4) >> 2;
+  const int query = query0 + quad * 32 + lane;  // a working thread's row of S
+  const bool live = query < b.q_len;
+  float lse2 = INFINITY, delta = 0.f;
+  const int64_t stat = (static_cast<int64_t>(rk) * p.heads + h) * p.mq + b.q0 + query;
+  if (warp >= 4 && live) {
+    const float l = p.lse[rk][h * p.ld_lse[rk] + b.q0 + query];
+    lse2 = l == -INFINITY ? INFINITY : l * kLog2e;
+    delta = p.delta[stat];
+  }
+  float* const sums = reinterpret_cast<float*>(smem + L::v);  // between rounds: [error, size][half][128 rows]
+
+  for (int round = 0;; ++round) {
+  const int g0 = round * n;  // blocks before this round: the barriers' phases count on
+  float err = 0.f, size = 0.f;
   if (warp < 4) {
     if (warp == 0) {  // ---- loads
-      uint32_t fix_uses = 0;
-      int k_armed = 0, v_armed = 0;
-      bool ok = true;
-      if (n > 0 && lane == 0) {
+      int k_armed = g0, v_armed = g0;
+      if (n > 0 && round == 0 && lane == 0) {
         mbar_arrive_expect_tx(&ctl->q_full, 2 * L::tile);
         load_block<D>(&p.maps[rk], smem + L::q, &ctl->q_full, h * D, b.q0 + query0);
         load_block<D>(&p.maps[3 * p.P + rk], smem + L::d_o, &ctl->q_full, h * D, b.q0 + query0);
       }
       for (int i = 0; ok && i < n; ++i) {
-        const int ks = i % kKStages, vs = i % kVStages;
-        ok = attn_wait(&ctl->k_empty[ks], ((i / kKStages) & 1) ^ 1, p, kSiteEmpty, lane) &&
+        const int g = g0 + i;
+        ks = g % kKStages;
+        vs = g % kVStages;
+        ok = attn_wait(&ctl->k_empty[ks], ((g / kKStages) & 1) ^ 1, p, kSiteEmpty, lane) &&
              load_summed<D>(p, &p.maps[p.P + rk], smem + L::k + ks * L::tile, &ctl->k_full[ks], &ctl->fix, fix_uses,
                             kvh * D, b.k0 + (i0 + i) * kBlk, b.k_len - (i0 + i) * kBlk, lane);
         if (!ok) break;
-        k_armed = i + 1;
-        ok = attn_wait(&ctl->v_empty[vs], ((i / kVStages) & 1) ^ 1, p, kSiteEmpty, lane);
+        k_armed = g + 1;
+        ok = attn_wait(&ctl->v_empty[vs], ((g / kVStages) & 1) ^ 1, p, kSiteEmpty, lane);
         if (!ok) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(&ctl->v_full[vs], L::tile);
           load_block<D>(&p.maps[2 * p.P + rk], smem + L::v + vs * L::tile, &ctl->v_full[vs], kvh * D,
                         b.k0 + (i0 + i) * kBlk);
         }
-        v_armed = i + 1;
+        v_armed = g + 1;
       }
       if (!ok && lane == 0) {  // wait for the copies in flight
         mbar_wait_drain(&ctl->q_full, 0, kAttnDrainNs);
@@ -449,10 +478,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
       }
     } else if (warp == 1 && n > 0) {  // ---- MMAs of S and dP
       const uint32_t qa = sbase + L::q, da = sbase + L::d_o;
-      bool ok = attn_wait(&ctl->q_full, 0, p, kSiteFull, lane), issued = false;
-      int ks = 0, vs = 0;
-      uint32_t kph = 0, vph = 0;
-      for (int i = 0; ok && i < n; ++i) {
+      ok = ok && attn_wait(&ctl->q_full, 0, p, kSiteFull, lane);
+      for (int i = g0; ok && i < g0 + n; ++i) {
         // S_i overwrites dS_{i-2}, which dQ_{i-2} has read; dP_i overwrites dP_{i-1}, which has been read
         ok = attn_wait(&ctl->k_full[ks], kph, p, kSiteFull, lane) &&
              (i < 2 || attn_wait(&ctl->s_free[i & 1], ((i >> 1) & 1) ^ 1, p, kSiteTmemEmpty, lane));
@@ -488,14 +515,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
         mbar_wait_drain(&ctl->drain[0], 0, kAttnDrainNs);
       }
     } else if (warp == 2 && n > 0) {  // ---- MMAs of dQ
-      bool ok = true, issued = false;
-      int ks = 0;
-      for (int i = 0; ok && i < n; ++i) {
+      for (int i = g0; ok && i < g0 + n; ++i) {
         ok = attn_wait(&ctl->ds_full, i & 1, p, kSiteTmemFull, lane);
         if (!ok) break;
         tc_fence_after();
         if (elect_lane()) {
-          issue_grad<D, 64>(tmem + kColDq, tmem + (i & 1) * 128, sbase + L::k + ks * L::tile, i == 0);
+          issue_grad<D, 64>(tmem + kColDq, tmem + (i & 1) * 128, sbase + L::k + ks * L::tile, i == g0);
           umma_commit(&ctl->s_free[i & 1]);
           umma_commit(&ctl->k_empty[ks]);
         }
@@ -503,30 +528,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
         issued = true;
         if (++ks == kKStages) ks = 0;
       }
-      if (ok && elect_lane()) umma_commit(&ctl->acc_full);
       if (!ok && issued && elect_lane()) {
         umma_commit(&ctl->drain[1]);
         mbar_wait_drain(&ctl->drain[1], 0, kAttnDrainNs);
       }
     }
   } else {  // ---- P and dS
-    const int quad = warp & 3, hf = (warp - 4) >> 2;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    const int query = query0 + quad * 32 + lane;  // this thread's row of S
-    const bool live = query < b.q_len;
-    float lse2 = INFINITY, delta = 0.f;
-    if (live) {
-      const float l = p.lse[rk][h * p.ld_lse[rk] + b.q0 + query];
-      lse2 = l == -INFINITY ? INFINITY : l * kLog2e;
-      delta = p.delta[(static_cast<int64_t>(rk) * p.heads + h) * p.mq + b.q0 + query];
-    }
     const int see = key_end(p.blocks.causal, query + 1, b.q_len, b.k_len);          // keys of this row
     const int all = key_end(p.blocks.causal, query0 + 1, b.q_len, b.k_len);         // keys of the block's first row
     const uint64_t c2 = pack2(p.scale_log2, p.scale_log2), l2 = pack2(-lse2, -lse2);
-    bool ok = true;
-    for (int i = 0; i < n; ++i) {
-      const uint32_t buf = lanes + (i & 1) * 128 + hf * 64;
-      ok = attn_wait(&ctl->s_full[i & 1], (i >> 1) & 1, p, kSiteTmemFull, lane);
+    uint64_t err2 = 0;
+    for (int i = 0; ok && i < n; ++i) {
+      const int g = g0 + i;
+      const uint32_t buf = lanes + (g & 1) * 128 + hf * 64;
+      ok = attn_wait(&ctl->s_full[g & 1], (g >> 1) & 1, p, kSiteTmemFull, lane);
       if (!ok) break;
       tc_fence_after();
       float s[64];
@@ -538,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
         s[k] = fast_exp2(x0);
         s[k + 1] = fast_exp2(x1);
       }
-      ok = attn_wait(&ctl->dp_full, i & 1, p, kSiteTmemFull, lane);
+      ok = attn_wait(&ctl->dp_full, g & 1, p, kSiteTmemFull, lane);
       if (!ok) break;
       tc_fence_after();
       float dp[64];
@@ -552,12 +568,65 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
         for (int k = 0; k < 64; ++k)
           if (k >= upto) s[k] = 0.f;
       }
+      if (round == 0 && p.delta_mode != kDeltaGiven) {
+#pragma unroll
+        for (int k = 0; k < 64; k += 2) {
+          err2 = fadd2(err2, pack2(s[k], s[k + 1]));
+          size += fabsf(s[k]) + fabsf(s[k + 1]);
+        }
+      }
       store64_bf16(buf, s);
       attn_publish(&ctl->ds_full, lane);
     }
+    float x, y;
+    unpack2(err2, x, y);
+    err = x + y;
+  }
+  if (round > 0 || n == 0 || p.delta_mode == kDeltaGiven) break;
+  // delta's error, row by row, and whether the block is worth a second round
+  __syncwarp();
+  if (warp >= 4) {
+    const int row = quad * 32 + lane;
+    sums[hf * kBlk + row] = live ? err : 0.f;
+    sums[(2 + hf) * kBlk + row] = live ? size : 0.f;
+  }
+  __syncthreads();
+  if (warp >= 4) {
+    const int row = quad * 32 + lane;
+    const float e = sums[row] + sums[kBlk + row];
+    delta += e;
+    if (live && hf == 0 && ok) {
+      if (p.delta_mode == kDeltaMeasure) {
+        p.eps[static_cast<int64_t>(split) * p.P * p.heads * p.mq + stat] = e;
+      } else {
+        p.delta[stat] = delta;
+      }
+    }
+  }
+  if (p.delta_mode == kDeltaMeasure) break;
+  float e2 = 0.f, a2 = 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float e = sums[k * 32 + lane] + sums[kBlk + k * 32 + lane];
+    const float a = sums[2 * kBlk + k * 32 + lane] + sums[3 * kBlk + k * 32 + lane];
+    e2 = fmaf(e, e, e2);
+    a2 = fmaf(a, a, a2);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    e2 += __shfl_xor_sync(0xffffffffu, e2, o);
+    a2 += __shfl_xor_sync(0xffffffffu, a2, o);
+  }
+  if (!(e2 > 0x1p-22f * a2)) break;
+  __syncthreads();               // every warp has read the sums: the stage may be loaded again
+  fence_proxy_async_shared();
+  }
+  if (n > 0 && warp == 2 && ok && elect_lane()) umma_commit(&ctl->acc_full);
+  if (warp >= 4) {
     if (ok && n > 0) ok = attn_wait(&ctl->acc_full, 0, p, kSiteDrain, lane);
-    if (ok) {
+    if (ok && p.delta_mode != kDeltaMeasure) {
       tc_fence_after();
+      const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
       const int64_t row = b.q0 + query;
       if (p.splits > 1) {
         const int64_t at = ((static_cast<int64_t>(split) * p.P + rk) * p.mq + row) * p.heads * D + h * D;
@@ -604,6 +673,16 @@ __global__ void __launch_bounds__(256) delta_kernel(const __grid_constant__ Trai
 #pragma unroll
   for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   if (i < total && sub == 0) p.delta[(static_cast<int64_t>(rk) * p.heads + h) * p.mq + row] = s;
+}
+
+// delta += its error, summed over the parts of the walk in order
+__global__ void __launch_bounds__(256) delta_add_kernel(const __grid_constant__ TrainArgs p) {
+  const int64_t total = static_cast<int64_t>(p.P) * p.heads * p.mq;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= total) return;
+  float e = 0.f;
+  for (int s = 0; s < p.splits; ++s) e += p.eps[s * total + i];
+  p.delta[i] += e;
 }
 
 // Sums of the parts in order (the same inputs give the same bits), 4 columns per thread
@@ -661,6 +740,13 @@ cudaError_t attn_part_sum_launch(const PartSumArgs& a, cudaStream_t s) {
   const int64_t work = a.P * a.rows * (a.cols / 4);
   if (work == 0) return cudaSuccess;
   part_sum_kernel<<<dim3(static_cast<unsigned>((work + 255) / 256), a.outputs), 256, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t attn_delta_add_launch(const TrainArgs& a, cudaStream_t s) {
+  const int64_t total = static_cast<int64_t>(a.P) * a.heads * a.mq;
+  if (total == 0) return cudaSuccess;
+  delta_add_kernel<<<static_cast<unsigned>((total + 255) / 256), 256, 0, s>>>(a);
   return cudaGetLastError();
 }
 

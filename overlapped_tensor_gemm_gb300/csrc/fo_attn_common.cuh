@@ -109,6 +109,8 @@ struct TrainArgs {
   // fp32 sums to part[((s * P + r) * rows + row) * cols + col] (dV: part_v), which are added after
   int32_t splits;
   float *part, *part_v;
+  int32_t delta_mode;           // dQ: a DeltaMode
+  float* eps;                   // kDeltaMeasure: [splits][P][heads][mq]
   Blocks blocks;
   int32_t P, heads, kv_heads;
   int32_t mq;
@@ -272,12 +274,16 @@ __device__ __forceinline__ void attn_store_rows(uint32_t taddr, int col0, int n,
   }
 }
 
+// What the dQ pass does about delta's error (see there)
+enum DeltaMode : int32_t { kDeltaCorrect = 0, kDeltaMeasure = 1, kDeltaGiven = 2 };
+
 // fo_attn_fwd.cu
 cudaError_t attn_fwd_configure();
 cudaError_t attn_fwd_launch(const TrainArgs& a, int dim, cudaStream_t s);
 // fo_attn_bwd.cu
 cudaError_t attn_bwd_configure();
 cudaError_t attn_delta_launch(const TrainArgs& a, int dim, cudaStream_t s);
+cudaError_t attn_delta_add_launch(const TrainArgs& a, cudaStream_t s);  // delta += sum over the parts of eps
 cudaError_t attn_dkv_launch(const TrainArgs& a, int dim, cudaStream_t s);
 cudaError_t attn_dq_launch(const TrainArgs& a, int dim, cudaStream_t s);
 // out[r][row, col] = sum over the parts, rounded to bf16, for the rows of the sequences

@@ -352,22 +352,32 @@ fo_status fo_attn_backward(fo_ctx* ctx, const fo_mat* Q, const fo_mat* K, const 
   Blocks b[2];
   FO_TRY_HOST(make_blocks(ctx, c, cuts, 2, s, b));
   cudaError_t e = attn_delta_launch(a, head_dim, s);
-  // dK / dV, then dQ: a walk that would leave SMs idle is cut into parts
+  // dQ (which corrects delta), then dK / dV: a walk that would leave SMs idle is cut into parts
   const int group = heads / kv_heads;
   for (int pass = 0; pass < 2 && e == cudaSuccess; ++pass) {
-    const bool keys = pass == 0;
+    const bool keys = pass == 1;
     const int64_t rows = keys ? c.mk : c.mq, cols = keys ? kc : qc;
-    a.blocks = b[pass];
+    a.blocks = b[keys ? 0 : 1];
     if (a.blocks.count == 0) continue;
     const int64_t walk = keys ? (c.mq + kBlk - 1) / kBlk * group : (c.mk + kBlk - 1) / kBlk;
     a.splits = split_of(host_num_sms(ctx), static_cast<int64_t>(a.blocks.count) * (keys ? kv_heads : heads) * P, walk,
                         static_cast<size_t>(P) * rows * cols * 4 * (keys ? 2 : 1));
+    a.delta_mode = kDeltaCorrect;
     if (a.splits > 1) {
       void* part = nullptr;
       const int64_t floats = static_cast<int64_t>(a.splits) * P * rows * cols;
       FO_TRY_HOST(host_buffer_kept(ctx, kSlotAttnPart, static_cast<size_t>(floats) * 4 * (keys ? 2 : 1), s, &part));
       a.part = static_cast<float*>(part);
       a.part_v = a.part + floats;
+      if (!keys) {  // no CTA sees a whole row: measure delta's error, then compute with the corrected one
+        a.eps = a.part;  // (smaller than the partial sums, which come after it)
+        a.delta_mode = kDeltaMeasure;
+        e = cudaMemsetAsync(a.eps, 0, static_cast<size_t>(a.splits) * P * heads * c.mq * 4, s);
+        if (e == cudaSuccess) e = attn_dq_launch(a, head_dim, s);
+        if (e == cudaSuccess) e = attn_delta_add_launch(a, s);
+        if (e != cudaSuccess) break;
+        a.delta_mode = kDeltaGiven;
+      }
     }
     e = keys ? attn_dkv_launch(a, head_dim, s) : attn_dq_launch(a, head_dim, s);
     if (a.splits > 1 && e == cudaSuccess) {
