@@ -10,6 +10,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -2028,7 +2029,7 @@ fo_status host_check_ctx(const fo_ctx* ctx, int P) {
   return FO_OK;
 }
 int host_device(const fo_ctx* ctx) { return ctx->device; }
-fo_status host_buffer_kept(fo_ctx* ctx, int slot, size_t bytes, cudaStream_t s, void** out) {
+fo_status host_buffer_kept(fo_ctx* ctx, int slot, size_t bytes, cudaStream_t s, void** out) try {
   Buffer& b = ctx->bufs[kBufAttnRecv + slot];
   if (b.bytes < bytes) {
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
@@ -2043,12 +2044,15 @@ fo_status host_buffer_kept(fo_ctx* ctx, int slot, size_t bytes, cudaStream_t s, 
       cudaGetLastError();
       return fail(FO_ERR_OOM, "workspace growth to %zu bytes failed", rounded);
     }
-    if (b.ptr) ctx->retired.push_back(b.ptr);
+    const Buffer old = b;
     b.ptr = p;
     b.bytes = rounded;
+    if (old.ptr) ctx->retired.push_back(old.ptr);
   }
   *out = b.ptr;
   return FO_OK;
+} catch (...) {  // host memory for the bookkeeping
+  return fail(FO_ERR_OOM, "out of host memory");
 }
 bool host_same_view(const fo_mat& a, const fo_mat& b) {
   return a.ptr == b.ptr && a.dtype == b.dtype && a.rows == b.rows && a.cols == b.cols && (a.ld == b.ld || a.rows <= 1);
@@ -2067,6 +2071,42 @@ bool host_mats_overlap(const fo_mat& a, const fo_mat& b) {
     return gap < a.cols * ea || gap + b.cols * eb > pitch;
   }
   return true;
+}
+fo_status host_check_apart(const HostList* lists, int n, const int (*in_place)[2], int n_in_place) {
+  constexpr int kMaxLists = 12;
+  struct Span {
+    uintptr_t lo, hi;
+    int list, i;
+  };
+  Span spans[kMaxLists * kMaxP];
+  int count = 0;
+  if (n > kMaxLists) return fail(FO_ERR_INTERNAL, "too many matrix lists");
+  for (int l = 0; l < n; ++l)
+    for (int i = 0; lists[l].m && i < lists[l].n && i < kMaxP; ++i) {
+      const fo_mat& a = lists[l].m[i];
+      if (!a.ptr || a.rows <= 0 || a.cols <= 0) continue;
+      const uintptr_t lo = reinterpret_cast<uintptr_t>(a.ptr);
+      spans[count++] = Span{lo, lo + ((a.rows - 1) * a.ld + a.cols) * elem_size(a.dtype), l, i};
+    }
+  // by address: only spans that meet are looked at
+  std::sort(spans, spans + count, [](const Span& a, const Span& b) {
+    return a.lo != b.lo ? a.lo < b.lo : a.list != b.list ? a.list < b.list : a.i < b.i;
+  });
+  for (int x = 0; x < count; ++x)
+    for (int y = x + 1; y < count && spans[y].lo < spans[x].hi; ++y) {
+      // w: the written one (of two, the one of the earlier list or rank)
+      Span w = spans[x], o = spans[y];
+      const bool both = lists[w.list].written && lists[o.list].written;
+      if (!lists[w.list].written || (both && (o.list < w.list || (o.list == w.list && o.i < w.i)))) std::swap(w, o);
+      if (!lists[w.list].written || !host_mats_overlap(lists[w.list].m[w.i], lists[o.list].m[o.i])) continue;
+      bool fine = false;
+      for (int k = 0; k < n_in_place; ++k)
+        fine = fine || (in_place[k][0] == w.list && in_place[k][1] == o.list && w.i == o.i &&
+                        host_same_view(lists[w.list].m[w.i], lists[o.list].m[o.i]));
+      if (!fine)
+        return fail(FO_ERR_INVALID_ARG, "%s[%d] overlaps %s[%d]", lists[w.list].name, w.i, lists[o.list].name, o.i);
+    }
+  return FO_OK;
 }
 bool host_copies_first() { return copies_first(); }
 uint64_t host_timeout_ns(const fo_opts& o) { return timeout_ns(o); }

@@ -349,8 +349,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
 // most of dS's error (rows of 1-8 keys: dQ's and dK's error 2.3 times the output's rounding).
 // But sum_j dS_j of a row is exactly what delta is off by, and costs one sum.  So this pass runs
 // before dK / dV, which then have the corrected delta; and a block whose dS is off by more than
-// 2^-11 (2-norm over its rows of the error's sum against that of |dS|) walks its keys a second
-// time.  For spread attention these are the first one or two blocks of a sequence.
+// 2^-11 (2-norm over its rows of the error's sum against that of |dS|, the latter from a quarter
+// of the keys) walks its keys a second time.  For spread attention these are the first one or two blocks of a sequence.
 //
 // Two warps issue, one the scores and one
 // the gradient: what an issuing warp spends on barriers passes while the pipe runs the other's.
@@ -441,185 +441,184 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
   float* const sums = reinterpret_cast<float*>(smem + L::v);  // between rounds: [error, size][half][128 rows]
 
   for (int round = 0;; ++round) {
-  const int g0 = round * n;  // blocks before this round: the barriers' phases count on
-  float err = 0.f, size = 0.f;
-  if (warp < 4) {
-    if (warp == 0) {  // ---- loads
-      int k_armed = g0, v_armed = g0;
-      if (n > 0 && round == 0 && lane == 0) {
-        mbar_arrive_expect_tx(&ctl->q_full, 2 * L::tile);
-        load_block<D>(&p.maps[rk], smem + L::q, &ctl->q_full, h * D, b.q0 + query0);
-        load_block<D>(&p.maps[3 * p.P + rk], smem + L::d_o, &ctl->q_full, h * D, b.q0 + query0);
+    const int g0 = round * n;  // blocks before this round: the barriers' phases count on
+    float err = 0.f, size = 0.f;
+    if (warp < 4) {
+      if (warp == 0) {  // ---- loads
+        int k_armed = g0, v_armed = g0;
+        if (n > 0 && round == 0 && lane == 0) {
+          mbar_arrive_expect_tx(&ctl->q_full, 2 * L::tile);
+          load_block<D>(&p.maps[rk], smem + L::q, &ctl->q_full, h * D, b.q0 + query0);
+          load_block<D>(&p.maps[3 * p.P + rk], smem + L::d_o, &ctl->q_full, h * D, b.q0 + query0);
+        }
+        for (int i = 0; ok && i < n; ++i) {
+          const int g = g0 + i;
+          ks = g % kKStages;
+          vs = g % kVStages;
+          ok = attn_wait(&ctl->k_empty[ks], ((g / kKStages) & 1) ^ 1, p, kSiteEmpty, lane) &&
+               load_summed<D>(p, &p.maps[p.P + rk], smem + L::k + ks * L::tile, &ctl->k_full[ks], &ctl->fix, fix_uses,
+                              kvh * D, b.k0 + (i0 + i) * kBlk, b.k_len - (i0 + i) * kBlk, lane);
+          if (!ok) break;
+          k_armed = g + 1;
+          ok = attn_wait(&ctl->v_empty[vs], ((g / kVStages) & 1) ^ 1, p, kSiteEmpty, lane);
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&ctl->v_full[vs], L::tile);
+            load_block<D>(&p.maps[2 * p.P + rk], smem + L::v + vs * L::tile, &ctl->v_full[vs], kvh * D,
+                          b.k0 + (i0 + i) * kBlk);
+          }
+          v_armed = g + 1;
+        }
+        if (!ok && lane == 0) {  // wait for the copies in flight
+          mbar_wait_drain(&ctl->q_full, 0, kAttnDrainNs);
+          for (int i = k_armed - kKStages < 0 ? 0 : k_armed - kKStages; i < k_armed; ++i)
+            mbar_wait_drain(&ctl->k_full[i % kKStages], (i / kKStages) & 1, kAttnDrainNs);
+          for (int i = v_armed - kVStages < 0 ? 0 : v_armed - kVStages; i < v_armed; ++i)
+            mbar_wait_drain(&ctl->v_full[i % kVStages], (i / kVStages) & 1, kAttnDrainNs);
+        }
+      } else if (warp == 1 && n > 0) {  // ---- MMAs of S and dP
+        const uint32_t qa = sbase + L::q, da = sbase + L::d_o;
+        ok = ok && attn_wait(&ctl->q_full, 0, p, kSiteFull, lane);
+        for (int i = g0; ok && i < g0 + n; ++i) {
+          // S_i overwrites dS_{i-2}, which dQ_{i-2} has read; dP_i overwrites dP_{i-1}, which has been read
+          ok = attn_wait(&ctl->k_full[ks], kph, p, kSiteFull, lane) &&
+               (i < 2 || attn_wait(&ctl->s_free[i & 1], ((i >> 1) & 1) ^ 1, p, kSiteTmemEmpty, lane));
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_lane()) {
+            issue_scores<D>(tmem + (i & 1) * 128, qa, sbase + L::k + ks * L::tile);
+            umma_commit(&ctl->s_full[i & 1]);
+          }
+          __syncwarp();
+          issued = true;
+          ok = attn_wait(&ctl->v_full[vs], vph, p, kSiteFull, lane) &&
+               (i < 1 || attn_wait(&ctl->dp_free, (i - 1) & 1, p, kSiteTmemEmpty, lane));
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_lane()) {
+            issue_scores<D>(tmem + kColDp, da, sbase + L::v + vs * L::tile);
+            umma_commit(&ctl->dp_full);
+            umma_commit(&ctl->v_empty[vs]);
+          }
+          __syncwarp();
+          if (++ks == kKStages) {
+            ks = 0;
+            kph ^= 1;
+          }
+          if (++vs == kVStages) {
+            vs = 0;
+            vph ^= 1;
+          }
+        }
+        if (!ok && issued && elect_lane()) {
+          umma_commit(&ctl->drain[0]);
+          mbar_wait_drain(&ctl->drain[0], 0, kAttnDrainNs);
+        }
+      } else if (warp == 2 && n > 0) {  // ---- MMAs of dQ
+        for (int i = g0; ok && i < g0 + n; ++i) {
+          ok = attn_wait(&ctl->ds_full, i & 1, p, kSiteTmemFull, lane);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_lane()) {
+            issue_grad<D, 64>(tmem + kColDq, tmem + (i & 1) * 128, sbase + L::k + ks * L::tile, i == g0);
+            umma_commit(&ctl->s_free[i & 1]);
+            umma_commit(&ctl->k_empty[ks]);
+          }
+          __syncwarp();
+          issued = true;
+          if (++ks == kKStages) ks = 0;
+        }
+        if (!ok && issued && elect_lane()) {
+          umma_commit(&ctl->drain[1]);
+          mbar_wait_drain(&ctl->drain[1], 0, kAttnDrainNs);
+        }
       }
+    } else {  // ---- P and dS
+      const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+      const int see = key_end(p.blocks.causal, query + 1, b.q_len, b.k_len);          // keys of this row
+      const int all = key_end(p.blocks.causal, query0 + 1, b.q_len, b.k_len);         // keys of the block's first row
+      const uint64_t c2 = pack2(p.scale_log2, p.scale_log2), l2 = pack2(-lse2, -lse2);
+      uint64_t err2 = 0;
       for (int i = 0; ok && i < n; ++i) {
         const int g = g0 + i;
-        ks = g % kKStages;
-        vs = g % kVStages;
-        ok = attn_wait(&ctl->k_empty[ks], ((g / kKStages) & 1) ^ 1, p, kSiteEmpty, lane) &&
-             load_summed<D>(p, &p.maps[p.P + rk], smem + L::k + ks * L::tile, &ctl->k_full[ks], &ctl->fix, fix_uses,
-                            kvh * D, b.k0 + (i0 + i) * kBlk, b.k_len - (i0 + i) * kBlk, lane);
-        if (!ok) break;
-        k_armed = g + 1;
-        ok = attn_wait(&ctl->v_empty[vs], ((g / kVStages) & 1) ^ 1, p, kSiteEmpty, lane);
-        if (!ok) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&ctl->v_full[vs], L::tile);
-          load_block<D>(&p.maps[2 * p.P + rk], smem + L::v + vs * L::tile, &ctl->v_full[vs], kvh * D,
-                        b.k0 + (i0 + i) * kBlk);
-        }
-        v_armed = g + 1;
-      }
-      if (!ok && lane == 0) {  // wait for the copies in flight
-        mbar_wait_drain(&ctl->q_full, 0, kAttnDrainNs);
-        for (int i = k_armed - kKStages < 0 ? 0 : k_armed - kKStages; i < k_armed; ++i)
-          mbar_wait_drain(&ctl->k_full[i % kKStages], (i / kKStages) & 1, kAttnDrainNs);
-        for (int i = v_armed - kVStages < 0 ? 0 : v_armed - kVStages; i < v_armed; ++i)
-          mbar_wait_drain(&ctl->v_full[i % kVStages], (i / kVStages) & 1, kAttnDrainNs);
-      }
-    } else if (warp == 1 && n > 0) {  // ---- MMAs of S and dP
-      const uint32_t qa = sbase + L::q, da = sbase + L::d_o;
-      ok = ok && attn_wait(&ctl->q_full, 0, p, kSiteFull, lane);
-      for (int i = g0; ok && i < g0 + n; ++i) {
-        // S_i overwrites dS_{i-2}, which dQ_{i-2} has read; dP_i overwrites dP_{i-1}, which has been read
-        ok = attn_wait(&ctl->k_full[ks], kph, p, kSiteFull, lane) &&
-             (i < 2 || attn_wait(&ctl->s_free[i & 1], ((i >> 1) & 1) ^ 1, p, kSiteTmemEmpty, lane));
+        const uint32_t buf = lanes + (g & 1) * 128 + hf * 64;
+        ok = attn_wait(&ctl->s_full[g & 1], (g >> 1) & 1, p, kSiteTmemFull, lane);
         if (!ok) break;
         tc_fence_after();
-        if (elect_lane()) {
-          issue_scores<D>(tmem + (i & 1) * 128, qa, sbase + L::k + ks * L::tile);
-          umma_commit(&ctl->s_full[i & 1]);
+        float s[64];
+        load64(buf, s);
+#pragma unroll
+        for (int k = 0; k < 64; k += 2) {
+          float x0, x1;
+          unpack2(ffma2(pack2(s[k], s[k + 1]), c2, l2), x0, x1);
+          s[k] = fast_exp2(x0);
+          s[k + 1] = fast_exp2(x1);
         }
-        __syncwarp();
-        issued = true;
-        ok = attn_wait(&ctl->v_full[vs], vph, p, kSiteFull, lane) &&
-             (i < 1 || attn_wait(&ctl->dp_free, (i - 1) & 1, p, kSiteTmemEmpty, lane));
+        ok = attn_wait(&ctl->dp_full, g & 1, p, kSiteTmemFull, lane);
         if (!ok) break;
         tc_fence_after();
-        if (elect_lane()) {
-          issue_scores<D>(tmem + kColDp, da, sbase + L::v + vs * L::tile);
-          umma_commit(&ctl->dp_full);
-          umma_commit(&ctl->v_empty[vs]);
-        }
-        __syncwarp();
-        if (++ks == kKStages) {
-          ks = 0;
-          kph ^= 1;
-        }
-        if (++vs == kVStages) {
-          vs = 0;
-          vph ^= 1;
-        }
-      }
-      if (!ok && issued && elect_lane()) {
-        umma_commit(&ctl->drain[0]);
-        mbar_wait_drain(&ctl->drain[0], 0, kAttnDrainNs);
-      }
-    } else if (warp == 2 && n > 0) {  // ---- MMAs of dQ
-      for (int i = g0; ok && i < g0 + n; ++i) {
-        ok = attn_wait(&ctl->ds_full, i & 1, p, kSiteTmemFull, lane);
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_lane()) {
-          issue_grad<D, 64>(tmem + kColDq, tmem + (i & 1) * 128, sbase + L::k + ks * L::tile, i == g0);
-          umma_commit(&ctl->s_free[i & 1]);
-          umma_commit(&ctl->k_empty[ks]);
-        }
-        __syncwarp();
-        issued = true;
-        if (++ks == kKStages) ks = 0;
-      }
-      if (!ok && issued && elect_lane()) {
-        umma_commit(&ctl->drain[1]);
-        mbar_wait_drain(&ctl->drain[1], 0, kAttnDrainNs);
-      }
-    }
-  } else {  // ---- P and dS
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    const int see = key_end(p.blocks.causal, query + 1, b.q_len, b.k_len);          // keys of this row
-    const int all = key_end(p.blocks.causal, query0 + 1, b.q_len, b.k_len);         // keys of the block's first row
-    const uint64_t c2 = pack2(p.scale_log2, p.scale_log2), l2 = pack2(-lse2, -lse2);
-    uint64_t err2 = 0;
-    for (int i = 0; ok && i < n; ++i) {
-      const int g = g0 + i;
-      const uint32_t buf = lanes + (g & 1) * 128 + hf * 64;
-      ok = attn_wait(&ctl->s_full[g & 1], (g >> 1) & 1, p, kSiteTmemFull, lane);
-      if (!ok) break;
-      tc_fence_after();
-      float s[64];
-      load64(buf, s);
+        float dp[64];
+        load64(lanes + kColDp + hf * 64, dp);
+        attn_publish(&ctl->dp_free, lane);
 #pragma unroll
-      for (int k = 0; k < 64; k += 2) {
-        float x0, x1;
-        unpack2(ffma2(pack2(s[k], s[k + 1]), c2, l2), x0, x1);
-        s[k] = fast_exp2(x0);
-        s[k + 1] = fast_exp2(x1);
-      }
-      ok = attn_wait(&ctl->dp_full, g & 1, p, kSiteTmemFull, lane);
-      if (!ok) break;
-      tc_fence_after();
-      float dp[64];
-      load64(lanes + kColDp + hf * 64, dp);
-      attn_publish(&ctl->dp_free, lane);
+        for (int k = 0; k < 64; ++k) s[k] = s[k] * (dp[k] - delta);
+        if ((i0 + i + 1) * kBlk > all) {  // keys that this row does not see: whatever they hold
+          const int upto = see - (i0 + i) * kBlk - hf * 64;
 #pragma unroll
-      for (int k = 0; k < 64; ++k) s[k] = s[k] * (dp[k] - delta);
-      if ((i0 + i + 1) * kBlk > all) {  // keys that this row does not see: whatever they hold
-        const int upto = see - (i0 + i) * kBlk - hf * 64;
-#pragma unroll
-        for (int k = 0; k < 64; ++k)
-          if (k >= upto) s[k] = 0.f;
-      }
-      if (round == 0 && p.delta_mode != kDeltaGiven) {
+          for (int k = 0; k < 64; ++k)
+            if (k >= upto) s[k] = 0.f;
+        }
+        // (of use in the first round alone; a branch here measured 10% slower at head_dim 64)
 #pragma unroll
         for (int k = 0; k < 64; k += 2) {
           err2 = fadd2(err2, pack2(s[k], s[k + 1]));
-          size += fabsf(s[k]) + fabsf(s[k + 1]);
+          if (k % 8 == 0) size += fabsf(s[k]) + fabsf(s[k + 1]);  // a quarter of the keys stands for all
+        }
+        store64_bf16(buf, s);
+        attn_publish(&ctl->ds_full, lane);
+      }
+      float x, y;
+      unpack2(err2, x, y);
+      err = x + y;
+    }
+    if (round > 0 || n == 0 || p.delta_mode == kDeltaGiven) break;
+    // delta's error, row by row, and whether the block is worth a second round
+    __syncwarp();
+    if (warp >= 4) {
+      const int row = quad * 32 + lane;
+      sums[hf * kBlk + row] = live ? err : 0.f;
+      sums[(2 + hf) * kBlk + row] = live ? 4.f * size : 0.f;
+    }
+    __syncthreads();
+    if (warp >= 4) {
+      const int row = quad * 32 + lane;
+      const float e = sums[row] + sums[kBlk + row];
+      delta += e;
+      if (live && hf == 0 && ok) {
+        if (p.delta_mode == kDeltaMeasure) {
+          p.eps[static_cast<int64_t>(split) * p.P * p.heads * p.mq + stat] = e;
+        } else {
+          p.delta[stat] = delta;
         }
       }
-      store64_bf16(buf, s);
-      attn_publish(&ctl->ds_full, lane);
     }
-    float x, y;
-    unpack2(err2, x, y);
-    err = x + y;
-  }
-  if (round > 0 || n == 0 || p.delta_mode == kDeltaGiven) break;
-  // delta's error, row by row, and whether the block is worth a second round
-  __syncwarp();
-  if (warp >= 4) {
-    const int row = quad * 32 + lane;
-    sums[hf * kBlk + row] = live ? err : 0.f;
-    sums[(2 + hf) * kBlk + row] = live ? size : 0.f;
-  }
-  __syncthreads();
-  if (warp >= 4) {
-    const int row = quad * 32 + lane;
-    const float e = sums[row] + sums[kBlk + row];
-    delta += e;
-    if (live && hf == 0 && ok) {
-      if (p.delta_mode == kDeltaMeasure) {
-        p.eps[static_cast<int64_t>(split) * p.P * p.heads * p.mq + stat] = e;
-      } else {
-        p.delta[stat] = delta;
-      }
+    if (p.delta_mode == kDeltaMeasure) break;
+    float e2 = 0.f, a2 = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float e = sums[k * 32 + lane] + sums[kBlk + k * 32 + lane];
+      const float a = sums[2 * kBlk + k * 32 + lane] + sums[3 * kBlk + k * 32 + lane];
+      e2 = fmaf(e, e, e2);
+      a2 = fmaf(a, a, a2);
     }
-  }
-  if (p.delta_mode == kDeltaMeasure) break;
-  float e2 = 0.f, a2 = 0.f;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float e = sums[k * 32 + lane] + sums[kBlk + k * 32 + lane];
-    const float a = sums[2 * kBlk + k * 32 + lane] + sums[3 * kBlk + k * 32 + lane];
-    e2 = fmaf(e, e, e2);
-    a2 = fmaf(a, a, a2);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    e2 += __shfl_xor_sync(0xffffffffu, e2, o);
-    a2 += __shfl_xor_sync(0xffffffffu, a2, o);
-  }
-  if (!(e2 > 0x1p-22f * a2)) break;
-  __syncthreads();               // every warp has read the sums: the stage may be loaded again
-  fence_proxy_async_shared();
+    for (int o = 16; o > 0; o >>= 1) {
+      e2 += __shfl_xor_sync(0xffffffffu, e2, o);
+      a2 += __shfl_xor_sync(0xffffffffu, a2, o);
+    }
+    if (!(e2 > 0x1p-22f * a2)) break;
+    __syncthreads();  // every warp has read the sums: the stage may be loaded again
+    fence_proxy_async_shared();
   }
   if (n > 0 && warp == 2 && ok && elect_lane()) umma_commit(&ctl->acc_full);
   if (warp >= 4) {

@@ -159,21 +159,6 @@ fo_status check_call(const fo_mat* Q, const fo_mat* K, const fo_mat* V, int P, i
   return FO_OK;
 }
 
-struct View {
-  const fo_mat* m;
-  bool written;
-  const char* name;
-};
-fo_status check_apart(const View* v, int n, int P) {
-  for (int i = 0; i < n; ++i)
-    for (int j = 0; j < n && v[i].written; ++j)
-      for (int p = 0; p < P; ++p)
-        for (int q = 0; q < P; ++q)
-          if (!(i == j && p == q) && host_mats_overlap(v[i].m[p], v[j].m[q]))
-            return host_failf(FO_ERR_INVALID_ARG, "%s[%d] overlaps %s[%d]", v[i].name, p, v[j].name, q);
-  return FO_OK;
-}
-
 // Upper bound of the blocks of `unit` rows: exact for one sequence, one more per packed sequence
 int64_t block_bound(const Call& c, int64_t rows, int unit) {
   return c.n > 0 ? rows / unit + c.n : (rows + unit - 1) / unit;
@@ -270,12 +255,14 @@ fo_status fill_args(fo_ctx* ctx, const Call& c, const fo_mat* Q, const fo_mat* K
   if (opts) o = *opts;
   a->timeout_ns = host_timeout_ns(o);
   a->ctrl = host_ctrl(ctx);
-  static bool configured = false;
-  if (!configured) {
+  constexpr int kDevices = 64;  // kernel attributes are a device's own
+  static bool done[kDevices] = {};
+  const int device = host_device(ctx);
+  if (device >= kDevices || !done[device]) {
     cudaError_t e = attn_fwd_configure();
     if (e == cudaSuccess) e = attn_bwd_configure();
     if (e != cudaSuccess) return host_fail(FO_ERR_CUDA, "attention kernel configuration failed");
-    configured = true;
+    if (device < kDevices) done[device] = true;
   }
   return FO_OK;
 }
@@ -294,8 +281,8 @@ fo_status fo_attn_forward(fo_ctx* ctx, const fo_mat* Q, const fo_mat* K, const f
   FO_TRY_HOST(check_call(Q, K, V, P, heads, kv_heads, head_dim, mask, opts, &c));
   FO_TRY_HOST(check_shape(O, "O", P, c.mq, static_cast<int64_t>(heads) * head_dim, FO_BF16));
   FO_TRY_HOST(check_shape(LSE, "LSE", P, heads, c.mq, FO_F32));
-  const View views[] = {{Q, false, "Q"}, {K, false, "K"}, {V, false, "V"}, {O, true, "O"}, {LSE, true, "LSE"}};
-  FO_TRY_HOST(check_apart(views, 5, P));
+  const HostList views[] = {{Q, P, false, "Q"}, {K, P, false, "K"}, {V, P, false, "V"}, {O, P, true, "O"}, {LSE, P, true, "LSE"}};
+  FO_TRY_HOST(host_check_apart(views, 5));
   FO_TRY_HOST(host_check_ctx(ctx, P));
   if (c.mq == 0) return FO_OK;
   DeviceGuard dev(host_device(ctx));
@@ -324,9 +311,9 @@ fo_status fo_attn_backward(fo_ctx* ctx, const fo_mat* Q, const fo_mat* K, const 
   FO_TRY_HOST(check_shape(dQ, "dQ", P, c.mq, qc, FO_BF16));
   FO_TRY_HOST(check_shape(dK, "dK", P, c.mk, kc, FO_BF16));
   FO_TRY_HOST(check_shape(dV, "dV", P, c.mk, kc, FO_BF16));
-  const View views[] = {{Q, false, "Q"},     {K, false, "K"},  {V, false, "V"},  {O, false, "O"}, {LSE, false, "LSE"},
-                        {dO, false, "dO"}, {dQ, true, "dQ"}, {dK, true, "dK"}, {dV, true, "dV"}};
-  FO_TRY_HOST(check_apart(views, 9, P));
+  const HostList views[] = {{Q, P, false, "Q"},     {K, P, false, "K"},  {V, P, false, "V"},  {O, P, false, "O"}, {LSE, P, false, "LSE"},
+                        {dO, P, false, "dO"}, {dQ, P, true, "dQ"}, {dK, P, true, "dK"}, {dV, P, true, "dV"}};
+  FO_TRY_HOST(host_check_apart(views, 9));
   FO_TRY_HOST(host_check_ctx(ctx, P));
   if (c.mq == 0 && c.mk == 0) return FO_OK;
   DeviceGuard dev(host_device(ctx));

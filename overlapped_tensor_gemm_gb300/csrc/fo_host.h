@@ -46,6 +46,15 @@ fo_status host_buffer_kept(fo_ctx* ctx, int slot, size_t bytes, cudaStream_t s, 
 // both have one row pitch, so do their column ranges (views of one wider matrix may not).
 bool host_mats_overlap(const fo_mat& a, const fo_mat& b);
 bool host_same_view(const fo_mat& a, const fo_mat& b);
+// The matrices of a call: no written one may meet another, but for pairs of lists that a kernel
+// reads before it writes (in_place: written list, read list), rank by rank and as one view.
+struct HostList {
+  const fo_mat* m;   // null: absent
+  int n;
+  bool written;
+  const char* name;
+};
+fo_status host_check_apart(const HostList* lists, int n, const int (*in_place)[2] = nullptr, int n_in_place = 0);
 bool host_copies_first();  // host order of a ring's copies and the kernel that waits on them
 uint64_t host_timeout_ns(const fo_opts& o);
 int host_grid(fo_ctx* ctx, const fo_opts& o, int work);

@@ -114,35 +114,6 @@ fo_status check_dtype(const fo_mat& a, const char* what) {
   return a.dtype == FO_BF16 || a.dtype == FO_F32 ? FO_OK : host_failf(FO_ERR_INVALID_ARG, "%s: unknown dtype", what);
 }
 
-// No written matrix may meet another matrix of the call, but for one pair that a row's threads
-// read before they write it (`in_place`, per rank).
-struct View {
-  const fo_mat* m;
-  int n;
-  bool written;
-  const char* name;
-};
-fo_status check_apart(const View* v, int n, const int (*in_place)[2], int n_in_place) {
-  for (int i = 0; i < n; ++i) {
-    if (!v[i].m || !v[i].written) continue;
-    for (int j = 0; j < n; ++j) {
-      if (!v[j].m || (j == i && v[i].n == 1)) continue;
-      for (int p = 0; p < v[i].n; ++p)
-        for (int q = 0; q < v[j].n; ++q) {
-          if (i == j && p == q) continue;
-          if (!host_mats_overlap(v[i].m[p], v[j].m[q])) continue;
-          bool fine = false;
-          for (int k = 0; k < n_in_place; ++k)
-            if (in_place[k][0] == i && in_place[k][1] == j && p == q && host_same_view(v[i].m[p], v[j].m[q]))
-              fine = true;
-          if (!fine)
-            return host_failf(FO_ERR_INVALID_ARG, "%s[%d] overlaps %s[%d]", v[i].name, p, v[j].name, q);
-        }
-    }
-  }
-  return FO_OK;
-}
-
 struct NormCall {
   int64_t m = 0, cols = 0;
   int32_t tr = FO_BF16, ta = FO_BF16, tp = -1;  // residual stream, activations, parameters
@@ -243,12 +214,12 @@ fo_status fo_norm_residual(fo_ctx* ctx, const fo_mat* R, const fo_mat* Y, int P,
   FO_TRY_HOST(check_list(R, "R", P, c.m, c.cols, c.tr));
   FO_TRY_HOST(check_list(R_out, "R_out", P, c.m, c.cols, c.tr));
   FO_TRY_HOST(check_list(X, "X", P, c.m, c.cols, c.ta));
-  const View views[] = {{R, P, false, "R"},         {Y, P, false, "Y"},
+  const HostList views[] = {{R, P, false, "R"},         {Y, P, false, "Y"},
                         {R_out, P, true, "R_out"},  {X, P, true, "X"},
                         {prm->gate, prm->gate_per_token ? P : 1, false, "gate"},
                         {prm->w_post, 1, false, "w_post"}, {prm->w_pre, 1, false, "w_pre"}};
   const int in_place[][2] = {{2, 0}, {3, 1}};  // R_out over R, X over Y
-  FO_TRY_HOST(check_apart(views, 7, in_place, 2));
+  FO_TRY_HOST(host_check_apart(views, 7, in_place, 2));
   FO_TRY_HOST(host_check_ctx(ctx, P));
   if (c.m == 0) return FO_OK;
   DeviceGuard dev(host_device(ctx));
@@ -293,14 +264,14 @@ fo_status fo_norm_residual_backward(fo_ctx* ctx, const fo_mat* R_out, const fo_m
   } else {
     FO_TRY_HOST(check_vector(grads->gate, "dgate", c.cols));
   }
-  const View views[] = {{R_out, P, false, "R_out"}, {Y, P, false, "Y"},   {dX, P, false, "dX"},
+  const HostList views[] = {{R_out, P, false, "R_out"}, {Y, P, false, "Y"},   {dX, P, false, "dX"},
                         {dR_out, P, false, "dR_out"}, {dR, P, true, "dR"}, {dY, P, true, "dY"},
                         {prm->gate, token ? P : 1, false, "gate"},
                         {prm->w_post, 1, false, "w_post"}, {prm->w_pre, 1, false, "w_pre"},
                         {grads->gate, token ? P : 1, true, "dgate"},
                         {grads->w_post, 1, true, "dw_post"}, {grads->w_pre, 1, true, "dw_pre"}};
   const int in_place[][2] = {{4, 3}, {5, 2}};  // dR over dR_out, dY over dX
-  FO_TRY_HOST(check_apart(views, 12, in_place, 2));
+  FO_TRY_HOST(host_check_apart(views, 12, in_place, 2));
   FO_TRY_HOST(host_check_ctx(ctx, P));
   DeviceGuard dev(host_device(ctx));
   if (!dev.ok) return host_fail(FO_ERR_CUDA, "cudaSetDevice failed");

@@ -168,6 +168,7 @@ fo_status rope_run(fo_ctx* ctx, const fo_mat* X, int P, const fo_rope_table* tab
   if (dtype != FO_BF16 && dtype != FO_F32) return host_fail(FO_ERR_INVALID_ARG, "X: unknown dtype");
   if (cols < 1 || cols % head_dim != 0)
     return host_failf(FO_ERR_SHAPE, "%lld columns are no whole number of heads of %d", (long long)cols, head_dim);
+  if (cols > (1 << 26)) return host_fail(FO_ERR_UNSUPPORTED, "more than 2^26 columns");
   bool in_place = true;
   for (int r = 0; r < P; ++r) {
     FO_TRY_HOST(host_check_mat(X[r], dtype, "X", r));
@@ -179,12 +180,9 @@ fo_status rope_run(fo_ctx* ctx, const fo_mat* X, int P, const fo_rope_table* tab
       return host_failf(FO_ERR_UNSUPPORTED, "positions[%d]: not 4-byte aligned", r);
     in_place = in_place && host_same_view(X[r], Y[r]);
   }
-  for (int r = 0; r < P; ++r)
-    for (int q = 0; q < P; ++q) {
-      if (host_mats_overlap(Y[r], X[q]) && !(r == q && host_same_view(X[r], Y[r])))
-        return host_failf(FO_ERR_INVALID_ARG, "Y[%d] overlaps X[%d]", r, q);
-      if (r != q && host_mats_overlap(Y[r], Y[q])) return host_failf(FO_ERR_INVALID_ARG, "Y[%d] overlaps Y[%d]", r, q);
-    }
+  const HostList views[] = {{X, P, false, "X"}, {Y, P, true, "Y"}};
+  const int over[][2] = {{1, 0}};
+  FO_TRY_HOST(host_check_apart(views, 2, over, 1));
   FO_TRY_HOST(host_check_ctx(ctx, P));
   if (m == 0) return FO_OK;
   DeviceGuard dev(host_device(ctx));
