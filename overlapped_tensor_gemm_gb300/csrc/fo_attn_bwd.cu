@@ -59,13 +59,23 @@ __device__ __forceinline__ void store64_bf16(uint32_t taddr, const float (&v)[64
 // dK / dV: a block of 128 keys of one key/value head; walks the query heads of its group and
 // their blocks of 128 queries.
 //
-// TMEM: S^T (then P^T) [0, 128), dP^T (then dS^T) [128, 256), dV [256, 256 + D), dK [384, ...).
-// One buffer each: the tensor pipe runs dV_i and S_{i+1} while the working warps turn dP_i into
+// TMEM: S^T (then P^T) [0, 128), dP^T (then dS^T) [128, 256), dV [256, 256 + D), dK behind it.
+// One buffer each (head_dim 128): the tensor pipe runs dV_i and S_{i+1} while the working warps turn dP_i into
 // dS_i, and dK_i and dP_{i+1} while they turn S_{i+1} into P_{i+1}.  The MMAs of a CTA execute in
 // the order in which its one issuing thread issues them: S_{i+1} overwrites P_i after dV_i has
 // read it, dP_{i+1} overwrites dS_i after dK_i has.
 // ---------------------------------------------------------------------------
-constexpr uint32_t kColS = 0, kColP = 128, kColV = 256, kColK = 384;
+constexpr uint32_t kColP = 128, kColV = 256;
+// head_dim 64 leaves room for a second S^T: scores then never wait for the weights they would
+// overwrite
+template <int D>
+struct DkvCols {
+  static constexpr int bufs = D == 64 ? 2 : 1;
+  static constexpr uint32_t k = 256 + D;
+  __device__ static uint32_t s(int i) { return bufs == 2 && (i & 1) ? 384 : 0; }
+  __device__ static int buf(int i) { return i % bufs; }
+  __device__ static uint32_t parity(int i) { return (i / bufs) & 1; }
+};
 
 template <int D>
 struct DkvSmem {
@@ -75,7 +85,7 @@ struct DkvSmem {
 };
 struct alignas(8) DkvCtl {
   uint64_t kv_full, q_full[2], do_full[2], empty[2], st_full[2], st_empty[2];
-  uint64_t s_full, p_full, dp_full, ds_full, acc_full, fix, drain;
+  uint64_t s_full[2], p_full, dp_full, ds_full, acc_full, fix, drain;
   uint32_t tmem_base, pad;
 };
 template <int D>
@@ -95,6 +105,7 @@ struct QueryWalk {
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_constant__ TrainArgs p) {
   using L = DkvSmem<D>;
+  using Cols = DkvCols<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   DkvCtl* ctl = reinterpret_cast<DkvCtl*>(smem + L::ctl);
@@ -122,7 +133,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
       mbar_init(&ctl->st_full[s], 1);
       mbar_init(&ctl->st_empty[s], kWorkWarps);
     }
-    mbar_init(&ctl->s_full, 1);
+    mbar_init(&ctl->s_full[0], 1);
+    mbar_init(&ctl->s_full[1], 1);
     mbar_init(&ctl->p_full, kWorkWarps);
     mbar_init(&ctl->dp_full, 1);
     mbar_init(&ctl->ds_full, kWorkWarps);
@@ -185,8 +197,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
       if (ok) {
         tc_fence_after();
         if (elect_lane()) {
-          issue_scores<D>(tmem + kColS, ka, sbase + L::q);
-          umma_commit(&ctl->s_full);
+          issue_scores<D>(tmem + Cols::s(0), ka, sbase + L::q);
+          umma_commit(&ctl->s_full[0]);
         }
         __syncwarp();
         issued = true;
@@ -202,15 +214,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
         const uint32_t ph = i & 1, nph = ((i + 1) >> 1) & 1;
         const bool more = i + 1 < w.n;
         // the next block's operands first: once P_i is there, sixteen products follow without a pause
-        ok = (!more || attn_wait(&ctl->q_full[nx], nph, p, kSiteFull, lane)) &&
-             attn_wait(&ctl->p_full, ph, p, kSiteTmemFull, lane);
+        ok = !more || attn_wait(&ctl->q_full[nx], nph, p, kSiteFull, lane);
+        if (Cols::bufs == 2 && ok && more) {
+          if (elect_lane()) {
+            issue_scores<D>(tmem + Cols::s(i + 1), ka, sbase + L::q + nx * L::tile);
+            umma_commit(&ctl->s_full[Cols::buf(i + 1)]);
+          }
+          __syncwarp();
+        }
+        ok = ok && attn_wait(&ctl->p_full, ph, p, kSiteTmemFull, lane);
         if (!ok) break;
         tc_fence_after();
         if (elect_lane()) {
-          issue_grad<D, 64>(tmem + kColV, tmem + kColS, sbase + L::d_o + st * L::tile, i == 0);
-          if (more) {
-            issue_scores<D>(tmem + kColS, ka, sbase + L::q + nx * L::tile);
-            umma_commit(&ctl->s_full);
+          issue_grad<D, 64>(tmem + kColV, tmem + Cols::s(i), sbase + L::d_o + st * L::tile, i == 0);
+          if (Cols::bufs == 1 && more) {
+            issue_scores<D>(tmem + Cols::s(i + 1), ka, sbase + L::q + nx * L::tile);
+            umma_commit(&ctl->s_full[0]);
           }
         }
         __syncwarp();
@@ -219,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
         if (!ok) break;
         tc_fence_after();
         if (elect_lane()) {
-          issue_grad<D, 64>(tmem + kColK, tmem + kColP, sbase + L::q + st * L::tile, i == 0);
+          issue_grad<D, 64>(tmem + Cols::k, tmem + kColP, sbase + L::q + st * L::tile, i == 0);
           umma_commit(&ctl->empty[st]);  // dV_i and dK_i have read the stage
           if (more) {
             issue_scores<D>(tmem + kColP, va, sbase + L::d_o + nx * L::tile);
@@ -269,11 +288,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
       const float* lse = stats + st * 2 * kBlk + hf * 64;
       const float* del = lse + kBlk;
       ok = attn_wait(&ctl->st_full[st], (i >> 1) & 1, p, kSiteFull, lane) &&
-           attn_wait(&ctl->s_full, ph, p, kSiteTmemFull, lane);
+           attn_wait(&ctl->s_full[Cols::buf(i)], Cols::parity(i), p, kSiteTmemFull, lane);
       if (!ok) break;
       tc_fence_after();
       float s[64];
-      load64(lanes + kColS + hf * 64, s);
+      load64(lanes + Cols::s(i) + hf * 64, s);
 #pragma unroll
       for (int k = 0; k < 64; k += 4) {
         const float4 l = *reinterpret_cast<const float4*>(lse + k);
@@ -292,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
         for (int k = 0; k < 64; ++k)
           if (k < from) s[k] = 0.f;
       }
-      store64_bf16(lanes + kColS + hf * 64, s);
+      store64_bf16(lanes + Cols::s(i) + hf * 64, s);
       attn_publish(&ctl->p_full, lane);
       ok = attn_wait(&ctl->dp_full, ph, p, kSiteTmemFull, lane);
       if (!ok) break;
@@ -319,11 +338,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
       if (p.splits > 1) {
         const int64_t at = ((static_cast<int64_t>(split) * p.P + rk) * p.blocks.mk + row) * p.kv_heads * D + kvh * D;
         attn_store_rows(lanes + kColV, hf * (D / 2), D / 2, 1.f, live ? p.part_v + at : nullptr, w.n == 0);
-        attn_store_rows(lanes + kColK, hf * (D / 2), D / 2, p.scale, live ? p.part + at : nullptr, w.n == 0);
+        attn_store_rows(lanes + Cols::k, hf * (D / 2), D / 2, p.scale, live ? p.part + at : nullptr, w.n == 0);
       } else {
         attn_store_rows(lanes + kColV, hf * (D / 2), D / 2, 1.f,
                         live ? p.dv[rk] + row * p.ld_dv[rk] + kvh * D : nullptr, w.n == 0);
-        attn_store_rows(lanes + kColK, hf * (D / 2), D / 2, p.scale,
+        attn_store_rows(lanes + Cols::k, hf * (D / 2), D / 2, p.scale,
                         live ? p.dk[rk] + row * p.ld_dk[rk] + kvh * D : nullptr, w.n == 0);
       }
     }

@@ -7,10 +7,9 @@
 // 4-7 and 8-11 are the softmax of tile 0 and tile 1 (a thread holds a whole query row: no
 // exchange between threads; two threads per row measured 3% slower).
 //
-// TMEM: tile t's scores [128 t, 128 t + 128), overwritten in its first half by their bf16
-// weights, which the product with V reads as its A operand; tile t's output [256 + 128 t, + D).
-// Per tile and block the one issuing thread issues P V of block j, then the scores of block
-// j + 1 over the same columns: a thread's MMAs execute in issue order.  (One issuing warp per tile
+// TMEM: per tile the scores (128 columns), the output (head_dim) and the bf16 weights, which the
+// product with V reads as its A operand.  A thread's MMAs execute in issue order, which is what
+// keeps scores from overwriting weights that are still to be read.  (One issuing warp per tile
 // measured 20% slower: the two tiles' products interleave and both finish late.)
 //
 // The output is rescaled only where a row's maximum grew by more than 2^8 since the last time
@@ -29,10 +28,20 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kTileWarps = 4;
 constexpr uint32_t kTmem = 512;
-constexpr uint32_t kColO = 256;
 constexpr int kKStages = 3, kVStages = 2;
 constexpr float kRescale = 8.0f;  // log2 units
 constexpr float kLn2 = 0.6931471805599453f;
+
+// TMEM columns of tile t.  head_dim 128 fills TMEM: the weights lie over the scores they came from
+// and P V has to be issued before the next scores.  head_dim 64 has room for weights of their own:
+// the next scores go first and P V leaves the softmax's way.
+template <int D>
+struct Cols {
+  static constexpr bool apart = D == 64;
+  __device__ static uint32_t s(int t) { return t * 128; }
+  __device__ static uint32_t o(int t) { return 256 + t * D; }
+  __device__ static uint32_t p(int t) { return apart ? 384 + t * 64 : t * 128; }
+};
 
 template <int D>
 struct Smem {
@@ -142,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
       if (!ok) continue;
       tc_fence_after();
       if (elect_lane()) {
-        issue_scores<D>(tmem + t * 128, sbase + L::q + t * L::tile, sbase + L::k);
+        issue_scores<D>(tmem + Cols<D>::s(t), sbase + L::q + t * L::tile, sbase + L::k);
         umma_commit(&ctl->s_full[t]);
       }
       __syncwarp();
@@ -165,10 +174,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         if (!ok) continue;
         tc_fence_after();
         if (elect_lane()) {
-          issue_grad<D, 128>(tmem + kColO + t * 128, tmem + t * 128, sbase + L::v + vs * L::tile, j == 0);
+          const bool scores = j + 1 < (t ? n[1] : n[0]);
+          if (Cols<D>::apart && scores) {
+            issue_scores<D>(tmem + Cols<D>::s(t), sbase + L::q + t * L::tile, sbase + L::k + ks * L::tile);
+            umma_commit(&ctl->s_full[t]);
+          }
+          issue_grad<D, 128>(tmem + Cols<D>::o(t), tmem + Cols<D>::p(t), sbase + L::v + vs * L::tile, j == 0);
           umma_commit(&ctl->o_done[t]);
-          if (j + 1 < (t ? n[1] : n[0])) {
-            issue_scores<D>(tmem + t * 128, sbase + L::q + t * L::tile, sbase + L::k + ks * L::tile);
+          if (!Cols<D>::apart && scores) {
+            issue_scores<D>(tmem + Cols<D>::s(t), sbase + L::q + t * L::tile, sbase + L::k + ks * L::tile);
             umma_commit(&ctl->s_full[t]);
           }
         }
@@ -198,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
   } else if (warp >= 4) {  // ---- softmax
     const int t = (warp - 4) >> 2, quad = warp & 3;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    const uint32_t sc = lanes + t * 128, oc = lanes + kColO + t * 128;
+    const uint32_t sc = lanes + Cols<D>::s(t), oc = lanes + Cols<D>::o(t), pc = lanes + Cols<D>::p(t);
     const int query = q0[t] + quad * 32 + lane;
     const int see = query < b.q_len ? key_end(p.blocks.causal, query + 1, b.q_len, b.k_len) : 0;  // keys of this row
     const int all = key_end(p.blocks.causal, q0[t] + 1, b.q_len, b.k_len);                        // of the tile's first row
@@ -298,12 +312,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         }
       }
       sum = ffma2(sum, pack2(alpha, alpha), fadd2(bsum[0], bsum[1]));
+      if (Cols<D>::apart && j > 0) {  // the last block's weights have been read
+        ok = attn_wait(&ctl->o_done[t], (j - 1) & 1, p, kSiteDrain, lane);
+        if (!ok) break;
+        tc_fence_after();
+      }
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         uint32_t w[32];
 #pragma unroll
         for (int k = 0; k < 32; ++k) w[k] = packed[c * 32 + k];
-        tmem_st32(sc + c * 32, w);
+        tmem_st32(pc + c * 32, w);
       }
       tmem_wait_st();
       attn_publish(&ctl->p_full[t], lane);
