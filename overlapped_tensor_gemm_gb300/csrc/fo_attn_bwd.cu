@@ -213,39 +213,49 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
         const int st = i & 1, nx = st ^ 1;
         const uint32_t ph = i & 1, nph = ((i + 1) >> 1) & 1;
         const bool more = i + 1 < w.n;
-        // the next block's operands first: once P_i is there, sixteen products follow without a pause
-        ok = !more || attn_wait(&ctl->q_full[nx], nph, p, kSiteFull, lane);
-        if (Cols::bufs == 2 && ok && more) {
+        // The waits for the next block's operands stand between two groups of MMAs, where they pass
+        // while the first group runs.
+        if (Cols::bufs == 2 && more) {
+          ok = attn_wait(&ctl->q_full[nx], nph, p, kSiteFull, lane);
+          if (!ok) break;
           if (elect_lane()) {
             issue_scores<D>(tmem + Cols::s(i + 1), ka, sbase + L::q + nx * L::tile);
             umma_commit(&ctl->s_full[Cols::buf(i + 1)]);
           }
           __syncwarp();
         }
-        ok = ok && attn_wait(&ctl->p_full, ph, p, kSiteTmemFull, lane);
+        ok = attn_wait(&ctl->p_full, ph, p, kSiteTmemFull, lane);
         if (!ok) break;
         tc_fence_after();
-        if (elect_lane()) {
+        if (elect_lane())
           issue_grad<D, 64>(tmem + kColV, tmem + Cols::s(i), sbase + L::d_o + st * L::tile, i == 0);
-          if (Cols::bufs == 1 && more) {
+        __syncwarp();
+        if (Cols::bufs == 1 && more) {
+          ok = attn_wait(&ctl->q_full[nx], nph, p, kSiteFull, lane);
+          if (!ok) break;
+          if (elect_lane()) {
             issue_scores<D>(tmem + Cols::s(i + 1), ka, sbase + L::q + nx * L::tile);
             umma_commit(&ctl->s_full[0]);
           }
+          __syncwarp();
         }
-        __syncwarp();
-        ok = (!more || attn_wait(&ctl->do_full[nx], nph, p, kSiteFull, lane)) &&
-             attn_wait(&ctl->ds_full, ph, p, kSiteTmemFull, lane);
+        ok = attn_wait(&ctl->ds_full, ph, p, kSiteTmemFull, lane);
         if (!ok) break;
         tc_fence_after();
         if (elect_lane()) {
           issue_grad<D, 64>(tmem + Cols::k, tmem + kColP, sbase + L::q + st * L::tile, i == 0);
           umma_commit(&ctl->empty[st]);  // dV_i and dK_i have read the stage
-          if (more) {
+        }
+        __syncwarp();
+        if (more) {
+          ok = attn_wait(&ctl->do_full[nx], nph, p, kSiteFull, lane);
+          if (!ok) break;
+          if (elect_lane()) {
             issue_scores<D>(tmem + kColP, va, sbase + L::d_o + nx * L::tile);
             umma_commit(&ctl->dp_full);
           }
+          __syncwarp();
         }
-        __syncwarp();
       }
       if (ok && elect_lane()) umma_commit(&ctl->acc_full);
       if (!ok && issued && elect_lane()) {

@@ -28,7 +28,6 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kTileWarps = 4;
 constexpr uint32_t kTmem = 512;
-constexpr int kKStages = 3, kVStages = 2;
 constexpr float kRescale = 8.0f;  // log2 units
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -45,11 +44,13 @@ struct Cols {
 
 template <int D>
 struct Smem {
+  static constexpr int ks = D == 64 ? 4 : 2, vs = D == 64 ? 4 : 3;  // stages of keys and of values
   static constexpr uint32_t tile = D / 64 * kHalf;
-  static constexpr uint32_t q = 0, k = 2 * tile, v = k + kKStages * tile, ctl = v + kVStages * tile;
+  static constexpr uint32_t q = 0, k = 2 * tile, v = k + ks * tile, ctl = v + vs * tile;
 };
+constexpr int kMaxStages = 4;
 struct alignas(8) Ctl {
-  uint64_t q_full[2], k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
+  uint64_t q_full[2], k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
   uint64_t s_full[2], p_full[2], o_done[2], fix, drain;
   uint32_t tmem_base, pad;
 };
@@ -62,6 +63,7 @@ static_assert(smem_bytes<128>() <= 232448, "shared memory of one CTA");
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_constant__ TrainArgs p) {
   using L = Smem<D>;
+  constexpr int kKStages = L::ks, kVStages = L::vs;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + L::ctl);
@@ -157,51 +159,59 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
       __syncwarp();
       issued = true;
     }
-    if (ok && elect_lane()) umma_commit(&ctl->k_empty[0]);
-    __syncwarp();
+    // Waits that do not depend on the softmax stand between two groups of MMAs, where they pass
+    // while the first group runs, and the stages that the last block has left are released there.
     int ks = 1, vs = 0;  // stages of block j + 1's keys and of block j's values
     uint32_t kph = 0, vph = 0;
+    ok = ok && attn_wait(&ctl->v_full[0], 0, p, kSiteFull, lane);
     for (int j = 0; ok && j < nmax; ++j) {
-      // the operands first: once a tile's weights are there, its sixteen products follow
-      // without a pause
       const bool more = j + 1 < nmax;
-      ok = attn_wait(&ctl->v_full[vs], vph, p, kSiteFull, lane) &&
-           (!more || attn_wait(&ctl->k_full[ks], kph, p, kSiteFull, lane));
+      const int vn = vs + 1 == kVStages ? 0 : vs + 1;
 #pragma unroll 1
       for (int t = 0; t < 2; ++t) {
-        if (!ok || j >= (t ? n[1] : n[0])) continue;
-        ok = attn_wait(&ctl->p_full[t], j & 1, p, kSiteTmemFull, lane);
-        if (!ok) continue;
-        tc_fence_after();
+        const bool here = j < (t ? n[1] : n[0]), scores = j + 1 < (t ? n[1] : n[0]);
+        auto operands = [&]() -> bool {
+          return !more || (t == 0 ? attn_wait(&ctl->k_full[ks], kph, p, kSiteFull, lane)
+                                  : attn_wait(&ctl->v_full[vn], vn == 0 ? vph ^ 1 : vph, p, kSiteFull, lane));
+        };
+        if (Cols<D>::apart) ok = operands();
+        if (ok && here) {
+          ok = attn_wait(&ctl->p_full[t], j & 1, p, kSiteTmemFull, lane);
+          if (!ok) break;
+          tc_fence_after();
+          if (!Cols<D>::apart) {
+            if (elect_lane()) {
+              issue_grad<D, 128>(tmem + Cols<D>::o(t), tmem + Cols<D>::p(t), sbase + L::v + vs * L::tile, j == 0);
+              umma_commit(&ctl->o_done[t]);
+            }
+            __syncwarp();
+          }
+        }
+        if (!Cols<D>::apart) ok = operands();
+        if (!ok) break;
         if (elect_lane()) {
-          const bool scores = j + 1 < (t ? n[1] : n[0]);
-          if (Cols<D>::apart && scores) {
+          if (scores) {
             issue_scores<D>(tmem + Cols<D>::s(t), sbase + L::q + t * L::tile, sbase + L::k + ks * L::tile);
             umma_commit(&ctl->s_full[t]);
           }
-          issue_grad<D, 128>(tmem + Cols<D>::o(t), tmem + Cols<D>::p(t), sbase + L::v + vs * L::tile, j == 0);
-          umma_commit(&ctl->o_done[t]);
-          if (!Cols<D>::apart && scores) {
-            issue_scores<D>(tmem + Cols<D>::s(t), sbase + L::q + t * L::tile, sbase + L::k + ks * L::tile);
-            umma_commit(&ctl->s_full[t]);
+          if (Cols<D>::apart && here) {
+            issue_grad<D, 128>(tmem + Cols<D>::o(t), tmem + Cols<D>::p(t), sbase + L::v + vs * L::tile, j == 0);
+            umma_commit(&ctl->o_done[t]);
+          }
+          if (t == 0) {  // block j's scores and block j - 1's products with V were the last issued of both tiles
+            umma_commit(&ctl->k_empty[ks == 0 ? kKStages - 1 : ks - 1]);
+            if (j > 0) umma_commit(&ctl->v_empty[vs == 0 ? kVStages - 1 : vs - 1]);
           }
         }
         __syncwarp();
       }
       if (!ok) break;
-      if (elect_lane()) {
-        umma_commit(&ctl->v_empty[vs]);
-        if (more) umma_commit(&ctl->k_empty[ks]);
-      }
-      __syncwarp();
       if (++ks == kKStages) {
         ks = 0;
         kph ^= 1;
       }
-      if (++vs == kVStages) {
-        vs = 0;
-        vph ^= 1;
-      }
+      vs = vn;
+      if (vs == 0) vph ^= 1;
     }
     if (!ok && issued) {
       if (elect_lane()) {
