@@ -47,14 +47,27 @@ __device__ __forceinline__ void load64(uint32_t taddr, float (&v)[64]) {
 #pragma unroll
   for (int k = 0; k < 64; ++k) v[k] = __uint_as_float(w[k >> 5][k & 31]);
 }
-// their bf16 values, two per column, over the first 32 of them
-__device__ __forceinline__ void store64_bf16(uint32_t taddr, const float (&v)[64]) {
+// their bf16 values, two per column, over the first 32 of them; fine: what bf16 leaves of them over
+// the other 32
+__device__ __forceinline__ void store64_bf16(uint32_t taddr, const float (&v)[64], bool fine) {
   uint32_t w[32];
 #pragma unroll
   for (int k = 0; k < 32; ++k) w[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
   tmem_st32(taddr, w);
+  if (fine) {
+#pragma unroll
+    for (int k = 0; k < 32; ++k) w[k] = rest_bf16x2(v[2 * k], v[2 * k + 1], w[k]);
+    tmem_st32(taddr + 32, w);
+  }
   tmem_wait_st();
 }
+// D += A B with A from such columns
+template <int D>
+__device__ __forceinline__ void issue_grad64(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, bool first, bool fine) {
+  issue_grad<D, 64>(d_tmem, a_tmem, b, first);
+  if (fine) issue_grad<D, 64>(d_tmem, a_tmem + 32, b, false);
+}
+
 // ---------------------------------------------------------------------------
 // dK / dV: a block of 128 keys of one key/value head; walks the query heads of its group and
 // their blocks of 128 queries.
@@ -121,6 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
   w.per_head = (b.q_len + kBlk - 1) / kBlk - w.first;
   if (w.per_head < 0) w.per_head = 0;
   const int walk = group * w.per_head;
+  const bool fine = w.per_head <= kFineWalk;
   w.i0 = static_cast<int>(static_cast<int64_t>(walk) * split / p.splits);
   w.n = static_cast<int>(static_cast<int64_t>(walk) * (split + 1) / p.splits) - w.i0;
 
@@ -228,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
         if (!ok) break;
         tc_fence_after();
         if (elect_lane())
-          issue_grad<D, 64>(tmem + kColV, tmem + Cols::s(i), sbase + L::d_o + st * L::tile, i == 0);
+          issue_grad64<D>(tmem + kColV, tmem + Cols::s(i), sbase + L::d_o + st * L::tile, i == 0, fine);
         __syncwarp();
         if (Cols::bufs == 1 && more) {
           ok = attn_wait(&ctl->q_full[nx], nph, p, kSiteFull, lane);
@@ -243,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
         if (!ok) break;
         tc_fence_after();
         if (elect_lane()) {
-          issue_grad<D, 64>(tmem + Cols::k, tmem + kColP, sbase + L::q + st * L::tile, i == 0);
+          issue_grad64<D>(tmem + Cols::k, tmem + kColP, sbase + L::q + st * L::tile, i == 0, fine);
           umma_commit(&ctl->empty[st]);  // dV_i and dK_i have read the stage
         }
         __syncwarp();
@@ -321,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
         for (int k = 0; k < 64; ++k)
           if (k < from) s[k] = 0.f;
       }
-      store64_bf16(lanes + Cols::s(i) + hf * 64, s);
+      store64_bf16(lanes + Cols::s(i) + hf * 64, s, fine);
       attn_publish(&ctl->p_full, lane);
       ok = attn_wait(&ctl->dp_full, ph, p, kSiteTmemFull, lane);
       if (!ok) break;
@@ -336,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
         dp[k + 2] = s[k + 2] * (dp[k + 2] - d.z);
         dp[k + 3] = s[k + 3] * (dp[k + 3] - d.w);
       }
-      store64_bf16(lanes + kColP + hf * 64, dp);
+      store64_bf16(lanes + kColP + hf * 64, dp, fine);
       attn_publish(&ctl->ds_full, lane);
       if (lane == 0) mbar_arrive(&ctl->st_empty[st]);
     }
@@ -417,6 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
   const int q_end = query0 + kBlk < b.q_len ? query0 + kBlk : b.q_len;
   // key blocks [i0, i0 + n) of the walk
   const int walk = (key_end(p.blocks.causal, q_end, b.q_len, b.k_len) + kBlk - 1) / kBlk;
+  const bool fine = walk <= kFineWalk;
   const int i0 = static_cast<int>(static_cast<int64_t>(walk) * split / p.splits);
   const int n = static_cast<int>(static_cast<int64_t>(walk) * (split + 1) / p.splits) - i0;
 
@@ -549,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
           if (!ok) break;
           tc_fence_after();
           if (elect_lane()) {
-            issue_grad<D, 64>(tmem + kColDq, tmem + (i & 1) * 128, sbase + L::k + ks * L::tile, i == g0);
+            issue_grad64<D>(tmem + kColDq, tmem + (i & 1) * 128, sbase + L::k + ks * L::tile, i == g0, fine);
             umma_commit(&ctl->s_free[i & 1]);
             umma_commit(&ctl->k_empty[ks]);
           }
@@ -603,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
           err2 = fadd2(err2, pack2(s[k], s[k + 1]));
           if (k % 8 == 0) size += fabsf(s[k]) + fabsf(s[k + 1]);  // a quarter of the keys stands for all
         }
-        store64_bf16(buf, s);
+        store64_bf16(buf, s, fine);
         attn_publish(&ctl->ds_full, lane);
       }
       float x, y;

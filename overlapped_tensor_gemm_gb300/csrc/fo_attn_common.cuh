@@ -216,6 +216,16 @@ __device__ __forceinline__ void issue_grad(uint32_t d_tmem, uint32_t a_tmem, uin
     umma_ts(d_tmem, a_tmem + k * 16 / kPart * kPart + k * 16 % kPart / 2, bd + k * (2048 >> 4), idesc,
             first && k == 0 ? 0u : 1u);
 }
+// Weights and dS enter their products as bf16.  Over many keys the roundings average out; in a
+// short sequence (a walk of at most kFineWalk blocks) a single weight's rounding reaches a whole
+// row of the result.  There they are split into two bf16 parts, both multiplied: the products are
+// then as exact as the fp32 sums, and so short a walk is bound by latency, not by the tensor pipe.
+constexpr int kFineWalk = 2;
+// what bf16 leaves of a pair whose rounding is `hi`
+__device__ __forceinline__ uint32_t rest_bf16x2(float a, float b, uint32_t hi) {
+  return pack_bf16x2(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xFFFF0000u));
+}
+
 __device__ __forceinline__ void attn_publish(uint64_t* bar, int lane) {
   tc_fence_before();
   __syncwarp();

@@ -81,6 +81,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     n[t] = q0[t] < b.q_len ? (key_end(p.blocks.causal, end, b.q_len, b.k_len) + kBlk - 1) / kBlk : 0;
   }
   const int nmax = n[0] > n[1] ? n[0] : n[1];
+  const bool fine = nmax <= kFineWalk, apart = Cols<D>::apart && !fine;  // fine: the rest of the weights over the scores
 
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
@@ -174,27 +175,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
           return !more || (t == 0 ? attn_wait(&ctl->k_full[ks], kph, p, kSiteFull, lane)
                                   : attn_wait(&ctl->v_full[vn], vn == 0 ? vph ^ 1 : vph, p, kSiteFull, lane));
         };
-        if (Cols<D>::apart) ok = operands();
+        if (apart) ok = operands();
         if (ok && here) {
           ok = attn_wait(&ctl->p_full[t], j & 1, p, kSiteTmemFull, lane);
           if (!ok) break;
           tc_fence_after();
-          if (!Cols<D>::apart) {
+          if (!apart) {
             if (elect_lane()) {
               issue_grad<D, 128>(tmem + Cols<D>::o(t), tmem + Cols<D>::p(t), sbase + L::v + vs * L::tile, j == 0);
+              if (fine)
+                issue_grad<D, 128>(tmem + Cols<D>::o(t), tmem + Cols<D>::s(t) + 64, sbase + L::v + vs * L::tile, false);
               umma_commit(&ctl->o_done[t]);
             }
             __syncwarp();
           }
         }
-        if (!Cols<D>::apart) ok = operands();
+        if (!apart) ok = operands();
         if (!ok) break;
         if (elect_lane()) {
           if (scores) {
             issue_scores<D>(tmem + Cols<D>::s(t), sbase + L::q + t * L::tile, sbase + L::k + ks * L::tile);
             umma_commit(&ctl->s_full[t]);
           }
-          if (Cols<D>::apart && here) {
+          if (apart && here) {
             issue_grad<D, 128>(tmem + Cols<D>::o(t), tmem + Cols<D>::p(t), sbase + L::v + vs * L::tile, j == 0);
             umma_commit(&ctl->o_done[t]);
           }
@@ -322,7 +325,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         }
       }
       sum = ffma2(sum, pack2(alpha, alpha), fadd2(bsum[0], bsum[1]));
-      if (Cols<D>::apart && j > 0) {  // the last block's weights have been read
+      if (fine) {
+        // chunks from the last: each one's rests go over scores that have been read
+        const uint64_t nm = m_ref == -INFINITY ? 0 : pack2(-m_ref, -m_ref);
+#pragma unroll
+        for (int c = 3; c >= 0; --c) {
+          uint32_t w[32], rest[16];
+          tmem_ld32(sc + c * 32, w);
+          tmem_wait_ld();
+          maxima(w, c);  // (the keys that this row does not see)
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            float x0, x1;
+            unpack2(ffma2(pack2(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1])), c2, nm), x0, x1);
+            rest[k] = rest_bf16x2(fast_exp2(x0), fast_exp2(x1), packed[c * 16 + k]);
+          }
+          tmem_st16(sc + 64 + c * 16, rest);
+        }
+      }
+      if (apart && j > 0) {  // the last block's weights have been read
         ok = attn_wait(&ctl->o_done[t], (j - 1) & 1, p, kSiteDrain, lane);
         if (!ok) break;
         tc_fence_after();
