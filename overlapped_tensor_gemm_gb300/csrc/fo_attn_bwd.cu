@@ -115,7 +115,7 @@ struct QueryWalk {
   }
 };
 
-template <int D>
+template <int D, bool kShort>
 __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_constant__ TrainArgs p) {
   using L = DkvSmem<D>;
   using Cols = DkvCols<D>;
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
   w.per_head = (b.q_len + kBlk - 1) / kBlk - w.first;
   if (w.per_head < 0) w.per_head = 0;
   const int walk = group * w.per_head;
-  const bool fine = w.per_head <= kFineWalk;
+  const bool fine = kShort && w.per_head <= kFineWalk;
   w.i0 = static_cast<int>(static_cast<int64_t>(walk) * split / p.splits);
   w.n = static_cast<int>(static_cast<int64_t>(walk) * (split + 1) / p.splits) - w.i0;
 
@@ -416,7 +416,7 @@ constexpr int dq_smem() {
   return static_cast<int>(DqSmem<D>::ctl + sizeof(DqCtl) + 1024);
 }
 
-template <int D>
+template <int D, bool kShort>
 __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_constant__ TrainArgs p) {
   using L = DqSmem<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
   const int q_end = query0 + kBlk < b.q_len ? query0 + kBlk : b.q_len;
   // key blocks [i0, i0 + n) of the walk
   const int walk = (key_end(p.blocks.causal, q_end, b.q_len, b.k_len) + kBlk - 1) / kBlk;
-  const bool fine = walk <= kFineWalk;
+  const bool fine = kShort && walk <= kFineWalk;
   const int i0 = static_cast<int>(static_cast<int64_t>(walk) * split / p.splits);
   const int n = static_cast<int>(static_cast<int64_t>(walk) * (split + 1) / p.splits) - i0;
 
@@ -759,10 +759,14 @@ static cudaError_t configure(K* kernel, int smem) {
 }
 
 cudaError_t attn_bwd_configure() {
-  cudaError_t e = configure(attn_dkv_kernel<64>, dkv_smem<64>());
-  if (e == cudaSuccess) e = configure(attn_dkv_kernel<128>, dkv_smem<128>());
-  if (e == cudaSuccess) e = configure(attn_dq_kernel<64>, dq_smem<64>());
-  if (e == cudaSuccess) e = configure(attn_dq_kernel<128>, dq_smem<128>());
+  cudaError_t e = configure(attn_dkv_kernel<64, false>, dkv_smem<64>());
+  if (e == cudaSuccess) e = configure(attn_dkv_kernel<64, true>, dkv_smem<64>());
+  if (e == cudaSuccess) e = configure(attn_dkv_kernel<128, false>, dkv_smem<128>());
+  if (e == cudaSuccess) e = configure(attn_dkv_kernel<128, true>, dkv_smem<128>());
+  if (e == cudaSuccess) e = configure(attn_dq_kernel<64, false>, dq_smem<64>());
+  if (e == cudaSuccess) e = configure(attn_dq_kernel<64, true>, dq_smem<64>());
+  if (e == cudaSuccess) e = configure(attn_dq_kernel<128, false>, dq_smem<128>());
+  if (e == cudaSuccess) e = configure(attn_dq_kernel<128, true>, dq_smem<128>());
   return e;
 }
 static_assert(dkv_smem<128>() <= 232448 && dq_smem<128>() <= 232448, "shared memory of one CTA");
@@ -796,22 +800,18 @@ cudaError_t attn_delta_add_launch(const TrainArgs& a, cudaStream_t s) {
 cudaError_t attn_dkv_launch(const TrainArgs& a, int dim, cudaStream_t s) {
   const unsigned grid = static_cast<unsigned>(a.blocks.count) * a.kv_heads * a.P * a.splits;
   if (grid == 0) return cudaSuccess;
-  if (dim == 64) {
-    attn_dkv_kernel<64><<<grid, kThreads, dkv_smem<64>(), s>>>(a);
-  } else {
-    attn_dkv_kernel<128><<<grid, kThreads, dkv_smem<128>(), s>>>(a);
-  }
+  const auto kernel = dim == 64 ? (a.short_walks ? attn_dkv_kernel<64, true> : attn_dkv_kernel<64, false>)
+                                : (a.short_walks ? attn_dkv_kernel<128, true> : attn_dkv_kernel<128, false>);
+  kernel<<<grid, kThreads, dim == 64 ? dkv_smem<64>() : dkv_smem<128>(), s>>>(a);
   return cudaGetLastError();
 }
 
 cudaError_t attn_dq_launch(const TrainArgs& a, int dim, cudaStream_t s) {
   const unsigned grid = static_cast<unsigned>(a.blocks.count) * a.heads * a.P * a.splits;
   if (grid == 0) return cudaSuccess;
-  if (dim == 64) {
-    attn_dq_kernel<64><<<grid, kThreads, dq_smem<64>(), s>>>(a);
-  } else {
-    attn_dq_kernel<128><<<grid, kThreads, dq_smem<128>(), s>>>(a);
-  }
+  const auto kernel = dim == 64 ? (a.short_walks ? attn_dq_kernel<64, true> : attn_dq_kernel<64, false>)
+                                : (a.short_walks ? attn_dq_kernel<128, true> : attn_dq_kernel<128, false>);
+  kernel<<<grid, kThreads, dim == 64 ? dq_smem<64>() : dq_smem<128>(), s>>>(a);
   return cudaGetLastError();
 }
 

@@ -109,6 +109,7 @@ struct TrainArgs {
   // fp32 sums to part[((s * P + r) * rows + row) * cols + col] (dV: part_v), which are added after
   int32_t splits;
   float *part, *part_v;
+  int32_t short_walks;          // some walks may be short (kFineWalk)
   int32_t delta_mode;           // dQ: a DeltaMode
   float* eps;                   // kDeltaMeasure: [splits][P][heads][mq]
   Blocks blocks;
@@ -220,6 +221,8 @@ __device__ __forceinline__ void issue_grad(uint32_t d_tmem, uint32_t a_tmem, uin
 // short sequence (a walk of at most kFineWalk blocks) a single weight's rounding reaches a whole
 // row of the result.  There they are split into two bf16 parts, both multiplied: the products are
 // then as exact as the fp32 sums, and so short a walk is bound by latency, not by the tensor pipe.
+// Instantiations with kShort look at each walk; long single sequences run those without (the test
+// and its code cost their loops 4%).
 constexpr int kFineWalk = 2;
 // what bf16 leaves of a pair whose rounding is `hi`
 __device__ __forceinline__ uint32_t rest_bf16x2(float a, float b, uint32_t hi) {

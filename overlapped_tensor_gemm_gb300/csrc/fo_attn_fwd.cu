@@ -60,7 +60,7 @@ constexpr int smem_bytes() {
 }
 static_assert(smem_bytes<128>() <= 232448, "shared memory of one CTA");
 
-template <int D>
+template <int D, bool kShort>
 __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_constant__ TrainArgs p) {
   using L = Smem<D>;
   constexpr int kKStages = L::ks, kVStages = L::vs;
@@ -81,7 +81,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     n[t] = q0[t] < b.q_len ? (key_end(p.blocks.causal, end, b.q_len, b.k_len) + kBlk - 1) / kBlk : 0;
   }
   const int nmax = n[0] > n[1] ? n[0] : n[1];
-  const bool fine = nmax <= kFineWalk, apart = Cols<D>::apart && !fine;  // fine: the rest of the weights over the scores
+  const bool fine = kShort && nmax <= kFineWalk;  // the rest of the weights over the scores
+  const bool apart = Cols<D>::apart && !fine;
 
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
@@ -382,21 +383,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
 
 }  // namespace
 
+template <typename K>
+static cudaError_t configure(K* kernel, int smem) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+}
+
 cudaError_t attn_fwd_configure() {
-  cudaError_t e = cudaFuncSetAttribute(attn_fwd_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<64>());
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(attn_fwd_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<128>());
+  cudaError_t e = configure(attn_fwd_kernel<64, false>, smem_bytes<64>());
+  if (e == cudaSuccess) e = configure(attn_fwd_kernel<64, true>, smem_bytes<64>());
+  if (e == cudaSuccess) e = configure(attn_fwd_kernel<128, false>, smem_bytes<128>());
+  if (e == cudaSuccess) e = configure(attn_fwd_kernel<128, true>, smem_bytes<128>());
   return e;
 }
 
 cudaError_t attn_fwd_launch(const TrainArgs& a, int dim, cudaStream_t s) {
   const unsigned grid = static_cast<unsigned>(a.blocks.count) * a.heads * a.P;
   if (grid == 0) return cudaSuccess;
-  if (dim == 64) {
-    attn_fwd_kernel<64><<<grid, kThreads, smem_bytes<64>(), s>>>(a);
-  } else {
-    attn_fwd_kernel<128><<<grid, kThreads, smem_bytes<128>(), s>>>(a);
-  }
+  const auto kernel = dim == 64 ? (a.short_walks ? attn_fwd_kernel<64, true> : attn_fwd_kernel<64, false>)
+                                : (a.short_walks ? attn_fwd_kernel<128, true> : attn_fwd_kernel<128, false>);
+  kernel<<<grid, kThreads, dim == 64 ? smem_bytes<64>() : smem_bytes<128>(), s>>>(a);
   return cudaGetLastError();
 }
 

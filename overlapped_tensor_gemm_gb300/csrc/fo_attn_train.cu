@@ -248,6 +248,7 @@ fo_status fill_args(fo_ctx* ctx, const Call& c, const fo_mat* Q, const fo_mat* K
   a->heads = c.heads;
   a->kv_heads = c.kv_heads;
   a->mq = static_cast<int32_t>(c.mq);
+  a->short_walks = c.n > 0 || c.mk <= kFineWalk * kBlk || c.mq <= kFineWalk * kBlk;
   a->scale = c.scale;
   a->scale_log2 = static_cast<float>(static_cast<double>(c.scale) * 1.4426950408889634);
   fo_opts o;
