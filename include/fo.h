@@ -373,7 +373,7 @@ typedef struct {
  *   O = exp(S - LSE) V.  A query without keys: O = 0, LSE = -infinity.
  * Any number of rows.  Softmax statistics and sums are fp32; the weights enter the product
  * with V as bf16.  Values of the sequences' rows have to be finite.
- * opts: timeout_us applies (null: defaults). */
+ * opts: timeout_us applies, nothing else has an effect (null: defaults). */
 FO_API fo_status fo_attn_forward(fo_ctx* ctx, const fo_mat* Q, const fo_mat* K, const fo_mat* V, int P,
                                  int heads, int kv_heads, int head_dim, const fo_attn_mask* mask,
                                  const fo_mat* O, const fo_mat* LSE, const fo_opts* opts, void* stream);

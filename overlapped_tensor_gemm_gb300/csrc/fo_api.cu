@@ -207,9 +207,7 @@ fo_status check_mat(const fo_mat& a, int32_t dtype, const char* what, int r) {
   return FO_OK;
 }
 
-fo_status check_common(fo_ctx* ctx, int P, const fo_opts* opts) {
-  if (!ctx) return fail(FO_ERR_INVALID_ARG, "null context");
-  if (P < 1 || P > kMaxP) return fail(FO_ERR_INVALID_ARG, "P=%d outside [1, %d]", P, kMaxP);
+fo_status check_opts(const fo_opts* opts) {
   if (opts) {
     if (opts->order < FO_ORDER_FLASH || opts->order > FO_ORDER_SERIAL)
       return fail(FO_ERR_INVALID_ARG, "unknown order %d", opts->order);
@@ -228,6 +226,12 @@ fo_status check_common(fo_ctx* ctx, int P, const fo_opts* opts) {
     if (opts->split_layer < 0 || opts->split_layer > 1) return fail(FO_ERR_INVALID_ARG, "split_layer must be 0 or 1");
   }
   return FO_OK;
+}
+
+fo_status check_common(fo_ctx* ctx, int P, const fo_opts* opts) {
+  if (!ctx) return fail(FO_ERR_INVALID_ARG, "null context");
+  if (P < 1 || P > kMaxP) return fail(FO_ERR_INVALID_ARG, "P=%d outside [1, %d]", P, kMaxP);
+  return check_opts(opts);
 }
 
 fo_opts default_opts() {
@@ -2028,6 +2032,7 @@ fo_status host_check_ctx(const fo_ctx* ctx, int P) {
   if (P < 1 || P > kMaxP) return fail(FO_ERR_INVALID_ARG, "P=%d outside [1, %d]", P, kMaxP);
   return FO_OK;
 }
+fo_status host_check_opts(const fo_opts* opts) { return check_opts(opts); }
 int host_device(const fo_ctx* ctx) { return ctx->device; }
 fo_status host_buffer_kept(fo_ctx* ctx, int slot, size_t bytes, cudaStream_t s, void** out) try {
   Buffer& b = ctx->bufs[kBufAttnRecv + slot];

@@ -138,7 +138,7 @@ fo_status check_call(const fo_mat* Q, const fo_mat* K, const fo_mat* V, int P, i
     return host_fail(FO_ERR_INVALID_ARG, "num_seqs > 0 goes with q_offsets");
   if (reinterpret_cast<uintptr_t>(mask->q_offsets) % 4 != 0 || reinterpret_cast<uintptr_t>(mask->k_offsets) % 4 != 0)
     return host_fail(FO_ERR_UNSUPPORTED, "offsets not 4-byte aligned");
-  if (opts && opts->num_sms < 0) return host_fail(FO_ERR_INVALID_ARG, "num_sms < 0");
+  FO_TRY_HOST(host_check_opts(opts));
   c->P = P;
   c->heads = heads;
   c->kv_heads = kv_heads;

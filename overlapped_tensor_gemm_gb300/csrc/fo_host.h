@@ -37,6 +37,7 @@ fo_status host_check_mat(const fo_mat& a, int32_t dtype, const char* what, int r
 fo_status host_fail(fo_status st, const char* msg);
 fo_status host_failf(fo_status st, const char* fmt, ...);
 fo_status host_check_ctx(const fo_ctx* ctx, int P);  // null context, P out of range
+fo_status host_check_opts(const fo_opts* opts);      // null: fine
 int host_device(const fo_ctx* ctx);
 // As host_buffer, for calls that a stream capture may hold: a buffer that has to grow stays
 // allocated until the context is destroyed (a captured launch may still use it), and growth

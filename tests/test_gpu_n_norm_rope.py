@@ -167,6 +167,28 @@ def test_norm_without_a_block_and_in_place(ctx):
     assert torch.equal(grads[0], grads[2]) and torch.equal(grads[1], grads[3])
 
 
+def test_norm_after_a_call_that_timed_out(ctx):
+    """The abort word of a timed-out call ends other kernels' waits; a norm waits for its own copies only."""
+    import overlapped_tensor_gemm_gb300 as fo
+    g = torch.Generator().manual_seed(6)
+    m, h = 256, 1
+    qkv = [torch.randn((m, 128), generator=g).to(BF).cuda() for _ in range(3)]
+    O = [torch.empty((m, 128), dtype=BF, device="cuda") for _ in range(2)]
+    with fo.Context(0) as c:
+        c.qsplit_attn([qkv[0]] * 2, [qkv[1]] * 2, [qkv[2]] * 2, O, heads=h, head_dim=128, fault="skip_hop",
+                      timeout_us=20000)
+        R, r64 = _randn(g, (300, 4096), F32)
+        w, w64 = _randn(g, (4096,), BF, 0.2, 1.0)
+        X = guarded((300, 4096), BF)
+        c.norm_residual([R], None, None, [X], w_pre=w)
+        torch.cuda.synchronize()
+        _, x, _ = tr.norm_residual(r64, None, w_pre=w64)
+        _close(X, x, 2 * np.abs(x), BF, "X")
+        with pytest.raises(fo.FoError) as e:
+            c.poll()
+        assert e.value.status == fo.FO_ERR_TIMEOUT
+
+
 def test_norm_no_rows(ctx):
     e = torch.empty((0, 64), dtype=BF, device="cuda")
     w = torch.ones(64, dtype=BF, device="cuda")

@@ -313,6 +313,56 @@ def test_captured_and_replayed(ctx):
         assert torch.equal(a, b[0])
 
 
+@pytest.mark.parametrize("lq,lk", [(0, 40), (40, 0), (0, 0)])
+@pytest.mark.parametrize("packed", [False, True])
+def test_no_queries_or_no_keys(ctx, lq, lk, packed):
+    pb = Problem(1, 2, 1, 64, [(lq, lk)], True, 39, packed=packed)
+    O, LSE, dQ, dK, dV = pb.outputs()
+    ctx.attn_forward(pb.q, pb.k, pb.v, O, LSE, **pb.kw)
+    ctx.attn_backward(pb.q, pb.k, pb.v, O, LSE, pb.do, dQ, dK, dV, **pb.kw)
+    torch.cuda.synchronize()
+    ctx.poll()
+    assert (O[0] == 0).all() and torch.isneginf(LSE[0]).all()
+    assert (dQ[0] == 0).all() and (dK[0] == 0).all() and (dV[0] == 0).all()
+
+
+def test_a_capture_before_the_first_call_is_refused():
+    """Growing a workspace is not something a stream capture can hold: the call says so and enqueues nothing."""
+    import overlapped_tensor_gemm_gb300 as fo
+    pb = Problem(1, 2, 2, 64, [(50, 50)], True, 40)
+    O, LSE, dQ, dK, dV = pb.outputs()
+    with fo.Context(0) as c:
+        c.attn_forward(pb.q, pb.k, pb.v, O, LSE, **pb.kw)  # one sequence: needs no workspace
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            with pytest.raises(fo.FoError) as e:
+                c.attn_backward(pb.q, pb.k, pb.v, O, LSE, pb.do, dQ, dK, dV, **pb.kw)
+            c.attn_forward(pb.q, pb.k, pb.v, O, LSE, **pb.kw)
+        assert e.value.status == fo.FO_ERR_UNSUPPORTED and "capture" in str(e.value)
+        graph.replay()
+        c.attn_backward(pb.q, pb.k, pb.v, O, LSE, pb.do, dQ, dK, dV, **pb.kw)
+        torch.cuda.synchronize()
+        c.poll()
+    assert torch.isfinite(dQ[0].float()).all()
+
+
+def test_a_short_timeout_ends_the_call_with_an_error(ctx):
+    """Waits are bounded: with a limit of one microsecond the kernels give up (or, on a lucky run, finish), the poll
+    says so, and the context computes correctly afterwards."""
+    import overlapped_tensor_gemm_gb300 as fo
+    pb = Problem(1, 2, 1, 128, [(1500, 1500)], True, 42)
+    O, LSE, dQ, dK, dV = pb.outputs()
+    ctx.attn_forward(pb.q, pb.k, pb.v, O, LSE, timeout_us=1, **pb.kw)
+    ctx.attn_backward(pb.q, pb.k, pb.v, O, LSE, pb.do, dQ, dK, dV, timeout_us=1, **pb.kw)
+    torch.cuda.synchronize()
+    try:
+        ctx.poll()
+    except fo.FoError as e:
+        assert e.status == fo.FO_ERR_TIMEOUT
+    _check(ctx, Problem(1, 2, 1, 128, [(300, 300)], True, 43))
+
+
 def test_a_block_of_a_training_step(ctx):
     """The operators together: norm, QKV projection, rotary positions, attention, output projection, gated residual;
     and back.  Against fp32 torch autograd of the same chain on the rounded weights: rel-L2 of each gradient within

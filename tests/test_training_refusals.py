@@ -201,6 +201,15 @@ def test_attention_refusals(lib, change, want, text):
         _refused(run(c), want, text)
 
 
+def test_attention_refuses_bad_options(lib):
+    c = Attn()
+    o = fo.opts()
+    o.order = 7
+    st = fo.load().fo_attn_forward(NULL, c.Q, c.K, c.V, c.P, c.heads, c.kv, c.dim, ctypes.byref(c.mask), c.O, c.LSE,
+                                   ctypes.byref(o), NULL)
+    _refused(st, BAD, "order")
+
+
 def test_attention_outputs_may_not_overlap(lib):
     c = Attn()
     c.O[1] = c.Q[0]
