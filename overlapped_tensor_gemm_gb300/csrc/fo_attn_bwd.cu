@@ -78,10 +78,10 @@ __device__ __forceinline__ void issue_grad64(uint32_t d_tmem, uint32_t a_tmem, u
 // their blocks of 128 queries.
 //
 // TMEM: S^T (then P^T) [0, 128), dP^T (then dS^T) [128, 256), dV [256, 256 + D), dK behind it.
-// One buffer each (head_dim 128): the tensor pipe runs dV_i and S_{i+1} while the working warps turn dP_i into
-// dS_i, and dK_i and dP_{i+1} while they turn S_{i+1} into P_{i+1}.  The MMAs of a CTA execute in
-// the order in which its one issuing thread issues them: S_{i+1} overwrites P_i after dV_i has
-// read it, dP_{i+1} overwrites dS_i after dK_i has.
+// One buffer each (head_dim 128): the tensor pipe runs dV_i and S_{i+1} while the working warps
+// turn dP_i into dS_i, and dK_i and dP_{i+1} while they turn S_{i+1} into P_{i+1}.  The MMAs of
+// a CTA execute in the order in which its one issuing thread issues them: S_{i+1} overwrites P_i
+// after dV_i has read it, dP_{i+1} overwrites dS_i after dK_i has.
 // ---------------------------------------------------------------------------
 constexpr uint32_t kColP = 128, kColV = 256;
 // head_dim 64 leaves room for a second S^T: scores then never wait for the weights they would
@@ -162,6 +162,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
     mbar_init(&ctl->drain, 1);
     fence_barrier_init();
     fence_proxy_async_shared();
+    if (w.n > 0) {  // the first loads go out while the other warps set up
+      mbar_arrive_expect_tx(&ctl->kv_full, 2 * L::tile);
+      load_block<D>(&p.maps[p.P + rk], smem + L::k, &ctl->kv_full, kvh * D, b.k0 + key0);
+      load_block<D>(&p.maps[2 * p.P + rk], smem + L::v, &ctl->kv_full, kvh * D, b.k0 + key0);
+    }
   }
   if (warp == 1) {
     tmem_alloc(&ctl->tmem_base, kTmem);
@@ -179,11 +184,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
       uint32_t fix_uses = 0;
       int armed = 0;  // iterations whose loads have been issued
       bool ok = true, q_armed = false;
-      if (w.n > 0 && lane == 0) {
-        mbar_arrive_expect_tx(&ctl->kv_full, 2 * L::tile);
-        load_block<D>(&p.maps[p.P + rk], smem + L::k, &ctl->kv_full, kvh * D, b.k0 + key0);
-        load_block<D>(&p.maps[2 * p.P + rk], smem + L::v, &ctl->kv_full, kvh * D, b.k0 + key0);
-      }
       for (int i = 0; ok && i < w.n; ++i) {
         const int st = i & 1;
         const uint32_t free_parity = ((i >> 1) & 1) ^ 1;
@@ -462,6 +462,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
     mbar_init(&ctl->fix, 1);
     fence_barrier_init();
     fence_proxy_async_shared();
+    if (n > 0) {  // the first loads go out while the other warps set up
+      mbar_arrive_expect_tx(&ctl->q_full, 2 * L::tile);
+      load_block<D>(&p.maps[rk], smem + L::q, &ctl->q_full, h * D, b.q0 + query0);
+      load_block<D>(&p.maps[3 * p.P + rk], smem + L::d_o, &ctl->q_full, h * D, b.q0 + query0);
+      mbar_arrive_expect_tx(&ctl->v_full[0], L::tile);
+      load_block<D>(&p.maps[2 * p.P + rk], smem + L::v, &ctl->v_full[0], kvh * D, b.k0 + i0 * kBlk);
+    }
   }
   if (warp == 1) {
     tmem_alloc(&ctl->tmem_base, kTmem);
@@ -494,12 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
     float err = 0.f, size = 0.f;
     if (warp < 4) {
       if (warp == 0) {  // ---- loads
-        int k_armed = g0, v_armed = g0;
-        if (n > 0 && round == 0 && lane == 0) {
-          mbar_arrive_expect_tx(&ctl->q_full, 2 * L::tile);
-          load_block<D>(&p.maps[rk], smem + L::q, &ctl->q_full, h * D, b.q0 + query0);
-          load_block<D>(&p.maps[3 * p.P + rk], smem + L::d_o, &ctl->q_full, h * D, b.q0 + query0);
-        }
+        int k_armed = g0, v_armed = g0 > 0 ? g0 : n > 0 ? 1 : 0;  // blocks whose loads have been issued
         for (int i = 0; ok && i < n; ++i) {
           const int g = g0 + i;
           ks = g % kKStages;
@@ -511,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
           k_armed = g + 1;
           ok = attn_wait(&ctl->v_empty[vs], ((g / kVStages) & 1) ^ 1, p, kSiteEmpty, lane);
           if (!ok) break;
-          if (lane == 0) {
+          if (lane == 0 && g > 0) {
             mbar_arrive_expect_tx(&ctl->v_full[vs], L::tile);
             load_block<D>(&p.maps[2 * p.P + rk], smem + L::v + vs * L::tile, &ctl->v_full[vs], kvh * D,
                           b.k0 + (i0 + i) * kBlk);

@@ -95,7 +95,6 @@ __host__ __device__ __forceinline__ int query_begin(int causal, int k, int q_len
   return q < 0 ? 0 : q > q_len ? q_len : q;
 }
 
-
 // Arguments of the training kernels: P independent ranks of one shape.
 struct TrainArgs {
   // per rank r: Q = r, K = P + r, V = 2P + r, dO = 3P + r (boxes of 64 columns x 128 rows)
@@ -105,7 +104,7 @@ struct TrainArgs {
   float* lse[kMaxP];
   int64_t ld_o[kMaxP], ld_do[kMaxP], ld_lse[kMaxP], ld_dq[kMaxP], ld_dk[kMaxP], ld_dv[kMaxP];
   float* delta;                 // backward: [P][heads][mq]
-  // Backward, a block's walk cut into `splits` parts (0, 1: not cut): part s of rank r writes its
+  // Backward, a block's walk cut into `splits` parts (1: not cut): part s of rank r writes its
   // fp32 sums to part[((s * P + r) * rows + row) * cols + col] (dV: part_v), which are added after
   int32_t splits;
   float *part, *part_v;
@@ -122,9 +121,9 @@ struct TrainArgs {
 
 constexpr uint64_t kAttnDrainNs = 200ull * 1000 * 1000;
 constexpr float kLog2e = 1.4426950408889634f;
-
 constexpr int kBlk = 128;                     // queries or keys per block
 constexpr uint32_t kHalf = kBlk * 128;        // 64 columns of a block: 128 rows of one 128-byte swizzle atom
+
 // A whole warp waits: every lane tests the phase (one broadcast access, no exchange between
 // lanes), only a phase that is not complete yet takes lane 0 into the bounded loop.
 __device__ __forceinline__ bool attn_wait(uint64_t* bar, uint32_t parity, const TrainArgs& p, uint32_t site, int lane) {
@@ -169,9 +168,9 @@ __device__ bool load_summed(const TrainArgs& p, const CUtensorMap* map, uint8_t*
 }
 
 // True for one lane of a converged warp, the same one every time.  The compiler knows that code
-// under it runs in one thread and keeps descriptors in uniform registers: an MMA then takes two
-// instructions fewer to issue than under `lane == 0`, on a warp that competes with the softmax
-// warps for issue slots.
+// under it runs in one thread, and issuing an MMA takes less of it: 40 cycles per small MMA in a
+// loop of its own, 46 under `lane == 0`, 68 predicated; on a warp that competes with the softmax
+// warps for issue slots it made the kernels 10-20% faster.
 __device__ __forceinline__ bool elect_lane() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(r));
@@ -205,6 +204,7 @@ __device__ __forceinline__ void issue_scores(uint32_t d_tmem, uint32_t a, uint32
     }
   }
 }
+
 // D[128 x D] += A B over 128 summed rows: A bf16 in TMEM (rows kPart h + 2c, kPart h + 2c + 1 of the
 // sum in column kPart h + c: each group of kPart score columns, overwritten in its first half), B the
 // tile's rows as they lie (MN-major)
@@ -217,6 +217,7 @@ __device__ __forceinline__ void issue_grad(uint32_t d_tmem, uint32_t a_tmem, uin
     umma_ts(d_tmem, a_tmem + k * 16 / kPart * kPart + k * 16 % kPart / 2, bd + k * (2048 >> 4), idesc,
             first && k == 0 ? 0u : 1u);
 }
+
 // Weights and dS enter their products as bf16.  Over many keys the roundings average out; in a
 // short sequence (a walk of at most kFineWalk blocks) a single weight's rounding reaches a whole
 // row of the result.  There they are split into two bf16 parts, both multiplied: the products are
@@ -257,16 +258,19 @@ __device__ __forceinline__ void attn_store_rows(uint32_t taddr, int col0, int n,
       tmem_ld32(taddr + c, v);
       tmem_wait_ld();
     }
-    if (!row) continue;
+    if (row) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      *reinterpret_cast<float4*>(row + c + 4 * k) =
-          make_float4(__uint_as_float(v[4 * k]) * scale, __uint_as_float(v[4 * k + 1]) * scale,
-                      __uint_as_float(v[4 * k + 2]) * scale, __uint_as_float(v[4 * k + 3]) * scale);
+      for (int k = 0; k < 8; ++k)
+        *reinterpret_cast<float4*>(row + c + 4 * k) =
+            make_float4(__uint_as_float(v[4 * k]) * scale, __uint_as_float(v[4 * k + 1]) * scale,
+                        __uint_as_float(v[4 * k + 2]) * scale, __uint_as_float(v[4 * k + 3]) * scale);
+    }
+    __syncwarp();  // TMEM loads are a whole warp's
   }
 }
 // The same as bf16
-__device__ __forceinline__ void attn_store_rows(uint32_t taddr, int col0, int n, float scale, uint16_t* row, bool zero) {
+__device__ __forceinline__ void attn_store_rows(uint32_t taddr, int col0, int n, float scale, uint16_t* row,
+                                                bool zero) {
   for (int c = col0; c < col0 + n; c += 32) {
     uint32_t v[32];
     if (zero) {
@@ -276,14 +280,16 @@ __device__ __forceinline__ void attn_store_rows(uint32_t taddr, int col0, int n,
       tmem_ld32(taddr + c, v);
       tmem_wait_ld();
     }
-    if (!row) continue;
+    if (row) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      st_v4_u32(row + c + 8 * k,
-                pack_bf16x2(__uint_as_float(v[8 * k + 0]) * scale, __uint_as_float(v[8 * k + 1]) * scale),
-                pack_bf16x2(__uint_as_float(v[8 * k + 2]) * scale, __uint_as_float(v[8 * k + 3]) * scale),
-                pack_bf16x2(__uint_as_float(v[8 * k + 4]) * scale, __uint_as_float(v[8 * k + 5]) * scale),
-                pack_bf16x2(__uint_as_float(v[8 * k + 6]) * scale, __uint_as_float(v[8 * k + 7]) * scale));
+      for (int k = 0; k < 4; ++k)
+        st_v4_u32(row + c + 8 * k,
+                  pack_bf16x2(__uint_as_float(v[8 * k + 0]) * scale, __uint_as_float(v[8 * k + 1]) * scale),
+                  pack_bf16x2(__uint_as_float(v[8 * k + 2]) * scale, __uint_as_float(v[8 * k + 3]) * scale),
+                  pack_bf16x2(__uint_as_float(v[8 * k + 4]) * scale, __uint_as_float(v[8 * k + 5]) * scale),
+                  pack_bf16x2(__uint_as_float(v[8 * k + 6]) * scale, __uint_as_float(v[8 * k + 7]) * scale));
+    }
+    __syncwarp();
   }
 }
 

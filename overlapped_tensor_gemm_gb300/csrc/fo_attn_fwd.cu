@@ -107,6 +107,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     mbar_init(&ctl->drain, 1);
     fence_barrier_init();
     fence_proxy_async_shared();
+    // the first loads go out while the other warps set up
+    for (int t = 0; t < 2; ++t)
+      if (n[t] > 0) {
+        mbar_arrive_expect_tx(&ctl->q_full[t], L::tile);
+        load_block<D>(&p.maps[rk], smem + L::q + t * L::tile, &ctl->q_full[t], h * D, b.q0 + q0[t]);
+      }
+    if (nmax > 0) {
+      mbar_arrive_expect_tx(&ctl->k_full[0], L::tile);
+      load_block<D>(&p.maps[p.P + rk], smem + L::k, &ctl->k_full[0], kvh * D, b.k0);
+    }
   }
   if (warp == 1) {
     tmem_alloc(&ctl->tmem_base, kTmem);
@@ -120,19 +130,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
 
   if (warp == 0) {  // ---- loads
     uint32_t fix_uses = 0;
-    int k_armed = 0, v_armed = 0;
+    int k_armed = nmax > 0 ? 1 : 0, v_armed = 0;  // blocks whose loads have been issued
     bool ok = true;
-    if (lane == 0)
-      for (int t = 0; t < 2; ++t)
-        if (n[t] > 0) {
-          mbar_arrive_expect_tx(&ctl->q_full[t], L::tile);
-          load_block<D>(&p.maps[rk], smem + L::q + t * L::tile, &ctl->q_full[t], h * D, b.q0 + q0[t]);
-        }
     for (int j = 0; ok && j < nmax; ++j) {
       const int ks = j % kKStages, vs = j % kVStages;
       ok = attn_wait(&ctl->k_empty[ks], ((j / kKStages) & 1) ^ 1, p, kSiteEmpty, lane);
       if (!ok) break;
-      if (lane == 0) {
+      if (lane == 0 && j > 0) {
         mbar_arrive_expect_tx(&ctl->k_full[ks], L::tile);
         load_block<D>(&p.maps[p.P + rk], smem + L::k + ks * L::tile, &ctl->k_full[ks], kvh * D, b.k0 + j * kBlk);
       }

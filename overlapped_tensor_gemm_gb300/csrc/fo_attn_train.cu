@@ -282,7 +282,11 @@ fo_status fo_attn_forward(fo_ctx* ctx, const fo_mat* Q, const fo_mat* K, const f
   FO_TRY_HOST(check_call(Q, K, V, P, heads, kv_heads, head_dim, mask, opts, &c));
   FO_TRY_HOST(check_shape(O, "O", P, c.mq, static_cast<int64_t>(heads) * head_dim, FO_BF16));
   FO_TRY_HOST(check_shape(LSE, "LSE", P, heads, c.mq, FO_F32));
-  const HostList views[] = {{Q, P, false, "Q"}, {K, P, false, "K"}, {V, P, false, "V"}, {O, P, true, "O"}, {LSE, P, true, "LSE"}};
+  const HostList views[] = {{Q, P, false, "Q"},
+                            {K, P, false, "K"},
+                            {V, P, false, "V"},
+                            {O, P, true, "O"},
+                            {LSE, P, true, "LSE"}};
   FO_TRY_HOST(host_check_apart(views, 5));
   FO_TRY_HOST(host_check_ctx(ctx, P));
   if (c.mq == 0) return FO_OK;
@@ -312,8 +316,9 @@ fo_status fo_attn_backward(fo_ctx* ctx, const fo_mat* Q, const fo_mat* K, const 
   FO_TRY_HOST(check_shape(dQ, "dQ", P, c.mq, qc, FO_BF16));
   FO_TRY_HOST(check_shape(dK, "dK", P, c.mk, kc, FO_BF16));
   FO_TRY_HOST(check_shape(dV, "dV", P, c.mk, kc, FO_BF16));
-  const HostList views[] = {{Q, P, false, "Q"},     {K, P, false, "K"},  {V, P, false, "V"},  {O, P, false, "O"}, {LSE, P, false, "LSE"},
-                        {dO, P, false, "dO"}, {dQ, P, true, "dQ"}, {dK, P, true, "dK"}, {dV, P, true, "dV"}};
+  const HostList views[] = {{Q, P, false, "Q"},     {K, P, false, "K"},   {V, P, false, "V"},
+                            {O, P, false, "O"},     {LSE, P, false, "LSE"}, {dO, P, false, "dO"},
+                            {dQ, P, true, "dQ"},    {dK, P, true, "dK"},  {dV, P, true, "dV"}};
   FO_TRY_HOST(host_check_apart(views, 9));
   FO_TRY_HOST(host_check_ctx(ctx, P));
   if (c.mq == 0 && c.mk == 0) return FO_OK;

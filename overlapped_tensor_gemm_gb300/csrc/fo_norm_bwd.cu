@@ -182,10 +182,11 @@ __global__ void __launch_bounds__(T, T <= 512 ? 512 / T : 1) norm_bwd_kernel(con
 template <bool kVec, int T>
 NormKernel of(bool r32, bool a32, bool p32) {
   const int i = (r32 ? 4 : 0) + (a32 ? 2 : 0) + (p32 ? 1 : 0);
-  const NormKernel k[8] = {norm_bwd_kernel<uint16_t, uint16_t, uint16_t, kVec, T>, norm_bwd_kernel<uint16_t, uint16_t, float, kVec, T>,
-                           norm_bwd_kernel<uint16_t, float, uint16_t, kVec, T>,    norm_bwd_kernel<uint16_t, float, float, kVec, T>,
-                           norm_bwd_kernel<float, uint16_t, uint16_t, kVec, T>,    norm_bwd_kernel<float, uint16_t, float, kVec, T>,
-                           norm_bwd_kernel<float, float, uint16_t, kVec, T>,       norm_bwd_kernel<float, float, float, kVec, T>};
+  const NormKernel k[8] = {
+      norm_bwd_kernel<uint16_t, uint16_t, uint16_t, kVec, T>, norm_bwd_kernel<uint16_t, uint16_t, float, kVec, T>,
+      norm_bwd_kernel<uint16_t, float, uint16_t, kVec, T>, norm_bwd_kernel<uint16_t, float, float, kVec, T>,
+      norm_bwd_kernel<float, uint16_t, uint16_t, kVec, T>, norm_bwd_kernel<float, uint16_t, float, kVec, T>,
+      norm_bwd_kernel<float, float, uint16_t, kVec, T>, norm_bwd_kernel<float, float, float, kVec, T>};
   return k[i];
 }
 
