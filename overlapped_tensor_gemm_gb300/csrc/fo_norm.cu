@@ -77,7 +77,8 @@ fo_status plan_launch(fo_ctx* ctx, NormArgs* a, bool backward, bool r32, bool a3
   while (ctas > 1 && 2 * static_cast<int>(stage) > kNormSmem / ctas - kNormStatic) --ctas;
   const int room = kNormSmem / ctas - kNormStatic;
   uint32_t pitch = (static_cast<uint32_t>(a->cols) * (p32 ? 4 : 2) + 127) / 128 * 128;
-  if (!backward || !vec || !(a->w_post || a->w_pre || a->gate) || 2 * static_cast<int>(stage) + 3 * static_cast<int>(pitch) > room)
+  if (!backward || !vec || !(a->w_post || a->w_pre || a->gate) ||
+      2 * static_cast<int>(stage) + 3 * static_cast<int>(pitch) > room)
     pitch = 0;
   a->par_pitch = pitch;
   a->stages = stage ? (room - 3 * static_cast<int>(pitch)) / static_cast<int>(stage) : 2;
@@ -292,7 +293,8 @@ fo_status fo_norm_residual_backward(fo_ctx* ctx, const fo_mat* R_out, const fo_m
   FO_TRY_HOST(plan_launch(ctx, &a, true, c.tr == FO_F32, c.ta == FO_F32, c.tp == FO_F32, &l));
   const int grid = l.grid;
   void* part = nullptr;
-  FO_TRY_HOST(host_buffer_kept(ctx, kSlotNormPart, static_cast<size_t>(host_num_sms(ctx)) * 2 * 3 * c.cols * 4, s, &part));
+  const size_t part_bytes = static_cast<size_t>(host_num_sms(ctx)) * 2 * 3 * c.cols * 4;  // two CTAs per SM at most
+  FO_TRY_HOST(host_buffer_kept(ctx, kSlotNormPart, part_bytes, s, &part));
   a.part = static_cast<float*>(part);
   if (grid > 0) {
     l.kernel<<<grid, l.threads, l.smem, s>>>(a);
