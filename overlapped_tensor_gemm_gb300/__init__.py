@@ -164,7 +164,9 @@ def mat(t) -> FoMat:
     else:
         raise TypeError(f"unsupported dtype {t.dtype}")
     ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
-    return FoMat(t.data_ptr(), dt, 0, t.shape[0], t.shape[1], max(ld, t.shape[1]))
+    if ld < t.shape[1]:
+        raise ValueError(f"rows {ld} elements apart share memory (an expanded view?): need {t.shape[1]} or more")
+    return FoMat(t.data_ptr(), dt, 0, t.shape[0], t.shape[1], ld)
 
 
 _MAT_ARRAYS = [FoMat * n for n in range(65)]  # array types by length
@@ -349,14 +351,14 @@ class Context:
             if t.get_device() != self.device:
                 self._here(t, what)
             dt, shape, stride = codes.get(t.dtype), t.shape, t.stride()
-            if dt is None or len(shape) != 2 or (stride[1] != 1 and shape[1] > 1):
+            if dt is None or len(shape) != 2 or (stride[1] != 1 and shape[1] > 1) or stride[0] < shape[1]:
                 m = mat(t)
                 ptr, dt, rows, cols, ld = m.ptr, m.dtype, m.rows, m.cols, m.ld
             else:
                 ptr, (rows, cols), ld = t.data_ptr(), shape, stride[0]
             if rows <= 1:  # the row pitch of one row is not used: any whole number of 16 bytes
                 ld = cols + 7 & -8
-            _PACK_MAT(arr, at, ptr or 0, dt, 0, rows, cols, ld if ld > cols else cols)
+            _PACK_MAT(arr, at, ptr or 0, dt, 0, rows, cols, ld)
             at += _MAT_BYTES
         return arr
 

@@ -3,6 +3,7 @@ argument is checked before the context is, so a null context reaches the checks 
 import ctypes
 import math
 import os
+import types
 
 import numpy as np
 import pytest
@@ -293,3 +294,21 @@ def test_rope_table_frequencies(lib, kw, how, rot, base):
     want -= np.floor(want)
     # a few roundings in 64 bits (pow: 1 ulp; a frequency above one turn loses its whole turns' bits)
     assert np.abs(got - want).max() <= 16 * 2.0 ** -53 * max(1.0, freq.max())
+
+
+def test_views_whose_rows_share_memory(lib):
+    """An expanded gradient (the gradient of a sum, say) has rows 0 elements apart: read as if its rows lay one
+    behind another, it would be read past its end."""
+    torch = pytest.importorskip("torch")
+    here = types.SimpleNamespace(device=-1)  # what get_device() says of the host
+    for t in (torch.zeros(1, 16).expand(4, 16), torch.zeros(64).as_strided((4, 16), (8, 1)),
+              torch.zeros(1, 4, 4).expand(4, 4, 4)):
+        with pytest.raises(ValueError, match="share memory"):
+            fo.mat(t)
+        with pytest.raises(ValueError, match="share memory"):
+            fo.Context._list(here, [t], 1, "dO")
+    for t in (torch.zeros(1, 16), torch.zeros(64).as_strided((1, 16), (0, 1)), torch.zeros(0, 16),
+              torch.zeros(4, 24)[:, :16]):
+        m = fo.Context._list(here, [t], 1, "dO")[0]
+        assert (m.ptr or 0, m.rows, m.cols) == (t.data_ptr(), *t.shape)
+        assert m.ld == (24 if t.shape[0] == 4 else 16)
