@@ -375,8 +375,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
       const float l = lo + hi;
       const bool live = query < b.q_len;
       const int64_t row = b.q0 + query;
-      if (live) p.lse[rk][h * p.ld_lse[rk] + row] = l > 0.f ? fmaf(m_ref, kLn2, logf(l)) : -INFINITY;
-      attn_store_rows(oc, 0, D, l > 0.f ? 1.f / l : 0.f, live ? p.out_o[rk] + row * p.ld_o[rk] + h * D : nullptr,
+      const bool none = l == 0.f;  // no key; a NaN among the row's scores stays one in both outputs
+      if (live) p.lse[rk][h * p.ld_lse[rk] + row] = none ? -INFINITY : fmaf(m_ref, kLn2, logf(l));
+      attn_store_rows(oc, 0, D, none ? 0.f : 1.f / l, live ? p.out_o[rk] + row * p.ld_o[rk] + h * D : nullptr,
                       n[t] == 0);
     }
   }

@@ -249,6 +249,19 @@ def test_constant_values_come_through(ctx):
     assert (O[0].float() - 1.5).abs().max() <= 1.5 * 2 * HALF
 
 
+@pytest.mark.parametrize("n,d", [(700, 128), (90, 128), (700, 64), (90, 64)])
+def test_a_nan_stays_in_its_row(ctx, n, d):
+    """A NaN query turns its row's output and statistic into NaN, in its head alone, and nothing else."""
+    pb = Problem(1, 2, 1, d, [(n, n)], True, 37)
+    (O, LSE, *_), (O2, LSE2, *_) = pb.outputs(), pb.outputs()
+    ctx.attn_forward(pb.q, pb.k, pb.v, O, LSE, **pb.kw)
+    pb.q[0][50, d + 3] = float("nan")
+    ctx.attn_forward(pb.q, pb.k, pb.v, O2, LSE2, **pb.kw)
+    assert torch.isnan(O2[0][50, d:]).all() and torch.isnan(LSE2[0][1, 50])
+    O2[0][50, d:], LSE2[0][1, 50] = O[0][50, d:], LSE[0][1, 50]
+    assert torch.equal(O2[0], O[0]) and torch.equal(LSE2[0], LSE[0])
+
+
 def test_bad_offsets_are_reported(ctx):
     import overlapped_tensor_gemm_gb300 as fo
     pb = Problem(1, 2, 2, 64, [(40, 40), (30, 30)], True, 35, behind=1)
