@@ -57,6 +57,10 @@ struct alignas(8) Ctl {
   uint64_t q_full[2], k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
   uint64_t s_full[2], p_full[2], o_done[2], fix, drain;
   uint32_t tmem_base, pad;
+  // the sequence's outputs of this head
+  float* lse;
+  uint16_t* out;
+  int64_t ld_out;
 };
 template <int D>
 constexpr int smem_bytes() {
@@ -121,6 +125,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
   if (warp == 1) {
     tmem_alloc(&ctl->tmem_base, kTmem);
     tmem_relinquish();
+  }
+  if (warp == 2 && lane == 0) {  // a rank's arguments come late: fetched here, nobody waits for them
+    ctl->lse = p.lse[rk] + h * p.ld_lse[rk] + b.q0;
+    ctl->ld_out = p.ld_o[rk];
+    ctl->out = p.out_o[rk] + b.q0 * ctl->ld_out + h * D;
   }
   tc_fence_before();
   __syncthreads();
@@ -374,11 +383,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
       unpack2(sum, lo, hi);
       const float l = lo + hi;
       const bool live = query < b.q_len;
-      const int64_t row = b.q0 + query;
       const bool none = l == 0.f;  // no key; a NaN among the row's scores stays one in both outputs
-      if (live) p.lse[rk][h * p.ld_lse[rk] + row] = none ? -INFINITY : fmaf(m_ref, kLn2, logf(l));
-      attn_store_rows(oc, 0, D, none ? 0.f : 1.f / l, live ? p.out_o[rk] + row * p.ld_o[rk] + h * D : nullptr,
-                      n[t] == 0);
+      if (live) ctl->lse[query] = none ? -INFINITY : fmaf(m_ref, kLn2, logf(l));
+      attn_store_rows(oc, 0, D, none ? 0.f : 1.f / l, live ? ctl->out + query * ctl->ld_out : nullptr, n[t] == 0);
     }
   }
   __syncwarp();
