@@ -362,17 +362,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
     if (ok && w.n > 0) ok = attn_wait(&ctl->acc_full, 0, p, kSiteDrain, lane);
     if (ok) {
       tc_fence_after();
-      const bool live = key < b.k_len;
-      const int64_t row = b.k0 + key;
+      // the tiles of K and V have been read: their memory turns the rows
+      const int first = key0 + quad * 32, rows = b.k_len - first;
+      const int64_t row = b.k0 + first;
       if (p.splits > 1) {
-        const int64_t at = ((static_cast<int64_t>(split) * p.P + rk) * p.blocks.mk + row) * p.kv_heads * D + kvh * D;
-        attn_store_rows(lanes + kColV, hf * (D / 2), D / 2, 1.f, live ? p.part_v + at : nullptr, w.n == 0);
-        attn_store_rows(lanes + Cols::k, hf * (D / 2), D / 2, p.scale, live ? p.part + at : nullptr, w.n == 0);
+        const int64_t ld = static_cast<int64_t>(p.kv_heads) * D;
+        const int64_t at = ((static_cast<int64_t>(split) * p.P + rk) * p.blocks.mk + row) * ld + kvh * D + hf * (D / 2);
+        uint8_t* stage = smem + L::k + (warp - 4) * (32 * D / 2 * 4);
+        attn_store_rows<D / 2>(lanes + kColV, hf * (D / 2), 1.f, stage, p.part_v + at, ld, rows, w.n == 0);
+        attn_store_rows<D / 2>(lanes + Cols::k, hf * (D / 2), p.scale, stage, p.part + at, ld, rows, w.n == 0);
       } else {
-        attn_store_rows(lanes + kColV, hf * (D / 2), D / 2, 1.f,
-                        live ? p.dv[rk] + row * p.ld_dv[rk] + kvh * D : nullptr, w.n == 0);
-        attn_store_rows(lanes + Cols::k, hf * (D / 2), D / 2, p.scale,
-                        live ? p.dk[rk] + row * p.ld_dk[rk] + kvh * D : nullptr, w.n == 0);
+        uint8_t* stage = smem + L::k + (warp - 4) * (32 * D / 2 * 2);
+        const int col = kvh * D + hf * (D / 2);
+        attn_store_rows<D / 2>(lanes + kColV, hf * (D / 2), 1.f, stage, p.dv[rk] + row * p.ld_dv[rk] + col, p.ld_dv[rk],
+                               rows, w.n == 0);
+        attn_store_rows<D / 2>(lanes + Cols::k, hf * (D / 2), p.scale, stage, p.dk[rk] + row * p.ld_dk[rk] + col,
+                               p.ld_dk[rk], rows, w.n == 0);
       }
     }
   }
@@ -677,13 +682,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
     if (ok && p.delta_mode != kDeltaMeasure) {
       tc_fence_after();
       const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-      const int64_t row = b.q0 + query;
+      // the tiles of K have been read: their memory turns the rows
+      const int first = query0 + quad * 32, rows = b.q_len - first;
+      const int64_t row = b.q0 + first;
       if (p.splits > 1) {
-        const int64_t at = ((static_cast<int64_t>(split) * p.P + rk) * p.mq + row) * p.heads * D + h * D;
-        attn_store_rows(lanes + kColDq, hf * (D / 2), D / 2, p.scale, live ? p.part + at : nullptr, n == 0);
+        const int64_t ld = static_cast<int64_t>(p.heads) * D;
+        const int64_t at = ((static_cast<int64_t>(split) * p.P + rk) * p.mq + row) * ld + h * D + hf * (D / 2);
+        attn_store_rows<D / 2>(lanes + kColDq, hf * (D / 2), p.scale, smem + L::k + (warp - 4) * (32 * D / 2 * 4),
+                               p.part + at, ld, rows, n == 0);
       } else {
-        attn_store_rows(lanes + kColDq, hf * (D / 2), D / 2, p.scale,
-                        live ? p.dq[rk] + row * p.ld_dq[rk] + h * D : nullptr, n == 0);
+        attn_store_rows<D / 2>(lanes + kColDq, hf * (D / 2), p.scale, smem + L::k + (warp - 4) * (32 * D / 2 * 2),
+                               p.dq[rk] + row * p.ld_dq[rk] + h * D + hf * (D / 2), p.ld_dq[rk], rows, n == 0);
       }
     }
   }

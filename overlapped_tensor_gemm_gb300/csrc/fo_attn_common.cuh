@@ -246,51 +246,55 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
       : "memory");
 }
 
-// A warp's 32 accumulator rows, columns [col0, col0 + n), times `scale`, as fp32 to `row` (null:
-// not stored); zero: nothing was accumulated
-__device__ __forceinline__ void attn_store_rows(uint32_t taddr, int col0, int n, float scale, float* row, bool zero) {
-  for (int c = col0; c < col0 + n; c += 32) {
+// A warp's 32 accumulator rows, N columns from col0 on, times `scale`, to the first `rows` rows of a
+// matrix at `out` (16-byte aligned rows); zero: nothing was accumulated.  `stage`: 32 * N * sizeof(T)
+// bytes of shared memory that nothing reads any more.  A thread's row is turned there, so that a
+// store covers whole lines: with each lane storing its own row (32 lines per instruction) a tile's
+// rows took 2300 cycles.  16-byte pieces change places inside a row by the row's index (no bank
+// conflicts in either direction).
+template <int N, typename T>
+__device__ __forceinline__ void attn_store_rows(uint32_t taddr, int col0, float scale, uint8_t* stage, T* out,
+                                                int64_t ld, int rows, bool zero) {
+  constexpr int kPieces = N * static_cast<int>(sizeof(T)) / 16, kPer = 16 / static_cast<int>(sizeof(T));
+  static_assert(kPieces == 4 || kPieces == 8 || kPieces == 16, "pieces of a row");
+  auto at = [&](int row, int piece) {
+    return reinterpret_cast<uint4*>(stage + (row * kPieces + (piece ^ (kPieces == 4 ? row >> 1 & 3 : row & 7))) * 16);
+  };
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int c = 0; c < N; c += 32) {
     uint32_t v[32];
     if (zero) {
 #pragma unroll
       for (int k = 0; k < 32; ++k) v[k] = 0u;
     } else {
-      tmem_ld32(taddr + c, v);
+      tmem_ld32(taddr + col0 + c, v);
       tmem_wait_ld();
     }
-    if (row) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        *reinterpret_cast<float4*>(row + c + 4 * k) =
-            make_float4(__uint_as_float(v[4 * k]) * scale, __uint_as_float(v[4 * k + 1]) * scale,
-                        __uint_as_float(v[4 * k + 2]) * scale, __uint_as_float(v[4 * k + 3]) * scale);
+    for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * scale);
+#pragma unroll
+    for (int k = 0; k < 32 / kPer; ++k) {
+      uint4 w;
+      if constexpr (sizeof(T) == 4) {
+        w = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+      } else {
+        uint32_t q[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          q[i] = pack_bf16x2(__uint_as_float(v[8 * k + 2 * i]), __uint_as_float(v[8 * k + 2 * i + 1]));
+        w = make_uint4(q[0], q[1], q[2], q[3]);
+      }
+      *at(lane, c / kPer + k) = w;
     }
-    __syncwarp();  // TMEM loads are a whole warp's
   }
-}
-// The same as bf16
-__device__ __forceinline__ void attn_store_rows(uint32_t taddr, int col0, int n, float scale, uint16_t* row,
-                                                bool zero) {
-  for (int c = col0; c < col0 + n; c += 32) {
-    uint32_t v[32];
-    if (zero) {
-#pragma unroll
-      for (int k = 0; k < 32; ++k) v[k] = 0u;
-    } else {
-      tmem_ld32(taddr + c, v);
-      tmem_wait_ld();
-    }
-    if (row) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        st_v4_u32(row + c + 8 * k,
-                  pack_bf16x2(__uint_as_float(v[8 * k + 0]) * scale, __uint_as_float(v[8 * k + 1]) * scale),
-                  pack_bf16x2(__uint_as_float(v[8 * k + 2]) * scale, __uint_as_float(v[8 * k + 3]) * scale),
-                  pack_bf16x2(__uint_as_float(v[8 * k + 4]) * scale, __uint_as_float(v[8 * k + 5]) * scale),
-                  pack_bf16x2(__uint_as_float(v[8 * k + 6]) * scale, __uint_as_float(v[8 * k + 7]) * scale));
-    }
-    __syncwarp();
+  __syncwarp();
+#pragma unroll 4
+  for (int i = 0; i < kPieces; ++i) {
+    const int row = (i * 32 + lane) / kPieces, piece = lane % kPieces;
+    if (row < rows) *reinterpret_cast<uint4*>(out + row * ld + piece * kPer) = *at(row, piece);
   }
+  __syncwarp();  // the stage may be written again
 }
 
 // What the dQ pass does about delta's error (see there)

@@ -382,10 +382,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
       float lo, hi;
       unpack2(sum, lo, hi);
       const float l = lo + hi;
-      const bool live = query < b.q_len;
       const bool none = l == 0.f;  // no key; a NaN among the row's scores stays one in both outputs
-      if (live) ctl->lse[query] = none ? -INFINITY : fmaf(m_ref, kLn2, logf(l));
-      attn_store_rows(oc, 0, D, none ? 0.f : 1.f / l, live ? ctl->out + query * ctl->ld_out : nullptr, n[t] == 0);
+      if (query < b.q_len) ctl->lse[query] = none ? -INFINITY : fmaf(m_ref, kLn2, logf(l));
+      const int first = q0[t] + quad * 32;  // (every product that reads the tile's queries is done)
+      attn_store_rows<D>(oc, 0, none ? 0.f : 1.f / l, smem + L::q + t * L::tile + quad * (32 * D * 2),
+                         ctl->out + first * ctl->ld_out, ctl->ld_out, b.q_len - first, n[t] == 0);
     }
   }
   __syncwarp();
