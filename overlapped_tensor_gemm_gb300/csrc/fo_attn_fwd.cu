@@ -57,16 +57,38 @@ struct alignas(8) Ctl {
   uint64_t q_full[2], k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
   uint64_t s_full[2], p_full[2], o_done[2], fix, drain;
   uint32_t tmem_base, pad;
-  // the sequence's outputs of this head
-  float* lse;
-  uint16_t* out;
-  int64_t ld_out;
 };
 template <int D>
 constexpr int smem_bytes() {
   return static_cast<int>(Smem<D>::ctl + sizeof(Ctl) + 1024);
 }
 static_assert(smem_bytes<128>() <= 232448, "shared memory of one CTA");
+
+// A warp's 32 output rows times `scale` as bf16 to `row` (null: not stored), each lane its own; zero:
+// nothing was accumulated.  (Turned in shared memory into whole lines first, as the backward does it,
+// the kernel took 403 instead of 395 us at 8192 tokens: the walk over the keys spilled more.)
+__device__ __forceinline__ void store_rows(uint32_t taddr, int n, float scale, uint16_t* row, bool zero) {
+  for (int c = 0; c < n; c += 32) {
+    uint32_t v[32];
+    if (zero) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) v[k] = 0u;
+    } else {
+      tmem_ld32(taddr + c, v);
+      tmem_wait_ld();
+    }
+    if (row) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        st_v4_u32(row + c + 8 * k,
+                  pack_bf16x2(__uint_as_float(v[8 * k + 0]) * scale, __uint_as_float(v[8 * k + 1]) * scale),
+                  pack_bf16x2(__uint_as_float(v[8 * k + 2]) * scale, __uint_as_float(v[8 * k + 3]) * scale),
+                  pack_bf16x2(__uint_as_float(v[8 * k + 4]) * scale, __uint_as_float(v[8 * k + 5]) * scale),
+                  pack_bf16x2(__uint_as_float(v[8 * k + 6]) * scale, __uint_as_float(v[8 * k + 7]) * scale));
+    }
+    __syncwarp();
+  }
+}
 
 template <int D, bool kShort>
 __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_constant__ TrainArgs p) {
@@ -125,11 +147,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
   if (warp == 1) {
     tmem_alloc(&ctl->tmem_base, kTmem);
     tmem_relinquish();
-  }
-  if (warp == 2 && lane == 0) {  // a rank's arguments come late: fetched here, nobody waits for them
-    ctl->lse = p.lse[rk] + h * p.ld_lse[rk] + b.q0;
-    ctl->ld_out = p.ld_o[rk];
-    ctl->out = p.out_o[rk] + b.q0 * ctl->ld_out + h * D;
   }
   tc_fence_before();
   __syncthreads();
@@ -382,11 +399,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
       float lo, hi;
       unpack2(sum, lo, hi);
       const float l = lo + hi;
+      const bool live = query < b.q_len;
+      const int64_t row = b.q0 + query;
       const bool none = l == 0.f;  // no key; a NaN among the row's scores stays one in both outputs
-      if (query < b.q_len) ctl->lse[query] = none ? -INFINITY : fmaf(m_ref, kLn2, logf(l));
-      const int first = q0[t] + quad * 32;  // (every product that reads the tile's queries is done)
-      attn_store_rows<D>(oc, 0, none ? 0.f : 1.f / l, smem + L::q + t * L::tile + quad * (32 * D * 2),
-                         ctl->out + first * ctl->ld_out, ctl->ld_out, b.q_len - first, n[t] == 0);
+      if (live) p.lse[rk][h * p.ld_lse[rk] + row] = none ? -INFINITY : fmaf(m_ref, kLn2, logf(l));
+      store_rows(oc, D, none ? 0.f : 1.f / l, live ? p.out_o[rk] + row * p.ld_o[rk] + h * D : nullptr, n[t] == 0);
     }
   }
   __syncwarp();
