@@ -73,6 +73,15 @@ __device__ __forceinline__ void issue_grad64(uint32_t d_tmem, uint32_t a_tmem, u
   if (fine) issue_grad<D, 64>(d_tmem, a_tmem + 32, b, false);
 }
 
+// Part `split` of a walk: n iterations from i0 on
+__device__ __forceinline__ void part_of(int walk, int split, int splits, int* i0, int* n) {
+  *i0 = 0;
+  *n = walk;
+  if (splits == 1) return;
+  *i0 = static_cast<int>(static_cast<int64_t>(walk) * split / splits);
+  *n = static_cast<int>(static_cast<int64_t>(walk) * (split + 1) / splits) - *i0;
+}
+
 // ---------------------------------------------------------------------------
 // dK / dV: a block of 128 keys of one key/value head; walks the query heads of its group and
 // their blocks of 128 queries.
@@ -111,12 +120,24 @@ constexpr int dkv_smem() {
   return static_cast<int>(DkvSmem<D>::ctl + sizeof(DkvCtl) + 1024);
 }
 
-// Where the walk stands: query head and block of the i-th iteration
+// The walk over the query heads and their blocks
 struct QueryWalk {
   int h0, first, per_head, i0, n;  // first query head, first block, blocks per head, iterations [i0, i0 + n)
-  __device__ void head_block(int i, int* h, int* qb) const {
-    *h = h0 + (i0 + i) / per_head;
-    *qb = first + (i0 + i) % per_head;
+};
+// Where it stands: query head and block of an iteration
+struct QueryAt {
+  int h, qb, end;
+  __device__ __forceinline__ explicit QueryAt(const QueryWalk& w) : h(w.h0), qb(w.first), end(w.first + w.per_head) {
+    if (w.i0 > 0 && w.per_head > 0) {
+      h += w.i0 / w.per_head;
+      qb += w.i0 % w.per_head;
+    }
+  }
+  __device__ __forceinline__ void next(const QueryWalk& w) {
+    if (++qb == end) {
+      qb = w.first;
+      ++h;
+    }
   }
 };
 
@@ -128,11 +149,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   DkvCtl* ctl = reinterpret_cast<DkvCtl*>(smem + L::ctl);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int split = blockIdx.x % p.splits, item = blockIdx.x / p.splits;
-  const int hp = p.kv_heads * p.P, ph = item % hp, rk = ph / p.kv_heads, kvh = ph % p.kv_heads;
+  const int item = p.by_splits.of(blockIdx.x), split = blockIdx.x - item * p.splits;
+  const int e = p.by_k[0].of(item), ph = item - e * p.kv_heads * p.P;
+  const int rk = p.by_k[1].of(ph), kvh = ph - rk * p.kv_heads;
   Block b;
-  if (!block_at(p.blocks, item / hp, &b)) return;
-  const int group = p.heads / p.kv_heads, key0 = b.blk * kBlk;
+  if (!block_at(p.blocks, e, &b)) return;
+  const int group = p.by_k[1].of(p.heads), key0 = b.blk * kBlk;
   QueryWalk w;
   w.h0 = kvh * group;
   w.first = query_begin(p.blocks.causal, key0, b.q_len, b.k_len) / kBlk;
@@ -140,11 +162,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
   if (w.per_head < 0) w.per_head = 0;
   const int walk = group * w.per_head;
   const bool fine = kShort && w.per_head <= kFineWalk;
-  w.i0 = static_cast<int>(static_cast<int64_t>(walk) * split / p.splits);
-  w.n = static_cast<int>(static_cast<int64_t>(walk) * (split + 1) / p.splits) - w.i0;
+  part_of(walk, split, p.splits, &w.i0, &w.n);
 
   if (threadIdx.x == 0) {
+    // the first loads go out before anything else
     mbar_init(&ctl->kv_full, 1);
+    fence_barrier_init();
+    fence_proxy_async_shared();
+    if (w.n > 0) {
+      mbar_arrive_expect_tx(&ctl->kv_full, 2 * L::tile);
+      load_block<D>(&p.maps[p.P + rk], smem + L::k, &ctl->kv_full, kvh * D, b.k0 + key0);
+      load_block<D>(&p.maps[2 * p.P + rk], smem + L::v, &ctl->kv_full, kvh * D, b.k0 + key0);
+    }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&ctl->q_full[s], 1);
       mbar_init(&ctl->do_full[s], 1);
@@ -162,11 +191,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
     mbar_init(&ctl->drain, 1);
     fence_barrier_init();
     fence_proxy_async_shared();
-    if (w.n > 0) {  // the first loads go out while the other warps set up
-      mbar_arrive_expect_tx(&ctl->kv_full, 2 * L::tile);
-      load_block<D>(&p.maps[p.P + rk], smem + L::k, &ctl->kv_full, kvh * D, b.k0 + key0);
-      load_block<D>(&p.maps[2 * p.P + rk], smem + L::v, &ctl->kv_full, kvh * D, b.k0 + key0);
-    }
   }
   if (warp == 1) {
     tmem_alloc(&ctl->tmem_base, kTmem);
@@ -184,11 +208,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
       uint32_t fix_uses = 0;
       int armed = 0;  // iterations whose loads have been issued
       bool ok = true, q_armed = false;
-      for (int i = 0; ok && i < w.n; ++i) {
+      QueryAt at(w);
+      for (int i = 0; ok && i < w.n; ++i, at.next(w)) {
         const int st = i & 1;
         const uint32_t free_parity = ((i >> 1) & 1) ^ 1;
-        int h, qb;
-        w.head_block(i, &h, &qb);
+        const int h = at.h, qb = at.qb;
         const int valid = b.q_len - qb * kBlk;
         q_armed = false;
         ok = attn_wait(&ctl->empty[st], free_parity, p, kSiteEmpty, lane);
@@ -282,10 +306,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
         mbar_wait_drain(&ctl->drain, 0, kAttnDrainNs);
       }
     } else if (warp == 2) {  // ---- row statistics of the queries
-      for (int i = 0; i < w.n; ++i) {
+      QueryAt at(w);
+      for (int i = 0; i < w.n; ++i, at.next(w)) {
         const int st = i & 1;
-        int h, qb;
-        w.head_block(i, &h, &qb);
+        const int h = at.h, qb = at.qb;
         if (!attn_wait(&ctl->st_empty[st], ((i >> 1) & 1) ^ 1, p, kSiteEmpty, lane)) break;
         const float* lse = p.lse[rk] + h * p.ld_lse[rk] + b.q0;
         const float* del = p.delta + (static_cast<int64_t>(rk) * p.heads + h) * p.mq + b.q0;
@@ -309,11 +333,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
     const int off = b.k_len - b.q_len;
     const uint64_t c2 = pack2(p.scale_log2, p.scale_log2);
     bool ok = true;
-    for (int i = 0; i < w.n; ++i) {
+    QueryAt at(w);
+    for (int i = 0; i < w.n; ++i, at.next(w)) {
       const int st = i & 1;
       const uint32_t ph = i & 1;
-      int h, qb;
-      w.head_block(i, &h, &qb);
+      const int qb = at.qb;
       const float* lse = stats + st * 2 * kBlk + hf * 64;
       const float* del = lse + kBlk;
       ok = attn_wait(&ctl->st_full[st], (i >> 1) & 1, p, kSiteFull, lane) &&
@@ -433,28 +457,37 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   DqCtl* ctl = reinterpret_cast<DqCtl*>(smem + L::ctl);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int split = blockIdx.x % p.splits, item = blockIdx.x / p.splits;
-  const int hp = p.heads * p.P, ph = item % hp, rk = ph / p.heads, h = ph % p.heads;
+  const int item = p.by_splits.of(blockIdx.x), split = blockIdx.x - item * p.splits;
+  const int e = p.by_q[0].of(item), ph = item - e * p.heads * p.P;
+  const int rk = p.by_q[1].of(ph), h = ph - rk * p.heads;
   Block b;
-  if (!block_at(p.blocks, item / hp, &b)) return;
-  const int kvh = h / (p.heads / p.kv_heads), query0 = b.blk * kBlk;
+  if (!block_at(p.blocks, e, &b)) return;
+  const int kvh = p.by_group.of(h), query0 = b.blk * kBlk;
   const int q_end = query0 + kBlk < b.q_len ? query0 + kBlk : b.q_len;
   // key blocks [i0, i0 + n) of the walk
   const int walk = (key_end(p.blocks.causal, q_end, b.q_len, b.k_len) + kBlk - 1) / kBlk;
   const bool fine = kShort && walk <= kFineWalk;
-  const int i0 = static_cast<int>(static_cast<int64_t>(walk) * split / p.splits);
-  const int n = static_cast<int>(static_cast<int64_t>(walk) * (split + 1) / p.splits) - i0;
+  int i0, n;
+  part_of(walk, split, p.splits, &i0, &n);
 
   if (threadIdx.x == 0) {
+    // the first loads go out before anything else
     mbar_init(&ctl->q_full, 1);
+    for (int s = 0; s < kVStages; ++s) mbar_init(&ctl->v_full[s], 1);
+    fence_barrier_init();
+    fence_proxy_async_shared();
+    if (n > 0) {
+      mbar_arrive_expect_tx(&ctl->q_full, 2 * L::tile);
+      load_block<D>(&p.maps[rk], smem + L::q, &ctl->q_full, h * D, b.q0 + query0);
+      load_block<D>(&p.maps[3 * p.P + rk], smem + L::d_o, &ctl->q_full, h * D, b.q0 + query0);
+      mbar_arrive_expect_tx(&ctl->v_full[0], L::tile);
+      load_block<D>(&p.maps[2 * p.P + rk], smem + L::v, &ctl->v_full[0], kvh * D, b.k0 + i0 * kBlk);
+    }
     for (int s = 0; s < kKStages; ++s) {
       mbar_init(&ctl->k_full[s], 1);
       mbar_init(&ctl->k_empty[s], 1);
     }
-    for (int s = 0; s < kVStages; ++s) {
-      mbar_init(&ctl->v_full[s], 1);
-      mbar_init(&ctl->v_empty[s], 1);
-    }
+    for (int s = 0; s < kVStages; ++s) mbar_init(&ctl->v_empty[s], 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&ctl->s_full[s], 1);
       mbar_init(&ctl->s_free[s], 1);
@@ -467,13 +500,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
     mbar_init(&ctl->fix, 1);
     fence_barrier_init();
     fence_proxy_async_shared();
-    if (n > 0) {  // the first loads go out while the other warps set up
-      mbar_arrive_expect_tx(&ctl->q_full, 2 * L::tile);
-      load_block<D>(&p.maps[rk], smem + L::q, &ctl->q_full, h * D, b.q0 + query0);
-      load_block<D>(&p.maps[3 * p.P + rk], smem + L::d_o, &ctl->q_full, h * D, b.q0 + query0);
-      mbar_arrive_expect_tx(&ctl->v_full[0], L::tile);
-      load_block<D>(&p.maps[2 * p.P + rk], smem + L::v, &ctl->v_full[0], kvh * D, b.k0 + i0 * kBlk);
-    }
   }
   if (warp == 1) {
     tmem_alloc(&ctl->tmem_base, kTmem);

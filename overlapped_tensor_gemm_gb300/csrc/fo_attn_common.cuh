@@ -53,6 +53,22 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+// Division by a number that the host knows, for 0 <= n < 2^31: with 2^(s-1) < d <= 2^s and
+// mul = floor(2^(31+s) / d) + 1, mul d exceeds 2^(31+s) by at most d <= 2^s, so n mul / 2^(31+s)
+// exceeds n / d by less than 1/d.  (A CTA's place from six divisions took 1000 cycles before its
+// first load.)
+struct FastDiv {
+  uint32_t mul, shift;
+  static FastDiv by(uint32_t d) {
+    uint32_t s = 0;
+    while ((1ull << s) < d) ++s;
+    return FastDiv{static_cast<uint32_t>((1ull << (31 + s)) / d + 1), 31 + s};
+  }
+  __host__ __device__ __forceinline__ int of(int n) const {
+    return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(n)) * mul >> shift);
+  }
+};
+
 constexpr int kBlockInts = 8;        // a table entry: q0, q_len, k0, k_len, block, 3 unused
 
 // One block of a sequence: its query rows q0 .. q0 + q_len and key rows k0 .. k0 + k_len, and
@@ -71,11 +87,12 @@ struct Blocks {           // how a kernel finds its blocks
 // The e-th block; false past the last one.  Blocks with the most work come first: a causal
 // sequence's last queries see the most keys, its first keys are seen by the most queries.
 __device__ __forceinline__ bool block_at(const Blocks& b, int e, Block* out) {
-  if (b.table) {
-    if (e >= b.table[0]) return false;
-    const int32_t* t = b.table + kBlockInts * (1 + e);
-    *out = Block{t[0], t[1], t[2], t[3], t[4]};
-    return true;
+  if (b.table) {  // e is inside the table's memory: entry and count are read at once
+    const int32_t* t = b.table + kBlockInts * (1 + static_cast<int64_t>(e));
+    const int4 w = *reinterpret_cast<const int4*>(t);
+    const int blk = t[4], n = b.table[0];
+    *out = Block{w.x, w.y, w.z, w.w, blk};
+    return e < n;
   }
   if (e >= b.count) return false;
   *out = Block{0, b.mq, 0, b.mk, b.by_keys ? e : b.count - 1 - e};
@@ -113,6 +130,7 @@ struct TrainArgs {
   float* eps;                   // kDeltaMeasure: [splits][P][heads][mq]
   Blocks blocks;
   int32_t P, heads, kv_heads;
+  FastDiv by_q[2], by_k[2], by_group, by_splits;  // heads * P and heads; kv_heads * P and kv_heads
   int32_t mq;
   float scale, scale_log2;      // of the scores; times log2(e)
   uint64_t timeout_ns;

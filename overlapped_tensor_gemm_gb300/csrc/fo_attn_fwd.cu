@@ -98,10 +98,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + L::ctl);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int hp = p.heads * p.P, ph = blockIdx.x % hp, rk = ph / p.heads, h = ph % p.heads;
+  const int e = p.by_q[0].of(blockIdx.x), ph = blockIdx.x - e * p.heads * p.P;
+  const int rk = p.by_q[1].of(ph), h = ph - rk * p.heads;
   Block b;
-  if (!block_at(p.blocks, blockIdx.x / hp, &b)) return;
-  const int kvh = h / (p.heads / p.kv_heads);
+  if (!block_at(p.blocks, e, &b)) return;
+  const int kvh = p.by_group.of(h);
   // first query of each tile and the key blocks it walks
   int q0[2], n[2];
 #pragma unroll
@@ -115,16 +116,27 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
   const bool apart = Cols<D>::apart && !fine;
 
   if (threadIdx.x == 0) {
+    // the first loads go out before anything else
+    mbar_init(&ctl->q_full[0], 1);
+    mbar_init(&ctl->q_full[1], 1);
+    for (int s = 0; s < kKStages; ++s) mbar_init(&ctl->k_full[s], 1);
+    fence_barrier_init();
+    fence_proxy_async_shared();
+    if (nmax > 0) {
+      mbar_arrive_expect_tx(&ctl->k_full[0], L::tile);
+      load_block<D>(&p.maps[p.P + rk], smem + L::k, &ctl->k_full[0], kvh * D, b.k0);
+    }
+    for (int t = 0; t < 2; ++t)
+      if (n[t] > 0) {
+        mbar_arrive_expect_tx(&ctl->q_full[t], L::tile);
+        load_block<D>(&p.maps[rk], smem + L::q + t * L::tile, &ctl->q_full[t], h * D, b.q0 + q0[t]);
+      }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&ctl->q_full[t], 1);
       mbar_init(&ctl->s_full[t], 1);
       mbar_init(&ctl->p_full[t], kTileWarps);
       mbar_init(&ctl->o_done[t], 1);
     }
-    for (int s = 0; s < kKStages; ++s) {
-      mbar_init(&ctl->k_full[s], 1);
-      mbar_init(&ctl->k_empty[s], 1);
-    }
+    for (int s = 0; s < kKStages; ++s) mbar_init(&ctl->k_empty[s], 1);
     for (int s = 0; s < kVStages; ++s) {
       mbar_init(&ctl->v_full[s], 1);
       mbar_init(&ctl->v_empty[s], 1);
@@ -133,16 +145,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     mbar_init(&ctl->drain, 1);
     fence_barrier_init();
     fence_proxy_async_shared();
-    // the first loads go out while the other warps set up
-    for (int t = 0; t < 2; ++t)
-      if (n[t] > 0) {
-        mbar_arrive_expect_tx(&ctl->q_full[t], L::tile);
-        load_block<D>(&p.maps[rk], smem + L::q + t * L::tile, &ctl->q_full[t], h * D, b.q0 + q0[t]);
-      }
-    if (nmax > 0) {
-      mbar_arrive_expect_tx(&ctl->k_full[0], L::tile);
-      load_block<D>(&p.maps[p.P + rk], smem + L::k, &ctl->k_full[0], kvh * D, b.k0);
-    }
   }
   if (warp == 1) {
     tmem_alloc(&ctl->tmem_base, kTmem);

@@ -247,6 +247,11 @@ fo_status fill_args(fo_ctx* ctx, const Call& c, const fo_mat* Q, const fo_mat* K
   a->P = c.P;
   a->heads = c.heads;
   a->kv_heads = c.kv_heads;
+  a->by_q[0] = FastDiv::by(static_cast<uint32_t>(c.heads) * c.P);
+  a->by_q[1] = FastDiv::by(c.heads);
+  a->by_k[0] = FastDiv::by(static_cast<uint32_t>(c.kv_heads) * c.P);
+  a->by_k[1] = FastDiv::by(c.kv_heads);
+  a->by_group = FastDiv::by(c.heads / c.kv_heads);
   a->mq = static_cast<int32_t>(c.mq);
   a->short_walks = c.n > 0 || c.mk <= kFineWalk * kBlk || c.mq <= kFineWalk * kBlk;
   a->scale = c.scale;
@@ -355,6 +360,7 @@ fo_status fo_attn_backward(fo_ctx* ctx, const fo_mat* Q, const fo_mat* K, const 
     const int64_t walk = keys ? (c.mq + kBlk - 1) / kBlk * group : (c.mk + kBlk - 1) / kBlk;
     a.splits = split_of(host_num_sms(ctx), static_cast<int64_t>(a.blocks.count) * (keys ? kv_heads : heads) * P, walk,
                         static_cast<size_t>(P) * rows * cols * 4 * (keys ? 2 : 1));
+    a.by_splits = FastDiv::by(a.splits);
     a.delta_mode = kDeltaCorrect;
     if (a.splits > 1) {
       void* part = nullptr;
