@@ -60,7 +60,7 @@ struct NormArgs {
   int64_t m, total_rows;      // rows per rank, rows of all ranks
   int32_t cols, tpr, gate_mode, stages;
   uint32_t stage_bytes;
-  uint32_t par_off, par_pitch;  // copies of w_post, w_pre and gate in shared memory (pitch 0: none)
+  uint32_t par_off, par_pitch;  // backward: w_pre and gate w_post in shared memory, fp32 (pitch 0: not there)
   int32_t has_y, pre, has_dr;
   float alpha, eps;
   float* part;                // backward: [grid][3][cols] column sums (pre, gate, post)
@@ -72,7 +72,9 @@ typedef void (*NormKernel)(const NormArgs);
 // the kernel for rows of `threads` threads; vec: every matrix is staged and rows are whole groups
 // of 8 columns
 NormKernel norm_fwd_kernel_of(bool r32, bool a32, bool p32, bool vec, int threads);
-NormKernel norm_bwd_kernel_of(bool r32, bool a32, bool p32, bool vec, int threads);
+// (backward) full: every operand is given, the gate as a row, the parameters have room in shared
+// memory, and rows fill their threads (of 512: 16-bit matrices only, others have no such room)
+NormKernel norm_bwd_kernel_of(bool r32, bool a32, bool p32, bool vec, bool full, int threads);
 
 namespace {
 
@@ -201,19 +203,36 @@ template <typename T, bool kVec>
 __device__ __forceinline__ void par8(const void* base, int c, int n, Pair (&v)[4]) {
   load8(static_cast<const T*>(base) + c, kVec ? 8 : n, v);
 }
-// A parameter vector as the backward reads it: its copy in shared memory (slot k) where there is
-// room, else where it lies.  Read from L2 anew for every row, the vectors of a wide row are as
-// many bytes as the row itself.  (The forward, two CTAs of 64 registers per SM, has no registers
-// for it: 233 -> 262 us at 16384 rows of 8192.)  Called by every thread; Walk::start has the barrier behind it.
+// The parameters as the backward reads them: 8 columns of f and, where it is there, times g (null f:
+// ones).  Where there is room (par_pitch) the products lie in shared memory in fp32, slot k: read
+// from L2 and unpacked anew for every row, the vectors of a wide row are as many bytes as the row
+// itself.  (The forward, two CTAs of 64 registers per SM, has no registers for it: 233 -> 262 us at
+// 16384 rows of 8192.)
+template <typename T, bool kVec>
+__device__ __forceinline__ void pars8(const void* f, const void* g, int c, int n, Pair (&v)[4]) {
+  if (f) {
+    par8<T, kVec>(f, c, n, v);
+    if (!g) return;
+    Pair w[4];
+    par8<T, kVec>(g, c, n, w);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = mul2(v[k], w[k]);
+  } else if (g) {
+    par8<T, kVec>(g, c, n, v);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = both(1.f);
+  }
+}
+// Called by every thread; Walk::start has the barrier behind it.
 template <typename T>
-__device__ __forceinline__ const T* place_par(const NormArgs& a, uint8_t* smem, int k, const void* base) {
-  const T* p = static_cast<const T*>(base);
-  if (!p || a.par_pitch == 0) return p;
-  uint8_t* to = smem + a.par_off + k * a.par_pitch;
-  const int n = a.cols * static_cast<int>(sizeof(T)) / 16;  // whole 16-byte vectors: kVec rows
-  for (int i = threadIdx.x; i < n; i += blockDim.x)
-    reinterpret_cast<uint4*>(to)[i] = reinterpret_cast<const uint4*>(p)[i];
-  return reinterpret_cast<const T*>(to);
+__device__ __forceinline__ void place_pars(const NormArgs& a, uint8_t* smem, int k, const void* f, const void* g) {
+  float* to = reinterpret_cast<float*>(smem + a.par_off + k * a.par_pitch);
+  for (int c = threadIdx.x * 8; c < a.cols; c += blockDim.x * 8) {  // kVec: whole groups of 8
+    Pair v[4];
+    pars8<T, true>(f, g, c, 8, v);
+    store8(to + c, 8, v);
+  }
 }
 template <typename T, bool kVec>
 __device__ __forceinline__ void put8(void* const* base, const int64_t* ld, const RowAt& r, int c, int n,

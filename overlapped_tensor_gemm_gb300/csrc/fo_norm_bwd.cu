@@ -4,44 +4,64 @@
 namespace fo {
 namespace {
 
-// T: most threads of a CTA; up to 512 threads share an SM (128 registers each: 48 of them hold
-// the sums over tokens)
-template <typename TR, typename TA, typename TP, bool kVec, int T>
+// T: most threads of a CTA; up to 512 threads share an SM (128 registers each: 32 of them hold
+// the sums over tokens).  One sum s = sum_tokens t u (u = Y / rms(Y), or Y) serves both the gate,
+// dg = w_post s, and the post norm, dw_post = g s; a gate per token enters s itself.
+// kFull: what norm_bwd_kernel_of says, known while compiling.
+template <typename TR, typename TA, typename TP, bool kVec, bool kFull, int T>
 __global__ void __launch_bounds__(T, T <= 512 ? 512 / T : 1) norm_bwd_kernel(const __grid_constant__ NormArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float buf[2 * kSumBuf];
   __shared__ uint64_t bars[kNormMaxStages];
   int turn = 0;
   const int rpc = blockDim.x / a.tpr, t = threadIdx.x % a.tpr, sub = threadIdx.x / a.tpr;
-  const bool has_y = a.has_y, post = a.w_post != nullptr, pre = a.pre;
+  const bool has_y = kFull || a.has_y, post = kFull || a.w_post != nullptr, pre = kFull || a.pre;
+  const bool has_dr = kFull || a.has_dr, token = !kFull && a.gate_mode == kGateToken;
+  const bool placed = kFull || (kVec && a.par_pitch != 0);
   const float inv_cols = 1.f / static_cast<float>(a.cols);
-  Pair acc[3][kC][4];  // sums over this thread's tokens: dw_pre, dgate, dw_post
+  Pair acc[2][kC][4];  // sums over this thread's tokens: dw_pre, s
 #pragma unroll
-  for (int v = 0; v < 3; ++v)
+  for (int v = 0; v < 2; ++v)
 #pragma unroll
     for (int i = 0; i < kC; ++i)
 #pragma unroll
       for (int k = 0; k < 4; ++k) acc[v][i][k] = 0;
-  const TP* w_post = place_par<TP>(a, smem, 0, a.w_post);
-  const TP* w_pre = place_par<TP>(a, smem, 1, a.w_pre);
-  const TP* w_gate = place_par<TP>(a, smem, 2, a.gate);
+  if (placed) {
+    place_pars<TP>(a, smem, 0, a.w_pre, nullptr);
+    place_pars<TP>(a, smem, 1, a.w_post, a.gate);
+  }
+  const float* const par = reinterpret_cast<const float*>(smem + a.par_off);
+  auto w_pre8 = [&](int c, int n, Pair (&v)[4]) {
+    if (placed) {
+      load8(par + c, 8, v);
+    } else {
+      par8<TP, kVec>(a.w_pre, c, n, v);
+    }
+  };
+  auto gw_post8 = [&](int c, int n, Pair (&v)[4]) {  // (the row gate's product with w_post)
+    if (placed) {
+      load8(par + a.par_pitch / 4 + c, 8, v);
+    } else {
+      pars8<TP, kVec>(a.w_post, a.gate, c, n, v);
+    }
+  };
   Walk walk;
   walk.start(a, smem, bars, rpc);
   RowAt at{0, static_cast<int64_t>(blockIdx.x) * rpc + sub};
   for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * rpc; row0 < a.total_rows; row0 += walk.step) {
     const uint8_t* st = walk.next(a, row0);
     if (!st) return;
-    const bool live = row0 + sub < a.total_rows;
+    const bool live = kFull || row0 + sub < a.total_rows;
     if (live) at.wrap(a.m);
     // sums of R'^2, dX w_pre R' and Y^2: everything the two norms need before t is known
     Pair q3[3] = {0, 0, 0};
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
-      const int c = (i * a.tpr + t) * 8, n = live ? a.cols - c : 0;
+      const int c = (i * a.tpr + t) * 8, n = kFull ? 8 : live ? a.cols - c : 0;
       if (n <= 0) continue;
       if (pre) {
         Pair r[4], dx[4], w[4];
-        par8<TP, kVec>(w_pre, c, n, w);
+        w_pre8(c, n, w);
         get8<TR, kVec, kInR>(a, st, at, sub, c, n, r);
         get8<TA, kVec, kInDx>(a, st, at, sub, c, n, dx);
 #pragma unroll
@@ -67,9 +87,9 @@ __global__ void __launch_bounds__(T, T <= 512 ? 512 / T : 1) norm_bwd_kernel(con
     Pair dr[kC][4];
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
-      const int c = (i * a.tpr + t) * 8, n = live ? a.cols - c : 0;
+      const int c = (i * a.tpr + t) * 8, n = kFull ? 8 : live ? a.cols - c : 0;
       if (n <= 0) continue;
-      if (a.has_dr) {
+      if (has_dr) {
         get8<TR, kVec, kInDr>(a, st, at, sub, c, n, dr[i]);
       } else {
 #pragma unroll
@@ -77,7 +97,7 @@ __global__ void __launch_bounds__(T, T <= 512 ? 512 / T : 1) norm_bwd_kernel(con
       }
       if (pre) {
         Pair r[4], dx[4], w[4];
-        par8<TP, kVec>(w_pre, c, n, w);
+        w_pre8(c, n, w);
         get8<TR, kVec, kInR>(a, st, at, sub, c, n, r);
         get8<TA, kVec, kInDx>(a, st, at, sub, c, n, dx);
 #pragma unroll
@@ -96,35 +116,31 @@ __global__ void __launch_bounds__(T, T <= 512 ? 512 / T : 1) norm_bwd_kernel(con
       Pair y[4], w[4];
       get8<TA, kVec, kInY>(a, st, at, sub, c, n, y);
       if (post) {
-        par8<TP, kVec>(w_post, c, n, w);
 #pragma unroll
         for (int k = 0; k < 4; ++k) y[k] = mul2(y[k], inv_y2);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) o[k] = mul2(dr[i][k], mul2(y[k], w[k]));  // t z
-      } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) o[k] = mul2(dr[i][k], y[k]);
       }
-      if (a.gate_mode != kGateNone) {
+      if (token) {
         Pair g[4];
-        if (a.gate_mode == kGateToken) {
-          put8<TP, kVec>(a.dgate, a.ld_dgate, at, c, n, o);
-          get8<TP, kVec, kInGate>(a, st, at, sub, c, n, g);
-        } else {
-          par8<TP, kVec>(w_gate, c, n, g);
+        if (post) {
+          par8<TP, kVec>(a.w_post, c, n, w);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) acc[1][i][k] = fadd2(acc[1][i][k], o[k]);
+          for (int k = 0; k < 4; ++k) o[k] = mul2(dr[i][k], mul2(y[k], w[k]));  // t z
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[k] = mul2(dr[i][k], y[k]);
         }
+        put8<TP, kVec>(a.dgate, a.ld_dgate, at, c, n, o);
+        get8<TP, kVec, kInGate>(a, st, at, sub, c, n, g);
 #pragma unroll
         for (int k = 0; k < 4; ++k) dr[i][k] = mul2(dr[i][k], g[k]);
       }
-      if (post) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          acc[2][i][k] = ffma2(dr[i][k], y[k], acc[2][i][k]);
-          dr[i][k] = mul2(dr[i][k], w[k]);
-          q1 = ffma2(dr[i][k], y[k], q1);
-        }
+      for (int k = 0; k < 4; ++k) acc[1][i][k] = ffma2(dr[i][k], y[k], acc[1][i][k]);
+      gw_post8(c, n, w);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        dr[i][k] = mul2(dr[i][k], w[k]);
+        q1 = ffma2(dr[i][k], y[k], q1);
       }
     }
     if (has_y) {
@@ -136,7 +152,7 @@ __global__ void __launch_bounds__(T, T <= 512 ? 512 / T : 1) norm_bwd_kernel(con
       }
 #pragma unroll
       for (int i = 0; i < kC; ++i) {
-        const int c = (i * a.tpr + t) * 8, n = live ? a.cols - c : 0;
+        const int c = (i * a.tpr + t) * 8, n = kFull ? 8 : live ? a.cols - c : 0;
         if (n <= 0) continue;
         if (post) {
           Pair y[4];
@@ -154,20 +170,31 @@ __global__ void __launch_bounds__(T, T <= 512 ? 512 / T : 1) norm_bwd_kernel(con
   float* part = a.part + static_cast<int64_t>(blockIdx.x) * 3 * a.cols;
   float* sums = reinterpret_cast<float*>(smem);  // [row groups][cols]: the stages are done with
 #pragma unroll
-  for (int v = 0; v < 3; ++v) {
+  for (int v = 0; v < 3; ++v) {  // dw_pre, dgate = w_post s, dw_post = g s
     if (v == 0 ? !pre : v == 1 ? !(has_y && a.gate_mode == kGateRow) : !post) continue;
     float* out = rpc > 1 ? sums + sub * a.cols : part + v * a.cols;
+    const TP* by = static_cast<const TP*>(v == 1 ? a.w_post : v == 2 ? a.gate : nullptr);
     if (rpc > 1) __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kC; ++i)
+    for (int i = 0; i < kC; ++i) {
+      const int c = (i * a.tpr + t) * 8, n = a.cols - c;
+      if (n <= 0) continue;
+      Pair w[4];
+      pars8<TP, false>(by, nullptr, c, n, w);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int c = (i * a.tpr + t) * 8 + 2 * k;
-        float x, y;
-        unpack2(acc[v][i][k], x, y);
-        if (c < a.cols) out[c] = x;
-        if (c + 1 < a.cols) out[c + 1] = y;
+      for (int k = 0; k < 4; ++k) w[k] = mul2(w[k], acc[v == 0 ? 0 : 1][i][k]);
+      if constexpr (kVec) {
+        store8(out + c, 8, w);
+      } else {  // a row of sums starts at any multiple of 4 bytes
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float x, y;
+          unpack2(w[k], x, y);
+          if (2 * k < n) out[c + 2 * k] = x;
+          if (2 * k + 1 < n) out[c + 2 * k + 1] = y;
+        }
       }
+    }
     if (rpc > 1) {
       __syncthreads();
       for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
@@ -179,23 +206,27 @@ __global__ void __launch_bounds__(T, T <= 512 ? 512 / T : 1) norm_bwd_kernel(con
   }
 }
 
-template <bool kVec, int T>
+template <bool kVec, bool kFull, int T>
 NormKernel of(bool r32, bool a32, bool p32) {
+  typedef uint16_t H;
   const int i = (r32 ? 4 : 0) + (a32 ? 2 : 0) + (p32 ? 1 : 0);
   const NormKernel k[8] = {
-      norm_bwd_kernel<uint16_t, uint16_t, uint16_t, kVec, T>, norm_bwd_kernel<uint16_t, uint16_t, float, kVec, T>,
-      norm_bwd_kernel<uint16_t, float, uint16_t, kVec, T>, norm_bwd_kernel<uint16_t, float, float, kVec, T>,
-      norm_bwd_kernel<float, uint16_t, uint16_t, kVec, T>, norm_bwd_kernel<float, uint16_t, float, kVec, T>,
-      norm_bwd_kernel<float, float, uint16_t, kVec, T>, norm_bwd_kernel<float, float, float, kVec, T>};
+      norm_bwd_kernel<H, H, H, kVec, kFull, T>,         norm_bwd_kernel<H, H, float, kVec, kFull, T>,
+      norm_bwd_kernel<H, float, H, kVec, kFull, T>,     norm_bwd_kernel<H, float, float, kVec, kFull, T>,
+      norm_bwd_kernel<float, H, H, kVec, kFull, T>,     norm_bwd_kernel<float, H, float, kVec, kFull, T>,
+      norm_bwd_kernel<float, float, H, kVec, kFull, T>, norm_bwd_kernel<float, float, float, kVec, kFull, T>};
   return k[i];
 }
 
 }  // namespace
 
-NormKernel norm_bwd_kernel_of(bool r32, bool a32, bool p32, bool vec, int threads) {
-  if (!vec) return threads <= 512 ? of<false, 512>(r32, a32, p32) : of<false, 1024>(r32, a32, p32);
-  if (threads <= 256) return of<true, 256>(r32, a32, p32);
-  return threads <= 512 ? of<true, 512>(r32, a32, p32) : of<true, 1024>(r32, a32, p32);
+NormKernel norm_bwd_kernel_of(bool r32, bool a32, bool p32, bool vec, bool full, int threads) {
+  if (full && threads <= 256) return of<true, true, 256>(r32, a32, p32);
+  if (full) return p32 ? norm_bwd_kernel<uint16_t, uint16_t, float, true, true, 512>
+                       : norm_bwd_kernel<uint16_t, uint16_t, uint16_t, true, true, 512>;
+  if (!vec) return threads <= 512 ? of<false, false, 512>(r32, a32, p32) : of<false, false, 1024>(r32, a32, p32);
+  if (threads <= 256) return of<true, false, 256>(r32, a32, p32);
+  return threads <= 512 ? of<true, false, 512>(r32, a32, p32) : of<true, false, 1024>(r32, a32, p32);
 }
 
 }  // namespace fo

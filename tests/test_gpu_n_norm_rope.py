@@ -137,6 +137,16 @@ def test_norm_backward(ctx, case, rest):
             assert torch.equal(v, again[k]), k
 
 
+@pytest.mark.parametrize("case", [
+    (1, 307, 8192, BF, BF, BF, True, "row", True, 1.0), (2, 3, 8192, BF, BF, F32, True, "row", True, 0.5),
+    (2, 12, 512, BF, BF, BF, True, "row", True, 1.0), (1, 40, 1024, F32, F32, F32, True, "row", True, 1.5),
+    (1, 41, 1024, F32, BF, F32, True, "row", True, 1.0), (3, 5, 4096, BF, F32, BF, True, "row", True, 1.0),
+], ids=lambda c: "x".join(str(x).replace("torch.", "") for x in c))
+def test_norm_backward_of_a_whole_block(ctx, case):
+    """Every operand given, rows that fill their threads (and one count of rows that does not)."""
+    test_norm_backward(ctx, case, True)
+
+
 def test_norm_without_a_block_and_in_place(ctx):
     g = torch.Generator().manual_seed(5)
     R, r64 = _randn(g, (37, 320), F32)
