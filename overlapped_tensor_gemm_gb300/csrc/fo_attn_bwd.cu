@@ -26,9 +26,10 @@
 // a select sets to zero; as terms of a sum (Q and dO in dK / dV, K in dQ) they would turn the
 // sum into NaN even with weight 0, so the loader clears them in shared memory.
 //
-// Measured: 16384 tokens, 8 heads on 2, causal 1224 us for both passes (1122 TFLOP/s counting five
-// products, 1570 counting the seven executed); 8192 tokens, 32 heads on 8: 1256 us; head_dim 64,
-// 8192 tokens, 16 heads: 511-522 us.  Bound by a CTA's chain of score product, softmax and gradient
+// Measured: 16384 tokens, 8 heads on 2, causal 1195-1210 us for both passes (1145 TFLOP/s counting
+// five products, 1600 counting the seven executed); 8192 tokens, 32 heads on 8: 1202 us; head_dim
+// 64, 8192 tokens, 16 heads: 484-488 us.  A step of dK / dV takes 2200 cycles, of which its four
+// products are 2048; a CTA spends 4000 cycles before its first step and 4000 after its last.  Bound by a CTA's chain of score product, softmax and gradient
 // product; without its softmax arithmetic a pass is 5% faster, with half its loads not at all.
 #include <cuda_bf16.h>
 

@@ -16,8 +16,8 @@
 // (the sum and the final division use the same reference, so this is exact); the weights, at
 // most 2^8, enter the product with V as bf16: half a step, 2^-9 of a weight's binade, as for any
 // bf16 operand, averaged over the keys.
-// Measured: 8192 tokens, 32 heads on 8, causal 395 us (1392 TFLOP/s of the pairs that attend); 16384
-// tokens, 8 heads on 2: 377 us (1458); head_dim 64, 8192 tokens, 16 heads: 180 us (764).  Bound by
+// Measured: 8192 tokens, 32 heads on 8, causal 391 us (1407 TFLOP/s of the pairs that attend); 16384
+// tokens, 8 heads on 2: 384 us (1431); head_dim 64, 8192 tokens, 16 heads: 178 us (770).  Bound by
 // a tile's chain of scores, softmax and P V; the tensor pipe is active about three quarters of the
 // time at full size.
 #include <cuda_bf16.h>

@@ -50,7 +50,8 @@ struct Launch {
 
 fo_status plan_launch(fo_ctx* ctx, NormArgs* a, bool backward, bool r32, bool a32, bool p32, Launch* l) {
   a->tpr = 32;
-  while (a->tpr * 8 * kC < a->cols) a->tpr *= 2;
+  while (a->tpr < kNormThreads && a->tpr * 8 * kC < a->cols) a->tpr *= 2;
+  if (a->tpr * 8 * kC < a->cols) a->tpr = (a->cols + 32 * 8 * kC - 1) / (32 * 8 * kC) * 32;  // one row per CTA
   l->threads = a->tpr > kNormThreads ? a->tpr : kNormThreads;
   const int rpc = l->threads / a->tpr;
   // matrices that fit two stages are staged, the others are read directly
@@ -85,9 +86,9 @@ fo_status plan_launch(fo_ctx* ctx, NormArgs* a, bool backward, bool r32, bool a3
   l->smem = static_cast<int>(a->par_off + 2 * pitch);
   if (backward && rpc > 1 && l->smem < rpc * a->cols * 4) l->smem = rpc * a->cols * 4;
   // the common form of a whole block has a kernel without the tests that the other forms need
-  const bool full = vec && pitch > 0 && (l->threads <= 256 || (l->threads <= 512 && !r32 && !a32)) && a->has_y && a->pre &&
-                    a->has_dr && a->w_post && a->gate_mode == kGateRow && a->cols == a->tpr * 8 * kC && a->total_rows % rpc == 0;
-  l->kernel = backward ? norm_bwd_kernel_of(r32, a32, p32, vec, full, l->threads)
+  const bool full = vec && l->threads <= 512 && (pitch > 0 || l->threads > 256) && a->has_y && a->pre && a->has_dr &&
+                    a->w_post && a->gate_mode == kGateRow && a->cols == a->tpr * 8 * kC && a->total_rows % rpc == 0;
+  l->kernel = backward ? norm_bwd_kernel_of(r32, a32, p32, vec, full, pitch > 0, l->threads)
                        : norm_fwd_kernel_of(r32, a32, p32, vec, l->threads);
   const int64_t row_groups = (a->total_rows + rpc - 1) / rpc, cap = static_cast<int64_t>(host_num_sms(ctx)) * ctas;
   l->grid = static_cast<int>(row_groups < cap ? row_groups : cap);

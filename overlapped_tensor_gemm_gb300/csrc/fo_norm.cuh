@@ -18,7 +18,7 @@
 // the registers.  All arithmetic is fp32, in packed pairs (two columns per instruction: with one,
 // instruction issue took longer than the copies); each output is rounded once to its type (X
 // from the unrounded R').  Measured, 16384 rows of 8192, all bf16: forward 230 us (4.67 TB/s),
-// backward 402 us (4.0 TB/s, held back by instruction issue and the reductions).
+// backward 287 us (5.6 TB/s).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -72,9 +72,9 @@ typedef void (*NormKernel)(const NormArgs);
 // the kernel for rows of `threads` threads; vec: every matrix is staged and rows are whole groups
 // of 8 columns
 NormKernel norm_fwd_kernel_of(bool r32, bool a32, bool p32, bool vec, int threads);
-// (backward) full: every operand is given, the gate as a row, the parameters have room in shared
-// memory, and rows fill their threads (of 512: 16-bit matrices only, others have no such room)
-NormKernel norm_bwd_kernel_of(bool r32, bool a32, bool p32, bool vec, bool full, int threads);
+// (backward) full: every operand is given, the gate as a row, and rows fill their threads (at most
+// 512); placed: its parameters lie in shared memory (256 threads: always)
+NormKernel norm_bwd_kernel_of(bool r32, bool a32, bool p32, bool vec, bool full, bool placed, int threads);
 
 namespace {
 
@@ -288,7 +288,7 @@ struct Walk {
 constexpr int kSumBuf = 32 * 3;  // one half of row_sum's buffer: 32 warps, at most 3 values
 
 // Sums of N values over the tpr threads of a row; every thread of the CTA takes part.  tpr is
-// 32 or a multiple of it; with more than one warp per row the warps' sums meet in `buf`, of
+// 32 times a power of two, or a multiple of 32 and the CTA's only row; with more than one warp per row the warps' sums meet in `buf`, of
 // which successive calls use alternate halves (so one barrier per call is enough).
 template <int N>
 __device__ __forceinline__ void row_sum(float (&v)[N], int tpr, float* buf, int& turn) {
@@ -304,7 +304,7 @@ __device__ __forceinline__ void row_sum(float (&v)[N], int tpr, float* buf, int&
 #pragma unroll
     for (int k = 0; k < N; ++k) b[k * 32 + warp] = v[k];
   __syncthreads();
-  const int w0 = warp & ~(wpr - 1);  // wpr is a power of two
+  const int w0 = (wpr & (wpr - 1)) == 0 ? warp & ~(wpr - 1) : 0;
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     v[k] = lane < wpr ? b[k * 32 + w0 + lane] : 0.f;
