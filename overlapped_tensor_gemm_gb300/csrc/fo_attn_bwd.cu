@@ -29,8 +29,9 @@
 // Measured: 16384 tokens, 8 heads on 2, causal 1195-1210 us for both passes (1145 TFLOP/s counting
 // five products, 1600 counting the seven executed); 8192 tokens, 32 heads on 8: 1202 us; head_dim
 // 64, 8192 tokens, 16 heads: 484-488 us.  A step of dK / dV takes 2200 cycles, of which its four
-// products are 2048; a CTA spends 4000 cycles before its first step and 4000 after its last.  Bound by a CTA's chain of score product, softmax and gradient
-// product; without its softmax arithmetic a pass is 5% faster, with half its loads not at all.
+// products are 2048; a CTA spends 4000 cycles before its first step and 4000 after its last.  Bound
+// by a CTA's chain of score product, softmax and gradient product; without its softmax arithmetic a
+// pass is 5% faster, with half its loads not at all.
 #include <cuda_bf16.h>
 
 #include "fo_attn_common.cuh"

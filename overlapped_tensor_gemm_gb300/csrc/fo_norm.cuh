@@ -288,8 +288,9 @@ struct Walk {
 constexpr int kSumBuf = 32 * 3;  // one half of row_sum's buffer: 32 warps, at most 3 values
 
 // Sums of N values over the tpr threads of a row; every thread of the CTA takes part.  tpr is
-// 32 times a power of two, or a multiple of 32 and the CTA's only row; with more than one warp per row the warps' sums meet in `buf`, of
-// which successive calls use alternate halves (so one barrier per call is enough).
+// 32 times a power of two, or a multiple of 32 and the CTA's only row; with more than one warp per
+// row the warps' sums meet in `buf`, of which successive calls use alternate halves (so one barrier
+// per call is enough).
 template <int N>
 __device__ __forceinline__ void row_sum(float (&v)[N], int tpr, float* buf, int& turn) {
 #pragma unroll
