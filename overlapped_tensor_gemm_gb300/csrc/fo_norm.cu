@@ -75,21 +75,23 @@ fo_status plan_launch(fo_ctx* ctx, NormArgs* a, bool backward, bool r32, bool a3
   int ctas = backward ? (l->threads < 512 ? 512 / l->threads : 1) : 1024 / l->threads;
   while (ctas > 1 && 2 * static_cast<int>(stage) > kNormSmem / ctas - kNormStatic) --ctas;
   const int room = kNormSmem / ctas - kNormStatic;
-  uint32_t pitch = (static_cast<uint32_t>(a->cols) * 4 + 127) / 128 * 128;
-  if (!backward || !vec || !(a->w_post || a->w_pre || a->gate) ||
-      2 * static_cast<int>(stage) + 2 * static_cast<int>(pitch) > room)
+  // the common form of a whole block has kernels without the tests that the other forms need
+  bool full = vec && l->threads <= 512 && a->has_y && a->pre && (a->has_dr || !backward) && a->w_post &&
+              a->gate_mode == kGateRow && a->cols == a->tpr * 8 * kC && a->total_rows % rpc == 0;
+  const int slots = backward ? 2 : 1;
+  int pitch = (a->cols * 4 + 127) / 128 * 128;
+  if (!vec || !(full || (backward && (a->w_post || a->w_pre || a->gate))) ||
+      2 * static_cast<int>(stage) + slots * pitch > room)
     pitch = 0;
+  if (pitch == 0 && ((backward && l->threads <= 256) || (!r32 && !a32))) full = false;  // (does not happen)
   a->par_pitch = pitch;
-  a->stages = stage ? (room - 2 * static_cast<int>(pitch)) / static_cast<int>(stage) : 2;
+  a->stages = stage ? (room - slots * pitch) / static_cast<int>(stage) : 2;
   if (a->stages > kNormMaxStages) a->stages = kNormMaxStages;
   a->par_off = a->stages * stage;
-  l->smem = static_cast<int>(a->par_off + 2 * pitch);
+  l->smem = static_cast<int>(a->par_off) + slots * pitch;
   if (backward && rpc > 1 && l->smem < rpc * a->cols * 4) l->smem = rpc * a->cols * 4;
-  // the common form of a whole block has a kernel without the tests that the other forms need
-  const bool full = vec && l->threads <= 512 && (pitch > 0 || l->threads > 256) && a->has_y && a->pre && a->has_dr &&
-                    a->w_post && a->gate_mode == kGateRow && a->cols == a->tpr * 8 * kC && a->total_rows % rpc == 0;
   l->kernel = backward ? norm_bwd_kernel_of(r32, a32, p32, vec, full, pitch > 0, l->threads)
-                       : norm_fwd_kernel_of(r32, a32, p32, vec, l->threads);
+                       : norm_fwd_kernel_of(r32, a32, p32, vec, full, pitch > 0, l->threads);
   const int64_t row_groups = (a->total_rows + rpc - 1) / rpc, cap = static_cast<int64_t>(host_num_sms(ctx)) * ctas;
   l->grid = static_cast<int>(row_groups < cap ? row_groups : cap);
   if (l->smem > 44 * 1024 &&

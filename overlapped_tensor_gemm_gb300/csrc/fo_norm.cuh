@@ -60,7 +60,7 @@ struct NormArgs {
   int64_t m, total_rows;      // rows per rank, rows of all ranks
   int32_t cols, tpr, gate_mode, stages;
   uint32_t stage_bytes;
-  uint32_t par_off, par_pitch;  // backward: w_pre and gate w_post in shared memory, fp32 (pitch 0: not there)
+  uint32_t par_off, par_pitch;  // gate w_post (backward: w_pre, then it) in shared memory, fp32 (pitch 0: not)
   int32_t has_y, pre, has_dr;
   float alpha, eps;
   float* part;                // backward: [grid][3][cols] column sums (pre, gate, post)
@@ -71,9 +71,9 @@ struct NormArgs {
 typedef void (*NormKernel)(const NormArgs);
 // the kernel for rows of `threads` threads; vec: every matrix is staged and rows are whole groups
 // of 8 columns
-NormKernel norm_fwd_kernel_of(bool r32, bool a32, bool p32, bool vec, int threads);
-// (backward) full: every operand is given, the gate as a row, and rows fill their threads (at most
-// 512); placed: its parameters lie in shared memory (256 threads: always)
+// full: every operand is given, the gate as a row, and rows fill their threads (at most 512);
+// placed: the parameters lie in shared memory (backward, 256 threads: always)
+NormKernel norm_fwd_kernel_of(bool r32, bool a32, bool p32, bool vec, bool full, bool placed, int threads);
 NormKernel norm_bwd_kernel_of(bool r32, bool a32, bool p32, bool vec, bool full, bool placed, int threads);
 
 namespace {
@@ -203,11 +203,9 @@ template <typename T, bool kVec>
 __device__ __forceinline__ void par8(const void* base, int c, int n, Pair (&v)[4]) {
   load8(static_cast<const T*>(base) + c, kVec ? 8 : n, v);
 }
-// The parameters as the backward reads them: 8 columns of f and, where it is there, times g (null f:
-// ones).  Where there is room (par_pitch) the products lie in shared memory in fp32, slot k: read
-// from L2 and unpacked anew for every row, the vectors of a wide row are as many bytes as the row
-// itself.  (The forward, two CTAs of 64 registers per SM, has no registers for it: 233 -> 262 us at
-// 16384 rows of 8192.)
+// Parameters: 8 columns of f and, where it is there, times g (null f: ones).  Where there is room
+// (par_pitch) the products lie in shared memory in fp32: read from L2 and unpacked anew for every
+// row, the vectors of a wide row are as many bytes as the row itself.
 template <typename T, bool kVec>
 __device__ __forceinline__ void pars8(const void* f, const void* g, int c, int n, Pair (&v)[4]) {
   if (f) {

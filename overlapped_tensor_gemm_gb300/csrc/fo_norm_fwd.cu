@@ -4,23 +4,26 @@
 namespace fo {
 namespace {
 
-// T: most threads of a CTA; 64 registers a thread, so 1024 threads share an SM
-template <typename TR, typename TA, typename TP, bool kVec, int T>
+// T: most threads of a CTA; 64 registers a thread, so 1024 threads share an SM.  kFull, kPlaced:
+// what norm_fwd_kernel_of says, known while compiling.
+template <typename TR, typename TA, typename TP, bool kVec, bool kFull, bool kPlaced, int T>
 __global__ void __launch_bounds__(T, 1024 / T) norm_fwd_kernel(const __grid_constant__ NormArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float buf[2 * kSumBuf];
   __shared__ uint64_t bars[kNormMaxStages];
   int turn = 0;
   const int rpc = blockDim.x / a.tpr, t = threadIdx.x % a.tpr, sub = threadIdx.x / a.tpr;
-  const bool has_y = a.has_y, post = a.w_post != nullptr, pre = a.pre;
+  const bool has_y = kFull || a.has_y, post = kFull || a.w_post != nullptr, pre = kFull || a.pre;
   const float inv_cols = 1.f / static_cast<float>(a.cols);
+  if (kPlaced) place_pars<TP>(a, smem, 0, a.w_post, a.gate);
+  const float* const par = reinterpret_cast<const float*>(smem + a.par_off);
   Walk walk;
   walk.start(a, smem, bars, rpc);
   RowAt at{0, static_cast<int64_t>(blockIdx.x) * rpc + sub};
   for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * rpc; row0 < a.total_rows; row0 += walk.step) {
     const uint8_t* st = walk.next(a, row0);
     if (!st) return;
-    const bool live = row0 + sub < a.total_rows;
+    const bool live = kFull || row0 + sub < a.total_rows;
     if (live) at.wrap(a.m);
     Pair r[kC][4];
     float ss[1];
@@ -29,7 +32,7 @@ __global__ void __launch_bounds__(T, 1024 / T) norm_fwd_kernel(const __grid_cons
       Pair sq = 0;
 #pragma unroll
       for (int i = 0; i < kC; ++i) {
-        const int c = (i * a.tpr + t) * 8, n = live ? a.cols - c : 0;
+        const int c = (i * a.tpr + t) * 8, n = kFull ? 8 : live ? a.cols - c : 0;
         if (n <= 0) continue;
         Pair y[4];
         get8<TA, kVec, kInY>(a, st, at, sub, c, n, y);
@@ -44,25 +47,35 @@ __global__ void __launch_bounds__(T, 1024 / T) norm_fwd_kernel(const __grid_cons
     const Pair inv2 = both(inv), alpha2 = both(a.alpha);
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
-      const int c = (i * a.tpr + t) * 8, n = live ? a.cols - c : 0;
+      const int c = (i * a.tpr + t) * 8, n = kFull ? 8 : live ? a.cols - c : 0;
       if (n <= 0) continue;
       get8<TR, kVec, kInR>(a, st, at, sub, c, n, r[i]);
       if (has_y) {
         Pair y[4], w[4];
         get8<TA, kVec, kInY>(a, st, at, sub, c, n, y);
-        if (post) {
-          par8<TP, kVec>(a.w_post, c, n, w);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) y[k] = mul2(mul2(y[k], inv2), w[k]);
-        }
-        if (a.gate_mode != kGateNone) {
-          if (a.gate_mode == kGateToken) {
-            get8<TP, kVec, kInGate>(a, st, at, sub, c, n, w);
+        if (kFull) {
+          if (kPlaced) {
+            load8(par + c, 8, w);
           } else {
-            par8<TP, kVec>(a.gate, c, n, w);
+            pars8<TP, true>(a.w_post, a.gate, c, n, w);
           }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) y[k] = mul2(y[k], w[k]);
+          for (int k = 0; k < 4; ++k) y[k] = mul2(mul2(y[k], inv2), w[k]);
+        } else {
+          if (post) {
+            par8<TP, kVec>(a.w_post, c, n, w);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] = mul2(mul2(y[k], inv2), w[k]);
+          }
+          if (a.gate_mode != kGateNone) {
+            if (a.gate_mode == kGateToken) {
+              get8<TP, kVec, kInGate>(a, st, at, sub, c, n, w);
+            } else {
+              par8<TP, kVec>(a.gate, c, n, w);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] = mul2(y[k], w[k]);
+          }
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) r[i][k] = ffma2(alpha2, r[i][k], y[k]);
@@ -77,7 +90,7 @@ __global__ void __launch_bounds__(T, 1024 / T) norm_fwd_kernel(const __grid_cons
       const Pair scale = both(rsqrtf(ss[0] * inv_cols + a.eps));
 #pragma unroll
       for (int i = 0; i < kC; ++i) {
-        const int c = (i * a.tpr + t) * 8, n = live ? a.cols - c : 0;
+        const int c = (i * a.tpr + t) * 8, n = kFull ? 8 : live ? a.cols - c : 0;
         if (n <= 0) continue;
         Pair w[4];
         par8<TP, kVec>(a.w_pre, c, n, w);
@@ -90,23 +103,32 @@ __global__ void __launch_bounds__(T, 1024 / T) norm_fwd_kernel(const __grid_cons
   }
 }
 
-template <bool kVec, int T>
+template <bool kVec, bool kFull, bool kPlaced, int T>
 NormKernel of(bool r32, bool a32, bool p32) {
+  typedef uint16_t H;
+  constexpr bool kNarrow = kPlaced || kFull;  // 16-bit matrices always leave room for the parameters
   const int i = (r32 ? 4 : 0) + (a32 ? 2 : 0) + (p32 ? 1 : 0);
-  const NormKernel k[8] = {
-      norm_fwd_kernel<uint16_t, uint16_t, uint16_t, kVec, T>, norm_fwd_kernel<uint16_t, uint16_t, float, kVec, T>,
-      norm_fwd_kernel<uint16_t, float, uint16_t, kVec, T>, norm_fwd_kernel<uint16_t, float, float, kVec, T>,
-      norm_fwd_kernel<float, uint16_t, uint16_t, kVec, T>, norm_fwd_kernel<float, uint16_t, float, kVec, T>,
-      norm_fwd_kernel<float, float, uint16_t, kVec, T>, norm_fwd_kernel<float, float, float, kVec, T>};
+  const NormKernel k[8] = {norm_fwd_kernel<H, H, H, kVec, kFull, kNarrow, T>,
+                           norm_fwd_kernel<H, H, float, kVec, kFull, kNarrow, T>,
+                           norm_fwd_kernel<H, float, H, kVec, kFull, kPlaced, T>,
+                           norm_fwd_kernel<H, float, float, kVec, kFull, kPlaced, T>,
+                           norm_fwd_kernel<float, H, H, kVec, kFull, kPlaced, T>,
+                           norm_fwd_kernel<float, H, float, kVec, kFull, kPlaced, T>,
+                           norm_fwd_kernel<float, float, H, kVec, kFull, kPlaced, T>,
+                           norm_fwd_kernel<float, float, float, kVec, kFull, kPlaced, T>};
   return k[i];
 }
 
 }  // namespace
 
-NormKernel norm_fwd_kernel_of(bool r32, bool a32, bool p32, bool vec, int threads) {
-  if (!vec) return threads <= 512 ? of<false, 512>(r32, a32, p32) : of<false, 1024>(r32, a32, p32);
-  if (threads <= 256) return of<true, 256>(r32, a32, p32);
-  return threads <= 512 ? of<true, 512>(r32, a32, p32) : of<true, 1024>(r32, a32, p32);
+NormKernel norm_fwd_kernel_of(bool r32, bool a32, bool p32, bool vec, bool full, bool placed, int threads) {
+  if (full && threads <= 256)
+    return placed ? of<true, true, true, 256>(r32, a32, p32) : of<true, true, false, 256>(r32, a32, p32);
+  if (full) return placed ? of<true, true, true, 512>(r32, a32, p32) : of<true, true, false, 512>(r32, a32, p32);
+  if (!vec)
+    return threads <= 512 ? of<false, false, false, 512>(r32, a32, p32) : of<false, false, false, 1024>(r32, a32, p32);
+  if (threads <= 256) return of<true, false, false, 256>(r32, a32, p32);
+  return threads <= 512 ? of<true, false, false, 512>(r32, a32, p32) : of<true, false, false, 1024>(r32, a32, p32);
 }
 
 }  // namespace fo
