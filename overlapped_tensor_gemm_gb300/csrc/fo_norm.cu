@@ -76,8 +76,8 @@ fo_status plan_launch(fo_ctx* ctx, NormArgs* a, bool backward, bool r32, bool a3
   while (ctas > 1 && 2 * static_cast<int>(stage) > kNormSmem / ctas - kNormStatic) --ctas;
   const int room = kNormSmem / ctas - kNormStatic;
   // the common form of a whole block has kernels without the tests that the other forms need
-  bool full = vec && l->threads <= 512 && a->has_y && a->pre && (a->has_dr || !backward) && a->w_post &&
-              a->gate_mode == kGateRow && a->cols == a->tpr * 8 * kC && a->total_rows % rpc == 0;
+  bool full = vec && l->threads <= 512 && a->has_y && a->pre && a->cols == a->tpr * 8 * kC && a->total_rows % rpc == 0;
+  full = full && (backward ? a->has_dr && a->gate_mode != kGateToken : a->w_post && a->gate_mode == kGateRow);
   const int slots = backward ? 2 : 1;
   int pitch = (a->cols * 4 + 127) / 128 * 128;
   if (!vec || !(full || (backward && (a->w_post || a->w_pre || a->gate))) ||
@@ -90,7 +90,7 @@ fo_status plan_launch(fo_ctx* ctx, NormArgs* a, bool backward, bool r32, bool a3
   a->par_off = a->stages * stage;
   l->smem = static_cast<int>(a->par_off) + slots * pitch;
   if (backward && rpc > 1 && l->smem < rpc * a->cols * 4) l->smem = rpc * a->cols * 4;
-  l->kernel = backward ? norm_bwd_kernel_of(r32, a32, p32, vec, full, pitch > 0, l->threads)
+  l->kernel = backward ? norm_bwd_kernel_of(r32, a32, p32, vec, full, a->w_post, pitch > 0, l->threads)
                        : norm_fwd_kernel_of(r32, a32, p32, vec, full, pitch > 0, l->threads);
   const int64_t row_groups = (a->total_rows + rpc - 1) / rpc, cap = static_cast<int64_t>(host_num_sms(ctx)) * ctas;
   l->grid = static_cast<int>(row_groups < cap ? row_groups : cap);

@@ -71,10 +71,11 @@ struct NormArgs {
 typedef void (*NormKernel)(const NormArgs);
 // the kernel for rows of `threads` threads; vec: every matrix is staged and rows are whole groups
 // of 8 columns
-// full: every operand is given, the gate as a row, and rows fill their threads (at most 512);
-// placed: the parameters lie in shared memory (backward, 256 threads: always)
+// full: a block's output and a norm behind it (backward: and a gradient of the residual stream)
+// are given, the gate not per token, and rows fill their threads (at most 512); forward: with post
+// norm and gate.  placed: the parameters lie in shared memory (backward, 256 threads: always)
 NormKernel norm_fwd_kernel_of(bool r32, bool a32, bool p32, bool vec, bool full, bool placed, int threads);
-NormKernel norm_bwd_kernel_of(bool r32, bool a32, bool p32, bool vec, bool full, bool placed, int threads);
+NormKernel norm_bwd_kernel_of(bool r32, bool a32, bool p32, bool vec, bool full, bool post, bool placed, int threads);
 
 namespace {
 

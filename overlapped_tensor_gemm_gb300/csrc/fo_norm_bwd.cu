@@ -4,19 +4,23 @@
 namespace fo {
 namespace {
 
+// Full forms have a post norm or not
+enum Form { kAnyForm, kPlainForm, kPostForm };
+
 // T: most threads of a CTA; up to 512 threads share an SM (128 registers each: 32 of them hold
 // the sums over tokens).  One sum s = sum_tokens t u (u = Y / rms(Y), or Y) serves both the gate,
 // dg = w_post s, and the post norm, dw_post = g s; a gate per token enters s itself.
-// kFull, kPlaced: what norm_bwd_kernel_of says, known while compiling (tested for every row they
+// kForm, kPlaced: what norm_bwd_kernel_of says, known while compiling (tested for every row they
 // cost 15%).
-template <typename TR, typename TA, typename TP, bool kVec, bool kFull, bool kPlaced, int T>
+template <typename TR, typename TA, typename TP, bool kVec, Form kForm, bool kPlaced, int T>
 __global__ void __launch_bounds__(T, T <= 512 ? 512 / T : 1) norm_bwd_kernel(const __grid_constant__ NormArgs a) {
+  constexpr bool kFull = kForm != kAnyForm;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float buf[2 * kSumBuf];
   __shared__ uint64_t bars[kNormMaxStages];
   int turn = 0;
   const int rpc = blockDim.x / a.tpr, t = threadIdx.x % a.tpr, sub = threadIdx.x / a.tpr;
-  const bool has_y = kFull || a.has_y, post = kFull || a.w_post != nullptr, pre = kFull || a.pre;
+  const bool has_y = kFull || a.has_y, post = kFull ? kForm == kPostForm : a.w_post != nullptr, pre = kFull || a.pre;
   const bool has_dr = kFull || a.has_dr, token = !kFull && a.gate_mode == kGateToken;
   const bool placed = kPlaced || (kVec && !kFull && a.par_pitch != 0);
   const float inv_cols = 1.f / static_cast<float>(a.cols);
@@ -207,31 +211,38 @@ __global__ void __launch_bounds__(T, T <= 512 ? 512 / T : 1) norm_bwd_kernel(con
   }
 }
 
-template <bool kVec, bool kFull, bool kPlaced, int T>
+template <bool kVec, Form kForm, bool kPlaced, int T>
 NormKernel of(bool r32, bool a32, bool p32) {
   typedef uint16_t H;
-  constexpr bool kNarrow = kPlaced || kFull;  // 16-bit matrices always leave room for the parameters
+  constexpr bool kNarrow = kPlaced || kForm != kAnyForm;  // 16-bit matrices always leave room for the parameters
   const int i = (r32 ? 4 : 0) + (a32 ? 2 : 0) + (p32 ? 1 : 0);
-  const NormKernel k[8] = {norm_bwd_kernel<H, H, H, kVec, kFull, kNarrow, T>,
-                           norm_bwd_kernel<H, H, float, kVec, kFull, kNarrow, T>,
-                           norm_bwd_kernel<H, float, H, kVec, kFull, kPlaced, T>,
-                           norm_bwd_kernel<H, float, float, kVec, kFull, kPlaced, T>,
-                           norm_bwd_kernel<float, H, H, kVec, kFull, kPlaced, T>,
-                           norm_bwd_kernel<float, H, float, kVec, kFull, kPlaced, T>,
-                           norm_bwd_kernel<float, float, H, kVec, kFull, kPlaced, T>,
-                           norm_bwd_kernel<float, float, float, kVec, kFull, kPlaced, T>};
+  const NormKernel k[8] = {norm_bwd_kernel<H, H, H, kVec, kForm, kNarrow, T>,
+                           norm_bwd_kernel<H, H, float, kVec, kForm, kNarrow, T>,
+                           norm_bwd_kernel<H, float, H, kVec, kForm, kPlaced, T>,
+                           norm_bwd_kernel<H, float, float, kVec, kForm, kPlaced, T>,
+                           norm_bwd_kernel<float, H, H, kVec, kForm, kPlaced, T>,
+                           norm_bwd_kernel<float, H, float, kVec, kForm, kPlaced, T>,
+                           norm_bwd_kernel<float, float, H, kVec, kForm, kPlaced, T>,
+                           norm_bwd_kernel<float, float, float, kVec, kForm, kPlaced, T>};
   return k[i];
+}
+
+template <Form kForm>
+NormKernel full_of(bool r32, bool a32, bool p32, bool placed, int threads) {
+  if (threads <= 256) return of<true, kForm, true, 256>(r32, a32, p32);
+  return placed ? of<true, kForm, true, 512>(r32, a32, p32) : of<true, kForm, false, 512>(r32, a32, p32);
 }
 
 }  // namespace
 
-NormKernel norm_bwd_kernel_of(bool r32, bool a32, bool p32, bool vec, bool full, bool placed, int threads) {
-  if (full && threads <= 256) return of<true, true, true, 256>(r32, a32, p32);
-  if (full) return placed ? of<true, true, true, 512>(r32, a32, p32) : of<true, true, false, 512>(r32, a32, p32);
-  if (!vec)
-    return threads <= 512 ? of<false, false, false, 512>(r32, a32, p32) : of<false, false, false, 1024>(r32, a32, p32);
-  if (threads <= 256) return of<true, false, false, 256>(r32, a32, p32);
-  return threads <= 512 ? of<true, false, false, 512>(r32, a32, p32) : of<true, false, false, 1024>(r32, a32, p32);
+NormKernel norm_bwd_kernel_of(bool r32, bool a32, bool p32, bool vec, bool full, bool post, bool placed, int threads) {
+  if (full)
+    return post ? full_of<kPostForm>(r32, a32, p32, placed, threads)
+                : full_of<kPlainForm>(r32, a32, p32, placed, threads);
+  constexpr Form any = kAnyForm;
+  if (!vec) return threads <= 512 ? of<false, any, false, 512>(r32, a32, p32) : of<false, any, false, 1024>(r32, a32, p32);
+  if (threads <= 256) return of<true, any, false, 256>(r32, a32, p32);
+  return threads <= 512 ? of<true, any, false, 512>(r32, a32, p32) : of<true, any, false, 1024>(r32, a32, p32);
 }
 
 }  // namespace fo

@@ -143,7 +143,9 @@ def test_norm_backward(ctx, case, rest):
     (1, 41, 1024, F32, BF, F32, True, "row", True, 1.0), (1, 21, 8192, F32, BF, BF, True, "row", True, 1.0),
     (1, 17, 6144, F32, F32, F32, True, "row", True, 0.5), (2, 9, 5120, BF, BF, BF, True, "row", True, 1.0),
     (1, 11, 5128, BF, BF, BF, True, "row", True, 1.0), (1, 7, 9000, BF, F32, BF, True, "row", True, 1.0),
-    (3, 5, 4096, BF, F32, BF, True, "row", True, 1.0),
+    (3, 5, 4096, BF, F32, BF, True, "row", True, 1.0), (1, 19, 8192, BF, BF, F32, False, None, True, 1.0),
+    (2, 8, 2048, F32, BF, BF, False, "row", True, 0.5), (1, 31, 4096, BF, BF, BF, True, None, True, 1.0),
+    (1, 12, 8192, F32, BF, BF, False, None, True, 1.0),
 ], ids=lambda c: "x".join(str(x).replace("torch.", "") for x in c))
 def test_norm_of_a_whole_block(ctx, case):
     """Every operand given, rows that fill their threads (and one count of rows that does not)."""
