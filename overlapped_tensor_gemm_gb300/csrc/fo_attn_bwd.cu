@@ -96,7 +96,9 @@ __device__ __forceinline__ void part_of(int walk, int split, int splits, int* i0
 // ---------------------------------------------------------------------------
 constexpr uint32_t kColP = 128, kColV = 256;
 // head_dim 64 leaves room for a second S^T: scores then never wait for the weights they would
-// overwrite
+// overwrite.  The weights may then be written for block i + 1 before the issuing warp has looked
+// at those of block i: a parity tells a phase from the next one, not from the one after, so each
+// buffer's weights have a barrier of their own.
 template <int D>
 struct DkvCols {
   static constexpr int bufs = D == 64 ? 2 : 1;
@@ -114,7 +116,7 @@ struct DkvSmem {
 };
 struct alignas(8) DkvCtl {
   uint64_t kv_full, q_full[2], do_full[2], empty[2], st_full[2], st_empty[2];
-  uint64_t s_full[2], p_full, dp_full, ds_full, acc_full, fix, drain;
+  uint64_t s_full[2], p_full[2], dp_full, ds_full, acc_full, fix, drain;
   uint32_t tmem_base, pad;
 };
 template <int D>
@@ -185,7 +187,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
     }
     mbar_init(&ctl->s_full[0], 1);
     mbar_init(&ctl->s_full[1], 1);
-    mbar_init(&ctl->p_full, kWorkWarps);
+    mbar_init(&ctl->p_full[0], kWorkWarps);
+    mbar_init(&ctl->p_full[1], kWorkWarps);
     mbar_init(&ctl->dp_full, 1);
     mbar_init(&ctl->ds_full, kWorkWarps);
     mbar_init(&ctl->acc_full, 1);
@@ -269,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
           }
           __syncwarp();
         }
-        ok = attn_wait(&ctl->p_full, ph, p, kSiteTmemFull, lane);
+        ok = attn_wait(&ctl->p_full[Cols::buf(i)], Cols::parity(i), p, kSiteTmemFull, lane);
         if (!ok) break;
         tc_fence_after();
         if (elect_lane())
@@ -367,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
           if (k < from) s[k] = 0.f;
       }
       store64_bf16(lanes + Cols::s(i) + hf * 64, s, fine);
-      attn_publish(&ctl->p_full, lane);
+      attn_publish(&ctl->p_full[Cols::buf(i)], lane);
       ok = attn_wait(&ctl->dp_full, ph, p, kSiteTmemFull, lane);
       if (!ok) break;
       tc_fence_after();
@@ -431,8 +434,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
 // 2^-11 (2-norm over its rows of the error's sum against that of |dS|, the latter from a quarter
 // of the keys) walks its keys a second time.  For spread attention these are the first one or two blocks of a sequence.
 //
-// Two warps issue, one the scores and one
-// the gradient: what an issuing warp spends on barriers passes while the pipe runs the other's.
+// Two warps issue, one the scores and one the gradient: what an issuing warp spends on barriers
+// passes while the pipe runs the other's.  dS_{i+1} waits for the scores alone and may be written
+// before the gradient's warp has looked at dS_i, so each score buffer's dS has its own barrier.
 // ---------------------------------------------------------------------------
 constexpr uint32_t kColDp = 256, kColDq = 384;
 constexpr int kKStages = 3, kVStages = 2;
@@ -444,7 +448,7 @@ struct DqSmem {
 };
 struct alignas(8) DqCtl {
   uint64_t q_full, k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
-  uint64_t s_full[2], s_free[2], dp_full, dp_free, ds_full, acc_full, fix, drain[2];
+  uint64_t s_full[2], s_free[2], dp_full, dp_free, ds_full[2], acc_full, fix, drain[2];
   uint32_t tmem_base, pad;
 };
 template <int D>
@@ -493,11 +497,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
     for (int s = 0; s < 2; ++s) {
       mbar_init(&ctl->s_full[s], 1);
       mbar_init(&ctl->s_free[s], 1);
+      mbar_init(&ctl->ds_full[s], kWorkWarps);
       mbar_init(&ctl->drain[s], 1);
     }
     mbar_init(&ctl->dp_full, 1);
     mbar_init(&ctl->dp_free, kWorkWarps);
-    mbar_init(&ctl->ds_full, kWorkWarps);
     mbar_init(&ctl->acc_full, 1);
     mbar_init(&ctl->fix, 1);
     fence_barrier_init();
@@ -600,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
         }
       } else if (warp == 2 && n > 0) {  // ---- MMAs of dQ
         for (int i = g0; ok && i < g0 + n; ++i) {
-          ok = attn_wait(&ctl->ds_full, i & 1, p, kSiteTmemFull, lane);
+          ok = attn_wait(&ctl->ds_full[i & 1], (i >> 1) & 1, p, kSiteTmemFull, lane);
           if (!ok) break;
           tc_fence_after();
           if (elect_lane()) {
@@ -659,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
           if (k % 8 == 0) size += fabsf(s[k]) + fabsf(s[k + 1]);  // a quarter of the keys stands for all
         }
         store64_bf16(buf, s, fine);
-        attn_publish(&ctl->ds_full, lane);
+        attn_publish(&ctl->ds_full[g & 1], lane);
       }
       float x, y;
       unpack2(err2, x, y);
