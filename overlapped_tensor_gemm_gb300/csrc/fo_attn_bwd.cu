@@ -228,9 +228,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
         q_armed = true;
         ok = load_summed<D>(p, &p.maps[3 * p.P + rk], smem + L::d_o + st * L::tile, &ctl->do_full[st], &ctl->fix,
                             fix_uses, h * D, b.q0 + qb * kBlk, valid, lane);
-        if (ok) armed = i + 1;
+        if (!ok) break;
+        armed = i + 1;
+        q_armed = false;
       }
-      if (!ok && lane == 0) {  // wait for the copies in flight
+      if (lane == 0 && w.n > 0) {  // no copy in flight when the CTA leaves, whichever warp gave up
         mbar_wait_drain(&ctl->kv_full, 0, kAttnDrainNs);
         for (int i = armed - 2 < 0 ? 0 : armed - 2; i < armed + (q_armed ? 1 : 0); ++i) {
           mbar_wait_drain(&ctl->q_full[i & 1], (i >> 1) & 1, kAttnDrainNs);
@@ -306,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
         }
       }
       if (ok && elect_lane()) umma_commit(&ctl->acc_full);
-      if (!ok && issued && elect_lane()) {
+      if (issued && elect_lane()) {  // and no MMA
         umma_commit(&ctl->drain);
         mbar_wait_drain(&ctl->drain, 0, kAttnDrainNs);
       }
@@ -557,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
           }
           v_armed = g + 1;
         }
-        if (!ok && lane == 0) {  // wait for the copies in flight
+        if (lane == 0 && n > 0) {  // no copy in flight after the round, whichever warp gave up
           mbar_wait_drain(&ctl->q_full, 0, kAttnDrainNs);
           for (int i = k_armed - kKStages < 0 ? 0 : k_armed - kKStages; i < k_armed; ++i)
             mbar_wait_drain(&ctl->k_full[i % kKStages], (i / kKStages) & 1, kAttnDrainNs);
@@ -598,10 +600,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
             vph ^= 1;
           }
         }
-        if (!ok && issued && elect_lane()) {
-          umma_commit(&ctl->drain[0]);
-          mbar_wait_drain(&ctl->drain[0], 0, kAttnDrainNs);
-        }
       } else if (warp == 2 && n > 0) {  // ---- MMAs of dQ
         for (int i = g0; ok && i < g0 + n; ++i) {
           ok = attn_wait(&ctl->ds_full[i & 1], (i >> 1) & 1, p, kSiteTmemFull, lane);
@@ -615,10 +613,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
           __syncwarp();
           issued = true;
           if (++ks == kKStages) ks = 0;
-        }
-        if (!ok && issued && elect_lane()) {
-          umma_commit(&ctl->drain[1]);
-          mbar_wait_drain(&ctl->drain[1], 0, kAttnDrainNs);
         }
       }
     } else {  // ---- P and dS
@@ -709,6 +703,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
     fence_proxy_async_shared();
   }
   if (n > 0 && warp == 2 && ok && elect_lane()) umma_commit(&ctl->acc_full);
+  if ((warp == 1 || warp == 2) && issued && elect_lane()) {  // no MMA in flight when the CTA leaves
+    umma_commit(&ctl->drain[warp - 1]);
+    mbar_wait_drain(&ctl->drain[warp - 1], 0, kAttnDrainNs);
+  }
   if (warp >= 4) {
     if (ok && n > 0) ok = attn_wait(&ctl->acc_full, 0, p, kSiteDrain, lane);
     if (ok && p.delta_mode != kDeltaMeasure) {

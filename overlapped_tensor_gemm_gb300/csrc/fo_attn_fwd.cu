@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                           kvh * D, b.k0 + j * kBlk, b.k_len - j * kBlk, lane);
       if (ok) v_armed = j + 1;
     }
-    if (!ok && lane == 0) {  // wait for the copies in flight
+    if (lane == 0) {  // no copy in flight when the CTA leaves, whichever warp gave up
       for (int t = 0; t < 2; ++t)
         if (n[t] > 0) mbar_wait_drain(&ctl->q_full[t], 0, kAttnDrainNs);
       for (int j = k_armed - kKStages < 0 ? 0 : k_armed - kKStages; j < k_armed; ++j)
@@ -253,11 +253,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
       vs = vn;
       if (vs == 0) vph ^= 1;
     }
-    if (!ok && issued) {
-      if (elect_lane()) {
-        umma_commit(&ctl->drain);
-        mbar_wait_drain(&ctl->drain, 0, kAttnDrainNs);
-      }
+    if (issued && elect_lane()) {  // and no MMA
+      umma_commit(&ctl->drain);
+      mbar_wait_drain(&ctl->drain, 0, kAttnDrainNs);
     }
   } else if (warp >= 4) {  // ---- softmax
     const int t = (warp - 4) >> 2, quad = warp & 3;
