@@ -239,6 +239,18 @@ __device__ __forceinline__ void put8(void* const* base, const int64_t* ld, const
   store8(static_cast<T*>(base[r.rk]) + r.row * ld[r.rk] + c, kVec ? 8 : n, v);
 }
 
+// Waits, with a limit each, for the stages that are armed while the group at row0 is due in stage s
+static __device__ __noinline__ void drain_stages(const NormArgs& a, uint64_t* bars, int s, uint32_t phase,
+                                                 int64_t row0, int64_t step) {
+  for (int k = 0; k < a.stages && row0 < a.total_rows; ++k, row0 += step) {
+    mbar_wait_drain(&bars[s], phase, kAttnDrainNs);
+    if (++s == a.stages) {
+      s = 0;
+      phase ^= 1u;
+    }
+  }
+}
+
 // The CTA's walk over its row groups: start() arms the first stages; next() waits for the group's
 // stage and refills the one before it, which every thread has left.
 struct Walk {
@@ -272,9 +284,13 @@ struct Walk {
       fill_stage(a, base + ahead * a.stage_bytes, &bars[ahead], row, rpc, threadIdx.x);
     }
     // the copies depend on nothing but memory: an abort that an earlier call left behind does not
-    // end this wait, so that no CTA exits with copies in flight
-    const bool ok = mbar_try_wait(&bars[s], phase) || mbar_wait_drain(&bars[s], phase, a.timeout_ns);
-    if (!ok) raise_error(a.ctrl, FO_ERR_TIMEOUT, kSiteFull, blockIdx.x);
+    // end this wait.  A warp gives up as a whole, and then waits for every copy in flight.
+    const bool ok = __all_sync(0xffffffffu, mbar_try_wait(&bars[s], phase) ||
+                                                mbar_wait_drain(&bars[s], phase, a.timeout_ns));
+    if (!ok) {
+      raise_error(a.ctrl, FO_ERR_TIMEOUT, kSiteFull, blockIdx.x);
+      drain_stages(a, bars, s, phase, row0, step);
+    }
     const uint8_t* here = base + s * a.stage_bytes;
     if (++s == a.stages) {
       s = 0;
