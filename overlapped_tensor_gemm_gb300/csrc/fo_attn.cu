@@ -106,6 +106,7 @@ struct alignas(8) AttnCtl {
   uint64_t p_full[kSBufs];          // per score buffer: every softmax warp has written its P
   uint64_t s_free[kSBufs];          // per score buffer: the P.V that read its P has completed
   uint64_t drain, drain_pv;         // failure paths: the score / P.V issuer's MMAs have completed
+  uint64_t drain_end[2];            // likewise, where a warp behind them gave up
   uint64_t item_full[kItemSlots];   // the slot holds the CTA's next claimed item
   uint64_t item_empty[kItemSlots];  // every reader has taken the slot's item
   int32_t item[kItemSlots];
@@ -338,11 +339,10 @@ __device__ void attn_producer(const AttnParams& p, uint8_t* smem, AttnCtl* ctl, 
       if (bi.i < 0) ok = false;
     }
   }
-  if (!ok) {
-    if (q_armed) mbar_wait_drain(&ctl->q_full, (q_uses - 1) & 1u, kDrainNs);
-    for (int i = 0; i < nst; ++i)
-      if ((armed >> i) & 1u) mbar_wait_drain(&full[i], (armed_ph >> i) & 1u, kDrainNs);
-  }
+  // leave no TMA write in flight into this CTA's shared memory, whichever warp gave up
+  if (q_armed) mbar_wait_drain(&ctl->q_full, (q_uses - 1) & 1u, kDrainNs);
+  for (int i = 0; i < nst; ++i)
+    if ((armed >> i) & 1u) mbar_wait_drain(&full[i], (armed_ph >> i) & 1u, kDrainNs);
 }
 
 // S = Q K^T for one 128-key block: Q and K from the two 64-dim swizzle halves of their
@@ -661,6 +661,8 @@ __global__ void __maxnreg__(136) attn_kernel(const __grid_constant__ AttnParams 
       for (int b = 0; b < 2; ++b) mbar_init(&ctl->xchg[q][b], 2);
     mbar_init(&ctl->drain, 1);
     mbar_init(&ctl->drain_pv, 1);
+    mbar_init(&ctl->drain_end[0], 1);
+    mbar_init(&ctl->drain_end[1], 1);
     for (int s = 0; s < kItemSlots; ++s) {
       mbar_init(&ctl->item_full[s], 1);
       mbar_init(&ctl->item_empty[s], kItemReaders);
@@ -694,7 +696,16 @@ __global__ void __maxnreg__(136) attn_kernel(const __grid_constant__ AttnParams 
     attn_softmax(p, smem, ctl, tmem_base, warp, lane);
   }
   tc_fence_before();
-  __syncthreads();
+  // A warp behind the issuers gave up: their MMAs may still be in flight, and TMEM is released.  (An
+  // issuer that waits for its own at its end, whatever happened, took 10% more time per launch.)
+  if (__syncthreads_or(aborted(p.ctrl))) {
+    if ((warp == 1 || warp == 11) && lane == 0) {
+      uint64_t* const drain = warp == 1 ? &ctl->drain_end[0] : &ctl->drain_end[1];
+      umma_commit(drain);
+      mbar_wait_drain(drain, 0, kDrainNs);
+    }
+    __syncthreads();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, kTmemCols);

@@ -157,11 +157,9 @@ __device__ void producer_loop(const GemmParams& p, uint8_t* tiles, SmemCtl* ctl)
       }
     }
   }
-  if (!ok) {
-    // leave no TMA write in flight into this CTA's shared memory
-    for (int s = 0; s < kStages; ++s)
-      if ((armed >> s) & 1u) mbar_wait_drain(&ctl->full[s], (armed_phase >> s) & 1u, kDrainNs);
-  }
+  // leave no TMA write in flight into this CTA's shared memory, whichever warp gave up
+  for (int s = 0; s < kStages; ++s)
+    if ((armed >> s) & 1u) mbar_wait_drain(&ctl->full[s], (armed_phase >> s) & 1u, kDrainNs);
 }
 
 // The operand orientation is a template argument: the instruction descriptor stays a
@@ -217,8 +215,8 @@ __device__ void mma_loop(const GemmParams& p, uint8_t* tiles, SmemCtl* ctl, uint
     acc ^= 1;
     if (acc == 0) acc_phase ^= 1u;
   }
-  if (!ok && issued) {
-    // wait for every issued MMA before TMEM is released
+  if (issued) {
+    // wait for every issued MMA before TMEM is released, whichever warp gave up
     umma_commit(&ctl->drain);
     mbar_wait_drain(&ctl->drain, 0, kDrainNs);
   }

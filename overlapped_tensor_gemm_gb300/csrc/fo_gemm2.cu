@@ -217,15 +217,16 @@ __device__ void pair_producer(const GemmParams& p, uint8_t* tiles, PairCtl* ctl,
       }
     }
   }
+  // leave no TMA write in flight into either CTA's shared memory, whichever warp gave up: the
+  // leader's barriers count both CTAs' loads, and no CTA leaves before its peer
+  if (cta == 0) {
+    for (int s = 0; s < kPairStages; ++s)
+      if ((armed >> s) & 1u) mbar_wait_drain(&ctl->full[s], (armed_phase >> s) & 1u, kPDrainNs);
+  }
   if (!ok) {
-    if (cta == 0) {
-      for (int s = 0; s < kPairStages; ++s)
-        if ((armed >> s) & 1u) mbar_wait_drain(&ctl->full[s], (armed_phase >> s) & 1u, kPDrainNs);
-    } else {
-      // this CTA's loads complete on the leader's barriers: give them time to land
-      const uint64_t t0 = global_timer_ns();
-      while (global_timer_ns() - t0 < 50000ull) __nanosleep(1000);
-    }
+    // the peer may have loaded for a stage that the leader has not armed: give that time to land
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 50000ull) __nanosleep(1000);
   }
 }
 
@@ -287,7 +288,7 @@ __device__ void pair_mma(const GemmParams& p, uint8_t* tiles, PairCtl* ctl, uint
     acc ^= 1;
     if (acc == 0) acc_phase ^= 1u;
   }
-  if (!ok && issued) {
+  if (issued) {  // no MMA in flight when TMEM is released, whichever warp gave up
     umma_commit_pair(&ctl->drain);
     mbar_wait_drain(&ctl->drain, 0, kPDrainNs);
   }
