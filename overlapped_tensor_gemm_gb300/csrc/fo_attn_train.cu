@@ -169,7 +169,7 @@ struct Cut {
   bool by_keys;
 };
 
-// Blocks for up to two cuts of the call's rows; packed sequences: launches the table kernel
+// Blocks for up to two cuts of the call's rows; packed sequences: their workspace, then the table kernel
 fo_status make_blocks(fo_ctx* ctx, const Call& c, const Cut* cuts, int n, cudaStream_t s, Blocks* out) {
   PlanArgs p;
   std::memset(&p, 0, sizeof(p));
@@ -343,31 +343,38 @@ fo_status fo_attn_backward(fo_ctx* ctx, const fo_mat* Q, const fo_mat* K, const 
   fill(dQ, P, a.dq, a.ld_dq);
   fill(dK, P, a.dk, a.ld_dk);
   fill(dV, P, a.dv, a.ld_dv);
-  void* delta = nullptr;
+  // dQ (which corrects delta), then dK / dV: a walk that would leave SMs idle is cut into parts
+  const int group = heads / kv_heads;
+  int splits[2];
+  size_t part_bytes = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    const bool keys = pass == 1;
+    const int64_t rows = keys ? c.mk : c.mq, items = block_bound(c, rows, kBlk) * (keys ? kv_heads : heads) * P;
+    const int64_t walk = keys ? (c.mq + kBlk - 1) / kBlk * group : (c.mk + kBlk - 1) / kBlk;
+    const size_t bytes = static_cast<size_t>(P) * rows * (keys ? 2 * kc : qc) * 4;  // of one part's sums
+    splits[pass] = items > 0 ? split_of(host_num_sms(ctx), items, walk, bytes) : 1;
+    if (splits[pass] > 1 && splits[pass] * bytes > part_bytes) part_bytes = splits[pass] * bytes;
+  }
+  // Every workspace before the first launch: a call that cannot have them enqueues nothing.
+  void *delta = nullptr, *part = nullptr;
   FO_TRY_HOST(host_buffer_kept(ctx, kSlotAttnStats, static_cast<size_t>(P) * heads * c.mq * 4, s, &delta));
+  if (part_bytes > 0) FO_TRY_HOST(host_buffer_kept(ctx, kSlotAttnPart, part_bytes, s, &part));
   a.delta = static_cast<float*>(delta);
   const Cut cuts[2] = {{kBlk, true}, {kBlk, false}};
   Blocks b[2];
   FO_TRY_HOST(make_blocks(ctx, c, cuts, 2, s, b));
   cudaError_t e = attn_delta_launch(a, head_dim, s);
-  // dQ (which corrects delta), then dK / dV: a walk that would leave SMs idle is cut into parts
-  const int group = heads / kv_heads;
   for (int pass = 0; pass < 2 && e == cudaSuccess; ++pass) {
     const bool keys = pass == 1;
     const int64_t rows = keys ? c.mk : c.mq, cols = keys ? kc : qc;
     a.blocks = b[keys ? 0 : 1];
     if (a.blocks.count == 0) continue;
-    const int64_t walk = keys ? (c.mq + kBlk - 1) / kBlk * group : (c.mk + kBlk - 1) / kBlk;
-    a.splits = split_of(host_num_sms(ctx), static_cast<int64_t>(a.blocks.count) * (keys ? kv_heads : heads) * P, walk,
-                        static_cast<size_t>(P) * rows * cols * 4 * (keys ? 2 : 1));
+    a.splits = splits[pass];
     a.by_splits = FastDiv::by(a.splits);
     a.delta_mode = kDeltaCorrect;
     if (a.splits > 1) {
-      void* part = nullptr;
-      const int64_t floats = static_cast<int64_t>(a.splits) * P * rows * cols;
-      FO_TRY_HOST(host_buffer_kept(ctx, kSlotAttnPart, static_cast<size_t>(floats) * 4 * (keys ? 2 : 1), s, &part));
       a.part = static_cast<float*>(part);
-      a.part_v = a.part + floats;
+      a.part_v = a.part + static_cast<int64_t>(a.splits) * P * rows * cols;
       if (!keys) {  // no CTA sees a whole row: measure delta's error, then compute with the corrected one
         a.eps = a.part;  // (smaller than the partial sums, which come after it)
         a.delta_mode = kDeltaMeasure;

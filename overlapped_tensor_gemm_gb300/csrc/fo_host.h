@@ -17,7 +17,7 @@ enum HostSlot : int {
   kSlotNormPart = 2,    // norm backward: partial column sums
   kSlotAttnTable = 3,   // attention forward / backward: block tables of packed sequences
   kSlotAttnStats = 4,   // attention backward: per-row statistics
-  kSlotAttnPart = 5,    // attention backward: partial dK / dV
+  kSlotAttnPart = 5,    // attention backward: partial sums (dK and dV; dQ and delta's error)
 };
 fo_status host_buffer(fo_ctx* ctx, int slot, size_t bytes, void** out);  // attention workspace slots 0..7
 fo_status host_flags(fo_ctx* ctx, uint32_t** out);                       // arrival flags [rank*P + slice]
