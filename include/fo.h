@@ -386,8 +386,12 @@ FO_API fo_status fo_attn_forward(fo_ctx* ctx, const fo_mat* Q, const fo_mat* K, 
  *   share a key/value head.
  * dQ as Q, dK and dV as K (bf16, rounded once; P and dS enter their products as bf16).  The
  * outputs must not overlap the inputs.  No atomics: the same inputs give the same bits.
- * Workspace: 4 bytes per query row and head and, where few blocks of rows would leave SMs idle,
- * fp32 partial sums (at most 256 MiB); it is kept for later calls. */
+ * Workspace: 4 bytes per query row and head; where few blocks of rows would leave SMs idle, fp32
+ * partial sums (at most 256 MiB); for packed sequences (forward too) 32 bytes per block of 128
+ * rows.  Each is kept for later calls, grows to at least twice its size, and keeps its outgrown
+ * buffers until the context is destroyed (a captured launch may still use them): less than four
+ * times the largest call's need in all, while memory for it is there.  All of it is had before the first launch: a call refused
+ * for want of it (FO_ERR_OOM; FO_ERR_UNSUPPORTED in a stream capture) enqueues nothing. */
 FO_API fo_status fo_attn_backward(fo_ctx* ctx, const fo_mat* Q, const fo_mat* K, const fo_mat* V,
                                   const fo_mat* O, const fo_mat* LSE, const fo_mat* dO, int P, int heads,
                                   int kv_heads, int head_dim, const fo_attn_mask* mask, const fo_mat* dQ,

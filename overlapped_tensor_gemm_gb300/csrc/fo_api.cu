@@ -2042,10 +2042,18 @@ fo_status host_buffer_kept(fo_ctx* ctx, int slot, size_t bytes, cudaStream_t s, 
     if (cap != cudaStreamCaptureStatusNone)
       return fail(FO_ERR_UNSUPPORTED, "the workspace has to grow, which a stream capture cannot hold: make the call "
                   "once before capturing it");
-    const size_t want = bytes > 2 * b.bytes ? bytes : 2 * b.bytes;  // outgrown buffers sum to less than the last
-    const size_t rounded = (want + (2u << 20) - 1) & ~static_cast<size_t>((2u << 20) - 1);
+    ctx->retired.reserve(ctx->retired.size() + 1);  // (what may throw, first)
+    auto round = [](size_t n) { return (n + (2u << 20) - 1) & ~static_cast<size_t>((2u << 20) - 1); };
+    // twice as much, so that outgrown buffers sum to less than the last; where that fails, what is needed
+    size_t rounded = round(bytes > 2 * b.bytes ? bytes : 2 * b.bytes);
     void* p = nullptr;
-    if (cudaMalloc(&p, rounded) != cudaSuccess) {
+    cudaError_t e = cudaMalloc(&p, rounded);
+    if (e != cudaSuccess && rounded > round(bytes)) {
+      cudaGetLastError();
+      rounded = round(bytes);
+      e = cudaMalloc(&p, rounded);
+    }
+    if (e != cudaSuccess) {
       cudaGetLastError();
       return fail(FO_ERR_OOM, "workspace growth to %zu bytes failed", rounded);
     }
