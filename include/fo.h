@@ -474,7 +474,8 @@ typedef enum {
   FO_ROPE_INTERLEAVED = 1  /* pair i = dimensions 2i and 2i + 1                    */
 } fo_rope_layout;
 
-/* Fills *table (host only, no GPU).  scaling null: unscaled.  rot_dim even, 2 .. 512. */
+/* Fills *table (host only, no GPU): turns rounded to 2^-64.  scaling null: unscaled.  rot_dim
+ * even, 2 .. 512. */
 FO_API fo_status fo_rope_table_init(fo_rope_table* table, int rot_dim, double base,
                                     const fo_rope_scaling* scaling);
 
@@ -482,8 +483,9 @@ FO_API fo_status fo_rope_table_init(fo_rope_table* table, int rot_dim, double ba
  * instance the query and key columns of a QKV matrix), bf16 or fp32, Y[r] alike.  Of each
  * head the first table->rot_dim dimensions turn, the others are copied.  Row i of rank r is at
  * position positions[r][i] (device int32), or, with positions null, at
- * start + r*rank_stride + i.  fp32 arithmetic, angles exact to 2^-33 of a turn at any
- * position, one rounding.  Y may be X (in place; the same view); no other overlap. */
+ * start + r*rank_stride + i.  fp32 arithmetic, one rounding; angles within 2^-26 of a turn (their
+ * rounding to fp32) and |position| 2^-65 (the table's).  Y may be X (in place; the same view); no
+ * other overlap. */
 FO_API fo_status fo_rope(fo_ctx* ctx, const fo_mat* X, int P, const fo_rope_table* table, int head_dim,
                          int layout, const int32_t* const* positions, int64_t start, int64_t rank_stride,
                          const fo_mat* Y, void* stream);

@@ -6,9 +6,10 @@
 // Bound by HBM: the matrix is read and written once.  A CTA takes a few token rows, computes
 // their cos / sin once into shared memory (they serve every head), then walks the heads with
 // 16-byte accesses.  Angles: a frequency is a fraction of a turn per position, held as a 64-bit
-// fixed-point number; position * fraction wraps modulo one turn by integer overflow, so the
-// angle is as exact at position 2^31 as at 0 (a product in fp32 would be off by 0.1 rad at
-// position 2^20).  Measured: 16384 tokens of 40 heads of 128, bf16: 57 us (5.85 TB/s, 86% of a copy).
+// fixed-point number; position * fraction wraps modulo one turn by integer overflow.  The fraction
+// is rounded to 2^-64, so the angle is off by position * 2^-65 of a turn (2^-34 at position 2^31)
+// and by its rounding to fp32 for the sine and cosine, at most 2^-26 of a turn at any position (a
+// product in fp32 would be off by 0.1 rad at position 2^20).  Measured: 16384 tokens of 40 heads of 128, bf16: 57 us (5.85 TB/s, 86% of a copy).
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -264,7 +265,67 @@ fo_status rope_run(fo_ctx* ctx, const fo_mat* X, int P, const fo_rope_table* tab
   return e == cudaSuccess ? FO_OK : host_fail(FO_ERR_CUDA, cudaGetErrorString(e));
 }
 
-constexpr double kTwoPi = 6.283185307179586476925286766559;
+// Numbers of about 100 bits as the sum of two doubles, |lo| at most half a step of hi: a frequency
+// in double alone would be off by 2^-55 of a turn per position.  Sums and products are those of
+// error-free transformations (Dekker, Knuth); every function below is host code.
+struct Wide {
+  double hi, lo;
+};
+Wide sum_of(double a, double b) {  // exact
+  const double s = a + b, t = s - a;
+  return Wide{s, (a - (s - t)) + (b - t)};
+}
+Wide product_of(double a, double b) {  // exact
+  const double p = a * b;
+  return Wide{p, std::fma(a, b, -p)};
+}
+Wide operator+(const Wide& a, const Wide& b) {
+  const Wide s = sum_of(a.hi, b.hi), t = sum_of(a.lo, b.lo), u = sum_of(s.hi, s.lo + t.hi);
+  return sum_of(u.hi, u.lo + t.lo);
+}
+Wide operator-(const Wide& a, const Wide& b) { return a + Wide{-b.hi, -b.lo}; }
+Wide operator*(const Wide& a, const Wide& b) {
+  const Wide p = product_of(a.hi, b.hi);
+  return sum_of(p.hi, p.lo + (a.hi * b.lo + a.lo * b.hi));
+}
+Wide operator/(const Wide& a, const Wide& b) {
+  const double q = a.hi / b.hi;
+  const Wide r = a - b * Wide{q, 0.0};
+  const double q2 = r.hi / b.hi;
+  const Wide r2 = r - b * Wide{q2, 0.0};
+  return sum_of(q, q2) + Wide{r2.hi / b.hi, 0.0};
+}
+// exp(x) = exp(x / 4096)^4096, |x| < 1000: 18 terms of the series leave less than 2^-90
+Wide exp_of(const Wide& x) {
+  const Wide r = {std::ldexp(x.hi, -12), std::ldexp(x.lo, -12)};
+  Wide e = {1.0, 0.0};
+  for (int k = 18; k > 0; --k) e = Wide{1.0, 0.0} + r * e / Wide{static_cast<double>(k), 0.0};
+  for (int k = 0; k < 12; ++k) e = e * e;
+  return e;
+}
+// ln(x), x from 1/2 to 2: one Newton step on exp(y) = x from the double
+Wide near_log(double x) {
+  const Wide y = {std::log(x), 0.0};
+  return y + (Wide{x, 0.0} * exp_of(Wide{0.0, 0.0} - y) - Wide{1.0, 0.0});
+}
+Wide log_of(double x) {
+  int e = 0;
+  const double m = std::frexp(x, &e);
+  return near_log(m) + Wide{static_cast<double>(e), 0.0} * near_log(2.0);
+}
+constexpr Wide kTwoPi = {6.283185307179586, 2.4492935982947064e-16};
+
+// x modulo 1, times 2^64, rounded
+uint64_t fixed_of(Wide x) {
+  x = sum_of(x.hi - std::floor(x.hi), x.lo);
+  const double scaled = std::ldexp(x.hi, 64), whole = std::floor(scaled);
+  const int64_t rest = std::llrint((scaled - whole) + std::ldexp(x.lo, 64));
+  // (just below a whole turn hi may be 1, just above one the sum may be negative: both wrap)
+  const uint64_t w = whole >= 18446744073709551616.0 ? 0u
+                     : whole < 0.0                   ? 0u - static_cast<uint64_t>(-whole)
+                                                     : static_cast<uint64_t>(whole);
+  return w + static_cast<uint64_t>(rest);
+}
 
 }  // namespace
 }  // namespace fo
@@ -299,29 +360,30 @@ fo_status fo_rope_table_init(fo_rope_table* table, int rot_dim, double base, con
   if (kind == FO_ROPE_RAMPED) {
     amplitude = factor > 1.0 ? 0.1 * std::log(factor) + 1.0 : 1.0;
     // index of the pair that makes `turns` turns over original_length positions
-    auto pair_of = [&](double turns) { return rot_dim * std::log(length / (kTwoPi * turns)) / (2.0 * std::log(base)); };
+    auto pair_of = [&](double turns) {
+      return rot_dim * std::log(length / (kTwoPi.hi * turns)) / (2.0 * std::log(base));
+    };
     ramp0 = std::floor(pair_of(hi));
     ramp1 = std::ceil(pair_of(lo));
     if (ramp0 < 0.0) ramp0 = 0.0;
     if (ramp1 > rot_dim - 1.0) ramp1 = rot_dim - 1.0;
   }
-  for (int i = 0; i < rot_dim / 2; ++i) {
-    double f = std::pow(base, -2.0 * i / rot_dim);
-    double keep = 0.0;  // share of the unscaled frequency
+  const Wide zero = {0.0, 0.0}, one = {1.0, 0.0}, per_turn = one / kTwoPi, per_factor = one / Wide{factor, 0.0};
+  const Wide ratio = exp_of(Wide{-2.0, 0.0} / Wide{static_cast<double>(rot_dim), 0.0} * log_of(base));
+  Wide f = one;
+  for (int i = 0; i < rot_dim / 2; ++i, f = f * ratio) {
+    Wide keep = zero;  // share of the unscaled frequency
     if (kind == FO_ROPE_UNSCALED) {
-      keep = 1.0;
+      keep = one;
     } else if (kind == FO_ROPE_BANDED) {
-      keep = (length * f / kTwoPi - lo) / (hi - lo);
+      keep = (Wide{length, 0.0} * f * per_turn - Wide{lo, 0.0}) / sum_of(hi, -lo);
     } else if (kind == FO_ROPE_RAMPED) {
       const double width = ramp1 - ramp0;
-      keep = 1.0 - (i - ramp0) / (width > 0.001 ? width : 0.001);
+      keep = one - Wide{i - ramp0, 0.0} / Wide{width > 0.001 ? width : 0.001, 0.0};
     }
-    keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
-    f = (1.0 - keep) * f / factor + keep * f;
-    double turn = f / kTwoPi;
-    turn -= std::floor(turn);
-    const double fixed = std::ldexp(turn, 64);
-    table->turns[i] = fixed >= 18446744073709549568.0 ? 0ull : static_cast<uint64_t>(fixed);
+    if (keep.hi < 0.0) keep = zero;
+    if (keep.hi > 1.0 || (keep.hi == 1.0 && keep.lo > 0.0)) keep = one;
+    table->turns[i] = fixed_of(((one - keep) * f * per_factor + keep * f) * per_turn);
   }
   table->rot_dim = rot_dim;
   table->amplitude = static_cast<float>(amplitude);
