@@ -11,11 +11,13 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
 #include <map>
+#include <mutex>
 #include <string>
 #include <vector>
 
@@ -67,8 +69,10 @@ struct DriverFns {
 
 const DriverFns* driver() {
   static DriverFns fns;
-  static bool loaded = false;
-  if (!loaded) {
+  static std::atomic<bool> loaded{false};  // contexts of several host threads may come here at once
+  static std::mutex loading;
+  if (!loaded.load(std::memory_order_acquire)) {
+    const std::lock_guard<std::mutex> lock(loading);
     cudaDriverEntryPointQueryResult q;
     cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", reinterpret_cast<void**>(&fns.encode_tiled), 12000,
                                      cudaEnableDefault, &q);
@@ -78,9 +82,10 @@ const DriverFns* driver() {
                                      cudaEnableDefault, &q);
     cudaGetDriverEntryPointByVersion("cuGetErrorString", reinterpret_cast<void**>(&fns.get_error_string), 12000,
                                      cudaEnableDefault, &q);
-    loaded = fns.encode_tiled && fns.write_value32 && fns.wait_value32 && fns.get_error_string;
+    loaded.store(fns.encode_tiled && fns.write_value32 && fns.wait_value32 && fns.get_error_string,
+                 std::memory_order_release);
   }
-  return loaded ? &fns : nullptr;
+  return loaded.load(std::memory_order_acquire) ? &fns : nullptr;
 }
 
 #define FO_CU(expr)                                                       \

@@ -40,6 +40,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstring>
 
@@ -786,9 +787,9 @@ fo_status attn_run(fo_ctx* ctx, const fo_mat* Q, const fo_mat* K, const fo_mat* 
   auto k_slot = [&](int r, int s) { return krecv + (static_cast<int64_t>(r) * M + s * m) * HD * 2; };
   auto vt_slot = [&](int r, int s) { return vtb + (static_cast<int64_t>(r) * P + s) * HD * m * 2; };
 
-  static bool configured = false;
-  static int reserve_sms = 0;
-  if (!configured) {
+  static std::atomic<int> reserved{-1};  // -1: not configured yet (by any host thread)
+  int reserve_sms = reserved.load();
+  if (reserve_sms < 0) {
     if (cudaFuncSetAttribute(attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttnSmem) != cudaSuccess)
       return host_fail(FO_ERR_CUDA, "attention kernel configuration failed");
     // Register headroom per SM sub-partition (16K registers, up to 3 of the 10 warps):
@@ -799,7 +800,7 @@ fo_status attn_run(fo_ctx* ctx, const fo_mat* Q, const fo_mat* K, const fo_mat* 
     const int regs = (fa.numRegs + 7) / 8 * 8;
     const int warps_per_quarter = (kAttnThreads / 32 + 3) / 4;
     reserve_sms = warps_per_quarter * 32 * regs > 16384 - 3072 ? 8 : 0;
-    configured = true;
+    reserved.store(reserve_sms);
   }
   AttnParams p;
   std::memset(&p, 0, sizeof(p));

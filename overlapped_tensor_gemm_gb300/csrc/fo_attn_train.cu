@@ -11,6 +11,7 @@
 // reads the offsets on the device, checks them and writes a table of blocks, longest first.
 #include <cuda_bf16.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstring>
 
@@ -261,8 +262,8 @@ fo_status fill_args(fo_ctx* ctx, const Call& c, const fo_mat* Q, const fo_mat* K
   if (opts) o = *opts;
   a->timeout_ns = host_timeout_ns(o);
   a->ctrl = host_ctrl(ctx);
-  constexpr int kDevices = 64;  // kernel attributes are a device's own
-  static bool done[kDevices] = {};
+  constexpr int kDevices = 64;  // kernel attributes are a device's own; host threads may come here at once
+  static std::atomic<bool> done[kDevices];
   const int device = host_device(ctx);
   if (device >= kDevices || !done[device]) {
     cudaError_t e = attn_fwd_configure();

@@ -3,6 +3,8 @@
 // the SM count by the caller's launch helper.
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "fo_internal.h"
 
 namespace fo {
@@ -73,12 +75,14 @@ __global__ void fill_u32_kernel(uint32_t* flags, int64_t n, uint32_t value) {
 }
 
 int sm_count() {
-  static int n = 0;
+  static std::atomic<int> known{0};
+  int n = known.load();
   if (n == 0) {
     int dev = 0;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
     if (n <= 0) n = 1;
+    known.store(n);
   }
   return n;
 }

@@ -81,3 +81,40 @@ def test_limits_of_a_microsecond(ctx, shape, d):
             for a, b in zip(want, got):
                 assert all(torch.equal(x.nan_to_num(7.0), y.nan_to_num(7.0)) for x, y in zip(a, b))
     _check(ctx, pb)
+
+
+def test_contexts_of_several_threads_at_once():
+    """A host thread may own a context: the first calls of four of them at the same time, each right."""
+    import threading
+
+    import overlapped_tensor_gemm_gb300 as fo
+    pbs = [Problem(1, 4, 2, 64 if i % 2 else 128, [(400 + 37 * i,) * 2, (90, 90)], True, 90 + i) for i in range(4)]
+    outs, wrong = [None] * 4, []
+    torch.cuda.synchronize()
+    start = threading.Barrier(4)
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()), fo.Context(0) as c:
+                start.wait()
+                for _ in range(5):
+                    outs[i] = _step(c, pbs[i])
+                torch.cuda.current_stream().synchronize()
+                c.poll()
+        except BaseException as e:  # noqa: BLE001
+            wrong.append(e)
+            start.abort()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong
+    with fo.Context(0) as c:
+        for pb, got in zip(pbs, outs):
+            want = _step(c, pb)
+            torch.cuda.synchronize()
+            c.poll()
+            for a, b in zip(want, got):
+                assert all(torch.equal(x.nan_to_num(7.0), y.nan_to_num(7.0)) for x, y in zip(a, b))
