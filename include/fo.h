@@ -351,9 +351,9 @@ FO_API fo_status fo_gemm_rs_noalloc(const fo_mat* X, const fo_mat* W_row, int P,
  * num_seqs > 0: packed sequences.  q_offsets (device, num_seqs + 1 int32): sequence s holds
  * the query rows q_offsets[s] .. q_offsets[s+1]; k_offsets likewise for the key rows (null:
  * q_offsets, K then has as many rows as Q).  Sequences may be empty.  Rows in front of the
- * first and behind the last sequence are neither read nor written, whatever they hold.  The
- * offsets are read on the device: values that decrease or lie outside [0, rows] end the call
- * with FO_ERR_RANGE from fo_ctx_poll and nothing is computed. */
+ * first and behind the last sequence may be read, but have no effect, whatever they hold, and
+ * are not written.  The offsets are read on the device: values that decrease or lie outside
+ * [0, rows] end the call with FO_ERR_RANGE from fo_ctx_poll and nothing is computed. */
 typedef struct {
   int32_t causal;
   int32_t num_seqs;           /* 0: one sequence of all rows */
@@ -379,6 +379,9 @@ FO_API fo_status fo_attn_forward(fo_ctx* ctx, const fo_mat* Q, const fo_mat* K, 
                                  const fo_mat* O, const fo_mat* LSE, const fo_opts* opts, void* stream);
 
 /* Backward of fo_attn_forward from its inputs, its outputs O and LSE and the gradient dO.
+ * O and LSE have to be those of the same queries, keys and mask: delta is driven to the sum over
+ * the keys that the call has, so statistics of a longer range of keys with one slice of them (a
+ * ring over the context) give another gradient than that slice's share.
  * The probabilities are recomputed, never stored:
  *   P = exp(S - LSE), delta_i = sum_j P_ij (dO V^T)_ij (= sum_d dO_id O_id; taken from the
  *   given O, whose rounding is then corrected), dS = P (dO V^T - delta),
@@ -388,10 +391,11 @@ FO_API fo_status fo_attn_forward(fo_ctx* ctx, const fo_mat* Q, const fo_mat* K, 
  * outputs must not overlap the inputs.  No atomics: the same inputs give the same bits.
  * Workspace: 4 bytes per query row and head; where few blocks of rows would leave SMs idle, fp32
  * partial sums (at most 256 MiB); for packed sequences (forward too) 32 bytes per block of 128
- * rows.  Each is kept for later calls, grows to at least twice its size, and keeps its outgrown
- * buffers until the context is destroyed (a captured launch may still use them): less than four
- * times the largest call's need in all, while memory for it is there.  All of it is had before the first launch: a call refused
- * for want of it (FO_ERR_OOM; FO_ERR_UNSUPPORTED in a stream capture) enqueues nothing. */
+ * rows and per sequence.  Each is kept for later calls, grows to at least twice its size, and
+ * keeps its outgrown buffers until the context is destroyed (a captured launch may still use
+ * them): less than four times the largest call's need in all, while memory for it is there.  All
+ * of it is had before the first launch: a call refused for want of it (FO_ERR_OOM;
+ * FO_ERR_UNSUPPORTED in a stream capture) enqueues nothing. */
 FO_API fo_status fo_attn_backward(fo_ctx* ctx, const fo_mat* Q, const fo_mat* K, const fo_mat* V,
                                   const fo_mat* O, const fo_mat* LSE, const fo_mat* dO, int P, int heads,
                                   int kv_heads, int head_dim, const fo_attn_mask* mask, const fo_mat* dQ,
