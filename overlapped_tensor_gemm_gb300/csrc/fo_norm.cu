@@ -298,10 +298,14 @@ fo_status fo_norm_residual_backward(fo_ctx* ctx, const fo_mat* R_out, const fo_m
   Launch l;
   FO_TRY_HOST(plan_launch(ctx, &a, true, c.tr == FO_F32, c.ta == FO_F32, c.tp == FO_F32, &l));
   const int grid = l.grid;
-  void* part = nullptr;
-  const size_t part_bytes = static_cast<size_t>(host_num_sms(ctx)) * 2 * 3 * c.cols * 4;  // two CTAs per SM at most
-  FO_TRY_HOST(host_buffer_kept(ctx, kSlotNormPart, part_bytes, s, &part));
-  a.part = static_cast<float*>(part);
+  const fo_mat* outs[3] = {grads->w_pre, token ? nullptr : grads->gate, grads->w_post};
+  const bool any = outs[0] || outs[1] || outs[2];  // sums over tokens
+  if (any) {
+    void* part = nullptr;
+    const size_t part_bytes = static_cast<size_t>(host_num_sms(ctx)) * 2 * 3 * c.cols * 4;  // two CTAs per SM at most
+    FO_TRY_HOST(host_buffer_kept(ctx, kSlotNormPart, part_bytes, s, &part));
+    a.part = static_cast<float*>(part);
+  }
   if (grid > 0) {
     l.kernel<<<grid, l.threads, l.smem, s>>>(a);
     const cudaError_t e = cudaGetLastError();
@@ -312,13 +316,10 @@ fo_status fo_norm_residual_backward(fo_ctx* ctx, const fo_mat* R_out, const fo_m
   cs.part = a.part;
   cs.cols = a.cols;
   cs.rows = grid;
-  const fo_mat* outs[3] = {grads->w_pre, token ? nullptr : grads->gate, grads->w_post};
-  bool any = false;
   for (int v = 0; v < 3; ++v)
     if (outs[v]) {
       cs.out[v] = outs[v]->ptr;
       cs.f32[v] = outs[v]->dtype == FO_F32;
-      any = true;
     }
   if (any) {
     col_sum_kernel<<<dim3((a.cols + 31) / 32, 3), dim3(32, 32), 0, s>>>(cs);

@@ -1,4 +1,5 @@
-"""Workspaces of the training operators: a call that cannot have its own enqueues nothing."""
+"""Workspaces of the training operators: a call that cannot have its own enqueues nothing, one that needs none asks for
+none."""
 import pytest
 import torch
 
@@ -46,3 +47,23 @@ def test_a_capture_that_lacks_a_later_workspace_holds_nothing(packed):
         c.poll()
         for a, b in zip(want, (dQ, dK, dV)):
             assert torch.equal(a, b[0])
+
+
+def test_a_norm_without_vector_gradients_needs_no_workspace():
+    """Residual and a gate per token, no norm: nothing is summed over tokens, so the first call can be captured."""
+    import overlapped_tensor_gemm_gb300 as fo
+    g = torch.Generator(device="cuda").manual_seed(7)
+    R, Y, gate, dR_out = (torch.randn((50, 64), generator=g, device="cuda").to(torch.bfloat16) for _ in range(4))
+    dR, dY, dgate = (torch.zeros_like(R) for _ in range(3))
+    with fo.Context(0) as c:
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            c.norm_residual_backward([R], [Y], None, [dR_out], [dR], [dY], gate=[gate], dgate=[dgate])
+        graph.replay()
+        torch.cuda.synchronize()
+        c.poll()
+    assert torch.equal(dR, dR_out)
+    # one fp32 product each, rounded to bf16
+    assert torch.equal(dY, (dR_out.float() * gate.float()).to(torch.bfloat16))
+    assert torch.equal(dgate, (dR_out.float() * Y.float()).to(torch.bfloat16))
