@@ -83,7 +83,10 @@ fo_status plan_launch(fo_ctx* ctx, NormArgs* a, bool backward, bool r32, bool a3
   if (!vec || !(full || (backward && (a->w_post || a->w_pre || a->gate))) ||
       2 * static_cast<int>(stage) + slots * pitch > room)
     pitch = 0;
-  if (pitch == 0 && ((backward && l->threads <= 256) || (!r32 && !a32))) full = false;  // (does not happen)
+  // its backward kernels for 256 threads, and all of them for 16-bit matrices, have the parameters
+  // placed (a backward with an fp32 stream and 2048 or 4096 columns, where two stages leave no room
+  // for them beside a second CTA, runs the general kernel)
+  if (pitch == 0 && ((backward && l->threads <= 256) || (!r32 && !a32))) full = false;
   a->par_pitch = pitch;
   a->stages = stage ? (room - slots * pitch) / static_cast<int>(stage) : 2;
   if (a->stages > kNormMaxStages) a->stages = kNormMaxStages;
