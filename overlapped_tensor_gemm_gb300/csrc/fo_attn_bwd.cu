@@ -9,7 +9,7 @@
 // Seven products instead of the five of a single pass, but each gradient is summed in TMEM by
 // the one CTA that owns it: no atomics, no fp32 gradient in memory, the same bits every time.
 // A single pass would add dQ's 128 x 128 fp32 block to memory once per pair of blocks: 64 KiB
-// through shared memory twice, about as long as the two products it saves.
+// through shared memory twice, by estimate about as long as the two products it saves (not built).
 //
 // The pass over the queries computes S and dP transposed (keys on the TMEM lanes), so that P^T
 // and dS^T, written as bf16 over the scores they came from, are the A operands of the products
@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
 // 2^-11 (2-norm over its rows of the error's sum against that of |dS|) walks its keys a second
 // time.  For spread attention these are the first one or two blocks of a sequence; where a few keys
 // hold most of a row's weight, |dS| is small beside delta's error and most blocks do (8192 tokens,
-// 32 heads, scores of standard deviation 4 and 8: 1800 us backward instead of 1200).  Instantiations
+// 32 heads, scores of standard deviation 4 and 8: 1730-1810 us backward instead of 1200).  Instantiations
 // with kShort sum |dS| over every key.  The others take a quarter of them for all (every key: 3% more
 // time at 8192 tokens): keys 4 and 5 of each 8, so that where the first keys hold much of dS it is
 // estimated low and the block walks again; two keys of opposite dS that hold all of it, both among

@@ -19,7 +19,8 @@
 // Measured: 8192 tokens, 32 heads on 8, causal 391 us (1407 TFLOP/s of the pairs that attend); 16384
 // tokens, 8 heads on 2: 384 us (1431); head_dim 64, 8192 tokens, 16 heads: 178 us (770).  Bound by
 // a tile's chain of scores, softmax and P V; the tensor pipe is active about three quarters of the
-// time at full size.
+// time at full size.  These are scores of standard deviation 1; with 4 and 8, where maxima rise by
+// more than 2^8 late in a row and their blocks are computed again, 8192 tokens take 570 and 618 us.
 #include <cuda_bf16.h>
 
 #include "fo_attn_common.cuh"
