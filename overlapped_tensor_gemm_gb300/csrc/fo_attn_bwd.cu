@@ -436,11 +436,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
 // 2^-11 (2-norm over its rows of the error's sum against that of |dS|) walks its keys a second
 // time.  For spread attention these are the first one or two blocks of a sequence; where a few keys
 // hold most of a row's weight, |dS| is small beside delta's error and most blocks do (8192 tokens,
-// 32 heads, scores of standard deviation 4 and 8: 1730-1810 us backward instead of 1200).  Instantiations
-// with kShort sum |dS| over every key.  The others take a quarter of them for all (every key: 3% more
-// time at 8192 tokens): keys 4 and 5 of each 8, so that where the first keys hold much of dS it is
-// estimated low and the block walks again; two keys of opposite dS that hold all of it, both among
-// the sampled, would let through four times as much.
+// 32 heads, scores of standard deviation 4 and 8: 1730-1810 us backward instead of 1200).
+// Instantiations with kShort sum |dS| over every key.  The others take a quarter of them for all
+// (every key: 3% more time at 8192 tokens): keys 4 and 5 of each 8, so that where the first keys
+// hold much of dS it is estimated low and the block walks again; two keys of opposite dS that hold
+// all of it, both among the sampled, would let through four times as much.
 //
 // Two warps issue, one the scores and one the gradient: what an issuing warp spends on barriers
 // passes while the pipe runs the other's.  dS_{i+1} waits for the scores alone and may be written

@@ -9,7 +9,8 @@
 // fixed-point number; position * fraction wraps modulo one turn by integer overflow.  The fraction
 // is rounded to 2^-64, so the angle is off by position * 2^-65 of a turn (2^-34 at position 2^31)
 // and by its rounding to fp32 for the sine and cosine, at most 2^-26 of a turn at any position (a
-// product in fp32 would be off by 0.1 rad at position 2^20).  Measured: 16384 tokens of 40 heads of 128, bf16: 57 us (5.85 TB/s, 86% of a copy).
+// product in fp32 would be off by 0.1 rad at position 2^20).  Measured: 16384 tokens of 40 heads of
+// 128, bf16: 57 us (5.85 TB/s, 86% of a copy).
 #include <cuda_bf16.h>
 
 #include <cmath>
