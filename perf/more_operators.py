@@ -342,6 +342,16 @@ def _gradient(s, z, log_total, counted, dlogp, dentropy=None):
     return d.reshape(-1, p, c).permute(1, 0, 2).to(DTYPES[case["grad"]])
 
 
+def _pair_loss(case, gap):
+    """Loss of each pair by its gap, and its derivative."""
+    beta, x = case["beta"], case["beta"] * gap
+    if case["loss"] == "sigmoid":
+        return (-x).clamp(min=0) + (-x.abs()).exp().log1p(), -beta / (1 + x.exp())
+    if case["loss"] == "squared":
+        return (gap - 0.5 / beta).square(), 2 * (gap - 0.5 / beta)
+    return (1 - x).clamp(min=0), torch.where(x < 1, -beta, 0.0)
+
+
 def _plain_logits(s):
     case = s["case"]
     z, log_total, own_z, counted, top = _rows(s)
@@ -384,16 +394,11 @@ def _plain_logits(s):
         share = 1 / torch.zeros_like(score).index_add_(0, seq, counted.double()).clamp(min=1)
         score = score * share
     gap = (score[:pairs] - score[pairs:]).float()
-    beta, eps = case["beta"], case["smoothing"]
-    x = beta * gap
-    if case["loss"] == "sigmoid":
-        loss = (1 - eps) * (1 + (-x.abs()).exp()).log() + eps * (1 + (-x.abs()).exp()).log()
-        loss = loss + (1 - eps) * (-x).clamp(min=0) + eps * x.clamp(min=0)
-        dgap = beta * (1 / (1 + (-x).exp()) - (1 - eps))
-    elif case["loss"] == "squared":
-        loss, dgap = (gap - 0.5 / beta).square(), 2 * (gap - 0.5 / beta)
-    else:
-        loss, dgap = (1 - x).clamp(min=0), torch.where(x < 1, -beta, 0.0)
+    x, eps = case["beta"] * gap, case["smoothing"]
+    loss, dgap = _pair_loss(case, gap)
+    if eps:  # some labels are the wrong way round
+        loss2, dgap2 = _pair_loss(case, -gap)
+        loss, dgap = (1 - eps) * loss + eps * loss2, (1 - eps) * dgap - eps * dgap2
     out["loss"], out["margins"] = loss.double().mean().float()[None], x
     coef = torch.cat([dgap, -dgap]) / pairs * share.float()
     out["dlogits"] = _gradient(s, z, log_total, counted, coef[seq])
@@ -538,12 +543,10 @@ def _exact_logits(s):
             score.append(d / max(1, int(counted[lo:hi].sum())) if case["average"] else d)
         gap = torch.stack(score[:n]) - torch.stack(score[n:])
         x, eps = case["beta"] * gap, case["smoothing"]
-        if case["loss"] == "sigmoid":
-            each = -(1 - eps) * torch.nn.functional.logsigmoid(x) - eps * torch.nn.functional.logsigmoid(-x)
-        elif case["loss"] == "squared":
-            each = (gap - 1 / (2 * case["beta"])) ** 2
-        else:
-            each = torch.relu(1 - x)
+        each = {"sigmoid": lambda d: -torch.nn.functional.logsigmoid(case["beta"] * d),
+                "squared": lambda d: (d - 1 / (2 * case["beta"])) ** 2,
+                "hinge": lambda d: torch.relu(1 - case["beta"] * d)}[case["loss"]]
+        each = (1 - eps) * each(gap) + eps * each(-gap)
         loss = each.mean() + 0 * h.sum()
         out["loss"], out["margins"] = loss.detach()[None], x.detach()
     dlp, dh = torch.autograd.grad(loss, [lp, h], allow_unused=True)
