@@ -499,6 +499,161 @@ FO_API fo_status fo_rope_backward(fo_ctx* ctx, const fo_mat* dY, int P, const fo
                                   int layout, const int32_t* const* positions, int64_t start,
                                   int64_t rank_stride, const fo_mat* dX, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Training: losses from the logits of a column-parallel output projection, and the update.
+ * ------------------------------------------------------------------------- */
+
+/* Logits are P matrices, as fo_ag_gemm leaves them: logits[r] [M, V_r], bf16 or fp32 (all ranks
+ * one type), the vocabulary's columns in rank order: id y is column y - (V_0 + .. + V_{r-1}) of
+ * rank r (V_r may differ).  Gradients dlogits[r] have the same shapes, bf16 or fp32 of their own,
+ * and are what fo_col_linear_backward takes as dY; dlogits may be logits (one type, rank by rank
+ * as one view).  No other overlap of an output with anything.
+ * targets (device, int32, M entries): the token's id; negative: the row does not count.  Rows
+ * that do not count are not read, whatever they hold; their outputs and gradients are 0.  An id
+ * of V or above ends the call with FO_ERR_RANGE from fo_ctx_poll, and its row does not count.
+ * Vectors are device fp32 with one entry per row unless said otherwise.
+ *   z = scale logits,  p = softmax(z) over all ranks' columns,  lse = log sum exp z,
+ *   logp = z_y - lse,  H = -sum p log p.
+ * Statistics are fp32, relative to the row's maximum; columns of -infinity have weight 0 (a row of
+ * nothing else gives NaN, as the formula does).  scale > 0 (1 / temperature).  No atomics on
+ * results: the same inputs give the same bits. */
+
+/* logp (null: none of it, then lse or entropy), lse and entropy (each may be null). */
+FO_API fo_status fo_token_logprobs(fo_ctx* ctx, const fo_mat* logits, int P, const int32_t* targets, float scale,
+                                   float* logp, float* lse, float* entropy, void* stream);
+
+/* Gradient of sum_t dlogp_t logp_t + dentropy_t H_t, from the lse (and, with dentropy, the
+ * entropy) that fo_token_logprobs gave (the probabilities carry the rounding of lse to fp32):
+ *   dlogits = scale (dlogp (1[y] - p) - dentropy p (log p + H)).
+ * dentropy null: none (then entropy is not read and may be null). */
+FO_API fo_status fo_token_logprobs_backward(fo_ctx* ctx, const fo_mat* logits, int P, const int32_t* targets,
+                                            float scale, const float* lse, const float* entropy,
+                                            const float* dlogp, const float* dentropy, const fo_mat* dlogits,
+                                            void* stream);
+
+/* Clipped policy loss with a KL term and an entropy bonus, with its gradient in the same pass over
+ * the logits.  Per token, with ratio = exp(logp - old_logp) and x = ref_logp - logp:
+ *   L = -min(ratio A, clip(ratio, 1 - clip_low, 1 + clip_high) A)
+ *       + kl_coef (exp(x) - x - 1) - entropy_coef H.
+ * A: advantages.  old_logp null: the policy itself (ratio 1; its gradient is that of logp).
+ * ref_logp null: no KL term (kl_coef has to be 0).  weights null: 1; a row of weight 0 does not
+ * count.  The loss is sum_t w_t L_t, divided by sum_t w_t over the counted rows where mean is set
+ * (0 where nothing counts).
+ *   logp: as above (null: not wanted).  stats: 4 values, summed or averaged like the loss: the
+ *   loss, the KL term (without kl_coef), the share of clipped tokens, the entropy.
+ *   dlogits null: no gradient.
+ * Where the clipped value is the smaller one the ratio has no gradient.  Values of vectors in rows
+ * that do not count have no effect. */
+typedef struct {
+  float scale;                 /* of the logits */
+  float clip_low, clip_high;   /* >= 0; clip_low <= 1 */
+  float kl_coef, entropy_coef;
+  int32_t mean;
+} fo_policy_params;
+FO_API fo_status fo_policy_loss(fo_ctx* ctx, const fo_mat* logits, int P, const int32_t* targets,
+                                const float* old_logp, const float* advantages, const float* ref_logp,
+                                const float* weights, const fo_policy_params* params, float* logp, float* stats,
+                                const fo_mat* dlogits, void* stream);
+
+typedef enum {
+  FO_PREF_SIGMOID = 0,  /* l(d) = log(1 + exp(-beta d))     */
+  FO_PREF_SQUARED = 1,  /* l(d) = (d - 1 / (2 beta))^2      */
+  FO_PREF_HINGE = 2     /* l(d) = max(0, 1 - beta d)        */
+} fo_preference_kind;
+
+/* Preference loss of pairs of packed sequences.  offsets (device, 2 num_pairs + 1 int32): sequence
+ * s holds the rows offsets[s] .. offsets[s+1]; sequence i is the preferred one of pair i, sequence
+ * num_pairs + i the other.  With score_s = the sum over the sequence's counted rows of
+ * logp - ref_logp (average: their mean; nothing counted: 0) and
+ * d_i = score_i - score_{num_pairs+i} - margin:
+ *   loss = mean over pairs of (1 - e) l(d_i) + e l(-d_i),   e = label_smoothing.
+ * ref_logp null: 0.  loss: 1 value; margins: num_pairs values beta d_i (null: not wanted); logp as
+ * above (null: not wanted); dlogits null: no gradient.  Sequences may be empty.  Rows in front of
+ * the first and behind the last sequence are neither read nor written.  Offsets that decrease or
+ * lie outside [0, M] end the call with FO_ERR_RANGE from fo_ctx_poll and nothing is computed.
+ * Workspace: 16 bytes per row and 12 per pair, kept and grown like those of fo_attn_backward. */
+typedef struct {
+  int32_t kind;                /* fo_preference_kind */
+  int32_t average;
+  float scale;                 /* of the logits */
+  float beta;                  /* > 0 */
+  float label_smoothing;       /* 0 .. 1 */
+  float margin;
+} fo_preference_params;
+FO_API fo_status fo_preference_loss(fo_ctx* ctx, const fo_mat* logits, int P, const int32_t* targets,
+                                    const int32_t* offsets, int num_pairs, const float* ref_logp,
+                                    const fo_preference_params* params, float* logp, float* margins, float* loss,
+                                    const fo_mat* dlogits, void* stream);
+
+/* One tensor of an AdamW step: n elements, contiguous, every pointer 16-byte aligned (the ranges
+ * of 8-bit states 8-byte).  Gradients fp32 or bf16; parameters fp32, or bf16 with or without an
+ * fp32 master.  States m and v are fp32, or (m_scale and v_range given) 8 bits each, in blocks of
+ * 256 elements of the tensor:
+ *   m = e4m3 value * m_scale[block];
+ *   v = 0 for code 0, else 2^(v_range[2 block] + (code - 1) v_range[2 block + 1])
+ * (255 values, evenly spaced in log2, between the block's smallest and largest; a largest value
+ * 2^24 times v is taken for v's stead at most).  All bytes zero: states of zero.  Both are rounded
+ * to one of the two neighbouring values at random, so that the mean is the value: rounded to the
+ * nearest, a mean that moves by a few percent or less a step would not move at all. */
+typedef struct {
+  void* param;
+  const void* grad;
+  float* master;       /* null: none */
+  void* m;
+  void* v;
+  float* m_scale;      /* ceil(n / 256) values; null: fp32 states */
+  float* v_range;      /* 2 ceil(n / 256) values */
+  int64_t n;
+  int32_t param_dtype, grad_dtype;   /* fo_dtype */
+} fo_adamw_tensor;
+
+/* The tensors of a step, checked once and laid out for the kernels (host only, no GPU).  The group
+ * keeps the addresses, not the memory behind them: the caller keeps that alive and in place.  No
+ * tensor that a step writes may overlap another.  A group is not changed by its use: calls of
+ * several contexts may share it. */
+typedef struct fo_adamw_group fo_adamw_group;
+FO_API fo_status fo_adamw_group_create(const fo_adamw_tensor* tensors, int count, fo_adamw_group** out);
+FO_API fo_status fo_adamw_group_destroy(fo_adamw_group* group);
+
+/* norm[0] = sqrt(sum of the squares of every gradient in the group) (device fp32; the squares are
+ * fp32, so elements above 1.8e19 read as infinite).  Workspace: 8 bytes per CTA. */
+FO_API fo_status fo_grad_norm(fo_ctx* ctx, const fo_adamw_group* group, float* norm, void* stream);
+
+/* One step for every tensor.  With g = grad_scale * gradient, times
+ * max_norm / (|grad_scale| norm) where norm is given, max_norm > 0 and that is below 1:
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2,
+ *   w = w - lr (weight_decay w + (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps)),
+ * w being the master where there is one (the parameter is then w rounded).  fp32 arithmetic.
+ * norm (null: none): where it is not finite nothing is written at all.  Without it gradients have
+ * to be finite.  lr_dev, step_dev (device; null: lr, step): read when the kernel runs, so that a
+ * captured step can be replayed with others.  step >= 1 (a smaller one in memory ends the call with
+ * FO_ERR_RANGE from fo_ctx_poll and nothing is written).
+ * stochastic: bf16 parameters without a master are rounded up or down at random (mean: w) instead
+ * of to the nearest.  What is random depends on (seed, step, place of the tensor in the group,
+ * element) alone: word = h(b + 0x9E3779B9 e) for element e of the block whose
+ * b = h(h(k + tensor) + block), k = h(h(lo(seed) ^ h(step)) ^ hi(seed)), with
+ * h(x): x ^= x >> 16, x *= 0x7feb352d, x ^= x >> 15, x *= 0x846ca68b, x ^= x >> 16 (32 bits).  Its
+ * low half rounds m, its high half v, the high half of word * 0x9E3779B9 the parameter. */
+typedef struct {
+  double beta1, beta2;         /* 0 .. below 1 */
+  float lr, eps, weight_decay;
+  float grad_scale, max_norm;
+  int32_t stochastic;
+  int64_t step;
+  uint64_t seed;
+  const float* lr_dev;
+  const int32_t* step_dev;
+  const float* norm;
+} fo_adamw_params;
+FO_API fo_status fo_adamw_step(fo_ctx* ctx, const fo_adamw_group* group, const fo_adamw_params* params,
+                               void* stream);
+
+/* The 8-bit states of a group as values: m[i], v[i] (device, n elements of tensor i, `dtype`
+ * fo_dtype, 16-byte aligned; entries of tensors with fp32 states are not looked at and may be
+ * null).  For checkpoints and inspection. */
+FO_API fo_status fo_adamw_unpack(fo_ctx* ctx, const fo_adamw_group* group, void* const* m, void* const* v,
+                                 int dtype, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

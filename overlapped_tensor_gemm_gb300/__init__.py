@@ -32,6 +32,8 @@ EPILOGUES = {"plain": 0, "silu": 1}
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 ROPE_SCALINGS = {None: 0, "linear": 1, "banded": 2, "ramped": 3}
 ROPE_MAX_PAIRS = 256
+PREFERENCE_KINDS = {"sigmoid": 0, "squared": 1, "hinge": 2}
+STATE_BLOCK = 256  # elements that share the ranges of 8-bit optimizer states
 
 # Every entry point declared in include/fo.h.
 ABI_SYMBOLS = ("fo_version", "fo_last_error_string", "fo_ctx_create", "fo_ctx_destroy", "fo_ctx_poll",
@@ -39,7 +41,9 @@ ABI_SYMBOLS = ("fo_version", "fo_last_error_string", "fo_ctx_create", "fo_ctx_de
                "fo_mlp_layer_host", "fo_qsplit_attn", "fo_attn_layer", "fo_gemm_a2a", "fo_a2a_gemm", "fo_col_linear_backward",
                "fo_row_linear_backward", "fo_step_order",
                "fo_gemm_rs_noalloc", "fo_attn_forward", "fo_attn_backward", "fo_norm_residual",
-               "fo_norm_residual_backward", "fo_rope_table_init", "fo_rope", "fo_rope_backward")
+               "fo_norm_residual_backward", "fo_rope_table_init", "fo_rope", "fo_rope_backward",
+               "fo_token_logprobs", "fo_token_logprobs_backward", "fo_policy_loss", "fo_preference_loss",
+               "fo_adamw_group_create", "fo_adamw_group_destroy", "fo_grad_norm", "fo_adamw_step", "fo_adamw_unpack")
 
 
 class FoMat(ctypes.Structure):
@@ -78,6 +82,31 @@ class FoRopeTable(ctypes.Structure):
 class FoRopeScaling(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int32), ("reserved", ctypes.c_int32), ("factor", ctypes.c_double),
                 ("low", ctypes.c_double), ("high", ctypes.c_double), ("original_length", ctypes.c_int64)]
+
+
+class FoPolicyParams(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("clip_low", ctypes.c_float), ("clip_high", ctypes.c_float),
+                ("kl_coef", ctypes.c_float), ("entropy_coef", ctypes.c_float), ("mean", ctypes.c_int32)]
+
+
+class FoPreferenceParams(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("average", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("beta", ctypes.c_float), ("label_smoothing", ctypes.c_float), ("margin", ctypes.c_float)]
+
+
+class FoAdamWTensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("master", ctypes.c_void_p),
+                ("m", ctypes.c_void_p), ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p),
+                ("v_range", ctypes.c_void_p), ("n", ctypes.c_int64), ("param_dtype", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32)]
+
+
+class FoAdamWParams(ctypes.Structure):
+    _fields_ = [("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("lr", ctypes.c_float),
+                ("eps", ctypes.c_float), ("weight_decay", ctypes.c_float), ("grad_scale", ctypes.c_float),
+                ("max_norm", ctypes.c_float), ("stochastic", ctypes.c_int32), ("step", ctypes.c_int64),
+                ("seed", ctypes.c_uint64), ("lr_dev", ctypes.c_void_p), ("step_dev", ctypes.c_void_p),
+                ("norm", ctypes.c_void_p)]
 
 
 class FoError(RuntimeError):
@@ -133,6 +162,17 @@ def load() -> ctypes.CDLL:
         lib.fo_rope_table_init.argtypes = [P(FoRopeTable), ci, ctypes.c_double, P(FoRopeScaling)]
         for name in ("fo_rope", "fo_rope_backward"):
             getattr(lib, name).argtypes = [vp, P(FoMat), ci, P(FoRopeTable), ci, ci, P(vp), i64, i64, P(FoMat), vp]
+        cf = ctypes.c_float
+        lib.fo_token_logprobs.argtypes = [vp, P(FoMat), ci, vp, cf, vp, vp, vp, vp]
+        lib.fo_token_logprobs_backward.argtypes = [vp, P(FoMat), ci, vp, cf, vp, vp, vp, vp, P(FoMat), vp]
+        lib.fo_policy_loss.argtypes = [vp, P(FoMat), ci, vp, vp, vp, vp, vp, P(FoPolicyParams), vp, vp, P(FoMat), vp]
+        lib.fo_preference_loss.argtypes = [vp, P(FoMat), ci, vp, vp, ci, vp, P(FoPreferenceParams), vp, vp, vp,
+                                           P(FoMat), vp]
+        lib.fo_adamw_group_create.argtypes = [P(FoAdamWTensor), ci, P(vp)]
+        lib.fo_adamw_group_destroy.argtypes = [vp]
+        lib.fo_grad_norm.argtypes = [vp, vp, vp, vp]
+        lib.fo_adamw_step.argtypes = [vp, vp, P(FoAdamWParams), vp]
+        lib.fo_adamw_unpack.argtypes = [vp, vp, P(vp), P(vp), ci, vp]
         lib.fo_gemm_rs_noalloc.argtypes = [P(FoMat), P(FoMat), ctypes.c_int, P(FoMat), ctypes.c_uint32,
                                            vp, vp]
         for name in ABI_SYMBOLS:
@@ -174,6 +214,14 @@ _MAT_BYTES = ctypes.sizeof(FoMat)
 _PACK_MAT = struct.Struct("@Piiqqq").pack_into  # FoMat's fields
 assert struct.calcsize("@Piiqqq") == _MAT_BYTES
 _DTYPE_CODES: dict = {}
+_F32 = None
+
+
+def _f32():
+    global _F32
+    import torch
+    _F32 = torch.float32
+    return _F32
 
 
 def _dtype_codes() -> dict:
@@ -223,6 +271,82 @@ class RopeTable:
     @property
     def rot_dim(self) -> int:
         return self.c.rot_dim
+
+
+def adamw_states(params, bits: int = 32):
+    """(m, v, m_scale, v_range) of zeros for a list of parameters: fp32 states (m_scale and v_range None), or 8 bits
+    (m float8_e4m3fn, v uint8, fp32 ranges of every block of 256 elements)."""
+    import torch
+    if bits not in (8, 32):
+        raise ValueError(f"states of {bits} bits: 8 or 32")
+    if bits == 32:
+        return ([torch.zeros(p.shape, dtype=torch.float32, device=p.device) for p in params],
+                [torch.zeros(p.shape, dtype=torch.float32, device=p.device) for p in params], None, None)
+    zeros = lambda p, dt: torch.zeros(p.shape, dtype=torch.uint8, device=p.device).view(dt)  # noqa: E731
+    blocks = [-(-p.numel() // STATE_BLOCK) for p in params]
+    return ([zeros(p, torch.float8_e4m3fn) for p in params], [zeros(p, torch.uint8) for p in params],
+            [torch.zeros(b, dtype=torch.float32, device=p.device) for p, b in zip(params, blocks)],
+            [torch.zeros(2 * b, dtype=torch.float32, device=p.device) for p, b in zip(params, blocks)])
+
+
+class AdamWTensors:
+    """The tensors of an AdamW step, checked and laid out once (the object keeps them alive; they have to stay in
+    place).  Lists of contiguous tensors on one device: params bf16 or fp32, grads bf16 or fp32, m and v fp32 -- or,
+    with m_scale and v_range, m float8_e4m3fn, v uint8 and their blocks' ranges (``adamw_states(params, 8)``).
+    master: fp32 masters of bf16 parameters.  Entries of master, m_scale and v_range may be None."""
+
+    def __init__(self, params, grads, m, v, master=None, m_scale=None, v_range=None):
+        import torch
+        n = len(params)
+        f32, bf16 = torch.float32, torch.bfloat16
+        none = [None] * n
+        lists = {"params": params, "grads": grads, "master": master, "m": m, "v": v, "m_scale": m_scale,
+                 "v_range": v_range}
+        lists = {k: none if x is None else list(x) for k, x in lists.items()}
+        self._keep = lists
+        self.device = None
+        self._h = ctypes.c_void_p()
+        arr = (FoAdamWTensor * max(n, 1))()
+        for what, ts in lists.items():
+            if len(ts) != n:
+                raise ValueError(f"{what}: {len(ts)} tensors for {n} parameters")
+        for i in range(n):
+            p = lists["params"][i]
+            eight = lists["m_scale"][i] is not None
+            blocks = -(-p.numel() // STATE_BLOCK)
+            want = {"params": (p.numel(), (bf16, f32)), "grads": (p.numel(), (bf16, f32)), "master": (p.numel(), (f32,)),
+                    "m": (p.numel(), (torch.float8_e4m3fn,) if eight else (f32,)),
+                    "v": (p.numel(), (torch.uint8,) if eight else (f32,)), "m_scale": (blocks, (f32,)),
+                    "v_range": (2 * blocks, (f32,))}
+            at = {}
+            for what, (size, dtypes) in want.items():
+                t = lists[what][i]
+                if t is None:
+                    if what in ("params", "grads", "m", "v"):
+                        raise ValueError(f"{what}[{i}] is missing")
+                    at[what] = None
+                    continue
+                if t.device.type != "cuda" or (self.device is not None and t.device.index != self.device):
+                    raise ValueError(f"{what}[{i}] is on {t.device}: all tensors have to be on one GPU")
+                self.device = t.device.index
+                if t.dtype not in dtypes or t.numel() != size or not t.is_contiguous():
+                    raise ValueError(f"{what}[{i}] must be contiguous, {' or '.join(map(str, dtypes))}, {size} elements")
+                at[what] = t.data_ptr()
+            arr[i] = FoAdamWTensor(at["params"], at["grads"], at["master"], at["m"], at["v"], at["m_scale"],
+                                   at["v_range"], p.numel(), FO_F32 if p.dtype == f32 else FO_BF16,
+                                   FO_F32 if lists["grads"][i].dtype == f32 else FO_BF16)
+        self._lib = load()
+        _check(self._lib.fo_adamw_group_create(arr, n, ctypes.byref(self._h)))
+
+    def __len__(self) -> int:
+        return len(self._keep["params"])
+
+    def __del__(self):
+        try:
+            if self._h:
+                self._lib.fo_adamw_group_destroy(self._h)
+        except Exception:
+            pass
 
 
 class Context:
@@ -488,6 +612,124 @@ class Context:
                       positions=None, start: int = 0, rank_stride: int = 0, stream=None) -> None:
         """dX from the gradient dY of rope's output (dX may be dY)."""
         self._rope(self._lib.fo_rope_backward, dY, dX, table, head_dim, layout, positions, start, rank_stride, stream)
+
+    # -- losses from sharded logits, optimizer -----------------------------------------------
+
+    def _entries(self, t, what: str, n: int, dtype=None):
+        """Address of a contiguous vector of n entries, fp32 unless said otherwise (None stays None)."""
+        if t is None:
+            return None
+        if dtype is None:
+            dtype = _F32 or _f32()
+        if t.get_device() != self.device:
+            self._here(t, what)
+        if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+            raise ValueError(f"{what} must be a contiguous {dtype} vector of {n} entries")
+        return t.data_ptr()
+
+    def _targets(self, logits, targets):
+        import torch
+        P = len(logits)
+        z = self._list(logits, P, "logits")
+        return P, z, logits[0].shape[0], self._entries(targets, "targets", logits[0].shape[0], torch.int32)
+
+    def token_logprobs(self, logits, targets, logp, lse=None, entropy=None, scale: float = 1.0, stream=None) -> None:
+        """Log-probabilities logp of the targets (int32, one per row; negative: the row does not count, its outputs
+        are 0) under softmax(scale logits), logits[r] rank r's columns of the vocabulary.  lse, entropy: of the rows."""
+        P, z, n, y = self._targets(logits, targets)
+        _check(self._lib.fo_token_logprobs(self._h, z, P, y, scale, self._entries(logp, "logp", n),
+                                           self._entries(lse, "lse", n), self._entries(entropy, "entropy", n),
+                                           self._own_stream(stream)))
+
+    def token_logprobs_backward(self, logits, targets, lse, dlogp, dlogits, entropy=None, dentropy=None,
+                                scale: float = 1.0, stream=None) -> None:
+        """dlogits of sum(dlogp * logp) (+ sum(dentropy * entropy)), from token_logprobs' lse (and entropy).  dlogits
+        may be logits."""
+        P, z, n, y = self._targets(logits, targets)
+        _check(self._lib.fo_token_logprobs_backward(
+            self._h, z, P, y, scale, self._entries(lse, "lse", n), self._entries(entropy, "entropy", n),
+            self._entries(dlogp, "dlogp", n), self._entries(dentropy, "dentropy", n),
+            self._list(dlogits, P, "dlogits"), self._own_stream(stream)))
+
+    def policy_loss(self, logits, targets, advantages, stats, old_logp=None, ref_logp=None, weights=None, logp=None,
+                    dlogits=None, clip_low: float = 0.2, clip_high: float = 0.2, kl_coef: float = 0.0,
+                    entropy_coef: float = 0.0, mean: bool = True, scale: float = 1.0, stream=None) -> None:
+        """Clipped policy loss with a KL term (against ref_logp) and an entropy bonus over the tokens of `logits`,
+        and its gradient dlogits (may be logits) in the same pass.  stats: 4 values, the loss, the KL term, the share
+        of clipped tokens, the entropy; means over the counted tokens by weight, or sums."""
+        P, z, n, y = self._targets(logits, targets)
+        prm = FoPolicyParams(scale, clip_low, clip_high, kl_coef, entropy_coef, int(mean))
+        _check(self._lib.fo_policy_loss(
+            self._h, z, P, y, self._entries(old_logp, "old_logp", n), self._entries(advantages, "advantages", n),
+            self._entries(ref_logp, "ref_logp", n), self._entries(weights, "weights", n), ctypes.byref(prm),
+            self._entries(logp, "logp", n), self._entries(stats, "stats", 4), self._list(dlogits, P, "dlogits"),
+            self._own_stream(stream)))
+
+    def preference_loss(self, logits, targets, offsets, loss, ref_logp=None, logp=None, margins=None, dlogits=None,
+                        kind: str = "sigmoid", beta: float = 0.1, label_smoothing: float = 0.0, margin: float = 0.0,
+                        average: bool = False, scale: float = 1.0, stream=None) -> None:
+        """Preference loss of pairs of packed sequences (rows offsets[s] .. offsets[s+1]; sequence i is preferred to
+        sequence i + pairs), and its gradient dlogits (may be logits).  loss: 1 value, the mean over the pairs;
+        margins: beta times the pairs' gaps."""
+        import torch
+        P, z, n, y = self._targets(logits, targets)
+        if offsets.dim() != 1 or offsets.shape[0] < 3 or offsets.shape[0] % 2 == 0:
+            raise ValueError("offsets must have 2 * pairs + 1 entries")
+        pairs = offsets.shape[0] // 2
+        prm = FoPreferenceParams(PREFERENCE_KINDS[kind], int(average), scale, beta, label_smoothing, margin)
+        _check(self._lib.fo_preference_loss(
+            self._h, z, P, y, self._entries(offsets, "offsets", 2 * pairs + 1, torch.int32), pairs,
+            self._entries(ref_logp, "ref_logp", n), ctypes.byref(prm), self._entries(logp, "logp", n),
+            self._entries(margins, "margins", pairs), self._entries(loss, "loss", 1),
+            self._list(dlogits, P, "dlogits"), self._own_stream(stream)))
+
+    def _group(self, group: AdamWTensors):
+        if group.device is not None and group.device != self.device:
+            raise ValueError(f"the tensors are on cuda:{group.device}, the context on cuda:{self.device}")
+        return group._h
+
+    def grad_norm(self, group: AdamWTensors, norm, stream=None) -> None:
+        """norm[0] = the 2-norm of all gradients of the group."""
+        _check(self._lib.fo_grad_norm(self._h, self._group(group), self._entries(norm, "norm", 1),
+                                      self._own_stream(stream)))
+
+    def adamw_step(self, group: AdamWTensors, lr, step, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+                   weight_decay: float = 0.01, norm=None, max_norm: float = 0.0, grad_scale: float = 1.0,
+                   stochastic: bool = False, seed: int = 0, stream=None) -> None:
+        """One AdamW step of every tensor in the group.  lr: a number or an fp32 tensor of one entry; step (1, 2, ..):
+        a number or an int32 tensor of one entry; as tensors they are read on the device (a captured step can be
+        replayed with others).  norm: grad_norm's result; gradients are scaled down to max_norm, and nothing is
+        written where it is not finite.  stochastic: bf16 parameters without masters are rounded stochastically.
+        seed: of the random roundings, together with the step."""
+        import torch
+        lr_t, step_t = isinstance(lr, torch.Tensor), isinstance(step, torch.Tensor)
+        prm = FoAdamWParams(beta1, beta2, 0.0 if lr_t else lr, eps, weight_decay, grad_scale, max_norm,
+                            int(stochastic), 1 if step_t else step, seed & 0xFFFFFFFFFFFFFFFF,
+                            self._entries(lr, "lr", 1) if lr_t else None,
+                            self._entries(step, "step", 1, torch.int32) if step_t else None,
+                            self._entries(norm, "norm", 1))
+        _check(self._lib.fo_adamw_step(self._h, self._group(group), ctypes.byref(prm), self._own_stream(stream)))
+
+    def adamw_unpack(self, group: AdamWTensors, m, v, stream=None) -> None:
+        """The 8-bit states of the group as values: lists of bf16 or fp32 tensors of the parameters' sizes (None for
+        parameters with fp32 states)."""
+        import torch
+        n = len(group)
+        if len(m) != n or len(v) != n:
+            raise ValueError(f"m and v must have {n} entries")
+        dtype = None
+        for i, p in enumerate(group._keep["params"]):
+            if group._keep["m_scale"][i] is None:
+                continue
+            for what, t in (("m", m[i]), ("v", v[i])):
+                dtype = dtype or t.dtype
+                self._here(t, what)
+                if t.dtype != dtype or dtype not in (torch.bfloat16, torch.float32) or t.numel() != p.numel() \
+                        or not t.is_contiguous():
+                    raise ValueError(f"{what}[{i}] must be contiguous, all bf16 or all fp32, {p.numel()} elements")
+        ptrs = [(ctypes.c_void_p * max(n, 1))(*(None if t is None else t.data_ptr() for t in ts)) for ts in (m, v)]
+        _check(self._lib.fo_adamw_unpack(self._h, self._group(group), ptrs[0], ptrs[1],
+                                         FO_F32 if dtype == torch.float32 else FO_BF16, self._own_stream(stream)))
 
 
 def step_order(op: str, P: int, order: str = "flash") -> list[list[tuple[int, int]]]:

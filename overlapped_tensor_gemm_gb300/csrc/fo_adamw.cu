@@ -1,0 +1,745 @@
+// AdamW over many tensors in few launches, the gradients' norm, and 8-bit states as values.
+//
+//   g = c gradient,  c = grad_scale, times max_norm / (|grad_scale| norm) where that is below 1
+//   m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2
+//   w = w - lr (weight_decay w + (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps))
+//
+// Bound by HBM: every value is read once and written once (fp32 master, bf16 copy and gradient, fp32
+// states: 28 bytes an element).  The tensors' addresses are kernel parameters (no table in memory
+// that a captured launch would have to keep).  A warp takes a block of 256 elements, two groups of
+// four per lane, so that every access of the warp is whole lines in all types.
+//
+// 8-bit states.  A block has its own ranges: m is e4m3 times max|m| / 448; v is one of 255 values
+// evenly spaced in log2 between the block's smallest and largest v (few percent apart: rows of a
+// weight differ by powers of two, elements of one by less).  Both are rounded up or down at random:
+// m moves by 1 - b1 of its distance to g in a step, v by 1 - b2, which is mostly less than half the
+// distance of two values, so that rounded to the nearest they would stay where they are.  What v's
+// rounding adds to it in the mean: nothing to first order (part_of below); its spread is that of
+// the values over sqrt(1 - b2^2) steps.
+#include <cfloat>
+#include <cmath>
+#include <cstring>
+
+#include <algorithm>
+#include <new>
+#include <vector>
+
+#include <cuda_fp8.h>
+
+#include "fo_host.h"
+#include "fo_ptx.cuh"
+
+namespace fo {
+namespace {
+
+constexpr int kBlock = 256;           // elements of a block: 8 per lane of a warp
+constexpr int kAdamThreads = 256;
+constexpr int kListTensors = 400;     // tensors of one launch
+constexpr float kMaxE4m3 = 448.f;
+constexpr float kOctaves = 24.f;      // v's values span at most 2^24
+
+struct TensorRef {
+  void* param;
+  const void* grad;
+  float* master;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_range;
+  int64_t n;
+  int64_t first;        // blocks of the list's tensors in front of this one
+  uint32_t index;       // place in the caller's list
+  uint32_t reserved;
+};
+struct TensorList {
+  int64_t blocks;
+  int32_t count;
+  int32_t kind;         // KindBit
+  TensorRef t[kListTensors];
+};
+enum KindBit : int { kParam32 = 1, kGrad32 = 2, kMaster = 4, kStates8 = 8 };
+
+struct StepArgs {
+  float lr, eps, weight_decay, grad_scale, max_norm;
+  float beta1, beta2, rest1, rest2;   // rest = 1 - beta, before either is rounded
+  float fix1, fix2;                   // 1 / (1 - b1^t), 1 / (1 - b2^t)
+  double exact1, exact2;              // the betas
+  int64_t step;
+  uint32_t seed_low, seed_high;
+  const float* lr_dev;
+  const int32_t* step_dev;
+  const float* norm;
+  uint32_t* ctrl;
+};
+static_assert(sizeof(TensorList) + sizeof(StepArgs) <= 32764, "kernel parameters");
+
+// The tensor of block b: the last one that starts at or in front of it
+__device__ __forceinline__ int tensor_of(const TensorList& l, int64_t b) {
+  int lo = 0, hi = l.count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (l.t[mid].first <= b) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// 32 bits scattered: two rounds of xor-shift and multiply (constants of C. Wellons' search for
+// functions of this form whose output bits depend evenly on all input bits)
+__host__ __device__ __forceinline__ uint32_t scatter(uint32_t x) {
+  x = (x ^ (x >> 16)) * 0x7feb352du;
+  x = (x ^ (x >> 15)) * 0x846ca68bu;
+  return x ^ (x >> 16);
+}
+
+__device__ __forceinline__ float fast_log2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float exact_exp2(float x) {  // subnormal results kept
+  float y;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float fast_sqrt(float x) {
+  float y;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 4 elements from p on, the first n of them inside the tensor
+__device__ __forceinline__ void load4(const float* p, int n, float (&v)[4]) {
+  if (n >= 4) {
+    const float4 q = *reinterpret_cast<const float4*>(p);
+    v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = k < n ? p[k] : 0.f;
+  }
+}
+__device__ __forceinline__ void load4(const uint16_t* p, int n, float (&v)[4]) {
+  if (n >= 4) {
+    const uint2 q = *reinterpret_cast<const uint2*>(p);
+    v[0] = __uint_as_float(q.x << 16);
+    v[1] = __uint_as_float(q.x & 0xFFFF0000u);
+    v[2] = __uint_as_float(q.y << 16);
+    v[3] = __uint_as_float(q.y & 0xFFFF0000u);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = k < n ? __uint_as_float(static_cast<uint32_t>(p[k]) << 16) : 0.f;
+  }
+}
+__device__ __forceinline__ uint32_t load4(const uint8_t* p, int n) {
+  if (n >= 4) return *reinterpret_cast<const uint32_t*>(p);
+  uint32_t q = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (k < n) q |= static_cast<uint32_t>(p[k]) << (8 * k);
+  return q;
+}
+__device__ __forceinline__ void store4(float* p, int n, const float (&v)[4]) {
+  if (n >= 4) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k < n) p[k] = v[k];
+  }
+}
+__device__ __forceinline__ void store4(uint16_t* p, int n, const float (&v)[4]) {
+  const uint32_t q[2] = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+  if (n >= 4) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(q[0], q[1]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k < n) p[k] = static_cast<uint16_t>(q[k >> 1] >> (16 * (k & 1)));
+  }
+}
+__device__ __forceinline__ void store4(uint8_t* p, int n, uint32_t q) {
+  if (n >= 4) {
+    *reinterpret_cast<uint32_t*>(p) = q;
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k < n) p[k] = static_cast<uint8_t>(q >> (8 * k));
+  }
+}
+
+// 4 e4m3 values
+__device__ __forceinline__ void from_e4m3(uint32_t q, float (&v)[4]) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const __half2_raw h =
+        __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(q >> (16 * k)), __NV_E4M3);
+    const float2 f = __half22float2(__half2(h));
+    v[2 * k] = f.x;
+    v[2 * k + 1] = f.y;
+  }
+}
+__device__ __forceinline__ float level(uint32_t code, float low, float gap) {
+  return code ? exact_exp2(fmaf(static_cast<float>(code - 1), gap, low)) : 0.f;
+}
+
+// x (at most 448) up or down to an e4m3 value: what a step holds below is cut off after a random
+// part of a step is added.  Below 2^-6 the steps stay 2^-9 wide, as they are from 2^-6 to 2^-5, so
+// there the sum with 2^-6 is cut.
+__device__ __forceinline__ float cut_e4m3(float x, uint32_t half_word) {
+  const float size = fminf(fabsf(x), kMaxE4m3), lift = size < 0.015625f ? 0.015625f : 0.f;
+  const uint32_t q = (__float_as_uint(size + lift) + (half_word << 4)) & 0xFFF00000u;
+  return x == x ? copysignf(__uint_as_float(q) - lift, x) : x;
+}
+// A bf16 value next to w, by the upper half of `word`; infinities and NaN stay
+__device__ __forceinline__ float cut_bf16(float w, uint32_t word) {
+  const float q = __uint_as_float((__float_as_uint(w) + (word >> 16)) & 0xFFFF0000u);
+  return fabsf(w) <= FLT_MAX ? q : w;
+}
+
+// Corrections of a step that is read from memory: 1 / (1 - b^t) by repeated squaring in fp64
+__device__ __forceinline__ float correction(double beta, int64_t t) {
+  double p = 1.0, b = beta;
+  for (; t > 0; t >>= 1) {
+    if (t & 1) p *= b;
+    b *= b;
+  }
+  return static_cast<float>(1.0 / (1.0 - p));
+}
+
+template <bool kP32, bool kG32, bool kHasMaster, bool k8>
+__global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_constant__ TensorList l,
+                                                             const __grid_constant__ StepArgs a, bool cut) {
+  typedef typename std::conditional<kP32, float, uint16_t>::type TP;
+  typedef typename std::conditional<kG32, float, uint16_t>::type TG;
+  __shared__ float fixes[2];
+  const int lane = threadIdx.x & 31;
+  float c = a.grad_scale;
+  if (a.norm) {
+    const float norm = *a.norm;
+    if (!(norm <= FLT_MAX)) return;  // infinite or NaN: nothing is written
+    const float whole = norm * fabsf(a.grad_scale);
+    if (a.max_norm > 0.f && whole > a.max_norm) c *= a.max_norm / whole;
+  }
+  const float lr = a.lr_dev ? *a.lr_dev : a.lr;
+  const int64_t step = a.step_dev ? *a.step_dev : a.step;
+  float fix1 = a.fix1, fix2 = a.fix2;
+  if (a.step_dev) {
+    if (step < 1) {
+      if (blockIdx.x == 0 && threadIdx.x == 0)
+        note_error(a.ctrl, FO_ERR_RANGE, kSiteStep, static_cast<uint32_t>(step));
+      return;
+    }
+    if (threadIdx.x < 2) fixes[threadIdx.x] = correction(threadIdx.x ? a.exact2 : a.exact1, step);
+    __syncthreads();
+    fix1 = fixes[0];
+    fix2 = fixes[1];
+  }
+  const uint32_t key = scatter(scatter(a.seed_low ^ scatter(static_cast<uint32_t>(step))) ^ a.seed_high);
+  const float decay = lr * a.weight_decay, rate = lr * fix1;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kAdamThreads / 32);
+  int64_t b = static_cast<int64_t>(blockIdx.x) * (kAdamThreads / 32) + (threadIdx.x >> 5);
+  if (b >= l.blocks) return;
+  int i = tensor_of(l, b);
+  for (; b < l.blocks; b += warps) {
+    while (i + 1 < l.count && l.t[i + 1].first <= b) ++i;
+    const TensorRef& t = l.t[i];
+    const int64_t blk = b - t.first, at = blk * kBlock;
+    const int64_t left = t.n - at;
+    const int n = left < kBlock ? static_cast<int>(left) : kBlock;
+    float w[2][4], g[2][4], m[2][4], v[2][4];
+    float m_scale = 0.f, low = 0.f, gap = 0.f;
+    if (k8) {
+      m_scale = t.m_scale[blk];
+      const float2 r = reinterpret_cast<const float2*>(t.v_range)[blk];
+      low = r.x;
+      gap = r.y;
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int e = q * 128 + lane * 4, in = n - e;
+      load4(static_cast<const TG*>(t.grad) + at + e, in, g[q]);
+      if (kHasMaster) {
+        load4(t.master + at + e, in, w[q]);
+      } else {
+        load4(static_cast<const TP*>(t.param) + at + e, in, w[q]);
+      }
+      if (k8) {
+        from_e4m3(load4(static_cast<const uint8_t*>(t.m) + at + e, in), m[q]);
+        const uint32_t codes = load4(static_cast<const uint8_t*>(t.v) + at + e, in);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          m[q][k] *= m_scale;
+          v[q][k] = level(codes >> (8 * k) & 0xFFu, low, gap);
+        }
+      } else {
+        load4(static_cast<const float*>(t.m) + at + e, in, m[q]);
+        load4(static_cast<const float*>(t.v) + at + e, in, v[q]);
+      }
+    }
+    float top_m = 0.f, top_v = 0.f, min_v = INFINITY;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float x = g[q][k] * c;
+        m[q][k] = fmaf(a.beta1, m[q][k], a.rest1 * x);
+        v[q][k] = fmaf(a.beta2, v[q][k], a.rest2 * x * x);
+        const float root = fast_sqrt(v[q][k] * fix2) + a.eps;
+        w[q][k] = w[q][k] - fmaf(decay, w[q][k], __fdividef(rate * m[q][k], root));
+        if (k8) {
+          top_m = fmaxf(top_m, fabsf(m[q][k]));
+          top_v = fmaxf(top_v, v[q][k]);
+          if (v[q][k] > 0.f) min_v = fminf(min_v, v[q][k]);
+        }
+      }
+    }
+    float scale = 0.f, inv_scale = 0.f, inv_gap = 0.f, bend = 0.f;
+    uint32_t base = 0;
+    if (k8) {
+      // (bits of values that are not negative are ordered as the values are)
+      top_m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top_m)));
+      top_v = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top_v)));
+      min_v = __uint_as_float(__reduce_min_sync(0xffffffffu, __float_as_uint(min_v)));
+      if (top_m > 1e-30f) {  // smaller ones are kept as zeros
+        scale = top_m / kMaxE4m3;
+        inv_scale = kMaxE4m3 / top_m;
+      }
+      low = gap = 0.f;
+      if (top_v > 0.f) {
+        const float top = fast_log2(top_v);
+        low = fmaxf(fast_log2(min_v), top - kOctaves);
+        gap = (top - low) * (1.f / 254.f);
+        inv_gap = gap > 0.f ? 1.f / gap : 0.f;
+        bend = 0.34657359f * gap;  // ln 2 / 2
+      }
+    }
+    if (k8 || cut) base = scatter(scatter(key + t.index) + static_cast<uint32_t>(blk));
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int e = q * 128 + lane * 4, in = n - e;
+      uint32_t word[4] = {0, 0, 0, 0};
+      if (k8 || cut) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) word[k] = scatter(base + static_cast<uint32_t>(e + k) * 0x9E3779B9u);
+      }
+      if (kHasMaster) store4(t.master + at + e, in, w[q]);
+      if (!kP32 && !kHasMaster && cut) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[q][k] = cut_bf16(w[q][k], word[k] * 0x9E3779B9u);
+      }
+      store4(static_cast<TP*>(t.param) + at + e, in, w[q]);
+      if (k8) {
+        uint32_t mq[2], vq = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          m[q][k] = cut_e4m3(m[q][k] * inv_scale, word[k] & 0xFFFFu);
+          const float y = fminf(fmaxf((fast_log2(v[q][k]) - low) * inv_gap, 0.f), 254.f);
+          const float whole = floorf(y);
+          float part = y - whole;
+          part = part - bend * part * (1.f - part);
+          const float up = static_cast<float>(word[k] >> 16) * (1.f / 65536.f) < part ? 1.f : 0.f;
+          const uint32_t code = v[q][k] > 0.f ? static_cast<uint32_t>(whole + up) + 1u : 0u;
+          vq |= code << (8 * k);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          mq[k] = __nv_cvt_float2_to_fp8x2(make_float2(m[q][2 * k], m[q][2 * k + 1]), __NV_SATFINITE, __NV_E4M3);
+        store4(static_cast<uint8_t*>(t.m) + at + e, in, mq[0] | mq[1] << 16);
+        store4(static_cast<uint8_t*>(t.v) + at + e, in, vq);
+      } else {
+        store4(static_cast<float*>(t.m) + at + e, in, m[q]);
+        store4(static_cast<float*>(t.v) + at + e, in, v[q]);
+      }
+    }
+    if (k8 && lane == 0) {
+      t.m_scale[blk] = scale;
+      reinterpret_cast<float2*>(t.v_range)[blk] = make_float2(low, gap);
+    }
+  }
+}
+
+// Fixed-order sum over the CTA, in thread 0
+__device__ __forceinline__ double block_sum(double v, double* buf) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.0;
+  for (int w = 0; w < kAdamThreads / 32; ++w) v += buf[w];
+  return v;
+}
+
+// Squares of one list's gradients; the CTA that comes last adds the CTAs' sums in order to what the
+// lists in front left, and behind the last list takes the root
+struct NormArgs {
+  double* part;    // [0]: sum of the lists so far; then one per CTA
+  float* norm;
+  int32_t first, last;
+  uint32_t* ctrl;
+};
+template <bool kG32>
+__global__ void __launch_bounds__(kAdamThreads) grad_norm_kernel(const __grid_constant__ TensorList l,
+                                                                 const __grid_constant__ NormArgs a) {
+  typedef typename std::conditional<kG32, float, uint16_t>::type TG;
+  __shared__ double buf[kAdamThreads / 32];
+  __shared__ bool last;
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kAdamThreads / 32);
+  int64_t b = static_cast<int64_t>(blockIdx.x) * (kAdamThreads / 32) + (threadIdx.x >> 5);
+  double total = 0.0;
+  if (b < l.blocks) {
+    int i = tensor_of(l, b);
+    float sum = 0.f;
+    for (int turn = 0; b < l.blocks; b += warps) {
+      while (i + 1 < l.count && l.t[i + 1].first <= b) ++i;
+      const TensorRef& t = l.t[i];
+      const int64_t at = (b - t.first) * kBlock, left = t.n - at;
+      const int n = left < kBlock ? static_cast<int>(left) : kBlock;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int e = q * 128 + lane * 4;
+        float g[4];
+        load4(static_cast<const TG*>(t.grad) + at + e, n - e, g);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum = fmaf(g[k], g[k], sum);
+      }
+      if (++turn == 64) {  // at most 512 squares in a row in fp32
+        total += sum;
+        sum = 0.f;
+        turn = 0;
+      }
+    }
+    total += sum;
+  }
+  total = block_sum(total, buf);
+  if (threadIdx.x == 0) {
+    a.part[1 + blockIdx.x] = total;
+    __threadfence();
+    last = atomicInc(a.ctrl + kCtrlDone, gridDim.x - 1) == gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  total = 0.0;
+  for (unsigned i = threadIdx.x; i < gridDim.x; i += kAdamThreads) total += __ldcg(a.part + 1 + i);
+  __syncthreads();
+  total = block_sum(total, buf);
+  if (threadIdx.x == 0) {
+    if (!a.first) total += __ldcg(a.part);
+    a.part[0] = total;
+    if (a.last) a.norm[0] = static_cast<float>(sqrt(total));
+  }
+}
+
+struct UnpackList {
+  int64_t blocks;
+  int32_t count;
+  int32_t reserved;
+  struct Ref {
+    const uint8_t* m;
+    const uint8_t* v;
+    const float* m_scale;
+    const float* v_range;
+    void* m_out;
+    void* v_out;
+    int64_t n, first;
+  } t[kListTensors];
+};
+static_assert(sizeof(UnpackList) <= 32764, "kernel parameters");
+
+template <typename T>
+__global__ void __launch_bounds__(kAdamThreads) unpack_kernel(const __grid_constant__ UnpackList l) {
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kAdamThreads / 32);
+  for (int64_t b = static_cast<int64_t>(blockIdx.x) * (kAdamThreads / 32) + (threadIdx.x >> 5); b < l.blocks;
+       b += warps) {
+    int lo = 0, hi = l.count - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (l.t[mid].first <= b) lo = mid; else hi = mid - 1;
+    }
+    const UnpackList::Ref& t = l.t[lo];
+    const int64_t blk = b - t.first, at = blk * kBlock, left = t.n - at;
+    const int n = left < kBlock ? static_cast<int>(left) : kBlock;
+    const float scale = t.m_scale[blk];
+    const float2 r = reinterpret_cast<const float2*>(t.v_range)[blk];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int e = q * 128 + lane * 4, in = n - e;
+      float m[4], v[4];
+      from_e4m3(load4(t.m + at + e, in), m);
+      const uint32_t codes = load4(t.v + at + e, in);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        m[k] *= scale;
+        v[k] = level(codes >> (8 * k) & 0xFFu, r.x, r.y);
+      }
+      store4(static_cast<T*>(t.m_out) + at + e, in, m);
+      store4(static_cast<T*>(t.v_out) + at + e, in, v);
+    }
+  }
+}
+
+typedef void (*StepKernel)(TensorList, StepArgs, bool);
+template <bool kP32, bool kMast>
+StepKernel step_kernel_of(int kind) {
+  if (kind & kGrad32)
+    return kind & kStates8 ? adamw_kernel<kP32, true, kMast, true> : adamw_kernel<kP32, true, kMast, false>;
+  return kind & kStates8 ? adamw_kernel<kP32, false, kMast, true> : adamw_kernel<kP32, false, kMast, false>;
+}
+StepKernel step_kernel(int kind) {
+  if (kind & kParam32) return step_kernel_of<true, false>(kind);
+  return kind & kMaster ? step_kernel_of<false, true>(kind) : step_kernel_of<false, false>(kind);
+}
+
+constexpr int kCtasPerSm = 4;
+int grid_for(fo_ctx* ctx, int64_t blocks) {
+  const int64_t ctas = (blocks + kAdamThreads / 32 - 1) / (kAdamThreads / 32);
+  const int64_t most = static_cast<int64_t>(host_num_sms(ctx)) * kCtasPerSm;
+  return static_cast<int>(ctas < most ? ctas : most);
+}
+
+int64_t blocks_of(int64_t n) { return (n + kBlock - 1) / kBlock; }
+
+fo_status check_ptr(const void* p, const char* what, int i, int align = 16) {
+  if (!p) return host_failf(FO_ERR_INVALID_ARG, "%s[%d]: null pointer", what, i);
+  if (reinterpret_cast<uintptr_t>(p) % align != 0)
+    return host_failf(FO_ERR_UNSUPPORTED, "%s[%d]: pointer not %d-byte aligned", what, i, align);
+  return FO_OK;
+}
+
+struct Span {
+  uintptr_t lo, hi;
+  int tensor;
+  const char* what;
+  bool written;
+};
+
+}  // namespace
+}  // namespace fo
+
+using namespace fo;
+
+struct fo_adamw_group {
+  std::vector<TensorList> lists;       // by kind
+  std::vector<fo_adamw_tensor> tensors;
+};
+
+extern "C" {
+
+fo_status fo_adamw_group_create(const fo_adamw_tensor* tensors, int count, fo_adamw_group** out) try {
+  if (!out) return host_fail(FO_ERR_INVALID_ARG, "null out pointer");
+  *out = nullptr;
+  if (count < 0 || (count > 0 && !tensors)) return host_fail(FO_ERR_INVALID_ARG, "null tensor array");
+  std::vector<Span> spans;
+  for (int i = 0; i < count; ++i) {
+    const fo_adamw_tensor& t = tensors[i];
+    if (t.n < 0) return host_failf(FO_ERR_SHAPE, "tensor %d: negative size", i);
+    if (t.n > (1ll << 39)) return host_failf(FO_ERR_UNSUPPORTED, "tensor %d: more than 2^39 elements", i);
+    if (t.param_dtype != FO_BF16 && t.param_dtype != FO_F32)
+      return host_failf(FO_ERR_INVALID_ARG, "param[%d]: unknown dtype", i);
+    if (t.grad_dtype != FO_BF16 && t.grad_dtype != FO_F32)
+      return host_failf(FO_ERR_INVALID_ARG, "grad[%d]: unknown dtype", i);
+    if (t.master && t.param_dtype == FO_F32)
+      return host_failf(FO_ERR_INVALID_ARG, "master[%d]: an fp32 parameter has none", i);
+    if ((t.m_scale != nullptr) != (t.v_range != nullptr))
+      return host_failf(FO_ERR_INVALID_ARG, "tensor %d: m_scale and v_range go together", i);
+    if (t.n == 0) continue;
+    const bool eight = t.m_scale != nullptr;
+    FO_TRY_HOST(check_ptr(t.param, "param", i));
+    FO_TRY_HOST(check_ptr(t.grad, "grad", i));
+    if (t.master) FO_TRY_HOST(check_ptr(t.master, "master", i));
+    FO_TRY_HOST(check_ptr(t.m, "m", i));
+    FO_TRY_HOST(check_ptr(t.v, "v", i));
+    if (eight) {
+      FO_TRY_HOST(check_ptr(t.m_scale, "m_scale", i, 4));
+      FO_TRY_HOST(check_ptr(t.v_range, "v_range", i, 8));
+    }
+    auto add = [&](const void* p, int64_t bytes, const char* what, bool written) {
+      const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+      if (p) spans.push_back(Span{lo, lo + static_cast<uintptr_t>(bytes), i, what, written});
+    };
+    const int64_t state = eight ? t.n : 4 * t.n;
+    add(t.param, t.n * (t.param_dtype == FO_F32 ? 4 : 2), "param", true);
+    add(t.grad, t.n * (t.grad_dtype == FO_F32 ? 4 : 2), "grad", false);
+    add(t.master, 4 * t.n, "master", true);
+    add(t.m, state, "m", true);
+    add(t.v, state, "v", true);
+    add(t.m_scale, 4 * blocks_of(t.n), "m_scale", true);
+    add(t.v_range, 8 * blocks_of(t.n), "v_range", true);
+  }
+  std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
+  // the written span and the span of any kind that reach furthest so far
+  const Span* reach = nullptr;
+  const Span* written = nullptr;
+  for (const Span& x : spans) {
+    const Span* hit = x.written ? reach : written;
+    if (hit && hit->hi > x.lo)
+      return host_failf(FO_ERR_INVALID_ARG, "%s[%d] overlaps %s[%d]", x.what, x.tensor, hit->what, hit->tensor);
+    if (!reach || x.hi > reach->hi) reach = &x;
+    if (x.written && (!written || x.hi > written->hi)) written = &x;
+  }
+  fo_adamw_group* g = new fo_adamw_group();
+  try {
+    g->tensors.assign(tensors, tensors + count);
+    for (int kind = 0; kind < 16; ++kind) {
+      int open = -1;  // list that takes the kind's next tensor
+      for (int i = 0; i < count; ++i) {
+        const fo_adamw_tensor& t = tensors[i];
+        const int k = (t.param_dtype == FO_F32 ? kParam32 : 0) | (t.grad_dtype == FO_F32 ? kGrad32 : 0) |
+                      (t.master ? kMaster : 0) | (t.m_scale ? kStates8 : 0);
+        if (k != kind || t.n == 0) continue;
+        if (open < 0 || g->lists[open].count == kListTensors) {
+          g->lists.emplace_back();
+          open = static_cast<int>(g->lists.size()) - 1;
+          std::memset(&g->lists[open], 0, sizeof(TensorList));
+          g->lists[open].kind = kind;
+        }
+        TensorList& l = g->lists[open];
+        l.t[l.count++] = TensorRef{t.param, t.grad, t.master, t.m, t.v, t.m_scale, t.v_range, t.n, l.blocks,
+                                   static_cast<uint32_t>(i), 0};
+        l.blocks += blocks_of(t.n);
+      }
+    }
+  } catch (...) {
+    delete g;
+    throw;
+  }
+  *out = g;
+  return FO_OK;
+} catch (...) {
+  return host_fail(FO_ERR_OOM, "out of host memory");
+}
+
+fo_status fo_adamw_group_destroy(fo_adamw_group* group) {
+  delete group;
+  return FO_OK;
+}
+
+fo_status fo_grad_norm(fo_ctx* ctx, const fo_adamw_group* group, float* norm, void* stream) {
+  if (!group) return host_fail(FO_ERR_INVALID_ARG, "null group");
+  FO_TRY_HOST(check_ptr(norm, "norm", 0, 4));
+  FO_TRY_HOST(host_check_ctx(ctx, 1));
+  DeviceGuard dev(host_device(ctx));
+  if (!dev.ok) return host_fail(FO_ERR_CUDA, "cudaSetDevice failed");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (group->lists.empty()) {
+    const cudaError_t e = cudaMemsetAsync(norm, 0, sizeof(float), s);
+    return e == cudaSuccess ? FO_OK : host_fail(FO_ERR_CUDA, cudaGetErrorString(e));
+  }
+  void* part = nullptr;
+  FO_TRY_HOST(host_buffer_kept(ctx, kSlotGradNorm, (1 + static_cast<size_t>(host_num_sms(ctx)) * kCtasPerSm) * 8, s,
+                               &part));
+  NormArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.part = static_cast<double*>(part);
+  a.norm = norm;
+  a.ctrl = host_ctrl(ctx);
+  for (size_t i = 0; i < group->lists.size(); ++i) {
+    const TensorList& l = group->lists[i];
+    a.first = i == 0;
+    a.last = i + 1 == group->lists.size();
+    const int grid = grid_for(ctx, l.blocks);
+    if (l.kind & kGrad32) {
+      grad_norm_kernel<true><<<grid, kAdamThreads, 0, s>>>(l, a);
+    } else {
+      grad_norm_kernel<false><<<grid, kAdamThreads, 0, s>>>(l, a);
+    }
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return host_fail(FO_ERR_CUDA, cudaGetErrorString(e));
+  }
+  return FO_OK;
+}
+
+fo_status fo_adamw_step(fo_ctx* ctx, const fo_adamw_group* group, const fo_adamw_params* prm, void* stream) {
+  if (!group) return host_fail(FO_ERR_INVALID_ARG, "null group");
+  if (!prm) return host_fail(FO_ERR_INVALID_ARG, "null parameters");
+  if (!(prm->beta1 >= 0.0 && prm->beta1 < 1.0 && prm->beta2 >= 0.0 && prm->beta2 < 1.0))
+    return host_fail(FO_ERR_INVALID_ARG, "beta1 and beta2 must be from 0 to below 1");
+  if (!(prm->eps >= 0.f) || !std::isfinite(prm->eps))
+    return host_fail(FO_ERR_INVALID_ARG, "eps must be finite and not negative");
+  if ((!prm->lr_dev && !std::isfinite(prm->lr)) || !std::isfinite(prm->weight_decay) ||
+      !std::isfinite(prm->grad_scale) || !std::isfinite(prm->max_norm))
+    return host_fail(FO_ERR_INVALID_ARG, "lr, weight_decay, grad_scale and max_norm must be finite");
+  if (!prm->step_dev && prm->step < 1)
+    return host_failf(FO_ERR_INVALID_ARG, "step=%lld: the first is 1", (long long)prm->step);
+  if (prm->max_norm > 0.f && !prm->norm) return host_fail(FO_ERR_INVALID_ARG, "max_norm needs norm");
+  if (prm->stochastic != 0 && prm->stochastic != 1) return host_fail(FO_ERR_INVALID_ARG, "stochastic must be 0 or 1");
+  if (prm->lr_dev) FO_TRY_HOST(check_ptr(prm->lr_dev, "lr_dev", 0, 4));
+  if (prm->step_dev) FO_TRY_HOST(check_ptr(prm->step_dev, "step_dev", 0, 4));
+  if (prm->norm) FO_TRY_HOST(check_ptr(prm->norm, "norm", 0, 4));
+  FO_TRY_HOST(host_check_ctx(ctx, 1));
+  DeviceGuard dev(host_device(ctx));
+  if (!dev.ok) return host_fail(FO_ERR_CUDA, "cudaSetDevice failed");
+  StepArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.lr = prm->lr;
+  a.exact1 = prm->beta1;
+  a.exact2 = prm->beta2;
+  a.beta1 = static_cast<float>(prm->beta1);
+  a.beta2 = static_cast<float>(prm->beta2);
+  a.rest1 = static_cast<float>(1.0 - prm->beta1);
+  a.rest2 = static_cast<float>(1.0 - prm->beta2);
+  a.eps = prm->eps;
+  a.weight_decay = prm->weight_decay;
+  a.grad_scale = prm->grad_scale;
+  a.max_norm = prm->max_norm;
+  a.step = prm->step;
+  if (!prm->step_dev) {
+    const double t = static_cast<double>(prm->step);
+    a.fix1 = static_cast<float>(1.0 / (1.0 - std::pow(prm->beta1, t)));
+    a.fix2 = static_cast<float>(1.0 / (1.0 - std::pow(prm->beta2, t)));
+  }
+  a.seed_low = static_cast<uint32_t>(prm->seed);
+  a.seed_high = static_cast<uint32_t>(prm->seed >> 32);
+  a.lr_dev = prm->lr_dev;
+  a.step_dev = prm->step_dev;
+  a.norm = prm->norm;
+  a.ctrl = host_ctrl(ctx);
+  for (const TensorList& l : group->lists) {
+    step_kernel(l.kind)<<<grid_for(ctx, l.blocks), kAdamThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+        l, a, prm->stochastic && !(l.kind & (kParam32 | kMaster)));
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return host_fail(FO_ERR_CUDA, cudaGetErrorString(e));
+  }
+  return FO_OK;
+}
+
+fo_status fo_adamw_unpack(fo_ctx* ctx, const fo_adamw_group* group, void* const* m, void* const* v, int dtype,
+                          void* stream) {
+  if (!group) return host_fail(FO_ERR_INVALID_ARG, "null group");
+  if (dtype != FO_BF16 && dtype != FO_F32) return host_failf(FO_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+  const int count = static_cast<int>(group->tensors.size());
+  if (count > 0 && (!m || !v)) return host_fail(FO_ERR_INVALID_ARG, "null tensor array");
+  for (int i = 0; i < count; ++i) {
+    if (!group->tensors[i].m_scale || group->tensors[i].n == 0) continue;
+    FO_TRY_HOST(check_ptr(m[i], "m", i));
+    FO_TRY_HOST(check_ptr(v[i], "v", i));
+  }
+  FO_TRY_HOST(host_check_ctx(ctx, 1));
+  DeviceGuard dev(host_device(ctx));
+  if (!dev.ok) return host_fail(FO_ERR_CUDA, "cudaSetDevice failed");
+  UnpackList l;
+  for (int i = 0; i < count;) {
+    std::memset(&l, 0, sizeof(l));
+    for (; i < count && l.count < kListTensors; ++i) {
+      const fo_adamw_tensor& t = group->tensors[i];
+      if (!t.m_scale || t.n == 0) continue;
+      l.t[l.count++] = UnpackList::Ref{static_cast<const uint8_t*>(t.m), static_cast<const uint8_t*>(t.v), t.m_scale,
+                                       t.v_range, m[i], v[i], t.n, l.blocks};
+      l.blocks += blocks_of(t.n);
+    }
+    if (l.count == 0) break;
+    const int grid = grid_for(ctx, l.blocks);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (dtype == FO_F32) {
+      unpack_kernel<float><<<grid, kAdamThreads, 0, s>>>(l);
+    } else {
+      unpack_kernel<uint16_t><<<grid, kAdamThreads, 0, s>>>(l);
+    }
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return host_fail(FO_ERR_CUDA, cudaGetErrorString(e));
+  }
+  return FO_OK;
+}
+
+}  // extern "C"

@@ -1723,6 +1723,11 @@ fo_status fo_ctx_poll(fo_ctx* ctx) {
   if (w[kCtrlError] == FO_ERR_RANGE && w[kCtrlWhere] == kSiteOffsets)
     return fail(FO_ERR_RANGE, "sequence offsets out of range (entry %u): they have to start at 0 or above, not "
                 "decrease and end at or below the row count; nothing was computed", w[kCtrlDetail]);
+  if (w[kCtrlError] == FO_ERR_RANGE && w[kCtrlWhere] == kSiteTargets)
+    return fail(FO_ERR_RANGE, "a target behind the vocabulary (row %u); its row was not counted", w[kCtrlDetail]);
+  if (w[kCtrlError] == FO_ERR_RANGE && w[kCtrlWhere] == kSiteStep)
+    return fail(FO_ERR_RANGE, "step %d read from memory: the first is 1; nothing was written",
+                static_cast<int>(w[kCtrlDetail]));
   if (w[kCtrlError] == FO_ERR_RANGE)
     return fail(FO_ERR_RANGE, "input value out of the kernels' range (site %u, row %u): |V| above 65504, "
                 "the largest finite fp16 value", w[kCtrlWhere], w[kCtrlDetail]);

@@ -174,6 +174,8 @@ enum CtrlWord : int {
   kCtrlTiles = 4,     // SM-pair GEMM: the next unclaimed tile of the running launch (zero
                       // between launches: the launch's last claim resets it)
   kCtrlItems = 5,     // attention: the next unclaimed item of the running launch (likewise)
+  kCtrlDone = 6,      // losses, gradient norm: CTAs of the running launch that are done (zero
+                      // between launches: the last one's count wraps)
   kCtrlWords = 8
 };
 
@@ -181,7 +183,8 @@ enum WaitSite : uint32_t {
   kSiteAgFlag = 1, kSiteFull = 2, kSiteEmpty = 3, kSiteTmemFull = 4,
   kSiteTmemEmpty = 5, kSiteAccInFlag = 6, kSiteDrain = 7, kSiteAttnFlag = 8,
   kSiteAttnBar = 9, kSiteVRange = 10, kSiteRowsReady = 11, kSiteBounds = 12,
-  kSiteSched = 13, kSiteOffsets = 14
+  kSiteSched = 13, kSiteOffsets = 14, kSiteTargets = 15,
+  kSiteStep = 16
 };
 
 // host launchers (fo_gemm.cu: single-SM 128x256 tiles; fo_gemm2.cu: SM-pair 256x256 tiles)

@@ -1,0 +1,85 @@
+// Losses from the logits of a column-parallel output projection, and their gradients.
+//
+// A row of logits lies in P matrices, each rank's columns of the vocabulary.  With z = scale times
+// the logits and m = max z, all in fp32:
+//   d_j = z_j - m,  s = sum exp d,  logp = d_y - log s,  lse = m + log s,
+//   H = log s - (sum exp(d) d) / s,   p_j = exp(d_j) / s,
+//   d logp / dz_j = 1[j = y] - p_j,   d H / dz_j = -p_j (d_j - log s + H).
+// A loss enters a row's gradient through two numbers, a = dL/dlogp and h = dL/dH:
+//   dz_j = a 1[j = y] - p_j (a + h (d_j - log s + H)).
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "fo_attn_common.cuh"
+#include "fo_internal.h"
+#include "fo_ptx.cuh"
+
+namespace fo {
+
+constexpr int kLossThreads = 512;
+
+enum LossMode : int {
+  kLossForward = 0,   // statistics alone
+  kLossPolicy = 1,    // statistics, the policy loss, and (d[0] given) the gradient
+  kLossBackward = 2   // the gradient, from statistics given
+};
+
+struct LossArgs {
+  const void* z[kMaxP];
+  void* d[kMaxP];             // d[0] null: no gradient
+  int64_t ldz[kMaxP], ldd[kMaxP];
+  int32_t cols[kMaxP];
+  int32_t first[kMaxP + 1];   // vocabulary ids: rank r has first[r] .. first[r + 1]
+  int32_t P;
+  int64_t rows;
+  float scale;
+  const int32_t* targets;
+  float* logp;                // outputs, each may be null
+  float* lse;
+  float* entropy;
+  float4* stat;               // (m, log s, d_y, -) of every row: what the preference loss keeps
+  const float* in_lse;        // backward: statistics given (or stat)
+  const float* in_entropy;
+  const float* dlogp;         // a of every row (or coef, by sequence)
+  const float* dentropy;      // h
+  const float* old_logp;      // policy
+  const float* advantages;
+  const float* ref_logp;
+  const float* weights;
+  float ratio_lo, ratio_hi, kl_coef, entropy_coef;
+  int32_t mean;
+  float* stats;
+  double* part;               // [grid][4] sums of stats
+  const int32_t* offsets;     // packed sequences: rows offsets[0] .. offsets[2 pairs] take part
+  int32_t pairs;
+  const float* coef;          // a of every sequence's counted rows
+  uint32_t* ctrl;
+};
+
+// The pairs' scores, losses and coefficients from the rows' log-probabilities
+struct PairArgs {
+  const int32_t* offsets;
+  const int32_t* targets;
+  int64_t rows;
+  int32_t pairs, vocab, kind, average;
+  const float4* stat;
+  const float* ref_logp;
+  float beta, smoothing, margin;
+  float* coef;                // [2 pairs]
+  float* pair_loss;           // [pairs]
+  float* margins;
+  float* loss;
+  uint32_t* ctrl;
+};
+
+struct LossKind {
+  bool z32, d32;   // types of logits and gradients
+  int mode;
+  bool entropy;    // the entropy is wanted or has a gradient
+};
+// fo_loss_rows.cu
+cudaError_t loss_rows_launch(const LossArgs& a, const LossKind& k, int num_sms, cudaStream_t s);
+int loss_rows_parts(int num_sms);   // rows of LossArgs::part that any launch may use
+
+}  // namespace fo
