@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constan
       const int32_t y = a.targets[i];
       if (y < 0 || y >= a.vocab) continue;
       const float4 st = a.stat[i];
-      sum += (static_cast<double>(st.z) - st.y) - (a.ref_logp ? a.ref_logp[i] : 0.f);
+      sum += (static_cast<double>(st.z) - st.y) * 0.69314718055994531 - (a.ref_logp ? a.ref_logp[i] : 0.f);
       ++n;
     }
     const double count = block_sum(n, buf);
@@ -153,6 +153,9 @@ fo_status check_logits(const fo_mat* logits, int P, const fo_mat* d, const int32
   a->rows = logits[0].rows;
   a->scale = scale;
   a->targets = targets;
+  fo_opts o;
+  std::memset(&o, 0, sizeof(o));
+  a->timeout_ns = host_timeout_ns(o);
   k->z32 = logits[0].dtype == FO_F32;
   k->d32 = d && d[0].dtype == FO_F32;
   return check_vec(targets, a->rows, true, "targets");
@@ -277,7 +280,7 @@ fo_status fo_policy_loss(fo_ctx* ctx, const fo_mat* logits, int P, const int32_t
   a.part = static_cast<double*>(part);
   a.ctrl = host_ctrl(ctx);
   k.mode = kLossPolicy;
-  k.entropy = true;
+  k.entropy = prm->entropy_coef != 0.f;
   return run_rows(ctx, a, k, s);
 }
 
@@ -351,6 +354,7 @@ fo_status fo_preference_loss(fo_ctx* ctx, const fo_mat* logits, int P, const int
   if (e != cudaSuccess) return host_fail(FO_ERR_CUDA, cudaGetErrorString(e));
   if (!dlogits) return FO_OK;
   back.coef = p.coef;
+  back.backwards = 1;  // the rows that were read last may still be in L2
   k.mode = kLossBackward;
   return run_rows(ctx, back, k, s);
 }

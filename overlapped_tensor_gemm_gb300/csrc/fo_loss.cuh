@@ -17,7 +17,12 @@
 
 namespace fo {
 
-constexpr int kLossThreads = 512;
+constexpr int kLossWarps = 16;                          // warps that compute
+constexpr int kLossThreads = 32 * (kLossWarps + 1);     // and one that orders the copies
+constexpr int kLossChunk = 16384;                       // bytes of a copy
+constexpr int kLossSlots = 13;                          // chunks in shared memory
+constexpr int kLossSmem = kLossSlots * kLossChunk;
+constexpr int kLossMaxCtas = 8;                         // CTAs of one row
 
 enum LossMode : int {
   kLossForward = 0,   // statistics alone
@@ -31,6 +36,10 @@ struct LossArgs {
   int64_t ldz[kMaxP], ldd[kMaxP];
   int32_t cols[kMaxP];
   int32_t first[kMaxP + 1];   // vocabulary ids: rank r has first[r] .. first[r + 1]
+  int32_t groups[kMaxP + 1];  // the whole 16-byte groups of columns: rank r has groups[r] .. groups[r + 1]
+  int32_t ctas;               // CTAs of one row: each takes a range of the groups
+  int32_t twice;              // a CTA's range does not fit: it is copied again for the gradient
+  int32_t backwards;          // rows from the last one on
   int32_t P;
   int64_t rows;
   float scale;
@@ -38,7 +47,7 @@ struct LossArgs {
   float* logp;                // outputs, each may be null
   float* lse;
   float* entropy;
-  float4* stat;               // (m, log s, d_y, -) of every row: what the preference loss keeps
+  float4* stat;               // (m, log2 s, d_y log2 e, -) of every row: what the preference loss keeps
   const float* in_lse;        // backward: statistics given (or stat)
   const float* in_entropy;
   const float* dlogp;         // a of every row (or coef, by sequence)
@@ -54,6 +63,7 @@ struct LossArgs {
   const int32_t* offsets;     // packed sequences: rows offsets[0] .. offsets[2 pairs] take part
   int32_t pairs;
   const float* coef;          // a of every sequence's counted rows
+  uint64_t timeout_ns;
   uint32_t* ctrl;
 };
 
@@ -79,7 +89,7 @@ struct LossKind {
   bool entropy;    // the entropy is wanted or has a gradient
 };
 // fo_loss_rows.cu
-cudaError_t loss_rows_launch(const LossArgs& a, const LossKind& k, int num_sms, cudaStream_t s);
+cudaError_t loss_rows_launch(LossArgs a, const LossKind& k, int num_sms, cudaStream_t s);
 int loss_rows_parts(int num_sms);   // rows of LossArgs::part that any launch may use
 
 }  // namespace fo
