@@ -3,7 +3,7 @@
 // Bound by HBM: the logits are read once (the gradient of a policy loss waits for its row's sum, and
 // the row waits in shared memory), the gradients written once.  A row belongs to a cluster of 1 to 8
 // CTAs, each with a range of its columns that fits shared memory beside the copies under way for the
-// next rows.  One warp orders the copies (cp.async.bulk, 16 KB each, into a ring of slots); sixteen
+// next rows.  One warp orders the copies (cp.async.bulk, 32 KB each, into a ring of slots); sixteen
 // warps walk a row's slots twice: for the row's statistics, then for its gradient, after which a slot
 // takes a chunk of a later row.  Between the walks every warp tells every CTA of the row its part of
 // the statistics (stores into their shared memory and an arrival at their barrier): one exchange a
@@ -25,7 +25,8 @@ constexpr float kOctaves = 16.f;  // a sum's reference may lie so far below its 
 // 2^d is 0 in fp32 from here on down: where d multiplies it, d ends here (0 times -infinity)
 constexpr float kFarBelow = -160.f;
 constexpr int kChunkGroups = kLossChunk / 16;
-constexpr int kLossFit = 8;  // a row's chunks in one CTA, where more CTAs can share it
+constexpr int kLossFit = 4;  // a row's chunks in one CTA, where more CTAs can share it
+constexpr int kBatch = kChunkGroups / (32 * kLossWarps);  // groups of a chunk per thread
 constexpr uint64_t kLossDrainNs = 2000000000ull;
 
 typedef uint64_t Pair;
@@ -62,8 +63,13 @@ struct Group;
 template <>
 struct Group<uint16_t> {
   static constexpr int kCols = 8;
-  static __device__ __forceinline__ float top(const uint4& q) {
-    const uint32_t m = max_bf16x2(max_bf16x2(q.x, q.y), max_bf16x2(q.z, q.w));
+  // the largest of n groups
+  template <int n>
+  static __device__ __forceinline__ float top(const uint4 (&q)[n]) {
+    uint32_t m = max_bf16x2(max_bf16x2(q[0].x, q[0].y), max_bf16x2(q[0].z, q[0].w));
+#pragma unroll
+    for (int k = 1; k < n; ++k)
+      m = max_bf16x2(m, max_bf16x2(max_bf16x2(q[k].x, q[k].y), max_bf16x2(q[k].z, q[k].w)));
     return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
   }
   static __device__ __forceinline__ void pairs(const uint4& q, Pair (&v)[4]) {
@@ -75,8 +81,14 @@ struct Group<uint16_t> {
 template <>
 struct Group<float> {
   static constexpr int kCols = 4;
-  static __device__ __forceinline__ float top(const uint4& q) {
-    return fmaxf(fmaxf(__uint_as_float(q.x), __uint_as_float(q.y)), fmaxf(__uint_as_float(q.z), __uint_as_float(q.w)));
+  template <int n>
+  static __device__ __forceinline__ float top(const uint4 (&q)[n]) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < n; ++k)
+      m = fmax3(fmax3(m, __uint_as_float(q[k].x), __uint_as_float(q[k].y)), __uint_as_float(q[k].z),
+                __uint_as_float(q[k].w));
+    return m;
   }
   static __device__ __forceinline__ void pairs(const uint4& q, Pair (&v)[2]) {
     v[0] = pack2(__uint_as_float(q.x), __uint_as_float(q.y));
@@ -145,6 +157,75 @@ __device__ __forceinline__ Part merge(const Part& v, const Part& w, float c) {
   r.z_y = v.z_y + w.z_y;
   return r;
 }
+
+// A thread's sums over a row: s and t relative to m, two columns side by side
+struct Sums {
+  float m;
+  Pair s, t;
+};
+// n groups into the sums
+template <typename TZ, bool kEnt, int n>
+__device__ __forceinline__ void add_groups(const uint4 (&q)[n], float c, float slack, Sums& v) {
+  constexpr int kPairs = Group<TZ>::kCols / 2;
+  const float top = Group<TZ>::top(q);
+  if (top > v.m + slack) {
+    const float d = (base_of(v.m) - base_of(top)) * c;
+    const Pair f = both(fast_exp2(d));
+    if (kEnt) v.t = mul2(f, ffma2(v.s, both(fmaxf(d, kFarBelow)), v.t));
+    v.s = mul2(f, v.s);
+    v.m = top;
+  }
+  const Pair base = both(-base_of(v.m)), c2 = both(c);
+#pragma unroll
+  for (int k = 0; k < n; ++k) {
+    Pair x[kPairs];
+    Group<TZ>::pairs(q[k], x);
+#pragma unroll
+    for (int e = 0; e < kPairs; ++e) {
+      float lo, hi;
+      unpack2(mul2(fadd2(x[e], base), c2), lo, hi);
+      const Pair w = pack2(fast_exp2(lo), fast_exp2(hi));
+      v.s = fadd2(v.s, w);
+      if (kEnt) v.t = ffma2(w, pack2(fmaxf(lo, kFarBelow), fmaxf(hi, kFarBelow)), v.t);
+    }
+  }
+}
+
+// How a row's gradient is made: 2^d (k0 + k1 d) with d = (z - base) c
+struct Slope {
+  float base, c, k0, k1;
+};
+template <bool kEnt>
+__device__ __forceinline__ float slope_at(const Slope& g, float z) {
+  const float d = (z - g.base) * g.c;
+  return fast_exp2(d) * (kEnt ? fmaf(fmaxf(d, kFarBelow), g.k1, g.k0) : g.k0);
+}
+template <typename TZ, typename TD, bool kEnt>
+__device__ __forceinline__ void put_group(const uint4& q, const Slope& g, TD* to) {
+  constexpr int kPairs = Group<TZ>::kCols / 2;
+  const Pair nbase = both(-g.base), c2 = both(g.c), k0 = both(g.k0), k1 = both(g.k1);
+  Pair x[kPairs];
+  Group<TZ>::pairs(q, x);
+#pragma unroll
+  for (int e = 0; e < kPairs; ++e) {
+    float lo, hi;
+    unpack2(mul2(fadd2(x[e], nbase), c2), lo, hi);
+    const Pair w = pack2(fast_exp2(lo), fast_exp2(hi));
+    x[e] = kEnt ? mul2(w, ffma2(pack2(fmaxf(lo, kFarBelow), fmaxf(hi, kFarBelow)), k1, k0)) : mul2(w, k0);
+  }
+  store_group<kPairs>(to, x);
+}
+
+// A place in the ring that advances chunk by chunk
+struct Place {
+  uint32_t slot = 0, turn = 0;  // turn: parity of the slot's use
+  __device__ __forceinline__ void next() {
+    if (++slot == kLossSlots) {
+      slot = 0;
+      turn ^= 1;
+    }
+  }
+};
 
 __device__ __forceinline__ bool offsets_fine(const int32_t* off, int n, int64_t rows, uint32_t* ctrl) {
   int bad = -1;
@@ -302,7 +383,6 @@ __global__ void __launch_bounds__(kLossThreads, 1) loss_rows_kernel(const __grid
       mbar_wait_drain(&sm.full[k % kLossSlots], (k / kLossSlots) & 1, kLossDrainNs);
   } else {
     const float c = static_cast<float>(a.scale * kLog2e);
-    const Pair c2 = both(c);
     const float slack = kOctaves / c;
     float per_weight = 1.f;
     if (kMode == kLossPolicy && a.mean) {
@@ -319,7 +399,8 @@ __global__ void __launch_bounds__(kLossThreads, 1) loss_rows_kernel(const __grid
     double sums[4] = {0.0, 0.0, 0.0, 0.0};  // thread 0 of a row's first CTA: stats
     RowIn r = {-1, false};
     float in0 = 0.f, in1 = 0.f, in2 = 0.f, in3 = 0.f;
-    uint32_t count = 0, told = 0;
+    uint32_t told = 0;
+    Place place;
     bool fine = true;
     for (int64_t n = 0; n < mine; ++n) {
       const int64_t i = row_at(n);
@@ -383,64 +464,37 @@ __global__ void __launch_bounds__(kLossThreads, 1) loss_rows_kernel(const __grid
 
       // first walk: the row's statistics
       Part v;
-      const uint32_t count0 = count;
+      const Place start = place;
       if (kStat) {
-        v = Part{z_t, 0.f, 0.f, 0.f};
-        Pair s2 = 0, t2 = 0;
-        if (t_col >= 0) {
-          v.s = fast_exp2((z_t - base_of(z_t)) * c);
-          if (y_here) v.z_y = z_t;
-        }
-        for (int k = 0; k < chunks; ++k, ++count) {
-          const uint32_t slot = count % kLossSlots;
-          if (!wait_full(&sm.full[slot], (count / kLossSlots) & 1, a)) {
+        v = Part{z_t, t_col >= 0 ? fast_exp2((z_t - base_of(z_t)) * c) : 0.f, 0.f, y_here ? z_t : 0.f};
+        Sums sums2 = {-INFINITY, 0, 0};
+        for (int k = 0; k < chunks; ++k, place.next()) {
+          if (!wait_full(&sm.full[place.slot], place.turn, a)) {
             fine = false;
             break;
           }
           const int g0 = g_lo + k * kChunkGroups, left = g_hi - g0;
-          const uint4* src = reinterpret_cast<const uint4*>(ring + slot * kLossChunk);
+          const uint4* src = reinterpret_cast<const uint4*>(ring + place.slot * kLossChunk) + tid;
+          if (left >= kChunkGroups) {
+            uint4 q[kBatch];
 #pragma unroll
-          for (int j = 0; j < kChunkGroups / (32 * kLossWarps); ++j) {
-            const int g = j * 32 * kLossWarps + tid;
-            if (g >= left) break;
-            const uint4 q = src[g];
-            const float top = Group<TZ>::top(q);
-            if (top > v.m + slack) {
-              const float step = (base_of(v.m) - base_of(top)) * c, f = fast_exp2(step);
-              if (kStatEnt) t2 = mul2(both(f), ffma2(s2, both(fmaxf(step, kFarBelow)), t2));
-              s2 = mul2(both(f), s2);
-              if (kStatEnt) v.t = f * fmaf(v.s, fmaxf(step, kFarBelow), v.t);
-              v.s *= f;
-              v.m = top;
-            }
-            const Pair base = both(-base_of(v.m));
-            Pair x[kPairs];
-            Group<TZ>::pairs(q, x);
-            if (g0 + g == y_group) {
-#pragma unroll
-              for (int e = 0; e < kPairs; ++e) {
-                float lo, hi;
-                unpack2(x[e], lo, hi);
-                if (y_col % kCols == 2 * e) v.z_y = lo;
-                if (y_col % kCols == 2 * e + 1) v.z_y = hi;
-              }
-            }
-#pragma unroll
-            for (int e = 0; e < kPairs; ++e) {
-              float lo, hi;
-              unpack2(mul2(fadd2(x[e], base), c2), lo, hi);
-              const Pair w = pack2(fast_exp2(lo), fast_exp2(hi));
-              s2 = fadd2(s2, w);
-              if (kStatEnt) t2 = ffma2(w, pack2(fmaxf(lo, kFarBelow), fmaxf(hi, kFarBelow)), t2);
+            for (int j = 0; j < kBatch; ++j) q[j] = src[j * 32 * kLossWarps];
+            add_groups<TZ, kStatEnt>(q, c, slack, sums2);
+          } else {
+            for (int g = tid; g < left; g += 32 * kLossWarps) {
+              const uint4 q[1] = {src[g - tid]};
+              add_groups<TZ, kStatEnt>(q, c, slack, sums2);
             }
           }
+          const int at_y = y_group - g0;
+          if (at_y >= 0 && at_y < left && at_y < kChunkGroups && at_y % (32 * kLossWarps) == tid)
+            v.z_y = load1(reinterpret_cast<const TZ*>(src - tid + at_y) + y_col % kCols);
           if (!grad || twice) {
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.empty[slot]);
+            if (lane == 0) mbar_arrive(&sm.empty[place.slot]);
           }
         }
-        v.s += sum2(s2);
-        v.t += sum2(t2);
+        v = merge<kStatEnt>(v, Part{sums2.m, sum2(sums2.s), sum2(sums2.t), 0.f}, c);
         if (!fine) break;
         // every warp's part to every CTA of the row
         v = join<kStatEnt>(v, c);
@@ -519,49 +573,40 @@ __global__ void __launch_bounds__(kLossThreads, 1) loss_rows_kernel(const __grid
       const float inv = exp2f(-log_s);
       const float k0 = -a.scale * inv * (kEnt ? da + dh * (entropy - kLn2 * log_s) : da);
       const float k1 = -a.scale * inv * dh * kLn2;
-      const Pair nbase = both(-base), k02 = both(k0), k12 = both(k1);
-      if (t_col >= 0) {
-        const float d = (z_t - base) * c;
-        float x = fast_exp2(d) * (kEnt ? fmaf(fmaxf(d, kFarBelow), k1, k0) : k0);
-        if (y_here) x += own;
-        store1(static_cast<TD*>(a.d[t_rk]) + i * a.ldd[t_rk] + t_col, x);
-      }
+      const Slope slope = {base, c, k0, k1};
+      if (t_col >= 0)
+        store1(static_cast<TD*>(a.d[t_rk]) + i * a.ldd[t_rk] + t_col, slope_at<kEnt>(slope, z_t) + (y_here ? own : 0.f));
+      if (kStat && !twice) place = start;
       int rk = 0;
-      uint32_t at_chunk = kStat && !twice ? count0 : count;
-      for (int k = 0; k < chunks; ++k, ++at_chunk) {
-        const uint32_t slot = at_chunk % kLossSlots;
-        if ((!kStat || twice) && !wait_full(&sm.full[slot], (at_chunk / kLossSlots) & 1, a)) {
+      for (int k = 0; k < chunks; ++k, place.next()) {
+        if ((!kStat || twice) && !wait_full(&sm.full[place.slot], place.turn, a)) {
           fine = false;
           break;
         }
         const int g0 = g_lo + k * kChunkGroups, left = g_hi - g0;
-        const uint4* src = reinterpret_cast<const uint4*>(ring + slot * kLossChunk);
+        while (g0 >= a.groups[rk + 1]) ++rk;
+        const uint4* src = reinterpret_cast<const uint4*>(ring + place.slot * kLossChunk) + tid;
+        if (left >= kChunkGroups && g0 + kChunkGroups <= a.groups[rk + 1]) {
+          TD* to = static_cast<TD*>(a.d[rk]) + i * a.ldd[rk] + static_cast<int64_t>(g0 + tid - a.groups[rk]) * kCols;
 #pragma unroll
-        for (int j = 0; j < kChunkGroups / (32 * kLossWarps); ++j) {
-          const int g = j * 32 * kLossWarps + tid;
-          if (g >= left) break;
-          Pair x[kPairs];
-          Group<TZ>::pairs(src[g], x);
-#pragma unroll
-          for (int e = 0; e < kPairs; ++e) {
-            float lo, hi;
-            unpack2(mul2(fadd2(x[e], nbase), c2), lo, hi);
-            const Pair w = pack2(fast_exp2(lo), fast_exp2(hi));
-            x[e] = kEnt ? mul2(w, ffma2(pack2(fmaxf(lo, kFarBelow), fmaxf(hi, kFarBelow)), k12, k02)) : mul2(w, k02);
+          for (int j = 0; j < kBatch; ++j)
+            put_group<TZ, TD, kEnt>(src[j * 32 * kLossWarps], slope, to + j * 32 * kLossWarps * kCols);
+        } else {
+          int r2 = rk;
+          for (int g = tid; g < left && g < kChunkGroups; g += 32 * kLossWarps) {
+            while (g0 + g >= a.groups[r2 + 1]) ++r2;
+            put_group<TZ, TD, kEnt>(src[g - tid], slope,
+                                    static_cast<TD*>(a.d[r2]) + i * a.ldd[r2] +
+                                        static_cast<int64_t>(g0 + g - a.groups[r2]) * kCols);
           }
-          if (g0 + g == y_group) {
-#pragma unroll
-            for (int e = 0; e < kPairs; ++e)
-              x[e] = fadd2(x[e], pack2(y_col % kCols == 2 * e ? own : 0.f, y_col % kCols == 2 * e + 1 ? own : 0.f));
-          }
-          while (g0 + g >= a.groups[rk + 1]) ++rk;
-          store_group<kPairs>(static_cast<TD*>(a.d[rk]) + i * a.ldd[rk] + static_cast<int64_t>(g0 + g - a.groups[rk]) * kCols,
-                              x);
         }
+        const int at_y = y_group - g0;  // the thread that wrote the target's group writes its column again
+        if (at_y >= 0 && at_y < left && at_y < kChunkGroups && at_y % (32 * kLossWarps) == tid)
+          store1(static_cast<TD*>(a.d[y_rk]) + i * a.ldd[y_rk] + y_col,
+                 slope_at<kEnt>(slope, load1(reinterpret_cast<const TZ*>(src - tid + at_y) + y_col % kCols)) + own);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.empty[slot]);
+        if (lane == 0) mbar_arrive(&sm.empty[place.slot]);
       }
-      if (!kStat || twice) count = at_chunk;
       if (!fine) break;
     }
     if (!fine && lane == 0) raise_error(a.ctrl, FO_ERR_TIMEOUT, kSiteFull, blockIdx.x);
