@@ -17,12 +17,8 @@
 
 namespace fo {
 
-constexpr int kLossWarps = 16;                          // warps that compute
-constexpr int kLossThreads = 32 * (kLossWarps + 1);     // and one that orders the copies
-constexpr int kLossChunk = 32768;                       // bytes of a copy: 4 vectors a thread
-constexpr int kLossSlots = 6;                           // chunks in shared memory
-constexpr int kLossSmem = kLossSlots * kLossChunk;
-constexpr int kLossMaxCtas = 8;                         // CTAs of one row
+constexpr int kLossChunk = 32768;   // bytes of a copy
+constexpr int kLossMaxCtas = 8;     // CTAs of one row
 
 enum LossMode : int {
   kLossForward = 0,   // statistics alone

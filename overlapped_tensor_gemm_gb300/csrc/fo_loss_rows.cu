@@ -1,13 +1,17 @@
 // Row kernels of the losses (formulas in fo_loss.cuh).
 //
-// Bound by HBM: the logits are read once (the gradient of a policy loss waits for its row's sum, and
-// the row waits in shared memory), the gradients written once.  A row belongs to a cluster of 1 to 8
-// CTAs, each with a range of its columns that fits shared memory beside the copies under way for the
-// next rows.  One warp orders the copies (cp.async.bulk, 32 KB each, into a ring of slots); sixteen
-// warps walk a row's slots twice: for the row's statistics, then for its gradient, after which a slot
-// takes a chunk of a later row.  Between the walks every warp tells every CTA of the row its part of
-// the statistics (stores into their shared memory and an arrival at their barrier): one exchange a
-// row, over which the copies go on.
+// Bound by HBM.  A row's columns are shared by a team of 1 to 8 CTAs.  One warp of a CTA orders the
+// copies of its columns (cp.async.bulk, 32 KB each, into a ring of slots in shared memory, rows
+// ahead); the others compute on them.
+//   Statistics: every warp sums what it sees of a row and tells its part to every CTA of the team;
+// one warp of each CTA, another one for each row, adds the parts.  Nobody waits for it but the
+// gradient.
+//   Policy loss with gradient: the row waits in shared memory for its sum, so that the logits are
+// read once, is turned into its gradient in place and copied from there (where both have one type).
+// Two sets of eight warps take the rows in turn, so that one's waits are covered by the other.
+//   Backward: the gradient alone, from statistics given.
+// Statistics alone and gradients alone run two CTAs on an SM, for the same reason; the policy loss
+// has one, for room.
 //
 // A thread sums relative to a column of its own that is near its maximum (at most 16 octaves below),
 // so that a new maximum does not cost a pass; log2 domain, two columns per instruction.
@@ -25,8 +29,23 @@ constexpr float kOctaves = 16.f;  // a sum's reference may lie so far below its 
 // 2^d is 0 in fp32 from here on down: where d multiplies it, d ends here (0 times -infinity)
 constexpr float kFarBelow = -160.f;
 constexpr int kChunkGroups = kLossChunk / 16;
-constexpr int kLossFit = 4;  // a row's chunks in one CTA, where more CTAs can share it
-constexpr int kBatch = kChunkGroups / (32 * kLossWarps);  // groups of a chunk per thread
+
+// How a kernel's CTA is made up
+template <int kMode>
+struct Shape {
+  static constexpr bool kOne = kMode == kLossPolicy;
+  static constexpr int kPerSm = kOne ? 1 : 2;
+  static constexpr int kSets = kOne ? 2 : 1;            // sets of warps that take the rows in turn
+  static constexpr int kWarps = 8;                      // warps of a set
+  static constexpr int kMore = kOne ? 2 : 1;            // warps that order the copies in, and the copies out
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kAll = kSets * kThreads;
+  static constexpr int kSlots = kOne ? 6 : 3;
+  static constexpr int kZeros = kOne ? 8192 : 0;        // bytes of zeros behind the ring
+  static constexpr int kBatch = kChunkGroups / kThreads;  // groups of a chunk per thread
+};
+constexpr int kLossFit = 2;   // a row's chunks in one CTA, where more CTAs can share it: both sets' rows and the
+                              // next one's copies have room
 constexpr uint64_t kLossDrainNs = 2000000000ull;
 
 typedef uint64_t Pair;
@@ -72,10 +91,15 @@ struct Group<uint16_t> {
       m = max_bf16x2(m, max_bf16x2(max_bf16x2(q[k].x, q[k].y), max_bf16x2(q[k].z, q[k].w)));
     return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
   }
-  static __device__ __forceinline__ void pairs(const uint4& q, Pair (&v)[4]) {
+  // the columns less base
+  static __device__ __forceinline__ void above(const uint4& q, float nbase, Pair (&v)[4]) {
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = pack2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
+    for (int k = 0; k < 4; ++k) {
+      float lo, hi;
+      asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; add.f32.bf16 %0, l, %3; add.f32.bf16 %1, h, %3;}" : "=f"(lo), "=f"(hi) : "r"(w[k]), "f"(nbase));
+      v[k] = pack2(lo, hi);
+    }
   }
 };
 template <>
@@ -90,9 +114,9 @@ struct Group<float> {
                 __uint_as_float(q[k].w));
     return m;
   }
-  static __device__ __forceinline__ void pairs(const uint4& q, Pair (&v)[2]) {
-    v[0] = pack2(__uint_as_float(q.x), __uint_as_float(q.y));
-    v[1] = pack2(__uint_as_float(q.z), __uint_as_float(q.w));
+  static __device__ __forceinline__ void above(const uint4& q, float nbase, Pair (&v)[2]) {
+    v[0] = fadd2(pack2(__uint_as_float(q.x), __uint_as_float(q.y)), both(nbase));
+    v[1] = fadd2(pack2(__uint_as_float(q.z), __uint_as_float(q.w)), both(nbase));
   }
 };
 __device__ __forceinline__ float load1(const uint16_t* p) { return __uint_as_float(static_cast<uint32_t>(*p) << 16); }
@@ -129,8 +153,8 @@ __device__ __forceinline__ void store_group(float* p, const Pair (&v)[kPairs]) {
 __device__ __forceinline__ float base_of(float m) { return fmaxf(m, -FLT_MAX); }
 
 // A part of a row's statistics: reference m, s = sum 2^d, t = sum 2^d d with d = (z - m) c
-struct Part {
-  float m, s, t, z_y;  // z_y: the target's logit (0 in the parts that do not have it)
+struct __align__(16) Part {  // (moved by 16-byte stores)
+  float m, s, t, reserved;
 };
 
 // The parts of all lanes as one, in every lane
@@ -141,9 +165,9 @@ __device__ __forceinline__ Part join(Part v, float c) {
   const float f = fast_exp2(d);
   Part r;
   r.m = m;
-  if (kEnt) r.t = warp_sum(f * fmaf(v.s, fmaxf(d, kFarBelow), v.t));
+  r.t = kEnt ? warp_sum(f * fmaf(v.s, fmaxf(d, kFarBelow), v.t)) : 0.f;
   r.s = warp_sum(f * v.s);
-  r.z_y = warp_sum(v.z_y);
+  r.reserved = 0.f;
   return r;
 }
 template <bool kEnt>
@@ -152,9 +176,9 @@ __device__ __forceinline__ Part merge(const Part& v, const Part& w, float c) {
   r.m = fmaxf(v.m, w.m);
   const float dv = (base_of(v.m) - base_of(r.m)) * c, dw = (base_of(w.m) - base_of(r.m)) * c;
   const float fv = fast_exp2(dv), fw = fast_exp2(dw);
-  if (kEnt) r.t = fv * fmaf(v.s, fmaxf(dv, kFarBelow), v.t) + fw * fmaf(w.s, fmaxf(dw, kFarBelow), w.t);
+  r.t = kEnt ? fv * fmaf(v.s, fmaxf(dv, kFarBelow), v.t) + fw * fmaf(w.s, fmaxf(dw, kFarBelow), w.t) : 0.f;
   r.s = fv * v.s + fw * w.s;
-  r.z_y = v.z_y + w.z_y;
+  r.reserved = 0.f;
   return r;
 }
 
@@ -163,10 +187,13 @@ struct Sums {
   float m;
   Pair s, t;
 };
-// n groups into the sums
-template <typename TZ, bool kEnt, int n>
-__device__ __forceinline__ void add_groups(const uint4 (&q)[n], float c, float slack, Sums& v) {
+// n groups in shared memory, `pitch` apart, into the sums
+template <typename TZ, bool kEnt, int n, int pitch>
+__device__ __forceinline__ void add_groups(const uint4* src, float c, float slack, Sums& v) {
   constexpr int kPairs = Group<TZ>::kCols / 2;
+  uint4 q[n];
+#pragma unroll
+  for (int k = 0; k < n; ++k) q[k] = src[k * pitch];
   const float top = Group<TZ>::top(q);
   if (top > v.m + slack) {
     const float d = (base_of(v.m) - base_of(top)) * c;
@@ -175,18 +202,34 @@ __device__ __forceinline__ void add_groups(const uint4 (&q)[n], float c, float s
     v.s = mul2(f, v.s);
     v.m = top;
   }
-  const Pair base = both(-base_of(v.m)), c2 = both(c);
+  const float nbase = -base_of(v.m);
+  const Pair c2 = both(c), before = v.t;
 #pragma unroll
   for (int k = 0; k < n; ++k) {
     Pair x[kPairs];
-    Group<TZ>::pairs(q[k], x);
+    Group<TZ>::above(q[k], nbase, x);
 #pragma unroll
     for (int e = 0; e < kPairs; ++e) {
+      const Pair d = mul2(x[e], c2);
       float lo, hi;
-      unpack2(mul2(fadd2(x[e], base), c2), lo, hi);
+      unpack2(d, lo, hi);
       const Pair w = pack2(fast_exp2(lo), fast_exp2(hi));
       v.s = fadd2(v.s, w);
-      if (kEnt) v.t = ffma2(w, pack2(fmaxf(lo, kFarBelow), fmaxf(hi, kFarBelow)), v.t);
+      if (kEnt) v.t = ffma2(w, d, v.t);
+    }
+  }
+  if (kEnt && !(sum2(v.t) < INFINITY)) {  // 0 times -infinity: again, with d at least kFarBelow
+    v.t = before;
+#pragma unroll 1
+    for (int k = 0; k < n; ++k) {
+      Pair x[kPairs];
+      Group<TZ>::above(src[k * pitch], nbase, x);
+#pragma unroll
+      for (int e = 0; e < kPairs; ++e) {
+        float lo, hi;
+        unpack2(mul2(x[e], c2), lo, hi);
+        v.t = ffma2(pack2(fast_exp2(lo), fast_exp2(hi)), pack2(fmaxf(lo, kFarBelow), fmaxf(hi, kFarBelow)), v.t);
+      }
     }
   }
 }
@@ -203,13 +246,13 @@ __device__ __forceinline__ float slope_at(const Slope& g, float z) {
 template <typename TZ, typename TD, bool kEnt>
 __device__ __forceinline__ void put_group(const uint4& q, const Slope& g, TD* to) {
   constexpr int kPairs = Group<TZ>::kCols / 2;
-  const Pair nbase = both(-g.base), c2 = both(g.c), k0 = both(g.k0), k1 = both(g.k1);
+  const Pair c2 = both(g.c), k0 = both(g.k0), k1 = both(g.k1);
   Pair x[kPairs];
-  Group<TZ>::pairs(q, x);
+  Group<TZ>::above(q, -g.base, x);
 #pragma unroll
   for (int e = 0; e < kPairs; ++e) {
     float lo, hi;
-    unpack2(mul2(fadd2(x[e], nbase), c2), lo, hi);
+    unpack2(mul2(x[e], c2), lo, hi);
     const Pair w = pack2(fast_exp2(lo), fast_exp2(hi));
     x[e] = kEnt ? mul2(w, ffma2(pack2(fmaxf(lo, kFarBelow), fmaxf(hi, kFarBelow)), k1, k0)) : mul2(w, k0);
   }
@@ -217,13 +260,17 @@ __device__ __forceinline__ void put_group(const uint4& q, const Slope& g, TD* to
 }
 
 // A place in the ring that advances chunk by chunk
+template <int kSlots>
 struct Place {
   uint32_t slot = 0, turn = 0;  // turn: parity of the slot's use
   __device__ __forceinline__ void next() {
-    if (++slot == kLossSlots) {
+    if (++slot == kSlots) {
       slot = 0;
       turn ^= 1;
     }
+  }
+  __device__ __forceinline__ void skip(int n) {
+    for (; n > 0; --n) next();
   }
 };
 
@@ -240,9 +287,10 @@ __device__ __forceinline__ bool offsets_fine(const int32_t* off, int n, int64_t 
 
 // Sum of the counted rows' weights over the computing warps, in the same order in every CTA
 // (compensated: any number of rows)
+template <int kWarps>
 __device__ __forceinline__ float total_weight(const LossArgs& a, float* buf) {
   float sum = 0.f, low = 0.f;
-  for (int64_t i = threadIdx.x; i < a.rows; i += 32 * kLossWarps) {
+  for (int64_t i = threadIdx.x; i < a.rows; i += 32 * kWarps) {
     const int32_t y = a.targets[i];
     if (y < 0 || y >= a.first[a.P]) continue;
     const float x = (a.weights ? a.weights[i] : 1.f) - low, next = sum + x;
@@ -252,14 +300,19 @@ __device__ __forceinline__ float total_weight(const LossArgs& a, float* buf) {
   sum = warp_sum(sum);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (lane == 0) buf[warp] = sum;
-  asm volatile("bar.sync 1, %0;" ::"n"(32 * kLossWarps) : "memory");
-  return warp_sum(lane < kLossWarps ? buf[lane] : 0.f);
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+  return warp_sum(lane < kWarps ? buf[lane] : 0.f);
 }
 
+constexpr int kBoxes = 4;
+
+template <typename S>
 struct Smem {
-  uint64_t full[kLossSlots], empty[kLossSlots], told[2];
-  Part part[2][kLossMaxCtas * kLossWarps];
-  float buf[kLossWarps];
+  uint64_t full[S::kSlots], empty[S::kSlots], made[S::kSlots], told[kBoxes], ready[S::kSets];
+  Part part[kBoxes][kLossMaxCtas * S::kWarps];
+  float4 slope[S::kSets];          // base, k0, k1, own of a set's row (Slope)
+  double sums[S::kSets * S::kWarps][4];
+  float buf[S::kSets * S::kWarps];
 };
 
 // A lane's row of a batch of 32
@@ -268,6 +321,10 @@ struct RowIn {
   bool on;
 };
 
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
+}
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                    smem_u32(dst)),
@@ -292,25 +349,38 @@ __device__ __forceinline__ bool wait_told(uint64_t* bar, uint32_t parity, const 
 // kEnt: forward: the entropy is wanted; policy and backward: it has a gradient.  (The policy loss's
 // statistics have the entropy anyway.)
 template <typename TZ, typename TD, int kMode, bool kEnt>
-__global__ void __launch_bounds__(kLossThreads, 1) loss_rows_kernel(const __grid_constant__ LossArgs a) {
+__global__ void __launch_bounds__(Shape<kMode>::kAll + 32 * Shape<kMode>::kMore, Shape<kMode>::kPerSm)
+    loss_rows_kernel(const __grid_constant__ LossArgs a) {
+  typedef Shape<kMode> S;
+  typedef Place<S::kSlots> P;
   extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ Smem sm;
+  __shared__ Smem<S> sm;
   constexpr bool kStat = kMode != kLossBackward;
   constexpr bool kStatEnt = kMode == kLossPolicy || (kMode == kLossForward && kEnt);
   constexpr int kCols = Group<TZ>::kCols, kPairs = kCols / 2;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
+  constexpr int kSlots = S::kSlots, kSets = S::kSets, kWarps = S::kWarps, kThreads = S::kThreads;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(blockIdx.x % a.ctas);
   const int64_t team = blockIdx.x / a.ctas, teams = gridDim.x / a.ctas;
   const bool together = kStat && a.ctas > 1;  // launched as clusters
-  if (tid == 0) {
-    for (int i = 0; i < kLossSlots; ++i) {
+  const bool grad = kMode != kLossForward && a.d[0];
+  const bool twice = kStat && grad && a.twice;
+  // gradients are made in the slots, in the logits' place, and copied from there
+  const bool out = kMode == kLossPolicy && sizeof(TZ) == sizeof(TD) && grad && !twice;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kSlots; ++i) {
       mbar_init(&sm.full[i], 1);
-      mbar_init(&sm.empty[i], kLossWarps);
+      mbar_init(&sm.empty[i], out ? 1 : kWarps);
+      mbar_init(&sm.made[i], kWarps);
     }
-    for (int i = 0; i < 2; ++i) mbar_init(&sm.told[i], a.ctas * kLossWarps);
+    for (int i = 0; i < kBoxes; ++i) mbar_init(&sm.told[i], together ? 1 : kWarps);
+    for (int i = 0; i < kSets; ++i) mbar_init(&sm.ready[i], 1);
     fence_barrier_init();
     fence_proxy_async_shared();
   }
+  for (int k = threadIdx.x * 16; k < S::kZeros; k += blockDim.x * 16)
+    *reinterpret_cast<uint4*>(ring + kSlots * kLossChunk + k) = make_uint4(0, 0, 0, 0);
+  if (S::kZeros) fence_proxy_async_shared();
   int64_t row0 = 0, rows = a.rows;
   if (a.offsets) {
     // (every CTA sees the same offsets: all of them leave)
@@ -324,71 +394,111 @@ __global__ void __launch_bounds__(kLossThreads, 1) loss_rows_kernel(const __grid
   const int g_lo = static_cast<int>(static_cast<int64_t>(a.groups[a.P]) * rank / a.ctas);
   const int g_hi = static_cast<int>(static_cast<int64_t>(a.groups[a.P]) * (rank + 1) / a.ctas);
   const int chunks = (g_hi - g_lo + kChunkGroups - 1) / kChunkGroups;
-  const bool grad = kMode != kLossForward && a.d[0];
-  const bool twice = kStat && grad && a.twice;
-  const int64_t mine = rows > team ? (rows - team + teams - 1) / teams : 0;  // the team's rows: team, team + teams, ..
-  auto row_at = [&](int64_t n) {
-    const int64_t k = team + n * teams;
-    return row0 + (a.backwards ? rows - 1 - k : k);
-  };
-  auto fetch = [&](int64_t n) {  // this lane's row of the batch that starts at n
+  // the team's rows: team, team + teams, .. from the first row on, or from the last one back
+  const int mine = rows > team ? static_cast<int>((rows - team + teams - 1) / teams) : 0;
+  const int64_t stride = a.backwards ? -teams : teams;
+  int64_t i = row0 + (a.backwards ? rows - 1 - team : team);
+  auto fetch = [&](int n) {  // this lane's row of the batch that starts at the team's row n
     RowIn r = {-1, false};
     if (n + lane < mine) {
-      const int64_t i = row_at(n + lane);
-      r.y = a.targets[i];
-      r.on = r.y >= 0 && r.y < a.first[a.P] && (!a.weights || a.weights[i] != 0.f);
+      const int64_t k = i + lane * stride;
+      r.y = a.targets[k];
+      r.on = r.y >= 0 && r.y < a.first[a.P] && (!a.weights || a.weights[k] != 0.f);
     }
     return r;
   };
 
-  if (warp == kLossWarps) {
-    // the copies, in the order in which the chunks are used
+  if (warp == kSets * kWarps) {
+    // the copies, in the order in which the chunks are used: of each row for its statistics, and (twice)
+    // again for its gradient
     RowIn r = {-1, false};
     uint32_t count = 0;
     bool fine = true;
-    for (int64_t n = 0; n < mine && fine; ++n) {
+    auto copy_row = [&](int64_t row) {
+      int rk = 0;
+      for (int c = 0; c < chunks && fine; ++c, ++count) {
+        const uint32_t slot = count % kSlots, turn = count / kSlots;
+        if (turn > 0 && !wait_full(&sm.empty[slot], (turn - 1) & 1, a)) {
+          fine = false;
+          break;
+        }
+        if (lane == 0) {
+          int g = g_lo + c * kChunkGroups;
+          const int end = g + kChunkGroups < g_hi ? g + kChunkGroups : g_hi;
+          uint8_t* dst = ring + slot * kLossChunk;
+          mbar_arrive_expect_tx(&sm.full[slot], static_cast<uint32_t>(end - g) * 16u);
+          while (g < end) {
+            while (g >= a.groups[rk + 1]) ++rk;
+            const int stop = end < a.groups[rk + 1] ? end : a.groups[rk + 1];
+            const uint8_t* src = static_cast<const uint8_t*>(a.z[rk]) + row * a.ldz[rk] * sizeof(TZ) +
+                                 static_cast<int64_t>(g - a.groups[rk]) * 16;
+            bulk_load(dst, src, static_cast<uint32_t>(stop - g) * 16u, &sm.full[slot]);
+            dst += (stop - g) * 16;
+            g = stop;
+          }
+        }
+        __syncwarp();
+      }
+    };
+    for (int n = 0; n < mine && fine; ++n, i += stride) {
       if ((n & 31) == 0) r = fetch(n);
       if (!__shfl_sync(0xffffffffu, r.on, n & 31)) continue;
-      const int64_t i = row_at(n);
-      for (int pass = 0; pass < (twice ? 2 : 1) && fine; ++pass) {
-        int rk = 0;
-        for (int c = 0; c < chunks; ++c, ++count) {
-          const uint32_t slot = count % kLossSlots, turn = count / kLossSlots;
-          if (turn > 0 && !wait_full(&sm.empty[slot], (turn - 1) & 1, a)) {
-            fine = false;
-            break;
-          }
-          if (lane == 0) {
-            int g = g_lo + c * kChunkGroups;
-            const int end = g + kChunkGroups < g_hi ? g + kChunkGroups : g_hi;
-            uint8_t* dst = ring + slot * kLossChunk;
-            mbar_arrive_expect_tx(&sm.full[slot], static_cast<uint32_t>(end - g) * 16u);
-            while (g < end) {
-              while (g >= a.groups[rk + 1]) ++rk;
-              const int stop = end < a.groups[rk + 1] ? end : a.groups[rk + 1];
-              const uint8_t* src = static_cast<const uint8_t*>(a.z[rk]) + i * a.ldz[rk] * sizeof(TZ) +
-                                   static_cast<int64_t>(g - a.groups[rk]) * 16;
-              bulk_load(dst, src, static_cast<uint32_t>(stop - g) * 16u, &sm.full[slot]);
-              dst += (stop - g) * 16;
-              g = stop;
-            }
-          }
-          __syncwarp();
-        }
-      }
+      copy_row(i);
+      if (twice) copy_row(i);
     }
     if (!fine && lane == 0) raise_error(a.ctrl, FO_ERR_TIMEOUT, kSiteEmpty, blockIdx.x);
     // no copy may be in flight behind a CTA whose computing warps gave up
-    for (uint32_t k = count > kLossSlots ? count - kLossSlots : 0; k < count; ++k)
-      mbar_wait_drain(&sm.full[k % kLossSlots], (k / kLossSlots) & 1, kLossDrainNs);
+    for (uint32_t k = count > kSlots ? count - kSlots : 0; k < count; ++k)
+      mbar_wait_drain(&sm.full[k % kSlots], (k / kSlots) & 1, kLossDrainNs);
+  } else if (warp > kSets * kWarps) {
+    // the copies of the gradients, in the order in which they are made; rows that do not count are
+    // copies of zeros
+    RowIn r = {-1, false};
+    P place;
+    bool fine = true;
+    for (int n = 0; n < mine && out && fine; ++n, i += stride) {
+      if ((n & 31) == 0) r = fetch(n);
+      const bool on = __shfl_sync(0xffffffffu, r.on, n & 31);
+      int rk = 0;
+      for (int g = g_lo; g < g_hi && fine;) {
+        const int left = g_hi - g, end = g + (left < kChunkGroups ? left : kChunkGroups);
+        if (on && !wait_full(&sm.made[place.slot], place.turn, a)) {
+          fine = false;
+          break;
+        }
+        if (lane == 0) {
+          const uint8_t* src = ring + (on ? place.slot * kLossChunk : kSlots * kLossChunk);
+          while (g < end) {
+            while (g >= a.groups[rk + 1]) ++rk;
+            int stop = end < a.groups[rk + 1] ? end : a.groups[rk + 1];
+            if (!on && stop > g + S::kZeros / 16) stop = g + S::kZeros / 16;
+            bulk_store(static_cast<uint8_t*>(a.d[rk]) + (i * a.ldd[rk] * sizeof(TD) + static_cast<int64_t>(g - a.groups[rk]) * 16),
+                       src, static_cast<uint32_t>(stop - g) * 16u);
+            if (on) src += (stop - g) * 16;
+            g = stop;
+          }
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          if (on) {
+            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            mbar_arrive(&sm.empty[place.slot]);
+          }
+        }
+        __syncwarp();
+        g = end;
+        if (on) place.next();
+      }
+    }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (!fine && lane == 0) raise_error(a.ctrl, FO_ERR_TIMEOUT, kSiteDrain, blockIdx.x);
   } else {
     const float c = static_cast<float>(a.scale * kLog2e);
     const float slack = kOctaves / c;
     float per_weight = 1.f;
     if (kMode == kLossPolicy && a.mean) {
-      const float total = total_weight(a, sm.buf);
+      const float total = total_weight<kSets * kWarps>(a, sm.buf);
       per_weight = total == 0.f ? 0.f : 1.f / total;
     }
+    const int set = kSets > 1 ? warp / kWarps : 0, tid = kSets > 1 ? threadIdx.x % kThreads : threadIdx.x;
     // columns behind a rank's last whole group: one each for the first threads of a row's first CTA
     const int t_rk = tid >> 3;
     int t_col = -1;
@@ -396,24 +506,34 @@ __global__ void __launch_bounds__(kLossThreads, 1) loss_rows_kernel(const __grid
       const int ragged = a.cols[t_rk] % kCols;
       if ((tid & 7) < ragged) t_col = a.cols[t_rk] - ragged + (tid & 7);
     }
-    double sums[4] = {0.0, 0.0, 0.0, 0.0};  // thread 0 of a row's first CTA: stats
+    double sums[4] = {0.0, 0.0, 0.0, 0.0};  // stats of the rows that this warp finished (lane 0)
     RowIn r = {-1, false};
-    float in0 = 0.f, in1 = 0.f, in2 = 0.f, in3 = 0.f;
-    uint32_t told = 0;
-    Place place;
+    int y_rk = 0, y_col = 0, y_group = -1;               // this lane's row: where the target is
+    float z_y = 0.f;
+    float in0 = 0.f, in1 = 0.f, in2 = 0.f, in3 = 0.f;    // what else goes with it (backward: its Slope)
+    uint32_t count = 0;                                  // rows that counted so far
+    P place;
     bool fine = true;
-    for (int64_t n = 0; n < mine; ++n) {
-      const int64_t i = row_at(n);
-      const int at = static_cast<int>(n & 31);
+    for (int n = 0; n < mine; ++n, i += stride) {
+      const int at = n & 31;
       if (at == 0) {
         r = fetch(n);
-        const int64_t k = n + lane < mine ? row_at(n + lane) : 0;
+        const int64_t k = i + lane * stride;
         if (kStat && warp == 0 && rank == 0 && n + lane < mine && !r.on) {
           if (r.y >= a.first[a.P]) note_error(a.ctrl, FO_ERR_RANGE, kSiteTargets, static_cast<uint32_t>(k));
           if (a.logp) a.logp[k] = 0.f;
           if (a.lse) a.lse[k] = 0.f;
           if (a.entropy) a.entropy[k] = 0.f;
           if (a.stat) a.stat[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        if (r.on) {
+          y_rk = 0;
+          while (r.y >= a.first[y_rk + 1]) ++y_rk;
+          y_col = r.y - a.first[y_rk];
+          // (read now: no CTA writes a gradient over a row before every warp has told its part of it)
+          z_y = load1(static_cast<const TZ*>(a.z[y_rk]) + k * a.ldz[y_rk] + y_col);
+          const int whole = a.groups[y_rk + 1] - a.groups[y_rk];
+          y_group = y_col / kCols < whole ? a.groups[y_rk] + y_col / kCols : -1;
         }
         if (kMode == kLossPolicy && r.on) {
           in0 = a.weights ? a.weights[k] : 1.f;
@@ -422,210 +542,249 @@ __global__ void __launch_bounds__(kLossThreads, 1) loss_rows_kernel(const __grid
           if (a.ref_logp) in3 = a.ref_logp[k];
         }
         if (kMode == kLossBackward && r.on) {
+          float da, dh = 0.f, log_s = 0.f, entropy = 0.f;
           if (a.coef) {
             int lo = 0, hi = 2 * a.pairs - 1;  // the sequence: the last one that starts at or in front of row k
             while (lo < hi) {
               const int mid = (lo + hi + 1) >> 1;
               if (a.offsets[mid] <= k) lo = mid; else hi = mid - 1;
             }
-            in0 = a.coef[lo];
+            da = a.coef[lo];
             const float4 st = a.stat[k];
-            in2 = st.x;
-            in3 = st.y;
+            in0 = st.x;
+            log_s = st.y;
           } else {
-            in0 = a.dlogp[k];
-            if (kEnt) in1 = a.dentropy[k];
-            in2 = a.in_lse[k] / a.scale;
-            in3 = kEnt ? a.in_entropy[k] : 0.f;
+            da = a.dlogp[k];
+            if (kEnt) {
+              dh = a.dentropy[k];
+              entropy = a.in_entropy[k];
+            }
+            in0 = a.in_lse[k] / a.scale;
           }
+          in1 = -a.scale * exp2f(-log_s) * (kEnt ? fmaf(dh, entropy, da) : da);
+          in2 = -a.scale * dh * kLn2;
+          in3 = a.scale * da;
         }
       }
-      const int32_t y = __shfl_sync(0xffffffffu, r.y, at);
       if (!__shfl_sync(0xffffffffu, r.on, at)) {
-        if (grad) {
+        if (grad && n % kSets == set) {
           const Pair zero[kPairs] = {};
           int rk = 0;
-          for (int g = g_lo + tid; g < g_hi; g += 32 * kLossWarps) {
+          for (int g = g_lo + tid; g < g_hi && !out; g += kThreads) {
             while (g >= a.groups[rk + 1]) ++rk;
-            store_group<kPairs>(static_cast<TD*>(a.d[rk]) + i * a.ldd[rk] + static_cast<int64_t>(g - a.groups[rk]) * kCols, zero);
+            store_group<kPairs>(
+                static_cast<TD*>(a.d[rk]) + i * a.ldd[rk] + static_cast<int64_t>(g - a.groups[rk]) * kCols, zero);
           }
           if (t_col >= 0) store1(static_cast<TD*>(a.d[t_rk]) + i * a.ldd[t_rk] + t_col, 0.f);
         }
         continue;
       }
-      // the target's place: a group of this CTA, or a column behind the groups
-      int y_rk = 0;
-      while (y >= a.first[y_rk + 1]) ++y_rk;
-      const int y_col = y - a.first[y_rk];
-      const int whole = a.groups[y_rk + 1] - a.groups[y_rk];
-      const int y_group = y_col < whole * kCols ? a.groups[y_rk] + y_col / kCols : -1;
-      const bool y_here = t_col >= 0 && t_rk == y_rk && t_col == y_col;
+      const uint32_t q = count++;
+      if (kSets > 1 && q % kSets != static_cast<uint32_t>(set)) {
+        place.skip(twice ? 2 * chunks : chunks);
+        continue;
+      }
+      const int col_y = __shfl_sync(0xffffffffu, y_col, at), rk_y = __shfl_sync(0xffffffffu, y_rk, at);
+      const int group_y = __shfl_sync(0xffffffffu, y_group, at) - g_lo;
+      const float zy = __shfl_sync(0xffffffffu, z_y, at);
       const float z_t = t_col >= 0 ? load1(static_cast<const TZ*>(a.z[t_rk]) + i * a.ldz[t_rk] + t_col) : -INFINITY;
+      const P start = place;
+      float4 w;  // the row's Slope, and what its target's column has more
 
-      // first walk: the row's statistics
-      Part v;
-      const Place start = place;
       if (kStat) {
-        v = Part{z_t, t_col >= 0 ? fast_exp2((z_t - base_of(z_t)) * c) : 0.f, 0.f, y_here ? z_t : 0.f};
-        Sums sums2 = {-INFINITY, 0, 0};
+        Sums some = {-INFINITY, 0, 0};
         for (int k = 0; k < chunks; ++k, place.next()) {
           if (!wait_full(&sm.full[place.slot], place.turn, a)) {
             fine = false;
             break;
           }
-          const int g0 = g_lo + k * kChunkGroups, left = g_hi - g0;
+          const int left = g_hi - g_lo - k * kChunkGroups;
           const uint4* src = reinterpret_cast<const uint4*>(ring + place.slot * kLossChunk) + tid;
           if (left >= kChunkGroups) {
-            uint4 q[kBatch];
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j) q[j] = src[j * 32 * kLossWarps];
-            add_groups<TZ, kStatEnt>(q, c, slack, sums2);
+            add_groups<TZ, kStatEnt, S::kBatch, kThreads>(src, c, slack, some);
           } else {
-            for (int g = tid; g < left; g += 32 * kLossWarps) {
-              const uint4 q[1] = {src[g - tid]};
-              add_groups<TZ, kStatEnt>(q, c, slack, sums2);
-            }
+            for (int g = tid; g < left; g += kThreads)
+              add_groups<TZ, kStatEnt, 1, 1>(src + (g - tid), c, slack, some);
           }
-          const int at_y = y_group - g0;
-          if (at_y >= 0 && at_y < left && at_y < kChunkGroups && at_y % (32 * kLossWarps) == tid)
-            v.z_y = load1(reinterpret_cast<const TZ*>(src - tid + at_y) + y_col % kCols);
           if (!grad || twice) {
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.empty[place.slot]);
           }
         }
-        v = merge<kStatEnt>(v, Part{sums2.m, sum2(sums2.s), sum2(sums2.t), 0.f}, c);
         if (!fine) break;
-        // every warp's part to every CTA of the row
+        Part v = {some.m, sum2(some.s), sum2(some.t), 0.f};
+        if (t_col >= 0) v = merge<kStatEnt>(v, Part{z_t, fast_exp2((z_t - base_of(z_t)) * c), 0.f, 0.f}, c);
         v = join<kStatEnt>(v, c);
-        Part* const box = sm.part[told & 1];
-        uint64_t* const bar = &sm.told[told & 1];
-        if (!together) {
-          if (lane == 0) {
-            box[warp] = v;
-            mbar_arrive(bar);
-          }
-        } else if (lane < a.ctas) {
-          const uint32_t to = map_to_cta(smem_u32(box + rank * kLossWarps + warp), lane);
-          asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(v.m), "f"(v.s), "f"(v.t),
-                       "f"(v.z_y)
-                       : "memory");
-          mbar_arrive_cluster(map_to_cta(smem_u32(bar), lane));
-        }
-        if (!wait_told(bar, (told >> 1) & 1, a)) {
+        // the warp's part to every CTA of the row.  A box is free again when the row kBoxes - kSets back
+        // has been told by all: the warps that added the row kBoxes back told that one afterwards
+        const uint32_t box = q % kBoxes, back = q - (kBoxes - kSets);
+        if (q >= kBoxes - kSets && !wait_told(&sm.told[back % kBoxes], (back / kBoxes) & 1, a)) {
           fine = false;
           break;
         }
-        ++told;
-        v = Part{-INFINITY, 0.f, 0.f, 0.f};
-        for (int k = lane; k < (together ? a.ctas : 1) * kLossWarps; k += 32) v = merge<kStatEnt>(v, box[k], c);
-        v = join<kStatEnt>(v, c);
-      }
-
-      // the row: p_j = 2^((z_j - base) c - log_s)
-      float base, log_s, entropy = 0.f, dy = 0.f;
-      if (kStat) {
-        base = base_of(v.m);
-        log_s = log2f(v.s);
-        dy = (v.z_y - base) * c;
-        if (kStatEnt) entropy = kLn2 * (log_s - v.t / v.s);
-        if (rank == 0 && tid == 0) {
-          if (a.logp) a.logp[i] = kLn2 * (dy - log_s);
-          if (a.lse) a.lse[i] = fmaf(base, a.scale, kLn2 * log_s);
-          if (kMode == kLossForward && a.entropy) a.entropy[i] = entropy;
-          if (a.stat) a.stat[i] = make_float4(base, log_s, dy, 0.f);
+        if (!together) {
+          if (lane == 0) {
+            sm.part[box][warp % kWarps] = v;
+            mbar_arrive(&sm.told[box]);
+          }
+        } else if (lane < a.ctas) {
+          if (warp % kWarps == 0 && lane == 0)
+            mbar_arrive_expect_tx(&sm.told[box], static_cast<uint32_t>(a.ctas * kWarps * sizeof(Part)));
+          const uint32_t to = map_to_cta(smem_u32(&sm.part[box][rank * kWarps + warp % kWarps]), lane);
+          // (a store that counts at the barrier by itself: an arrival with release would wait for the
+          // gradients under way to memory)
+          asm volatile(
+              "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
+              "r"(__float_as_uint(v.m)), "r"(__float_as_uint(v.s)), "r"(__float_as_uint(v.t)), "r"(0),
+              "r"(map_to_cta(smem_u32(&sm.told[box]), lane))
+              : "memory");
         }
-      }
-      if (kMode == kLossForward) continue;
-      // the loss through this row: da = dL/dlogp, dh = dL/dH
-      const float v0 = __shfl_sync(0xffffffffu, in0, at), v1 = __shfl_sync(0xffffffffu, in1, at);
-      const float v2 = __shfl_sync(0xffffffffu, in2, at), v3 = __shfl_sync(0xffffffffu, in3, at);
-      float da = v0, dh = v1;
-      if (kMode == kLossBackward) {
-        base = v2;
-        log_s = a.coef ? v3 : 0.f;
-        if (kEnt) entropy = v3;
+        __syncwarp();
+        // one warp of each CTA adds the row's parts
+        if (static_cast<int>(q / kSets % kWarps) == warp % kWarps) {
+          if (!wait_told(&sm.told[box], (q / kBoxes) & 1, a)) {
+            fine = false;
+            break;
+          }
+          v = Part{-INFINITY, 0.f, 0.f, 0.f};
+          for (int k = lane; k < a.ctas * kWarps; k += 32) v = merge<kStatEnt>(v, sm.part[box][k], c);
+          v = join<kStatEnt>(v, c);
+          // p_j = 2^((z_j - base) c - log_s)
+          const float base = base_of(v.m), log_s = log2f(v.s);
+          const float dy = (zy - base) * c, lp = kLn2 * (dy - log_s);
+          const float entropy = kStatEnt ? kLn2 * (log_s - v.t / v.s) : 0.f;
+          if (rank == 0 && lane == 0) {
+            if (a.logp) a.logp[i] = lp;
+            if (a.lse) a.lse[i] = fmaf(base, a.scale, kLn2 * log_s);
+            if (kMode == kLossForward && a.entropy) a.entropy[i] = entropy;
+            if (a.stat) a.stat[i] = make_float4(base, log_s, dy, 0.f);
+          }
+          if (kMode == kLossPolicy) {
+            // the loss through this row: da = dL/dlogp, dh = dL/dH
+            const float weight = __shfl_sync(0xffffffffu, in0, at) * per_weight, adv = __shfl_sync(0xffffffffu, in1, at);
+            const float old = __shfl_sync(0xffffffffu, in2, at), ref = __shfl_sync(0xffffffffu, in3, at);
+            const float ratio = expf(a.old_logp ? lp - old : 0.f);
+            const float held = fminf(fmaxf(ratio, a.ratio_lo), a.ratio_hi) * adv, free = ratio * adv;
+            const bool clipped = held < free;
+            float kl = 0.f, dkl = 0.f;
+            if (a.ref_logp) {
+              const float x = ref - lp;
+              dkl = expm1f(x);
+              kl = dkl - x;
+            }
+            const float da = weight * ((clipped ? 0.f : -free) - a.kl_coef * dkl), dh = -a.entropy_coef * weight;
+            if (rank == 0) {
+              const float loss = -(clipped ? held : free) + a.kl_coef * kl - a.entropy_coef * entropy;
+              sums[0] += static_cast<double>(weight) * loss;
+              sums[1] += static_cast<double>(weight) * kl;
+              if (clipped) sums[2] += weight;
+              sums[3] += static_cast<double>(weight) * entropy;
+            }
+            if (grad && lane == 0) {
+              const float inv = -a.scale * exp2f(-log_s);
+              sm.slope[set] =
+                  make_float4(base, inv * (kEnt ? da + dh * (entropy - kLn2 * log_s) : da), inv * dh * kLn2, a.scale * da);
+              mbar_arrive(&sm.ready[set]);
+            }
+          }
+        }
+        if (kMode == kLossForward || !grad) continue;
+        if (!wait_full(&sm.ready[set], (q / kSets) & 1, a)) {
+          fine = false;
+          break;
+        }
+        w = sm.slope[set];
       } else {
-        const float lp = kLn2 * (dy - log_s), w = v0 * per_weight, adv = v1;
-        const float ratio = expf(a.old_logp ? lp - v2 : 0.f);
-        const float held = fminf(fmaxf(ratio, a.ratio_lo), a.ratio_hi) * adv, free = ratio * adv;
-        const bool clipped = held < free;
-        float kl = 0.f, dkl = 0.f;
-        if (a.ref_logp) {
-          const float x = v3 - lp;
-          dkl = expm1f(x);
-          kl = dkl - x;
-        }
-        da = w * ((clipped ? 0.f : -free) - a.kl_coef * dkl);
-        dh = -a.entropy_coef * w;
-        if (rank == 0 && tid == 0) {
-          const float loss = -(clipped ? held : free) + a.kl_coef * kl - a.entropy_coef * entropy;
-          sums[0] += static_cast<double>(w) * loss;
-          sums[1] += static_cast<double>(w) * kl;
-          if (clipped) sums[2] += w;
-          sums[3] += static_cast<double>(w) * entropy;
-        }
+        w.x = __shfl_sync(0xffffffffu, in0, at);
+        w.y = __shfl_sync(0xffffffffu, in1, at);
+        w.z = kEnt ? __shfl_sync(0xffffffffu, in2, at) : 0.f;
+        w.w = __shfl_sync(0xffffffffu, in3, at);
       }
-      if (!grad) continue;
 
-      // second walk: dz_j = own 1[j = y] + 2^d (k0 + k1 d) with d = (z_j - base) c
-      const float own = a.scale * da;
-      const float inv = exp2f(-log_s);
-      const float k0 = -a.scale * inv * (kEnt ? da + dh * (entropy - kLn2 * log_s) : da);
-      const float k1 = -a.scale * inv * dh * kLn2;
-      const Slope slope = {base, c, k0, k1};
-      if (t_col >= 0)
-        store1(static_cast<TD*>(a.d[t_rk]) + i * a.ldd[t_rk] + t_col, slope_at<kEnt>(slope, z_t) + (y_here ? own : 0.f));
-      if (kStat && !twice) place = start;
+      // the gradient: dz_j = own 1[j = y] + 2^d (k0 + k1 d) with d = (z_j - base) c
+      const Slope slope = {w.x, c, w.y, w.z};
+      const bool kept = kStat && !twice;  // the chunks have waited in their slots
+      if (kept) place = start;
       int rk = 0;
       for (int k = 0; k < chunks; ++k, place.next()) {
-        if ((!kStat || twice) && !wait_full(&sm.full[place.slot], place.turn, a)) {
+        if (!kept && !wait_full(&sm.full[place.slot], place.turn, a)) {
           fine = false;
           break;
         }
         const int g0 = g_lo + k * kChunkGroups, left = g_hi - g0;
-        while (g0 >= a.groups[rk + 1]) ++rk;
-        const uint4* src = reinterpret_cast<const uint4*>(ring + place.slot * kLossChunk) + tid;
-        if (left >= kChunkGroups && g0 + kChunkGroups <= a.groups[rk + 1]) {
-          TD* to = static_cast<TD*>(a.d[rk]) + i * a.ldd[rk] + static_cast<int64_t>(g0 + tid - a.groups[rk]) * kCols;
+        uint4* src = reinterpret_cast<uint4*>(ring + place.slot * kLossChunk) + tid;
+        if (kMode == kLossPolicy && sizeof(TZ) == sizeof(TD) && out) {
+          if (left >= kChunkGroups) {
+            uint4 x[S::kBatch];
 #pragma unroll
-          for (int j = 0; j < kBatch; ++j)
-            put_group<TZ, TD, kEnt>(src[j * 32 * kLossWarps], slope, to + j * 32 * kLossWarps * kCols);
+            for (int j = 0; j < S::kBatch; ++j) x[j] = src[j * kThreads];
+#pragma unroll
+            for (int j = 0; j < S::kBatch; ++j)
+              put_group<TZ, TD, kEnt>(x[j], slope, reinterpret_cast<TD*>(src + j * kThreads));
+          } else {
+            for (int g = tid; g < left; g += kThreads)
+              put_group<TZ, TD, kEnt>(src[g - tid], slope, reinterpret_cast<TD*>(src + (g - tid)));
+          }
+          const int at_y = group_y - k * kChunkGroups;
+          if (at_y >= 0 && at_y < left && at_y < kChunkGroups && at_y % kThreads == tid)
+            store1(reinterpret_cast<TD*>(src + (at_y - tid)) + col_y % kCols, slope_at<kEnt>(slope, zy) + w.w);
+          fence_proxy_async_shared();
         } else {
-          int r2 = rk;
-          for (int g = tid; g < left && g < kChunkGroups; g += 32 * kLossWarps) {
-            while (g0 + g >= a.groups[r2 + 1]) ++r2;
-            put_group<TZ, TD, kEnt>(src[g - tid], slope,
-                                    static_cast<TD*>(a.d[r2]) + i * a.ldd[r2] +
-                                        static_cast<int64_t>(g0 + g - a.groups[r2]) * kCols);
+          while (g0 >= a.groups[rk + 1]) ++rk;
+          if (left >= kChunkGroups && g0 + kChunkGroups <= a.groups[rk + 1]) {
+            TD* to = static_cast<TD*>(a.d[rk]) + i * a.ldd[rk] + static_cast<int64_t>(g0 + tid - a.groups[rk]) * kCols;
+            uint4 x[S::kBatch];  // (all read first: a store might be to what is read next)
+#pragma unroll
+            for (int j = 0; j < S::kBatch; ++j) x[j] = src[j * kThreads];
+#pragma unroll
+            for (int j = 0; j < S::kBatch; ++j) put_group<TZ, TD, kEnt>(x[j], slope, to + j * kThreads * kCols);
+          } else {
+            int r2 = rk;
+            for (int g = tid; g < left && g < kChunkGroups; g += kThreads) {
+              while (g0 + g >= a.groups[r2 + 1]) ++r2;
+              put_group<TZ, TD, kEnt>(src[g - tid], slope,
+                                      static_cast<TD*>(a.d[r2]) + i * a.ldd[r2] +
+                                          static_cast<int64_t>(g0 + g - a.groups[r2]) * kCols);
+            }
           }
         }
-        const int at_y = y_group - g0;  // the thread that wrote the target's group writes its column again
-        if (at_y >= 0 && at_y < left && at_y < kChunkGroups && at_y % (32 * kLossWarps) == tid)
-          store1(static_cast<TD*>(a.d[y_rk]) + i * a.ldd[y_rk] + y_col,
-                 slope_at<kEnt>(slope, load1(reinterpret_cast<const TZ*>(src - tid + at_y) + y_col % kCols)) + own);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.empty[place.slot]);
+        if (lane == 0) mbar_arrive(out ? &sm.made[place.slot] : &sm.empty[place.slot]);
       }
       if (!fine) break;
+      // the columns behind the groups, and the target's column again by the thread that has just written it
+      if (t_col >= 0)
+        store1(static_cast<TD*>(a.d[t_rk]) + i * a.ldd[t_rk] + t_col,
+               slope_at<kEnt>(slope, z_t) + (t_rk == rk_y && t_col == col_y ? w.w : 0.f));
+      if (!out && group_y >= 0 && group_y < g_hi - g_lo && group_y % kChunkGroups % kThreads == tid)
+        store1(static_cast<TD*>(a.d[rk_y]) + i * a.ldd[rk_y] + col_y, slope_at<kEnt>(slope, zy) + w.w);
     }
     if (!fine && lane == 0) raise_error(a.ctrl, FO_ERR_TIMEOUT, kSiteFull, blockIdx.x);
-    if (kMode == kLossPolicy && rank == 0 && warp == 0 && fine) {
-      // the row's team that comes last adds everyone's sums, in the order of the teams
-      int last = 0;
-      if (lane == 0) {
-        for (int k = 0; k < 4; ++k) a.part[team * 4 + k] = sums[k];
-        __threadfence();
-        last = atomicInc(a.ctrl + kCtrlDone, static_cast<unsigned>(teams - 1)) == static_cast<unsigned>(teams - 1);
-      }
-      if (__shfl_sync(0xffffffffu, last, 0)) {
-        __threadfence();
-        for (int k = 0; k < 4; ++k) {
-          double s = 0.0;
-          for (int64_t b = lane; b < teams; b += 32) s += __ldcg(a.part + b * 4 + k);
+    if (kMode == kLossPolicy && rank == 0) {
+      if (lane == 0)
+        for (int k = 0; k < 4; ++k) sm.sums[warp][k] = sums[k];
+      asm volatile("bar.sync 1, %0;" ::"n"(S::kAll) : "memory");
+      if (warp == 0 && fine) {
+        // the team that comes last adds everyone's sums, in the order of the teams
+        int last = 0;
+        if (lane == 0) {
+          for (int k = 0; k < 4; ++k) {
+            double s = 0.0;
+            for (int q = 0; q < kSets * kWarps; ++q) s += sm.sums[q][k];
+            a.part[team * 4 + k] = s;
+          }
+          __threadfence();
+          last = atomicInc(a.ctrl + kCtrlDone, static_cast<unsigned>(teams - 1)) == static_cast<unsigned>(teams - 1);
+        }
+        if (__shfl_sync(0xffffffffu, last, 0)) {
+          __threadfence();
+          for (int k = 0; k < 4; ++k) {
+            double s = 0.0;
+            for (int64_t b = lane; b < teams; b += 32) s += __ldcg(a.part + b * 4 + k);
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-          if (lane == 0) a.stats[k] = static_cast<float>(s);
+            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            if (lane == 0) a.stats[k] = static_cast<float>(s);
+          }
         }
       }
     }
@@ -650,32 +809,37 @@ void (*kernel_of(const LossKind& k))(LossArgs) {
 int loss_rows_parts(int num_sms) { return num_sms; }
 
 cudaError_t loss_rows_launch(LossArgs a, const LossKind& k, int num_sms, cudaStream_t s) {
+  const bool one = k.mode == kLossPolicy;
+  const int threads = one ? Shape<kLossPolicy>::kAll : Shape<kLossForward>::kAll;
+  const int smem = one ? Shape<kLossPolicy>::kSlots * kLossChunk + Shape<kLossPolicy>::kZeros
+                       : Shape<kLossForward>::kSlots * kLossChunk;
+  const int places = num_sms * (one ? Shape<kLossPolicy>::kPerSm : Shape<kLossForward>::kPerSm);
   const int cols = k.z32 ? Group<float>::kCols : Group<uint16_t>::kCols;
   for (int r = 0; r < a.P; ++r) a.groups[r + 1] = a.groups[r] + a.cols[r] / cols;
   const int64_t chunks = (a.groups[a.P] + kChunkGroups - 1) / kChunkGroups;
-  const bool resident = k.mode == kLossPolicy && a.d[0];  // a row waits in shared memory for its sum
-  // CTAs of a row: more where a row would leave little room for the next ones' copies, and where
-  // there are fewer rows than SMs
+  // CTAs of a row: as many as let both sets' rows wait in shared memory for their sums, and more where
+  // there are fewer rows than CTAs
   a.ctas = 1;
-  while (resident && a.ctas < kLossMaxCtas && chunks > a.ctas * kLossFit) a.ctas *= 2;
-  if (resident && chunks > static_cast<int64_t>(a.ctas) * (kLossSlots - 1)) {
-    a.twice = 1;
-    a.ctas = 1;
+  if (one && a.d[0]) {
+    while (a.ctas < kLossMaxCtas && chunks > a.ctas * kLossFit) a.ctas *= 2;
+    if (chunks > a.ctas * Shape<kLossPolicy>::kSlots) {
+      a.twice = 1;
+      a.ctas = 1;
+    }
   }
-  while (a.ctas < kLossMaxCtas && a.rows * a.ctas * 2 <= num_sms && a.groups[a.P] >= a.ctas * 2 * 32 * kLossWarps)
-    a.ctas *= 2;
+  while (a.ctas < kLossMaxCtas && a.rows * a.ctas * 2 <= places && a.groups[a.P] >= a.ctas * 2 * threads) a.ctas *= 2;
   void (*kernel)(LossArgs) = k.z32 ? (k.d32 ? kernel_of<float, float>(k) : kernel_of<float, uint16_t>(k))
                                    : (k.d32 ? kernel_of<uint16_t, float>(k) : kernel_of<uint16_t, uint16_t>(k));
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kLossSmem);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  // teams of CTAs that fit the GPU at once (clusters of 2 all SMs, of 4 144, of 8 120 of 152)
-  const int fit = num_sms * (a.ctas <= 2 ? 152 : a.ctas == 4 ? 144 : 120) / 152 / a.ctas;
+  // teams that fit the GPU at once (clusters of 2 all SMs, of 4 144, of 8 120 of 152)
+  const int fit = places * (a.ctas <= 2 ? 152 : a.ctas == 4 ? 144 : 120) / 152 / a.ctas;
   const int64_t teams = a.rows < 1 ? 1 : a.rows < fit ? a.rows : fit;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = dim3(static_cast<unsigned>(teams * a.ctas));
-  cfg.blockDim = dim3(kLossThreads);
-  cfg.dynamicSmemBytes = kLossSmem;
+  cfg.blockDim = dim3(threads + 32 * (one ? Shape<kLossPolicy>::kMore : Shape<kLossForward>::kMore));
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;

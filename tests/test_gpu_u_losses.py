@@ -444,7 +444,8 @@ def test_rows_behind_2_31_elements(ctx):
         z[at:at + 4000].normal_(generator=torch.Generator(device="cuda").manual_seed(at))
     y = torch.arange(m, dtype=torch.int32, device="cuda") * 7 % v
     y[::2] = -1
-    adv, old = torch.randn(m, device="cuda"), torch.full((m,), -11.0, device="cuda")
+    # (log-probabilities are near -11.6: ratios near a half, which a negative advantage would clip)
+    adv, old = 0.5 + torch.rand(m, device="cuda"), torch.full((m,), -11.0, device="cuda")
     rows = torch.tensor([1, 3, 32767, 32769, 39997, 39999], device="cuda")
     some = z[rows].clone()
     logp, stats = torch.empty(m, device="cuda"), torch.empty(4, device="cuda")
