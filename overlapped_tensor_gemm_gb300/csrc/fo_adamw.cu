@@ -26,6 +26,7 @@
 
 #include <cuda_fp8.h>
 
+#include "fo_attn_common.cuh"
 #include "fo_host.h"
 #include "fo_ptx.cuh"
 
@@ -34,7 +35,9 @@ namespace {
 
 constexpr int kBlock = 256;           // elements of a block: 8 per lane of a warp
 constexpr int kAdamThreads = 256;
+constexpr int kCtasPerSm = 4;
 constexpr int kListTensors = 400;     // tensors of one launch
+constexpr int kAhead = 4;             // blocks that a warp of the norm and of the unpacking loads at once
 constexpr float kMaxE4m3 = 448.f;
 constexpr float kOctaves = 24.f;      // v's values span at most 2^24
 
@@ -74,7 +77,8 @@ struct StepArgs {
 static_assert(sizeof(TensorList) + sizeof(StepArgs) <= 32764, "kernel parameters");
 
 // The tensor of block b: the last one that starts at or in front of it
-__device__ __forceinline__ int tensor_of(const TensorList& l, int64_t b) {
+template <typename List>
+__device__ __forceinline__ int tensor_of(const List& l, int64_t b) {
   int lo = 0, hi = l.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -91,96 +95,135 @@ __host__ __device__ __forceinline__ uint32_t scatter(uint32_t x) {
   return x ^ (x >> 16);
 }
 
+typedef uint64_t Pair;  // two fp32 values
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Pair sub2(Pair a, Pair b) {
+  Pair r;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Pair both(float f) { return pack2(f, f); }
+// (numbers below 2^-126 count as 0)
 __device__ __forceinline__ float fast_log2(float x) {
   float y;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float exact_exp2(float x) {  // subnormal results kept
-  float y;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ float fast_sqrt(float x) {
   float y;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float fast_inverse(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
-// 4 elements from p on, the first n of them inside the tensor
-__device__ __forceinline__ void load4(const float* p, int n, float (&v)[4]) {
-  if (n >= 4) {
-    const float4 q = *reinterpret_cast<const float4*>(p);
-    v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
-  } else {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = k < n ? p[k] : 0.f;
-  }
+// 4 elements from p on as they lie there, the first n of them inside the tensor.  (What is read is
+// converted later: a wait inside a condition would keep the next load back.)
+template <bool kFull>
+__device__ __forceinline__ float4 load4(const float* p, int n) {
+  if (kFull || n >= 4) return *reinterpret_cast<const float4*>(p);
+  return make_float4(0 < n ? p[0] : 0.f, 1 < n ? p[1] : 0.f, 2 < n ? p[2] : 0.f, 0.f);
 }
-__device__ __forceinline__ void load4(const uint16_t* p, int n, float (&v)[4]) {
-  if (n >= 4) {
-    const uint2 q = *reinterpret_cast<const uint2*>(p);
-    v[0] = __uint_as_float(q.x << 16);
-    v[1] = __uint_as_float(q.x & 0xFFFF0000u);
-    v[2] = __uint_as_float(q.y << 16);
-    v[3] = __uint_as_float(q.y & 0xFFFF0000u);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = k < n ? __uint_as_float(static_cast<uint32_t>(p[k]) << 16) : 0.f;
-  }
+template <bool kFull>
+__device__ __forceinline__ uint2 load4(const uint16_t* p, int n) {
+  if (kFull || n >= 4) return *reinterpret_cast<const uint2*>(p);
+  return make_uint2((0 < n ? p[0] : 0u) | (1 < n ? static_cast<uint32_t>(p[1]) << 16 : 0u), 2 < n ? p[2] : 0u);
 }
+template <bool kFull>
 __device__ __forceinline__ uint32_t load4(const uint8_t* p, int n) {
-  if (n >= 4) return *reinterpret_cast<const uint32_t*>(p);
-  uint32_t q = 0;
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (k < n) q |= static_cast<uint32_t>(p[k]) << (8 * k);
-  return q;
+  if (kFull || n >= 4) return *reinterpret_cast<const uint32_t*>(p);
+  return (0 < n ? p[0] : 0u) | (1 < n ? static_cast<uint32_t>(p[1]) << 8 : 0u) |
+         (2 < n ? static_cast<uint32_t>(p[2]) << 16 : 0u);
 }
-__device__ __forceinline__ void store4(float* p, int n, const float (&v)[4]) {
-  if (n >= 4) {
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+__device__ __forceinline__ void values(const float4& q, Pair (&v)[2]) {
+  v[0] = pack2(q.x, q.y);
+  v[1] = pack2(q.z, q.w);
+}
+__device__ __forceinline__ void values(const uint2& q, Pair (&v)[2]) {
+  v[0] = pack2(__uint_as_float(q.x << 16), __uint_as_float(q.x & 0xFFFF0000u));
+  v[1] = pack2(__uint_as_float(q.y << 16), __uint_as_float(q.y & 0xFFFF0000u));
+}
+template <bool kFull>
+__device__ __forceinline__ void store4(float* p, int n, const Pair (&v)[2]) {
+  float f[4];
+  unpack2(v[0], f[0], f[1]);
+  unpack2(v[1], f[2], f[3]);
+  if (kFull || n >= 4) {
+    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
   } else {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (k < n) p[k] = v[k];
+    for (int k = 0; k < 3; ++k)
+      if (k < n) p[k] = f[k];
   }
 }
-__device__ __forceinline__ void store4(uint16_t* p, int n, const float (&v)[4]) {
-  const uint32_t q[2] = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-  if (n >= 4) {
+template <bool kFull>
+__device__ __forceinline__ void store4(uint16_t* p, int n, const Pair (&v)[2]) {
+  uint32_t q[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    float x, y;
+    unpack2(v[k], x, y);
+    q[k] = pack_bf16x2(x, y);
+  }
+  if (kFull || n >= 4) {
     *reinterpret_cast<uint2*>(p) = make_uint2(q[0], q[1]);
   } else {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < 3; ++k)
       if (k < n) p[k] = static_cast<uint16_t>(q[k >> 1] >> (16 * (k & 1)));
   }
 }
+template <bool kFull>
 __device__ __forceinline__ void store4(uint8_t* p, int n, uint32_t q) {
-  if (n >= 4) {
+  if (kFull || n >= 4) {
     *reinterpret_cast<uint32_t*>(p) = q;
   } else {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < 3; ++k)
       if (k < n) p[k] = static_cast<uint8_t>(q >> (8 * k));
   }
 }
 
+// A half of `pair` in fp32 (an addition that takes one f16 operand: no conversion)
+__device__ __forceinline__ float low_half(uint32_t pair, float plus) {
+  float r;
+  asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; add.f32.f16 %0, l, %2;}" : "=f"(r) : "r"(pair), "f"(plus));
+  return r;
+}
+__device__ __forceinline__ float high_half(uint32_t pair, float plus) {
+  float r;
+  asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; add.f32.f16 %0, h, %2;}" : "=f"(r) : "r"(pair), "f"(plus));
+  return r;
+}
 // 4 e4m3 values
-__device__ __forceinline__ void from_e4m3(uint32_t q, float (&v)[4]) {
+__device__ __forceinline__ void from_e4m3(uint32_t q, Pair (&v)[2]) {
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const __half2_raw h =
         __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(q >> (16 * k)), __NV_E4M3);
-    const float2 f = __half22float2(__half2(h));
-    v[2 * k] = f.x;
-    v[2 * k + 1] = f.y;
+    const uint32_t pair = h.x | static_cast<uint32_t>(h.y) << 16;
+    v[k] = pack2(low_half(pair, 0.f), high_half(pair, 0.f));
   }
 }
-__device__ __forceinline__ float level(uint32_t code, float low, float gap) {
-  return code ? exact_exp2(fmaf(static_cast<float>(code - 1), gap, low)) : 0.f;
+// 4 codes of v as values: a code is the low byte of an f16 from 1024 on, where steps are 1
+__device__ __forceinline__ void from_levels(uint32_t q, float low, float gap, Pair (&v)[2]) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t pair = __byte_perm(q, 0x64646464u, k ? 0x4342 : 0x4140);
+    const Pair n = pack2(low_half(pair, -1025.f), high_half(pair, -1025.f));  // code - 1
+    float x, y, a, b;
+    unpack2(n, a, b);
+    unpack2(ffma2(n, both(gap), both(low)), x, y);
+    v[k] = pack2(a >= 0.f ? fast_exp2(x) : 0.f, b >= 0.f ? fast_exp2(y) : 0.f);
+  }
 }
-
 // x (at most 448) up or down to an e4m3 value: what a step holds below is cut off after a random
 // part of a step is added.  Below 2^-6 the steps stay 2^-9 wide, as they are from 2^-6 to 2^-5, so
 // there the sum with 2^-6 is cut.
@@ -188,6 +231,29 @@ __device__ __forceinline__ float cut_e4m3(float x, uint32_t half_word) {
   const float size = fminf(fabsf(x), kMaxE4m3), lift = size < 0.015625f ? 0.015625f : 0.f;
   const uint32_t q = (__float_as_uint(size + lift) + (half_word << 4)) & 0xFFF00000u;
   return x == x ? copysignf(__uint_as_float(q) - lift, x) : x;
+}
+// The codes of two v (low bytes).  y = (log2 v - low) / gap counts codes from 1; with s = y - 1/2 less
+// its nearest whole number w, y is w and a part s + 1/2; up with probability part - bend part (1 - part)
+// (the mean of the two values, not of their logarithms, is v: to first order in gap).
+struct Levels {
+  float per_gap, offset, bend;  // 1 / gap, -low / gap - 1/2, gap ln 2 / 2
+};
+__device__ __forceinline__ void levels_of(Pair v, const Levels& l, uint32_t word0, uint32_t word1, uint32_t (&code)[2]) {
+  const Pair magic = both(12582912.f);  // 1.5 2^23: a sum's last bits are the nearest whole number
+  float a, b, x, y;
+  unpack2(v, a, b);
+  unpack2(ffma2(pack2(fast_log2(a), fast_log2(b)), both(l.per_gap), both(l.offset)), x, y);
+  const Pair at = pack2(fminf(fmaxf(x, -0.5f), 253.5f), fminf(fmaxf(y, -0.5f), 253.5f));
+  const Pair sum = fadd2(at, magic), s = sub2(at, sub2(sum, magic));
+  const Pair part = ffma2(s, ffma2(s, both(l.bend), both(1.f)), both(fmaf(l.bend, -0.25f, 0.5f)));
+  const Pair r = fadd2(pack2(__uint_as_float(0x4B000000u | word0 >> 16), __uint_as_float(0x4B000000u | word1 >> 16)),
+                       both(-8388608.f));
+  float r0, r1, p0, p1;
+  unpack2(r, r0, r1);
+  unpack2(mul2(part, both(65536.f)), p0, p1);
+  unpack2(sum, x, y);
+  code[0] = a > 0.f ? __float_as_uint(x) + (r0 < p0 ? 2u : 1u) : 0u;
+  code[1] = b > 0.f ? __float_as_uint(y) + (r1 < p1 ? 2u : 1u) : 0u;
 }
 // A bf16 value next to w, by the upper half of `word`; infinities and NaN stay
 __device__ __forceinline__ float cut_bf16(float w, uint32_t word) {
@@ -205,23 +271,166 @@ __device__ __forceinline__ float correction(double beta, int64_t t) {
   return static_cast<float>(1.0 / (1.0 - p));
 }
 
-template <bool kP32, bool kG32, bool kHasMaster, bool k8>
-__global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_constant__ TensorList l,
-                                                             const __grid_constant__ StepArgs a, bool cut) {
+// What a step's blocks share
+struct Step {
+  float beta1, beta2, rest1, rest2, eps, decay, rate, fix2, c;
+  uint32_t key;
+  bool cut;
+};
+// One block, the first n of its elements inside the tensor.  Squares, roots and quotients keep to
+// numbers from 2^-126 on: a smaller v counts as that in the root (its update is smaller for it).
+template <bool kP32, bool kG32, bool kHasMaster, bool k8, bool kFull>
+__device__ __forceinline__ void step_block(const TensorRef& t, int64_t blk, int n, const Step& a) {
   typedef typename std::conditional<kP32, float, uint16_t>::type TP;
   typedef typename std::conditional<kG32, float, uint16_t>::type TG;
-  __shared__ float fixes[2];
+  typedef typename std::conditional<kHasMaster, float, TP>::type TW;
   const int lane = threadIdx.x & 31;
-  float c = a.grad_scale;
+  const int64_t at = blk * kBlock + lane * 4;
+  n -= lane * 4;
+  TW* const tw = (kHasMaster ? reinterpret_cast<TW*>(t.master) : static_cast<TW*>(t.param)) + at;
+  const TG* const tg = static_cast<const TG*>(t.grad) + at;
+  auto g0 = load4<kFull>(tg, n), g1 = load4<kFull>(tg + 128, n - 128);
+  auto w0 = load4<kFull>(tw, n), w1 = load4<kFull>(tw + 128, n - 128);
+  Pair g[4], w[4], m[4], v[4];
+  float keep1 = a.beta1;
+  if constexpr (k8) {
+    const uint8_t* const tm = static_cast<const uint8_t*>(t.m) + at;
+    const uint8_t* const tv = static_cast<const uint8_t*>(t.v) + at;
+    const uint32_t m0 = load4<kFull>(tm, n), m1 = load4<kFull>(tm + 128, n - 128);
+    const uint32_t v0 = load4<kFull>(tv, n), v1 = load4<kFull>(tv + 128, n - 128);
+    keep1 *= t.m_scale[blk];
+    const float2 r = reinterpret_cast<const float2*>(t.v_range)[blk];
+    from_e4m3(m0, reinterpret_cast<Pair(&)[2]>(m[0]));
+    from_e4m3(m1, reinterpret_cast<Pair(&)[2]>(m[2]));
+    from_levels(v0, r.x, r.y, reinterpret_cast<Pair(&)[2]>(v[0]));
+    from_levels(v1, r.x, r.y, reinterpret_cast<Pair(&)[2]>(v[2]));
+  } else {
+    const float* const tm = static_cast<const float*>(t.m) + at;
+    const float* const tv = static_cast<const float*>(t.v) + at;
+    const float4 m0 = load4<kFull>(tm, n), m1 = load4<kFull>(tm + 128, n - 128);
+    const float4 v0 = load4<kFull>(tv, n), v1 = load4<kFull>(tv + 128, n - 128);
+    values(m0, reinterpret_cast<Pair(&)[2]>(m[0]));
+    values(m1, reinterpret_cast<Pair(&)[2]>(m[2]));
+    values(v0, reinterpret_cast<Pair(&)[2]>(v[0]));
+    values(v1, reinterpret_cast<Pair(&)[2]>(v[2]));
+  }
+  values(g0, reinterpret_cast<Pair(&)[2]>(g[0]));
+  values(g1, reinterpret_cast<Pair(&)[2]>(g[2]));
+  values(w0, reinterpret_cast<Pair(&)[2]>(w[0]));
+  values(w1, reinterpret_cast<Pair(&)[2]>(w[2]));
+
+  // (the bits of values that are not negative are ordered as the values are; those of 0, less one,
+  // come last)
+  float top_m = 0.f;
+  uint32_t top_v = 0, min_v = 0xFFFFFFFFu;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const Pair x = mul2(g[q], both(a.c));
+    m[q] = ffma2(both(keep1), m[q], mul2(both(a.rest1), x));
+    v[q] = ffma2(both(a.beta2), v[q], mul2(mul2(both(a.rest2), x), x));
+    float x0, x1, y0, y1;
+    unpack2(v[q], x0, x1);
+    unpack2(mul2(pack2(fmaxf(x0, FLT_MIN), fmaxf(x1, FLT_MIN)), both(a.fix2)), y0, y1);
+    unpack2(fadd2(pack2(fast_sqrt(y0), fast_sqrt(y1)), both(a.eps)), y0, y1);
+    const Pair change = mul2(mul2(both(a.rate), m[q]), pack2(fast_inverse(y0), fast_inverse(y1)));
+    w[q] = sub2(w[q], ffma2(both(a.decay), w[q], change));
+    if (k8) {
+      top_v = max(top_v, max(__float_as_uint(x0), __float_as_uint(x1)));
+      min_v = min(min_v, min(__float_as_uint(x0) - 1u, __float_as_uint(x1) - 1u));
+      unpack2(m[q], y0, y1);
+      top_m = fmax3(top_m, fabsf(y0), fabsf(y1));
+    }
+  }
+  uint32_t word[8];
+  if (k8 || a.cut) {
+    const uint32_t base =
+        scatter(scatter(a.key + t.index) + static_cast<uint32_t>(blk)) + static_cast<uint32_t>(lane * 4) * 0x9E3779B9u;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) word[k] = scatter(base + static_cast<uint32_t>((k & 4) * 32 + (k & 3)) * 0x9E3779B9u);
+  }
+  if constexpr (k8) {
+    top_m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top_m)));
+    top_v = __reduce_max_sync(0xffffffffu, top_v);
+    min_v = __reduce_min_sync(0xffffffffu, min_v);
+    float scale = 0.f, inv_scale = 0.f, low = 0.f, gap = 0.f;
+    Levels l = {0.f, -0.5f, 0.f};
+    if (top_m > 1e-30f) {  // smaller ones are kept as zeros
+      scale = top_m * (1.f / kMaxE4m3);
+      inv_scale = __fdividef(kMaxE4m3, top_m);
+    }
+    if (top_v != 0) {
+      const float top = fast_log2(fmaxf(__uint_as_float(top_v), FLT_MIN));
+      low = fmaxf(fast_log2(fmaxf(__uint_as_float(min_v + 1u), FLT_MIN)), top - kOctaves);
+      gap = (top - low) * (1.f / 254.f);
+      if (gap > 0.f) {
+        l.per_gap = __fdividef(1.f, gap);
+        l.offset = -low * l.per_gap - 0.5f;
+        l.bend = 0.34657359f * gap;
+      }
+    }
+    uint8_t* const tm = static_cast<uint8_t*>(t.m) + at;
+    uint8_t* const tv = static_cast<uint8_t*>(t.v) + at;
+#pragma unroll
+    for (int q = 0; q < 4; q += 2) {
+      uint32_t c0[2], c1[2], e[2];
+      levels_of(v[q], l, word[2 * q], word[2 * q + 1], c0);
+      levels_of(v[q + 1], l, word[2 * q + 2], word[2 * q + 3], c1);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float x, y;
+        unpack2(mul2(m[q + k], both(inv_scale)), x, y);
+        e[k] = __nv_cvt_float2_to_fp8x2(make_float2(cut_e4m3(x, word[2 * q + 2 * k] & 0xFFFFu),
+                                                    cut_e4m3(y, word[2 * q + 2 * k + 1] & 0xFFFFu)),
+                                        __NV_SATFINITE, __NV_E4M3);
+      }
+      store4<kFull>(tm + q * 64, n - q * 64, e[0] | e[1] << 16);
+      store4<kFull>(tv + q * 64, n - q * 64,
+                    __byte_perm(__byte_perm(c0[0], c0[1], 0x0040), __byte_perm(c1[0], c1[1], 0x0040), 0x5410));
+    }
+    if (lane == 0) {
+      t.m_scale[blk] = scale;
+      reinterpret_cast<float2*>(t.v_range)[blk] = make_float2(low, gap);
+    }
+  } else {
+    float* const tm = static_cast<float*>(t.m) + at;
+    float* const tv = static_cast<float*>(t.v) + at;
+#pragma unroll
+    for (int q = 0; q < 4; q += 2) {
+      store4<kFull>(tm + q * 64, n - q * 64, reinterpret_cast<Pair(&)[2]>(m[q]));
+      store4<kFull>(tv + q * 64, n - q * 64, reinterpret_cast<Pair(&)[2]>(v[q]));
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < 4; q += 2) {
+    if (kHasMaster) store4<kFull>(t.master + at + q * 64, n - q * 64, reinterpret_cast<Pair(&)[2]>(w[q]));
+    if (!kP32 && !kHasMaster && a.cut) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float x, y;
+        unpack2(w[q + k], x, y);
+        w[q + k] = pack2(cut_bf16(x, word[2 * q + 2 * k] * 0x9E3779B9u), cut_bf16(y, word[2 * q + 2 * k + 1] * 0x9E3779B9u));
+      }
+    }
+    store4<kFull>(static_cast<TP*>(t.param) + at + q * 64, n - q * 64, reinterpret_cast<Pair(&)[2]>(w[q]));
+  }
+}
+
+template <bool kP32, bool kG32, bool kHasMaster, bool k8>
+__global__ void __launch_bounds__(kAdamThreads, kCtasPerSm)
+    adamw_kernel(const __grid_constant__ TensorList l, const __grid_constant__ StepArgs a, bool cut) {
+  __shared__ float fixes[2];
+  Step s;
+  s.c = a.grad_scale;
   if (a.norm) {
     const float norm = *a.norm;
     if (!(norm <= FLT_MAX)) return;  // infinite or NaN: nothing is written
     const float whole = norm * fabsf(a.grad_scale);
-    if (a.max_norm > 0.f && whole > a.max_norm) c *= a.max_norm / whole;
+    if (a.max_norm > 0.f && whole > a.max_norm) s.c *= a.max_norm / whole;
   }
   const float lr = a.lr_dev ? *a.lr_dev : a.lr;
   const int64_t step = a.step_dev ? *a.step_dev : a.step;
-  float fix1 = a.fix1, fix2 = a.fix2;
+  float fix1 = a.fix1;
+  s.fix2 = a.fix2;
   if (a.step_dev) {
     if (step < 1) {
       if (blockIdx.x == 0 && threadIdx.x == 0)
@@ -231,10 +440,17 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_consta
     if (threadIdx.x < 2) fixes[threadIdx.x] = correction(threadIdx.x ? a.exact2 : a.exact1, step);
     __syncthreads();
     fix1 = fixes[0];
-    fix2 = fixes[1];
+    s.fix2 = fixes[1];
   }
-  const uint32_t key = scatter(scatter(a.seed_low ^ scatter(static_cast<uint32_t>(step))) ^ a.seed_high);
-  const float decay = lr * a.weight_decay, rate = lr * fix1;
+  s.beta1 = a.beta1;
+  s.beta2 = a.beta2;
+  s.rest1 = a.rest1;
+  s.rest2 = a.rest2;
+  s.eps = a.eps;
+  s.decay = lr * a.weight_decay;
+  s.rate = lr * fix1;
+  s.key = scatter(scatter(a.seed_low ^ scatter(static_cast<uint32_t>(step))) ^ a.seed_high);
+  s.cut = cut;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kAdamThreads / 32);
   int64_t b = static_cast<int64_t>(blockIdx.x) * (kAdamThreads / 32) + (threadIdx.x >> 5);
   if (b >= l.blocks) return;
@@ -242,117 +458,11 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_consta
   for (; b < l.blocks; b += warps) {
     while (i + 1 < l.count && l.t[i + 1].first <= b) ++i;
     const TensorRef& t = l.t[i];
-    const int64_t blk = b - t.first, at = blk * kBlock;
-    const int64_t left = t.n - at;
-    const int n = left < kBlock ? static_cast<int>(left) : kBlock;
-    float w[2][4], g[2][4], m[2][4], v[2][4];
-    float m_scale = 0.f, low = 0.f, gap = 0.f;
-    if (k8) {
-      m_scale = t.m_scale[blk];
-      const float2 r = reinterpret_cast<const float2*>(t.v_range)[blk];
-      low = r.x;
-      gap = r.y;
-    }
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int e = q * 128 + lane * 4, in = n - e;
-      load4(static_cast<const TG*>(t.grad) + at + e, in, g[q]);
-      if (kHasMaster) {
-        load4(t.master + at + e, in, w[q]);
-      } else {
-        load4(static_cast<const TP*>(t.param) + at + e, in, w[q]);
-      }
-      if (k8) {
-        from_e4m3(load4(static_cast<const uint8_t*>(t.m) + at + e, in), m[q]);
-        const uint32_t codes = load4(static_cast<const uint8_t*>(t.v) + at + e, in);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          m[q][k] *= m_scale;
-          v[q][k] = level(codes >> (8 * k) & 0xFFu, low, gap);
-        }
-      } else {
-        load4(static_cast<const float*>(t.m) + at + e, in, m[q]);
-        load4(static_cast<const float*>(t.v) + at + e, in, v[q]);
-      }
-    }
-    float top_m = 0.f, top_v = 0.f, min_v = INFINITY;
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float x = g[q][k] * c;
-        m[q][k] = fmaf(a.beta1, m[q][k], a.rest1 * x);
-        v[q][k] = fmaf(a.beta2, v[q][k], a.rest2 * x * x);
-        const float root = fast_sqrt(v[q][k] * fix2) + a.eps;
-        w[q][k] = w[q][k] - fmaf(decay, w[q][k], __fdividef(rate * m[q][k], root));
-        if (k8) {
-          top_m = fmaxf(top_m, fabsf(m[q][k]));
-          top_v = fmaxf(top_v, v[q][k]);
-          if (v[q][k] > 0.f) min_v = fminf(min_v, v[q][k]);
-        }
-      }
-    }
-    float scale = 0.f, inv_scale = 0.f, inv_gap = 0.f, bend = 0.f;
-    uint32_t base = 0;
-    if (k8) {
-      // (bits of values that are not negative are ordered as the values are)
-      top_m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top_m)));
-      top_v = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top_v)));
-      min_v = __uint_as_float(__reduce_min_sync(0xffffffffu, __float_as_uint(min_v)));
-      if (top_m > 1e-30f) {  // smaller ones are kept as zeros
-        scale = top_m / kMaxE4m3;
-        inv_scale = kMaxE4m3 / top_m;
-      }
-      low = gap = 0.f;
-      if (top_v > 0.f) {
-        const float top = fast_log2(top_v);
-        low = fmaxf(fast_log2(min_v), top - kOctaves);
-        gap = (top - low) * (1.f / 254.f);
-        inv_gap = gap > 0.f ? 1.f / gap : 0.f;
-        bend = 0.34657359f * gap;  // ln 2 / 2
-      }
-    }
-    if (k8 || cut) base = scatter(scatter(key + t.index) + static_cast<uint32_t>(blk));
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int e = q * 128 + lane * 4, in = n - e;
-      uint32_t word[4] = {0, 0, 0, 0};
-      if (k8 || cut) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) word[k] = scatter(base + static_cast<uint32_t>(e + k) * 0x9E3779B9u);
-      }
-      if (kHasMaster) store4(t.master + at + e, in, w[q]);
-      if (!kP32 && !kHasMaster && cut) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) w[q][k] = cut_bf16(w[q][k], word[k] * 0x9E3779B9u);
-      }
-      store4(static_cast<TP*>(t.param) + at + e, in, w[q]);
-      if (k8) {
-        uint32_t mq[2], vq = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          m[q][k] = cut_e4m3(m[q][k] * inv_scale, word[k] & 0xFFFFu);
-          const float y = fminf(fmaxf((fast_log2(v[q][k]) - low) * inv_gap, 0.f), 254.f);
-          const float whole = floorf(y);
-          float part = y - whole;
-          part = part - bend * part * (1.f - part);
-          const float up = static_cast<float>(word[k] >> 16) * (1.f / 65536.f) < part ? 1.f : 0.f;
-          const uint32_t code = v[q][k] > 0.f ? static_cast<uint32_t>(whole + up) + 1u : 0u;
-          vq |= code << (8 * k);
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          mq[k] = __nv_cvt_float2_to_fp8x2(make_float2(m[q][2 * k], m[q][2 * k + 1]), __NV_SATFINITE, __NV_E4M3);
-        store4(static_cast<uint8_t*>(t.m) + at + e, in, mq[0] | mq[1] << 16);
-        store4(static_cast<uint8_t*>(t.v) + at + e, in, vq);
-      } else {
-        store4(static_cast<float*>(t.m) + at + e, in, m[q]);
-        store4(static_cast<float*>(t.v) + at + e, in, v[q]);
-      }
-    }
-    if (k8 && lane == 0) {
-      t.m_scale[blk] = scale;
-      reinterpret_cast<float2*>(t.v_range)[blk] = make_float2(low, gap);
+    const int64_t blk = b - t.first, left = t.n - blk * kBlock;
+    if (left >= kBlock) {
+      step_block<kP32, kG32, kHasMaster, k8, true>(t, blk, kBlock, s);
+    } else {
+      step_block<kP32, kG32, kHasMaster, k8, false>(t, blk, static_cast<int>(left), s);
     }
   }
 }
@@ -388,27 +498,46 @@ __global__ void __launch_bounds__(kAdamThreads) grad_norm_kernel(const __grid_co
   double total = 0.0;
   if (b < l.blocks) {
     int i = tensor_of(l, b);
-    float sum = 0.f;
-    for (int turn = 0; b < l.blocks; b += warps) {
-      while (i + 1 < l.count && l.t[i + 1].first <= b) ++i;
-      const TensorRef& t = l.t[i];
-      const int64_t at = (b - t.first) * kBlock, left = t.n - at;
-      const int n = left < kBlock ? static_cast<int>(left) : kBlock;
+    while (b < l.blocks) {
+      float sum = 0.f;  // at most 512 squares in fp32
+#pragma unroll 1
+      for (int turn = 0; turn < 16 && b < l.blocks; ++turn) {
+        while (i + 1 < l.count && l.t[i + 1].first <= b) ++i;
+        const TensorRef& t = l.t[i];
+        const int64_t blk = b - t.first, left = t.n - blk * kBlock, ahead = (kAhead - 1) * warps * kBlock;
+        const TG* const tg = static_cast<const TG*>(t.grad) + blk * kBlock + lane * 4;
+        Pair s = 0;
+        if (left >= ahead + kBlock) {  // the warp's next blocks are whole ones of this tensor
+          decltype(load4<true>(tg, 0)) g[kAhead][2];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int e = q * 128 + lane * 4;
-        float g[4];
-        load4(static_cast<const TG*>(t.grad) + at + e, n - e, g);
+          for (int u = 0; u < kAhead; ++u)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) sum = fmaf(g[k], g[k], sum);
+            for (int q = 0; q < 2; ++q) g[u][q] = load4<true>(tg + u * warps * kBlock + q * 128, 4);
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              Pair v[2];
+              values(g[u][q], v);
+              s = ffma2(v[0], v[0], ffma2(v[1], v[1], s));
+            }
+          b += kAhead * warps;
+        } else {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            Pair v[2];
+            const int64_t in = left - lane * 4 - q * 128;
+            values(load4<false>(tg + q * 128, in < 4 ? static_cast<int>(in < 0 ? 0 : in) : 4), v);
+            s = ffma2(v[0], v[0], ffma2(v[1], v[1], s));
+          }
+          b += warps;
+        }
+        float x, y;
+        unpack2(s, x, y);
+        sum += x + y;
       }
-      if (++turn == 64) {  // at most 512 squares in a row in fp32
-        total += sum;
-        sum = 0.f;
-        turn = 0;
-      }
+      total += sum;
     }
-    total += sum;
   }
   total = block_sum(total, buf);
   if (threadIdx.x == 0) {
@@ -446,35 +575,55 @@ struct UnpackList {
 };
 static_assert(sizeof(UnpackList) <= 32764, "kernel parameters");
 
-template <typename T>
-__global__ void __launch_bounds__(kAdamThreads) unpack_kernel(const __grid_constant__ UnpackList l) {
+// count blocks, `pitch` blocks apart; the first n elements of each are inside the tensor
+template <typename T, int count, bool kFull>
+__device__ __forceinline__ void unpack_blocks(const UnpackList::Ref& t, int64_t blk, int64_t pitch, int n) {
   const int lane = threadIdx.x & 31;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kAdamThreads / 32);
-  for (int64_t b = static_cast<int64_t>(blockIdx.x) * (kAdamThreads / 32) + (threadIdx.x >> 5); b < l.blocks;
-       b += warps) {
-    int lo = 0, hi = l.count - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (l.t[mid].first <= b) lo = mid; else hi = mid - 1;
-    }
-    const UnpackList::Ref& t = l.t[lo];
-    const int64_t blk = b - t.first, at = blk * kBlock, left = t.n - at;
-    const int n = left < kBlock ? static_cast<int>(left) : kBlock;
-    const float scale = t.m_scale[blk];
-    const float2 r = reinterpret_cast<const float2*>(t.v_range)[blk];
+  const int64_t at = blk * kBlock + lane * 4;
+  n -= lane * 4;
+  uint32_t mq[count][2], vq[count][2];
+  float scale[count];
+  float2 range[count];
+#pragma unroll
+  for (int u = 0; u < count; ++u) {
+    scale[u] = t.m_scale[blk + u * pitch];
+    range[u] = reinterpret_cast<const float2*>(t.v_range)[blk + u * pitch];
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      const int e = q * 128 + lane * 4, in = n - e;
-      float m[4], v[4];
-      from_e4m3(load4(t.m + at + e, in), m);
-      const uint32_t codes = load4(t.v + at + e, in);
+      mq[u][q] = load4<kFull>(t.m + at + u * pitch * kBlock + q * 128, n - q * 128);
+      vq[u][q] = load4<kFull>(t.v + at + u * pitch * kBlock + q * 128, n - q * 128);
+    }
+  }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        m[k] *= scale;
-        v[k] = level(codes >> (8 * k) & 0xFFu, r.x, r.y);
-      }
-      store4(static_cast<T*>(t.m_out) + at + e, in, m);
-      store4(static_cast<T*>(t.v_out) + at + e, in, v);
+  for (int u = 0; u < count; ++u)
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      Pair m[2], v[2];
+      from_e4m3(mq[u][q], m);
+      from_levels(vq[u][q], range[u].x, range[u].y, v);
+      m[0] = mul2(m[0], both(scale[u]));
+      m[1] = mul2(m[1], both(scale[u]));
+      store4<kFull>(static_cast<T*>(t.m_out) + at + u * pitch * kBlock + q * 128, n - q * 128, m);
+      store4<kFull>(static_cast<T*>(t.v_out) + at + u * pitch * kBlock + q * 128, n - q * 128, v);
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kAdamThreads) unpack_kernel(const __grid_constant__ UnpackList l) {
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kAdamThreads / 32);
+  int64_t b = static_cast<int64_t>(blockIdx.x) * (kAdamThreads / 32) + (threadIdx.x >> 5);
+  if (b >= l.blocks) return;
+  int i = tensor_of(l, b);
+  while (b < l.blocks) {
+    while (i + 1 < l.count && l.t[i + 1].first <= b) ++i;
+    const UnpackList::Ref& t = l.t[i];
+    const int64_t blk = b - t.first, left = t.n - blk * kBlock, ahead = (kAhead - 1) * warps * kBlock;
+    if (left >= ahead + kBlock) {  // the warp's next blocks are whole ones of this tensor
+      unpack_blocks<T, kAhead, true>(t, blk, warps, kBlock);
+      b += kAhead * warps;
+    } else {
+      unpack_blocks<T, 1, false>(t, blk, 0, static_cast<int>(left < kBlock ? left : kBlock));
+      b += warps;
     }
   }
 }
@@ -491,7 +640,6 @@ StepKernel step_kernel(int kind) {
   return kind & kMaster ? step_kernel_of<false, true>(kind) : step_kernel_of<false, false>(kind);
 }
 
-constexpr int kCtasPerSm = 4;
 int grid_for(fo_ctx* ctx, int64_t blocks) {
   const int64_t ctas = (blocks + kAdamThreads / 32 - 1) / (kAdamThreads / 32);
   const int64_t most = static_cast<int64_t>(host_num_sms(ctx)) * kCtasPerSm;
