@@ -28,47 +28,79 @@ __device__ __forceinline__ float pair_loss(int kind, float beta, float gap, floa
   return fmaxf(-x, 0.f) + log1pf(e);
 }
 
-// Fixed-order sum over the CTA, in every thread
-__device__ __forceinline__ double block_sum(double v, double* buf) {
+// A number as the sum of two fp32 values, |lo| at most half a step of hi (sums of error-free
+// transformations, Knuth; fp64 arithmetic is slow here)
+struct Wide {
+  float hi, lo;
+};
+__device__ __forceinline__ Wide plus(const Wide& a, const Wide& b) {
+  const float s = a.hi + b.hi, t = s - a.hi;
+  const float lo = ((a.hi - (s - t)) + (b.hi - t)) + (a.lo + b.lo), hi = s + lo;
+  return Wide{hi, lo - (hi - s)};
+}
+__device__ __forceinline__ Wide wide(float v) { return Wide{v, 0.f}; }
+// Over a warp, in every lane
+__device__ __forceinline__ Wide warp_sum(Wide v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = 0.0;
-  for (int w = 0; w < kPairThreads / 32; ++w) v += buf[w];
+  for (int o = 16; o > 0; o >>= 1)
+    v = plus(v, Wide{__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)});
   return v;
 }
 
-// One CTA per pair: scores of its two sequences, loss and coefficient; the last CTA averages the
-// losses in order.  A pair's gap is a small difference of long sums: the log-probabilities enter as
-// the two numbers that they are the difference of, unrounded, and are summed in fp64.
+// One CTA per pair, half of it per sequence: scores, loss and coefficient; the last CTA averages the
+// losses in order.  A pair's gap is a small difference of long sums: the log-probabilities enter as the
+// two numbers that they are the difference of, unrounded (in log2), and are summed in twice fp32.
 __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constant__ PairArgs a) {
-  __shared__ double buf[kPairThreads / 32];
-  __shared__ bool last;
-  int bad = 0;
-  for (int i = threadIdx.x; i < 2 * a.pairs + 1; i += blockDim.x) {
-    const int32_t v = a.offsets[i];
-    bad |= v < 0 || v > a.rows || (i > 0 && a.offsets[i - 1] > v);
+  constexpr int kHalf = kPairThreads / 2, kWarps = kHalf / 32;
+  __shared__ Wide logs[2][kWarps], refs[2][kWarps];
+  __shared__ int counted[2][kWarps];
+  let_next_start();
+  wait_for_previous();
+  if (!*a.fine) return;
+  const int half = threadIdx.x / kHalf, at = threadIdx.x % kHalf, lane = threadIdx.x & 31;
+  const int seq = blockIdx.x + half * a.pairs, end = a.offsets[seq + 1];
+  Wide log = {0.f, 0.f}, ref = {0.f, 0.f};
+  int n = 0;
+#pragma unroll 4
+  for (int i = a.offsets[seq] + at; i < end; i += kHalf) {
+    const int32_t y = a.targets[i];
+    const float4 st = a.stat[i];  // (rows that do not count: 0)
+    const float r = a.ref_logp ? a.ref_logp[i] : 0.f;
+    const bool on = y >= 0 && y < a.vocab;
+    log = plus(log, plus(wide(on ? st.z : 0.f), wide(on ? -st.y : 0.f)));
+    ref = plus(ref, wide(on ? r : 0.f));
+    n += on;
   }
-  if (__syncthreads_or(bad)) return;  // reported by the row kernel
-  double score[2], share[2];
-  for (int k = 0; k < 2; ++k) {
-    const int seq = blockIdx.x + k * a.pairs;
-    double sum = 0.0;
-    int n = 0;
-    for (int i = a.offsets[seq] + threadIdx.x; i < a.offsets[seq + 1]; i += blockDim.x) {
-      const int32_t y = a.targets[i];
-      if (y < 0 || y >= a.vocab) continue;
-      const float4 st = a.stat[i];
-      sum += (static_cast<double>(st.z) - st.y) * 0.69314718055994531 - (a.ref_logp ? a.ref_logp[i] : 0.f);
-      ++n;
-    }
-    const double count = block_sum(n, buf);
-    share[k] = a.average ? 1.0 / (count > 1.0 ? count : 1.0) : 1.0;
-    score[k] = block_sum(sum, buf) * share[k];
+  log = warp_sum(log);
+  ref = warp_sum(ref);
+  n = __reduce_add_sync(0xffffffffu, n);
+  if (lane == 0) {
+    logs[half][at >> 5] = log;
+    refs[half][at >> 5] = ref;
+    counted[half][at >> 5] = n;
   }
+  __syncthreads();
+  if (threadIdx.x >= 32) return;
+  int last = 0;
   if (threadIdx.x == 0) {
+    double score[2];
+    float share[2];
+    for (int h = 0; h < 2; ++h) {
+      log = logs[h][0];
+      ref = refs[h][0];
+      n = counted[h][0];
+      for (int w = 1; w < kWarps; ++w) {
+        log = plus(log, logs[h][w]);
+        ref = plus(ref, refs[h][w]);
+        n += counted[h][w];
+      }
+      score[h] = (static_cast<double>(log.hi) + log.lo) * 0.69314718055994531 - (static_cast<double>(ref.hi) + ref.lo);
+      share[h] = 1.f;
+      if (a.average) {
+        score[h] /= n > 1 ? n : 1;
+        share[h] = 1.f / static_cast<float>(n > 1 ? n : 1);
+      }
+    }
     const float gap = static_cast<float>(score[0] - score[1] - a.margin);
     float slope, back;
     float loss = pair_loss(a.kind, a.beta, gap, &slope);
@@ -76,21 +108,20 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constan
       loss = (1.f - a.smoothing) * loss + a.smoothing * pair_loss(a.kind, a.beta, -gap, &back);
       slope = (1.f - a.smoothing) * slope - a.smoothing * back;
     }
-    const double each = slope / static_cast<double>(a.pairs);
-    a.coef[blockIdx.x] = static_cast<float>(each * share[0]);
-    a.coef[blockIdx.x + a.pairs] = static_cast<float>(-each * share[1]);
+    const float each = slope / static_cast<float>(a.pairs);
+    a.coef[blockIdx.x] = each * share[0];
+    a.coef[blockIdx.x + a.pairs] = -each * share[1];
     if (a.margins) a.margins[blockIdx.x] = a.beta * gap;
     a.pair_loss[blockIdx.x] = loss;
     __threadfence();
     last = atomicInc(a.ctrl + kCtrlDone, gridDim.x - 1) == gridDim.x - 1;
   }
-  __syncthreads();
-  if (!last) return;
+  if (!__shfl_sync(0xffffffffu, last, 0)) return;
   __threadfence();
-  double sum = 0.0;
-  for (int i = threadIdx.x; i < a.pairs; i += blockDim.x) sum += __ldcg(a.pair_loss + i);
-  sum = block_sum(sum, buf);
-  if (threadIdx.x == 0) a.loss[0] = static_cast<float>(sum / a.pairs);
+  Wide sum = {0.f, 0.f};
+  for (int i = lane; i < a.pairs; i += 32) sum = plus(sum, wide(__ldcg(a.pair_loss + i)));
+  sum = warp_sum(sum);
+  if (lane == 0) a.loss[0] = (sum.hi + sum.lo) / static_cast<float>(a.pairs);
 }
 
 // ---------------------------------------------------------------------------
@@ -320,7 +351,7 @@ fo_status fo_preference_loss(fo_ctx* ctx, const fo_mat* logits, int P, const int
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // statistics of every row; coefficients and losses of the pairs
   void* work = nullptr;
-  FO_TRY_HOST(host_buffer_kept(ctx, kSlotLoss, static_cast<size_t>(a.rows * 16 + seqs * 4 + num_pairs * 4), s, &work));
+  FO_TRY_HOST(host_buffer_kept(ctx, kSlotLoss, static_cast<size_t>(a.rows * 16 + seqs * 4 + num_pairs * 4 + 4), s, &work));
   float4* stat = static_cast<float4*>(work);
   PairArgs p;
   std::memset(&p, 0, sizeof(p));
@@ -340,6 +371,8 @@ fo_status fo_preference_loss(fo_ctx* ctx, const fo_mat* logits, int P, const int
   p.pair_loss = p.coef + seqs;
   p.margins = margins;
   p.loss = loss;
+  a.fine = reinterpret_cast<int32_t*>(p.pair_loss + num_pairs);
+  p.fine = a.fine;
   p.ctrl = a.ctrl = host_ctrl(ctx);
   a.offsets = offsets;
   a.pairs = num_pairs;
@@ -349,13 +382,24 @@ fo_status fo_preference_loss(fo_ctx* ctx, const fo_mat* logits, int P, const int
   a.logp = logp;
   k.mode = kLossForward;
   FO_TRY_HOST(run_rows(ctx, a, k, s));
-  pair_kernel<<<num_pairs, kPairThreads, 0, s>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(num_pairs);
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, pair_kernel, p);
+  if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return host_fail(FO_ERR_CUDA, cudaGetErrorString(e));
   if (!dlogits) return FO_OK;
   back.coef = p.coef;
   back.backwards = 1;  // the rows that were read last may still be in L2
   k.mode = kLossBackward;
+  k.early = true;
   return run_rows(ctx, back, k, s);
 }
 

@@ -59,6 +59,7 @@ struct LossArgs {
   const int32_t* offsets;     // packed sequences: rows offsets[0] .. offsets[2 pairs] take part
   int32_t pairs;
   const float* coef;          // a of every sequence's counted rows
+  int32_t* fine;              // whether the offsets are (the statistics' launch writes it, the next two read it)
   uint64_t timeout_ns;
   uint32_t* ctrl;
 };
@@ -72,6 +73,7 @@ struct PairArgs {
   const float4* stat;
   const float* ref_logp;
   float beta, smoothing, margin;
+  const int32_t* fine;
   float* coef;                // [2 pairs]
   float* pair_loss;           // [pairs]
   float* margins;
@@ -83,7 +85,13 @@ struct LossKind {
   bool z32, d32;   // types of logits and gradients
   int mode;
   bool entropy;    // the entropy is wanted or has a gradient
+  bool early;      // may start while the launch in front of it ends (it waits for that one's results itself)
 };
+
+// Between the launches of one call: what follows may start; wait for what is in front
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // fo_loss_rows.cu
 cudaError_t loss_rows_launch(LossArgs a, const LossKind& k, int num_sms, cudaStream_t s);
 int loss_rows_parts(int num_sms);   // rows of LossArgs::part that any launch may use

@@ -149,6 +149,13 @@ __device__ __forceinline__ void store_group(float* p, const Pair (&v)[kPairs]) {
   }
 }
 
+// The sum over each eight lanes, in all of them
+__device__ __forceinline__ double eighth_sum(double v) {
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
 // What is subtracted for a reference m: finite also where every column is -infinity
 __device__ __forceinline__ float base_of(float m) { return fmaxf(m, -FLT_MAX); }
 
@@ -382,9 +389,13 @@ __global__ void __launch_bounds__(Shape<kMode>::kAll + 32 * Shape<kMode>::kMore,
     *reinterpret_cast<uint4*>(ring + kSlots * kLossChunk + k) = make_uint4(0, 0, 0, 0);
   if (S::kZeros) fence_proxy_async_shared();
   int64_t row0 = 0, rows = a.rows;
+  if (kMode == kLossForward) let_next_start();
+  if (kMode == kLossBackward && a.offsets) wait_for_previous();
   if (a.offsets) {
     // (every CTA sees the same offsets: all of them leave)
-    if (!offsets_fine(a.offsets, 2 * a.pairs + 1, a.rows, a.ctrl)) return;
+    const bool fine = kStat ? offsets_fine(a.offsets, 2 * a.pairs + 1, a.rows, a.ctrl) : *a.fine != 0;
+    if (kStat && blockIdx.x == 0 && threadIdx.x == 0) *a.fine = fine;
+    if (!fine) return;
     row0 = a.offsets[0];
     rows = a.offsets[2 * a.pairs] - row0;
   }
@@ -765,26 +776,26 @@ __global__ void __launch_bounds__(Shape<kMode>::kAll + 32 * Shape<kMode>::kMore,
         for (int k = 0; k < 4; ++k) sm.sums[warp][k] = sums[k];
       asm volatile("bar.sync 1, %0;" ::"n"(S::kAll) : "memory");
       if (warp == 0 && fine) {
-        // the team that comes last adds everyone's sums, in the order of the teams
+        // eight lanes for each of the four values; the team that comes last adds everyone's sums, in
+        // the order of the teams
+        const int k = lane >> 3;
+        double s = 0.0;
+        for (int q = lane & 7; q < kSets * kWarps; q += 8) s += sm.sums[q][k];
+        s = eighth_sum(s);
         int last = 0;
-        if (lane == 0) {
-          for (int k = 0; k < 4; ++k) {
-            double s = 0.0;
-            for (int q = 0; q < kSets * kWarps; ++q) s += sm.sums[q][k];
-            a.part[team * 4 + k] = s;
-          }
+        if ((lane & 7) == 0) {
+          a.part[team * 4 + k] = s;
           __threadfence();
-          last = atomicInc(a.ctrl + kCtrlDone, static_cast<unsigned>(teams - 1)) == static_cast<unsigned>(teams - 1);
         }
+        __syncwarp();
+        if (lane == 0)
+          last = atomicInc(a.ctrl + kCtrlDone, static_cast<unsigned>(teams - 1)) == static_cast<unsigned>(teams - 1);
         if (__shfl_sync(0xffffffffu, last, 0)) {
           __threadfence();
-          for (int k = 0; k < 4; ++k) {
-            double s = 0.0;
-            for (int64_t b = lane; b < teams; b += 32) s += __ldcg(a.part + b * 4 + k);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            if (lane == 0) a.stats[k] = static_cast<float>(s);
-          }
+          s = 0.0;
+          for (int64_t b = lane & 7; b < teams; b += 8) s += __ldcg(a.part + b * 4 + k);
+          s = eighth_sum(s);
+          if ((lane & 7) == 0) a.stats[k] = static_cast<float>(s);
         }
       }
     }
@@ -817,36 +828,56 @@ cudaError_t loss_rows_launch(LossArgs a, const LossKind& k, int num_sms, cudaStr
   const int cols = k.z32 ? Group<float>::kCols : Group<uint16_t>::kCols;
   for (int r = 0; r < a.P; ++r) a.groups[r + 1] = a.groups[r] + a.cols[r] / cols;
   const int64_t chunks = (a.groups[a.P] + kChunkGroups - 1) / kChunkGroups;
-  // CTAs of a row: as many as let both sets' rows wait in shared memory for their sums, and more where
-  // there are fewer rows than CTAs
-  a.ctas = 1;
-  if (one && a.d[0]) {
-    while (a.ctas < kLossMaxCtas && chunks > a.ctas * kLossFit) a.ctas *= 2;
-    if (chunks > a.ctas * Shape<kLossPolicy>::kSlots) {
-      a.twice = 1;
-      a.ctas = 1;
+  // CTAs of a row: as many as let both sets' rows wait in shared memory for their sums; beyond that what
+  // takes least by this estimate: rounds of teams, each the copies of a row's share and what a row costs
+  // beside them (0.5 us, 0.7 where CTAs exchange parts).  1024 rows of 256 KB, statistics alone: 46 us with
+  // one CTA (four rounds, the last a third full), 44 with two
+  // (the policy loss is cut alike with and without a gradient: the same sums)
+  int least = 1;
+  if (one) {
+    while (least < kLossMaxCtas && chunks > least * kLossFit) least *= 2;
+    if (chunks > least * Shape<kLossPolicy>::kSlots) {
+      a.twice = a.d[0] != nullptr;
+      least = 1;
     }
   }
-  while (a.ctas < kLossMaxCtas && a.rows * a.ctas * 2 <= places && a.groups[a.P] >= a.ctas * 2 * threads) a.ctas *= 2;
+  // teams that fit the GPU at once (clusters of 2 all SMs, of 4 144, of 8 120 of 152)
+  auto fit = [&](int ctas) { return places * (ctas <= 2 ? 152 : ctas == 4 ? 144 : 120) / 152 / ctas; };
+  const double ns = (static_cast<double>(a.groups[a.P]) * (k.mode == kLossForward ? 16 : 32)) * places / 6700.0;
+  a.ctas = least;
+  double best = 0.0;
+  for (int ctas = least; ctas <= kLossMaxCtas && (ctas == least || a.groups[a.P] >= ctas * threads); ctas *= 2) {
+    const int64_t rounds = (a.rows + fit(ctas) - 1) / fit(ctas);
+    const double cost = rounds * (ns / ctas + (ctas > 1 && k.mode != kLossBackward ? 700.0 : 500.0));
+    if (ctas == least || cost < best) {
+      a.ctas = ctas;
+      best = cost;
+    }
+  }
   void (*kernel)(LossArgs) = k.z32 ? (k.d32 ? kernel_of<float, float>(k) : kernel_of<float, uint16_t>(k))
                                    : (k.d32 ? kernel_of<uint16_t, float>(k) : kernel_of<uint16_t, uint16_t>(k));
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  // teams that fit the GPU at once (clusters of 2 all SMs, of 4 144, of 8 120 of 152)
-  const int fit = places * (a.ctas <= 2 ? 152 : a.ctas == 4 ? 144 : 120) / 152 / a.ctas;
-  const int64_t teams = a.rows < 1 ? 1 : a.rows < fit ? a.rows : fit;
+  const int64_t teams = a.rows < 1 ? 1 : a.rows < fit(a.ctas) ? a.rows : fit(a.ctas);
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = dim3(static_cast<unsigned>(teams * a.ctas));
   cfg.blockDim = dim3(threads + 32 * (one ? Shape<kLossPolicy>::kMore : Shape<kLossForward>::kMore));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = a.ctas;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = k.mode != kLossBackward && a.ctas > 1 ? 1 : 0;
+  cudaLaunchAttribute attr[2];
+  cfg.attrs = attr;
+  if (k.mode != kLossBackward && a.ctas > 1) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = a.ctas;
+    attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+  }
+  if (k.early) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+    ++cfg.numAttrs;
+  }
   e = cudaLaunchKernelEx(&cfg, kernel, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
