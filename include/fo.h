@@ -616,7 +616,7 @@ FO_API fo_status fo_adamw_group_create(const fo_adamw_tensor* tensors, int count
 FO_API fo_status fo_adamw_group_destroy(fo_adamw_group* group);
 
 /* norm[0] = sqrt(sum of the squares of every gradient in the group) (device fp32; the squares are
- * fp32, so elements above 1.8e19 read as infinite).  Workspace: 8 bytes per CTA. */
+ * fp32: an element above 1.8e19 gives a norm that is not finite).  Workspace: 8 bytes per CTA. */
 FO_API fo_status fo_grad_norm(fo_ctx* ctx, const fo_adamw_group* group, float* norm, void* stream);
 
 /* One step for every tensor.  With g = grad_scale * gradient, times

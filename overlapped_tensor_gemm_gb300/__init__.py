@@ -215,6 +215,17 @@ _PACK_MAT = struct.Struct("@Piiqqq").pack_into  # FoMat's fields
 assert struct.calcsize("@Piiqqq") == _MAT_BYTES
 _DTYPE_CODES: dict = {}
 _F32 = None
+_RAW_STREAM = None
+
+
+def _current_stream(device: int) -> int:
+    """Handle of torch's current stream on a device."""
+    global _RAW_STREAM
+    if _RAW_STREAM is None:
+        import torch
+        _RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda d: torch.cuda.current_stream(d).cuda_stream)
+    return _RAW_STREAM(device)
 
 
 def _f32():
@@ -335,6 +346,7 @@ class AdamWTensors:
             arr[i] = FoAdamWTensor(at["params"], at["grads"], at["master"], at["m"], at["v"], at["m_scale"],
                                    at["v_range"], p.numel(), FO_F32 if p.dtype == f32 else FO_BF16,
                                    FO_F32 if lists["grads"][i].dtype == f32 else FO_BF16)
+        self._packed = [(i, params[i].numel()) for i in range(n) if lists["m_scale"][i] is not None]
         self._lib = load()
         _check(self._lib.fo_adamw_group_create(arr, n, ctypes.byref(self._h)))
 
@@ -505,9 +517,8 @@ class Context:
 
     def _own_stream(self, stream):
         if stream is None:
-            import torch
-            stream = torch.cuda.current_stream(self.device)
-        return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+            return _current_stream(self.device)
+        return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
     def _mask(self, causal, scale, q_offsets, k_offsets):
         import torch
@@ -714,20 +725,23 @@ class Context:
         """The 8-bit states of the group as values: lists of bf16 or fp32 tensors of the parameters' sizes (None for
         parameters with fp32 states)."""
         import torch
-        n = len(group)
-        if len(m) != n or len(v) != n:
-            raise ValueError(f"m and v must have {n} entries")
-        dtype = None
-        for i, p in enumerate(group._keep["params"]):
-            if group._keep["m_scale"][i] is None:
-                continue
-            for what, t in (("m", m[i]), ("v", v[i])):
-                dtype = dtype or t.dtype
-                self._here(t, what)
-                if t.dtype != dtype or dtype not in (torch.bfloat16, torch.float32) or t.numel() != p.numel() \
-                        or not t.is_contiguous():
-                    raise ValueError(f"{what}[{i}] must be contiguous, all bf16 or all fp32, {p.numel()} elements")
-        ptrs = [(ctypes.c_void_p * max(n, 1))(*(None if t is None else t.data_ptr() for t in ts)) for ts in (m, v)]
+        n, dtype, ptrs = len(group), None, []
+        for what, ts in (("m", m), ("v", v)):
+            if len(ts) != n:
+                raise ValueError(f"{what} must have {n} entries")
+            at = (ctypes.c_void_p * max(n, 1))()
+            for i, size in group._packed:  # parameters with 8-bit states
+                t = ts[i]
+                if dtype is None:
+                    dtype = t.dtype
+                if t.get_device() != self.device:
+                    self._here(t, f"{what}[{i}]")
+                if t.dtype is not dtype or t.numel() != size or not t.is_contiguous():
+                    raise ValueError(f"{what}[{i}] must be contiguous, {dtype} like the others, {size} elements")
+                at[i] = t.data_ptr()
+            ptrs.append(at)
+        if dtype not in (None, torch.bfloat16, torch.float32):
+            raise ValueError(f"m and v must be bf16 or fp32, not {dtype}")
         _check(self._lib.fo_adamw_unpack(self._h, self._group(group), ptrs[0], ptrs[1],
                                          FO_F32 if dtype == torch.float32 else FO_BF16, self._own_stream(stream)))
 

@@ -29,6 +29,7 @@
 #include "fo_attn_common.cuh"
 #include "fo_host.h"
 #include "fo_ptx.cuh"
+#include "fo_wide.cuh"
 
 namespace fo {
 namespace {
@@ -50,14 +51,14 @@ struct TensorRef {
   float* m_scale;
   float* v_range;
   int64_t n;
-  int64_t first;        // blocks of the list's tensors in front of this one
   uint32_t index;       // place in the caller's list
   uint32_t reserved;
 };
 struct TensorList {
   int64_t blocks;
   int32_t count;
-  int32_t kind;         // KindBit
+  int32_t kind;                   // KindBit
+  int64_t first[kListTensors];    // blocks of the tensors in front of each (side by side: a search meets few lines)
   TensorRef t[kListTensors];
 };
 enum KindBit : int { kParam32 = 1, kGrad32 = 2, kMaster = 4, kStates8 = 8 };
@@ -82,7 +83,7 @@ __device__ __forceinline__ int tensor_of(const List& l, int64_t b) {
   int lo = 0, hi = l.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (l.t[mid].first <= b) lo = mid; else hi = mid - 1;
+    if (l.first[mid] <= b) lo = mid; else hi = mid - 1;
   }
   return lo;
 }
@@ -456,9 +457,9 @@ __global__ void __launch_bounds__(kAdamThreads, kCtasPerSm)
   if (b >= l.blocks) return;
   int i = tensor_of(l, b);
   for (; b < l.blocks; b += warps) {
-    while (i + 1 < l.count && l.t[i + 1].first <= b) ++i;
+    while (i + 1 < l.count && l.first[i + 1] <= b) ++i;
     const TensorRef& t = l.t[i];
-    const int64_t blk = b - t.first, left = t.n - blk * kBlock;
+    const int64_t blk = b - l.first[i], left = t.n - blk * kBlock;
     if (left >= kBlock) {
       step_block<kP32, kG32, kHasMaster, k8, true>(t, blk, kBlock, s);
     } else {
@@ -468,20 +469,19 @@ __global__ void __launch_bounds__(kAdamThreads, kCtasPerSm)
 }
 
 // Fixed-order sum over the CTA, in thread 0
-__device__ __forceinline__ double block_sum(double v, double* buf) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+__device__ __forceinline__ Wide block_sum(Wide v, Wide* buf) {
+  v = warp_sum(v);
   if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = 0.0;
-  for (int w = 0; w < kAdamThreads / 32; ++w) v += buf[w];
+  v = buf[0];
+  for (int w = 1; w < kAdamThreads / 32; ++w) v = plus(v, buf[w]);
   return v;
 }
 
 // Squares of one list's gradients; the CTA that comes last adds the CTAs' sums in order to what the
 // lists in front left, and behind the last list takes the root
 struct NormArgs {
-  double* part;    // [0]: sum of the lists so far; then one per CTA
+  Wide* part;      // [0]: sum of the lists so far; then one per CTA
   float* norm;
   int32_t first, last;
   uint32_t* ctrl;
@@ -490,21 +490,21 @@ template <bool kG32>
 __global__ void __launch_bounds__(kAdamThreads) grad_norm_kernel(const __grid_constant__ TensorList l,
                                                                  const __grid_constant__ NormArgs a) {
   typedef typename std::conditional<kG32, float, uint16_t>::type TG;
-  __shared__ double buf[kAdamThreads / 32];
+  __shared__ Wide buf[kAdamThreads / 32];
   __shared__ bool last;
   const int lane = threadIdx.x & 31;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kAdamThreads / 32);
   int64_t b = static_cast<int64_t>(blockIdx.x) * (kAdamThreads / 32) + (threadIdx.x >> 5);
-  double total = 0.0;
+  Wide total = {0.f, 0.f};
   if (b < l.blocks) {
     int i = tensor_of(l, b);
     while (b < l.blocks) {
       float sum = 0.f;  // at most 512 squares in fp32
 #pragma unroll 1
       for (int turn = 0; turn < 16 && b < l.blocks; ++turn) {
-        while (i + 1 < l.count && l.t[i + 1].first <= b) ++i;
+        while (i + 1 < l.count && l.first[i + 1] <= b) ++i;
         const TensorRef& t = l.t[i];
-        const int64_t blk = b - t.first, left = t.n - blk * kBlock, ahead = (kAhead - 1) * warps * kBlock;
+        const int64_t blk = b - l.first[i], left = t.n - blk * kBlock, ahead = (kAhead - 1) * warps * kBlock;
         const TG* const tg = static_cast<const TG*>(t.grad) + blk * kBlock + lane * 4;
         Pair s = 0;
         if (left >= ahead + kBlock) {  // the warp's next blocks are whole ones of this tensor
@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(kAdamThreads) grad_norm_kernel(const __grid_co
         unpack2(s, x, y);
         sum += x + y;
       }
-      total += sum;
+      total = plus(total, wide(sum));
     }
   }
   total = block_sum(total, buf);
@@ -548,14 +548,20 @@ __global__ void __launch_bounds__(kAdamThreads) grad_norm_kernel(const __grid_co
   __syncthreads();
   if (!last) return;
   __threadfence();
-  total = 0.0;
-  for (unsigned i = threadIdx.x; i < gridDim.x; i += kAdamThreads) total += __ldcg(a.part + 1 + i);
+  total = Wide{0.f, 0.f};
+  for (unsigned i = threadIdx.x; i < gridDim.x; i += kAdamThreads) {
+    const float2 p = __ldcg(reinterpret_cast<const float2*>(a.part + 1 + i));
+    total = plus(total, Wide{p.x, p.y});
+  }
   __syncthreads();
   total = block_sum(total, buf);
   if (threadIdx.x == 0) {
-    if (!a.first) total += __ldcg(a.part);
+    if (!a.first) {
+      const float2 p = __ldcg(reinterpret_cast<const float2*>(a.part));
+      total = plus(total, Wide{p.x, p.y});
+    }
     a.part[0] = total;
-    if (a.last) a.norm[0] = static_cast<float>(sqrt(total));
+    if (a.last) a.norm[0] = sqrtf(total.hi + total.lo);
   }
 }
 
@@ -563,6 +569,7 @@ struct UnpackList {
   int64_t blocks;
   int32_t count;
   int32_t reserved;
+  int64_t first[kListTensors];
   struct Ref {
     const uint8_t* m;
     const uint8_t* v;
@@ -570,7 +577,7 @@ struct UnpackList {
     const float* v_range;
     void* m_out;
     void* v_out;
-    int64_t n, first;
+    int64_t n;
   } t[kListTensors];
 };
 static_assert(sizeof(UnpackList) <= 32764, "kernel parameters");
@@ -615,9 +622,9 @@ __global__ void __launch_bounds__(kAdamThreads) unpack_kernel(const __grid_const
   if (b >= l.blocks) return;
   int i = tensor_of(l, b);
   while (b < l.blocks) {
-    while (i + 1 < l.count && l.t[i + 1].first <= b) ++i;
+    while (i + 1 < l.count && l.first[i + 1] <= b) ++i;
     const UnpackList::Ref& t = l.t[i];
-    const int64_t blk = b - t.first, left = t.n - blk * kBlock, ahead = (kAhead - 1) * warps * kBlock;
+    const int64_t blk = b - l.first[i], left = t.n - blk * kBlock, ahead = (kAhead - 1) * warps * kBlock;
     if (left >= ahead + kBlock) {  // the warp's next blocks are whole ones of this tensor
       unpack_blocks<T, kAhead, true>(t, blk, warps, kBlock);
       b += kAhead * warps;
@@ -743,8 +750,9 @@ fo_status fo_adamw_group_create(const fo_adamw_tensor* tensors, int count, fo_ad
           g->lists[open].kind = kind;
         }
         TensorList& l = g->lists[open];
-        l.t[l.count++] = TensorRef{t.param, t.grad, t.master, t.m, t.v, t.m_scale, t.v_range, t.n, l.blocks,
-                                   static_cast<uint32_t>(i), 0};
+        l.first[l.count] = l.blocks;
+        l.t[l.count++] =
+            TensorRef{t.param, t.grad, t.master, t.m, t.v, t.m_scale, t.v_range, t.n, static_cast<uint32_t>(i), 0};
         l.blocks += blocks_of(t.n);
       }
     }
@@ -779,7 +787,7 @@ fo_status fo_grad_norm(fo_ctx* ctx, const fo_adamw_group* group, float* norm, vo
                                &part));
   NormArgs a;
   std::memset(&a, 0, sizeof(a));
-  a.part = static_cast<double*>(part);
+  a.part = static_cast<Wide*>(part);
   a.norm = norm;
   a.ctrl = host_ctrl(ctx);
   for (size_t i = 0; i < group->lists.size(); ++i) {
@@ -872,8 +880,9 @@ fo_status fo_adamw_unpack(fo_ctx* ctx, const fo_adamw_group* group, void* const*
     for (; i < count && l.count < kListTensors; ++i) {
       const fo_adamw_tensor& t = group->tensors[i];
       if (!t.m_scale || t.n == 0) continue;
+      l.first[l.count] = l.blocks;
       l.t[l.count++] = UnpackList::Ref{static_cast<const uint8_t*>(t.m), static_cast<const uint8_t*>(t.v), t.m_scale,
-                                       t.v_range, m[i], v[i], t.n, l.blocks};
+                                       t.v_range, m[i], v[i], t.n};
       l.blocks += blocks_of(t.n);
     }
     if (l.count == 0) break;

@@ -5,6 +5,7 @@
 
 #include "fo_host.h"
 #include "fo_loss.cuh"
+#include "fo_wide.cuh"
 
 namespace fo {
 namespace {
@@ -26,25 +27,6 @@ __device__ __forceinline__ float pair_loss(int kind, float beta, float gap, floa
   const float e = expf(-fabsf(x));  // log(1 + exp(-x)), of a number at most 1
   *slope = -beta * (x >= 0.f ? e / (1.f + e) : 1.f / (1.f + e));
   return fmaxf(-x, 0.f) + log1pf(e);
-}
-
-// A number as the sum of two fp32 values, |lo| at most half a step of hi (sums of error-free
-// transformations, Knuth; fp64 arithmetic is slow here)
-struct Wide {
-  float hi, lo;
-};
-__device__ __forceinline__ Wide plus(const Wide& a, const Wide& b) {
-  const float s = a.hi + b.hi, t = s - a.hi;
-  const float lo = ((a.hi - (s - t)) + (b.hi - t)) + (a.lo + b.lo), hi = s + lo;
-  return Wide{hi, lo - (hi - s)};
-}
-__device__ __forceinline__ Wide wide(float v) { return Wide{v, 0.f}; }
-// Over a warp, in every lane
-__device__ __forceinline__ Wide warp_sum(Wide v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    v = plus(v, Wide{__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)});
-  return v;
 }
 
 // One CTA per pair, half of it per sequence: scores, loss and coefficient; the last CTA averages the
@@ -253,6 +235,7 @@ fo_status fo_token_logprobs_backward(fo_ctx* ctx, const fo_mat* logits, int P, c
   if (a.rows == 0) return FO_OK;
   DeviceGuard dev(host_device(ctx));
   if (!dev.ok) return host_fail(FO_ERR_CUDA, "cudaSetDevice failed");
+  a.backwards = 1;  // the rows whose statistics were taken last may still be in L2
   a.in_lse = lse;
   a.in_entropy = entropy;
   a.dlogp = dlogp;
@@ -397,7 +380,7 @@ fo_status fo_preference_loss(fo_ctx* ctx, const fo_mat* logits, int P, const int
   if (e != cudaSuccess) return host_fail(FO_ERR_CUDA, cudaGetErrorString(e));
   if (!dlogits) return FO_OK;
   back.coef = p.coef;
-  back.backwards = 1;  // the rows that were read last may still be in L2
+  back.backwards = 1;
   k.mode = kLossBackward;
   k.early = true;
   return run_rows(ctx, back, k, s);
