@@ -30,18 +30,18 @@ __device__ __forceinline__ float pair_loss(int kind, float beta, float gap, floa
 }
 
 // One CTA per pair, half of it per sequence: scores, loss and coefficient; the last CTA averages the
-// losses in order.  A pair's gap is a small difference of long sums: the log-probabilities enter as the
-// two numbers that they are the difference of, unrounded (in log2), and are summed in twice fp32.
+// losses in order.  A pair's gap is a small difference of long sums: the log-probabilities come,
+// and are summed, in twice fp32.
 __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constant__ PairArgs a) {
   constexpr int kHalf = kPairThreads / 2, kWarps = kHalf / 32;
-  __shared__ Wide logs[2][kWarps], refs[2][kWarps];
+  __shared__ Wide sums[2][kWarps];
   __shared__ int counted[2][kWarps];
   let_next_start();
   wait_for_previous();
   if (!*a.fine) return;
   const int half = threadIdx.x / kHalf, at = threadIdx.x % kHalf, lane = threadIdx.x & 31;
   const int seq = blockIdx.x + half * a.pairs, end = a.offsets[seq + 1];
-  Wide log = {0.f, 0.f}, ref = {0.f, 0.f};
+  Wide sum = {0.f, 0.f};
   int n = 0;
 #pragma unroll 4
   for (int i = a.offsets[seq] + at; i < end; i += kHalf) {
@@ -49,41 +49,37 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constan
     const float4 st = a.stat[i];  // (rows that do not count: 0)
     const float r = a.ref_logp ? a.ref_logp[i] : 0.f;
     const bool on = y >= 0 && y < a.vocab;
-    log = plus(log, plus(wide(on ? st.z : 0.f), wide(on ? -st.y : 0.f)));
-    ref = plus(ref, wide(on ? r : 0.f));
+    sum = plus(sum, plus(Wide{on ? st.z : 0.f, on ? st.w : 0.f}, wide(on ? -r : 0.f)));
     n += on;
   }
-  log = warp_sum(log);
-  ref = warp_sum(ref);
+  sum = warp_sum(sum);
   n = __reduce_add_sync(0xffffffffu, n);
   if (lane == 0) {
-    logs[half][at >> 5] = log;
-    refs[half][at >> 5] = ref;
+    sums[half][at >> 5] = sum;
     counted[half][at >> 5] = n;
   }
   __syncthreads();
   if (threadIdx.x >= 32) return;
   int last = 0;
   if (threadIdx.x == 0) {
-    double score[2];
+    Wide score[2];
     float share[2];
     for (int h = 0; h < 2; ++h) {
-      log = logs[h][0];
-      ref = refs[h][0];
+      score[h] = sums[h][0];
       n = counted[h][0];
       for (int w = 1; w < kWarps; ++w) {
-        log = plus(log, logs[h][w]);
-        ref = plus(ref, refs[h][w]);
+        score[h] = plus(score[h], sums[h][w]);
         n += counted[h][w];
       }
-      score[h] = (static_cast<double>(log.hi) + log.lo) * 0.69314718055994531 - (static_cast<double>(ref.hi) + ref.lo);
       share[h] = 1.f;
-      if (a.average) {
-        score[h] /= n > 1 ? n : 1;
-        share[h] = 1.f / static_cast<float>(n > 1 ? n : 1);
+      if (a.average) {  // (a quotient and what it leaves)
+        const float count = static_cast<float>(n > 1 ? n : 1), q = score[h].hi / count;
+        score[h] = plus(wide(q), wide((fmaf(-q, count, score[h].hi) + score[h].lo) / count));
+        share[h] = 1.f / count;
       }
     }
-    const float gap = static_cast<float>(score[0] - score[1] - a.margin);
+    const Wide wide_gap = plus(plus(score[0], Wide{-score[1].hi, -score[1].lo}), wide(-a.margin));
+    const float gap = wide_gap.hi + wide_gap.lo;
     float slope, back;
     float loss = pair_loss(a.kind, a.beta, gap, &slope);
     if (a.smoothing != 0.f) {
@@ -100,7 +96,7 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constan
   }
   if (!__shfl_sync(0xffffffffu, last, 0)) return;
   __threadfence();
-  Wide sum = {0.f, 0.f};
+  sum = Wide{0.f, 0.f};
   for (int i = lane; i < a.pairs; i += 32) sum = plus(sum, wide(__ldcg(a.pair_loss + i)));
   sum = warp_sum(sum);
   if (lane == 0) a.loss[0] = (sum.hi + sum.lo) / static_cast<float>(a.pairs);

@@ -43,7 +43,7 @@ struct LossArgs {
   float* logp;                // outputs, each may be null
   float* lse;
   float* entropy;
-  float4* stat;               // (m, log2 s, d_y log2 e, -) of every row: what the preference loss keeps
+  float4* stat;               // (m, log2 s, logp in twice fp32) of every row: what the preference loss keeps
   const float* in_lse;        // backward: statistics given (or stat)
   const float* in_entropy;
   const float* dlogp;         // a of every row (or coef, by sequence)

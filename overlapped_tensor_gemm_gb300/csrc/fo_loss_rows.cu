@@ -19,6 +19,7 @@
 #include <cstring>
 
 #include "fo_loss.cuh"
+#include "fo_wide.cuh"
 
 namespace fo {
 namespace {
@@ -163,6 +164,17 @@ __device__ __forceinline__ float base_of(float m) { return fmaxf(m, -FLT_MAX); }
 struct __align__(16) Part {  // (moved by 16-byte stores)
   float m, s, t, reserved;
 };
+
+// ln s in twice fp32: the exponent's share in two products of which one is exact, and the logarithm of a
+// number near 1
+__device__ __forceinline__ Wide wide_log(float s) {
+  const int bits = __float_as_int(s);
+  if (static_cast<uint32_t>(bits) - 0x00800000u >= 0x7f000000u) return wide(logf(s));  // 0, subnormal, infinite, NaN
+  const int e = (bits - 0x3f400000) >> 23;  // s = 2^e m, m from 3/4 to 3/2
+  const float m = __int_as_float(bits - (e << 23)), n = static_cast<float>(e);
+  // ln 2 = 0.693145751953125 (16 bits) + 1.42860677e-6
+  return plus(wide(n * 0.693145751953125f), wide(fmaf(n, 1.42860677e-6f, logf(m))));
+}
 
 // The parts of all lanes as one, in every lane
 template <bool kEnt>
@@ -661,14 +673,16 @@ __global__ void __launch_bounds__(Shape<kMode>::kAll + 32 * Shape<kMode>::kMore,
           for (int k = lane; k < a.ctas * kWarps; k += 32) v = merge<kStatEnt>(v, sm.part[box][k], c);
           v = join<kStatEnt>(v, c);
           // p_j = 2^((z_j - base) c - log_s)
-          const float base = base_of(v.m), log_s = log2f(v.s);
-          const float dy = (zy - base) * c, lp = kLn2 * (dy - log_s);
+          const float base = base_of(v.m), log_s = log2f(v.s), dz = zy - base, dy = a.scale * dz;
+          const Wide total = wide_log(v.s);
+          const Wide wide_lp = plus(Wide{dy, fmaf(a.scale, dz, -dy)}, Wide{-total.hi, -total.lo});
+          const float lp = wide_lp.hi;
           const float entropy = kStatEnt ? kLn2 * (log_s - v.t / v.s) : 0.f;
           if (rank == 0 && lane == 0) {
             if (a.logp) a.logp[i] = lp;
-            if (a.lse) a.lse[i] = fmaf(base, a.scale, kLn2 * log_s);
+            if (a.lse) a.lse[i] = fmaf(base, a.scale, total.hi) + total.lo;
             if (kMode == kLossForward && a.entropy) a.entropy[i] = entropy;
-            if (a.stat) a.stat[i] = make_float4(base, log_s, dy, 0.f);
+            if (a.stat) a.stat[i] = make_float4(base, log_s, wide_lp.hi, wide_lp.lo);
           }
           if (kMode == kLossPolicy) {
             // the loss through this row: da = dL/dlogp, dh = dL/dH

@@ -458,3 +458,36 @@ def test_rows_behind_2_31_elements(ctx):
     assert torch.allclose(logp[rows], few, rtol=0, atol=1e-4)
     assert torch.allclose(z[rows].float(), some.float(), rtol=2.0 ** -7, atol=1e-9)
     assert z[rows].abs().sum() > 0 and (z[32768] == 0).all()
+
+
+def test_a_pair_whose_target_has_no_probability(ctx):
+    """The preferred sequence holds a token of probability 0: the loss is infinite, the other pair's gradient is not."""
+    z = torch.zeros((4, 16), device="cuda")
+    z[0, 3] = -float("inf")
+    y = torch.tensor([3, 1, 2, 1], dtype=torch.int32, device="cuda")
+    off = torch.tensor([0, 1, 2, 3, 4], dtype=torch.int32, device="cuda")
+    (loss, margins, logp), d = (torch.empty(n, device="cuda") for n in (1, 2, 4)), torch.empty_like(z)
+    ctx.preference_loss([z], y, off, loss, logp=logp, margins=margins, dlogits=[d], beta=0.5)
+    torch.cuda.synchronize()
+    ctx.poll()
+    assert loss.item() == float("inf") and margins[0] == -float("inf") and margins[1] == 0
+    assert logp[0] == -float("inf") and torch.isfinite(logp[1:]).all()
+    # pair 1: slope -beta / 2, over two pairs
+    p = 1 / 16
+    want = torch.full((16,), 0.125 * p, device="cuda")
+    want[1] -= 0.125
+    assert torch.allclose(d[1], want, atol=1e-6) and torch.allclose(d[3], -want, atol=1e-6)
+
+
+def test_summed_log_probabilities_keep_twice_fp32(ctx):
+    """A pair of 4000 tokens a side: its gap, a difference of sums near -40000, to 4000 errors of a token's own sum
+    (its exponentials' 2^-22 and roundings, at random signs: 3e-7 each) -- fp32 sums would be off by 2e-3."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    z = torch.randn((8000, 600), generator=g, device="cuda") * 2
+    y = torch.randint(0, 600, (8000,), generator=g, device="cuda", dtype=torch.int32)
+    off = torch.tensor([0, 4000, 8000], dtype=torch.int32, device="cuda")
+    loss, margins = torch.empty(1, device="cuda"), torch.empty(1, device="cuda")
+    ctx.preference_loss([z], y, off, loss, margins=margins, beta=1.0)
+    lp = torch.log_softmax(z.double(), 1).gather(1, y.long()[:, None])[:, 0]
+    gap = (lp[:4000].sum() - lp[4000:].sum()).item()
+    assert abs(margins.item() - gap) <= 2.0 ** -24 * abs(gap) + 5 * 3e-7 * 8000 ** 0.5
