@@ -641,6 +641,8 @@ class Context:
     def _targets(self, logits, targets):
         import torch
         P = len(logits)
+        if P == 0:
+            raise ValueError("no logits")
         z = self._list(logits, P, "logits")
         return P, z, logits[0].shape[0], self._entries(targets, "targets", logits[0].shape[0], torch.int32)
 

@@ -491,3 +491,89 @@ def test_summed_log_probabilities_keep_twice_fp32(ctx):
     lp = torch.log_softmax(z.double(), 1).gather(1, y.long()[:, None])[:, 0]
     gap = (lp[:4000].sum() - lp[4000:].sum()).item()
     assert abs(margins.item() - gap) <= 2.0 ** -24 * abs(gap) + 5 * 3e-7 * 8000 ** 0.5
+
+
+@pytest.mark.parametrize("types", [(F32, F32), (BF, BF), (BF, F32)], ids=str)
+@pytest.mark.parametrize("m", [1, 5])
+def test_rows_that_do_not_fit_shared_memory(ctx, types, m):
+    """Vocabularies of a million: a policy loss's rows are read twice."""
+    r = Rows(m, [500001, 400008, 7, 100000], dtype=types[0], seed=m, masked=0.2)
+    rng = np.random.default_rng(6)
+    lp = np.zeros(m)
+    lp[r.on] = ls.token_stats(r.z64[r.on], r.y[r.on])[0]
+    adv, old = rng.uniform(0.5, 1.5, m), lp + 0.1
+    want, wlogp, _, a, h = ls.policy_loss(r.z64, r.y, adv.astype(np.float32).astype(np.float64),
+                                          old.astype(np.float32).astype(np.float64), ent_coef=float(np.float32(0.02)))
+    stats, logp, d = torch.empty(4, device="cuda"), torch.empty(m, device="cuda"), r.outputs(types[1])
+    ctx.policy_loss(r.logits, r.targets, _vec(adv), stats, old_logp=_vec(old), logp=logp, dlogits=d, entropy_coef=0.02)
+    torch.cuda.synchronize()
+    ctx.poll()
+    err = np.zeros(m)
+    err[r.on] = _logp_error(r, r.on)
+    _within(logp, wlogp, err, "logp")
+    # (the ratio is exp of a difference that is off by err)
+    _check_gradient(r, d, types[1], a, h, np.abs(a) * (err + 32 * u), np.abs(h) * 8 * u)
+    if types[0] == types[1]:
+        same = r.copies()
+        ctx.policy_loss(same, r.targets, _vec(adv), stats, old_logp=_vec(old), dlogits=same, entropy_coef=0.02)
+        for x, y in zip(same, d):
+            assert torch.equal(x, y)
+
+
+def test_calls_behind_a_failed_one(ctx):
+    """The losses wait for nothing that an earlier call's failure ends: with its abort word raised they are right."""
+    import overlapped_tensor_gemm_gb300 as fo
+    from test_gpu_p_training_failures import _fail
+    r = Rows(50, [3000, 1001], seed=9)
+    adv, stats, loss = torch.ones(50, device="cuda"), torch.empty(4, device="cuda"), torch.empty(1, device="cuda")
+    off = torch.tensor([0, 20, 50], dtype=torch.int32, device="cuda")
+    got = []
+    with fo.Context(0) as c:
+        for fail in (False, True):
+            if fail:
+                _fail(c)
+            d, d2 = r.outputs(BF), r.outputs(BF)
+            c.policy_loss(r.logits, r.targets, adv, stats, dlogits=d)
+            c.preference_loss(r.logits, r.targets, off, loss, dlogits=d2)
+            torch.cuda.synchronize()
+            got.append([t.clone() for t in (stats, loss, *d, *d2)])
+        with pytest.raises(fo.FoError) as e:
+            c.poll()
+        assert e.value.status == fo.FO_ERR_TIMEOUT
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+
+
+def test_contexts_of_four_threads(ctx):
+    """Each thread its own context and stream, losses of several shapes at once: the bits of one after the other."""
+    import threading
+
+    import overlapped_tensor_gemm_gb300 as fo
+    rows = [Rows(*s, seed=20 + i) for i, s in enumerate([(64, [4096, 4096]), (300, [515, 64, 100]), (9, [32000]), (130, [96])])]
+    adv = [torch.rand(r.m, device="cuda") for r in rows]
+
+    def step(c, i):
+        r = rows[i]
+        stats, d = torch.empty(4, device="cuda"), r.outputs(BF)
+        c.policy_loss(r.logits, r.targets, adv[i], stats, dlogits=d, entropy_coef=0.1)
+        return [stats] + d
+    want = [[t.clone() for t in step(ctx, i)] for i in range(4)]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        try:
+            with fo.Context(0) as c, torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    got = step(c, i)
+                torch.cuda.current_stream().synchronize()
+                c.poll()
+                wrong.extend((i, k) for k, (x, y) in enumerate(zip(got, want[i])) if not torch.equal(x, y))
+        except Exception as e:  # noqa: BLE001
+            wrong.append((i, repr(e)))
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
