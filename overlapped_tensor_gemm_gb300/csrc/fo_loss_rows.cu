@@ -309,12 +309,22 @@ __device__ __forceinline__ bool offsets_fine(const int32_t* off, int n, int64_t 
 template <int kWarps>
 __device__ __forceinline__ float total_weight(const LossArgs& a, float* buf) {
   float sum = 0.f, low = 0.f;
-  for (int64_t i = threadIdx.x; i < a.rows; i += 32 * kWarps) {
-    const int32_t y = a.targets[i];
-    if (y < 0 || y >= a.first[a.P]) continue;
-    const float x = (a.weights ? a.weights[i] : 1.f) - low, next = sum + x;
-    low = (next - sum) - x;
-    sum = next;
+  constexpr int kTogether = 4;  // (loads under way at once)
+  for (int64_t i = threadIdx.x; i < a.rows; i += kTogether * 32 * kWarps) {
+    int32_t y[kTogether];
+    float w[kTogether];
+#pragma unroll
+    for (int k = 0; k < kTogether; ++k) {
+      const int64_t at = i + k * 32 * kWarps;
+      y[k] = at < a.rows ? a.targets[at] : -1;
+      w[k] = at < a.rows && a.weights ? a.weights[at] : 1.f;
+    }
+#pragma unroll
+    for (int k = 0; k < kTogether; ++k) {
+      const float x = (y[k] >= 0 && y[k] < a.first[a.P] ? w[k] : 0.f) - low, next = sum + x;
+      low = (next - sum) - x;
+      sum = next;
+    }
   }
   sum = warp_sum(sum);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -411,8 +421,6 @@ __global__ void __launch_bounds__(Shape<kMode>::kAll + 32 * Shape<kMode>::kMore,
     row0 = a.offsets[0];
     rows = a.offsets[2 * a.pairs] - row0;
   }
-  if (together) cluster_sync_all(); else __syncthreads();
-
   // this CTA's groups, and how many chunks they are
   const int g_lo = static_cast<int>(static_cast<int64_t>(a.groups[a.P]) * rank / a.ctas);
   const int g_hi = static_cast<int>(static_cast<int64_t>(a.groups[a.P]) * (rank + 1) / a.ctas);
@@ -430,6 +438,8 @@ __global__ void __launch_bounds__(Shape<kMode>::kAll + 32 * Shape<kMode>::kMore,
     }
     return r;
   };
+  const RowIn first = fetch(0);  // (asked for in front of the barrier)
+  if (together) cluster_sync_all(); else __syncthreads();
 
   if (warp == kSets * kWarps) {
     // the copies, in the order in which the chunks are used: of each row for its statistics, and (twice)
@@ -464,7 +474,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kAll + 32 * Shape<kMode>::kMore,
       }
     };
     for (int n = 0; n < mine && fine; ++n, i += stride) {
-      if ((n & 31) == 0) r = fetch(n);
+      if ((n & 31) == 0) r = n ? fetch(n) : first;
       if (!__shfl_sync(0xffffffffu, r.on, n & 31)) continue;
       copy_row(i);
       if (twice) copy_row(i);
@@ -480,7 +490,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kAll + 32 * Shape<kMode>::kMore,
     P place;
     bool fine = true;
     for (int n = 0; n < mine && out && fine; ++n, i += stride) {
-      if ((n & 31) == 0) r = fetch(n);
+      if ((n & 31) == 0) r = n ? fetch(n) : first;
       const bool on = __shfl_sync(0xffffffffu, r.on, n & 31);
       int rk = 0;
       for (int g = g_lo; g < g_hi && fine;) {
@@ -540,7 +550,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kAll + 32 * Shape<kMode>::kMore,
     for (int n = 0; n < mine; ++n, i += stride) {
       const int at = n & 31;
       if (at == 0) {
-        r = fetch(n);
+        r = n ? fetch(n) : first;
         const int64_t k = i + lane * stride;
         if (kStat && warp == 0 && rank == 0 && n + lane < mine && !r.on) {
           if (r.y >= a.first[a.P]) note_error(a.ctrl, FO_ERR_RANGE, kSiteTargets, static_cast<uint32_t>(k));
