@@ -38,7 +38,7 @@ constexpr int kBlock = 256;           // elements of a block: 8 per lane of a wa
 constexpr int kAdamThreads = 256;
 constexpr int kCtasPerSm = 4;
 constexpr int kListTensors = 400;     // tensors of one launch
-constexpr int kAhead = 4;             // blocks that a warp of the norm and of the unpacking loads at once
+constexpr int kAhead = 4;             // see run_of
 constexpr float kMaxE4m3 = 448.f;
 constexpr float kOctaves = 24.f;      // v's values span at most 2^24
 
@@ -77,6 +77,9 @@ struct StepArgs {
 };
 static_assert(sizeof(TensorList) + sizeof(StepArgs) <= 32764, "kernel parameters");
 
+// Blocks that a warp of the norm or of the unpacking takes in a row: several, loaded at once, where there
+// are enough for every warp
+__host__ __device__ inline int run_of(int64_t blocks, int64_t warps) { return blocks >= 4 * kAhead * warps ? kAhead : 1; }
 // The tensor of block b: the last one that starts at or in front of it
 template <typename List>
 __device__ __forceinline__ int tensor_of(const List& l, int64_t b) {
@@ -494,43 +497,53 @@ __global__ void __launch_bounds__(kAdamThreads) grad_norm_kernel(const __grid_co
   __shared__ bool last;
   const int lane = threadIdx.x & 31;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kAdamThreads / 32);
-  int64_t b = static_cast<int64_t>(blockIdx.x) * (kAdamThreads / 32) + (threadIdx.x >> 5);
+  const int run = run_of(l.blocks, warps);
+  int64_t b = (static_cast<int64_t>(blockIdx.x) * (kAdamThreads / 32) + (threadIdx.x >> 5)) * run;
   Wide total = {0.f, 0.f};
   if (b < l.blocks) {
     int i = tensor_of(l, b);
     while (b < l.blocks) {
       float sum = 0.f;  // at most 512 squares in fp32
 #pragma unroll 1
-      for (int turn = 0; turn < 16 && b < l.blocks; ++turn) {
+      for (int turn = 0; turn < 64 / kAhead && b < l.blocks; ++turn, b += warps * run) {
         while (i + 1 < l.count && l.first[i + 1] <= b) ++i;
-        const TensorRef& t = l.t[i];
-        const int64_t blk = b - l.first[i], left = t.n - blk * kBlock, ahead = (kAhead - 1) * warps * kBlock;
-        const TG* const tg = static_cast<const TG*>(t.grad) + blk * kBlock + lane * 4;
         Pair s = 0;
-        if (left >= ahead + kBlock) {  // the warp's next blocks are whole ones of this tensor
-          decltype(load4<true>(tg, 0)) g[kAhead][2];
+        const int64_t blk = b - l.first[i];
+        if (run == kAhead && l.t[i].n - blk * kBlock >= kAhead * kBlock) {  // whole blocks of this tensor
+          // (16 bytes a lane: a block is one load in bf16, two in fp32)
+          constexpr int kLoads = kAhead * (kG32 ? 2 : 1);
+          const uint4* p = reinterpret_cast<const uint4*>(static_cast<const TG*>(l.t[i].grad) + blk * kBlock) + lane;
+          uint4 g[kLoads];
 #pragma unroll
-          for (int u = 0; u < kAhead; ++u)
+          for (int q = 0; q < kLoads; ++q) g[q] = p[q * 32];
 #pragma unroll
-            for (int q = 0; q < 2; ++q) g[u][q] = load4<true>(tg + u * warps * kBlock + q * 128, 4);
-#pragma unroll
-          for (int u = 0; u < kAhead; ++u)
+          for (int q = 0; q < kLoads; ++q) {
+            Pair x[2], y[2];
+            if constexpr (kG32) {
+              x[0] = pack2(__uint_as_float(g[q].x), __uint_as_float(g[q].y));
+              x[1] = pack2(__uint_as_float(g[q].z), __uint_as_float(g[q].w));
+            } else {
+              values(make_uint2(g[q].x, g[q].y), x);
+              values(make_uint2(g[q].z, g[q].w), y);
+              s = ffma2(y[0], y[0], ffma2(y[1], y[1], s));
+            }
+            s = ffma2(x[0], x[0], ffma2(x[1], x[1], s));
+          }
+        } else {
+          int j = i;
+          for (int64_t k = b; k < b + run && k < l.blocks; ++k) {
+            while (j + 1 < l.count && l.first[j + 1] <= k) ++j;
+            const TensorRef& t = l.t[j];
+            const int64_t at = (k - l.first[j]) * kBlock + lane * 4, left = t.n - at;
+            const int n = left < kBlock ? static_cast<int>(left < 0 ? 0 : left) : kBlock;
+            const TG* const tg = static_cast<const TG*>(t.grad) + at;
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
               Pair v[2];
-              values(g[u][q], v);
+              values(load4<false>(tg + q * 128, n - q * 128), v);
               s = ffma2(v[0], v[0], ffma2(v[1], v[1], s));
             }
-          b += kAhead * warps;
-        } else {
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            Pair v[2];
-            const int64_t in = left - lane * 4 - q * 128;
-            values(load4<false>(tg + q * 128, in < 4 ? static_cast<int>(in < 0 ? 0 : in) : 4), v);
-            s = ffma2(v[0], v[0], ffma2(v[1], v[1], s));
           }
-          b += warps;
         }
         float x, y;
         unpack2(s, x, y);
@@ -582,9 +595,9 @@ struct UnpackList {
 };
 static_assert(sizeof(UnpackList) <= 32764, "kernel parameters");
 
-// count blocks, `pitch` blocks apart; the first n elements of each are inside the tensor
+// count blocks; the first n elements of each are inside the tensor
 template <typename T, int count, bool kFull>
-__device__ __forceinline__ void unpack_blocks(const UnpackList::Ref& t, int64_t blk, int64_t pitch, int n) {
+__device__ __forceinline__ void unpack_blocks(const UnpackList::Ref& t, int64_t blk, int n) {
   const int lane = threadIdx.x & 31;
   const int64_t at = blk * kBlock + lane * 4;
   n -= lane * 4;
@@ -593,12 +606,12 @@ __device__ __forceinline__ void unpack_blocks(const UnpackList::Ref& t, int64_t 
   float2 range[count];
 #pragma unroll
   for (int u = 0; u < count; ++u) {
-    scale[u] = t.m_scale[blk + u * pitch];
-    range[u] = reinterpret_cast<const float2*>(t.v_range)[blk + u * pitch];
+    scale[u] = t.m_scale[blk + u];
+    range[u] = reinterpret_cast<const float2*>(t.v_range)[blk + u];
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      mq[u][q] = load4<kFull>(t.m + at + u * pitch * kBlock + q * 128, n - q * 128);
-      vq[u][q] = load4<kFull>(t.v + at + u * pitch * kBlock + q * 128, n - q * 128);
+      mq[u][q] = load4<kFull>(t.m + at + u * kBlock + q * 128, n - q * 128);
+      vq[u][q] = load4<kFull>(t.v + at + u * kBlock + q * 128, n - q * 128);
     }
   }
 #pragma unroll
@@ -610,27 +623,30 @@ __device__ __forceinline__ void unpack_blocks(const UnpackList::Ref& t, int64_t 
       from_levels(vq[u][q], range[u].x, range[u].y, v);
       m[0] = mul2(m[0], both(scale[u]));
       m[1] = mul2(m[1], both(scale[u]));
-      store4<kFull>(static_cast<T*>(t.m_out) + at + u * pitch * kBlock + q * 128, n - q * 128, m);
-      store4<kFull>(static_cast<T*>(t.v_out) + at + u * pitch * kBlock + q * 128, n - q * 128, v);
+      store4<kFull>(static_cast<T*>(t.m_out) + at + u * kBlock + q * 128, n - q * 128, m);
+      store4<kFull>(static_cast<T*>(t.v_out) + at + u * kBlock + q * 128, n - q * 128, v);
     }
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kAdamThreads) unpack_kernel(const __grid_constant__ UnpackList l) {
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kAdamThreads / 32);
-  int64_t b = static_cast<int64_t>(blockIdx.x) * (kAdamThreads / 32) + (threadIdx.x >> 5);
+  const int run = run_of(l.blocks, warps);
+  int64_t b = (static_cast<int64_t>(blockIdx.x) * (kAdamThreads / 32) + (threadIdx.x >> 5)) * run;
   if (b >= l.blocks) return;
   int i = tensor_of(l, b);
-  while (b < l.blocks) {
+  for (; b < l.blocks; b += warps * run) {
     while (i + 1 < l.count && l.first[i + 1] <= b) ++i;
-    const UnpackList::Ref& t = l.t[i];
-    const int64_t blk = b - l.first[i], left = t.n - blk * kBlock, ahead = (kAhead - 1) * warps * kBlock;
-    if (left >= ahead + kBlock) {  // the warp's next blocks are whole ones of this tensor
-      unpack_blocks<T, kAhead, true>(t, blk, warps, kBlock);
-      b += kAhead * warps;
+    const int64_t blk = b - l.first[i];
+    if (run == kAhead && l.t[i].n - blk * kBlock >= kAhead * kBlock) {  // whole blocks of this tensor
+      unpack_blocks<T, kAhead, true>(l.t[i], blk, kBlock);
     } else {
-      unpack_blocks<T, 1, false>(t, blk, 0, static_cast<int>(left < kBlock ? left : kBlock));
-      b += warps;
+      int j = i;
+      for (int64_t k = b; k < b + run && k < l.blocks; ++k) {
+        while (j + 1 < l.count && l.first[j + 1] <= k) ++j;
+        const int64_t one = k - l.first[j], left = l.t[j].n - one * kBlock;
+        unpack_blocks<T, 1, false>(l.t[j], one, static_cast<int>(left < kBlock ? left : kBlock));
+      }
     }
   }
 }
