@@ -9,6 +9,9 @@
 // that a captured launch would have to keep).  A warp takes a block of 256 elements, two groups of
 // four per lane, so that every access of the warp is whole lines in all types.
 //
+// Measured, 176M parameters: 770 us (6.4 TB/s), 8-bit states 497 us (5.7 TB/s: 80 instructions an element),
+// norm of bf16 gradients 57 us, unpacking to bf16 166.
+//
 // 8-bit states.  A block has its own ranges: m is e4m3 times max|m| / 448; v is one of 255 values
 // evenly spaced in log2 between the block's smallest and largest v (few percent apart: rows of a
 // weight differ by powers of two, elements of one by less).  Both are rounded up or down at random:
