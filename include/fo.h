@@ -543,7 +543,7 @@ FO_API fo_status fo_token_logprobs_backward(fo_ctx* ctx, const fo_mat* logits, i
  *   loss, the KL term (without kl_coef), the share of clipped tokens, the entropy.
  *   dlogits null: no gradient.
  * Where the clipped value is the smaller one the ratio has no gradient.  Values of vectors in rows
- * that do not count have no effect. */
+ * that do not count have no effect.  Workspace: 32 bytes per SM. */
 typedef struct {
   float scale;                 /* of the logits */
   float clip_low, clip_high;   /* >= 0; clip_low <= 1 */
@@ -591,10 +591,11 @@ FO_API fo_status fo_preference_loss(fo_ctx* ctx, const fo_mat* logits, int P, co
  * 256 elements of the tensor:
  *   m = e4m3 value * m_scale[block];
  *   v = 0 for code 0, else 2^(v_range[2 block] + (code - 1) v_range[2 block + 1])
- * (255 values, evenly spaced in log2, between the block's smallest and largest; a largest value
- * 2^24 times v is taken for v's stead at most).  All bytes zero: states of zero.  Both are rounded
- * to one of the two neighbouring values at random, so that the mean is the value: rounded to the
- * nearest, a mean that moves by a few percent or less a step would not move at all. */
+ * (255 values, evenly spaced in log2, between the block's smallest and largest; smaller ones than
+ * 2^-24 of the largest are kept as that, and none but 0 below 2^-126; a block whose m are all below
+ * 1e-30 is kept as zeros).  All bytes zero: states of zero.  Both are rounded to one of the two
+ * neighbouring values at random, so that the mean is the value: rounded to the nearest, a mean that
+ * moves by a few percent or less a step would not move at all. */
 typedef struct {
   void* param;
   const void* grad;
@@ -623,7 +624,8 @@ FO_API fo_status fo_grad_norm(fo_ctx* ctx, const fo_adamw_group* group, float* n
  * max_norm / (|grad_scale| norm) where norm is given, max_norm > 0 and that is below 1:
  *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2,
  *   w = w - lr (weight_decay w + (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps)),
- * w being the master where there is one (the parameter is then w rounded).  fp32 arithmetic.
+ * w being the master where there is one (the parameter is then w rounded).  fp32 arithmetic; the root takes
+ * a v below 2^-126 for that.
  * norm (null: none): where it is not finite nothing is written at all.  Without it gradients have
  * to be finite.  lr_dev, step_dev (device; null: lr, step): read when the kernel runs, so that a
  * captured step can be replayed with others.  step >= 1 (a smaller one in memory ends the call with

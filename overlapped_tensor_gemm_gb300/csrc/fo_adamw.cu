@@ -16,9 +16,8 @@
 // evenly spaced in log2 between the block's smallest and largest v (few percent apart: rows of a
 // weight differ by powers of two, elements of one by less).  Both are rounded up or down at random:
 // m moves by 1 - b1 of its distance to g in a step, v by 1 - b2, which is mostly less than half the
-// distance of two values, so that rounded to the nearest they would stay where they are.  What v's
-// rounding adds to it in the mean: nothing to first order (part_of below); its spread is that of
-// the values over sqrt(1 - b2^2) steps.
+// distance of two values, so that rounded to the nearest they would stay where they are.  In the mean
+// v's rounding adds nothing to it, to first order in the distance (levels_of).
 #include <cfloat>
 #include <cmath>
 #include <cstring>

@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constan
   constexpr int kHalf = kPairThreads / 2, kWarps = kHalf / 32;
   __shared__ Wide sums[2][kWarps];
   __shared__ int counted[2][kWarps];
-  let_next_start();
+  if (a.more) let_next_start();
   wait_for_previous();
   if (!*a.fine) return;
   const int half = threadIdx.x / kHalf, at = threadIdx.x % kHalf, lane = threadIdx.x & 31;
@@ -352,6 +352,7 @@ fo_status fo_preference_loss(fo_ctx* ctx, const fo_mat* logits, int P, const int
   p.loss = loss;
   a.fine = reinterpret_cast<int32_t*>(p.pair_loss + num_pairs);
   p.fine = a.fine;
+  p.more = dlogits != nullptr;
   p.ctrl = a.ctrl = host_ctrl(ctx);
   a.offsets = offsets;
   a.pairs = num_pairs;

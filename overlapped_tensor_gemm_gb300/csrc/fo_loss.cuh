@@ -74,6 +74,7 @@ struct PairArgs {
   const float* ref_logp;
   float beta, smoothing, margin;
   const int32_t* fine;
+  int32_t more;               // a gradient's launch follows
   float* coef;                // [2 pairs]
   float* pair_loss;           // [pairs]
   float* margins;
