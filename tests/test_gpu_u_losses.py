@@ -577,3 +577,15 @@ def test_contexts_of_four_threads(ctx):
     for t in threads:
         t.join()
     assert not wrong
+
+
+def test_one_column_is_certain(ctx):
+    """Rows of one finite column: log-probability, entropy and gradient are 0 to the bit, lse the column itself."""
+    z = torch.full((3, 40), -float("inf"), device="cuda")
+    z[:, 7] = torch.tensor([0.0, -3.5, 88.25], device="cuda")
+    y = torch.full((3,), 7, dtype=torch.int32, device="cuda")
+    logp, lse, ent = (torch.empty(3, device="cuda") for _ in range(3))
+    ctx.token_logprobs([z], y, logp, lse=lse, entropy=ent)
+    stats, d = torch.empty(4, device="cuda"), torch.empty_like(z)
+    ctx.policy_loss([z], y, torch.ones(3, device="cuda"), stats, dlogits=[d], entropy_coef=0.5)
+    assert (logp == 0).all() and (ent == 0).all() and torch.equal(lse, z[:, 7]) and (d == 0).all()
