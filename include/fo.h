@@ -617,7 +617,8 @@ FO_API fo_status fo_adamw_group_create(const fo_adamw_tensor* tensors, int count
 FO_API fo_status fo_adamw_group_destroy(fo_adamw_group* group);
 
 /* norm[0] = sqrt(sum of the squares of every gradient in the group) (device fp32; the squares are
- * fp32: an element above 1.8e19 gives a norm that is not finite).  Workspace: 8 bytes per CTA. */
+ * fp32: an element above 1.8e19 gives a norm that is not finite).  It lies outside the group's
+ * tensors.  Workspace: 8 bytes per CTA. */
 FO_API fo_status fo_grad_norm(fo_ctx* ctx, const fo_adamw_group* group, float* norm, void* stream);
 
 /* One step for every tensor.  With g = grad_scale * gradient, times
@@ -628,7 +629,7 @@ FO_API fo_status fo_grad_norm(fo_ctx* ctx, const fo_adamw_group* group, float* n
  * a v below 2^-126 for that.
  * norm (null: none): where it is not finite nothing is written at all.  Without it gradients have
  * to be finite.  lr_dev, step_dev (device; null: lr, step): read when the kernel runs, so that a
- * captured step can be replayed with others.  step >= 1 (a smaller one in memory ends the call with
+ * captured step can be replayed with others; they and norm lie outside what the step writes.  step >= 1 (a smaller one in memory ends the call with
  * FO_ERR_RANGE from fo_ctx_poll and nothing is written).
  * stochastic: bf16 parameters without a master are rounded up or down at random (mean: w) instead
  * of to the nearest.  What is random depends on (seed, step, place of the tensor in the group,
@@ -651,8 +652,8 @@ FO_API fo_status fo_adamw_step(fo_ctx* ctx, const fo_adamw_group* group, const f
                                void* stream);
 
 /* The 8-bit states of a group as values: m[i], v[i] (device, n elements of tensor i, `dtype`
- * fo_dtype, 16-byte aligned; entries of tensors with fp32 states are not looked at and may be
- * null).  For checkpoints and inspection. */
+ * fo_dtype, 16-byte aligned, apart from each other and the group's tensors; entries of tensors with
+ * fp32 states are not looked at and may be null).  For checkpoints and inspection. */
 FO_API fo_status fo_adamw_unpack(fo_ctx* ctx, const fo_adamw_group* group, void* const* m, void* const* v,
                                  int dtype, void* stream);
 

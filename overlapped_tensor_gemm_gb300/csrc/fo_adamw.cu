@@ -24,6 +24,7 @@
 
 #include <algorithm>
 #include <new>
+#include <utility>
 #include <vector>
 
 #include <cuda_fp8.h>
@@ -686,6 +687,26 @@ struct Span {
   const char* what;
   bool written;
 };
+// Spans by address, each with the one in front of it or itself that reaches furthest
+struct Spans {
+  std::vector<Span> at, reach;
+  void seal() {
+    std::sort(at.begin(), at.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
+    reach = at;
+    for (size_t i = 1; i < reach.size(); ++i)
+      if (reach[i - 1].hi > reach[i].hi) reach[i] = reach[i - 1];
+  }
+  // one that meets lo .. hi, or null
+  const Span* meets(uintptr_t lo, uintptr_t hi) const {
+    const auto next = std::lower_bound(at.begin(), at.end(), hi, [](const Span& a, uintptr_t v) { return a.lo < v; });
+    const size_t n = next - at.begin();
+    return n > 0 && reach[n - 1].hi > lo ? &reach[n - 1] : nullptr;
+  }
+};
+Span span_of(const void* p, int64_t bytes, int tensor, const char* what, bool written) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+  return Span{lo, lo + static_cast<uintptr_t>(bytes), tensor, what, written};
+}
 
 }  // namespace
 }  // namespace fo
@@ -695,7 +716,17 @@ using namespace fo;
 struct fo_adamw_group {
   std::vector<TensorList> lists;       // by kind
   std::vector<fo_adamw_tensor> tensors;
+  Spans written, used;                 // what a step writes; that and the gradients
 };
+
+// One value beside the group's tensors (null: none)
+static fo_status check_beside(const Spans& spans, const void* p, const char* what) {
+  if (!p) return FO_OK;
+  const Span x = span_of(p, 4, 0, what, false);
+  if (const Span* hit = spans.meets(x.lo, x.hi))
+    return host_failf(FO_ERR_INVALID_ARG, "%s overlaps %s[%d]", what, hit->what, hit->tensor);
+  return FO_OK;
+}
 
 extern "C" {
 
@@ -703,7 +734,7 @@ fo_status fo_adamw_group_create(const fo_adamw_tensor* tensors, int count, fo_ad
   if (!out) return host_fail(FO_ERR_INVALID_ARG, "null out pointer");
   *out = nullptr;
   if (count < 0 || (count > 0 && !tensors)) return host_fail(FO_ERR_INVALID_ARG, "null tensor array");
-  std::vector<Span> spans;
+  Spans used, written;
   for (int i = 0; i < count; ++i) {
     const fo_adamw_tensor& t = tensors[i];
     if (t.n < 0) return host_failf(FO_ERR_SHAPE, "tensor %d: negative size", i);
@@ -727,9 +758,10 @@ fo_status fo_adamw_group_create(const fo_adamw_tensor* tensors, int count, fo_ad
       FO_TRY_HOST(check_ptr(t.m_scale, "m_scale", i, 4));
       FO_TRY_HOST(check_ptr(t.v_range, "v_range", i, 8));
     }
-    auto add = [&](const void* p, int64_t bytes, const char* what, bool written) {
-      const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-      if (p) spans.push_back(Span{lo, lo + static_cast<uintptr_t>(bytes), i, what, written});
+    auto add = [&](const void* p, int64_t bytes, const char* what, bool writes) {
+      if (!p) return;
+      used.at.push_back(span_of(p, bytes, i, what, writes));
+      if (writes) written.at.push_back(used.at.back());
     };
     const int64_t state = eight ? t.n : 4 * t.n;
     add(t.param, t.n * (t.param_dtype == FO_F32 ? 4 : 2), "param", true);
@@ -740,20 +772,23 @@ fo_status fo_adamw_group_create(const fo_adamw_tensor* tensors, int count, fo_ad
     add(t.m_scale, 4 * blocks_of(t.n), "m_scale", true);
     add(t.v_range, 8 * blocks_of(t.n), "v_range", true);
   }
-  std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
-  // the written span and the span of any kind that reach furthest so far
-  const Span* reach = nullptr;
-  const Span* written = nullptr;
-  for (const Span& x : spans) {
-    const Span* hit = x.written ? reach : written;
+  used.seal();
+  written.seal();
+  // each against what starts in front of it: a written one against all, a gradient against the written ones
+  const Span* all = nullptr;
+  const Span* writes = nullptr;
+  for (const Span& x : used.at) {
+    const Span* hit = x.written ? all : writes;
     if (hit && hit->hi > x.lo)
       return host_failf(FO_ERR_INVALID_ARG, "%s[%d] overlaps %s[%d]", x.what, x.tensor, hit->what, hit->tensor);
-    if (!reach || x.hi > reach->hi) reach = &x;
-    if (x.written && (!written || x.hi > written->hi)) written = &x;
+    if (!all || x.hi > all->hi) all = &x;
+    if (x.written && (!writes || x.hi > writes->hi)) writes = &x;
   }
   fo_adamw_group* g = new fo_adamw_group();
   try {
     g->tensors.assign(tensors, tensors + count);
+    g->used = std::move(used);
+    g->written = std::move(written);
     for (int kind = 0; kind < 16; ++kind) {
       int open = -1;  // list that takes the kind's next tensor
       for (int i = 0; i < count; ++i) {
@@ -792,6 +827,7 @@ fo_status fo_adamw_group_destroy(fo_adamw_group* group) {
 fo_status fo_grad_norm(fo_ctx* ctx, const fo_adamw_group* group, float* norm, void* stream) {
   if (!group) return host_fail(FO_ERR_INVALID_ARG, "null group");
   FO_TRY_HOST(check_ptr(norm, "norm", 0, 4));
+  FO_TRY_HOST(check_beside(group->used, norm, "norm"));
   FO_TRY_HOST(host_check_ctx(ctx, 1));
   DeviceGuard dev(host_device(ctx));
   if (!dev.ok) return host_fail(FO_ERR_CUDA, "cudaSetDevice failed");
@@ -841,6 +877,9 @@ fo_status fo_adamw_step(fo_ctx* ctx, const fo_adamw_group* group, const fo_adamw
   if (prm->lr_dev) FO_TRY_HOST(check_ptr(prm->lr_dev, "lr_dev", 0, 4));
   if (prm->step_dev) FO_TRY_HOST(check_ptr(prm->step_dev, "step_dev", 0, 4));
   if (prm->norm) FO_TRY_HOST(check_ptr(prm->norm, "norm", 0, 4));
+  FO_TRY_HOST(check_beside(group->written, prm->lr_dev, "lr_dev"));
+  FO_TRY_HOST(check_beside(group->written, prm->step_dev, "step_dev"));
+  FO_TRY_HOST(check_beside(group->written, prm->norm, "norm"));
   FO_TRY_HOST(host_check_ctx(ctx, 1));
   DeviceGuard dev(host_device(ctx));
   if (!dev.ok) return host_fail(FO_ERR_CUDA, "cudaSetDevice failed");
@@ -879,15 +918,29 @@ fo_status fo_adamw_step(fo_ctx* ctx, const fo_adamw_group* group, const fo_adamw
 }
 
 fo_status fo_adamw_unpack(fo_ctx* ctx, const fo_adamw_group* group, void* const* m, void* const* v, int dtype,
-                          void* stream) {
+                          void* stream) try {
   if (!group) return host_fail(FO_ERR_INVALID_ARG, "null group");
   if (dtype != FO_BF16 && dtype != FO_F32) return host_failf(FO_ERR_INVALID_ARG, "unknown dtype %d", dtype);
   const int count = static_cast<int>(group->tensors.size());
   if (count > 0 && (!m || !v)) return host_fail(FO_ERR_INVALID_ARG, "null tensor array");
+  std::vector<Span> outs;
+  outs.reserve(2 * group->tensors.size());
   for (int i = 0; i < count; ++i) {
-    if (!group->tensors[i].m_scale || group->tensors[i].n == 0) continue;
+    const int64_t n = group->tensors[i].n;
+    if (!group->tensors[i].m_scale || n == 0) continue;
     FO_TRY_HOST(check_ptr(m[i], "m", i));
     FO_TRY_HOST(check_ptr(v[i], "v", i));
+    outs.push_back(span_of(m[i], n * (dtype == FO_F32 ? 4 : 2), i, "m", true));
+    outs.push_back(span_of(v[i], n * (dtype == FO_F32 ? 4 : 2), i, "v", true));
+  }
+  std::sort(outs.begin(), outs.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
+  for (size_t i = 0; i < outs.size(); ++i) {
+    if (i > 0 && outs[i - 1].hi > outs[i].lo)
+      return host_failf(FO_ERR_INVALID_ARG, "%s[%d] overlaps %s[%d]", outs[i].what, outs[i].tensor, outs[i - 1].what,
+                        outs[i - 1].tensor);
+    if (const Span* hit = group->used.meets(outs[i].lo, outs[i].hi))
+      return host_failf(FO_ERR_INVALID_ARG, "%s[%d] overlaps the group's %s[%d]", outs[i].what, outs[i].tensor,
+                        hit->what, hit->tensor);
   }
   FO_TRY_HOST(host_check_ctx(ctx, 1));
   DeviceGuard dev(host_device(ctx));
@@ -915,6 +968,8 @@ fo_status fo_adamw_unpack(fo_ctx* ctx, const fo_adamw_group* group, void* const*
     if (e != cudaSuccess) return host_fail(FO_ERR_CUDA, cudaGetErrorString(e));
   }
   return FO_OK;
+} catch (...) {
+  return host_fail(FO_ERR_OOM, "out of host memory");
 }
 
 }  // extern "C"

@@ -201,13 +201,18 @@ def test_groups_of_nothing_and_of_shared_gradients(lib):  # noqa: F811
     (dict(beta2=-0.1), BAD, "beta2"),
     (dict(eps=-1.0), BAD, "eps"),
     (dict(lr=math.nan), BAD, "lr"),
-    (dict(lr=math.nan, lr_dev=PAGE), BAD, "null context"),
+    (dict(lr=math.nan, lr_dev=_at(40)), BAD, "null context"),
     (dict(weight_decay=math.inf), BAD, "weight_decay"),
     (dict(step=0), BAD, "step=0"),
-    (dict(step=0, step_dev=PAGE), BAD, "null context"),
+    (dict(step=0, step_dev=_at(40)), BAD, "null context"),
     (dict(step_dev=PAGE + 1), NO, "step_dev"),
     (dict(max_norm=1.0), BAD, "max_norm needs norm"),
-    (dict(max_norm=1.0, norm=PAGE), BAD, "null context"),
+    (dict(max_norm=1.0, norm=_at(40)), BAD, "null context"),
+    (dict(norm=_at(0)), BAD, "norm overlaps param[0]"),
+    (dict(lr_dev=_at(3, 3996)), BAD, "lr_dev overlaps m[0]"),
+    (dict(lr_dev=_at(3, 4000)), BAD, "null context"),
+    (dict(step_dev=_at(4)), BAD, "step_dev overlaps v[0]"),
+    (dict(norm=_at(1)), BAD, "null context"),  # (a step only reads its gradients)
     (dict(stochastic=2), BAD, "stochastic"),
 ])
 def test_step_refusals(lib, change, want, text):  # noqa: F811
@@ -225,12 +230,18 @@ def test_norm_and_unpack_refusals(lib):  # noqa: F811
     f = fo.load()
     _refused(f.fo_grad_norm(NULL, None, PAGE, NULL), BAD, "null group")
     _refused(f.fo_grad_norm(NULL, h, None, NULL), BAD, "norm[0]: null")
-    _refused(f.fo_grad_norm(NULL, h, PAGE, NULL), BAD, "null context")
+    _refused(f.fo_grad_norm(NULL, h, _at(40), NULL), BAD, "null context")
+    _refused(f.fo_grad_norm(NULL, h, _at(1, 1996), NULL), BAD, "norm overlaps grad[0]")
+    _refused(f.fo_grad_norm(NULL, h, _at(12), NULL), BAD, "norm overlaps v[1]")
     _refused(f.fo_adamw_step(NULL, None, None, NULL), BAD, "null group")
     _refused(f.fo_adamw_step(NULL, h, None, NULL), BAD, "null parameters")
     ptr = lambda *a: (ctypes.c_void_p * 2)(*a)  # noqa: E731
-    good, none = ptr(PAGE, None), ptr(None, None)
-    _refused(f.fo_adamw_unpack(NULL, h, good, good, 0, NULL), BAD, "null context")
+    good, good_v, none = ptr(_at(40), None), ptr(_at(41), None), ptr(None, None)
+    _refused(f.fo_adamw_unpack(NULL, h, good, good_v, 0, NULL), BAD, "null context")
+    _refused(f.fo_adamw_unpack(NULL, h, good, good, 0, NULL), BAD, "overlaps")
+    _refused(f.fo_adamw_unpack(NULL, h, good, ptr(_at(40, 2000), None), 0, NULL), BAD, "null context")
+    _refused(f.fo_adamw_unpack(NULL, h, good, ptr(_at(40, 2000), None), 1, NULL), BAD, "v[0] overlaps m[0]")
+    _refused(f.fo_adamw_unpack(NULL, h, good, ptr(_at(4, 16), None), 0, NULL), BAD, "v[0] overlaps the group's v[0]")
     _refused(f.fo_adamw_unpack(NULL, h, good, none, 0, NULL), BAD, "v[0]: null")
     _refused(f.fo_adamw_unpack(NULL, h, ptr(PAGE + 8, None), good, 1, NULL), NO, "m[0]")
     _refused(f.fo_adamw_unpack(NULL, h, good, good, 2, NULL), BAD, "dtype")
