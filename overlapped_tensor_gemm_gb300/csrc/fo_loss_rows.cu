@@ -561,12 +561,12 @@ __global__ void __launch_bounds__(Shape<kMode>::kAll + 32 * Shape<kMode>::kMore,
       if (at == 0) {
         r = n ? fetch(n) : first;
         const int64_t k = i + lane * stride;
-        if (kStat && warp == 0 && rank == 0 && n + lane < mine && !r.on) {
+        if (warp == 0 && rank == 0 && n + lane < mine && !r.on) {
           if (r.y >= a.first[a.P]) note_error(a.ctrl, FO_ERR_RANGE, kSiteTargets, static_cast<uint32_t>(k));
           if (a.logp) a.logp[k] = 0.f;
           if (a.lse) a.lse[k] = 0.f;
           if (a.entropy) a.entropy[k] = 0.f;
-          if (a.stat) a.stat[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (kStat && a.stat) a.stat[k] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
         if (r.on) {
           y_rk = 0;

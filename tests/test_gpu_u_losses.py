@@ -589,3 +589,24 @@ def test_one_column_is_certain(ctx):
     stats, d = torch.empty(4, device="cuda"), torch.empty_like(z)
     ctx.policy_loss([z], y, torch.ones(3, device="cuda"), stats, dlogits=[d], entropy_coef=0.5)
     assert (logp == 0).all() and (ent == 0).all() and torch.equal(lse, z[:, 7]) and (d == 0).all()
+
+
+@pytest.mark.parametrize("call", ["token_logprobs", "token_logprobs_backward", "preference_loss"])
+def test_every_call_tells_of_a_target_behind_the_vocabulary(ctx, call):
+    import overlapped_tensor_gemm_gb300 as fo
+    r = Rows(7, [20, 12], seed=21, masked=0.0, dtype=F32)
+    r.targets[5] = 2 ** 31 - 1
+    logp, d, one = torch.full((7,), 3.0, device="cuda"), r.outputs(BF), torch.ones(7, device="cuda")
+    if call == "token_logprobs":
+        ctx.token_logprobs(r.logits, r.targets, logp)
+    elif call == "token_logprobs_backward":
+        ctx.token_logprobs_backward(r.logits, r.targets, one, one, d)
+    else:
+        off = torch.tensor([0, 4, 7], dtype=torch.int32, device="cuda")
+        ctx.preference_loss(r.logits, r.targets, off, torch.empty(1, device="cuda"), logp=logp, dlogits=d)
+    torch.cuda.synchronize()
+    with pytest.raises(fo.FoError) as e:
+        ctx.poll()
+    assert e.value.status == fo.FO_ERR_RANGE and "row 5" in str(e.value)
+    assert call == "token_logprobs_backward" or logp[5] == 0
+    assert call == "token_logprobs" or all((x[5] == 0).all() for x in d)
