@@ -82,7 +82,9 @@ static_assert(sizeof(TensorList) + sizeof(StepArgs) <= 32764, "kernel parameters
 
 // Blocks that a warp of the norm or of the unpacking takes in a row: several, loaded at once, where there
 // are enough for every warp
-__host__ __device__ inline int run_of(int64_t blocks, int64_t warps) { return blocks >= 4 * kAhead * warps ? kAhead : 1; }
+__host__ __device__ inline int run_of(int64_t blocks, int64_t warps) {
+  return blocks >= 4 * kAhead * warps ? kAhead : 1;
+}
 // The tensor of block b: the last one that starts at or in front of it
 template <typename List>
 __device__ __forceinline__ int tensor_of(const List& l, int64_t b) {
@@ -245,7 +247,8 @@ __device__ __forceinline__ float cut_e4m3(float x, uint32_t half_word) {
 struct Levels {
   float per_gap, offset, bend;  // 1 / gap, -low / gap - 1/2, gap ln 2 / 2
 };
-__device__ __forceinline__ void levels_of(Pair v, const Levels& l, uint32_t word0, uint32_t word1, uint32_t (&code)[2]) {
+__device__ __forceinline__ void levels_of(Pair v, const Levels& l, uint32_t word0, uint32_t word1,
+                                          uint32_t (&code)[2]) {
   const Pair magic = both(12582912.f);  // 1.5 2^23: a sum's last bits are the nearest whole number
   float a, b, x, y;
   unpack2(v, a, b);
@@ -415,7 +418,8 @@ __device__ __forceinline__ void step_block(const TensorRef& t, int64_t blk, int 
       for (int k = 0; k < 2; ++k) {
         float x, y;
         unpack2(w[q + k], x, y);
-        w[q + k] = pack2(cut_bf16(x, word[2 * q + 2 * k] * 0x9E3779B9u), cut_bf16(y, word[2 * q + 2 * k + 1] * 0x9E3779B9u));
+        w[q + k] = pack2(cut_bf16(x, word[2 * q + 2 * k] * 0x9E3779B9u),
+                         cut_bf16(y, word[2 * q + 2 * k + 1] * 0x9E3779B9u));
       }
     }
     store4<kFull>(static_cast<TP*>(t.param) + at + q * 64, n - q * 64, reinterpret_cast<Pair(&)[2]>(w[q]));

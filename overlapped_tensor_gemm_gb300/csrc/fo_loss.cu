@@ -330,7 +330,8 @@ fo_status fo_preference_loss(fo_ctx* ctx, const fo_mat* logits, int P, const int
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // statistics of every row; coefficients and losses of the pairs
   void* work = nullptr;
-  FO_TRY_HOST(host_buffer_kept(ctx, kSlotLoss, static_cast<size_t>(a.rows * 16 + seqs * 4 + num_pairs * 4 + 4), s, &work));
+  const size_t bytes = static_cast<size_t>(a.rows * 16 + seqs * 4 + num_pairs * 4 + 4);
+  FO_TRY_HOST(host_buffer_kept(ctx, kSlotLoss, bytes, s, &work));
   float4* stat = static_cast<float4*>(work);
   PairArgs p;
   std::memset(&p, 0, sizeof(p));

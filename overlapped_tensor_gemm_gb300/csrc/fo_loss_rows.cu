@@ -102,7 +102,9 @@ struct Group<uint16_t> {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       float lo, hi;
-      asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; add.f32.bf16 %0, l, %3; add.f32.bf16 %1, h, %3;}" : "=f"(lo), "=f"(hi) : "r"(w[k]), "f"(nbase));
+      asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; add.f32.bf16 %0, l, %3; add.f32.bf16 %1, h, %3;}"
+          : "=f"(lo), "=f"(hi)
+          : "r"(w[k]), "f"(nbase));
       v[k] = pack2(lo, hi);
     }
   }
@@ -514,7 +516,8 @@ __global__ void __launch_bounds__(Shape<kMode>::kAll + 32 * Shape<kMode>::kMore,
             while (g >= a.groups[rk + 1]) ++rk;
             int stop = end < a.groups[rk + 1] ? end : a.groups[rk + 1];
             if (!on && stop > g + S::kZeros / 16) stop = g + S::kZeros / 16;
-            bulk_store(static_cast<uint8_t*>(a.d[rk]) + (i * a.ldd[rk] * sizeof(TD) + static_cast<int64_t>(g - a.groups[rk]) * 16),
+            bulk_store(static_cast<uint8_t*>(a.d[rk]) +
+                           (i * a.ldd[rk] * sizeof(TD) + static_cast<int64_t>(g - a.groups[rk]) * 16),
                        src, static_cast<uint32_t>(stop - g) * 16u);
             if (on) src += (stop - g) * 16;
             g = stop;
@@ -705,7 +708,8 @@ __global__ void __launch_bounds__(Shape<kMode>::kAll + 32 * Shape<kMode>::kMore,
           }
           if (kMode == kLossPolicy) {
             // the loss through this row: da = dL/dlogp, dh = dL/dH
-            const float weight = __shfl_sync(0xffffffffu, in0, at) * per_weight, adv = __shfl_sync(0xffffffffu, in1, at);
+            const float weight = __shfl_sync(0xffffffffu, in0, at) * per_weight;
+            const float adv = __shfl_sync(0xffffffffu, in1, at);
             const float old = __shfl_sync(0xffffffffu, in2, at), ref = __shfl_sync(0xffffffffu, in3, at);
             const float ratio = expf(a.old_logp ? lp - old : 0.f);
             const float held = fminf(fmaxf(ratio, a.ratio_lo), a.ratio_hi) * adv, free = ratio * adv;
@@ -726,8 +730,8 @@ __global__ void __launch_bounds__(Shape<kMode>::kAll + 32 * Shape<kMode>::kMore,
             }
             if (grad && lane == 0) {
               const float inv = -a.scale * exp2f(-log_s);
-              sm.slope[set] =
-                  make_float4(base, inv * (kEnt ? da + dh * (entropy - kLn2 * log_s) : da), inv * dh * kLn2, a.scale * da);
+              const float k0 = inv * (kEnt ? da + dh * (entropy - kLn2 * log_s) : da);
+              sm.slope[set] = make_float4(base, k0, inv * dh * kLn2, a.scale * da);
               mbar_arrive(&sm.ready[set]);
             }
           }
@@ -776,7 +780,8 @@ __global__ void __launch_bounds__(Shape<kMode>::kAll + 32 * Shape<kMode>::kMore,
         } else {
           while (g0 >= a.groups[rk + 1]) ++rk;
           if (left >= kChunkGroups && g0 + kChunkGroups <= a.groups[rk + 1]) {
-            TD* to = static_cast<TD*>(a.d[rk]) + i * a.ldd[rk] + static_cast<int64_t>(g0 + tid - a.groups[rk]) * kCols;
+            TD* to = static_cast<TD*>(a.d[rk]) + i * a.ldd[rk] +
+                     static_cast<int64_t>(g0 + tid - a.groups[rk]) * kCols;
             uint4 x[S::kBatch];  // (all read first: a store might be to what is read next)
 #pragma unroll
             for (int j = 0; j < S::kBatch; ++j) x[j] = src[j * kThreads];
