@@ -9,7 +9,7 @@
 // that a captured launch would have to keep).  A warp takes a block of 256 elements, two groups of
 // four per lane, so that every access of the warp is whole lines in all types.
 //
-// Measured, 176M parameters: 770 us (6.4 TB/s), 8-bit states 497 us (5.7 TB/s: 80 instructions an element),
+// Measured, 176M parameters: 762 us (6.5 TB/s), 8-bit states 461 us (6.1 TB/s: 69 instructions an element),
 // norm of bf16 gradients 57 us, unpacking to bf16 166.
 //
 // 8-bit states.  A block has its own ranges: m is e4m3 times max|m| / 448; v is one of 255 values
@@ -38,8 +38,14 @@ namespace fo {
 namespace {
 
 constexpr int kBlock = 256;           // elements of a block: 8 per lane of a warp
-constexpr int kAdamThreads = 256;
+constexpr int kAdamThreads = 256;     // norm, unpacking
 constexpr int kCtasPerSm = 4;
+constexpr int kStepThreads = 256;
+// CTAs of a step per SM.  8-bit states: as many as have the registers for a block under way beside the one
+// that is computed (4 without it: 742 us for 176M parameters with norm and unpacking, 706 with it).  32 bits
+// need less arithmetic than that, and fewer places in memory at once (3: 839 us with the norm, 2: 823, 1: 925;
+// 2 with the registers of 2: 833).
+constexpr int kStepCtas8 = 3, kStepCtas32 = 2;
 constexpr int kListTensors = 400;     // tensors of one launch
 constexpr int kAhead = 4;             // see run_of
 constexpr float kMaxE4m3 = 448.f;
@@ -221,49 +227,71 @@ __device__ __forceinline__ void from_e4m3(uint32_t q, Pair (&v)[2]) {
     v[k] = pack2(low_half(pair, 0.f), high_half(pair, 0.f));
   }
 }
-// 4 codes of v as values: a code is the low byte of an f16 from 1024 on, where steps are 1
+// 4 codes of v as values: a code is the low byte of an f16 from 1024 on, where steps are 1.  (Zeros are
+// rare: without them no code is looked at by itself.)
 __device__ __forceinline__ void from_levels(uint32_t q, float low, float gap, Pair (&v)[2]) {
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const uint32_t pair = __byte_perm(q, 0x64646464u, k ? 0x4342 : 0x4140);
-    const Pair n = pack2(low_half(pair, -1025.f), high_half(pair, -1025.f));  // code - 1
-    float x, y, a, b;
-    unpack2(n, a, b);
-    unpack2(ffma2(n, both(gap), both(low)), x, y);
-    v[k] = pack2(a >= 0.f ? fast_exp2(x) : 0.f, b >= 0.f ? fast_exp2(y) : 0.f);
+    float x, y;
+    unpack2(ffma2(pack2(low_half(pair, -1025.f), high_half(pair, -1025.f)), both(gap), both(low)), x, y);
+    v[k] = pack2(fast_exp2(x), fast_exp2(y));
+  }
+  if ((q - 0x01010101u) & ~q & 0x80808080u) {  // a byte is 0
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float x, y;
+      unpack2(v[k], x, y);
+      v[k] = pack2(q >> (16 * k) & 0xFFu ? x : 0.f, q >> (16 * k + 8) & 0xFFu ? y : 0.f);
+    }
   }
 }
-// x (at most 448) up or down to an e4m3 value: what a step holds below is cut off after a random
-// part of a step is added.  Below 2^-6 the steps stay 2^-9 wide, as they are from 2^-6 to 2^-5, so
-// there the sum with 2^-6 is cut.
-__device__ __forceinline__ float cut_e4m3(float x, uint32_t half_word) {
-  const float size = fminf(fabsf(x), kMaxE4m3), lift = size < 0.015625f ? 0.015625f : 0.f;
-  const uint32_t q = (__float_as_uint(size + lift) + (half_word << 4)) & 0xFFF00000u;
-  return x == x ? copysignf(__uint_as_float(q) - lift, x) : x;
+// 4 values of m (in units of the scale: at most 448 and a few units in the last place) up or down to e4m3:
+// a random part of a step is added and what a step holds below is cut off.  Times 2^-120 the ranges of
+// e4m3, its subnormal one too, are those of fp32: an e4m3 number is the bits from the 20th on, and the sign.
+__device__ __forceinline__ uint32_t to_e4m3(const Pair (&m)[2], float inv_scale, const uint32_t* word) {
+  uint32_t sum[4], sign[4];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    float x, y;
+    unpack2(mul2(mul2(m[k], both(inv_scale)), both(0x1p-120f)), x, y);
+    sign[2 * k] = __float_as_uint(x);
+    sign[2 * k + 1] = __float_as_uint(y);
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) sum[k] = (sign[k] << 4) + __byte_perm(word[k], 0, 0x4104);  // (low half, 8 up)
+  const uint32_t code = __byte_perm(__byte_perm(sum[0], sum[1], 0x0073), __byte_perm(sum[2], sum[3], 0x0073), 0x5410);
+  const uint32_t high = __byte_perm(__byte_perm(sign[0], sign[1], 0x0073), __byte_perm(sign[2], sign[3], 0x0073), 0x5410);
+  return code | (high & 0x80808080u);
 }
 // The codes of two v (low bytes).  y = (log2 v - low) / gap counts codes from 1; with s = y - 1/2 less
 // its nearest whole number w, y is w and a part s + 1/2; up with probability part - bend part (1 - part)
-// (the mean of the two values, not of their logarithms, is v: to first order in gap).
+// (the mean of the two values, not of their logarithms, is v: to first order in gap).  Up or not is the
+// sum of w and part less a random number rounded up.  Zeros are not looked at.
 struct Levels {
   float per_gap, offset, bend;  // 1 / gap, -low / gap - 1/2, gap ln 2 / 2
 };
+__device__ __forceinline__ Pair add2_up(Pair a, Pair b) {
+  Pair r;
+  asm("add.rp.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ void levels_of(Pair v, const Levels& l, uint32_t word0, uint32_t word1,
                                           uint32_t (&code)[2]) {
-  const Pair magic = both(12582912.f);  // 1.5 2^23: a sum's last bits are the nearest whole number
+  const Pair magic = both(12582913.f);  // 1.5 2^23 + 1: a sum's last bits are the nearest whole number and 1
   float a, b, x, y;
   unpack2(v, a, b);
   unpack2(ffma2(pack2(fast_log2(a), fast_log2(b)), both(l.per_gap), both(l.offset)), x, y);
   const Pair at = pack2(fminf(fmaxf(x, -0.5f), 253.5f), fminf(fmaxf(y, -0.5f), 253.5f));
   const Pair sum = fadd2(at, magic), s = sub2(at, sub2(sum, magic));
   const Pair part = ffma2(s, ffma2(s, both(l.bend), both(1.f)), both(fmaf(l.bend, -0.25f, 0.5f)));
-  const Pair r = fadd2(pack2(__uint_as_float(0x4B000000u | word0 >> 16), __uint_as_float(0x4B000000u | word1 >> 16)),
+  // 2^23 and the random number's upper half
+  const Pair r = fadd2(pack2(__uint_as_float(__byte_perm(word0, 0x4B000000u, 0x7432)),
+                             __uint_as_float(__byte_perm(word1, 0x4B000000u, 0x7432))),
                        both(-8388608.f));
-  float r0, r1, p0, p1;
-  unpack2(r, r0, r1);
-  unpack2(mul2(part, both(65536.f)), p0, p1);
-  unpack2(sum, x, y);
-  code[0] = a > 0.f ? __float_as_uint(x) + (r0 < p0 ? 2u : 1u) : 0u;
-  code[1] = b > 0.f ? __float_as_uint(y) + (r1 < p1 ? 2u : 1u) : 0u;
+  unpack2(add2_up(sum, ffma2(r, both(-0x1p-16f), part)), x, y);
+  code[0] = __float_as_uint(x);
+  code[1] = __float_as_uint(y);
 }
 // A bf16 value next to w, by the upper half of `word`; infinities and NaN stay
 __device__ __forceinline__ float cut_bf16(float w, uint32_t word) {
@@ -287,50 +315,66 @@ struct Step {
   uint32_t key;
   bool cut;
 };
-// One block, the first n of its elements inside the tensor.  Squares, roots and quotients keep to
-// numbers from 2^-126 on: a smaller v counts as that in the root (its update is smaller for it).
-template <bool kP32, bool kG32, bool kHasMaster, bool k8, bool kFull>
-__device__ __forceinline__ void step_block(const TensorRef& t, int64_t blk, int n, const Step& a) {
+// A block as it lies in memory
+template <bool kP32, bool kG32, bool kHasMaster, bool k8>
+struct Raw {
   typedef typename std::conditional<kP32, float, uint16_t>::type TP;
   typedef typename std::conditional<kG32, float, uint16_t>::type TG;
   typedef typename std::conditional<kHasMaster, float, TP>::type TW;
+  typedef typename std::conditional<k8, uint8_t, float>::type TS;
+  decltype(load4<true>(static_cast<const TG*>(nullptr), 0)) g[2];
+  decltype(load4<true>(static_cast<const TW*>(nullptr), 0)) w[2];
+  decltype(load4<true>(static_cast<const TS*>(nullptr), 0)) m[2], v[2];
+  float scale;
+  float2 range;
+  template <bool kFull>
+  __device__ __forceinline__ void load(const TensorRef& t, int64_t blk, int n) {
+    const int lane = threadIdx.x & 31;
+    const int64_t at = blk * kBlock + lane * 4;
+    n -= lane * 4;
+    const TW* const tw = (kHasMaster ? reinterpret_cast<const TW*>(t.master) : static_cast<const TW*>(t.param)) + at;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      g[q] = load4<kFull>(static_cast<const TG*>(t.grad) + at + q * 128, n - q * 128);
+      w[q] = load4<kFull>(tw + q * 128, n - q * 128);
+      m[q] = load4<kFull>(static_cast<const TS*>(t.m) + at + q * 128, n - q * 128);
+      v[q] = load4<kFull>(static_cast<const TS*>(t.v) + at + q * 128, n - q * 128);
+    }
+    if constexpr (k8) {
+      scale = t.m_scale[blk];
+      range = reinterpret_cast<const float2*>(t.v_range)[blk];
+    }
+  }
+};
+// One block, the first n of its elements inside the tensor.  Squares, roots and quotients keep to
+// numbers from 2^-126 on: a smaller v counts as that in the root (its update is smaller for it).
+template <bool kP32, bool kG32, bool kHasMaster, bool k8, bool kFull>
+__device__ __forceinline__ void step_block(const TensorRef& t, int64_t blk, int n, const Step& a,
+                                           const Raw<kP32, kG32, kHasMaster, k8>& raw) {
+  typedef typename std::conditional<kP32, float, uint16_t>::type TP;
   const int lane = threadIdx.x & 31;
   const int64_t at = blk * kBlock + lane * 4;
   n -= lane * 4;
-  TW* const tw = (kHasMaster ? reinterpret_cast<TW*>(t.master) : static_cast<TW*>(t.param)) + at;
-  const TG* const tg = static_cast<const TG*>(t.grad) + at;
-  auto g0 = load4<kFull>(tg, n), g1 = load4<kFull>(tg + 128, n - 128);
-  auto w0 = load4<kFull>(tw, n), w1 = load4<kFull>(tw + 128, n - 128);
   Pair g[4], w[4], m[4], v[4];
   float keep1 = a.beta1;
   if constexpr (k8) {
-    const uint8_t* const tm = static_cast<const uint8_t*>(t.m) + at;
-    const uint8_t* const tv = static_cast<const uint8_t*>(t.v) + at;
-    const uint32_t m0 = load4<kFull>(tm, n), m1 = load4<kFull>(tm + 128, n - 128);
-    const uint32_t v0 = load4<kFull>(tv, n), v1 = load4<kFull>(tv + 128, n - 128);
-    keep1 *= t.m_scale[blk];
-    const float2 r = reinterpret_cast<const float2*>(t.v_range)[blk];
-    from_e4m3(m0, reinterpret_cast<Pair(&)[2]>(m[0]));
-    from_e4m3(m1, reinterpret_cast<Pair(&)[2]>(m[2]));
-    from_levels(v0, r.x, r.y, reinterpret_cast<Pair(&)[2]>(v[0]));
-    from_levels(v1, r.x, r.y, reinterpret_cast<Pair(&)[2]>(v[2]));
+    keep1 *= raw.scale;
+    from_e4m3(raw.m[0], reinterpret_cast<Pair(&)[2]>(m[0]));
+    from_e4m3(raw.m[1], reinterpret_cast<Pair(&)[2]>(m[2]));
+    from_levels(raw.v[0], raw.range.x, raw.range.y, reinterpret_cast<Pair(&)[2]>(v[0]));
+    from_levels(raw.v[1], raw.range.x, raw.range.y, reinterpret_cast<Pair(&)[2]>(v[2]));
   } else {
-    const float* const tm = static_cast<const float*>(t.m) + at;
-    const float* const tv = static_cast<const float*>(t.v) + at;
-    const float4 m0 = load4<kFull>(tm, n), m1 = load4<kFull>(tm + 128, n - 128);
-    const float4 v0 = load4<kFull>(tv, n), v1 = load4<kFull>(tv + 128, n - 128);
-    values(m0, reinterpret_cast<Pair(&)[2]>(m[0]));
-    values(m1, reinterpret_cast<Pair(&)[2]>(m[2]));
-    values(v0, reinterpret_cast<Pair(&)[2]>(v[0]));
-    values(v1, reinterpret_cast<Pair(&)[2]>(v[2]));
+    values(raw.m[0], reinterpret_cast<Pair(&)[2]>(m[0]));
+    values(raw.m[1], reinterpret_cast<Pair(&)[2]>(m[2]));
+    values(raw.v[0], reinterpret_cast<Pair(&)[2]>(v[0]));
+    values(raw.v[1], reinterpret_cast<Pair(&)[2]>(v[2]));
   }
-  values(g0, reinterpret_cast<Pair(&)[2]>(g[0]));
-  values(g1, reinterpret_cast<Pair(&)[2]>(g[2]));
-  values(w0, reinterpret_cast<Pair(&)[2]>(w[0]));
-  values(w1, reinterpret_cast<Pair(&)[2]>(w[2]));
+  values(raw.g[0], reinterpret_cast<Pair(&)[2]>(g[0]));
+  values(raw.g[1], reinterpret_cast<Pair(&)[2]>(g[2]));
+  values(raw.w[0], reinterpret_cast<Pair(&)[2]>(w[0]));
+  values(raw.w[1], reinterpret_cast<Pair(&)[2]>(w[2]));
 
-  // (the bits of values that are not negative are ordered as the values are; those of 0, less one,
-  // come last)
+  // (the bits of values that are not negative are ordered as the values are)
   float top_m = 0.f;
   uint32_t top_v = 0, min_v = 0xFFFFFFFFu;
 #pragma unroll
@@ -346,7 +390,7 @@ __device__ __forceinline__ void step_block(const TensorRef& t, int64_t blk, int 
     w[q] = sub2(w[q], ffma2(both(a.decay), w[q], change));
     if (k8) {
       top_v = max(top_v, max(__float_as_uint(x0), __float_as_uint(x1)));
-      min_v = min(min_v, min(__float_as_uint(x0) - 1u, __float_as_uint(x1) - 1u));
+      min_v = min(min_v, min(__float_as_uint(x0), __float_as_uint(x1)));
       unpack2(m[q], y0, y1);
       top_m = fmax3(top_m, fabsf(y0), fabsf(y1));
     }
@@ -362,6 +406,17 @@ __device__ __forceinline__ void step_block(const TensorRef& t, int64_t blk, int 
     top_m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top_m)));
     top_v = __reduce_max_sync(0xffffffffu, top_v);
     min_v = __reduce_min_sync(0xffffffffu, min_v);
+    const bool zeros = min_v == 0;
+    if (zeros) {  // the smallest of the others: the bits of 0, less one, come last
+      min_v = 0xFFFFFFFFu;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float x, y;
+        unpack2(v[q], x, y);
+        min_v = min(min_v, min(__float_as_uint(x) - 1u, __float_as_uint(y) - 1u));
+      }
+      min_v = __reduce_min_sync(0xffffffffu, min_v) + 1u;
+    }
     float scale = 0.f, inv_scale = 0.f, low = 0.f, gap = 0.f;
     Levels l = {0.f, -0.5f, 0.f};
     if (top_m > 1e-30f) {  // smaller ones are kept as zeros
@@ -370,7 +425,7 @@ __device__ __forceinline__ void step_block(const TensorRef& t, int64_t blk, int 
     }
     if (top_v != 0) {
       const float top = fast_log2(fmaxf(__uint_as_float(top_v), FLT_MIN));
-      low = fmaxf(fast_log2(fmaxf(__uint_as_float(min_v + 1u), FLT_MIN)), top - kOctaves);
+      low = fmaxf(fast_log2(fmaxf(__uint_as_float(min_v), FLT_MIN)), top - kOctaves);
       gap = (top - low) * (1.f / 254.f);
       if (gap > 0.f) {
         l.per_gap = __fdividef(1.f, gap);
@@ -382,20 +437,21 @@ __device__ __forceinline__ void step_block(const TensorRef& t, int64_t blk, int 
     uint8_t* const tv = static_cast<uint8_t*>(t.v) + at;
 #pragma unroll
     for (int q = 0; q < 4; q += 2) {
-      uint32_t c0[2], c1[2], e[2];
+      uint32_t c0[2], c1[2];
       levels_of(v[q], l, word[2 * q], word[2 * q + 1], c0);
       levels_of(v[q + 1], l, word[2 * q + 2], word[2 * q + 3], c1);
+      uint32_t code = __byte_perm(__byte_perm(c0[0], c0[1], 0x0040), __byte_perm(c1[0], c1[1], 0x0040), 0x5410);
+      if (zeros) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float x, y;
-        unpack2(mul2(m[q + k], both(inv_scale)), x, y);
-        e[k] = __nv_cvt_float2_to_fp8x2(make_float2(cut_e4m3(x, word[2 * q + 2 * k] & 0xFFFFu),
-                                                    cut_e4m3(y, word[2 * q + 2 * k + 1] & 0xFFFFu)),
-                                        __NV_SATFINITE, __NV_E4M3);
+        for (int k = 0; k < 2; ++k) {
+          float x, y;
+          unpack2(v[q + k], x, y);
+          if (!(x > 0.f)) code &= ~(0xFFu << (16 * k));
+          if (!(y > 0.f)) code &= ~(0xFF00u << (16 * k));
+        }
       }
-      store4<kFull>(tm + q * 64, n - q * 64, e[0] | e[1] << 16);
-      store4<kFull>(tv + q * 64, n - q * 64,
-                    __byte_perm(__byte_perm(c0[0], c0[1], 0x0040), __byte_perm(c1[0], c1[1], 0x0040), 0x5410));
+      store4<kFull>(tm + q * 64, n - q * 64, to_e4m3(reinterpret_cast<Pair(&)[2]>(m[q]), inv_scale, word + 2 * q));
+      store4<kFull>(tv + q * 64, n - q * 64, code);
     }
     if (lane == 0) {
       t.m_scale[blk] = scale;
@@ -427,7 +483,7 @@ __device__ __forceinline__ void step_block(const TensorRef& t, int64_t blk, int 
 }
 
 template <bool kP32, bool kG32, bool kHasMaster, bool k8>
-__global__ void __launch_bounds__(kAdamThreads, kCtasPerSm)
+__global__ void __launch_bounds__(kStepThreads, kStepCtas8)
     adamw_kernel(const __grid_constant__ TensorList l, const __grid_constant__ StepArgs a, bool cut) {
   __shared__ float fixes[2];
   Step s;
@@ -462,18 +518,28 @@ __global__ void __launch_bounds__(kAdamThreads, kCtasPerSm)
   s.rate = lr * fix1;
   s.key = scatter(scatter(a.seed_low ^ scatter(static_cast<uint32_t>(step))) ^ a.seed_high);
   s.cut = cut;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kAdamThreads / 32);
-  int64_t b = static_cast<int64_t>(blockIdx.x) * (kAdamThreads / 32) + (threadIdx.x >> 5);
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kStepThreads / 32);
+  int64_t b = static_cast<int64_t>(blockIdx.x) * (kStepThreads / 32) + (threadIdx.x >> 5);
   if (b >= l.blocks) return;
   int i = tensor_of(l, b);
+  // while a block is computed the warp's next one comes, where the same tensor has it whole
+  Raw<kP32, kG32, kHasMaster, k8> next;
+  bool have = false;
   for (; b < l.blocks; b += warps) {
     while (i + 1 < l.count && l.first[i + 1] <= b) ++i;
     const TensorRef& t = l.t[i];
     const int64_t blk = b - l.first[i], left = t.n - blk * kBlock;
     if (left >= kBlock) {
-      step_block<kP32, kG32, kHasMaster, k8, true>(t, blk, kBlock, s);
+      if (!have) next.template load<true>(t, blk, kBlock);
+      const Raw<kP32, kG32, kHasMaster, k8> now = next;
+      have = left >= (warps + 1) * kBlock;
+      if (have) next.template load<true>(t, blk + warps, kBlock);
+      step_block<kP32, kG32, kHasMaster, k8, true>(t, blk, kBlock, s, now);
     } else {
-      step_block<kP32, kG32, kHasMaster, k8, false>(t, blk, static_cast<int>(left), s);
+      Raw<kP32, kG32, kHasMaster, k8> now;
+      now.template load<false>(t, blk, static_cast<int>(left));
+      step_block<kP32, kG32, kHasMaster, k8, false>(t, blk, static_cast<int>(left), s, now);
+      have = false;
     }
   }
 }
@@ -670,9 +736,9 @@ StepKernel step_kernel(int kind) {
   return kind & kMaster ? step_kernel_of<false, true>(kind) : step_kernel_of<false, false>(kind);
 }
 
-int grid_for(fo_ctx* ctx, int64_t blocks) {
-  const int64_t ctas = (blocks + kAdamThreads / 32 - 1) / (kAdamThreads / 32);
-  const int64_t most = static_cast<int64_t>(host_num_sms(ctx)) * kCtasPerSm;
+int grid_for(fo_ctx* ctx, int64_t blocks, int threads = kAdamThreads, int per_sm = kCtasPerSm) {
+  const int64_t ctas = (blocks + threads / 32 - 1) / (threads / 32);
+  const int64_t most = static_cast<int64_t>(host_num_sms(ctx)) * per_sm;
   return static_cast<int>(ctas < most ? ctas : most);
 }
 
@@ -913,7 +979,8 @@ fo_status fo_adamw_step(fo_ctx* ctx, const fo_adamw_group* group, const fo_adamw
   a.norm = prm->norm;
   a.ctrl = host_ctrl(ctx);
   for (const TensorList& l : group->lists) {
-    step_kernel(l.kind)<<<grid_for(ctx, l.blocks), kAdamThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+    const int grid = grid_for(ctx, l.blocks, kStepThreads, l.kind & kStates8 ? kStepCtas8 : kStepCtas32);
+    step_kernel(l.kind)<<<grid, kStepThreads, 0, static_cast<cudaStream_t>(stream)>>>(
         l, a, prm->stochastic && !(l.kind & (kParam32 | kMaster)));
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return host_fail(FO_ERR_CUDA, cudaGetErrorString(e));
