@@ -9,7 +9,7 @@
 // that a captured launch would have to keep).  A warp takes a block of 256 elements, two groups of
 // four per lane, so that every access of the warp is whole lines in all types.
 //
-// Measured, 176M parameters: 762 us (6.5 TB/s), 8-bit states 461 us (6.1 TB/s: 69 instructions an element),
+// Measured, 176M parameters: 762 us (6.5 TB/s), 8-bit states 461 us (6.1 TB/s: 77 instructions an element),
 // norm of bf16 gradients 57 us, unpacking to bf16 166.
 //
 // 8-bit states.  A block has its own ranges: m is e4m3 times max|m| / 448; v is one of 255 values
