@@ -316,3 +316,19 @@ def test_stochastic_weights_are_right_in_the_mean(ctx):
     assert moved[0] == 0
     # each step adds at most (2^-7)^2 / 4 of variance to an element; five standard deviations of the mean
     assert abs(moved[1] - steps * 2.0 ** -10) <= 5 * (2.0 ** -8) * np.sqrt(steps / n) + 1e-6
+
+
+@pytest.mark.parametrize("kinds", [KINDS[0:2], KINDS[3:5], KINDS[8:10], KINDS[10:11]],
+                         ids=["32-bit", "8-bit", "32-bit, bf16", "8-bit, bf16"])
+def test_long_tensors_between_short_ones(ctx, kinds):
+    """Several blocks of a tensor for every warp, then another tensor's: what is loaded ahead is the right block's."""
+    s = Set([2500001, 2500001, 700, 3, 1, 257, 2000256, 2000256], kinds, seed=14)
+    before = [s.values(i) for i in range(len(s.sizes))]
+    norm = torch.zeros(1, device="cuda")
+    ctx.grad_norm(s.group, norm)
+    ctx.adamw_step(s.group, step=5, stochastic=True, seed=99, norm=norm, **HYPER)
+    torch.cuda.synchronize()
+    s.check_guards()
+    _check_step(s, before, 5, 1.0, True, 99)
+    want = np.sqrt(sum((g.double() ** 2).sum().item() for g in s.g))
+    assert abs(norm.item() - want) <= want * 264 * u
