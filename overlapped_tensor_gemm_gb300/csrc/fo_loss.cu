@@ -158,6 +158,7 @@ fo_status check_logits(const fo_mat* logits, int P, const fo_mat* d, const int32
   }
   if (vocab < 1) return host_fail(FO_ERR_SHAPE, "the vocabulary must have at least one entry");
   a->first[P] = static_cast<int32_t>(vocab);
+  a->gradient = d != nullptr;
   a->P = P;
   a->rows = logits[0].rows;
   a->scale = scale;
@@ -359,7 +360,7 @@ fo_status fo_preference_loss(fo_ctx* ctx, const fo_mat* logits, int P, const int
   a.pairs = num_pairs;
   a.stat = stat;
   LossArgs back = a;
-  for (int r = 0; r < P; ++r) a.d[r] = nullptr;
+  a.gradient = 0;
   a.logp = logp;
   k.mode = kLossForward;
   FO_TRY_HOST(run_rows(ctx, a, k, s));

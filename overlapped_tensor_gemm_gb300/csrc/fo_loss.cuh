@@ -22,13 +22,13 @@ constexpr int kLossMaxCtas = 8;     // CTAs of one row
 
 enum LossMode : int {
   kLossForward = 0,   // statistics alone
-  kLossPolicy = 1,    // statistics, the policy loss, and (d[0] given) the gradient
+  kLossPolicy = 1,    // statistics, the policy loss, and (LossArgs::gradient) the gradient
   kLossBackward = 2   // the gradient, from statistics given
 };
 
 struct LossArgs {
   const void* z[kMaxP];
-  void* d[kMaxP];             // d[0] null: no gradient
+  void* d[kMaxP];             // null where a rank has no columns, or no gradient is wanted
   int64_t ldz[kMaxP], ldd[kMaxP];
   int32_t cols[kMaxP];
   int32_t first[kMaxP + 1];   // vocabulary ids: rank r has first[r] .. first[r + 1]
@@ -36,6 +36,7 @@ struct LossArgs {
   int32_t ctas;               // CTAs of one row: each takes a range of the groups
   int32_t twice;              // a CTA's range does not fit: it is copied again for the gradient
   int32_t backwards;          // rows from the last one on
+  int32_t gradient;           // whether a gradient is wanted
   int32_t P;
   int64_t rows;
   float scale;

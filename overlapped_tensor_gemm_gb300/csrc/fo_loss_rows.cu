@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kAll + 32 * Shape<kMode>::kMore,
   const int rank = static_cast<int>(blockIdx.x % a.ctas);
   const int64_t team = blockIdx.x / a.ctas, teams = gridDim.x / a.ctas;
   const bool together = kStat && a.ctas > 1;  // launched as clusters
-  const bool grad = kMode != kLossForward && a.d[0];
+  const bool grad = kMode != kLossForward && a.gradient;
   const bool twice = kStat && grad && a.twice;
   // gradients are made in the slots, in the logits' place, and copied from there
   const bool out = kMode == kLossPolicy && sizeof(TZ) == sizeof(TD) && grad && !twice;
@@ -874,7 +874,7 @@ cudaError_t loss_rows_launch(LossArgs a, const LossKind& k, int num_sms, cudaStr
   if (one) {
     while (least < kLossMaxCtas && chunks > least * kLossFit) least *= 2;
     if (chunks > least * Shape<kLossPolicy>::kSlots) {
-      a.twice = a.d[0] != nullptr;
+      a.twice = a.gradient;
       least = 1;
     }
   }
