@@ -712,7 +712,9 @@ __global__ void __launch_bounds__(Shape<kMode>::kAll + 32 * Shape<kMode>::kMore,
             const float adv = __shfl_sync(0xffffffffu, in1, at);
             const float old = __shfl_sync(0xffffffffu, in2, at), ref = __shfl_sync(0xffffffffu, in3, at);
             const float ratio = expf(a.old_logp ? lp - old : 0.f);
-            const float held = fminf(fmaxf(ratio, a.ratio_lo), a.ratio_hi) * adv, free = ratio * adv;
+            const float held = fminf(fmaxf(ratio, a.ratio_lo), a.ratio_hi) * adv;
+            // (a ratio may leave fp32: without an advantage it counts nothing all the same)
+            const float free = adv == 0.f && ratio == INFINITY ? 0.f : ratio * adv;
             const bool clipped = held < free;
             float kl = 0.f, dkl = 0.f;
             if (a.ref_logp) {
