@@ -536,8 +536,9 @@ FO_API fo_status fo_token_logprobs_backward(fo_ctx* ctx, const fo_mat* logits, i
  *   L = -min(ratio A, clip(ratio, 1 - clip_low, 1 + clip_high) A)
  *       + kl_coef (exp(x) - x - 1) - entropy_coef H.
  * A: advantages.  old_logp null: the policy itself (ratio 1; its gradient is that of logp).
- * ref_logp null: no KL term (kl_coef has to be 0).  An advantage of 0 counts nothing, also where ratio
- * is beyond fp32.  weights null: 1; a row of weight 0 does not count.  The loss is sum_t w_t L_t, divided by sum_t w_t
+ * ref_logp null: no KL term (kl_coef has to be 0); kl_coef 0: a statistic alone, which enters neither
+ * the loss nor its gradient.  An advantage of 0 counts nothing, also where ratio is beyond fp32.
+ * weights null: 1; a row of weight 0 does not count.  The loss is sum_t w_t L_t, divided by sum_t w_t
  * over the counted rows where mean is set (0 where nothing counts).
  *   logp: as above (null: not wanted).  stats: 4 values, summed or averaged like the loss: the
  *   loss, the KL term (without kl_coef), the share of clipped tokens, the entropy.

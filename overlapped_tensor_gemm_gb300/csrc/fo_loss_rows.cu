@@ -722,9 +722,12 @@ __global__ void __launch_bounds__(Shape<kMode>::kAll + 32 * Shape<kMode>::kMore,
               dkl = expm1f(x);
               kl = dkl - x;
             }
-            const float da = weight * ((clipped ? 0.f : -free) - a.kl_coef * dkl), dh = -a.entropy_coef * weight;
+            // (without a coefficient the KL term is a statistic: it may be infinite)
+            const float kl_loss = a.kl_coef != 0.f ? a.kl_coef * kl : 0.f;
+            const float kl_slope = a.kl_coef != 0.f ? a.kl_coef * dkl : 0.f;
+            const float da = weight * ((clipped ? 0.f : -free) - kl_slope), dh = -a.entropy_coef * weight;
             if (rank == 0) {
-              const float loss = -(clipped ? held : free) + a.kl_coef * kl - a.entropy_coef * entropy;
+              const float loss = -(clipped ? held : free) + kl_loss - a.entropy_coef * entropy;
               sums[0] += static_cast<double>(weight) * loss;
               sums[1] += static_cast<double>(weight) * kl;
               if (clipped) sums[2] += weight;

@@ -65,3 +65,16 @@ def test_a_ratio_beyond_fp32_is_clipped(ctx):
     old = lp + 0.1
     old[2] = lp[2] - 100.0
     _check(ctx, z, y, np.array([1.0, -0.5, 0.75, 0.25, 0.0, 2.0]), old, None)
+
+
+def test_a_reference_that_is_only_watched(ctx):
+    """Without a coefficient the KL term is a statistic: where it leaves fp32, loss and gradient do not follow."""
+    z, y, lp = _rows()
+    ref = lp - 0.2
+    ref[1] = lp[1] + 100.0
+    adv = np.array([1.0, -0.5, 0.3, 0.25, 0.1, 2.0])
+    stats, _ = _check(ctx, z, y, adv, lp + 0.05, ref)
+    assert stats[1] == np.inf
+    ref[1] = lp[1] - 0.2
+    stats, want = _check(ctx, z, y, adv, lp + 0.05, ref)
+    assert abs(stats[1] - want[1]) <= 128 * u
