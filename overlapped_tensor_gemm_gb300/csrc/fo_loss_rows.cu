@@ -816,11 +816,12 @@ __global__ void __launch_bounds__(Shape<kMode>::kAll + 32 * Shape<kMode>::kMore,
     if (!fine && lane == 0) raise_error(a.ctrl, FO_ERR_TIMEOUT, kSiteFull, blockIdx.x);
     if (kMode == kLossPolicy && rank == 0) {
       if (lane == 0)
-        for (int k = 0; k < 4; ++k) sm.sums[warp][k] = sums[k];
+        for (int k = 0; k < 4; ++k) sm.sums[warp][k] = fine ? sums[k] : static_cast<double>(NAN);
       asm volatile("bar.sync 1, %0;" ::"n"(S::kAll) : "memory");
-      if (warp == 0 && fine) {
+      if (warp == 0) {
         // eight lanes for each of the four values; the team that comes last adds everyone's sums, in
-        // the order of the teams
+        // the order of the teams.  A team whose waits ran out counts as well (or the next launch that counts on
+        // this context would take another CTA for its last), and makes the stats NaN
         const int k = lane >> 3;
         double s = 0.0;
         for (int q = lane & 7; q < kSets * kWarps; q += 8) s += sm.sums[q][k];
