@@ -173,7 +173,7 @@ fo_status check_logits(const fo_mat* logits, int P, const fo_mat* d, const int32
 const int kInPlace[][2] = {{1, 0}};  // dlogits over logits: lists 1 and 0 of every call
 
 fo_status run_rows(fo_ctx* ctx, const LossArgs& a, const LossKind& k, cudaStream_t s) {
-  const cudaError_t e = loss_rows_launch(a, k, host_num_sms(ctx), s);
+  const cudaError_t e = loss_rows_launch(a, k, host_device(ctx), host_num_sms(ctx), s);
   return e == cudaSuccess ? FO_OK : host_fail(FO_ERR_CUDA, cudaGetErrorString(e));
 }
 

@@ -13,12 +13,12 @@
 
 #include "fo_attn_common.cuh"
 #include "fo_internal.h"
+#include "fo_loss_cut.h"
 #include "fo_ptx.cuh"
 
 namespace fo {
 
 constexpr int kLossChunk = 32768;   // bytes of a copy
-constexpr int kLossMaxCtas = 8;     // CTAs of one row
 
 enum LossMode : int {
   kLossForward = 0,   // statistics alone
@@ -95,7 +95,7 @@ __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // fo_loss_rows.cu
-cudaError_t loss_rows_launch(LossArgs a, const LossKind& k, int num_sms, cudaStream_t s);
+cudaError_t loss_rows_launch(LossArgs a, const LossKind& k, int device, int num_sms, cudaStream_t s);
 int loss_rows_parts(int num_sms);   // rows of LossArgs::part that any launch may use
 
 }  // namespace fo

@@ -19,6 +19,7 @@
 //
 // A thread sums relative to a column of its own that is near its maximum (at most 16 octaves below),
 // so that a new maximum does not cost a pass; log2 domain, two columns per instruction.
+#include <atomic>
 #include <cfloat>
 #include <cstring>
 
@@ -859,52 +860,81 @@ void (*kernel_of(const LossKind& k))(LossArgs) {
                    : loss_rows_kernel<TZ, uint16_t, kLossForward, false>;
 }
 
+// Teams of `ctas` CTAs of one cluster that the current device holds at once: which SMs may share a cluster differs
+// from chip to chip.  0: none.  (All kernels of a mode have one shape.)
+template <int kMode>
+int clusters(int ctas) {
+  typedef Shape<kMode> S;
+  const auto kernel = loss_rows_kernel<uint16_t, uint16_t, kMode, true>;
+  constexpr int smem = S::kSlots * kLossChunk + S::kZeros;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return -1;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = ctas;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(S::kAll + 32 * S::kMore);
+  cfg.dynamicSmemBytes = smem;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : -1;
+}
+// The same, asked once per device and mode (what host threads share is atomic)
+int clusters_of(int device, bool one, int size) {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices][2][kLossSizes];  // the answer and 1
+  const bool keep = device >= 0 && device < kDevices;
+  if (keep)
+    if (const int n = known[device][one][size].load(std::memory_order_relaxed)) return n - 1;
+  const int n = one ? clusters<kLossPolicy>(1 << size) : clusters<kLossForward>(1 << size);
+  if (n < 0) {
+    cudaGetLastError();
+    return 0;
+  }
+  if (keep) known[device][one][size].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
 }  // namespace
 
 int loss_rows_parts(int num_sms) { return num_sms; }
 
-cudaError_t loss_rows_launch(LossArgs a, const LossKind& k, int num_sms, cudaStream_t s) {
+cudaError_t loss_rows_launch(LossArgs a, const LossKind& k, int device, int num_sms, cudaStream_t s) {
   const bool one = k.mode == kLossPolicy;
   const int threads = one ? Shape<kLossPolicy>::kAll : Shape<kLossForward>::kAll;
   const int smem = one ? Shape<kLossPolicy>::kSlots * kLossChunk + Shape<kLossPolicy>::kZeros
                        : Shape<kLossForward>::kSlots * kLossChunk;
-  const int places = num_sms * (one ? Shape<kLossPolicy>::kPerSm : Shape<kLossForward>::kPerSm);
   const int cols = k.z32 ? Group<float>::kCols : Group<uint16_t>::kCols;
   for (int r = 0; r < a.P; ++r) a.groups[r + 1] = a.groups[r] + a.cols[r] / cols;
-  const int64_t chunks = (a.groups[a.P] + kChunkGroups - 1) / kChunkGroups;
-  // CTAs of a row: as many as let both sets' rows wait in shared memory for their sums; beyond that what
-  // takes least by this estimate: rounds of teams, each the copies of a row's share and what a row costs
-  // beside them (0.5 us, 0.7 where CTAs exchange parts).  1024 rows of 256 KB: policy loss with an entropy
-  // bonus 113 us before, 99 with the estimate.  (It is cut alike with and without a gradient: the same sums.)
-  int least = 1;
-  if (one) {
-    while (least < kLossMaxCtas && chunks > least * kLossFit) least *= 2;
-    if (chunks > least * Shape<kLossPolicy>::kSlots) {
-      a.twice = a.gradient;
-      least = 1;
-    }
+  LossShape shape;
+  shape.rows = a.rows;
+  shape.groups = a.groups[a.P];
+  shape.chunk_groups = kChunkGroups;
+  shape.threads = threads;
+  shape.waits = one;
+  shape.slots = Shape<kLossPolicy>::kSlots;
+  shape.fit = kLossFit;
+  shape.reads_alone = k.mode == kLossForward;
+  shape.exchange = k.mode != kLossBackward;
+  shape.places = num_sms * (one ? Shape<kLossPolicy>::kPerSm : Shape<kLossForward>::kPerSm);
+  for (int i = 0; i < kLossSizes; ++i) {
+    const int most = shape.places >> i;
+    const int n = i > 0 && shape.exchange ? clusters_of(device, one, i) : most;
+    shape.teams[i] = n < most ? n : most;
   }
-  // teams that fit the GPU at once (clusters of 2 all SMs, of 4 144, of 8 120 of 152)
-  auto fit = [&](int ctas) { return places * (ctas <= 2 ? 152 : ctas == 4 ? 144 : 120) / 152 / ctas; };
-  const double ns = (static_cast<double>(a.groups[a.P]) * (k.mode == kLossForward ? 16 : 32)) * places / 6700.0;
-  a.ctas = least;
-  double best = 0.0;
-  for (int ctas = least; ctas <= kLossMaxCtas && (ctas == least || a.groups[a.P] >= ctas * threads); ctas *= 2) {
-    const int64_t rounds = (a.rows + fit(ctas) - 1) / fit(ctas);
-    const double cost = rounds * (ns / ctas + (ctas > 1 && k.mode != kLossBackward ? 700.0 : 500.0));
-    if (ctas == least || cost < best) {
-      a.ctas = ctas;
-      best = cost;
-    }
-  }
+  const LossCut cut = loss_cut(shape);
+  a.ctas = cut.ctas;
+  a.twice = cut.twice && a.gradient;
   void (*kernel)(LossArgs) = k.z32 ? (k.d32 ? kernel_of<float, float>(k) : kernel_of<float, uint16_t>(k))
                                    : (k.d32 ? kernel_of<uint16_t, float>(k) : kernel_of<uint16_t, uint16_t>(k));
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int64_t teams = a.rows < 1 ? 1 : a.rows < fit(a.ctas) ? a.rows : fit(a.ctas);
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3(static_cast<unsigned>(teams * a.ctas));
+  cfg.gridDim = dim3(static_cast<unsigned>(cut.teams * a.ctas));
   cfg.blockDim = dim3(threads + 32 * (one ? Shape<kLossPolicy>::kMore : Shape<kLossForward>::kMore));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
