@@ -597,7 +597,10 @@ FO_API fo_status fo_preference_loss(fo_ctx* ctx, const fo_mat* logits, int P, co
  * 2^-24 of the largest are kept as that, and none but 0 below 2^-126; a block whose m are all below
  * 1e-30 is kept as zeros).  All bytes zero: states of zero.  Both are rounded to one of the two
  * neighbouring values at random, so that the mean is the value: rounded to the nearest, a mean that
- * moves by a few percent or less a step would not move at all. */
+ * moves by a few percent or less a step would not move at all.  The codes of m are those of elementary
+ * fp32 operations, bit for bit: value times scale, beta1 m, (1 - beta1) g, their sum, the block's
+ * largest times fp32(1 / 448) as the scale and m over the scale are each rounded once; those of v carry an
+ * error of 2^-22 in the logarithm, which moves a few in ten thousand by one. */
 typedef struct {
   void* param;
   const void* grad;

@@ -75,6 +75,7 @@ enum KindBit : int { kParam32 = 1, kGrad32 = 2, kMaster = 4, kStates8 = 8 };
 struct StepArgs {
   float lr, eps, weight_decay, grad_scale, max_norm;
   float beta1, beta2, rest1, rest2;   // rest = 1 - beta, before either is rounded
+  float one;                          // 1, which the compiler does not know
   float fix1, fix2;                   // 1 / (1 - b1^t), 1 / (1 - b2^t)
   double exact1, exact2;              // the betas
   int64_t step;
@@ -246,15 +247,18 @@ __device__ __forceinline__ void from_levels(uint32_t q, float low, float gap, Pa
     }
   }
 }
-// 4 values of m (in units of the scale: at most 448 and a few units in the last place) up or down to e4m3:
+// 4 values of m, in units of the scale (at most 448 and a few units in the last place), up or down to e4m3:
 // a random part of a step is added and what a step holds below is cut off.  Times 2^-120 the ranges of
 // e4m3, its subnormal one too, are those of fp32: an e4m3 number is the bits from the 20th on, and the sign.
-__device__ __forceinline__ uint32_t to_e4m3(const Pair (&m)[2], float inv_scale, const uint32_t* word) {
+// The quotient is m over the scale rounded once (a product with an approximate inverse, corrected by what it
+// leaves: P. Markstein, IBM J. Res. Dev. 34, 1990): a last bit of it can decide a code.
+__device__ __forceinline__ uint32_t to_e4m3(const Pair (&m)[2], float scale, float inv_scale, const uint32_t* word) {
   uint32_t sum[4], sign[4];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     float x, y;
-    unpack2(mul2(mul2(m[k], both(inv_scale)), both(0x1p-120f)), x, y);
+    const Pair q = mul2(m[k], both(inv_scale)), rest = ffma2(q, both(-scale), m[k]);
+    unpack2(mul2(ffma2(rest, both(inv_scale), q), both(0x1p-120f)), x, y);
     sign[2 * k] = __float_as_uint(x);
     sign[2 * k + 1] = __float_as_uint(y);
   }
@@ -311,7 +315,7 @@ __device__ __forceinline__ float correction(double beta, int64_t t) {
 
 // What a step's blocks share
 struct Step {
-  float beta1, beta2, rest1, rest2, eps, decay, rate, fix2, c;
+  float beta1, beta2, rest1, rest2, one, eps, decay, rate, fix2, c;
   uint32_t key;
   bool cut;
 };
@@ -356,9 +360,7 @@ __device__ __forceinline__ void step_block(const TensorRef& t, int64_t blk, int 
   const int64_t at = blk * kBlock + lane * 4;
   n -= lane * 4;
   Pair g[4], w[4], m[4], v[4];
-  float keep1 = a.beta1;
   if constexpr (k8) {
-    keep1 *= raw.scale;
     from_e4m3(raw.m[0], reinterpret_cast<Pair(&)[2]>(m[0]));
     from_e4m3(raw.m[1], reinterpret_cast<Pair(&)[2]>(m[2]));
     from_levels(raw.v[0], raw.range.x, raw.range.y, reinterpret_cast<Pair(&)[2]>(v[0]));
@@ -380,7 +382,13 @@ __device__ __forceinline__ void step_block(const TensorRef& t, int64_t blk, int 
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const Pair x = mul2(g[q], both(a.c));
-    m[q] = ffma2(both(keep1), m[q], mul2(both(a.rest1), x));
+    if (k8) {
+      // each product and the sum rounded once (see to_e4m3).  An addition of the packed products becomes one
+      // operation with one of them, with .rn too: one block in six had another scale then
+      m[q] = ffma2(both(a.one), mul2(both(a.beta1), mul2(m[q], both(raw.scale))), mul2(both(a.rest1), x));
+    } else {
+      m[q] = ffma2(both(a.beta1), m[q], mul2(both(a.rest1), x));
+    }
     v[q] = ffma2(both(a.beta2), v[q], mul2(mul2(both(a.rest2), x), x));
     float x0, x1, y0, y1;
     unpack2(v[q], x0, x1);
@@ -421,7 +429,7 @@ __device__ __forceinline__ void step_block(const TensorRef& t, int64_t blk, int 
     Levels l = {0.f, -0.5f, 0.f};
     if (top_m > 1e-30f) {  // smaller ones are kept as zeros
       scale = top_m * (1.f / kMaxE4m3);
-      inv_scale = __fdividef(kMaxE4m3, top_m);
+      inv_scale = fast_inverse(scale);
     }
     if (top_v != 0) {
       const float top = fast_log2(fmaxf(__uint_as_float(top_v), FLT_MIN));
@@ -450,7 +458,7 @@ __device__ __forceinline__ void step_block(const TensorRef& t, int64_t blk, int 
           if (!(y > 0.f)) code &= ~(0xFF00u << (16 * k));
         }
       }
-      store4<kFull>(tm + q * 64, n - q * 64, to_e4m3(reinterpret_cast<Pair(&)[2]>(m[q]), inv_scale, word + 2 * q));
+      store4<kFull>(tm + q * 64, n - q * 64, to_e4m3(reinterpret_cast<Pair(&)[2]>(m[q]), scale, inv_scale, word + 2 * q));
       store4<kFull>(tv + q * 64, n - q * 64, code);
     }
     if (lane == 0) {
@@ -513,6 +521,7 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas8)
   s.beta2 = a.beta2;
   s.rest1 = a.rest1;
   s.rest2 = a.rest2;
+  s.one = a.one;
   s.eps = a.eps;
   s.decay = lr * a.weight_decay;
   s.rate = lr * fix1;
@@ -962,6 +971,7 @@ fo_status fo_adamw_step(fo_ctx* ctx, const fo_adamw_group* group, const fo_adamw
   a.beta2 = static_cast<float>(prm->beta2);
   a.rest1 = static_cast<float>(1.0 - prm->beta1);
   a.rest2 = static_cast<float>(1.0 - prm->beta2);
+  a.one = 1.f;
   a.eps = prm->eps;
   a.weight_decay = prm->weight_decay;
   a.grad_scale = prm->grad_scale;
