@@ -544,7 +544,7 @@ FO_API fo_status fo_token_logprobs_backward(fo_ctx* ctx, const fo_mat* logits, i
  *   loss, the KL term (without kl_coef), the share of clipped tokens, the entropy.
  *   dlogits null: no gradient.
  * Where the clipped value is the smaller one the ratio has no gradient.  Values of vectors in rows
- * that do not count have no effect.  Behind FO_ERR_TIMEOUT no output is to be used (stats are NaN
+ * that do not count have no effect.  Behind FO_ERR_TIMEOUT no output is to be used (the loss is NaN
  * where a row's sums are missing).  Workspace: 32 bytes per SM. */
 typedef struct {
   float scale;                 /* of the logits */

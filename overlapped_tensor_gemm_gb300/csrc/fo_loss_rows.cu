@@ -722,15 +722,13 @@ __global__ void __launch_bounds__(Shape<kMode>::kAll + 32 * Shape<kMode>::kMore,
               const float x = ref - lp;
               dkl = expm1f(x);
               kl = dkl - x;
+              if (rank == 0) sums[1] += static_cast<double>(weight) * kl;
+              if (a.kl_coef == 0.f) kl = dkl = 0.f;  // (a statistic alone: it may be infinite)
             }
-            // (without a coefficient the KL term is a statistic: it may be infinite)
-            const float kl_loss = a.kl_coef != 0.f ? a.kl_coef * kl : 0.f;
-            const float kl_slope = a.kl_coef != 0.f ? a.kl_coef * dkl : 0.f;
-            const float da = weight * ((clipped ? 0.f : -free) - kl_slope), dh = -a.entropy_coef * weight;
+            const float da = weight * ((clipped ? 0.f : -free) - a.kl_coef * dkl), dh = -a.entropy_coef * weight;
             if (rank == 0) {
-              const float loss = -(clipped ? held : free) + kl_loss - a.entropy_coef * entropy;
+              const float loss = -(clipped ? held : free) + a.kl_coef * kl - a.entropy_coef * entropy;
               sums[0] += static_cast<double>(weight) * loss;
-              sums[1] += static_cast<double>(weight) * kl;
               if (clipped) sums[2] += weight;
               sums[3] += static_cast<double>(weight) * entropy;
             }
@@ -814,15 +812,18 @@ __global__ void __launch_bounds__(Shape<kMode>::kAll + 32 * Shape<kMode>::kMore,
       if (!out && group_y >= 0 && group_y < g_hi - g_lo && group_y % kChunkGroups % kThreads == tid)
         store1(static_cast<TD*>(a.d[rk_y]) + i * a.ldd[rk_y] + col_y, slope_at<kEnt>(slope, zy) + w.w);
     }
-    if (!fine && lane == 0) raise_error(a.ctrl, FO_ERR_TIMEOUT, kSiteFull, blockIdx.x);
+    if (!fine && lane == 0) {
+      raise_error(a.ctrl, FO_ERR_TIMEOUT, kSiteFull, blockIdx.x);
+      sums[0] = static_cast<double>(NAN);
+    }
     if (kMode == kLossPolicy && rank == 0) {
       if (lane == 0)
-        for (int k = 0; k < 4; ++k) sm.sums[warp][k] = fine ? sums[k] : static_cast<double>(NAN);
+        for (int k = 0; k < 4; ++k) sm.sums[warp][k] = sums[k];
       asm volatile("bar.sync 1, %0;" ::"n"(S::kAll) : "memory");
       if (warp == 0) {
         // eight lanes for each of the four values; the team that comes last adds everyone's sums, in
         // the order of the teams.  A team whose waits ran out counts as well (or the next launch that counts on
-        // this context would take another CTA for its last), and makes the stats NaN
+        // this context would take another CTA for its last); its loss is NaN
         const int k = lane >> 3;
         double s = 0.0;
         for (int q = lane & 7; q < kSets * kWarps; q += 8) s += sm.sums[q][k];
