@@ -515,8 +515,8 @@ FO_API fo_status fo_rope_backward(fo_ctx* ctx, const fo_mat* dY, int P, const fo
  *   z = scale logits,  p = softmax(z) over all ranks' columns,  lse = log sum exp z,
  *   logp = z_y - lse,  H = -sum p log p.
  * Statistics are fp32, relative to the row's maximum; columns of -infinity have weight 0 (a row of
- * nothing else gives NaN, as the formula does).  scale > 0 (1 / temperature).  No atomics on
- * results: the same inputs give the same bits. */
+ * nothing else gives NaN, as the formula does), and a probability below 2^-126 counts as 0.
+ * scale > 0 (1 / temperature).  No atomics on results: the same inputs give the same bits. */
 
 /* logp (null: none of it, then lse or entropy), lse and entropy (each may be null). */
 FO_API fo_status fo_token_logprobs(fo_ctx* ctx, const fo_mat* logits, int P, const int32_t* targets, float scale,
@@ -535,7 +535,8 @@ FO_API fo_status fo_token_logprobs_backward(fo_ctx* ctx, const fo_mat* logits, i
  * the logits.  Per token, with ratio = exp(logp - old_logp) and x = ref_logp - logp:
  *   L = -min(ratio A, clip(ratio, 1 - clip_low, 1 + clip_high) A)
  *       + kl_coef (exp(x) - x - 1) - entropy_coef H.
- * A: advantages.  old_logp null: the policy itself (ratio 1; its gradient is that of logp).
+ * A: advantages.  old_logp null: the policy itself (ratio 1; its gradient is that of logp: with
+ * advantages of 1 that of the mean of -logp, the loss of supervised training, in one read of the logits).
  * ref_logp null: no KL term (kl_coef has to be 0); kl_coef 0: a statistic alone, which enters neither
  * the loss nor its gradient.  An advantage of 0 counts nothing, also where ratio is beyond fp32.
  * weights null: 1; a row of weight 0 does not count.  The loss is sum_t w_t L_t, divided by sum_t w_t
@@ -622,8 +623,8 @@ FO_API fo_status fo_adamw_group_create(const fo_adamw_tensor* tensors, int count
 FO_API fo_status fo_adamw_group_destroy(fo_adamw_group* group);
 
 /* norm[0] = sqrt(sum of the squares of every gradient in the group) (device fp32; the squares are
- * fp32: an element above 1.8e19 gives a norm that is not finite).  It lies outside the group's
- * tensors.  Workspace: 8 bytes per CTA. */
+ * fp32: an element above 1.8e19 gives a norm that is not finite, the square of one below 1e-19 loses bits
+ * and below 2.6e-23 it is 0).  It lies outside the group's tensors.  Workspace: 8 bytes per CTA. */
 FO_API fo_status fo_grad_norm(fo_ctx* ctx, const fo_adamw_group* group, float* norm, void* stream);
 
 /* One step for every tensor.  With g = grad_scale * gradient, times
@@ -634,8 +635,9 @@ FO_API fo_status fo_grad_norm(fo_ctx* ctx, const fo_adamw_group* group, float* n
  * a v below 2^-126 for that.
  * norm (null: none): where it is not finite nothing is written at all.  Without it gradients have
  * to be finite.  lr_dev, step_dev (device; null: lr, step): read when the kernel runs, so that a
- * captured step can be replayed with others; they and norm lie outside what the step writes.  step >= 1 (a smaller one in memory ends the call with
- * FO_ERR_RANGE from fo_ctx_poll and nothing is written).
+ * captured step can be replayed with others; they and norm lie outside what the step writes.
+ * step >= 1 (a smaller one in memory ends the call with FO_ERR_RANGE from fo_ctx_poll and nothing is
+ * written).
  * stochastic: bf16 parameters without a master are rounded up or down at random (mean: w) instead
  * of to the nearest.  What is random depends on (seed, step, place of the tensor in the group,
  * element) alone: word = h(b + 0x9E3779B9 e) for element e of the block whose

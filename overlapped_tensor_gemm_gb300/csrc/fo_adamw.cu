@@ -9,8 +9,8 @@
 // that a captured launch would have to keep).  A warp takes a block of 256 elements, two groups of
 // four per lane, so that every access of the warp is whole lines in all types.
 //
-// Measured, 176M parameters: 762 us (6.5 TB/s), 8-bit states 461 us (6.1 TB/s: 77 instructions an element),
-// norm of bf16 gradients 57 us, unpacking to bf16 166.
+// Measured, 176M parameters: 757-762 us (6.5 TB/s), 8-bit states 461-469 us (6.1 TB/s: 77 instructions an element),
+// norm of bf16 gradients 57 us, unpacking to bf16 166-175.
 //
 // 8-bit states.  A block has its own ranges: m is e4m3 times max|m| / 448; v is one of 255 values
 // evenly spaced in log2 between the block's smallest and largest v (few percent apart: rows of a
@@ -44,7 +44,8 @@ constexpr int kStepThreads = 256;
 // CTAs of a step per SM.  8-bit states: as many as have the registers for a block under way beside the one
 // that is computed (4 without it: 742 us for 176M parameters with norm and unpacking, 706 with it).  32 bits
 // need less arithmetic than that, and fewer places in memory at once (3: 839 us with the norm, 2: 823, 1: 925;
-// 2 with the registers of 2: 833).
+// 2 with the registers of 2: 833; all of it with masters.  Without them, in bf16, the registers of 3 spill 8 bytes,
+// 36 with fp32 gradients: not timed).
 constexpr int kStepCtas8 = 3, kStepCtas32 = 2;
 constexpr int kListTensors = 400;     // tensors of one launch
 constexpr int kAhead = 4;             // see run_of

@@ -168,7 +168,7 @@ __device__ __forceinline__ double eighth_sum(double v) {
 __device__ __forceinline__ float base_of(float m) { return fmaxf(m, -FLT_MAX); }
 
 // A part of a row's statistics: reference m, s = sum 2^d, t = sum 2^d d with d = (z - m) c
-struct __align__(16) Part {  // (moved by 16-byte stores)
+struct __align__(16) Part {  // (moved by 16-byte stores: st.async faults on a place that is not aligned)
   float m, s, t, reserved;
 };
 
@@ -184,8 +184,10 @@ __device__ __forceinline__ Wide wide_log(float s) {
 }
 
 // ex2.approx cuts its results off: they are 5.0e-8 too small in the mean (3e-8 the spread about that; measured
-// over 6 million arguments from -12 to 0), which would show in every row's logarithm with the same sign.
-// The largest column's own term, the 1 of a sum s, is exact: a part (s - 1) / s of the mean is added back.
+// on a GB300 over 6 million arguments from -12 to 0), which would show in every row's logarithm with the same
+// sign.  The largest column's own term, the 1 of a sum s, is exact: a part (s - 1) / s of the mean is added
+// back in logp and lse.  The entropy goes without it: it is less than a rounding of an entropy above 1/2, and
+// smaller ones have a small s - 1.
 constexpr float kExpMean = 5.0e-8f;
 
 // The parts of all lanes as one, in every lane
